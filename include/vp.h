@@ -115,6 +115,7 @@ typedef enum vp_dtype { VP_F32 = 0, VP_BF16 = 1 } vp_dtype;
 typedef enum vp_kl_direction { VP_KL_REVERSE = 0, VP_KL_FORWARD = 1 } vp_kl_direction;
 
 #define VP_ERRBIT_TARGET 1
+#define VP_ERRBIT_RULES 2   /* a row's rules are out of range (vp_logits_rules) */
 
 /* Row flags of vp_rowstat. */
 #define VP_ROW_NANINF   1u  /* the row holds a NaN or a +inf                          */
@@ -608,6 +609,134 @@ VP_API vp_status vp_linear_entropy_partial(const void *hidden, const void *weigh
 VP_API vp_status vp_linear_kl_partial(const void *ha, const void *wa, const void *hb, const void *wb, int64_t N,
                                       int64_t V, int64_t Da, int64_t Db, int direction, vp_partial *parts,
                                       void *workspace, size_t workspace_bytes, vp_stream stream);
+
+/* ------------------------------------------------------------------------ */
+/* Rules on logits: penalties for repeated tokens, biases, masks, temperature */
+/* (no counterpart on the pages: what a sampler does to the logits before it */
+/* draws, so that rollouts can be scored and trained on under the            */
+/* distribution they were drawn from)                                        */
+/* ------------------------------------------------------------------------ */
+
+/* The rules of N rows: a host struct of device pointers, read during the call
+ * only (the arrays behind it stay alive until the queued work is done). For
+ * row r and the column of id v, with c_p and c_o the number of times v stands
+ * among the row's prompt and output ids:
+ *   z = x
+ *   c_p + c_o > 0:  z = z > 0 ? z / repetition[r] : z * repetition[r]
+ *   c_o > 0:        z = z - frequency[r] c_o - presence[r]
+ *   v in the row's bias list:  z = z + bias(v), the last entry of v counting
+ *   z = z / temperature[r]
+ *   y = z where the mask allows the column, -inf elsewhere (whatever x holds)
+ * in fp32, y rounded once to the dtype of the logits.
+ *   ids, spans  spans[r] = {first, n_prompt, n_total}: row r's history is
+ *               ids[first .. first + n_total), the first n_prompt of them the
+ *               prompt. Rows may share ids (the rows of a sequence are
+ *               prefixes of it) and may be empty. Ids are global; negative ids
+ *               (padding) and ids outside [vocab_start, vocab_start + V) are
+ *               skipped. spans NULL: no history.
+ *   repetition, frequency, presence, temperature
+ *               one float per row, each array NULL for 1, 0, 0 and 1.
+ *               repetition and temperature must be finite and > 0.
+ *   bias_*      bias_spans[r] = {first, n}: entries bias_ids[first ..) and
+ *               bias_values[first ..). Values may be -inf. NULL: no biases.
+ *   mask        n_masks rows of 32-bit words, mask_stride words apart; bit
+ *               (j % 32) of word j / 32 allows column j of this call. Row r
+ *               uses mask row mask_rows[r], -1 for none; mask_rows NULL: row r
+ *               uses mask row r (n_masks >= N). mask NULL: all allowed.
+ * A row whose spans, mask row, repetition or temperature are out of range is a
+ * data error: its outputs (and gradients) are NaN and VP_ERRBIT_RULES is OR-ed
+ * into *err_word; nothing outside the arrays is read. */
+typedef struct vp_logits_rules {
+    const int64_t *ids;
+    int64_t n_ids;
+    const int64_t *spans;
+    const float *repetition, *frequency, *presence;
+    const int64_t *bias_ids;
+    const float *bias_values;
+    int64_t n_bias;
+    const int64_t *bias_spans;
+    const uint32_t *mask;
+    int64_t n_masks, mask_stride;
+    const int64_t *mask_rows;
+    const float *temperature;
+} vp_logits_rules;
+
+/* y = the rules put on x. y has R and strides y_s_o, y_s_i of its own and may
+ * be x itself (same pointer and strides); it must not overlap x otherwise.
+ * Argument errors as the forward calls above; a rules pointer NULL where
+ * another needs it (spans without ids, bias spans without entries): VP_ERR_NULL;
+ * n_masks < 1, a mask row shorter than V bits (mask_stride < ceil(V / 32) with
+ * more than one row), or fewer mask rows than N without mask_rows: VP_ERR_SHAPE. */
+VP_API vp_status vp_logits_process_fwd(const void *x, int dtype, int64_t N, int64_t V, int64_t R, int64_t s_o,
+                                       int64_t s_i, int64_t vocab_start, const vp_logits_rules *rules, void *y,
+                                       int64_t y_s_o, int64_t y_s_i, int32_t *err_word, vp_stream stream);
+
+/* dx_j = dy_j f_j / temperature, f_j = repetition's factor at x_j (1 / rep
+ * where x_j > 0, rep elsewhere) for an id of the history and 1 for others; 0
+ * where the mask does not allow j, whatever dy holds. The penalties' and
+ * biases' own values get no gradient. dy and dx contiguous [N, V], dx may be
+ * dy. x is read only at ids of the history. */
+VP_API vp_status vp_logits_process_bwd(const void *x, int dtype, int64_t N, int64_t V, int64_t R, int64_t s_o,
+                                       int64_t s_i, int64_t vocab_start, const vp_logits_rules *rules,
+                                       const void *dy, void *dx, int32_t *err_word, vp_stream stream);
+
+/* logp[r] = log softmax(y_r) at the row's target, y as above but kept in fp32
+ * and never written. Targets, special values and records as vp_logprobs_fwd
+ * (a row that the mask leaves nothing of is an all -inf row: NaN; a target
+ * that is masked has logp -inf). workspace: 8-byte aligned,
+ * vp_processed_logprobs_workspace_size(N, V) bytes. */
+VP_API size_t vp_processed_logprobs_workspace_size(int64_t N, int64_t V);
+VP_API vp_status vp_processed_logprobs_fwd(const void *x, int dtype, int64_t N, int64_t V, int64_t R, int64_t s_o,
+                                           int64_t s_i, int64_t vocab_start, const vp_logits_rules *rules,
+                                           const int64_t *targets, float *logp, vp_rowstat *stats, void *workspace,
+                                           size_t workspace_bytes, int32_t *err_word, vp_stream stream);
+
+/* dx_j = grad_out f_j / temperature (onehot_j - p_j), p the softmax of y from
+ * the forward's records; 0 where masked, a zero row for an ignored target, a
+ * NaN row where the forward's logp was NaN. dx contiguous [N, V] in the dtype
+ * of x; dx may be x when x is contiguous. */
+VP_API vp_status vp_processed_logprobs_bwd(const void *x, int dtype, int64_t N, int64_t V, int64_t R, int64_t s_o,
+                                           int64_t s_i, int64_t vocab_start, const vp_logits_rules *rules,
+                                           const int64_t *targets, const vp_rowstat *stats, const float *grad_out,
+                                           void *dx, int32_t *err_word, vp_stream stream);
+
+/* ------------------------------------------------------------------------ */
+/* MXFP4: quantisation and the head's product in microscaled 4-bit floating  */
+/* point (E2M1 elements, one E8M0 scale for each 32 columns; no counterpart  */
+/* on the pages: serving and scoring with a head of a quarter of the bytes)  */
+/* ------------------------------------------------------------------------ */
+/* An MXFP4 matrix of N rows and D columns (D a multiple of 64) is
+ *   codes   uint8 [N, D / 2], 16-byte aligned: column 2 i in the low four bits
+ *           of byte i, column 2 i + 1 in the high ones. A code's low three bits
+ *           choose 0, 0.5, 1, 1.5, 2, 3, 4 or 6, bit 3 is the sign.
+ *   scales  uint8, 16-byte aligned, vp_mxfp4_scale_bytes(N, D) bytes: tiles of
+ *           512 bytes for 128 rows x 128 columns, the tiles of a row group
+ *           consecutive. Block b (columns 32 b ..) of row r lies in tile
+ *           (r / 128) ceil(D / 128) + b / 4 at byte
+ *           16 (r % 32) + 4 ((r % 128) / 32) + b % 4. Bytes of rows past N and
+ *           of columns past D are 0. A byte s stands for 2^(s - 127), 255 for
+ *           NaN.
+ * A block's scale is 2^(floor(log2 max|x|) - 2), at least 2^-127; its elements
+ * are x / scale rounded to nearest even and saturated at 6. A block that holds
+ * a NaN or an infinity gets the NaN scale, so all its values are NaN. */
+VP_API size_t vp_mxfp4_scale_bytes(int64_t N, int64_t D);
+
+/* x: N rows of D elements with the rows' two strides as for logits (V = D). */
+VP_API vp_status vp_mxfp4_quantize(const void *x, int dtype, int64_t N, int64_t D, int64_t R, int64_t s_o, int64_t s_i,
+                                   uint8_t *codes, uint8_t *scales, vp_stream stream);
+
+/* out [N, D], contiguous, VP_F32 or VP_BF16: the values the codes stand for
+ * (exact in both types). */
+VP_API vp_status vp_mxfp4_dequantize(const uint8_t *codes, const uint8_t *scales, int64_t N, int64_t D, int dtype,
+                                     void *out, vp_stream stream);
+
+/* y[n, v] = sum_k x[n, k] w[v, k] over two MXFP4 matrices x [N, D] and w
+ * [V, D], accumulated in fp32 and rounded once to y's dtype (VP_F32 or VP_BF16);
+ * y contiguous [N, V]. An element's value does not depend on N. Forward only:
+ * quantised values have no gradient. */
+VP_API vp_status vp_linear_mxfp4_fwd(const uint8_t *x_codes, const uint8_t *x_scales, const uint8_t *w_codes,
+                                     const uint8_t *w_scales, int64_t N, int64_t V, int64_t D, int dtype, void *y,
+                                     vp_stream stream);
 
 /* ------------------------------------------------------------------------ */
 /* Misc                                                                      */

@@ -49,7 +49,21 @@ SIGNATURES = {
     "vp_logprobs_merge": [P, I64, I64, P, P, P, P],
     "vp_entropy_merge": [P, I64, I64, P, P, P],
     "vp_kl_merge": [P, I64, I64, I32, P, P, P, P],
+    "vp_logits_process_fwd": [P, I32, I64, I64, I64, I64, I64, I64, P, P, I64, I64, P, P],
+    "vp_logits_process_bwd": [P, I32, I64, I64, I64, I64, I64, I64, P, P, P, P, P],
+    "vp_processed_logprobs_fwd": [P, I32, I64, I64, I64, I64, I64, I64, P, P, P, P, P, ctypes.c_size_t, P, P],
+    "vp_processed_logprobs_bwd": [P, I32, I64, I64, I64, I64, I64, I64, P, P, P, P, P, P, P],
+    "vp_mxfp4_quantize": [P, I32, I64, I64, I64, I64, I64, P, P, P],
+    "vp_mxfp4_dequantize": [P, P, I64, I64, I32, P, P],
+    "vp_linear_mxfp4_fwd": [P, P, P, P, I64, I64, I64, I32, P, P],
 }
+
+
+class LogitsRulesStruct(ctypes.Structure):
+    """vp_logits_rules: a host struct of device pointers."""
+    _fields_ = [("ids", P), ("n_ids", I64), ("spans", P), ("repetition", P), ("frequency", P), ("presence", P),
+                ("bias_ids", P), ("bias_values", P), ("n_bias", I64), ("bias_spans", P), ("mask", P),
+                ("n_masks", I64), ("mask_stride", I64), ("mask_rows", P), ("temperature", P)]
 
 
 def path() -> str:
@@ -78,7 +92,9 @@ def lib():
                                ("vp_linear_kl_workspace_size", [I64, I64]),
                                ("vp_linear_kl_bwd_workspace_size", [I64, I64, I64, I64]),
                                ("vp_linear_jsd_workspace_size", [I64, I64]),
-                               ("vp_linear_jsd_bwd_workspace_size", [I64, I64, I64, I64])):
+                               ("vp_linear_jsd_bwd_workspace_size", [I64, I64, I64, I64]),
+                               ("vp_processed_logprobs_workspace_size", [I64, I64]),
+                               ("vp_mxfp4_scale_bytes", [I64, I64])):
                 fn = getattr(h, name)
                 fn.argtypes = args
                 fn.restype = ctypes.c_size_t

@@ -25,6 +25,7 @@ F32, BF16 = 0, 1
 KL_REVERSE, KL_FORWARD = 0, 1
 GRAD_EXACT, GRAD_FAST = 0, 1   # precision of the fused linear backwards (VP_GRAD_EXACT / VP_GRAD_FAST)
 ERRBIT_TARGET = 1
+ERRBIT_RULES = 2               # a row's rules are out of range (VP_ERRBIT_RULES)
 ROW_NANINF, ROW_EMPTY, ROW_MISMATCH, ROW_SHARDED, ROW_BADTARGET = 1, 2, 4, 8, 16
 ROWSTAT_FLOATS = 8  # sizeof(vp_rowstat) / 4
 PART_NANINF, PART_NANINF_B, PART_MISMATCH, PART_HAS_TARGET, PART_IGNORED = 1, 2, 4, 8, 16
@@ -677,3 +678,242 @@ def vp_linear_kl_partial(ha, wa, hb, wb, direction: int = KL_REVERSE, parts=None
                                            _ptr(parts), _ptr(workspace), workspace.numel(), _stream()),
            "vp_linear_kl_partial")
     return parts
+
+
+def _on_gpu(t):
+    """The library reads device memory: a tensor elsewhere is refused, as a missing device is."""
+    if not t.is_cuda:
+        raise VPError(8, f"needs a CUDA tensor, got one on {t.device}")
+
+
+def _rows_apart(y, N, V):
+    """An output view's rows may not share elements (an expanded or overlapping view)."""
+    span = V
+    for size, stride in sorted(zip(y.shape[:-1], y.stride()[:-1]), key=lambda d: d[1]):
+        if size > 1:
+            if stride < span:
+                raise VPError(4, f"rows of an output of shape {tuple(y.shape)} and strides {y.stride()} overlap")
+            span = stride * size
+
+
+class LogitsRules:
+    """The rules of N rows of logits (vp_logits_rules of include/vp.h); made by :func:`logits_rules`.
+
+    Holds the tensors, and the host struct of their device pointers that the calls take."""
+
+    # field -> (dtype, elements per row; None: of its own length)
+    _FIELDS = {"ids": (torch.int64, None), "spans": (torch.int64, 3), "repetition": (torch.float32, 1),
+               "frequency": (torch.float32, 1), "presence": (torch.float32, 1), "bias_ids": (torch.int64, None),
+               "bias_values": (torch.float32, None), "bias_spans": (torch.int64, 2), "mask_rows": (torch.int64, 1),
+               "temperature": (torch.float32, 1)}
+
+    def __init__(self, mask=None, **tensors):
+        self.rows, self.device, self.mask_bits, self.n_masks = None, None, None, 0
+        self.tensors, self.struct = tensors, _lib.LogitsRulesStruct()
+        for name, t in tensors.items():
+            dtype, per_row = self._FIELDS[name]
+            if t is None:
+                continue
+            if t.dtype != dtype:
+                raise VPError(3, f"{name}: needs {dtype}, got {t.dtype}")
+            if not t.is_contiguous():
+                raise VPError(4, f"{name}: needs a contiguous tensor")
+            self._on(t, name)
+            if per_row is not None:
+                rows = t.shape[0] if t.dim() else -1
+                if t.dim() != (1 if per_row == 1 else 2) or (per_row > 1 and t.shape[1] != per_row) or \
+                        self.rows not in (None, rows):
+                    raise VPError(2, f"{name}: shape {tuple(t.shape)}")
+                self.rows = rows
+            setattr(self.struct, name, t.data_ptr())
+        get = tensors.get
+        for spans, lists in (("spans", ("ids",)), ("bias_spans", ("bias_ids", "bias_values"))):
+            if get(spans) is None and any(get(n) is not None for n in lists) or \
+                    get(spans) is not None and any(get(n) is None for n in lists):
+                raise VPError(1, f"{spans} and {', '.join(lists)} go together")
+        if get("spans") is not None:
+            self.struct.n_ids = get("ids").numel()
+        elif any(get(n) is not None for n in ("repetition", "frequency", "presence")):
+            raise VPError(1, "penalties need ids and spans")
+        if get("bias_spans") is not None:
+            if get("bias_ids").numel() != get("bias_values").numel():
+                raise VPError(2, "bias_ids and bias_values differ in length")
+            self.struct.n_bias = get("bias_ids").numel()
+        self.mask = mask
+        if mask is not None:
+            if mask.dtype != torch.int32:
+                raise VPError(3, f"mask: needs {torch.int32}, got {mask.dtype}")
+            if mask.dim() != 2 or mask.shape[0] < 1:
+                raise VPError(2, f"mask: shape {tuple(mask.shape)}")
+            if mask.shape[1] > 1 and mask.stride(1) != 1:
+                raise VPError(4, "mask words need a unit stride")
+            self._on(mask, "mask")
+            self.mask_bits, self.n_masks = 32 * mask.shape[1], mask.shape[0]
+            self.struct.mask, self.struct.n_masks, self.struct.mask_stride = mask.data_ptr(), mask.shape[0], mask.stride(0)
+        elif get("mask_rows") is not None:
+            raise VPError(1, "mask_rows without mask")
+
+    def _on(self, t, name):
+        if self.device not in (None, t.device):
+            raise VPError(4, f"{name}: on {t.device}, others on {self.device}")
+        self.device = t.device
+
+    def check(self, N: int, V: int, device):
+        """The struct's address, for a call on N rows of V columns."""
+        if self.rows not in (None, N):
+            raise VPError(2, f"rules of {self.rows} rows for {N} rows of logits")
+        if self.device not in (None, device):
+            raise VPError(4, f"rules on {self.device}, logits on {device}")
+        if self.mask_bits is not None and (self.mask_bits < V or (self.tensors.get("mask_rows") is None
+                                                                  and self.n_masks < N)):
+            raise VPError(2, f"mask: {self.n_masks} rows of {self.mask_bits} bits for {N} rows of {V} logits")
+        return ctypes.byref(self.struct)
+
+
+def logits_rules(ids=None, spans=None, repetition=None, frequency=None, presence=None, bias_ids=None,
+                 bias_values=None, bias_spans=None, mask=None, mask_rows=None, temperature=None) -> LogitsRules:
+    """What a sampler does to N rows of logits before it draws (include/vp.h, vp_logits_rules).
+
+    ids int64 and spans int64 [N, 3] = (first, n_prompt, n_total): row r's history is
+    ids[first:first + n_total], its first n_prompt ids the prompt. repetition, frequency, presence and
+    temperature: fp32 [N]. bias_ids int64, bias_values fp32 and bias_spans int64 [N, 2] = (first, n): a list of
+    (id, bias) per row. mask: int32 [M, words], bit j % 32 of word j // 32 allowing column j; mask_rows int64
+    [N]: the mask row of each row, -1 for none (without it row r uses mask row r). Everything may be None."""
+    return LogitsRules(mask=mask, ids=ids, spans=spans, repetition=repetition, frequency=frequency, presence=presence,
+                       bias_ids=bias_ids, bias_values=bias_values, bias_spans=bias_spans, mask_rows=mask_rows,
+                       temperature=temperature)
+
+
+def vp_logits_process_fwd(x, rules: LogitsRules, vocab_start: int = 0, err_word=None, y=None):
+    """The rules put on x: y, of x's shape and dtype (contiguous, or as passed; y=x works in place)."""
+    N, V, R, s_o, s_i = rows_of(x)
+    q = rules.check(N, V, x.device)
+    _arg(err_word, 1, torch.int32, x, "err_word")
+    if y is None:
+        y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    elif y.shape != x.shape or y.dtype != x.dtype or y.device != x.device:
+        raise VPError(2 if y.shape != x.shape else 3 if y.dtype != x.dtype else 4, "y needs x's shape, dtype and device")
+    _, _, _, y_s_o, y_s_i = rows_of(y)
+    _rows_apart(y, N, V)
+    _on_gpu(x)
+    _check(_lib.lib().vp_logits_process_fwd(_ptr(x), _dtype_code(x), N, V, R, s_o, s_i, vocab_start, q, _ptr(y), y_s_o,
+                                            y_s_i, _ptr(err_word), _stream()), "vp_logits_process_fwd")
+    return y
+
+
+def vp_logits_process_bwd(x, rules: LogitsRules, dy, vocab_start: int = 0, err_word=None, dx=None):
+    """Gradient of vp_logits_process_fwd: dx, contiguous [N, V]; dy contiguous with N V elements of x's dtype."""
+    N, V, R, s_o, s_i = rows_of(x)
+    q = rules.check(N, V, x.device)
+    _arg(err_word, 1, torch.int32, x, "err_word")
+    _arg(dy, N * V, x.dtype, x, "dy")
+    _arg(dx, N * V, x.dtype, x, "dx")
+    _on_gpu(x)
+    dx = torch.empty((N, V), dtype=x.dtype, device=x.device) if dx is None else dx
+    _check(_lib.lib().vp_logits_process_bwd(_ptr(x), _dtype_code(x), N, V, R, s_o, s_i, vocab_start, q, _ptr(dy),
+                                            _ptr(dx), _ptr(err_word), _stream()), "vp_logits_process_bwd")
+    return dx
+
+
+def vp_processed_logprobs_workspace_size(N: int, V: int) -> int:
+    return int(_lib.lib().vp_processed_logprobs_workspace_size(N, V))
+
+
+def vp_processed_logprobs_fwd(x, rules: LogitsRules, targets, vocab_start: int = 0, err_word=None, logp=None,
+                              stats=None, workspace=None):
+    """Logprobs of the targets under the ruled logits: (logp fp32 [N], stats). Nothing of size [N, V] is written."""
+    N, V, R, s_o, s_i = rows_of(x)
+    q = rules.check(N, V, x.device)
+    _row_args(x, N, targets=targets, stats=(stats,), err_word=err_word, outs=(logp,))
+    if workspace is not None and (workspace.device != x.device or not workspace.is_contiguous()):
+        raise VPError(4, f"workspace: needs contiguous bytes on {x.device}")
+    _on_gpu(x)
+    logp = _f32(N, x) if logp is None else logp
+    stats = rowstats(N, x.device) if stats is None else stats
+    if workspace is None:
+        workspace = _workspace(_lib.lib().vp_processed_logprobs_workspace_size(N, V), x)
+    _check(_lib.lib().vp_processed_logprobs_fwd(_ptr(x), _dtype_code(x), N, V, R, s_o, s_i, vocab_start, q,
+                                                _ptr(targets), _ptr(logp), _ptr(stats), _ptr(workspace),
+                                                workspace.numel(), _ptr(err_word), _stream()),
+           "vp_processed_logprobs_fwd")
+    return logp, stats
+
+
+def vp_processed_logprobs_bwd(x, rules: LogitsRules, targets, stats, grad, vocab_start: int = 0, err_word=None,
+                              dx=None):
+    """Gradient of sum_r grad[r] logp[r] with respect to x: dx, contiguous [N, V] in the dtype of x."""
+    N, V, R, s_o, s_i = rows_of(x)
+    q = rules.check(N, V, x.device)
+    _row_args(x, N, targets=targets, stats=(stats,), grad=grad, err_word=err_word)
+    _arg(dx, N * V, x.dtype, x, "dx")
+    _on_gpu(x)
+    dx = torch.empty((N, V), dtype=x.dtype, device=x.device) if dx is None else dx
+    _check(_lib.lib().vp_processed_logprobs_bwd(_ptr(x), _dtype_code(x), N, V, R, s_o, s_i, vocab_start, q,
+                                                _ptr(targets), _ptr(stats), _ptr(grad), _ptr(dx), _ptr(err_word),
+                                                _stream()), "vp_processed_logprobs_bwd")
+    return dx
+
+
+def vp_mxfp4_scale_bytes(N: int, D: int) -> int:
+    """Bytes of the scale tiles of an MXFP4 matrix [N, D] (0 for sizes that are not taken)."""
+    return int(_lib.lib().vp_mxfp4_scale_bytes(N, D))
+
+
+def _mxfp4(codes, scales, what: str):
+    """(rows, D) of an MXFP4 matrix: codes uint8 [rows, D / 2] and its scale tiles."""
+    if codes.dim() != 2:
+        raise VPError(2, f"{what} codes must be [rows, D / 2], got {tuple(codes.shape)}")
+    N, D = codes.shape[0], 2 * codes.shape[1]
+    if D < 64 or D % 64:
+        raise VPError(2, f"{what} of {D} columns: MXFP4 takes multiples of 64")
+    _arg(codes, codes.numel(), torch.uint8, codes, f"{what} codes")
+    _arg(scales, vp_mxfp4_scale_bytes(N, D), torch.uint8, codes, f"{what} scales")
+    return N, D
+
+
+def vp_mxfp4_quantize(x, codes=None, scales=None):
+    """MXFP4 of x ([N, D] or [B, T, D] rows, D a multiple of 64): (codes uint8 [N, D / 2], scales uint8)."""
+    N, D, R, s_o, s_i = rows_of(x)
+    n = vp_mxfp4_scale_bytes(N, D)
+    _arg(codes, N * D // 2, torch.uint8, x, "codes")
+    _arg(scales, n, torch.uint8, x, "scales")
+    if n == 0 and N > 0:
+        raise VPError(2, f"rows of {D} columns: MXFP4 takes multiples of 64")
+    _on_gpu(x)
+    codes = torch.empty((N, D // 2), dtype=torch.uint8, device=x.device) if codes is None else codes
+    scales = torch.empty(n, dtype=torch.uint8, device=x.device) if scales is None else scales
+    _check(_lib.lib().vp_mxfp4_quantize(_ptr(x), _dtype_code(x), N, D, R, s_o, s_i, _ptr(codes), _ptr(scales),
+                                        _stream()), "vp_mxfp4_quantize")
+    return codes, scales
+
+
+_DTYPES = {torch.float32: F32, torch.bfloat16: BF16}
+
+
+def vp_mxfp4_dequantize(codes, scales, dtype=torch.bfloat16, out=None):
+    """The values of an MXFP4 matrix: [N, D] in dtype (fp32 or bf16, exact in both)."""
+    N, D = _mxfp4(codes, scales, "matrix")
+    if dtype not in _DTYPES:
+        raise VPError(3, f"dtype {dtype}")
+    _arg(out, N * D, dtype, codes, "out")
+    _on_gpu(codes)
+    out = torch.empty((N, D), dtype=dtype, device=codes.device) if out is None else out
+    _check(_lib.lib().vp_mxfp4_dequantize(_ptr(codes), _ptr(scales), N, D, _DTYPES[dtype], _ptr(out), _stream()),
+           "vp_mxfp4_dequantize")
+    return out
+
+
+def vp_linear_mxfp4_fwd(x_codes, x_scales, w_codes, w_scales, dtype=torch.bfloat16, y=None):
+    """y [N, V] = x . W^T of two MXFP4 matrices x [N, D] and W [V, D], in dtype (fp32 or bf16)."""
+    N, D = _mxfp4(x_codes, x_scales, "x")
+    V, Dw = _mxfp4(w_codes, w_scales, "w")
+    if D != Dw or w_codes.device != x_codes.device:
+        raise VPError(2 if D != Dw else 4, f"x [{N}, {D}] on {x_codes.device}, w [{V}, {Dw}] on {w_codes.device}")
+    if dtype not in _DTYPES:
+        raise VPError(3, f"dtype {dtype}")
+    _arg(y, N * V, dtype, x_codes, "y")
+    _on_gpu(x_codes)
+    y = torch.empty((N, V), dtype=dtype, device=x_codes.device) if y is None else y
+    _check(_lib.lib().vp_linear_mxfp4_fwd(_ptr(x_codes), _ptr(x_scales), _ptr(w_codes), _ptr(w_scales), N, V, D,
+                                          _DTYPES[dtype], _ptr(y), _stream()), "vp_linear_mxfp4_fwd")
+    return y

@@ -584,11 +584,12 @@ vp_status vp_fault_status(uint32_t *value, int clear) {
     if (!value) return VP_ERR_NULL;
     vp_status st = check_device();
     if (st != VP_OK) return st;
-    uint32_t a = 0, b = 0, c = 0;
+    uint32_t a = 0, b = 0, c = 0, d = 0;
     if (vp::read_fault(&a, clear != 0) != cudaSuccess || vp::read_linear_logp_fault(&b, clear != 0) != cudaSuccess ||
-        vp::read_linear_ent_kl_fault(&c, clear != 0) != cudaSuccess)
+        vp::read_linear_ent_kl_fault(&c, clear != 0) != cudaSuccess ||
+        vp::read_linear_mxfp4_fault(&d, clear != 0) != cudaSuccess)
         return VP_ERR_LAUNCH;
-    *value = a | ((b | c) << 2);
+    *value = a | ((b | c | d) << 2);
     return VP_OK;
 }
 
@@ -667,4 +668,166 @@ vp_status vp_linear_kl_partial(const void *ha, const void *wa, const void *hb, c
     vp::LinearKLArgs a{ha, wa, hb, wb, N, V, Da, Db, direction, nullptr, nullptr, nullptr, nullptr,
                        nullptr, nullptr, nullptr, nullptr, workspace, (cudaStream_t)stream, 0.f, parts};
     return launched(vp::launch_linear_kl_fwd(a));
+}
+
+// ---------------------------------------------------------------------------
+// Rules on logits
+// ---------------------------------------------------------------------------
+namespace {
+
+int64_t mask_words(int64_t V) { return (V + 31) / 32; }
+
+vp_status check_rules(const vp_logits_rules *q, int64_t N, int64_t V, vp::RuleSet *out) {
+    if (!q) return VP_ERR_NULL;
+    if (q->spans) {
+        if (q->n_ids < 0) return VP_ERR_SHAPE;
+        if (q->n_ids > 0 && !q->ids) return VP_ERR_NULL;
+        if (!aligned(q->ids, 8) || !aligned(q->spans, 8)) return VP_ERR_ALIGN;
+    }
+    if (!aligned(q->repetition, 4) || !aligned(q->frequency, 4) || !aligned(q->presence, 4) ||
+        !aligned(q->temperature, 4))
+        return VP_ERR_ALIGN;
+    if (q->bias_spans) {
+        if (q->n_bias < 0) return VP_ERR_SHAPE;
+        if (q->n_bias > 0 && (!q->bias_ids || !q->bias_values)) return VP_ERR_NULL;
+        if (!aligned(q->bias_ids, 8) || !aligned(q->bias_values, 4) || !aligned(q->bias_spans, 8)) return VP_ERR_ALIGN;
+    }
+    if (q->mask) {
+        if (q->n_masks < 1 || (!q->mask_rows && q->n_masks < N)) return VP_ERR_SHAPE;
+        if (q->mask_stride < 0) return VP_ERR_LAYOUT;
+        if (q->n_masks > 1 && q->mask_stride < mask_words(V)) return VP_ERR_SHAPE;
+        if (!aligned(q->mask, 4) || !aligned(q->mask_rows, 8)) return VP_ERR_ALIGN;
+    }
+    *out = vp::RuleSet{q->ids, q->n_ids, q->spans, q->repetition, q->frequency, q->presence, q->bias_ids,
+                       q->bias_values, q->n_bias, q->bias_spans, q->mask, q->n_masks, q->mask_stride, q->mask_rows,
+                       q->temperature};
+    return VP_OK;
+}
+
+}  // namespace
+
+vp_status vp_logits_process_fwd(const void *x, int dtype, int64_t N, int64_t V, int64_t R, int64_t s_o, int64_t s_i,
+                                int64_t vocab_start, const vp_logits_rules *rules, void *y, int64_t y_s_o,
+                                int64_t y_s_i, int32_t *err_word, vp_stream stream) {
+    vp_status st = check_rows(dtype, N, V, R, s_o, s_i);
+    if (st != VP_OK) return st;
+    if (y_s_o < 0 || y_s_i < 0) return VP_ERR_LAYOUT;
+    if (N == 0) return VP_OK;
+    if (!x || !y) return VP_ERR_NULL;
+    const size_t es = elem_size(dtype);
+    if (!aligned(x, es) || !aligned(y, es) || !aligned(err_word, 4)) return VP_ERR_ALIGN;
+    vp::RuleArgs a{x, nullptr, y, dtype == VP_BF16, N, V, R, s_o, s_i, y_s_o, y_s_i, vocab_start, {}, nullptr, nullptr,
+                   nullptr, nullptr, err_word, (cudaStream_t)stream};
+    if ((st = check_rules(rules, N, V, &a.rules)) != VP_OK) return st;
+    if ((st = check_device()) != VP_OK) return st;
+    return launched(vp::launch_process_fwd(a));
+}
+
+vp_status vp_logits_process_bwd(const void *x, int dtype, int64_t N, int64_t V, int64_t R, int64_t s_o, int64_t s_i,
+                                int64_t vocab_start, const vp_logits_rules *rules, const void *dy, void *dx,
+                                int32_t *err_word, vp_stream stream) {
+    vp_status st = check_rows(dtype, N, V, R, s_o, s_i);
+    if (st != VP_OK) return st;
+    if (N == 0) return VP_OK;
+    if (!x || !dy || !dx) return VP_ERR_NULL;
+    const size_t es = elem_size(dtype);
+    if (!aligned(x, es) || !aligned(dy, es) || !aligned(dx, es) || !aligned(err_word, 4)) return VP_ERR_ALIGN;
+    vp::RuleArgs a{x, dy, dx, dtype == VP_BF16, N, V, R, s_o, s_i, 0, 0, vocab_start, {}, nullptr, nullptr, nullptr,
+                   nullptr, err_word, (cudaStream_t)stream};
+    if ((st = check_rules(rules, N, V, &a.rules)) != VP_OK) return st;
+    if ((st = check_device()) != VP_OK) return st;
+    return launched(vp::launch_process_bwd(a));
+}
+
+size_t vp_processed_logprobs_workspace_size(int64_t N, int64_t V) {
+    if (N < 0 || N > kMaxRowsPerLaunch || V < 1 || V > kMaxV) return 0;
+    return (size_t)N * (size_t)vp::rule_slices(V) * sizeof(vp_partial);
+}
+
+vp_status vp_processed_logprobs_fwd(const void *x, int dtype, int64_t N, int64_t V, int64_t R, int64_t s_o,
+                                    int64_t s_i, int64_t vocab_start, const vp_logits_rules *rules,
+                                    const int64_t *targets, float *logp, vp_rowstat *stats, void *workspace,
+                                    size_t workspace_bytes, int32_t *err_word, vp_stream stream) {
+    vp_status st = check_rows(dtype, N, V, R, s_o, s_i);
+    if (st != VP_OK) return st;
+    if (N == 0) return VP_OK;
+    if (!x || !targets || !logp || !stats || !workspace) return VP_ERR_NULL;
+    if (!aligned(x, elem_size(dtype)) || !aligned(targets, 8) || !aligned(logp, 4) || !aligned(stats, 16) ||
+        !aligned(workspace, 8) || !aligned(err_word, 4))
+        return VP_ERR_ALIGN;
+    if (workspace_bytes < vp_processed_logprobs_workspace_size(N, V)) return VP_ERR_ARG;
+    vp::RuleArgs a{x, nullptr, nullptr, dtype == VP_BF16, N, V, R, s_o, s_i, 0, 0, vocab_start, {}, targets, nullptr,
+                   nullptr, workspace, err_word, (cudaStream_t)stream};
+    if ((st = check_rules(rules, N, V, &a.rules)) != VP_OK) return st;
+    if ((st = check_device()) != VP_OK) return st;
+    return launched(vp::launch_processed_logprobs_fwd(a, logp, stats));
+}
+
+vp_status vp_processed_logprobs_bwd(const void *x, int dtype, int64_t N, int64_t V, int64_t R, int64_t s_o,
+                                    int64_t s_i, int64_t vocab_start, const vp_logits_rules *rules,
+                                    const int64_t *targets, const vp_rowstat *stats, const float *grad_out, void *dx,
+                                    int32_t *err_word, vp_stream stream) {
+    vp_status st = check_rows(dtype, N, V, R, s_o, s_i);
+    if (st != VP_OK) return st;
+    if (N == 0) return VP_OK;
+    if (!x || !targets || !stats || !grad_out || !dx) return VP_ERR_NULL;
+    const size_t es = elem_size(dtype);
+    if (!aligned(x, es) || !aligned(dx, es) || !aligned(targets, 8) || !aligned(stats, 16) ||
+        !aligned(grad_out, 4) || !aligned(err_word, 4))
+        return VP_ERR_ALIGN;
+    vp::RuleArgs a{x, nullptr, dx, dtype == VP_BF16, N, V, R, s_o, s_i, 0, 0, vocab_start, {}, targets, stats,
+                   grad_out, nullptr, err_word, (cudaStream_t)stream};
+    if ((st = check_rules(rules, N, V, &a.rules)) != VP_OK) return st;
+    if ((st = check_device()) != VP_OK) return st;
+    return launched(vp::launch_processed_logprobs_bwd(a));
+}
+
+// ---------------------------------------------------------------------------
+// MXFP4
+// ---------------------------------------------------------------------------
+size_t vp_mxfp4_scale_bytes(int64_t N, int64_t D) {
+    if (!linear_dims_ok(N, 1, D)) return 0;
+    return (size_t)((N + 127) / 128) * (size_t)((D + 127) / 128) * 512;
+}
+
+vp_status vp_mxfp4_quantize(const void *x, int dtype, int64_t N, int64_t D, int64_t R, int64_t s_o, int64_t s_i,
+                            uint8_t *codes, uint8_t *scales, vp_stream stream) {
+    vp_status st = check_rows(dtype, N, D, R, s_o, s_i);
+    if (st != VP_OK) return st;
+    if (!linear_dims_ok(N, 1, D)) return VP_ERR_SHAPE;
+    if (N == 0) return VP_OK;
+    if (!x || !codes || !scales) return VP_ERR_NULL;
+    if (!aligned(x, elem_size(dtype)) || !aligned(codes, 16) || !aligned(scales, 16)) return VP_ERR_ALIGN;
+    if ((st = check_device()) != VP_OK) return st;
+    vp::Mxfp4QuantArgs a{x, dtype == VP_BF16, N, D, R, s_o, s_i, codes, scales, (cudaStream_t)stream};
+    return launched(vp::launch_mxfp4_quantize(a));
+}
+
+vp_status vp_mxfp4_dequantize(const uint8_t *codes, const uint8_t *scales, int64_t N, int64_t D, int dtype, void *out,
+                              vp_stream stream) {
+    if (dtype != VP_F32 && dtype != VP_BF16) return VP_ERR_DTYPE;
+    if (!linear_dims_ok(N, 1, D)) return VP_ERR_SHAPE;
+    if (N == 0) return VP_OK;
+    if (!codes || !scales || !out) return VP_ERR_NULL;
+    if (!aligned(codes, 16) || !aligned(scales, 16) || !aligned(out, 16)) return VP_ERR_ALIGN;
+    vp_status st = check_device();
+    if (st != VP_OK) return st;
+    vp::Mxfp4DequantArgs a{codes, scales, N, D, out, dtype == VP_BF16, (cudaStream_t)stream};
+    return launched(vp::launch_mxfp4_dequantize(a));
+}
+
+vp_status vp_linear_mxfp4_fwd(const uint8_t *x_codes, const uint8_t *x_scales, const uint8_t *w_codes,
+                              const uint8_t *w_scales, int64_t N, int64_t V, int64_t D, int dtype, void *y,
+                              vp_stream stream) {
+    if (dtype != VP_F32 && dtype != VP_BF16) return VP_ERR_DTYPE;
+    if (!linear_dims_ok(N, V, D)) return VP_ERR_SHAPE;
+    if (N == 0) return VP_OK;
+    if (!x_codes || !x_scales || !w_codes || !w_scales || !y) return VP_ERR_NULL;
+    if (!aligned(x_codes, 16) || !aligned(x_scales, 16) || !aligned(w_codes, 16) || !aligned(w_scales, 16) ||
+        !aligned(y, elem_size(dtype)))
+        return VP_ERR_ALIGN;
+    vp_status st = check_device();
+    if (st != VP_OK) return st;
+    vp::LinearMxfp4Args a{x_codes, x_scales, w_codes, w_scales, N, V, D, y, dtype == VP_BF16, (cudaStream_t)stream};
+    return launched(vp::launch_linear_mxfp4(a));
 }

@@ -4,16 +4,16 @@
 // the gradient GEMMs of the chunked backward.
 //
 // Each translation unit that includes this header gets its own copy of the
-// kernels' fault word (g_linear_fault); read_linear_fault reads every copy.
+// kernels' fault word (vp_gemm_host.cuh); vp_fault_status reads every copy.
 #pragma once
 
 #include <cuda.h>
-#include <cudaTypedefs.h>
 
 #include <algorithm>
 #include <atomic>
 
 #include "vp_device.cuh"
+#include "vp_gemm_host.cuh"
 #include "vp_launch.h"
 #include "vp_umma.cuh"
 
@@ -29,9 +29,6 @@ constexpr int kLThreads = 192;                     // TMA warp, MMA warp, 4 epil
 // Columns per epilogue thread in the dual form (one half of a 256-column tile).
 constexpr int kDualEpiCols = 128;
 constexpr uint32_t kLTmemCols = 2 * kLBN;          // two accumulators
-
-// Set when a bounded wait of the linear kernels gave up.
-static __device__ uint32_t g_linear_fault;   // one per translation unit
 
 struct LinearBars {
     uint64_t full[kLStages], empty[kLStages], acc_full[2], acc_empty[2];
@@ -522,20 +519,6 @@ struct StoreBf16Epi {
 // ---------------------------------------------------------------------------
 // Host side
 // ---------------------------------------------------------------------------
-static PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
-    static std::atomic<void *> fn{nullptr};
-    void *f = fn.load();
-    if (!f) {
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) !=
-                cudaSuccess ||
-            q != cudaDriverEntryPointSuccess)
-            return nullptr;
-        fn.store(f);
-    }
-    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
-}
-
 // Row-major bf16 matrix of `rows` rows of `cols` valid elements, `pitch`
 // elements apart; boxes of box_rows x 64 with the 128-byte swizzle. Boxes past
 // the extents read as zeros.
@@ -767,16 +750,6 @@ static cudaError_t chunk_gradient_gemms(const CUtensorMap &tm_h_mn, const __nv_b
         if (e != cudaSuccess) return e;
     }
     return cudaSuccess;
-}
-
-// Reads (and optionally clears) this translation unit's fault word.
-static cudaError_t read_tu_fault(uint32_t *value, bool clear) {
-    cudaError_t e = cudaMemcpyFromSymbol(value, g_linear_fault, sizeof(uint32_t));
-    if (e == cudaSuccess && clear && *value) {
-        const uint32_t zero = 0;
-        e = cudaMemcpyToSymbol(g_linear_fault, &zero, sizeof(uint32_t));
-    }
-    return e;
 }
 
 }  // namespace vp

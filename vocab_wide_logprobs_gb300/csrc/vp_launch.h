@@ -8,6 +8,7 @@
 namespace vp {
 
 constexpr int VP_ERRBIT_TARGET_ = 1;  // same value as VP_ERRBIT_TARGET in include/vp.h
+constexpr int VP_ERRBIT_RULES_ = 2;   // same value as VP_ERRBIT_RULES
 constexpr int VP_GRAD_EXACT_ = 0;     // same values as VP_GRAD_EXACT / VP_GRAD_FAST in include/vp.h
 constexpr int VP_GRAD_FAST_ = 1;
 
@@ -179,6 +180,69 @@ cudaError_t launch_linear_kl_bwd(const LinearKLArgs &a);
 // Fused linear generalized JSD, interior beta (kl = the JSD output)
 cudaError_t launch_linear_jsd_fwd(const LinearKLArgs &a);
 cudaError_t launch_linear_jsd_bwd(const LinearKLArgs &a);
+
+// Device pointers of vp_logits_rules; spans / bias_spans / mask NULL: no such rule.
+struct RuleSet {
+    const int64_t *ids;
+    int64_t n_ids;
+    const int64_t *spans;                               // [N, 3]
+    const float *repetition, *frequency, *presence;     // [N] or NULL
+    const int64_t *bias_ids;
+    const float *bias_values;
+    int64_t n_bias;
+    const int64_t *bias_spans;                          // [N, 2]
+    const uint32_t *mask;
+    int64_t n_masks, mask_stride;
+    const int64_t *mask_rows;                           // [N] or NULL (row r uses mask row r)
+    const float *temperature;                           // [N] or NULL
+};
+
+struct RuleArgs {
+    const void *x, *dy;
+    void *out;                    // y (its own strides, the same R), or a contiguous gradient
+    bool bf16;
+    int64_t N, V, R, s_o, s_i, out_s_o, out_s_i, vocab_start;
+    RuleSet rules;
+    const int64_t *targets;
+    const void *stats;            // backward: vp_rowstat [N]
+    const float *g;
+    void *parts;                  // ruled logprobs forward: vp_partial [slices, N]
+    int32_t *err;
+    cudaStream_t stream;
+};
+
+int64_t rule_slices(int64_t V);
+cudaError_t launch_process_fwd(const RuleArgs &a);
+cudaError_t launch_process_bwd(const RuleArgs &a);
+cudaError_t launch_processed_logprobs_fwd(const RuleArgs &a, float *logp, void *stats);
+cudaError_t launch_processed_logprobs_bwd(const RuleArgs &a);
+
+// MXFP4 matrices: codes [rows, D / 2] and scale tiles (include/vp.h).
+struct Mxfp4QuantArgs {
+    const void *x;
+    bool bf16;
+    int64_t N, D, R, s_o, s_i;
+    void *codes, *scales;
+    cudaStream_t stream;
+};
+struct Mxfp4DequantArgs {
+    const void *codes, *scales;
+    int64_t N, D;
+    void *out;                    // contiguous [N, D]
+    bool bf16;
+    cudaStream_t stream;
+};
+struct LinearMxfp4Args {
+    const void *x_codes, *x_scales, *w_codes, *w_scales;
+    int64_t N, V, D;
+    void *y;                      // contiguous [N, V]
+    bool bf16;
+    cudaStream_t stream;
+};
+cudaError_t launch_mxfp4_quantize(const Mxfp4QuantArgs &a);
+cudaError_t launch_mxfp4_dequantize(const Mxfp4DequantArgs &a);
+cudaError_t launch_linear_mxfp4(const LinearMxfp4Args &a);
+cudaError_t read_linear_mxfp4_fault(uint32_t *value, bool clear);
 
 cudaError_t launch_logprobs_fwd(const StatsArgs &a);
 cudaError_t launch_entropy_fwd(const StatsArgs &a);

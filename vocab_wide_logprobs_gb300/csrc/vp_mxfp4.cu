@@ -1,0 +1,413 @@
+// vp_mxfp4.cu -- MXFP4 matrices (OCP Microscaling formats: E2M1 elements, one
+// E8M0 scale for each block of 32): quantisation, the values back, and the
+// head's product of two such matrices on the block-scaled tensor cores.
+//
+// Layout of a matrix [rows, D]: include/vp.h. The scale tiles (512 bytes for
+// 128 rows x 4 blocks, 16 bytes for each row % 32) are what tcgen05.cp
+// 32x128b.warpx4 puts into tensor memory for the block-scaled MMA, so a stage's
+// scales are one contiguous bulk copy.
+#include <algorithm>
+
+#include "vp_device.cuh"
+#include "vp_gemm_host.cuh"
+#include "vp_launch.h"
+#include "vp_umma.cuh"
+
+namespace vp {
+
+// ---------------------------------------------------------------------------
+// Quantisation
+// ---------------------------------------------------------------------------
+// Eight values to eight E2M1 codes (round to nearest even, saturated), column i
+// in bits 4 i .. 4 i + 3.
+__device__ __forceinline__ uint32_t e2m1x8(const float (&v)[8]) {
+    uint32_t r;
+    asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b2, %6, %5;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n\t"
+        "mov.b32 %0, {b0, b1, b2, b3};\n\t}"
+        : "=r"(r)
+        : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]));
+    return r;
+}
+
+// Byte offset of the scale word (4 blocks) of row r in column tile kt of n_kt.
+__device__ __forceinline__ int64_t scale_word(int64_t r, int kt, int n_kt) {
+    return ((r >> 7) * n_kt + kt) * 512 + (r & 31) * 16 + ((r & 127) >> 5) * 4;
+}
+
+constexpr int kQThreads = 256;
+
+// A warp takes 256 consecutive columns of a row, a lane 8 of them: a block is
+// four lanes, its maximum two shuffles away. The scale comes from the maximum's
+// exponent bits (E: the scale byte is E - 2, at least 0), so x / scale is exact.
+// Rows N .. the next multiple of 128 only get their zero scale bytes.
+template <typename T>
+__global__ void __launch_bounds__(kQThreads)
+mxfp4_quantize_kernel(const T *__restrict__ x, Rows rows, int64_t N, int64_t n_rows, int D, uint8_t *__restrict__ codes,
+                      uint8_t *__restrict__ scales) {
+    pdl_enter<true>();
+    const int lane = threadIdx.x & 31;
+    const int n_kt = (D + 127) / 128, n_chunk = (D + 255) / 256;
+    const int64_t unit = (int64_t)blockIdx.x * (kQThreads / 32) + (threadIdx.x >> 5);
+    const int64_t r = unit / n_chunk;
+    if (r >= n_rows) return;
+    const int chunk = (int)(unit - r * n_chunk);
+    const int c = chunk * 256 + lane * 8;
+    float v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = 0.f;
+    const bool valid = r < N && c < D;                     // D is a multiple of 64: an octet is whole or absent
+    if (valid) {
+        const T *p = x + rows.off(r) + c;
+        if (((uintptr_t)p & 15u) == 0) {
+#pragma unroll
+            for (int i = 0; i < 8 / Elem<T>::kVec; ++i)
+                Elem<T>::unpack(ldg_stream(reinterpret_cast<const uint4 *>(p) + i), v + i * Elem<T>::kVec);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = Elem<T>::load1(p + i);
+        }
+    }
+    uint32_t amax = 0;                                     // bit patterns of |x| order like the values, NaN highest
+#pragma unroll
+    for (int i = 0; i < 8; ++i) amax = max(amax, __float_as_uint(v[i]) & 0x7fffffffu);
+    amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+    amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+    const uint32_t e = amax >> 23;
+    const uint32_t byte = e == 255u ? 255u : e > 2u ? e - 2u : 0u;
+    if (valid) {
+        const float inv = __uint_as_float((254u - min(byte, 253u)) << 23);   // 2^(127 - byte)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = byte == 255u ? 0.f : v[i] * inv;
+        *reinterpret_cast<uint32_t *>(codes + r * (D / 2) + (c >> 1)) = e2m1x8(v);
+    }
+    uint32_t word = valid ? byte << (8 * ((lane >> 2) & 3)) : 0u;
+    word |= __shfl_xor_sync(0xffffffffu, word, 4);
+    word |= __shfl_xor_sync(0xffffffffu, word, 8);
+    const int kt = chunk * 2 + (lane >> 4);
+    if ((lane & 15) == 0 && kt < n_kt) *reinterpret_cast<uint32_t *>(scales + scale_word(r, kt, n_kt)) = word;
+}
+
+cudaError_t launch_mxfp4_quantize(const Mxfp4QuantArgs &a) {
+    const int64_t n_rows = (a.N + 127) / 128 * 128, units = n_rows * ((a.D + 255) / 256);
+    const int64_t blocks = (units + kQThreads / 32 - 1) / (kQThreads / 32);
+    if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
+    const Rows rows{a.R, a.s_o, a.s_i};
+    if (a.bf16)
+        return launch_pdl(mxfp4_quantize_kernel<__nv_bfloat16>, dim3((unsigned)blocks), dim3(kQThreads), 0, a.stream,
+                          static_cast<const __nv_bfloat16 *>(a.x), rows, a.N, n_rows, (int)a.D,
+                          static_cast<uint8_t *>(a.codes), static_cast<uint8_t *>(a.scales));
+    return launch_pdl(mxfp4_quantize_kernel<float>, dim3((unsigned)blocks), dim3(kQThreads), 0, a.stream,
+                      static_cast<const float *>(a.x), rows, a.N, n_rows, (int)a.D, static_cast<uint8_t *>(a.codes),
+                      static_cast<uint8_t *>(a.scales));
+}
+
+// The value of a code times 2^(byte - 127); exact in fp32 (a subnormal scale
+// included), NaN for byte 255.
+__device__ __forceinline__ float e2m1_value(uint32_t code) {
+    // exponent field e and mantissa bit m: e ? (1 + m / 2) 2^(e - 1) : m / 2
+    const uint32_t e = (code >> 1) & 3u, m = code & 1u;
+    const float mag = e ? __uint_as_float(((126u + e) << 23) | (m << 22)) : 0.5f * (float)m;
+    return code & 8u ? -mag : mag;
+}
+
+__device__ __forceinline__ float e8m0_value(uint32_t byte) {
+    return byte == 255u ? qnan() : byte ? __uint_as_float(byte << 23) : __uint_as_float(0x00400000u);
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kQThreads)
+mxfp4_dequantize_kernel(const uint8_t *__restrict__ codes, const uint8_t *__restrict__ scales, int64_t N, int D,
+                        T *__restrict__ out) {
+    pdl_enter<true>();
+    const int n_kt = (D + 127) / 128, per_row = D / 8;
+    const int64_t i = (int64_t)blockIdx.x * kQThreads + threadIdx.x;
+    const int64_t r = i / per_row;
+    if (r >= N) return;
+    const int c = (int)(i - r * per_row) * 8;
+    const uint32_t w = __ldg(reinterpret_cast<const uint32_t *>(codes + r * (D / 2) + (c >> 1)));
+    const float s = e8m0_value(__ldg(scales + scale_word(r, c >> 7, n_kt) + ((c >> 5) & 3)));
+    float v[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] = e2m1_value(w >> (4 * k)) * s;
+    T *p = out + r * (int64_t)D + c;
+#pragma unroll
+    for (int k = 0; k < 8 / Elem<T>::kVec; ++k)
+        stg_stream(reinterpret_cast<uint4 *>(p) + k, Elem<T>::pack(v + k * Elem<T>::kVec));
+}
+
+cudaError_t launch_mxfp4_dequantize(const Mxfp4DequantArgs &a) {
+    const int64_t blocks = (a.N * (a.D / 8) + kQThreads - 1) / kQThreads;
+    if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
+    const uint8_t *codes = static_cast<const uint8_t *>(a.codes), *scales = static_cast<const uint8_t *>(a.scales);
+    if (a.bf16)
+        return launch_pdl(mxfp4_dequantize_kernel<__nv_bfloat16>, dim3((unsigned)blocks), dim3(kQThreads), 0, a.stream,
+                          codes, scales, a.N, (int)a.D, static_cast<__nv_bfloat16 *>(a.out));
+    return launch_pdl(mxfp4_dequantize_kernel<float>, dim3((unsigned)blocks), dim3(kQThreads), 0, a.stream, codes,
+                      scales, a.N, (int)a.D, static_cast<float *>(a.out));
+}
+
+// ---------------------------------------------------------------------------
+// Product: y[n, v] = sum_k x[n, k] w[v, k]
+// ---------------------------------------------------------------------------
+// The vocabulary runs along the MMA's 128 rows (operand A, the accumulator's
+// lanes) and the tokens along its columns (operand B), so that a single token
+// still reads the head at full width and a warp's stores of one token are
+// consecutive. K steps of 64 (kind::mxf4, one scale for each 32 columns);
+// a stage holds 256 columns: 128-byte rows of both operands in the 128-byte
+// swizzle and two scale tiles of each. One thread copies a stage's scales to
+// tensor memory (tcgen05.cp, executed in order with the MMAs that it is followed
+// by; two buffers) and issues the MMAs.
+constexpr int kXM = 128;                     // vocabulary rows of a tile
+constexpr int kXK = 256;                     // columns of a stage
+constexpr int kXRow = kXK / 2;               // their bytes in a row
+constexpr int kXAStage = kXM * kXRow;       // 16 KB
+constexpr int kXSStage = 2 * 512;            // scales of 128 rows
+constexpr int kXThreads = 192;               // TMA warp, MMA warp, 4 epilogue warps
+
+constexpr int x_stage_bytes(int nt) { return kXAStage + nt * kXRow + 2 * kXSStage; }
+constexpr int x_stages(int nt) { return (200 * 1024) / x_stage_bytes(nt) < 10 ? (200 * 1024) / x_stage_bytes(nt) : 10; }
+constexpr int x_smem_bytes(int nt) { return x_stages(nt) * x_stage_bytes(nt) + 1024; }
+constexpr uint32_t x_tmem_cols(int nt) {     // two accumulators, two buffers of 8 + 8 scale columns
+    return 2 * nt + 32 <= 64 ? 64 : 2 * nt + 32 <= 128 ? 128 : 2 * nt + 32 <= 256 ? 256 : 512;
+}
+
+// Instruction descriptor of kind::mxf4: E2M1 operands, both K-major, E8M0 scales.
+__host__ __device__ constexpr uint32_t umma_idesc_mxf4(int M, int N) {
+    return (1u << 7)                        // A format: E2M1            [7, 10)
+           | (1u << 10)                     // B format: E2M1            [10, 12)
+           | ((uint32_t)(N >> 3) << 17)     // N / 8                     [17, 23)
+           | (1u << 23)                     // scale format: E8M0        [23]
+           | ((uint32_t)(M >> 4) << 24);    // M / 16 (M / 128 at bit 27)
+}
+
+// ... with the scales of a K step in byte pair `id` (0 or 2) of their columns.
+__device__ __forceinline__ uint32_t idesc_scale_id(uint32_t idesc, uint32_t id) {
+    return idesc | (id << 4) | (id << 29);   // B's scale id [4, 6), A's [29, 31)
+}
+
+__device__ __forceinline__ void umma_mxf4(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                          uint32_t sfa, uint32_t sfb, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(
+            d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+        : "memory");
+}
+
+// A 512-byte scale tile in shared memory, as 32 rows of 16 bytes: no swizzle,
+// groups of 8 rows 128 bytes apart.
+__device__ __forceinline__ uint64_t scale_desc(const void *smem) {
+    return (uint64_t)((smem_u32(smem) >> 4) & 0x3FFFu) | (uint64_t)(128 >> 4) << 32 | (uint64_t)1 << 46;
+}
+
+// ... to four tensor-memory columns, repeated in the four quarters of the lanes.
+__device__ __forceinline__ void tmem_copy_scales(uint32_t taddr, uint64_t desc) {
+    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+}
+
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float *v) {
+    uint32_t r[16];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr)
+        : "memory");
+    tmem_wait_ld();
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+template <int kNT>
+struct Mxfp4Bars {
+    uint64_t full[x_stages(kNT)], empty[x_stages(kNT)], acc_full[2], acc_empty[2];
+    uint32_t tmem_base;
+};
+
+template <int kNT, typename T>
+__global__ void __launch_bounds__(kXThreads, 1)
+linear_mxfp4_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_x,
+                    const uint8_t *__restrict__ w_scales, const uint8_t *__restrict__ x_scales, int N, int V, int D,
+                    T *__restrict__ y) {
+    constexpr int kStages = x_stages(kNT), kStageBytes = x_stage_bytes(kNT);
+    constexpr uint32_t kScaleCol = 2 * kNT;
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ Mxfp4Bars<kNT> bars;
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int n_vb = (V + kXM - 1) / kXM, n_tb = (N + kNT - 1) / kNT;
+    const int64_t n_tiles = (int64_t)n_vb * n_tb;
+    const int n_k = (D + kXK - 1) / kXK, n_kt = (D + 127) / 128;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(&bars.full[s], 1);
+            mbar_init(&bars.empty[s], 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(&bars.acc_full[b], 1);
+            mbar_init(&bars.acc_empty[b], kXThreads - 64);
+        }
+        fence_mbar_init();
+        prefetch_tensormap(&tm_w);
+        prefetch_tensormap(&tm_x);
+    }
+    if (warp == 1) tmem_alloc(&bars.tmem_base, x_tmem_cols(kNT));
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = bars.tmem_base;
+    pdl_enter<false>();
+
+    if (warp == 0) {
+        if (lane == 0) {
+            const uint64_t pol_w = l2_policy(n_tb > 1 ? 2 : 1), pol_x = l2_policy(2);
+            uint32_t it = 0;
+            bool ok = true;
+            for (int64_t tile = blockIdx.x; tile < n_tiles && ok; tile += gridDim.x) {
+                const int vb = (int)(tile / n_tb), tb = (int)(tile - (int64_t)vb * n_tb);
+                for (int kb = 0; kb < n_k; ++kb, ++it) {
+                    const uint32_t st = it % kStages, use = it / kStages;
+                    if (use > 0 && !mbar_wait(&bars.empty[st], (use - 1) & 1)) { ok = false; break; }
+                    uint8_t *a = smem + st * kStageBytes, *b = a + kXAStage, *sa = b + kNT * kXRow, *sb = sa + kXSStage;
+                    const uint32_t sbytes = 512u * (uint32_t)min(2, n_kt - 2 * kb);
+                    mbar_arrive_expect_tx(&bars.full[st], kXAStage + kNT * kXRow + 2 * sbytes);
+                    tma_load_2d_hint(a, &tm_w, kb * kXRow, vb * kXM, &bars.full[st], pol_w);
+                    tma_load_2d_hint(b, &tm_x, kb * kXRow, tb * kNT, &bars.full[st], pol_x);
+                    bulk_g2s(sa, w_scales + ((int64_t)vb * n_kt + 2 * kb) * 512, sbytes, &bars.full[st], pol_w);
+                    bulk_g2s(sb, x_scales + ((int64_t)(tb * kNT / 128) * n_kt + 2 * kb) * 512, sbytes, &bars.full[st],
+                             pol_x);
+                }
+            }
+            if (!ok) {
+                atomicOr(&g_linear_fault, 1u);
+                // the copies in flight land before the CTA gives up its shared memory
+                for (uint32_t i = it > (uint32_t)kStages ? it - kStages : 0; i < it; ++i)
+                    mbar_wait(&bars.full[i % kStages], (i / kStages) & 1);
+            }
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            constexpr uint32_t idesc = umma_idesc_mxf4(kXM, kNT);
+            uint32_t it = 0, j = 0;
+            bool ok = true;
+            for (int64_t tile = blockIdx.x; tile < n_tiles && ok; tile += gridDim.x, ++j) {
+                const uint32_t buf = j & 1, use_b = j >> 1;
+                if (use_b > 0 && !mbar_wait(&bars.acc_empty[buf], (use_b - 1) & 1)) { ok = false; break; }
+                tc_fence_after();
+                const uint32_t d = tmem + buf * kNT;
+                for (int kb = 0; kb < n_k; ++kb, ++it) {
+                    const uint32_t st = it % kStages;
+                    if (!mbar_wait(&bars.full[st], (it / kStages) & 1)) { ok = false; break; }
+                    tc_fence_after();
+                    const uint8_t *a = smem + st * kStageBytes, *b = a + kXAStage, *sa = b + kNT * kXRow,
+                                  *sb = sa + kXSStage;
+                    const uint32_t sc = tmem + kScaleCol + (it & 1) * 16;
+                    const int steps = min(kXK, D - kb * kXK) / 64;
+                    for (int kt = 0; kt < (steps + 1) / 2; ++kt) {
+                        tmem_copy_scales(sc + 4 * kt, scale_desc(sa + 512 * kt));
+                        tmem_copy_scales(sc + 8 + 4 * kt, scale_desc(sb + 512 * kt));
+                    }
+                    for (int kk = 0; kk < steps; ++kk)
+                        umma_mxf4(d, umma_desc_sw128(a + kk * 32), umma_desc_sw128(b + kk * 32),
+                                  idesc_scale_id(idesc, (kk & 1) * 2), sc + 4 * (kk >> 1), sc + 8 + 4 * (kk >> 1),
+                                  (kb | kk) != 0);
+                    umma_commit(&bars.empty[st]);
+                }
+                umma_commit(&bars.acc_full[buf]);
+            }
+            if (!ok) atomicOr(&g_linear_fault, 2u);
+        }
+    } else {
+        const int q = warp & 3;
+        uint32_t j = 0;
+        bool ok = true;
+        for (int64_t tile = blockIdx.x; tile < n_tiles; tile += gridDim.x, ++j) {
+            const int vb = (int)(tile / n_tb), tb = (int)(tile - (int64_t)vb * n_tb);
+            const uint32_t buf = j & 1;
+            if (ok && !mbar_wait(&bars.acc_full[buf], (j >> 1) & 1)) {
+                ok = false;
+                atomicOr(&g_linear_fault, 4u);
+            }
+            tc_fence_after();
+            if (__all_sync(0xffffffffu, ok)) {
+                const int v = vb * kXM + q * 32 + lane;
+                const int64_t t0 = (int64_t)tb * kNT;
+#pragma unroll 1
+                for (int c = 0; c < kNT && t0 + c < N; c += 16) {
+                    float acc[16];
+                    tmem_ld16(tmem + buf * kNT + c + ((uint32_t)(q * 32) << 16), acc);
+                    T *p = y + (t0 + c) * V + v;
+                    if (v < V) {
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            if (t0 + c + i < N) Elem<T>::store1(p + (int64_t)i * V, acc[i]);
+                    }
+                }
+            }
+            tc_fence_before();
+            mbar_arrive(&bars.acc_empty[buf]);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) tmem_dealloc(tmem, x_tmem_cols(kNT));
+}
+
+// Codes [rows, D / 2] as bytes: boxes of kXRow bytes x box_rows, 128-byte swizzle;
+// zeros (the code of 0) past the extents.
+static bool make_map_codes(CUtensorMap *map, const void *ptr, int64_t rows, int64_t D, int box_rows) {
+    auto enc = encode_fn();
+    if (!enc) return false;
+    cuuint64_t dims[2] = {(cuuint64_t)(D / 2), (cuuint64_t)rows};
+    cuuint64_t strides[1] = {(cuuint64_t)(D / 2)};
+    cuuint32_t box[2] = {(cuuint32_t)kXRow, (cuuint32_t)box_rows};
+    cuuint32_t estr[2] = {1, 1};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(ptr), dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+static int sm_count() {
+    int dev = 0, sms = 0;
+    cudaGetDevice(&dev);
+    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    return std::max(1, sms);
+}
+
+template <int kNT, typename T>
+static cudaError_t launch_linear_t(const LinearMxfp4Args &a) {
+    CUtensorMap tw, tx;
+    if (!make_map_codes(&tw, a.w_codes, a.V, a.D, kXM) || !make_map_codes(&tx, a.x_codes, a.N, a.D, kNT))
+        return cudaErrorInvalidValue;
+    cudaError_t e = cudaFuncSetAttribute(linear_mxfp4_kernel<kNT, T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         x_smem_bytes(kNT));
+    if (e != cudaSuccess) return e;
+    const int64_t n_tiles = ((a.V + kXM - 1) / kXM) * ((a.N + kNT - 1) / kNT);
+    return launch_pdl(linear_mxfp4_kernel<kNT, T>, dim3((unsigned)std::min<int64_t>(n_tiles, sm_count())),
+                      dim3(kXThreads), x_smem_bytes(kNT), a.stream, tw, tx, static_cast<const uint8_t *>(a.w_scales),
+                      static_cast<const uint8_t *>(a.x_scales), (int)a.N, (int)a.V, (int)a.D, static_cast<T *>(a.y));
+}
+
+template <typename T>
+static cudaError_t launch_linear(const LinearMxfp4Args &a) {
+    return a.N <= 16 ? launch_linear_t<16, T>(a)
+           : a.N <= 32 ? launch_linear_t<32, T>(a)
+           : a.N <= 64 ? launch_linear_t<64, T>(a)
+                       : launch_linear_t<128, T>(a);
+}
+
+cudaError_t launch_linear_mxfp4(const LinearMxfp4Args &a) {
+    return a.bf16 ? launch_linear<__nv_bfloat16>(a) : launch_linear<float>(a);
+}
+
+cudaError_t read_linear_mxfp4_fault(uint32_t *value, bool clear) { return read_tu_fault(value, clear); }
+
+}  // namespace vp
