@@ -473,8 +473,8 @@ def test_entry_points_check_arguments_on_the_host():
     assert L.vp_processed_logprobs_fwd(*row, none, FAKE, FAKE, FAKE, FAKE, ctypes.c_size_t(8), None, None) == ERR_ARG
     assert L.vp_processed_logprobs_bwd(*row, none, FAKE, FAKE, None, FAKE, None, None) == ERR_NULL
     assert L.vp_processed_logprobs_bwd(*row, None, FAKE, FAKE, FAKE, FAKE, None, None) == ERR_NULL
-    assert vp.vp_processed_logprobs_workspace_size(3, 8192) == 3 * 40
-    assert vp.vp_processed_logprobs_workspace_size(3, 8193) == 2 * 3 * 40
+    assert vp.vp_processed_logprobs_workspace_size(3, 4096) == 3 * 40
+    assert vp.vp_processed_logprobs_workspace_size(3, 4097) == 2 * 3 * 40
     assert vp.vp_processed_logprobs_workspace_size(3, 0) == 0
 
 

@@ -584,12 +584,13 @@ vp_status vp_fault_status(uint32_t *value, int clear) {
     if (!value) return VP_ERR_NULL;
     vp_status st = check_device();
     if (st != VP_OK) return st;
-    uint32_t a = 0, b = 0, c = 0, d = 0;
+    uint32_t a = 0, b = 0, c = 0, d = 0, e = 0;
     if (vp::read_fault(&a, clear != 0) != cudaSuccess || vp::read_linear_logp_fault(&b, clear != 0) != cudaSuccess ||
         vp::read_linear_ent_kl_fault(&c, clear != 0) != cudaSuccess ||
-        vp::read_linear_mxfp4_fault(&d, clear != 0) != cudaSuccess)
+        vp::read_linear_mxfp4_fault(&d, clear != 0) != cudaSuccess ||
+        vp::read_rules_fault(&e, clear != 0) != cudaSuccess)
         return VP_ERR_LAUNCH;
-    *value = a | ((b | c | d) << 2);
+    *value = a | e | ((b | c | d) << 2);
     return VP_OK;
 }
 

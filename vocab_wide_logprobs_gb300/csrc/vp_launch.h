@@ -212,6 +212,7 @@ struct RuleArgs {
 };
 
 int64_t rule_slices(int64_t V);
+cudaError_t read_rules_fault(uint32_t *value, bool clear);
 cudaError_t launch_process_fwd(const RuleArgs &a);
 cudaError_t launch_process_bwd(const RuleArgs &a);
 cudaError_t launch_processed_logprobs_fwd(const RuleArgs &a, float *logp, void *stats);

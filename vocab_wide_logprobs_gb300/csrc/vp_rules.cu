@@ -9,84 +9,119 @@
 //   y = allowed(j) ? z / T : -inf
 //   f = dy/dx = allowed(j) ? (c_p + c_o > 0 ? (x > 0 ? 1 / rep : rep) : 1) / T : 0
 //
-// Shape: a CTA takes a slice of kSlice columns of one row. Its thread t holds
-// the octets (8 consecutive columns) t, t + 256, ... of the slice in registers,
-// loaded before anything else so that they arrive while the CTA builds its
-// tables in shared memory: a word per column with the number of output
-// occurrences and a prompt bit, a word with the last bias entry, and a bit per
-// column that is set where either is. Integer atomics only, so the order of
-// the ids does not matter. The pass over the octets then looks at one byte of
-// that bitmap and one byte of the mask per octet; only columns with a bit set
-// read the tables.
+// Shape. A tile is a slice of 8192 (bf16) or 4096 (fp32) columns of one row; a
+// CTA works through consecutive tiles (a row's slices follow one another, its
+// rules are read once). One bulk copy brings the next tile to shared memory
+// while this one is worked on. Thread t owns the 16-byte vectors t, t + kThreads,
+// ... of a tile. Of the ids the CTA builds tables for the tile: a word per
+// column with the number of output occurrences and a prompt bit, a word with
+// the last bias entry, and a bit per column that is set where either is.
+// Integer atomics only, so the order of the ids does not matter.
+//   - The vector pass treats every column as if no list named it: a few packed
+//     instructions per vector, one byte (fp32: four bits) of the mask for each.
+//   - The columns that a list names (a few in a hundred) and the target are
+//     walked apart: in the ruled logprobs' forward they are taken out of the
+//     vector pass and their exponentials summed as integers, elsewhere they
+//     overwrite what the vector pass stored. Looking the tables up vector by
+//     vector instead had nearly every warp go through the slow path for a lane
+//     or two.
+// The walk clears the entries that it has read, so the tables are zero again.
+// Of a row whose slices a CTA has several of, the ids are sorted by slice first:
+// going through all of them for every slice cost more than everything else.
 //
 // The ruled logprobs' forward writes one vp_partial record per (slice, row),
-// as a vocabulary shard would, and merge_stats_kernel joins a row's slices.
+// as a vocabulary shard would, and rules_join_kernel joins a row's slices.
 // The slices depend on V alone, so a row's results do not depend on N.
-#include "vp_launch.h"
+#include <atomic>
+
 #include "vp_device.cuh"
+#include "vp_gemm_host.cuh"
+#include "vp_launch.h"
+#include "vp_tma.cuh"
 
 namespace vp {
 
-constexpr int kRuleThreads = 256;
-constexpr int kOctsPerThread = 4;
-constexpr int kSlice = kRuleThreads * kOctsPerThread * 8;   // 8192 columns
 constexpr uint32_t kPromptBit = 0x80000000u;
+
+#ifndef VP_RULE_THREADS
+#define VP_RULE_THREADS 128
+#define VP_RULE_VECS 8
+#endif
+#ifndef VP_RULE_CTAS
+#define VP_RULE_CTAS 3
+#endif
+template <typename T> struct Tile {
+    static constexpr int kThreads = VP_RULE_THREADS, kWarps = kThreads / 32;
+    static constexpr int kVec = Elem<T>::kVec;                // columns of a vector
+    static constexpr int kVecs = VP_RULE_VECS;                // vectors of a thread
+    static constexpr int kWidth = kThreads * kVecs * kVec;    // columns of a tile
+    static constexpr int kWords = kWidth / 32;                // words of the bitmap
+    static constexpr uint32_t kAll = kVec == 8 ? 0xffu : 0xfu;
+};
 
 enum RuleOp { kProcFwd = 0, kProcBwd = 1, kLogpFwd = 2, kLogpBwd = 3 };
 
-// Raw bits of 8 elements: one 16-byte vector of bf16, two of fp32.
-template <typename T> struct Oct {
-    static constexpr int kVecs = sizeof(T) / 2;
-    uint4 u[kVecs];
-};
+__device__ __forceinline__ float to_float(float v) { return v; }
+__device__ __forceinline__ float to_float(__nv_bfloat16 v) { return __bfloat162float(v); }
 
-// Plain (coherent) loads: y may be x.
-__device__ __forceinline__ uint4 ld_once(const void *p) {
-    uint4 r;
-    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
-                 : "l"(p)
+__device__ __forceinline__ void cp_async4(void *smem, const void *p) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"((uint32_t)__cvta_generic_to_shared(smem)), "l"(p)
                  : "memory");
-    return r;
 }
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group 0;" ::: "memory"); }
 
-__device__ __forceinline__ float ld_elem(const float *p) { return *reinterpret_cast<const volatile float *>(p); }
-__device__ __forceinline__ float ld_elem(const __nv_bfloat16 *p) {
-    return __uint_as_float((uint32_t) * reinterpret_cast<const volatile unsigned short *>(p) << 16);
-}
+// Orders this thread's earlier stores to shared memory before later bulk copies there.
+__device__ __forceinline__ void fence_async_proxy() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
-// n valid elements at p (vec: n == 8 and p is 16-byte aligned); the rest is 0.
+// Tile copies. Rows that start on a 16-byte boundary come as one bulk copy, issued
+// by one thread and awaited by all; of others each thread copies its own vectors
+// (word by word where 4-byte alignment allows), which it alone reads before the
+// next barrier. Columns past the last whole vector are stored by the vector's
+// owner in both cases, padded with zeros.
 template <typename T>
-__device__ __forceinline__ void load_oct(Oct<T> &o, const T *p, int n, bool vec) {
-    if (vec && n >= 8) {
+__device__ __forceinline__ void stage_tail(T *stage, const T *p, int width) {
+    const int c = width & ~(Tile<T>::kVec - 1);
+    if (c < width && (c / Tile<T>::kVec) % Tile<T>::kThreads == (int)threadIdx.x) {
 #pragma unroll
-        for (int i = 0; i < Oct<T>::kVecs; ++i) o.u[i] = ld_once(reinterpret_cast<const uint4 *>(p) + i);
+        for (int i = 0; i < Tile<T>::kVec; ++i) stage[c + i] = c + i < width ? p[c + i] : T(0.f);
+        fence_async_proxy();
+    }
+}
+
+template <typename T>
+__device__ __forceinline__ void stage_unaligned(T *stage, const T *p, int width) {
+    const bool words = ((uintptr_t)p & 3u) == 0;
+#pragma unroll 1
+    for (int v = threadIdx.x; (v + 1) * Tile<T>::kVec <= width; v += Tile<T>::kThreads) {
+        const T *src = p + v * Tile<T>::kVec;
+        T *dst = stage + v * Tile<T>::kVec;
+        if (words) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                cp_async4(reinterpret_cast<uint32_t *>(dst) + q, reinterpret_cast<const uint32_t *>(src) + q);
+        } else {
+            T e[Tile<T>::kVec];
+#pragma unroll
+            for (int i = 0; i < Tile<T>::kVec; ++i) e[i] = src[i];
+#pragma unroll
+            for (int i = 0; i < Tile<T>::kVec; ++i) dst[i] = e[i];
+        }
+    }
+    cp_async_commit();
+}
+
+// n >= 1 columns of a vector to p.
+template <typename T>
+__device__ __forceinline__ void store_vec(T *p, const uint4 &u, int n, bool vec) {
+    if (vec && n >= Tile<T>::kVec) {
+        stg_stream(p, u);
         return;
     }
-    float v[8];
+    const T *e = reinterpret_cast<const T *>(&u);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = i < n ? ld_elem(p + i) : 0.f;
-#pragma unroll
-    for (int i = 0; i < Oct<T>::kVecs; ++i) o.u[i] = Elem<T>::pack(v + i * Elem<T>::kVec);
-}
-
-template <typename T>
-__device__ __forceinline__ void unpack_oct(const Oct<T> &o, float (&v)[8]) {
-#pragma unroll
-    for (int i = 0; i < Oct<T>::kVecs; ++i) Elem<T>::unpack(o.u[i], v + i * Elem<T>::kVec);
-}
-
-template <typename T>
-__device__ __forceinline__ void store_oct(T *p, const float (&v)[8], int n, bool vec) {
-    if (vec && n >= 8) {
-#pragma unroll
-        for (int i = 0; i < Oct<T>::kVecs; ++i)
-            stg_stream(reinterpret_cast<uint4 *>(p) + i, Elem<T>::pack(v + i * Elem<T>::kVec));
-        return;
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-        if (i < n) Elem<T>::store1(p + i, v[i]);
+    for (int i = 0; i < Tile<T>::kVec; ++i)
+        if (i < n) p[i] = e[i];
 }
 
 struct RuleKernelArgs {
@@ -103,12 +138,20 @@ struct RuleKernelArgs {
     int32_t *err;
 };
 
-// The rules of one row, read and checked once per CTA.
+// The rules of one row, read and checked when a CTA comes to it, and what else
+// its tiles share.
 struct RowRules {
     bool ok;
-    int64_t first, n_prompt, n_total, bias_first, n_bias;
-    float rep, freq, pres, inv_t;
+    uint32_t n_prompt, n_total, n_bias;
+    float rep, inv_rep, freq, pres, inv_t;
+    const int64_t *ids, *bias_ids;
+    const float *bias_values;
     const uint8_t *mask;      // the row's mask bytes, NULL: everything allowed
+    int target;               // the target's column of this call, -1: not in it
+    bool ignored;             // no target (logprobs)
+    bool nan_row;             // the row's outputs are NaN
+    float m, log_s, scale;    // logprobs backward: log p = (v / T - m) - log_s; scale = -g / T. Elsewhere scale = 1 / T
+    int64_t x_off, out_off;   // the row's first element in x (dy) and in the output
 };
 
 __device__ __forceinline__ bool span_ok(int64_t first, int64_t n, int64_t total) {
@@ -116,24 +159,32 @@ __device__ __forceinline__ bool span_ok(int64_t first, int64_t n, int64_t total)
     return first >= 0 && n >= 0 && n <= 0x7fffffff && n <= total && first <= total - n;
 }
 
-__device__ RowRules row_rules(const RuleSet &q, int64_t r) {
-    RowRules w{true, 0, 0, 0, 0, 0, 1.f, 0.f, 0.f, 1.f, nullptr};
+template <int kOp>
+__device__ RowRules row_rules(const RuleKernelArgs &a, int64_t r) {
+    const RuleSet &q = a.q;
+    RowRules w{};
+    w.ok = true;
+    w.rep = w.inv_rep = w.inv_t = 1.f;
     if (q.spans) {
-        w.first = q.spans[3 * r];
-        w.n_prompt = q.spans[3 * r + 1];
-        w.n_total = q.spans[3 * r + 2];
-        w.ok = span_ok(w.first, w.n_total, q.n_ids) && w.n_prompt >= 0 && w.n_prompt <= w.n_total;
+        const int64_t first = q.spans[3 * r], n_prompt = q.spans[3 * r + 1], n = q.spans[3 * r + 2];
+        w.ok = span_ok(first, n, q.n_ids) && n_prompt >= 0 && n_prompt <= n;
+        w.ids = q.ids + first;
+        w.n_prompt = (uint32_t)n_prompt;
+        w.n_total = (uint32_t)n;
         if (q.repetition) {
             w.rep = q.repetition[r];
+            w.inv_rep = 1.f / w.rep;
             w.ok = w.ok && w.rep > 0.f && w.rep < pinf();
         }
         if (q.frequency) w.freq = q.frequency[r];
         if (q.presence) w.pres = q.presence[r];
     }
     if (q.bias_spans) {
-        w.bias_first = q.bias_spans[2 * r];
-        w.n_bias = q.bias_spans[2 * r + 1];
-        w.ok = w.ok && span_ok(w.bias_first, w.n_bias, q.n_bias);
+        const int64_t first = q.bias_spans[2 * r], n = q.bias_spans[2 * r + 1];
+        w.ok = w.ok && span_ok(first, n, q.n_bias);
+        w.bias_ids = q.bias_ids + first;
+        w.bias_values = q.bias_values + first;
+        w.n_bias = (uint32_t)n;
     }
     if (q.temperature) {
         const float t = q.temperature[r];
@@ -145,236 +196,588 @@ __device__ RowRules row_rules(const RuleSet &q, int64_t r) {
         w.ok = w.ok && m >= -1 && m < q.n_masks;
         if (w.ok && m >= 0) w.mask = reinterpret_cast<const uint8_t *>(q.mask + m * q.mask_stride);
     }
-    if (!w.ok) w.n_total = w.n_bias = 0;
+    if (!w.ok) w.n_total = w.n_bias = 0u;
+    w.target = -1;
+    w.nan_row = !w.ok;
+    w.scale = w.inv_t;
+    w.x_off = a.xrows.off(r);
+    w.out_off = kOp == kProcFwd ? a.orows.off(r) : r * a.V;
+    if (kOp >= kLogpFwd) {
+        const int64_t tg = a.targets[r], tl = tg - a.vocab_start;
+        w.ignored = tg < 0;
+        if (tg >= 0 && tl >= 0 && tl < a.V) w.target = (int)tl;
+    }
+    if (kOp == kLogpBwd) {
+        const RowStat st = load_rowstat(a.stats + r);
+        w.nan_row = !w.ignored && (!w.ok || (st.flags & (kRowNanInf | kRowEmpty | kRowBadTarget)) != 0);
+        w.scale = w.ignored ? 0.f : -a.g[r] * w.inv_t;
+        w.m = st.m;
+        w.log_s = st.logS_hi;
+    }
     return w;
 }
 
+// The exponential of an element type, of t = u log p: bf16 takes the hardware's
+// 2^t (u = log2 e), fp32 e^t (u = 1).
+template <typename T> struct Scaled;
+template <> struct Scaled<__nv_bfloat16> {
+    static constexpr float kUnit = kLog2e;
+    static __device__ __forceinline__ float exp(float t) {
+        float y;
+        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(t));
+        return y;
+    }
+};
+template <> struct Scaled<float> {
+    static constexpr float kUnit = 1.f;
+    static __device__ __forceinline__ float exp(float t) { return expf(t); }
+};
+// ... of both values of a pair
+template <typename T>
+__device__ __forceinline__ float2 scaled_exp2(float2 t) {
+    return make_float2(Scaled<T>::exp(t.x), Scaled<T>::exp(t.y));
+}
+
+// Columns of a vector whose bit in `on` is clear become `off` (the bits of a
+// value, twice for bf16). bf16 takes the vector's keep words from a table of all
+// bytes in shared memory.
+template <typename T>
+__device__ __forceinline__ uint4 keep_vec(uint4 u, uint32_t on, uint32_t off, const uint4 *keep_words) {
+    if (sizeof(T) == 2) {
+        const uint4 k = keep_words[on];
+        return make_uint4((u.x & k.x) | (off & ~k.x), (u.y & k.y) | (off & ~k.y), (u.z & k.z) | (off & ~k.z),
+                          (u.w & k.w) | (off & ~k.w));
+    }
+    return make_uint4(on & 1u ? u.x : off, on & 2u ? u.y : off, on & 4u ? u.z : off, on & 8u ? u.w : off);
+}
+
+template <typename T> __device__ __forceinline__ uint32_t minus_inf_bits() {
+    return sizeof(T) == 2 ? 0xff80ff80u : 0xff800000u;
+}
+
+// The largest of a vector's values; NaN is passed over.
+template <typename T> __device__ __forceinline__ float vec_max(const uint4 &u) {
+    if (sizeof(T) == 2) {
+        const __nv_bfloat162 *p = reinterpret_cast<const __nv_bfloat162 *>(&u);
+        const __nv_bfloat162 m = __hmax2(__hmax2(p[0], p[1]), __hmax2(p[2], p[3]));
+        return fmaxf(__low2float(m), __high2float(m));
+    }
+    return fmaxf(fmaxf(__uint_as_float(u.x), __uint_as_float(u.y)), fmaxf(__uint_as_float(u.z), __uint_as_float(u.w)));
+}
+
+// Listed columns of a tile that are kept as a list; with more of them the bitmap
+// is walked instead. Ids of a row that a CTA keeps, sorted by slice.
+constexpr int kListed = 512, kRowIds = 2048, kSegment = 64;
+// The listed columns' exponentials are summed as integers, in units of 2^-48 of
+// the tile's largest, so that the order they are found in does not matter.
+constexpr float kFixed = 281474976710656.f;   // 2^48
+
+template <typename T>
+struct RuleSmem {
+    T stage[2][Tile<T>::kWidth];
+    uint4 keep_words[sizeof(T) == 2 ? 256 : 1];
+    uint64_t full[2];
+    unsigned long long listed_sum[2][Tile<T>::kWarps];
+    uint32_t touched[Tile<T>::kWords];
+    float red_top[2][Tile<T>::kWarps], red_all[2][Tile<T>::kWarps], red_s[2][Tile<T>::kWarps], target_z[2];
+    uint32_t n_listed[2];
+    uint32_t segment[kSegment + 1];                       // where a slice's ids begin in row_ids; counters before that
+    uint16_t listed[kListed];
+    uint16_t row_ids[kRowIds];                            // column of the slice, bit 15: prompt
+    // counts [kWidth] and, with a bias list, entries [kWidth] follow
+};
+
 template <typename T, int kOp>
-__global__ void __launch_bounds__(kRuleThreads) rules_kernel(const RuleKernelArgs a) {
-    extern __shared__ uint32_t tables[];                 // counts [kSlice], then (with a bias list) entries [kSlice]
-    __shared__ uint32_t touched[kSlice / 32];
-    __shared__ float red_m[kRuleThreads / 32];
-    __shared__ double red_s[kRuleThreads / 32];
-    __shared__ uint32_t red_flags;
-    __shared__ float target_z;
+__global__ void __launch_bounds__(Tile<T>::kThreads, VP_RULE_CTAS) rules_kernel(const __grid_constant__ RuleKernelArgs a) {
+    extern __shared__ __align__(16) uint8_t smem_raw[];
+    constexpr int kThreads = Tile<T>::kThreads, kVec = Tile<T>::kVec, kVecs = Tile<T>::kVecs, kSlice = Tile<T>::kWidth,
+                  kWords = Tile<T>::kWords, kWarps = Tile<T>::kWarps;
+    RuleSmem<T> &sm = *reinterpret_cast<RuleSmem<T> *>(smem_raw);
+    uint32_t *const counts = reinterpret_cast<uint32_t *>(smem_raw + sizeof(RuleSmem<T>)), *const entries = counts + kSlice;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint8_t *const touched8 = reinterpret_cast<const uint8_t *>(sm.touched);
+    const bool tabled = a.q.spans != nullptr, biased = a.q.bias_spans != nullptr;
+
+    // the tables are cleared once; a tile clears what it touched
+    for (int i = tid; i < kWords; i += kThreads) sm.touched[i] = 0u;
+    for (int i = tid; i < (biased ? 2 : tabled ? 1 : 0) * (kSlice / 4); i += kThreads)
+        reinterpret_cast<uint4 *>(counts)[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (sizeof(T) == 2)
+        for (int b = tid; b < 256; b += kThreads) {
+            uint32_t k[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                k[i] = (b >> (2 * i) & 1 ? 0xffffu : 0u) | (b >> (2 * i + 1) & 1 ? 0xffff0000u : 0u);
+            sm.keep_words[b] = make_uint4(k[0], k[1], k[2], k[3]);
+        }
+    if (tid < 2) sm.n_listed[tid] = 0u;
+    if (tid == 0) {
+        mbar_init(&sm.full[0], 1);
+        mbar_init(&sm.full[1], 1);
+        fence_mbar_init();
+    }
     pdl_enter<kOp != kLogpFwd>();
 
-    const int tid = threadIdx.x;
     const int64_t total = a.N * a.n_slices;
-    uint32_t *const counts = tables, *const entries = tables + kSlice;
-    for (int64_t tile = blockIdx.x; tile < total; tile += gridDim.x) {
-        const int64_t r = tile / a.n_slices;
-        const int slice = (int)(tile - r * a.n_slices);
-        const int s0 = slice * kSlice;
-        const int width = min(kSlice, a.V - s0);          // columns of this slice
-        const T *xrow = static_cast<const T *>(a.x) + a.xrows.off(r) + s0;
-        const bool xvec = ((uintptr_t)xrow & 15u) == 0;
+    const int64_t per = total / gridDim.x, more = total - per * gridDim.x;
+    int64_t tile = blockIdx.x * per + min((int64_t)blockIdx.x, more);
+    const int64_t end = tile + per + (blockIdx.x < more ? 1 : 0);
+    int64_t r = tile / a.n_slices;
+    int slice = (int)(tile - r * a.n_slices);
+    const uint64_t policy = policy_evict_first();
+    // bit b: buffer b's last tile came as a bulk copy; the parity of the phase that such a copy completes next
+    uint32_t bulk = 0u, parity = 0u;
+    bool arrived = true, fresh = true, sorted = false;   // fresh: the CTA's first tile of this row
+    int seg0 = 0;                                        // ... was this slice
 
-        // ---- the slice's logits (dy for the gradient of the rules), in flight from here
-        Oct<T> raw[kOctsPerThread];
-        const T *main_row = kOp == kProcBwd ? static_cast<const T *>(a.dy) + r * a.V + s0 : xrow;
-        const bool mvec = kOp == kProcBwd ? ((uintptr_t)main_row & 15u) == 0 : xvec;
-#pragma unroll
-        for (int k = 0; k < kOctsPerThread; ++k) {
-            const int c = (k * kRuleThreads + tid) * 8;
-            load_oct(raw[k], main_row + c, width - c, mvec);
-        }
-        const RowRules w = row_rules(a.q, r);
-        uint32_t allow[kOctsPerThread];
-#pragma unroll
-        for (int k = 0; k < kOctsPerThread; ++k) {
-            const int c = (k * kRuleThreads + tid) * 8;
-            allow[k] = w.mask && c < width ? __ldg(w.mask + ((s0 + c) >> 3)) : 0xffu;
-        }
-        if (!w.ok && slice == 0 && tid == 0 && a.err) atomicOr(a.err, VP_ERRBIT_RULES_);
-
-        // ---- tables
-        const bool listed = w.n_total > 0 || w.n_bias > 0;   // uniform in the CTA
-        if (listed) {
-            for (int i = tid; i < kSlice / 32; i += kRuleThreads) touched[i] = 0u;
-            if (w.n_total > 0)
-                for (int i = tid; i < kSlice / 4; i += kRuleThreads)
-                    reinterpret_cast<uint4 *>(counts)[i] = make_uint4(0u, 0u, 0u, 0u);
-            if (w.n_bias > 0)
-                for (int i = tid; i < kSlice / 4; i += kRuleThreads)
-                    reinterpret_cast<uint4 *>(entries)[i] = make_uint4(0u, 0u, 0u, 0u);
-            __syncthreads();
-            const uint64_t base = (uint64_t)a.vocab_start + (uint64_t)s0;
-            const int64_t *ids = a.q.ids + w.first;
-            constexpr int kUnroll = 4;
-            for (int64_t i0 = tid; i0 < w.n_total; i0 += kUnroll * kRuleThreads) {
-                int64_t id[kUnroll];
-#pragma unroll
-                for (int u = 0; u < kUnroll; ++u) {
-                    const int64_t i = i0 + u * kRuleThreads;
-                    id[u] = i < w.n_total ? __ldg(ids + i) : -1;
-                }
-#pragma unroll
-                for (int u = 0; u < kUnroll; ++u) {
-                    const uint64_t l = (uint64_t)id[u] - base;
-                    if (id[u] < 0 || l >= (uint64_t)width) continue;
-                    if (i0 + u * kRuleThreads < w.n_prompt) atomicOr(&counts[l], kPromptBit);
-                    else atomicAdd(&counts[l], 1u);
-                    atomicOr(&touched[l >> 5], 1u << (l & 31));
-                }
-            }
-            for (int64_t i = tid; i < w.n_bias; i += kRuleThreads) {
-                const int64_t id = __ldg(a.q.bias_ids + w.bias_first + i);
-                const uint64_t l = (uint64_t)id - base;
-                if (id < 0 || l >= (uint64_t)width) continue;
-                atomicMax(&entries[l], (uint32_t)i + 1u);
-                atomicOr(&touched[l >> 5], 1u << (l & 31));
-            }
-            __syncthreads();
-        }
-
-        // z and f of column l (0 <= l < width) whose bit is set, from x
-        auto ruled = [&](int l, float x, float &f) {
-            float z = x;
-            f = 1.f;
-            if (w.n_total > 0) {
-                const uint32_t c = counts[l];
-                if (c) {
-                    z = x > 0.f ? x / w.rep : x * w.rep;
-                    f = x > 0.f ? 1.f / w.rep : w.rep;
-                }
-                const uint32_t n = c & ~kPromptBit;
-                if (n) z = z - w.freq * (float)n - w.pres;
-            }
-            if (w.n_bias > 0) {
-                const uint32_t e = entries[l];
-                if (e) z += __ldg(a.q.bias_values + w.bias_first + (e - 1));
-            }
-            return z;
-        };
-
-        if constexpr (kOp == kProcFwd || kOp == kProcBwd) {
-            T *orow = static_cast<T *>(a.out) + (kOp == kProcFwd ? a.orows.off(r) : r * a.V) + s0;
-            const bool ovec = ((uintptr_t)orow & 15u) == 0;
-#pragma unroll
-            for (int k = 0; k < kOctsPerThread; ++k) {
-                const int o = k * kRuleThreads + tid, c = o * 8;
-                if (c >= width) break;
-                float v[8];
-                unpack_oct(raw[k], v);
-                const uint32_t hit = listed ? reinterpret_cast<const uint8_t *>(touched)[o] : 0u;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    if (hit >> i & 1u) {
-                        float f;
-                        if (kOp == kProcFwd) v[i] = ruled(c + i, v[i], f);
-                        else { ruled(c + i, ld_elem(xrow + c + i), f); v[i] *= f; }
-                    }
-                    v[i] *= w.inv_t;
-                    if (!(allow[k] >> i & 1u)) v[i] = kOp == kProcFwd ? -pinf() : 0.f;
-                    if (!w.ok) v[i] = qnan();
-                }
-                store_oct(orow + c, v, width - c, ovec);
-            }
-        } else if constexpr (kOp == kLogpFwd) {
-            float z[kOctsPerThread][8];
-            float m = kNegBig;
-            uint32_t flags = w.ok ? 0u : kPartNanInf;
-            const int64_t tg = a.targets[r];
-            const int64_t tl = tg - a.vocab_start - s0;      // the target's column in this slice, if any
-            const bool has_target = tg >= 0 && tl >= 0 && tl < width;
-#pragma unroll
-            for (int k = 0; k < kOctsPerThread; ++k) {
-                const int o = k * kRuleThreads + tid, c = o * 8;
-                unpack_oct(raw[k], z[k]);
-                const uint32_t hit = listed ? reinterpret_cast<const uint8_t *>(touched)[o] : 0u;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    float f;
-                    if (hit >> i & 1u) z[k][i] = ruled(c + i, z[k][i], f);
-                    z[k][i] *= w.inv_t;
-                    if (!(allow[k] >> i & 1u) || c + i >= width) z[k][i] = -pinf();
-                    if (!(z[k][i] < pinf())) flags = kPartNanInf;      // NaN or +inf
-                    m = fmaxf(m, z[k][i]);
-                    if (has_target && c + i == (int)tl) target_z = z[k][i];
-                }
-            }
-            m = warp_max(m);
-            if (tid == 0) red_flags = 0u;
-            if ((tid & 31) == 0) red_m[tid >> 5] = m;
-            __syncthreads();
-#pragma unroll
-            for (int i = 0; i < kRuleThreads / 32; ++i) m = fmaxf(m, red_m[i]);
-            if (flags) atomicOr(&red_flags, flags);
-            float s = 0.f;
-#pragma unroll
-            for (int k = 0; k < kOctsPerThread; ++k)
-#pragma unroll
-                for (int i = 0; i < 8; ++i) s += Elem<T>::exp(z[k][i] - m);
-            double sd = warp_sum((double)s);
-            if ((tid & 31) == 0) red_s[tid >> 5] = sd;
-            __syncthreads();
+    // brings a tile of a row's logits (dy for the gradient of the rules)
+    auto stage = [&](int buf, const RowRules &w, int sl) {
+        const int s0 = sl * kSlice, width = min(kSlice, a.V - s0);
+        const T *p = (kOp == kProcBwd ? static_cast<const T *>(a.dy) + w.out_off : static_cast<const T *>(a.x) + w.x_off) + s0;
+        const bool aligned = ((uintptr_t)p & 15u) == 0 && width >= kVec;
+        bulk = (bulk & ~(1u << buf)) | ((uint32_t)aligned << buf);
+        if (aligned) {
             if (tid == 0) {
-                sd = 0.0;
-                for (int i = 0; i < kRuleThreads / 32; ++i) sd += red_s[i];
-                flags = red_flags;
-                if (tg < 0) flags |= kPartIgnored;
-                if (has_target) flags |= kPartHasTarget;
-                a.parts[(int64_t)slice * a.N + r] = PartialRec{m, kNegBig, sd, 0.0, 0.0, has_target ? target_z : 0.f, flags};
+                const uint32_t bytes = (uint32_t)(width / kVec) * 16u;
+                mbar_arrive_expect_tx(&sm.full[buf], bytes);
+                bulk_g2s(sm.stage[buf], p, bytes, &sm.full[buf], policy);
             }
         } else {
-            const RowStat st = load_rowstat(a.stats + r);
-            const int64_t tg = a.targets[r];
-            const int64_t tl = tg - a.vocab_start - s0;
-            const bool ignored = tg < 0;
-            const bool nan_row = !ignored && (!w.ok || (st.flags & (kRowNanInf | kRowEmpty | kRowBadTarget)) != 0);
-            const int target = !ignored && tl >= 0 && tl < width ? (int)tl : -1;
-            const float g = ignored ? 0.f : a.g[r];
-            T *orow = static_cast<T *>(a.out) + r * a.V + s0;
-            const bool ovec = ((uintptr_t)orow & 15u) == 0;
+            stage_unaligned(sm.stage[buf], p, width);
+        }
+        stage_tail(sm.stage[buf], p, width);
+    };
+    // this thread's mask bits of a tile, vector k in byte k % 4 of word k / 4
+    struct Allow { uint32_t b[(kVecs + 3) / 4]; };
+    auto mask_bits = [&](const RowRules &w, int sl) {
+        Allow m;
 #pragma unroll
-            for (int k = 0; k < kOctsPerThread; ++k) {
-                const int o = k * kRuleThreads + tid, c = o * 8;
-                if (c >= width) break;
-                float v[8];
-                unpack_oct(raw[k], v);
-                const uint32_t hit = listed ? reinterpret_cast<const uint8_t *>(touched)[o] : 0u;
+        for (int k = 0; k < (kVecs + 3) / 4; ++k) m.b[k] = w.mask ? 0u : 0x01010101u * Tile<T>::kAll;
+        if (w.mask) {
+            const int o = (sl * kSlice + tid * kVec) >> 3, n = (a.V + 7) >> 3, sh = kVec == 8 ? 0 : (tid & 1) * 4;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    float f = 1.f;
-                    if (hit >> i & 1u) v[i] = ruled(c + i, v[i], f);
-                    const float d = ((v[i] * w.inv_t - st.m) - st.logS_hi) - st.logS_lo;     // log p
-                    f *= w.inv_t * g;
-                    v[i] = c + i == target ? -f * expm1f(d) : -f * Elem<T>::exp(d);
-                    if (!(allow[k] >> i & 1u) || ignored) v[i] = 0.f;
-                    if (nan_row) v[i] = qnan();
-                }
-                store_oct(orow + c, v, width - c, ovec);
+            for (int k = 0; k < kVecs; ++k) {
+                const int at = o + k * (kThreads * kVec / 8);
+                if (at < n) m.b[k / 4] |= ((uint32_t)__ldg(w.mask + at) >> sh & Tile<T>::kAll) << (8 * (k % 4));
             }
         }
-        if (tile + gridDim.x < total) __syncthreads();    // the tables are used again
+        return m;
+    };
+    RowRules w = row_rules<kOp>(a, r), next_w = w;
+    __syncthreads();                                     // the barriers are set up, the tables clear
+    stage(0, w, slice);
+    Allow allow = mask_bits(w, slice);
+
+    for (int buf = 0; tile < end; ++tile, buf ^= 1) {
+        const int s0 = slice * kSlice;
+        const int width = min(kSlice, a.V - s0);          // columns of this slice
+        const T *xrow = static_cast<const T *>(a.x) + w.x_off + s0;
+        const T *const st = sm.stage[buf];
+        if (!w.ok && slice == 0 && tid == 0 && a.err) atomicOr(a.err, VP_ERRBIT_RULES_);
+        // the target's column in this slice, if it lies here
+        const int target = kOp >= kLogpFwd && w.target >= s0 && w.target - s0 < width ? w.target - s0 : -1;
+
+        // ---- the next tile (every thread is done with the other buffer)
+        const bool row_ends = slice + 1 == a.n_slices;
+        const int next_slice = row_ends ? 0 : slice + 1;
+        Allow next_allow = allow;
+        const bool bulked = bulk >> buf & 1u;
+        if (!bulked) {
+            cp_async_wait();
+            fence_async_proxy();                          // a bulk copy may write there next
+        }
+        if (tile + 1 < end) {
+            if (row_ends) next_w = row_rules<kOp>(a, r + 1);
+            stage(buf ^ 1, row_ends ? next_w : w, next_slice);
+            next_allow = mask_bits(row_ends ? next_w : w, next_slice);
+        }
+
+        // ---- a row that this CTA has several slices of: its ids are sorted by slice once
+        if (fresh) {
+            fresh = false;
+            seg0 = slice;
+            const int64_t left = end - tile;
+            const int slices = (int)min(left, a.n_slices - (int64_t)slice);
+            sorted = w.n_total > 0u && slices > 1 && slices <= kSegment;
+            if (sorted) {
+                const uint64_t base = (uint64_t)a.vocab_start + (uint64_t)s0;
+                const uint64_t reach = (uint64_t)min((int64_t)slices * kSlice, (int64_t)a.V - s0);
+                // f(column past s0, index) for every id in reach
+                auto each = [&](auto f) {
+                    constexpr uint32_t kUnroll = 8;
+#pragma unroll 1
+                    for (uint32_t i0 = tid; i0 < w.n_total; i0 += kUnroll * kThreads) {
+                        uint64_t l[kUnroll];
+#pragma unroll
+                        for (uint32_t u = 0; u < kUnroll; ++u) {
+                            const uint32_t i = i0 + u * kThreads;
+                            l[u] = i < w.n_total ? (uint64_t)__ldg(w.ids + i) - base : ~0ull;
+                        }
+#pragma unroll
+                        for (uint32_t u = 0; u < kUnroll; ++u)
+                            if (l[u] < reach) f((uint32_t)l[u], i0 + u * kThreads);
+                    }
+                };
+                for (int i = tid; i <= kSegment; i += kThreads) sm.segment[i] = 0u;
+                __syncthreads();
+                each([&](uint32_t l, uint32_t) { atomicAdd(&sm.segment[l / kSlice + 1], 1u); });
+                __syncthreads();
+                if (warp == 0) {                          // counts to beginnings
+                    uint32_t lo = sm.segment[1 + lane], hi = sm.segment[33 + lane];
+#pragma unroll
+                    for (int d = 1; d < 32; d <<= 1) {
+                        const uint32_t a0 = __shfl_up_sync(0xffffffffu, lo, d), b0 = __shfl_up_sync(0xffffffffu, hi, d);
+                        if (lane >= d) { lo += a0; hi += b0; }
+                    }
+                    hi += __shfl_sync(0xffffffffu, lo, 31);
+                    sm.segment[1 + lane] = lo;
+                    sm.segment[33 + lane] = hi;
+                }
+                __syncthreads();
+                sorted = sm.segment[kSegment] <= (uint32_t)kRowIds;   // no cursor below is this one
+                if (sorted) {                             // the beginnings move to the ends as the ids are placed
+                    each([&](uint32_t l, uint32_t i) {
+                        const uint32_t at = atomicAdd(&sm.segment[l / kSlice], 1u);
+                        sm.row_ids[at] = (uint16_t)(l % kSlice | (i < w.n_prompt ? 0x8000u : 0u));
+                    });
+                    __syncthreads();
+                }
+            }
+        }
+
+        // ---- tables (the target is listed too, without an entry)
+        const bool listed = (w.n_total | w.n_bias) != 0u || target >= 0;    // uniform in the CTA
+        if (listed) {
+            auto mark = [&](uint32_t c) {
+                const uint32_t bit = 1u << (c & 31);
+                if (atomicOr(&sm.touched[c >> 5], bit) & bit) return;
+                const uint32_t at = atomicAdd(&sm.n_listed[buf], 1u);
+                if (at < (uint32_t)kListed) sm.listed[at] = (uint16_t)c;
+                if (kOp == kProcBwd) asm volatile("prefetch.global.L2 [%0];" ::"l"(xrow + c));
+            };
+            auto enter = [&](uint32_t c, bool prompt) {
+                if (prompt) atomicOr(&counts[c], kPromptBit);
+                else atomicAdd(&counts[c], 1u);
+                mark(c);
+            };
+            if (tid == 0 && target >= 0) mark((uint32_t)target);
+            const uint64_t base = (uint64_t)a.vocab_start + (uint64_t)s0;   // negative ids come out far above any width
+            if (sorted) {
+                const int k = slice - seg0;
+                const uint32_t to = sm.segment[k];
+                for (uint32_t i = (k ? sm.segment[k - 1] : 0u) + tid; i < to; i += kThreads)
+                    enter(sm.row_ids[i] & 0x7fffu, sm.row_ids[i] >> 15);
+            } else {
+                constexpr uint32_t kUnroll = 8;
+#pragma unroll 1
+                for (uint32_t i0 = tid; i0 < w.n_total; i0 += kUnroll * kThreads) {
+                    uint64_t l[kUnroll];
+#pragma unroll
+                    for (uint32_t u = 0; u < kUnroll; ++u) {
+                        const uint32_t i = i0 + u * kThreads;
+                        l[u] = i < w.n_total ? (uint64_t)__ldg(w.ids + i) - base : ~0ull;
+                    }
+#pragma unroll
+                    for (uint32_t u = 0; u < kUnroll; ++u)
+                        if (l[u] < (uint64_t)width) enter((uint32_t)l[u], i0 + u * kThreads < w.n_prompt);
+                }
+            }
+#pragma unroll 1
+            for (uint32_t i = tid; i < w.n_bias; i += kThreads) {
+                const uint64_t l = (uint64_t)__ldg(w.bias_ids + i) - base;
+                if (l >= (uint64_t)width) continue;
+                atomicMax(&entries[(uint32_t)l], i + 1u);
+                mark((uint32_t)l);
+            }
+        }
+        if (bulked) {
+            if (!mbar_wait(&sm.full[buf], parity >> buf & 1u)) arrived = false;
+            parity ^= 1u << buf;
+        }
+        if (listed) __syncthreads();                      // the tables, and what other threads copied
+        const uint32_t n_listed = listed ? sm.n_listed[buf] : 0u;
+        // f(column) for each listed column, by some thread
+        auto walk = [&](auto f) {
+            if (n_listed <= (uint32_t)kListed) {
+                for (uint32_t i = tid; i < n_listed; i += kThreads) f((int)sm.listed[i]);
+            } else {
+                for (int i = tid; i < kWords; i += kThreads)
+                    for (uint32_t bits = sm.touched[i]; bits; bits &= bits - 1) f(i * 32 + __ffs(bits) - 1);
+            }
+        };
+        // after the walk's last use of the bitmap
+        auto clear = [&]() {
+            if (n_listed <= (uint32_t)kListed) {
+                for (uint32_t i = tid; i < n_listed; i += kThreads) sm.touched[sm.listed[i] >> 5] = 0u;
+            } else {
+                for (int i = tid; i < kWords; i += kThreads) sm.touched[i] = 0u;
+            }
+        };
+
+        // v before the temperature, and f, of a listed column l from x; clears the column's entries if told to
+        auto ruled = [&](int l, float x, float &f, bool last) {
+            uint32_t c = 0u;
+            if (tabled) {
+                c = counts[l];
+                if (last) counts[l] = 0u;
+            }
+            const uint32_t n = c & ~kPromptBit;
+            f = c == 0u ? 1.f : x > 0.f ? w.inv_rep : w.rep;
+            float v = x * f;
+            if (n) v = fmaf(-w.freq, (float)n, v) - w.pres;
+            if (biased) {
+                const uint32_t e = entries[l];
+                if (last) entries[l] = 0u;
+                if (e) v += __ldg(w.bias_values + (e - 1));
+            }
+            return v;
+        };
+        auto allowed = [&](int l) { return !w.mask || (__ldg(w.mask + ((s0 + l) >> 3)) >> (l & 7) & 1); };
+
+        if constexpr (kOp == kLogpFwd) {
+            // Exponentials of u (v - top) / T, top the largest v before the temperature:
+            // v - top is exact where it matters and cannot overflow upwards. Each thread
+            // sums against its own top; warps and CTA join in a fixed order. NaN or +inf
+            // make the sum NaN.
+            const float c1 = w.inv_t * Scaled<T>::kUnit;
+            float top = kNegBig, ltop = kNegBig, s = 0.f;   // ltop: of the listed columns, whoever finds them
+            auto listed_value = [&](int l, bool last) {
+                float f, v = ruled(l, to_float(st[l]), f, last);
+                return allowed(l) ? v : -pinf();
+            };
+            walk([&](int l) {
+                const float v = listed_value(l, false);
+                if (!(v < pinf())) s = qnan();
+                ltop = fmaxf(ltop, v);
+                if (l == target) sm.target_z[buf] = v * w.inv_t;
+            });
+            uint4 u[kVecs];
+#pragma unroll
+            for (int k = 0; k < kVecs; ++k) {
+                const int o = k * kThreads + tid, n = width - o * kVec;
+                const uint32_t off = minus_inf_bits<T>();
+                u[k] = make_uint4(off, off, off, off);
+                if (n > 0) {
+                    u[k] = reinterpret_cast<const uint4 *>(st)[o];
+                    uint32_t on = allow.b[k / 4] >> (8 * (k % 4)) & Tile<T>::kAll;
+                    if (listed) on &= kVec == 8 ? ~(uint32_t)touched8[o] : ~((uint32_t)touched8[o >> 1] >> ((tid & 1) * 4));
+                    if (n < kVec) on &= (1u << n) - 1u;
+                    if (on != Tile<T>::kAll) u[k] = keep_vec<T>(u[k], on, off, sm.keep_words);
+                }
+                top = fmaxf(top, vec_max<T>(u[k]));
+            }
+            float2 e = make_float2(s, 0.f);
+#pragma unroll
+            for (int k = 0; k < kVecs; ++k) {
+                float v[kVec];
+                Elem<T>::unpack(u[k], v);
+#pragma unroll
+                for (int i = 0; i < kVec; i += 2)
+                    e = __fadd2_rn(e, scaled_exp2<T>(__fmul2_rn(__fadd2_rn(make_float2(v[i], v[i + 1]), f2(-top)), f2(c1))));
+            }
+            s = e.x + e.y;
+            const float wtop = warp_max(top);
+            s *= Scaled<T>::exp((top - wtop) * c1);
+#pragma unroll
+            for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
+            if (listed) ltop = warp_max(ltop);
+            if (lane == 0) {
+                sm.red_top[buf][warp] = wtop;
+                sm.red_all[buf][warp] = fmaxf(wtop, ltop);
+                sm.red_s[buf][warp] = s;
+            }
+            __syncthreads();                              // and every thread is done with the bitmap
+            float m = sm.red_all[buf][0];
+#pragma unroll
+            for (int i = 1; i < kWarps; ++i) m = fmaxf(m, sm.red_all[buf][i]);
+            if (listed) {
+                unsigned long long sum = 0ull;
+                walk([&](int l) { sum += __float2ull_rn(Scaled<T>::exp((listed_value(l, true) - m) * c1) * kFixed); });
+#pragma unroll
+                for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+                if (lane == 0) sm.listed_sum[buf][warp] = sum;
+                if (n_listed > (uint32_t)kListed) __syncthreads();   // the walk reads every word of the bitmap
+                clear();
+                if (tid == 0) sm.n_listed[buf] = 0u;
+                __syncthreads();                          // the sum is whole, the tables are clear
+            }
+            if (tid == 0) {
+                float t = 0.f;
+#pragma unroll
+                for (int i = 0; i < kWarps; ++i) t += sm.red_s[buf][i] * Scaled<T>::exp((sm.red_top[buf][i] - m) * c1);
+                if (listed) {
+                    unsigned long long sum = 0ull;
+#pragma unroll
+                    for (int i = 0; i < kWarps; ++i) sum += sm.listed_sum[buf][i];
+                    t += __ull2float_rn(sum) * (1.f / kFixed);
+                }
+                uint32_t flags = !w.ok || t != t ? kPartNanInf : 0u;
+                if (w.ignored) flags |= kPartIgnored;
+                if (target >= 0) flags |= kPartHasTarget;
+                // the record's maximum is after the temperature: what its rounding takes away (exact in the
+                // FMA) goes into the sum
+                float mz = kNegBig;
+                if (t != 0.f) {
+                    mz = fmaxf(m * w.inv_t, kNegBig);
+                    const float d = fmaf(m, w.inv_t, -mz);
+                    t *= fabsf(d) < 1e-3f ? fmaf(d, fmaf(0.5f, d, 1.f), 1.f) : expf(d);
+                }
+                a.parts[(int64_t)slice * a.N + r] =
+                    PartialRec{mz, kNegBig, (double)t, 0.0, 0.0, target >= 0 ? sm.target_z[buf] : 0.f, flags};
+            }
+        } else {
+            T *orow = static_cast<T *>(a.out) + w.out_off + s0;
+            const bool ovec = ((uintptr_t)orow & 15u) == 0;
+            const bool constant = w.nan_row || w.ignored;
+#pragma unroll
+            for (int k = 0; k < kVecs; ++k) {
+                const int o = k * kThreads + tid, n = width - o * kVec;
+                if (n > 0) {
+                    uint4 u = reinterpret_cast<const uint4 *>(st)[o];
+                    float v[kVec];
+                    Elem<T>::unpack(u, v);
+#pragma unroll
+                    for (int i = 0; i < kVec; i += 2) {
+                        float2 d = make_float2(v[i], v[i + 1]);
+                        if constexpr (kOp == kLogpBwd) {
+                            d = __fadd2_rn(__ffma2_rn(d, f2(w.inv_t), f2(-w.m)), f2(-w.log_s));
+                            if (Scaled<T>::kUnit != 1.f) d = __fmul2_rn(d, f2(Scaled<T>::kUnit));
+                            d = scaled_exp2<T>(d);
+                        }
+                        d = __fmul2_rn(d, f2(w.scale));
+                        v[i] = d.x;
+                        v[i + 1] = d.y;
+                    }
+                    if (constant) {
+#pragma unroll
+                        for (int i = 0; i < kVec; ++i) v[i] = w.nan_row ? qnan() : 0.f;
+                    }
+                    u = Elem<T>::pack(v);
+                    const uint32_t on = allow.b[k / 4] >> (8 * (k % 4)) & Tile<T>::kAll;
+                    if (on != Tile<T>::kAll && !constant)
+                        u = keep_vec<T>(u, on, kOp == kProcFwd ? minus_inf_bits<T>() : 0u, sm.keep_words);
+                    store_vec(orow + o * kVec, u, n, ovec);
+                }
+            }
+            __syncthreads();                              // the vector pass's stores come before the walk's
+            if (listed) {
+                walk([&](int l) {
+                    const float staged = to_float(st[l]);
+                    float f, v = ruled(l, kOp == kProcBwd ? to_float(xrow[l]) : staged, f, true);
+                    if (kOp == kProcFwd) {
+                        v *= w.inv_t;
+                    } else if (kOp == kProcBwd) {
+                        v = staged * (f * w.inv_t);
+                    } else {
+                        const float d = fmaf(v, w.inv_t, -w.m) - w.log_s;
+                        v = (l == target ? expm1f(d) : Scaled<T>::exp(d * Scaled<T>::kUnit)) * (f * w.scale);
+                    }
+                    if (!allowed(l)) v = kOp == kProcFwd ? -pinf() : 0.f;
+                    if (!constant) Elem<T>::store1(orow + l, v);
+                });
+                if (n_listed > (uint32_t)kListed) __syncthreads();   // the walk reads every word of the bitmap
+                clear();
+                if (tid == 0) sm.n_listed[buf] = 0u;
+                __syncthreads();                          // the tables are clear
+            }
+        }
+        if (row_ends) {
+            ++r;
+            w = next_w;
+            fresh = true;
+        }
+        allow = next_allow;
+        slice = next_slice;
+    }
+    if (!arrived) {                                       // a copy was late: flagged, and awaited once more
+        atomicOr(&g_linear_fault, 1u);
+        for (int b = 0; b < 2; ++b)
+            if (bulk >> b & 1u) mbar_wait(&sm.full[b], (parity >> b & 1u) ^ 1u);
     }
 }
 
-int64_t rule_slices(int64_t V) { return (V + kSlice - 1) / kSlice; }
+// Joins a row's records (slice-major) into its logprob and vp_rowstat: one warp per
+// row, lanes over the slices, the records' order fixed. What vp_logprobs_merge
+// does for shards, with the exponentials of the sums in fp32 (the sums are fp32
+// sums): its fp64 ones took 25 us for 8192 rows of 10 slices.
+constexpr int kJoinWarps = 8;
+__global__ void __launch_bounds__(kJoinWarps * 32)
+rules_join_kernel(const PartialRec *__restrict__ parts, int K, int64_t N, float *__restrict__ logp,
+                  RowStat *__restrict__ stats, int32_t *__restrict__ err) {
+    pdl_enter<true>();
+    const int64_t r = (int64_t)blockIdx.x * kJoinWarps + (threadIdx.x >> 5);
+    const int lane = threadIdx.x & 31;
+    if (r >= N) return;   // warp-uniform
+    float M = kNegBig, zt = 0.f;
+    uint32_t flags = 0u;
+    for (int k = lane; k < K; k += 32) {
+        const PartialRec &p = parts[(int64_t)k * N + r];
+        M = fmaxf(M, p.m);
+        flags |= p.flags;
+        if (p.flags & kPartHasTarget) zt = p.z_t;
+    }
+    M = warp_max(M);
+    const unsigned holders = __ballot_sync(0xffffffffu, (flags & kPartHasTarget) != 0u);   // one slice at most
+    flags = __reduce_or_sync(0xffffffffu, flags);
+    zt = __shfl_sync(0xffffffffu, zt, holders ? __ffs(holders) - 1 : 0);
+    double S = 0.0;
+    for (int k = lane; k < K; k += 32) {
+        const PartialRec &p = parts[(int64_t)k * N + r];
+        if (p.S > 0.0) S += (double)(expf(p.m - M) * (float)p.S);   // a slice without weight is skipped
+    }
+    S = warp_sum(S);
+    if (lane != 0) return;
+    uint32_t rf = kRowSharded;
+    if (flags & kPartNanInf) { S = (double)qnan(); rf |= kRowNanInf; }
+    else if (S == 0.0) rf |= kRowEmpty;
+    const double log_s = log(S);
+    const bool ignored = (flags & kPartIgnored) != 0u, lost = !ignored && !holders;
+    if (lost) rf |= kRowBadTarget;
+    store_rowstat(stats + r, M, log_s, 0.0, rf);
+    if (lost && err) atomicOr(err, VP_ERRBIT_TARGET_);
+    logp[r] = ignored ? 0.f : lost || (rf & (kRowNanInf | kRowEmpty)) ? qnan() : (float)(((double)zt - (double)M) - log_s);
+}
+
+int64_t rule_slices(int64_t V) { return (V + Tile<float>::kWidth - 1) / Tile<float>::kWidth; }
 
 template <typename T, int kOp>
-static cudaError_t launch_rules_t(const RuleKernelArgs &k, cudaStream_t stream) {
-    const size_t smem = (k.q.bias_spans ? 2 : k.q.spans ? 1 : 0) * (size_t)kSlice * 4;
-    if (smem > 48 * 1024) {
-        cudaError_t e = cudaFuncSetAttribute(rules_kernel<T, kOp>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             2 * kSlice * 4);
+static cudaError_t launch_rules_t(RuleKernelArgs k, cudaStream_t stream) {
+    // resident CTAs per SM for each number of tables, asked once per device
+    static std::atomic<int> resident[64][3];
+    k.n_slices = (k.V + Tile<T>::kWidth - 1) / Tile<T>::kWidth;
+    const int n_tables = k.q.bias_spans ? 2 : k.q.spans ? 1 : 0;
+    constexpr int table = Tile<T>::kWidth * 4;
+    const int smem = (int)sizeof(RuleSmem<T>) + n_tables * table;
+    int dev = 0, sms = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    int per_sm = resident[dev & 63][n_tables].load(std::memory_order_relaxed);
+    if (!per_sm) {
+        e = cudaFuncSetAttribute(rules_kernel<T, kOp>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 (int)sizeof(RuleSmem<T>) + 2 * table);
+        if (e == cudaSuccess)
+            e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, rules_kernel<T, kOp>, Tile<T>::kThreads, smem);
         if (e != cudaSuccess) return e;
+        per_sm = per_sm < 1 ? 1 : per_sm;
+        resident[dev & 63][n_tables].store(per_sm, std::memory_order_relaxed);
     }
-    const int64_t total = k.N * k.n_slices;
-    return launch_pdl(rules_kernel<T, kOp>, dim3((unsigned)(total < 0x7fffffff ? total : 0x7fffffff)), dim3(kRuleThreads),
-                      smem, stream, k);
+    if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
+    const int64_t total = k.N * k.n_slices, most = (int64_t)sms * per_sm;
+    return launch_pdl(rules_kernel<T, kOp>, dim3((unsigned)(total < most ? total : most)), dim3(Tile<T>::kThreads),
+                      (size_t)smem, stream, k);
 }
 
 template <int kOp>
 static cudaError_t launch_rules(const RuleArgs &a) {
-    RuleKernelArgs k{a.x, a.dy, a.out, a.N, rule_slices(a.V), a.vocab_start, (int)a.V, Rows{a.R, a.s_o, a.s_i},
+    RuleKernelArgs k{a.x, a.dy, a.out, a.N, 0, a.vocab_start, (int)a.V, Rows{a.R, a.s_o, a.s_i},
                      Rows{a.R, a.out_s_o, a.out_s_i}, a.rules, a.targets, static_cast<const RowStat *>(a.stats), a.g,
                      static_cast<PartialRec *>(a.parts), a.err};
     // no rule that reads the ids: the spans are not looked at
     if (!k.q.repetition && !k.q.frequency && !k.q.presence) k.q.spans = nullptr;
     return a.bf16 ? launch_rules_t<__nv_bfloat16, kOp>(k, a.stream) : launch_rules_t<float, kOp>(k, a.stream);
 }
+
+cudaError_t read_rules_fault(uint32_t *value, bool clear) { return read_tu_fault(value, clear); }
 
 cudaError_t launch_process_fwd(const RuleArgs &a) { return launch_rules<kProcFwd>(a); }
 cudaError_t launch_process_bwd(const RuleArgs &a) { return launch_rules<kProcBwd>(a); }
@@ -383,7 +786,10 @@ cudaError_t launch_processed_logprobs_bwd(const RuleArgs &a) { return launch_rul
 cudaError_t launch_processed_logprobs_fwd(const RuleArgs &a, float *logp, void *stats) {
     cudaError_t e = launch_rules<kLogpFwd>(a);
     if (e != cudaSuccess) return e;
-    return launch_logprobs_merge(MergeArgs{a.parts, rule_slices(a.V), a.N, logp, stats, nullptr, a.err, a.stream});
+    const int width = a.bf16 ? Tile<__nv_bfloat16>::kWidth : Tile<float>::kWidth;
+    return launch_pdl(rules_join_kernel, dim3((unsigned)((a.N + kJoinWarps - 1) / kJoinWarps)), dim3(kJoinWarps * 32), 0,
+                      a.stream, static_cast<const PartialRec *>(a.parts), (int)((a.V + width - 1) / width), a.N, logp,
+                      static_cast<RowStat *>(stats), a.err);
 }
 
 }  // namespace vp
