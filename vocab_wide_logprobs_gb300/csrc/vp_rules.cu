@@ -9,8 +9,7 @@
 //   y = allowed(j) ? z / T : -inf
 //   f = dy/dx = allowed(j) ? (c_p + c_o > 0 ? (x > 0 ? 1 / rep : rep) : 1) / T : 0
 //
-// Shape. A tile is a slice of 8192 (bf16) or 4096 (fp32) columns of one row; a
-// CTA works through consecutive tiles (a row's slices follow one another, its
+// Shape. A tile is a slice of 4096 columns of one row; a CTA works through consecutive tiles (a row's slices follow one another, its
 // rules are read once). One bulk copy brings the next tile to shared memory
 // while this one is worked on. Thread t owns the 16-byte vectors t, t + kThreads,
 // ... of a tile. Of the ids the CTA builds tables for the tile: a word per
@@ -43,18 +42,16 @@ namespace vp {
 
 constexpr uint32_t kPromptBit = 0x80000000u;
 
-#ifndef VP_RULE_THREADS
-#define VP_RULE_THREADS 128
-#define VP_RULE_VECS 8
-#endif
-#ifndef VP_RULE_CTAS
-#define VP_RULE_CTAS 3
-#endif
+// A tile's threads and size. Measured on GB300 at 4096 x 75968 bf16 with 1000 ids a
+// row (us, forward / backward of the ruled logprobs): 4 vectors a thread, five CTAs
+// an SM 336 / 268; 8 vectors, three CTAs 364 / 302; 256 threads with 4 vectors,
+// three CTAs 382 / 325. fp32 (2048 rows): 8 vectors 300 / 247, 4 vectors 343 / 320.
 template <typename T> struct Tile {
-    static constexpr int kThreads = VP_RULE_THREADS, kWarps = kThreads / 32;
-    static constexpr int kVec = Elem<T>::kVec;                // columns of a vector
-    static constexpr int kVecs = VP_RULE_VECS;                // vectors of a thread
-    static constexpr int kWidth = kThreads * kVecs * kVec;    // columns of a tile
+    static constexpr int kThreads = 128, kWarps = kThreads / 32;
+    static constexpr int kVec = Elem<T>::kVec;                // columns of a 16-byte vector
+    static constexpr int kVecs = 32 / kVec;                   // vectors of a thread
+    static constexpr int kCtas = sizeof(T) == 2 ? 5 : 3;      // of an SM
+    static constexpr int kWidth = kThreads * kVecs * kVec;    // columns of a tile: 4096
     static constexpr int kWords = kWidth / 32;                // words of the bitmap
     static constexpr uint32_t kAll = kVec == 8 ? 0xffu : 0xfu;
 };
@@ -136,6 +133,7 @@ struct RuleKernelArgs {
     const float *g;
     PartialRec *parts;
     int32_t *err;
+    int row_ids;              // capacity of the list of a row's ids
 };
 
 // The rules of one row, read and checked when a CTA comes to it, and what else
@@ -266,8 +264,10 @@ template <typename T> __device__ __forceinline__ float vec_max(const uint4 &u) {
 }
 
 // Listed columns of a tile that are kept as a list; with more of them the bitmap
-// is walked instead. Ids of a row that a CTA keeps, sorted by slice.
-constexpr int kListed = 512, kRowIds = 2048, kSegment = 64;
+// is walked instead. A CTA that has several slices of a row sorts the row's ids among
+// them by slice, if the slices are at most kSegment and the ids no more than a
+// capacity that the launch chooses.
+constexpr int kListed = 512, kSegment = 64, kRowIdsLeast = 2048, kRowIdsMost = 32768;
 // The listed columns' exponentials are summed as integers, in units of 2^-48 of
 // the tile's largest, so that the order they are found in does not matter.
 constexpr float kFixed = 281474976710656.f;   // 2^48
@@ -283,17 +283,18 @@ struct RuleSmem {
     uint32_t n_listed[2];
     uint32_t segment[kSegment + 1];                       // where a slice's ids begin in row_ids; counters before that
     uint16_t listed[kListed];
-    uint16_t row_ids[kRowIds];                            // column of the slice, bit 15: prompt
-    // counts [kWidth] and, with a bias list, entries [kWidth] follow
+    // counts [kWidth], with a bias list entries [kWidth], then the row's ids follow
 };
 
 template <typename T, int kOp>
-__global__ void __launch_bounds__(Tile<T>::kThreads, VP_RULE_CTAS) rules_kernel(const __grid_constant__ RuleKernelArgs a) {
+__global__ void __launch_bounds__(Tile<T>::kThreads, Tile<T>::kCtas) rules_kernel(const __grid_constant__ RuleKernelArgs a) {
     extern __shared__ __align__(16) uint8_t smem_raw[];
     constexpr int kThreads = Tile<T>::kThreads, kVec = Tile<T>::kVec, kVecs = Tile<T>::kVecs, kSlice = Tile<T>::kWidth,
                   kWords = Tile<T>::kWords, kWarps = Tile<T>::kWarps;
     RuleSmem<T> &sm = *reinterpret_cast<RuleSmem<T> *>(smem_raw);
     uint32_t *const counts = reinterpret_cast<uint32_t *>(smem_raw + sizeof(RuleSmem<T>)), *const entries = counts + kSlice;
+    // column of the slice, bit 15: prompt
+    uint16_t *const row_ids = reinterpret_cast<uint16_t *>(counts + (a.q.bias_spans ? 2 : a.q.spans ? 1 : 0) * kSlice);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint8_t *const touched8 = reinterpret_cast<const uint8_t *>(sm.touched);
     const bool tabled = a.q.spans != nullptr, biased = a.q.bias_spans != nullptr;
@@ -392,6 +393,37 @@ __global__ void __launch_bounds__(Tile<T>::kThreads, VP_RULE_CTAS) rules_kernel(
             next_allow = mask_bits(row_ends ? next_w : w, next_slice);
         }
 
+        // f(column past base, index) for the ids of the row's history whose columns lie below reach;
+        // 16 ids of a thread on their way at once
+        auto each = [&](uint64_t base, uint64_t reach, auto f) {
+            const uint32_t head = min(w.n_total, (uint32_t)((uintptr_t)w.ids >> 3 & 1u));   // to a 16-byte boundary
+            const uint32_t pairs = (w.n_total - head) / 2u;
+            auto one = [&](uint32_t i, uint64_t id) {
+                const uint64_t l = id - base;             // negative ids come out far above any reach
+                if (l < reach) f((uint32_t)l, i);
+            };
+            constexpr uint32_t kUnroll = 8;
+            const ulonglong2 *const p = reinterpret_cast<const ulonglong2 *>(w.ids + head);
+#pragma unroll 1
+            for (uint32_t i0 = tid; i0 < pairs; i0 += kUnroll * kThreads) {
+                ulonglong2 id[kUnroll];
+#pragma unroll
+                for (uint32_t u = 0; u < kUnroll; ++u) {
+                    const uint32_t i = i0 + u * kThreads;
+                    id[u] = i < pairs ? __ldg(p + i) : make_ulonglong2(~0ull, ~0ull);
+                }
+#pragma unroll
+                for (uint32_t u = 0; u < kUnroll; ++u) {
+                    const uint32_t i = head + 2u * (i0 + u * kThreads);
+                    one(i, id[u].x);
+                    one(i + 1u, id[u].y);
+                }
+            }
+            if (tid == 0 && head) one(0u, (uint64_t)__ldg(w.ids));
+            if (tid == 1 && (w.n_total - head) % 2u) one(w.n_total - 1u, (uint64_t)__ldg(w.ids + w.n_total - 1u));
+        };
+        const uint64_t base = (uint64_t)a.vocab_start + (uint64_t)s0;
+
         // ---- a row that this CTA has several slices of: its ids are sorted by slice once
         if (fresh) {
             fresh = false;
@@ -400,27 +432,10 @@ __global__ void __launch_bounds__(Tile<T>::kThreads, VP_RULE_CTAS) rules_kernel(
             const int slices = (int)min(left, a.n_slices - (int64_t)slice);
             sorted = w.n_total > 0u && slices > 1 && slices <= kSegment;
             if (sorted) {
-                const uint64_t base = (uint64_t)a.vocab_start + (uint64_t)s0;
                 const uint64_t reach = (uint64_t)min((int64_t)slices * kSlice, (int64_t)a.V - s0);
-                // f(column past s0, index) for every id in reach
-                auto each = [&](auto f) {
-                    constexpr uint32_t kUnroll = 8;
-#pragma unroll 1
-                    for (uint32_t i0 = tid; i0 < w.n_total; i0 += kUnroll * kThreads) {
-                        uint64_t l[kUnroll];
-#pragma unroll
-                        for (uint32_t u = 0; u < kUnroll; ++u) {
-                            const uint32_t i = i0 + u * kThreads;
-                            l[u] = i < w.n_total ? (uint64_t)__ldg(w.ids + i) - base : ~0ull;
-                        }
-#pragma unroll
-                        for (uint32_t u = 0; u < kUnroll; ++u)
-                            if (l[u] < reach) f((uint32_t)l[u], i0 + u * kThreads);
-                    }
-                };
                 for (int i = tid; i <= kSegment; i += kThreads) sm.segment[i] = 0u;
                 __syncthreads();
-                each([&](uint32_t l, uint32_t) { atomicAdd(&sm.segment[l / kSlice + 1], 1u); });
+                each(base, reach, [&](uint32_t l, uint32_t) { atomicAdd(&sm.segment[l / kSlice + 1], 1u); });
                 __syncthreads();
                 if (warp == 0) {                          // counts to beginnings
                     uint32_t lo = sm.segment[1 + lane], hi = sm.segment[33 + lane];
@@ -434,11 +449,11 @@ __global__ void __launch_bounds__(Tile<T>::kThreads, VP_RULE_CTAS) rules_kernel(
                     sm.segment[33 + lane] = hi;
                 }
                 __syncthreads();
-                sorted = sm.segment[kSegment] <= (uint32_t)kRowIds;   // no cursor below is this one
+                sorted = sm.segment[kSegment] <= (uint32_t)a.row_ids;   // no cursor below is this one
                 if (sorted) {                             // the beginnings move to the ends as the ids are placed
-                    each([&](uint32_t l, uint32_t i) {
+                    each(base, reach, [&](uint32_t l, uint32_t i) {
                         const uint32_t at = atomicAdd(&sm.segment[l / kSlice], 1u);
-                        sm.row_ids[at] = (uint16_t)(l % kSlice | (i < w.n_prompt ? 0x8000u : 0u));
+                        row_ids[at] = (uint16_t)(l % kSlice | (i < w.n_prompt ? 0x8000u : 0u));
                     });
                     __syncthreads();
                 }
@@ -461,26 +476,13 @@ __global__ void __launch_bounds__(Tile<T>::kThreads, VP_RULE_CTAS) rules_kernel(
                 mark(c);
             };
             if (tid == 0 && target >= 0) mark((uint32_t)target);
-            const uint64_t base = (uint64_t)a.vocab_start + (uint64_t)s0;   // negative ids come out far above any width
             if (sorted) {
                 const int k = slice - seg0;
                 const uint32_t to = sm.segment[k];
                 for (uint32_t i = (k ? sm.segment[k - 1] : 0u) + tid; i < to; i += kThreads)
-                    enter(sm.row_ids[i] & 0x7fffu, sm.row_ids[i] >> 15);
+                    enter(row_ids[i] & 0x7fffu, row_ids[i] >> 15);
             } else {
-                constexpr uint32_t kUnroll = 8;
-#pragma unroll 1
-                for (uint32_t i0 = tid; i0 < w.n_total; i0 += kUnroll * kThreads) {
-                    uint64_t l[kUnroll];
-#pragma unroll
-                    for (uint32_t u = 0; u < kUnroll; ++u) {
-                        const uint32_t i = i0 + u * kThreads;
-                        l[u] = i < w.n_total ? (uint64_t)__ldg(w.ids + i) - base : ~0ull;
-                    }
-#pragma unroll
-                    for (uint32_t u = 0; u < kUnroll; ++u)
-                        if (l[u] < (uint64_t)width) enter((uint32_t)l[u], i0 + u * kThreads < w.n_prompt);
-                }
+                each(base, (uint64_t)width, [&](uint32_t l, uint32_t i) { enter(l, i < w.n_prompt); });
             }
 #pragma unroll 1
             for (uint32_t i = tid; i < w.n_bias; i += kThreads) {
@@ -742,24 +744,31 @@ int64_t rule_slices(int64_t V) { return (V + Tile<float>::kWidth - 1) / Tile<flo
 
 template <typename T, int kOp>
 static cudaError_t launch_rules_t(RuleKernelArgs k, cudaStream_t stream) {
-    // resident CTAs per SM for each number of tables, asked once per device
-    static std::atomic<int> resident[64][3];
+    // resident CTAs per SM for each number of tables and capacity of row_ids, asked once per device
+    static std::atomic<int> resident[64][3][5];
     k.n_slices = (k.V + Tile<T>::kWidth - 1) / Tile<T>::kWidth;
     const int n_tables = k.q.bias_spans ? 2 : k.q.spans ? 1 : 0;
-    constexpr int table = Tile<T>::kWidth * 4;
-    const int smem = (int)sizeof(RuleSmem<T>) + n_tables * table;
+    // Room for twice the average row's ids: long histories take shared memory from other CTAs, but going
+    // through 16384 ids for every slice takes longer than the slice.
+    int step = 0;
+    if (k.q.spans)
+        while (step < 4 && (int64_t)(kRowIdsLeast << step) * k.N < 2 * k.q.n_ids) ++step;
+    static_assert(kRowIdsLeast << 4 == kRowIdsMost, "five capacities");
+    k.row_ids = k.q.spans ? kRowIdsLeast << step : 0;
+    auto bytes = [](int tables, int ids) { return (int)sizeof(RuleSmem<T>) + tables * Tile<T>::kWidth * 4 + ids * 2; };
+    const int smem = bytes(n_tables, k.row_ids);
     int dev = 0, sms = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
-    int per_sm = resident[dev & 63][n_tables].load(std::memory_order_relaxed);
+    std::atomic<int> &known = resident[dev & 63][n_tables][step];
+    int per_sm = known.load(std::memory_order_relaxed);
     if (!per_sm) {
-        e = cudaFuncSetAttribute(rules_kernel<T, kOp>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 (int)sizeof(RuleSmem<T>) + 2 * table);
+        e = cudaFuncSetAttribute(rules_kernel<T, kOp>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes(2, kRowIdsMost));
         if (e == cudaSuccess)
             e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, rules_kernel<T, kOp>, Tile<T>::kThreads, smem);
         if (e != cudaSuccess) return e;
         per_sm = per_sm < 1 ? 1 : per_sm;
-        resident[dev & 63][n_tables].store(per_sm, std::memory_order_relaxed);
+        known.store(per_sm, std::memory_order_relaxed);
     }
     if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
     const int64_t total = k.N * k.n_slices, most = (int64_t)sms * per_sm;
@@ -771,7 +780,7 @@ template <int kOp>
 static cudaError_t launch_rules(const RuleArgs &a) {
     RuleKernelArgs k{a.x, a.dy, a.out, a.N, 0, a.vocab_start, (int)a.V, Rows{a.R, a.s_o, a.s_i},
                      Rows{a.R, a.out_s_o, a.out_s_i}, a.rules, a.targets, static_cast<const RowStat *>(a.stats), a.g,
-                     static_cast<PartialRec *>(a.parts), a.err};
+                     static_cast<PartialRec *>(a.parts), a.err, 0};
     // no rule that reads the ids: the spans are not looked at
     if (!k.q.repetition && !k.q.frequency && !k.q.presence) k.q.spans = nullptr;
     return a.bf16 ? launch_rules_t<__nv_bfloat16, kOp>(k, a.stream) : launch_rules_t<float, kOp>(k, a.stream);
