@@ -699,75 +699,89 @@ def _rows_apart(y, N, V):
 class LogitsRules:
     """The rules of N rows of logits (vp_logits_rules of include/vp.h); made by :func:`logits_rules`.
 
-    Holds the tensors, and the host struct of their device pointers that the calls take."""
+    Holds the tensors, and the host struct of their device pointers that the calls take. A decode loop makes
+    one per step, so the checks are written out field by field."""
 
-    # field -> (dtype, elements per row; None: of its own length)
-    _FIELDS = {"ids": (torch.int64, None), "spans": (torch.int64, 3), "repetition": (torch.float32, 1),
-               "frequency": (torch.float32, 1), "presence": (torch.float32, 1), "bias_ids": (torch.int64, None),
-               "bias_values": (torch.float32, None), "bias_spans": (torch.int64, 2), "mask_rows": (torch.int64, 1),
-               "temperature": (torch.float32, 1)}
+    __slots__ = ("rows", "device", "mask_bits", "n_masks", "by_row", "tensors", "struct", "address")
 
-    def __init__(self, mask=None, **tensors):
+    def __init__(self, ids, spans, repetition, frequency, presence, bias_ids, bias_values, bias_spans, mask, mask_rows,
+                 temperature):
         self.rows, self.device, self.mask_bits, self.n_masks = None, None, None, 0
-        self.tensors, self.struct = tensors, _lib.LogitsRulesStruct()
-        for name, t in tensors.items():
-            dtype, per_row = self._FIELDS[name]
-            if t is None:
-                continue
-            if t.dtype != dtype:
-                raise VPError(3, f"{name}: needs {dtype}, got {t.dtype}")
-            if not t.is_contiguous():
-                raise VPError(4, f"{name}: needs a contiguous tensor")
-            self._on(t, name)
-            if per_row is not None:
-                rows = t.shape[0] if t.dim() else -1
-                if t.dim() != (1 if per_row == 1 else 2) or (per_row > 1 and t.shape[1] != per_row) or \
-                        self.rows not in (None, rows):
-                    raise VPError(2, f"{name}: shape {tuple(t.shape)}")
-                self.rows = rows
-            setattr(self.struct, name, t.data_ptr())
-        get = tensors.get
-        for spans, lists in (("spans", ("ids",)), ("bias_spans", ("bias_ids", "bias_values"))):
-            if get(spans) is None and any(get(n) is not None for n in lists) or \
-                    get(spans) is not None and any(get(n) is None for n in lists):
-                raise VPError(1, f"{spans} and {', '.join(lists)} go together")
-        if get("spans") is not None:
-            self.struct.n_ids = get("ids").numel()
-        elif any(get(n) is not None for n in ("repetition", "frequency", "presence")):
+        self.by_row = mask_rows is None
+        self.tensors = (ids, spans, repetition, frequency, presence, bias_ids, bias_values, bias_spans, mask, mask_rows,
+                        temperature)
+        q = self.struct = _lib.LogitsRulesStruct()
+        self.address = ctypes.addressof(q)
+        if (ids is None) != (spans is None):
+            raise VPError(1, "spans and ids go together")
+        if (bias_ids is None) != (bias_spans is None) or (bias_values is None) != (bias_spans is None):
+            raise VPError(1, "bias_spans, bias_ids and bias_values go together")
+        if ids is not None:
+            q.ids, q.n_ids = self._take(ids, torch.int64, "ids"), ids.numel()
+            q.spans = self._take(spans, torch.int64, "spans", 3)
+        elif repetition is not None or frequency is not None or presence is not None:
             raise VPError(1, "penalties need ids and spans")
-        if get("bias_spans") is not None:
-            if get("bias_ids").numel() != get("bias_values").numel():
+        if repetition is not None:
+            q.repetition = self._take(repetition, torch.float32, "repetition", 1)
+        if frequency is not None:
+            q.frequency = self._take(frequency, torch.float32, "frequency", 1)
+        if presence is not None:
+            q.presence = self._take(presence, torch.float32, "presence", 1)
+        if temperature is not None:
+            q.temperature = self._take(temperature, torch.float32, "temperature", 1)
+        if bias_spans is not None:
+            q.bias_ids = self._take(bias_ids, torch.int64, "bias_ids")
+            q.bias_values, q.n_bias = self._take(bias_values, torch.float32, "bias_values"), bias_ids.numel()
+            q.bias_spans = self._take(bias_spans, torch.int64, "bias_spans", 2)
+            if bias_ids.numel() != bias_values.numel():
                 raise VPError(2, "bias_ids and bias_values differ in length")
-            self.struct.n_bias = get("bias_ids").numel()
-        self.mask = mask
         if mask is not None:
             if mask.dtype != torch.int32:
                 raise VPError(3, f"mask: needs {torch.int32}, got {mask.dtype}")
             if mask.dim() != 2 or mask.shape[0] < 1:
                 raise VPError(2, f"mask: shape {tuple(mask.shape)}")
-            if mask.shape[1] > 1 and mask.stride(1) != 1:
-                raise VPError(4, "mask words need a unit stride")
+            self.n_masks, words = mask.shape
+            stride, unit = mask.stride()
+            if (words > 1 and unit != 1) or (self.n_masks > 1 and stride < words):
+                raise VPError(4, "mask rows need a unit stride and may not overlap")
             self._on(mask, "mask")
-            self.mask_bits, self.n_masks = 32 * mask.shape[1], mask.shape[0]
-            self.struct.mask, self.struct.n_masks, self.struct.mask_stride = mask.data_ptr(), mask.shape[0], mask.stride(0)
-        elif get("mask_rows") is not None:
+            self.mask_bits = 32 * words
+            q.mask, q.n_masks, q.mask_stride = mask.data_ptr(), self.n_masks, stride
+            if mask_rows is not None:
+                q.mask_rows = self._take(mask_rows, torch.int64, "mask_rows", 1)
+        elif mask_rows is not None:
             raise VPError(1, "mask_rows without mask")
 
     def _on(self, t, name):
-        if self.device not in (None, t.device):
+        if self.device is None:
+            self.device = t.device
+        elif self.device != t.device:
             raise VPError(4, f"{name}: on {t.device}, others on {self.device}")
-        self.device = t.device
+
+    def _take(self, t, dtype, name, per_row=0):
+        """The address of a tensor, checked: [rows] or [rows, per_row] elements of dtype; per_row 0: any number."""
+        if t.dtype != dtype:
+            raise VPError(3, f"{name}: needs {dtype}, got {t.dtype}")
+        if not t.is_contiguous():
+            raise VPError(4, f"{name}: needs a contiguous tensor")
+        self._on(t, name)
+        if per_row:
+            shape = t.shape
+            if len(shape) != (1 if per_row == 1 else 2) or (per_row > 1 and shape[1] != per_row) or \
+                    self.rows not in (None, shape[0]):
+                raise VPError(2, f"{name}: shape {tuple(shape)}")
+            self.rows = shape[0]
+        return t.data_ptr()
 
     def check(self, N: int, V: int, device):
         """The struct's address, for a call on N rows of V columns."""
-        if self.rows not in (None, N):
+        if self.rows is not None and self.rows != N:
             raise VPError(2, f"rules of {self.rows} rows for {N} rows of logits")
-        if self.device not in (None, device):
+        if self.device is not None and self.device != device:
             raise VPError(4, f"rules on {self.device}, logits on {device}")
-        if self.mask_bits is not None and (self.mask_bits < V or (self.tensors.get("mask_rows") is None
-                                                                  and self.n_masks < N)):
+        if self.mask_bits is not None and (self.mask_bits < V or (self.by_row and self.n_masks < N)):
             raise VPError(2, f"mask: {self.n_masks} rows of {self.mask_bits} bits for {N} rows of {V} logits")
-        return ctypes.byref(self.struct)
+        return self.address
 
 
 def logits_rules(ids=None, spans=None, repetition=None, frequency=None, presence=None, bias_ids=None,
@@ -779,9 +793,22 @@ def logits_rules(ids=None, spans=None, repetition=None, frequency=None, presence
     temperature: fp32 [N]. bias_ids int64, bias_values fp32 and bias_spans int64 [N, 2] = (first, n): a list of
     (id, bias) per row. mask: int32 [M, words], bit j % 32 of word j // 32 allowing column j; mask_rows int64
     [N]: the mask row of each row, -1 for none (without it row r uses mask row r). Everything may be None."""
-    return LogitsRules(mask=mask, ids=ids, spans=spans, repetition=repetition, frequency=frequency, presence=presence,
-                       bias_ids=bias_ids, bias_values=bias_values, bias_spans=bias_spans, mask_rows=mask_rows,
-                       temperature=temperature)
+    return LogitsRules(ids, spans, repetition, frequency, presence, bias_ids, bias_values, bias_spans, mask, mask_rows,
+                       temperature)
+
+
+# The calls below are made once per decoded token, where the host's time counts: pointers go as integers, and the
+# stream is asked for by its handle.
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _queue(device):
+    return torch._C._cuda_getCurrentRawStream(device.index)
+
+
+def _handle():
+    return _lib._handle or _lib.lib()
 
 
 def vp_logits_process_fwd(x, rules: LogitsRules, vocab_start: int = 0, err_word=None, y=None):
@@ -796,8 +823,8 @@ def vp_logits_process_fwd(x, rules: LogitsRules, vocab_start: int = 0, err_word=
     _, _, _, y_s_o, y_s_i = rows_of(y)
     _rows_apart(y, N, V)
     _on_gpu(x)
-    _check(_lib.lib().vp_logits_process_fwd(_ptr(x), _dtype_code(x), N, V, R, s_o, s_i, vocab_start, q, _ptr(y), y_s_o,
-                                            y_s_i, _ptr(err_word), _stream()), "vp_logits_process_fwd")
+    _check(_handle().vp_logits_process_fwd(_addr(x), _dtype_code(x), N, V, R, s_o, s_i, vocab_start, q, _addr(y), y_s_o,
+                                            y_s_i, _addr(err_word), _queue(x.device)), "vp_logits_process_fwd")
     return y
 
 
@@ -810,13 +837,13 @@ def vp_logits_process_bwd(x, rules: LogitsRules, dy, vocab_start: int = 0, err_w
     _arg(dx, N * V, x.dtype, x, "dx")
     _on_gpu(x)
     dx = torch.empty((N, V), dtype=x.dtype, device=x.device) if dx is None else dx
-    _check(_lib.lib().vp_logits_process_bwd(_ptr(x), _dtype_code(x), N, V, R, s_o, s_i, vocab_start, q, _ptr(dy),
-                                            _ptr(dx), _ptr(err_word), _stream()), "vp_logits_process_bwd")
+    _check(_handle().vp_logits_process_bwd(_addr(x), _dtype_code(x), N, V, R, s_o, s_i, vocab_start, q, _addr(dy),
+                                            _addr(dx), _addr(err_word), _queue(x.device)), "vp_logits_process_bwd")
     return dx
 
 
 def vp_processed_logprobs_workspace_size(N: int, V: int) -> int:
-    return int(_lib.lib().vp_processed_logprobs_workspace_size(N, V))
+    return int(_handle().vp_processed_logprobs_workspace_size(N, V))
 
 
 def vp_processed_logprobs_fwd(x, rules: LogitsRules, targets, vocab_start: int = 0, err_word=None, logp=None,
@@ -831,10 +858,10 @@ def vp_processed_logprobs_fwd(x, rules: LogitsRules, targets, vocab_start: int =
     logp = _f32(N, x) if logp is None else logp
     stats = rowstats(N, x.device) if stats is None else stats
     if workspace is None:
-        workspace = _workspace(_lib.lib().vp_processed_logprobs_workspace_size(N, V), x)
-    _check(_lib.lib().vp_processed_logprobs_fwd(_ptr(x), _dtype_code(x), N, V, R, s_o, s_i, vocab_start, q,
-                                                _ptr(targets), _ptr(logp), _ptr(stats), _ptr(workspace),
-                                                workspace.numel(), _ptr(err_word), _stream()),
+        workspace = _workspace(_handle().vp_processed_logprobs_workspace_size(N, V), x)
+    _check(_handle().vp_processed_logprobs_fwd(_addr(x), _dtype_code(x), N, V, R, s_o, s_i, vocab_start, q,
+                                                _addr(targets), _addr(logp), _addr(stats), _addr(workspace),
+                                                workspace.numel(), _addr(err_word), _queue(x.device)),
            "vp_processed_logprobs_fwd")
     return logp, stats
 
@@ -848,15 +875,19 @@ def vp_processed_logprobs_bwd(x, rules: LogitsRules, targets, stats, grad, vocab
     _arg(dx, N * V, x.dtype, x, "dx")
     _on_gpu(x)
     dx = torch.empty((N, V), dtype=x.dtype, device=x.device) if dx is None else dx
-    _check(_lib.lib().vp_processed_logprobs_bwd(_ptr(x), _dtype_code(x), N, V, R, s_o, s_i, vocab_start, q,
-                                                _ptr(targets), _ptr(stats), _ptr(grad), _ptr(dx), _ptr(err_word),
-                                                _stream()), "vp_processed_logprobs_bwd")
+    _check(_handle().vp_processed_logprobs_bwd(_addr(x), _dtype_code(x), N, V, R, s_o, s_i, vocab_start, q,
+                                                _addr(targets), _addr(stats), _addr(grad), _addr(dx), _addr(err_word),
+                                                _queue(x.device)), "vp_processed_logprobs_bwd")
     return dx
 
 
 def vp_mxfp4_scale_bytes(N: int, D: int) -> int:
     """Bytes of the scale tiles of an MXFP4 matrix [N, D] (0 for sizes that are not taken)."""
-    return int(_lib.lib().vp_mxfp4_scale_bytes(N, D))
+    return int(_handle().vp_mxfp4_scale_bytes(N, D))
+
+
+def _scale_bytes(N, D):
+    return -(-N // 128) * -(-D // 128) * 512
 
 
 def _mxfp4(codes, scales, what: str):
@@ -867,23 +898,23 @@ def _mxfp4(codes, scales, what: str):
     if D < 64 or D % 64:
         raise VPError(2, f"{what} of {D} columns: MXFP4 takes multiples of 64")
     _arg(codes, codes.numel(), torch.uint8, codes, f"{what} codes")
-    _arg(scales, vp_mxfp4_scale_bytes(N, D), torch.uint8, codes, f"{what} scales")
+    _arg(scales, _scale_bytes(N, D), torch.uint8, codes, f"{what} scales")
     return N, D
 
 
 def vp_mxfp4_quantize(x, codes=None, scales=None):
     """MXFP4 of x ([N, D] or [B, T, D] rows, D a multiple of 64): (codes uint8 [N, D / 2], scales uint8)."""
     N, D, R, s_o, s_i = rows_of(x)
-    n = vp_mxfp4_scale_bytes(N, D)
+    if D < 64 or D % 64:
+        raise VPError(2, f"rows of {D} columns: MXFP4 takes multiples of 64")
+    n = _scale_bytes(N, D)
     _arg(codes, N * D // 2, torch.uint8, x, "codes")
     _arg(scales, n, torch.uint8, x, "scales")
-    if n == 0 and N > 0:
-        raise VPError(2, f"rows of {D} columns: MXFP4 takes multiples of 64")
     _on_gpu(x)
     codes = torch.empty((N, D // 2), dtype=torch.uint8, device=x.device) if codes is None else codes
     scales = torch.empty(n, dtype=torch.uint8, device=x.device) if scales is None else scales
-    _check(_lib.lib().vp_mxfp4_quantize(_ptr(x), _dtype_code(x), N, D, R, s_o, s_i, _ptr(codes), _ptr(scales),
-                                        _stream()), "vp_mxfp4_quantize")
+    _check(_handle().vp_mxfp4_quantize(_addr(x), _dtype_code(x), N, D, R, s_o, s_i, _addr(codes), _addr(scales),
+                                        _queue(x.device)), "vp_mxfp4_quantize")
     return codes, scales
 
 
@@ -898,7 +929,7 @@ def vp_mxfp4_dequantize(codes, scales, dtype=torch.bfloat16, out=None):
     _arg(out, N * D, dtype, codes, "out")
     _on_gpu(codes)
     out = torch.empty((N, D), dtype=dtype, device=codes.device) if out is None else out
-    _check(_lib.lib().vp_mxfp4_dequantize(_ptr(codes), _ptr(scales), N, D, _DTYPES[dtype], _ptr(out), _stream()),
+    _check(_handle().vp_mxfp4_dequantize(_addr(codes), _addr(scales), N, D, _DTYPES[dtype], _addr(out), _queue(codes.device)),
            "vp_mxfp4_dequantize")
     return out
 
@@ -914,6 +945,6 @@ def vp_linear_mxfp4_fwd(x_codes, x_scales, w_codes, w_scales, dtype=torch.bfloat
     _arg(y, N * V, dtype, x_codes, "y")
     _on_gpu(x_codes)
     y = torch.empty((N, V), dtype=dtype, device=x_codes.device) if y is None else y
-    _check(_lib.lib().vp_linear_mxfp4_fwd(_ptr(x_codes), _ptr(x_scales), _ptr(w_codes), _ptr(w_scales), N, V, D,
-                                          _DTYPES[dtype], _ptr(y), _stream()), "vp_linear_mxfp4_fwd")
+    _check(_handle().vp_linear_mxfp4_fwd(_addr(x_codes), _addr(x_scales), _addr(w_codes), _addr(w_scales), N, V, D,
+                                          _DTYPES[dtype], _addr(y), _queue(x_codes.device)), "vp_linear_mxfp4_fwd")
     return y

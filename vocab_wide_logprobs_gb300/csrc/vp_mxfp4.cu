@@ -6,7 +6,10 @@
 // 128 rows x 4 blocks, 16 bytes for each row % 32) are what tcgen05.cp
 // 32x128b.warpx4 puts into tensor memory for the block-scaled MMA, so a stage's
 // scales are one contiguous bulk copy.
+#include <cuda_fp16.h>
+
 #include <algorithm>
+#include <atomic>
 
 #include "vp_device.cuh"
 #include "vp_gemm_host.cuh"
@@ -38,116 +41,172 @@ __device__ __forceinline__ int64_t scale_word(int64_t r, int kt, int n_kt) {
     return ((r >> 7) * n_kt + kt) * 512 + (r & 31) * 16 + ((r & 127) >> 5) * 4;
 }
 
-constexpr int kQThreads = 256;
+constexpr int kQThreads = 256, kQWarps = kQThreads / 32;
+constexpr int kQChunk = 256;                 // columns that a warp reads at once
+constexpr int kQChunks = 4;                  // chunks of a warp, all on their way before the first is used
 
-// A warp takes 256 consecutive columns of a row, a lane 8 of them: a block is
-// four lanes, its maximum two shuffles away. The scale comes from the maximum's
-// exponent bits (E: the scale byte is E - 2, at least 0), so x / scale is exact.
-// Rows N .. the next multiple of 128 only get their zero scale bytes.
+// Which rows and chunks a warp works on: groups of kQChunks chunks, row by row.
+struct QuantGrid {
+    int64_t rows, groups;                    // groups per row
+    unsigned blocks;
+    bool ok;
+};
+static QuantGrid quant_grid(int64_t rows, int64_t D) {
+    const int64_t groups = (D + kQChunk * kQChunks - 1) / (kQChunk * kQChunks);
+    const int64_t blocks = (rows * groups + kQWarps - 1) / kQWarps;
+    return {rows, groups, (unsigned)blocks, blocks <= 0x7fffffff};
+}
+// (row, first chunk) of this warp; row >= rows: nothing to do
+__device__ __forceinline__ int64_t quant_place(int64_t groups, int &chunk0) {
+    const int64_t unit = (int64_t)blockIdx.x * kQWarps + (threadIdx.x >> 5);
+    const int64_t r = unit >> 32 || groups >> 32 ? unit / groups : (int64_t)((uint32_t)unit / (uint32_t)groups);
+    chunk0 = (int)(unit - r * groups) * kQChunks;
+    return r;
+}
+
+// A lane takes 8 consecutive columns of a chunk: a block is four lanes, its
+// maximum two shuffles away. The scale comes from the maximum's exponent bits (E:
+// the scale byte is E - 2, at least 0), so x / scale is exact. Rows N .. the next
+// multiple of 128 only get their zero scale bytes. Bound by memory: one read of x,
+// 17/32 of a byte written per element.
 template <typename T>
 __global__ void __launch_bounds__(kQThreads)
-mxfp4_quantize_kernel(const T *__restrict__ x, Rows rows, int64_t N, int64_t n_rows, int D, uint8_t *__restrict__ codes,
-                      uint8_t *__restrict__ scales) {
+mxfp4_quantize_kernel(const T *__restrict__ x, Rows rows, int64_t N, int64_t n_rows, int64_t groups, int D,
+                      uint8_t *__restrict__ codes, uint8_t *__restrict__ scales) {
     pdl_enter<true>();
-    const int lane = threadIdx.x & 31;
-    const int n_kt = (D + 127) / 128, n_chunk = (D + 255) / 256;
-    const int64_t unit = (int64_t)blockIdx.x * (kQThreads / 32) + (threadIdx.x >> 5);
-    const int64_t r = unit / n_chunk;
+    constexpr int kVecs = 8 / Elem<T>::kVec;
+    const int lane = threadIdx.x & 31, n_kt = (D + 127) / 128;
+    int chunk0;
+    const int64_t r = quant_place(groups, chunk0);
     if (r >= n_rows) return;
-    const int chunk = (int)(unit - r * n_chunk);
-    const int c = chunk * 256 + lane * 8;
-    float v[8];
+    const T *row = x + (r < N ? (rows.R >= N ? r * rows.s_i : rows.off(r)) : 0);   // no division for one stride
+    const bool vec = ((uintptr_t)row & 15u) == 0;
+    uint4 u[kQChunks][kVecs];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = 0.f;
-    const bool valid = r < N && c < D;                     // D is a multiple of 64: an octet is whole or absent
-    if (valid) {
-        const T *p = x + rows.off(r) + c;
-        if (((uintptr_t)p & 15u) == 0) {
+    for (int k = 0; k < kQChunks; ++k) {
+        const int c = (chunk0 + k) * kQChunk + lane * 8;   // D is a multiple of 64: an octet is whole or absent
 #pragma unroll
-            for (int i = 0; i < 8 / Elem<T>::kVec; ++i)
-                Elem<T>::unpack(ldg_stream(reinterpret_cast<const uint4 *>(p) + i), v + i * Elem<T>::kVec);
-        } else {
+        for (int i = 0; i < kVecs; ++i) u[k][i] = make_uint4(0u, 0u, 0u, 0u);
+        if (r < N && c < D) {
+            if (vec) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = Elem<T>::load1(p + i);
+                for (int i = 0; i < kVecs; ++i) u[k][i] = ldg_stream(reinterpret_cast<const uint4 *>(row + c) + i);
+            } else {
+                T *e = reinterpret_cast<T *>(u[k]);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) e[i] = row[c + i];
+            }
         }
     }
-    uint32_t amax = 0;                                     // bit patterns of |x| order like the values, NaN highest
 #pragma unroll
-    for (int i = 0; i < 8; ++i) amax = max(amax, __float_as_uint(v[i]) & 0x7fffffffu);
-    amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-    amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-    const uint32_t e = amax >> 23;
-    const uint32_t byte = e == 255u ? 255u : e > 2u ? e - 2u : 0u;
-    if (valid) {
-        const float inv = __uint_as_float((254u - min(byte, 253u)) << 23);   // 2^(127 - byte)
+    for (int k = 0; k < kQChunks; ++k) {
+        const int chunk = chunk0 + k, c = chunk * kQChunk + lane * 8;
+        if (chunk * kQChunk >= D) break;                   // uniform in the warp
+        const bool valid = r < N && c < D;
+        float v[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = byte == 255u ? 0.f : v[i] * inv;
-        *reinterpret_cast<uint32_t *>(codes + r * (D / 2) + (c >> 1)) = e2m1x8(v);
+        for (int i = 0; i < kVecs; ++i) Elem<T>::unpack(u[k][i], v + i * Elem<T>::kVec);
+        uint32_t amax = 0;                                 // bit patterns of |x| order like the values, NaN highest
+#pragma unroll
+        for (int i = 0; i < 8; ++i) amax = max(amax, __float_as_uint(v[i]) & 0x7fffffffu);
+        amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+        amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+        const uint32_t e = amax >> 23;
+        const uint32_t byte = e == 255u ? 255u : e > 2u ? e - 2u : 0u;
+        if (valid) {
+            const float inv = __uint_as_float((254u - min(byte, 253u)) << 23);   // 2^(127 - byte)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = byte == 255u ? 0.f : v[i] * inv;
+            *reinterpret_cast<uint32_t *>(codes + r * (D / 2) + (c >> 1)) = e2m1x8(v);
+        }
+        uint32_t word = valid ? byte << (8 * ((lane >> 2) & 3)) : 0u;
+        word |= __shfl_xor_sync(0xffffffffu, word, 4);
+        word |= __shfl_xor_sync(0xffffffffu, word, 8);
+        const int kt = chunk * 2 + (lane >> 4);
+        if ((lane & 15) == 0 && kt < n_kt) *reinterpret_cast<uint32_t *>(scales + scale_word(r, kt, n_kt)) = word;
     }
-    uint32_t word = valid ? byte << (8 * ((lane >> 2) & 3)) : 0u;
-    word |= __shfl_xor_sync(0xffffffffu, word, 4);
-    word |= __shfl_xor_sync(0xffffffffu, word, 8);
-    const int kt = chunk * 2 + (lane >> 4);
-    if ((lane & 15) == 0 && kt < n_kt) *reinterpret_cast<uint32_t *>(scales + scale_word(r, kt, n_kt)) = word;
 }
 
 cudaError_t launch_mxfp4_quantize(const Mxfp4QuantArgs &a) {
-    const int64_t n_rows = (a.N + 127) / 128 * 128, units = n_rows * ((a.D + 255) / 256);
-    const int64_t blocks = (units + kQThreads / 32 - 1) / (kQThreads / 32);
-    if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
+    const QuantGrid g = quant_grid((a.N + 127) / 128 * 128, a.D);
+    if (!g.ok) return cudaErrorInvalidValue;
     const Rows rows{a.R, a.s_o, a.s_i};
+    uint8_t *codes = static_cast<uint8_t *>(a.codes), *scales = static_cast<uint8_t *>(a.scales);
     if (a.bf16)
-        return launch_pdl(mxfp4_quantize_kernel<__nv_bfloat16>, dim3((unsigned)blocks), dim3(kQThreads), 0, a.stream,
-                          static_cast<const __nv_bfloat16 *>(a.x), rows, a.N, n_rows, (int)a.D,
-                          static_cast<uint8_t *>(a.codes), static_cast<uint8_t *>(a.scales));
-    return launch_pdl(mxfp4_quantize_kernel<float>, dim3((unsigned)blocks), dim3(kQThreads), 0, a.stream,
-                      static_cast<const float *>(a.x), rows, a.N, n_rows, (int)a.D, static_cast<uint8_t *>(a.codes),
-                      static_cast<uint8_t *>(a.scales));
+        return launch_pdl(mxfp4_quantize_kernel<__nv_bfloat16>, dim3(g.blocks), dim3(kQThreads), 0, a.stream,
+                          static_cast<const __nv_bfloat16 *>(a.x), rows, a.N, g.rows, g.groups, (int)a.D, codes, scales);
+    return launch_pdl(mxfp4_quantize_kernel<float>, dim3(g.blocks), dim3(kQThreads), 0, a.stream,
+                      static_cast<const float *>(a.x), rows, a.N, g.rows, g.groups, (int)a.D, codes, scales);
 }
 
-// The value of a code times 2^(byte - 127); exact in fp32 (a subnormal scale
-// included), NaN for byte 255.
-__device__ __forceinline__ float e2m1_value(uint32_t code) {
-    // exponent field e and mantissa bit m: e ? (1 + m / 2) 2^(e - 1) : m / 2
-    const uint32_t e = (code >> 1) & 3u, m = code & 1u;
-    const float mag = e ? __uint_as_float(((126u + e) << 23) | (m << 22)) : 0.5f * (float)m;
-    return code & 8u ? -mag : mag;
+// Eight codes to their values (the hardware's conversion to fp16, exact).
+__device__ __forceinline__ void e2m1x8_values(uint32_t w, float (&v)[8]) {
+    uint32_t h[4];
+    asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+        "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %2, b2;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
+        : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+        : "r"(w));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h[i]));
+        v[2 * i] = f.x;
+        v[2 * i + 1] = f.y;
+    }
 }
 
+// 2^(byte - 127), exact in fp32 (a subnormal for byte 0), NaN for byte 255.
 __device__ __forceinline__ float e8m0_value(uint32_t byte) {
     return byte == 255u ? qnan() : byte ? __uint_as_float(byte << 23) : __uint_as_float(0x00400000u);
 }
 
 template <typename T>
 __global__ void __launch_bounds__(kQThreads)
-mxfp4_dequantize_kernel(const uint8_t *__restrict__ codes, const uint8_t *__restrict__ scales, int64_t N, int D,
-                        T *__restrict__ out) {
+mxfp4_dequantize_kernel(const uint8_t *__restrict__ codes, const uint8_t *__restrict__ scales, int64_t N, int64_t groups,
+                        int D, T *__restrict__ out) {
     pdl_enter<true>();
-    const int n_kt = (D + 127) / 128, per_row = D / 8;
-    const int64_t i = (int64_t)blockIdx.x * kQThreads + threadIdx.x;
-    const int64_t r = i / per_row;
+    const int lane = threadIdx.x & 31, n_kt = (D + 127) / 128;
+    int chunk0;
+    const int64_t r = quant_place(groups, chunk0);
     if (r >= N) return;
-    const int c = (int)(i - r * per_row) * 8;
-    const uint32_t w = __ldg(reinterpret_cast<const uint32_t *>(codes + r * (D / 2) + (c >> 1)));
-    const float s = e8m0_value(__ldg(scales + scale_word(r, c >> 7, n_kt) + ((c >> 5) & 3)));
-    float v[8];
+    uint32_t w[kQChunks], s[kQChunks];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) v[k] = e2m1_value(w >> (4 * k)) * s;
-    T *p = out + r * (int64_t)D + c;
+    for (int k = 0; k < kQChunks; ++k) {
+        const int c = (chunk0 + k) * kQChunk + lane * 8;
+        w[k] = s[k] = 0u;
+        if (c < D) {
+            w[k] = __ldg(reinterpret_cast<const uint32_t *>(codes + r * (D / 2) + (c >> 1)));
+            s[k] = __ldg(scales + scale_word(r, c >> 7, n_kt) + ((c >> 5) & 3));
+        }
+    }
 #pragma unroll
-    for (int k = 0; k < 8 / Elem<T>::kVec; ++k)
-        stg_stream(reinterpret_cast<uint4 *>(p) + k, Elem<T>::pack(v + k * Elem<T>::kVec));
+    for (int k = 0; k < kQChunks; ++k) {
+        const int c = (chunk0 + k) * kQChunk + lane * 8;
+        if (c >= D) break;
+        float v[8];
+        e2m1x8_values(w[k], v);
+        const float scale = e8m0_value(s[k]);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] *= scale;         // exact: at least 2^-128 or 0
+        T *p = out + r * (int64_t)D + c;
+#pragma unroll
+        for (int i = 0; i < 8 / Elem<T>::kVec; ++i)
+            stg_stream(reinterpret_cast<uint4 *>(p) + i, Elem<T>::pack(v + i * Elem<T>::kVec));
+    }
 }
 
 cudaError_t launch_mxfp4_dequantize(const Mxfp4DequantArgs &a) {
-    const int64_t blocks = (a.N * (a.D / 8) + kQThreads - 1) / kQThreads;
-    if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
+    const QuantGrid g = quant_grid(a.N, a.D);
+    if (!g.ok) return cudaErrorInvalidValue;
     const uint8_t *codes = static_cast<const uint8_t *>(a.codes), *scales = static_cast<const uint8_t *>(a.scales);
     if (a.bf16)
-        return launch_pdl(mxfp4_dequantize_kernel<__nv_bfloat16>, dim3((unsigned)blocks), dim3(kQThreads), 0, a.stream,
-                          codes, scales, a.N, (int)a.D, static_cast<__nv_bfloat16 *>(a.out));
-    return launch_pdl(mxfp4_dequantize_kernel<float>, dim3((unsigned)blocks), dim3(kQThreads), 0, a.stream, codes,
-                      scales, a.N, (int)a.D, static_cast<float *>(a.out));
+        return launch_pdl(mxfp4_dequantize_kernel<__nv_bfloat16>, dim3(g.blocks), dim3(kQThreads), 0, a.stream, codes,
+                          scales, a.N, g.groups, (int)a.D, static_cast<__nv_bfloat16 *>(a.out));
+    return launch_pdl(mxfp4_dequantize_kernel<float>, dim3(g.blocks), dim3(kQThreads), 0, a.stream, codes, scales, a.N,
+                      g.groups, (int)a.D, static_cast<float *>(a.out));
 }
 
 // ---------------------------------------------------------------------------
@@ -387,9 +446,15 @@ static cudaError_t launch_linear_t(const LinearMxfp4Args &a) {
     CUtensorMap tw, tx;
     if (!make_map_codes(&tw, a.w_codes, a.V, a.D, kXM) || !make_map_codes(&tx, a.x_codes, a.N, a.D, kNT))
         return cudaErrorInvalidValue;
-    cudaError_t e = cudaFuncSetAttribute(linear_mxfp4_kernel<kNT, T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         x_smem_bytes(kNT));
-    if (e != cudaSuccess) return e;
+    static std::atomic<uint64_t> attr_done{0};
+    int dev = 0;
+    cudaGetDevice(&dev);
+    if (!(attr_done.load() >> (dev & 63) & 1u)) {
+        cudaError_t e = cudaFuncSetAttribute(linear_mxfp4_kernel<kNT, T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             x_smem_bytes(kNT));
+        if (e != cudaSuccess) return e;
+        attr_done.fetch_or(1ull << (dev & 63));
+    }
     const int64_t n_tiles = ((a.V + kXM - 1) / kXM) * ((a.N + kNT - 1) / kNT);
     return launch_pdl(linear_mxfp4_kernel<kNT, T>, dim3((unsigned)std::min<int64_t>(n_tiles, sm_count())),
                       dim3(kXThreads), x_smem_bytes(kNT), a.stream, tw, tx, static_cast<const uint8_t *>(a.w_scales),
