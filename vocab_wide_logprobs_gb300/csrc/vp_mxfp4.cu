@@ -10,6 +10,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <type_traits>
 
 #include "vp_device.cuh"
 #include "vp_gemm_host.cuh"
@@ -212,15 +213,16 @@ cudaError_t launch_mxfp4_dequantize(const Mxfp4DequantArgs &a) {
 // ---------------------------------------------------------------------------
 // Product: y[n, v] = sum_k x[n, k] w[v, k]
 // ---------------------------------------------------------------------------
-// The vocabulary runs along the MMA's 128 rows (operand A, the accumulator's
-// lanes) and the tokens along its columns (operand B), so that a single token
-// still reads the head at full width and a warp's stores of one token are
-// consecutive. K steps of 64 (kind::mxf4, one scale for each 32 columns);
-// a stage holds 256 columns: 128-byte rows of both operands in the 128-byte
-// swizzle and two scale tiles of each. One thread copies a stage's scales to
-// tensor memory (tcgen05.cp, executed in order with the MMAs that it is followed
-// by; two buffers) and issues the MMAs.
-constexpr int kXM = 128;                     // vocabulary rows of a tile
+// The vocabulary runs along the MMA's rows (operand A, the accumulator's lanes)
+// and the tokens along its columns (operand B), so that a single token still reads
+// the head at full width and a warp's stores of one token are consecutive. K steps
+// of 64 (kind::mxf4, one scale for each 32 columns); a stage holds 256 columns:
+// 128-byte rows of both operands in the 128-byte swizzle and two scale tiles for
+// each 128 rows. One thread copies a stage's scales to tensor memory (tcgen05.cp,
+// executed in order with the MMAs that follow it) and issues its MMAs; every stage
+// in flight has scale columns of its own, so a copy never meets an MMA that still
+// reads them. (Copying a stage ahead of the MMAs measured 4% slower.)
+constexpr int kXM = 128;                     // vocabulary rows of a CTA's tile
 constexpr int kXK = 256;                     // columns of a stage
 constexpr int kXRow = kXK / 2;               // their bytes in a row
 constexpr int kXAStage = kXM * kXRow;       // 16 KB
@@ -230,8 +232,9 @@ constexpr int kXThreads = 192;               // TMA warp, MMA warp, 4 epilogue w
 constexpr int x_stage_bytes(int nt) { return kXAStage + nt * kXRow + 2 * kXSStage; }
 constexpr int x_stages(int nt) { return (200 * 1024) / x_stage_bytes(nt) < 10 ? (200 * 1024) / x_stage_bytes(nt) : 10; }
 constexpr int x_smem_bytes(int nt) { return x_stages(nt) * x_stage_bytes(nt) + 1024; }
-constexpr uint32_t x_tmem_cols(int nt) {     // two accumulators, two buffers of 8 + 8 scale columns
-    return 2 * nt + 32 <= 64 ? 64 : 2 * nt + 32 <= 128 ? 128 : 2 * nt + 32 <= 256 ? 256 : 512;
+constexpr uint32_t x_tmem_cols(int nt) {     // two accumulators, 8 + 8 scale columns of each stage
+    const int n = 2 * nt + 16 * x_stages(nt);
+    return n <= 64 ? 64 : n <= 128 ? 128 : n <= 256 ? 256 : 512;
 }
 
 // Instruction descriptor of kind::mxf4: E2M1 operands, both K-major, E8M0 scales.
@@ -284,6 +287,30 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, float *v) {
     for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
 }
 
+// One lane of a converged warp. Tensor-core and copy instructions take their operands
+// from the warp's uniform registers; behind elect.sync the compiler knows that one
+// lane is active and moves them there directly, behind `lane == 0` it does not (the
+// pair's MMAs alone, 8192 tokens at half their width: 360 us against 714).
+__device__ __forceinline__ bool elect_one() {
+    uint32_t one;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(one));
+    return one != 0;
+}
+
+// The issuing thread works at the latency of its own instructions, and an MMA of the
+// pair takes 128 clocks: descriptors are bases plus multiples of 16 bytes (the
+// address field holds them without carry: shared memory ends below 2^18), the
+// stage is counted and not divided for, and a whole stage's MMAs are unrolled.
+struct StageCount {
+    uint32_t st = 0, phase = 0;
+    __device__ __forceinline__ void next(uint32_t n) {
+        if (++st == n) {
+            st = 0;
+            phase ^= 1;
+        }
+    }
+};
+
 template <int kNT>
 struct Mxfp4Bars {
     uint64_t full[x_stages(kNT)], empty[x_stages(kNT)], acc_full[2], acc_empty[2];
@@ -326,15 +353,20 @@ linear_mxfp4_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_const
     pdl_enter<false>();
 
     if (warp == 0) {
-        if (lane == 0) {
+        if (elect_one()) {
             const uint64_t pol_w = l2_policy(n_tb > 1 ? 2 : 1), pol_x = l2_policy(2);
-            uint32_t it = 0;
+            StageCount at;
+            uint32_t it = 0;                             // stages begun, up to kStages
             bool ok = true;
             for (int64_t tile = blockIdx.x; tile < n_tiles && ok; tile += gridDim.x) {
                 const int vb = (int)(tile / n_tb), tb = (int)(tile - (int64_t)vb * n_tb);
-                for (int kb = 0; kb < n_k; ++kb, ++it) {
-                    const uint32_t st = it % kStages, use = it / kStages;
-                    if (use > 0 && !mbar_wait(&bars.empty[st], (use - 1) & 1)) { ok = false; break; }
+                for (int kb = 0; kb < n_k; ++kb, at.next(kStages)) {
+                    const uint32_t st = at.st;
+                    if (it == (uint32_t)kStages) {
+                        if (!mbar_wait(&bars.empty[st], at.phase ^ 1)) { ok = false; break; }
+                    } else {
+                        ++it;
+                    }
                     uint8_t *a = smem + st * kStageBytes, *b = a + kXAStage, *sa = b + kNT * kXRow, *sb = sa + kXSStage;
                     const uint32_t sbytes = 512u * (uint32_t)min(2, n_kt - 2 * kb);
                     mbar_arrive_expect_tx(&bars.full[st], kXAStage + kNT * kXRow + 2 * sbytes);
@@ -347,38 +379,47 @@ linear_mxfp4_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_const
             }
             if (!ok) {
                 atomicOr(&g_linear_fault, 1u);
-                // the copies in flight land before the CTA gives up its shared memory
-                for (uint32_t i = it > (uint32_t)kStages ? it - kStages : 0; i < it; ++i)
-                    mbar_wait(&bars.full[i % kStages], (i / kStages) & 1);
+                // the copies in flight land before the CTA gives up its shared memory: every other
+                // stage's last one (this stage's are in use or done)
+                for (uint32_t i = 0; i < it; ++i) {
+                    if (i == at.st) continue;
+                    mbar_wait(&bars.full[i], i < at.st ? at.phase : at.phase ^ 1);
+                }
             }
         }
     } else if (warp == 1) {
-        if (lane == 0) {
+        if (elect_one()) {
             constexpr uint32_t idesc = umma_idesc_mxf4(kXM, kNT);
-            uint32_t it = 0, j = 0;
+            const uint64_t a0 = umma_desc_sw128(smem), b0 = umma_desc_sw128(smem + kXAStage),
+                           sa0 = scale_desc(smem + kXAStage + kNT * kXRow), sb0 = sa0 + (kXSStage >> 4);
+            StageCount at;
             bool ok = true;
+            uint32_t j = 0;
             for (int64_t tile = blockIdx.x; tile < n_tiles && ok; tile += gridDim.x, ++j) {
                 const uint32_t buf = j & 1, use_b = j >> 1;
                 if (use_b > 0 && !mbar_wait(&bars.acc_empty[buf], (use_b - 1) & 1)) { ok = false; break; }
                 tc_fence_after();
                 const uint32_t d = tmem + buf * kNT;
-                for (int kb = 0; kb < n_k; ++kb, ++it) {
-                    const uint32_t st = it % kStages;
-                    if (!mbar_wait(&bars.full[st], (it / kStages) & 1)) { ok = false; break; }
+                for (int kb = 0; kb < n_k; ++kb) {
+                    if (!mbar_wait(&bars.full[at.st], at.phase)) { ok = false; break; }
                     tc_fence_after();
-                    const uint8_t *a = smem + st * kStageBytes, *b = a + kXAStage, *sa = b + kNT * kXRow,
-                                  *sb = sa + kXSStage;
-                    const uint32_t sc = tmem + kScaleCol + (it & 1) * 16;
-                    const int steps = min(kXK, D - kb * kXK) / 64;
-                    for (int kt = 0; kt < (steps + 1) / 2; ++kt) {
-                        tmem_copy_scales(sc + 4 * kt, scale_desc(sa + 512 * kt));
-                        tmem_copy_scales(sc + 8 + 4 * kt, scale_desc(sb + 512 * kt));
+                    const uint32_t to = at.st * (kStageBytes >> 4);
+                    const uint64_t a = a0 + to, b = b0 + to, sa = sa0 + to, sb = sb0 + to;
+                    const uint32_t sc = tmem + kScaleCol + at.st * 16;
+                    tmem_copy_scales(sc, sa);
+                    tmem_copy_scales(sc + 8, sb);
+                    if (n_kt - 2 * kb > 1) {
+                        tmem_copy_scales(sc + 4, sa + 32);
+                        tmem_copy_scales(sc + 12, sb + 32);
                     }
-                    for (int kk = 0; kk < steps; ++kk)
-                        umma_mxf4(d, umma_desc_sw128(a + kk * 32), umma_desc_sw128(b + kk * 32),
-                                  idesc_scale_id(idesc, (kk & 1) * 2), sc + 4 * (kk >> 1), sc + 8 + 4 * (kk >> 1),
-                                  (kb | kk) != 0);
-                    umma_commit(&bars.empty[st]);
+                    const int steps = min(kXK, D - kb * kXK) / 64;
+#pragma unroll
+                    for (int kk = 0; kk < kXK / 64; ++kk)
+                        if (kk < steps)
+                            umma_mxf4(d, a + 2 * kk, b + 2 * kk, idesc_scale_id(idesc, (kk & 1) * 2), sc + 4 * (kk >> 1),
+                                      sc + 8 + 4 * (kk >> 1), (kb | kk) != 0);
+                    umma_commit(&bars.empty[at.st]);
+                    at.next(kStages);
                 }
                 umma_commit(&bars.acc_full[buf]);
             }
@@ -420,6 +461,212 @@ linear_mxfp4_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_const
     if (warp == 1) tmem_dealloc(tmem, x_tmem_cols(kNT));
 }
 
+// ---------------------------------------------------------------------------
+// The same product on CTA pairs (tcgen05 cta_group::2), for more tokens than a
+// single CTA's tile: a pair computes 256 vocabulary rows x 256 tokens. CTA r holds
+// rows 128 r .. of the W tile and of the accumulator, tokens 128 r .. of the x tile
+// and the scales of its 128 rows and of all 256 tokens. Per 256 columns of K a CTA
+// takes 35 KB for 128 x 256 outputs, half of what a 128 x 128 tile does; that tile
+// was bound by this traffic (57 bytes a clock and SM).
+//   Tensor memory: the scales of six stages take 144 of the 512 columns, so the two
+// accumulators overlap in 144 columns. The epilogue reads these columns into
+// registers first and lets the next tile's MMAs begin; the other 112 it reads while
+// they run.
+// ---------------------------------------------------------------------------
+constexpr int kYStages = 6;
+constexpr int kYT = 256;                                  // tokens of a tile
+constexpr int kYBStage = kYT / 2 * kXRow;                 // 16 KB
+constexpr int kYStageBytes = kXAStage + kYBStage + 3 * kXSStage;
+constexpr int kYSmemBytes = kYStages * kYStageBytes + 1024;
+constexpr uint32_t kYScaleCols = 8 + 16;                  // of a stage: two scale tiles of W, four of x
+constexpr uint32_t kYScaleCol = 512 - kYStages * kYScaleCols;
+constexpr uint32_t kYAcc1 = kYScaleCol - kYT;             // the second accumulator's first column
+constexpr int kYOverlap = kYT - (int)kYAcc1;
+static_assert(kYAcc1 == 112 && kYOverlap == 144, "the epilogue's reads are written for these");
+
+struct PairMxfp4Bars {
+    uint64_t full[kYStages], empty[kYStages], acc_full[2], shared_free;
+    uint32_t tmem_base;
+};
+
+__device__ __forceinline__ void umma_mxf4_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                               uint32_t sfa, uint32_t sfb, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(
+            d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+        : "memory");
+}
+
+// In both CTAs, from the same place of each one's shared memory.
+__device__ __forceinline__ void tmem_copy_scales_pair(uint32_t taddr, uint64_t desc) {
+    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+}
+
+template <typename T>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kXThreads, 1)
+linear_mxfp4_pair_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_x,
+                         const __grid_constant__ CUtensorMap tm_ws, const __grid_constant__ CUtensorMap tm_xs, int N, int V,
+                         int D, T *__restrict__ y) {
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ PairMxfp4Bars bars;
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_rank();
+    const int n_vp = (V + 2 * kXM - 1) / (2 * kXM), n_tb = (N + kYT - 1) / kYT;
+    const int64_t n_tiles = (int64_t)n_vp * n_tb, pair = blockIdx.x >> 1, n_pairs = gridDim.x >> 1;
+    const int n_k = (D + kXK - 1) / kXK, n_kt = (D + 127) / 128;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kYStages; ++s) {
+            mbar_init(&bars.full[s], 1);
+            mbar_init(&bars.empty[s], 1);
+        }
+        mbar_init(&bars.acc_full[0], 1);
+        mbar_init(&bars.acc_full[1], 1);
+        mbar_init(&bars.shared_free, 2 * (kXThreads - 64));   // the epilogue threads of both CTAs
+        fence_mbar_init();
+        prefetch_tensormap(&tm_w);
+        prefetch_tensormap(&tm_x);
+        prefetch_tensormap(&tm_ws);
+        prefetch_tensormap(&tm_xs);
+    }
+    if (warp == 1) tmem_alloc_pair(&bars.tmem_base, 512);
+    tc_fence_before();
+    cluster_sync();                                      // barriers and tensor memory ready in both CTAs
+    tc_fence_after();
+    const uint32_t tmem = bars.tmem_base;
+    pdl_enter<false>();
+
+    if (warp == 0) {
+        // ---------------- TMA producer (both CTAs; all bytes count on the leader's barrier) ----------------
+        if (elect_one()) {
+            const uint64_t keep = l2_policy(2);
+            StageCount at;
+            bool ok = true, again = false;               // again: the ring has been filled once
+            for (int64_t tile = pair; tile < n_tiles && ok; tile += n_pairs) {
+                const int vp = (int)(tile / n_tb), tb = (int)(tile - (int64_t)vp * n_tb);
+                const int wb = 2 * vp + (int)rank;
+                for (int kb = 0; kb < n_k; ++kb, at.next(kYStages)) {
+                    const uint32_t st = at.st;
+                    if (again && !mbar_wait_cluster(&bars.empty[st], at.phase ^ 1)) { ok = false; break; }
+                    again = again || st == kYStages - 1;
+                    uint8_t *a = smem + st * kYStageBytes, *b = a + kXAStage, *sa = b + kYBStage, *sb = sa + kXSStage;
+                    const uint32_t fb = cluster_addr(&bars.full[st], 0);
+                    if (rank == 0) mbar_arrive_expect_tx(&bars.full[st], 2 * kYStageBytes);
+                    tma_load_2d_pair(a, &tm_w, kb * kXRow, wb * kXM, fb, keep);
+                    tma_load_2d_pair(b, &tm_x, kb * kXRow, tb * kYT + (int)rank * kXM, fb, keep);
+                    tma_load_2d_pair(sa, &tm_ws, kb * (kXSStage / 4), wb, fb, keep);
+                    tma_load_2d_pair(sb, &tm_xs, kb * (kXSStage / 4), 2 * tb, fb, keep);
+                    tma_load_2d_pair(sb + kXSStage, &tm_xs, kb * (kXSStage / 4), 2 * tb + 1, fb, keep);
+                }
+            }
+            if (!ok) atomicOr(&g_linear_fault, 1u);
+        }
+    } else if (warp == 1) {
+        // ---------------- MMA issuer (leader only) ----------------
+        if (rank == 0 && elect_one()) {
+            constexpr uint32_t idesc = umma_idesc_mxf4(2 * kXM, kYT);
+            const uint64_t a0 = umma_desc_sw128(smem), b0 = umma_desc_sw128(smem + kXAStage),
+                           sa0 = scale_desc(smem + kXAStage + kYBStage), sb0 = sa0 + (kXSStage >> 4);
+            StageCount at;
+            bool ok = true;
+            uint32_t j = 0;
+            for (int64_t tile = pair; tile < n_tiles && ok; tile += n_pairs, ++j) {
+                // the columns shared with the tile before it are read (and all of the one before that)
+                if (j > 0 && !mbar_wait_cluster(&bars.shared_free, (j - 1) & 1)) { ok = false; break; }
+                tc_fence_after();
+                const uint32_t d = tmem + (j & 1 ? kYAcc1 : 0u);
+                for (int kb = 0; kb < n_k; ++kb) {
+                    if (!mbar_wait(&bars.full[at.st], at.phase)) { ok = false; break; }
+                    tc_fence_after();
+                    const uint32_t to = at.st * (kYStageBytes >> 4);
+                    const uint64_t a = a0 + to, b = b0 + to, sa = sa0 + to, sb = sb0 + to, sb1 = sb + (kXSStage >> 4);
+                    const uint32_t sc = tmem + kYScaleCol + at.st * kYScaleCols;
+                    tmem_copy_scales_pair(sc, sa);
+                    tmem_copy_scales_pair(sc + 8, sb);
+                    tmem_copy_scales_pair(sc + 12, sb1);
+                    if (n_kt - 2 * kb > 1) {
+                        tmem_copy_scales_pair(sc + 4, sa + 32);
+                        tmem_copy_scales_pair(sc + 16, sb + 32);
+                        tmem_copy_scales_pair(sc + 20, sb1 + 32);
+                    }
+                    const int steps = min(kXK, D - kb * kXK) / 64;
+#pragma unroll
+                    for (int kk = 0; kk < kXK / 64; ++kk)
+                        if (kk < steps)
+                            umma_mxf4_pair(d, a + 2 * kk, b + 2 * kk, idesc_scale_id(idesc, (kk & 1) * 2),
+                                           sc + 4 * (kk >> 1), sc + 8 + 8 * (kk >> 1), (kb | kk) != 0);
+                    umma_commit_pair(&bars.empty[at.st]);
+                    at.next(kYStages);
+                }
+                umma_commit_pair(&bars.acc_full[j & 1]);
+            }
+            if (!ok) atomicOr(&g_linear_fault, 2u);
+        }
+    } else {
+        // ---------------- epilogue (both CTAs) ----------------
+        const int q = warp & 3;
+        const uint32_t lanes = (uint32_t)(q * 32) << 16;
+        uint32_t j = 0;
+        bool ok = true;
+        for (int64_t tile = pair; tile < n_tiles; tile += n_pairs, ++j) {
+            const int vp = (int)(tile / n_tb), tb = (int)(tile - (int64_t)vp * n_tb);
+            const int64_t t0 = (int64_t)tb * kYT, v = (int64_t)(2 * vp + (int)rank) * kXM + q * 32 + lane;
+            if (ok && !mbar_wait_cluster(&bars.acc_full[j & 1], (j >> 1) & 1)) {
+                ok = false;
+                atomicOr(&g_linear_fault, 4u);
+            }
+            tc_fence_after();
+            const bool all = __all_sync(0xffffffffu, ok);
+            // tokens t0 + c .. of the values acc[0 .. n)
+            auto store = [&](int c, const float *acc, auto count) {
+                constexpr int n = decltype(count)::value;
+                T *p = y + (t0 + c) * V + v;
+                if (v < V) {
+                    if (t0 + c + n <= N) {
+#pragma unroll
+                        for (int i = 0; i < n; ++i) Elem<T>::store1(p + (int64_t)i * V, acc[i]);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < n; ++i)
+                            if (t0 + c + i < N) Elem<T>::store1(p + (int64_t)i * V, acc[i]);
+                    }
+                }
+            };
+            // columns shared with the other accumulator: the first one's last, the second one's first
+            const int c0 = j & 1 ? 0 : (int)kYAcc1;
+            const uint32_t acc0 = tmem + (j & 1 ? kYAcc1 : 0u) + lanes;
+            uint32_t r[kYOverlap];
+            if (all) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) tmem_ld32_issue(acc0 + c0 + 32 * k, reinterpret_cast<uint32_t(&)[32]>(r[32 * k]));
+                tmem_ld16(acc0 + c0 + 128, reinterpret_cast<float *>(r + 128));   // waits for all
+            }
+            tc_fence_before();
+            mbar_arrive_cluster(cluster_addr(&bars.shared_free, 0));
+            if (all) store(c0, reinterpret_cast<const float *>(r), std::integral_constant<int, kYOverlap>());
+            const int c1 = j & 1 ? kYOverlap : 0;
+            if (all) {
+#pragma unroll 1
+                for (int c = 0; c < (int)kYAcc1; c += 16) {
+                    float acc[16];
+                    tmem_ld16(acc0 + c1 + c, acc);
+                    store(c1 + c, acc, std::integral_constant<int, 16>());
+                }
+            }
+            tc_fence_before();
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();                                      // no arrival or copy still targets either CTA
+    tc_fence_after();
+    if (warp == 1) tmem_dealloc_pair(tmem, 512);
+}
+
 // Codes [rows, D / 2] as bytes: boxes of kXRow bytes x box_rows, 128-byte swizzle;
 // zeros (the code of 0) past the extents.
 static bool make_map_codes(CUtensorMap *map, const void *ptr, int64_t rows, int64_t D, int box_rows) {
@@ -434,6 +681,32 @@ static bool make_map_codes(CUtensorMap *map, const void *ptr, int64_t rows, int6
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Scale tiles as rows of 32-bit words, one row for each 128 rows of the matrix;
+// boxes of one row and two tiles. Zeros (2^-127) past the extents.
+static bool make_map_scales(CUtensorMap *map, const void *ptr, int64_t rows, int64_t D) {
+    auto enc = encode_fn();
+    if (!enc) return false;
+    const cuuint64_t words = (cuuint64_t)((D + 127) / 128) * 128;
+    cuuint64_t dims[2] = {words, (cuuint64_t)((rows + 127) / 128)};
+    cuuint64_t strides[1] = {words * 4};
+    cuuint32_t box[2] = {(cuuint32_t)(kXSStage / 4), 1u};
+    cuuint32_t estr[2] = {1, 1};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, const_cast<void *>(ptr), dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Sets a kernel's shared memory limit once per device.
+template <typename K>
+static cudaError_t allow_smem(K kernel, int bytes, std::atomic<uint64_t> &done) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess || done.load(std::memory_order_relaxed) >> (dev & 63) & 1u) return e;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) done.fetch_or(1ull << (dev & 63), std::memory_order_relaxed);
+    return e;
+}
+
 static int sm_count() {
     int dev = 0, sms = 0;
     cudaGetDevice(&dev);
@@ -446,15 +719,9 @@ static cudaError_t launch_linear_t(const LinearMxfp4Args &a) {
     CUtensorMap tw, tx;
     if (!make_map_codes(&tw, a.w_codes, a.V, a.D, kXM) || !make_map_codes(&tx, a.x_codes, a.N, a.D, kNT))
         return cudaErrorInvalidValue;
-    static std::atomic<uint64_t> attr_done{0};
-    int dev = 0;
-    cudaGetDevice(&dev);
-    if (!(attr_done.load() >> (dev & 63) & 1u)) {
-        cudaError_t e = cudaFuncSetAttribute(linear_mxfp4_kernel<kNT, T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             x_smem_bytes(kNT));
-        if (e != cudaSuccess) return e;
-        attr_done.fetch_or(1ull << (dev & 63));
-    }
+    static std::atomic<uint64_t> done{0};
+    cudaError_t e = allow_smem(linear_mxfp4_kernel<kNT, T>, x_smem_bytes(kNT), done);
+    if (e != cudaSuccess) return e;
     const int64_t n_tiles = ((a.V + kXM - 1) / kXM) * ((a.N + kNT - 1) / kNT);
     return launch_pdl(linear_mxfp4_kernel<kNT, T>, dim3((unsigned)std::min<int64_t>(n_tiles, sm_count())),
                       dim3(kXThreads), x_smem_bytes(kNT), a.stream, tw, tx, static_cast<const uint8_t *>(a.w_scales),
@@ -462,11 +729,28 @@ static cudaError_t launch_linear_t(const LinearMxfp4Args &a) {
 }
 
 template <typename T>
+static cudaError_t launch_linear_pair(const LinearMxfp4Args &a) {
+    CUtensorMap tw, tx, tws, txs;
+    if (!make_map_codes(&tw, a.w_codes, a.V, a.D, kXM) || !make_map_codes(&tx, a.x_codes, a.N, a.D, kXM) ||
+        !make_map_scales(&tws, a.w_scales, a.V, a.D) || !make_map_scales(&txs, a.x_scales, a.N, a.D))
+        return cudaErrorInvalidValue;
+    static std::atomic<uint64_t> done{0};
+    cudaError_t e = allow_smem(linear_mxfp4_pair_kernel<T>, kYSmemBytes, done);
+    if (e != cudaSuccess) return e;
+    const int64_t n_tiles = ((a.V + 2 * kXM - 1) / (2 * kXM)) * ((a.N + kYT - 1) / kYT);
+    const int64_t pairs = std::max(1, sm_count() / 2);
+    return launch_pdl(linear_mxfp4_pair_kernel<T>, dim3((unsigned)(2 * std::min(n_tiles, pairs))), dim3(kXThreads),
+                      kYSmemBytes, a.stream, tw, tx, tws, txs, (int)a.N, (int)a.V, (int)a.D, static_cast<T *>(a.y));
+}
+
+// Up to 128 tokens one CTA's tile holds them all; more go to the pairs.
+template <typename T>
 static cudaError_t launch_linear(const LinearMxfp4Args &a) {
     return a.N <= 16 ? launch_linear_t<16, T>(a)
            : a.N <= 32 ? launch_linear_t<32, T>(a)
            : a.N <= 64 ? launch_linear_t<64, T>(a)
-                       : launch_linear_t<128, T>(a);
+           : a.N <= 128 ? launch_linear_t<128, T>(a)
+                        : launch_linear_pair<T>(a);
 }
 
 cudaError_t launch_linear_mxfp4(const LinearMxfp4Args &a) {
