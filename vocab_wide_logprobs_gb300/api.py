@@ -760,11 +760,14 @@ class LogitsRules:
 
     def _take(self, t, dtype, name, per_row=0):
         """The address of a tensor, checked: [rows] or [rows, per_row] elements of dtype; per_row 0: any number."""
-        if t.dtype != dtype:
+        if t.dtype is not dtype:
             raise VPError(3, f"{name}: needs {dtype}, got {t.dtype}")
         if not t.is_contiguous():
             raise VPError(4, f"{name}: needs a contiguous tensor")
-        self._on(t, name)
+        if self.device is None:
+            self.device = t.device
+        elif self.device != t.device:
+            raise VPError(4, f"{name}: on {t.device}, others on {self.device}")
         if per_row:
             shape = t.shape
             if len(shape) != (1 if per_row == 1 else 2) or (per_row > 1 and shape[1] != per_row) or \
@@ -817,14 +820,19 @@ def vp_logits_process_fwd(x, rules: LogitsRules, vocab_start: int = 0, err_word=
     q = rules.check(N, V, x.device)
     _arg(err_word, 1, torch.int32, x, "err_word")
     if y is None:
+        _on_gpu(x)
         y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    elif y.shape != x.shape or y.dtype != x.dtype or y.device != x.device:
-        raise VPError(2 if y.shape != x.shape else 3 if y.dtype != x.dtype else 4, "y needs x's shape, dtype and device")
-    _, _, _, y_s_o, y_s_i = rows_of(y)
-    _rows_apart(y, N, V)
-    _on_gpu(x)
-    _check(_handle().vp_logits_process_fwd(_addr(x), _dtype_code(x), N, V, R, s_o, s_i, vocab_start, q, _addr(y), y_s_o,
-                                            y_s_i, _addr(err_word), _queue(x.device)), "vp_logits_process_fwd")
+        y_s_o, y_s_i = R * V, V
+    else:
+        if y.shape != x.shape or y.dtype != x.dtype or y.device != x.device:
+            raise VPError(2 if y.shape != x.shape else 3 if y.dtype != x.dtype else 4,
+                          "y needs x's shape, dtype and device")
+        _, _, _, y_s_o, y_s_i = rows_of(y)
+        _rows_apart(y, N, V)
+        _on_gpu(x)
+    _check(_handle().vp_logits_process_fwd(x.data_ptr(), _dtype_code(x), N, V, R, s_o, s_i, vocab_start, q,
+                                           y.data_ptr(), y_s_o, y_s_i, _addr(err_word), _queue(x.device)),
+           "vp_logits_process_fwd")
     return y
 
 
@@ -911,8 +919,9 @@ def vp_mxfp4_quantize(x, codes=None, scales=None):
     _arg(codes, N * D // 2, torch.uint8, x, "codes")
     _arg(scales, n, torch.uint8, x, "scales")
     _on_gpu(x)
-    codes = torch.empty((N, D // 2), dtype=torch.uint8, device=x.device) if codes is None else codes
-    scales = torch.empty(n, dtype=torch.uint8, device=x.device) if scales is None else scales
+    device = x.device
+    codes = torch.empty((N, D // 2), dtype=torch.uint8, device=device) if codes is None else codes
+    scales = torch.empty(n, dtype=torch.uint8, device=device) if scales is None else scales
     _check(_handle().vp_mxfp4_quantize(_addr(x), _dtype_code(x), N, D, R, s_o, s_i, _addr(codes), _addr(scales),
                                         _queue(x.device)), "vp_mxfp4_quantize")
     return codes, scales

@@ -32,6 +32,7 @@
 // as a vocabulary shard would, and rules_join_kernel joins a row's slices.
 // The slices depend on V alone, so a row's results do not depend on N.
 #include <atomic>
+#include <type_traits>
 
 #include "vp_device.cuh"
 #include "vp_gemm_host.cuh"
@@ -42,83 +43,127 @@ namespace vp {
 
 constexpr uint32_t kPromptBit = 0x80000000u;
 
+enum RuleOp { kProcFwd = 0, kProcBwd = 1, kLogpFwd = 2, kLogpBwd = 3 };
+
 // A tile's threads and size. Measured on GB300 at 4096 x 75968 bf16 with 1000 ids a
 // row (us, forward / backward of the ruled logprobs): 4 vectors a thread, five CTAs
 // an SM 336 / 268; 8 vectors, three CTAs 364 / 302; 256 threads with 4 vectors,
 // three CTAs 382 / 325. fp32 (2048 rows): 8 vectors 300 / 247, 4 vectors 343 / 320.
-template <typename T> struct Tile {
-    static constexpr int kThreads = 128, kWarps = kThreads / 32;
+template <typename E, int kN> struct Tile {
+    using T = E;
+    static constexpr int kThreads = kN, kWarps = kThreads / 32;
     static constexpr int kVec = Elem<T>::kVec;                // columns of a 16-byte vector
-    static constexpr int kVecs = 32 / kVec;                   // vectors of a thread
-    static constexpr int kCtas = sizeof(T) == 2 ? 5 : 3;      // of an SM
-    static constexpr int kWidth = kThreads * kVecs * kVec;    // columns of a tile: 4096
+    static constexpr int kWidth = 4096;                       // columns of a tile
+    static constexpr int kVecs = kWidth / kVec / kThreads;    // vectors of a thread
+    static constexpr int kCtas = kThreads > 128 || sizeof(T) == 4 ? 3 : 5;   // of an SM
     static constexpr int kWords = kWidth / 32;                // words of the bitmap
     static constexpr uint32_t kAll = kVec == 8 ? 0xffu : 0xfu;
 };
-
-enum RuleOp { kProcFwd = 0, kProcBwd = 1, kLogpFwd = 2, kLogpBwd = 3 };
+constexpr int kRuleThreads = 128;
+// Rules on logits whose histories are longer than a tile: going through the ids is
+// most of the work, and four warps are few for it (64 x 151936 fp32 with up to 16384
+// ids a row: 97 us with 128 threads, 81 with 256; one row with 32768 ids: 58 and 38;
+// 1024 x 75968 bf16 with 1000 ids: 91 and 113).
+constexpr int kRuleThreadsLong = 256;
 
 __device__ __forceinline__ float to_float(float v) { return v; }
 __device__ __forceinline__ float to_float(__nv_bfloat16 v) { return __bfloat162float(v); }
 
-__device__ __forceinline__ void cp_async4(void *smem, const void *p) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"((uint32_t)__cvta_generic_to_shared(smem)), "l"(p)
-                 : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-__device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group 0;" ::: "memory"); }
-
 // Orders this thread's earlier stores to shared memory before later bulk copies there.
 __device__ __forceinline__ void fence_async_proxy() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
-// Tile copies. Rows that start on a 16-byte boundary come as one bulk copy, issued
-// by one thread and awaited by all; of others each thread copies its own vectors
-// (word by word where 4-byte alignment allows), which it alone reads before the
-// next barrier. Columns past the last whole vector are stored by the vector's
-// owner in both cases, padded with zeros.
+// A tile in shared memory lies as it does in memory modulo 16 bytes: column c at byte
+// phase + c sizeof(T) of its buffer, phase that of the tile's address. The whole
+// 16-byte blocks come as one bulk copy, issued by one thread and awaited by all; the
+// up to 15 bytes before and after them are stored by the threads whose vectors reach
+// into them.
 template <typename T>
-__device__ __forceinline__ void stage_tail(T *stage, const T *p, int width) {
-    const int c = width & ~(Tile<T>::kVec - 1);
-    if (c < width && (c / Tile<T>::kVec) % Tile<T>::kThreads == (int)threadIdx.x) {
-#pragma unroll
-        for (int i = 0; i < Tile<T>::kVec; ++i) stage[c + i] = c + i < width ? p[c + i] : T(0.f);
-        fence_async_proxy();
+struct TileSource {
+    const T *p;
+    uint32_t phase;
+    int first, last, width;   // columns [first, last) are whole blocks
+    __device__ __forceinline__ TileSource(const T *src, int w) : p(src), phase((uint32_t)(uintptr_t)src & 15u), width(w) {
+        first = min(w, (int)(((16u - phase) & 15u) / sizeof(T)));
+        last = first + (w - first) / Elem<T>::kVec * Elem<T>::kVec;
     }
-}
+    __device__ __forceinline__ bool bulk() const { return last > first; }
+    __device__ __forceinline__ T *at(T *buffer, int c) const { return buffer + phase / sizeof(T) + c; }
+};
 
-template <typename T>
-__device__ __forceinline__ void stage_unaligned(T *stage, const T *p, int width) {
-    const bool words = ((uintptr_t)p & 3u) == 0;
-#pragma unroll 1
-    for (int v = threadIdx.x; (v + 1) * Tile<T>::kVec <= width; v += Tile<T>::kThreads) {
-        const T *src = p + v * Tile<T>::kVec;
-        T *dst = stage + v * Tile<T>::kVec;
-        if (words) {
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-                cp_async4(reinterpret_cast<uint32_t *>(dst) + q, reinterpret_cast<const uint32_t *>(src) + q);
-        } else {
-            T e[Tile<T>::kVec];
-#pragma unroll
-            for (int i = 0; i < Tile<T>::kVec; ++i) e[i] = src[i];
-#pragma unroll
-            for (int i = 0; i < Tile<T>::kVec; ++i) dst[i] = e[i];
+template <class L>
+__device__ __forceinline__ void stage_edges(const TileSource<typename L::T> &t, typename L::T *buffer) {
+    constexpr int kVec = L::kVec;
+    bool wrote = false;
+    if (t.first > 0 && threadIdx.x == 0) {                // block 0 is read with vector 0
+        for (int c = 0; c < t.first; ++c) *t.at(buffer, c) = t.p[c];
+        wrote = true;
+    }
+    if (t.last < t.width) {                               // block b with vector b and, phase or not, the one before
+        const int b = (int)(t.phase / sizeof(typename L::T) + t.last) / kVec, me = (int)threadIdx.x;
+        if (me == b % L::kThreads || (t.phase && b > 0 && me == (b - 1) % L::kThreads)) {
+            for (int c = t.last; c < t.width; ++c) *t.at(buffer, c) = t.p[c];
+            wrote = true;
         }
     }
-    cp_async_commit();
+    if (wrote) fence_async_proxy();                       // a bulk copy may write there later
 }
 
-// n >= 1 columns of a vector to p.
-template <typename T>
-__device__ __forceinline__ void store_vec(T *p, const uint4 &u, int n, bool vec) {
-    if (vec && n >= Tile<T>::kVec) {
-        stg_stream(p, u);
+// Bytes t .. t + 15 (t < 16, a multiple of 2) of a and b, one after the other.
+__device__ __forceinline__ uint4 bytes_at(const uint4 &a, const uint4 &b, uint32_t t) {
+    uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    if (t & 8u) {
+#pragma unroll
+        for (int i = 0; i < 6; ++i) w[i] = w[i + 2];
+    }
+    if (t & 4u) {
+#pragma unroll
+        for (int i = 0; i < 5; ++i) w[i] = w[i + 1];
+    }
+    const uint32_t bits = (t & 3u) * 8u;
+    return make_uint4(__funnelshift_r(w[0], w[1], bits), __funnelshift_r(w[1], w[2], bits),
+                      __funnelshift_r(w[2], w[3], bits), __funnelshift_r(w[3], w[4], bits));
+}
+
+// Vector o of a staged tile.
+template <bool kAligned, typename T>
+__device__ __forceinline__ uint4 staged_vec(const T *buffer, uint32_t phase, int o) {
+    const uint4 *b = reinterpret_cast<const uint4 *>(buffer) + o;
+    return kAligned ? b[0] : bytes_at(b[0], b[1], phase);
+}
+
+// Stores a warp's 32 neighbouring vectors (this lane's n columns, n <= 0: none) at p.
+// Where p is off a 16-byte boundary (the whole tile's is, by the same phase), each
+// lane stores the aligned block that begins in the vector before its own; the ends of
+// the 32 vectors, and of the tile, go column by column. Called by whole warps.
+template <bool kAligned, typename T>
+__device__ __forceinline__ void store_vec(T *p, const uint4 &u, int n, uint32_t phase) {
+    constexpr int kVec = Elem<T>::kVec;
+    const T *e = reinterpret_cast<const T *>(&u);
+    if (kAligned || phase == 0) {
+        if (n >= kVec) {
+            stg_stream(p, u);
+        } else {
+#pragma unroll
+            for (int i = 0; i < kVec; ++i)
+                if (i < n) p[i] = e[i];
+        }
         return;
     }
-    const T *e = reinterpret_cast<const T *>(&u);
+    uint4 before;
+    before.x = __shfl_up_sync(0xffffffffu, u.x, 1);
+    before.y = __shfl_up_sync(0xffffffffu, u.y, 1);
+    before.z = __shfl_up_sync(0xffffffffu, u.z, 1);
+    before.w = __shfl_up_sync(0xffffffffu, u.w, 1);
+    const int lane = threadIdx.x & 31, split = (int)((16u - phase) / sizeof(T));   // columns of the block that begins here
+    const bool whole = n >= kVec, block = whole && lane > 0;
+    if (block) stg_stream(reinterpret_cast<char *>(p) - phase, bytes_at(before, u, 16u - phase));
+    // the next vector's block is not stored where it is not whole or in another warp
+    const int from = block ? split : 0, to = lane == 31 || n - kVec < kVec ? n : split;
+    if (from < to) {
 #pragma unroll
-    for (int i = 0; i < Tile<T>::kVec; ++i)
-        if (i < n) p[i] = e[i];
+        for (int i = 0; i < kVec; ++i)
+            if (i >= from && i < to) p[i] = e[i];
+    }
 }
 
 struct RuleKernelArgs {
@@ -272,27 +317,29 @@ constexpr int kListed = 512, kSegment = 64, kRowIdsLeast = 2048, kRowIdsMost = 3
 // the tile's largest, so that the order they are found in does not matter.
 constexpr float kFixed = 281474976710656.f;   // 2^48
 
-template <typename T>
+template <class L>
 struct RuleSmem {
-    T stage[2][Tile<T>::kWidth];
+    using T = typename L::T;
+    T stage[2][L::kWidth + L::kVec];                      // a tile, and its phase
     uint4 keep_words[sizeof(T) == 2 ? 256 : 1];
     uint64_t full[2];
-    unsigned long long listed_sum[2][Tile<T>::kWarps];
-    uint32_t touched[Tile<T>::kWords];
-    float red_top[2][Tile<T>::kWarps], red_all[2][Tile<T>::kWarps], red_s[2][Tile<T>::kWarps], target_z[2];
+    unsigned long long listed_sum[2][L::kWarps];
+    uint32_t touched[L::kWords];
+    float red_top[2][L::kWarps], red_all[2][L::kWarps], red_s[2][L::kWarps], target_z[2];
     uint32_t n_listed[2];
     uint32_t segment[kSegment + 1];                       // where a slice's ids begin in row_ids; counters before that
     uint16_t listed[kListed];
     // counts [kWidth], with a bias list entries [kWidth], then the row's ids follow
 };
 
-template <typename T, int kOp>
-__global__ void __launch_bounds__(Tile<T>::kThreads, Tile<T>::kCtas) rules_kernel(const __grid_constant__ RuleKernelArgs a) {
+template <typename T, int kOp, int kN>
+__global__ void __launch_bounds__(Tile<T, kN>::kThreads, Tile<T, kN>::kCtas) rules_kernel(const __grid_constant__ RuleKernelArgs a) {
     extern __shared__ __align__(16) uint8_t smem_raw[];
-    constexpr int kThreads = Tile<T>::kThreads, kVec = Tile<T>::kVec, kVecs = Tile<T>::kVecs, kSlice = Tile<T>::kWidth,
-                  kWords = Tile<T>::kWords, kWarps = Tile<T>::kWarps;
-    RuleSmem<T> &sm = *reinterpret_cast<RuleSmem<T> *>(smem_raw);
-    uint32_t *const counts = reinterpret_cast<uint32_t *>(smem_raw + sizeof(RuleSmem<T>)), *const entries = counts + kSlice;
+    using L = Tile<T, kN>;
+    constexpr int kThreads = L::kThreads, kVec = L::kVec, kVecs = L::kVecs, kSlice = L::kWidth,
+                  kWords = L::kWords, kWarps = L::kWarps;
+    RuleSmem<L> &sm = *reinterpret_cast<RuleSmem<L> *>(smem_raw);
+    uint32_t *const counts = reinterpret_cast<uint32_t *>(smem_raw + sizeof(RuleSmem<L>)), *const entries = counts + kSlice;
     // column of the slice, bit 15: prompt
     uint16_t *const row_ids = reinterpret_cast<uint16_t *>(counts + (a.q.bias_spans ? 2 : a.q.spans ? 1 : 0) * kSlice);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -332,34 +379,33 @@ __global__ void __launch_bounds__(Tile<T>::kThreads, Tile<T>::kCtas) rules_kerne
     int seg0 = 0;                                        // ... was this slice
 
     // brings a tile of a row's logits (dy for the gradient of the rules)
+    auto source = [&](const RowRules &w, int sl) {
+        const int s0 = sl * kSlice;
+        return TileSource<T>((kOp == kProcBwd ? static_cast<const T *>(a.dy) + w.out_off
+                                              : static_cast<const T *>(a.x) + w.x_off) + s0, min(kSlice, a.V - s0));
+    };
     auto stage = [&](int buf, const RowRules &w, int sl) {
-        const int s0 = sl * kSlice, width = min(kSlice, a.V - s0);
-        const T *p = (kOp == kProcBwd ? static_cast<const T *>(a.dy) + w.out_off : static_cast<const T *>(a.x) + w.x_off) + s0;
-        const bool aligned = ((uintptr_t)p & 15u) == 0 && width >= kVec;
-        bulk = (bulk & ~(1u << buf)) | ((uint32_t)aligned << buf);
-        if (aligned) {
-            if (tid == 0) {
-                const uint32_t bytes = (uint32_t)(width / kVec) * 16u;
-                mbar_arrive_expect_tx(&sm.full[buf], bytes);
-                bulk_g2s(sm.stage[buf], p, bytes, &sm.full[buf], policy);
-            }
-        } else {
-            stage_unaligned(sm.stage[buf], p, width);
+        const TileSource<T> t = source(w, sl);
+        bulk = (bulk & ~(1u << buf)) | ((uint32_t)t.bulk() << buf);
+        if (t.bulk() && tid == 0) {
+            const uint32_t bytes = (uint32_t)(t.last - t.first) * (uint32_t)sizeof(T);
+            mbar_arrive_expect_tx(&sm.full[buf], bytes);
+            bulk_g2s(t.at(sm.stage[buf], t.first), t.p + t.first, bytes, &sm.full[buf], policy);
         }
-        stage_tail(sm.stage[buf], p, width);
+        stage_edges<L>(t, sm.stage[buf]);
     };
     // this thread's mask bits of a tile, vector k in byte k % 4 of word k / 4
     struct Allow { uint32_t b[(kVecs + 3) / 4]; };
     auto mask_bits = [&](const RowRules &w, int sl) {
         Allow m;
 #pragma unroll
-        for (int k = 0; k < (kVecs + 3) / 4; ++k) m.b[k] = w.mask ? 0u : 0x01010101u * Tile<T>::kAll;
+        for (int k = 0; k < (kVecs + 3) / 4; ++k) m.b[k] = w.mask ? 0u : 0x01010101u * L::kAll;
         if (w.mask) {
             const int o = (sl * kSlice + tid * kVec) >> 3, n = (a.V + 7) >> 3, sh = kVec == 8 ? 0 : (tid & 1) * 4;
 #pragma unroll
             for (int k = 0; k < kVecs; ++k) {
                 const int at = o + k * (kThreads * kVec / 8);
-                if (at < n) m.b[k / 4] |= ((uint32_t)__ldg(w.mask + at) >> sh & Tile<T>::kAll) << (8 * (k % 4));
+                if (at < n) m.b[k / 4] |= ((uint32_t)__ldg(w.mask + at) >> sh & L::kAll) << (8 * (k % 4));
             }
         }
         return m;
@@ -373,7 +419,9 @@ __global__ void __launch_bounds__(Tile<T>::kThreads, Tile<T>::kCtas) rules_kerne
         const int s0 = slice * kSlice;
         const int width = min(kSlice, a.V - s0);          // columns of this slice
         const T *xrow = static_cast<const T *>(a.x) + w.x_off + s0;
-        const T *const st = sm.stage[buf];
+        const T *const buffer = sm.stage[buf];
+        const uint32_t phase = source(w, slice).phase;
+        const T *const st = buffer + phase / sizeof(T);   // column 0
         if (!w.ok && slice == 0 && tid == 0 && a.err) atomicOr(a.err, VP_ERRBIT_RULES_);
         // the target's column in this slice, if it lies here
         const int target = kOp >= kLogpFwd && w.target >= s0 && w.target - s0 < width ? w.target - s0 : -1;
@@ -383,10 +431,6 @@ __global__ void __launch_bounds__(Tile<T>::kThreads, Tile<T>::kCtas) rules_kerne
         const int next_slice = row_ends ? 0 : slice + 1;
         Allow next_allow = allow;
         const bool bulked = bulk >> buf & 1u;
-        if (!bulked) {
-            cp_async_wait();
-            fence_async_proxy();                          // a bulk copy may write there next
-        }
         if (tile + 1 < end) {
             if (row_ends) next_w = row_rules<kOp>(a, r + 1);
             stage(buf ^ 1, row_ends ? next_w : w, next_slice);
@@ -554,20 +598,24 @@ __global__ void __launch_bounds__(Tile<T>::kThreads, Tile<T>::kCtas) rules_kerne
                 if (l == target) sm.target_z[buf] = v * w.inv_t;
             });
             uint4 u[kVecs];
+            auto read = [&](auto aligned) {
 #pragma unroll
-            for (int k = 0; k < kVecs; ++k) {
-                const int o = k * kThreads + tid, n = width - o * kVec;
-                const uint32_t off = minus_inf_bits<T>();
-                u[k] = make_uint4(off, off, off, off);
-                if (n > 0) {
-                    u[k] = reinterpret_cast<const uint4 *>(st)[o];
-                    uint32_t on = allow.b[k / 4] >> (8 * (k % 4)) & Tile<T>::kAll;
-                    if (listed) on &= kVec == 8 ? ~(uint32_t)touched8[o] : ~((uint32_t)touched8[o >> 1] >> ((tid & 1) * 4));
-                    if (n < kVec) on &= (1u << n) - 1u;
-                    if (on != Tile<T>::kAll) u[k] = keep_vec<T>(u[k], on, off, sm.keep_words);
+                for (int k = 0; k < kVecs; ++k) {
+                    const int o = k * kThreads + tid, n = width - o * kVec;
+                    const uint32_t off = minus_inf_bits<T>();
+                    u[k] = make_uint4(off, off, off, off);
+                    if (n > 0) {
+                        u[k] = staged_vec<decltype(aligned)::value>(buffer, phase, o);
+                        uint32_t on = allow.b[k / 4] >> (8 * (k % 4)) & L::kAll;
+                        if (listed) on &= kVec == 8 ? ~(uint32_t)touched8[o] : ~((uint32_t)touched8[o >> 1] >> ((tid & 1) * 4));
+                        if (n < kVec) on &= (1u << n) - 1u;
+                        if (on != L::kAll) u[k] = keep_vec<T>(u[k], on, off, sm.keep_words);
+                    }
+                    top = fmaxf(top, vec_max<T>(u[k]));
                 }
-                top = fmaxf(top, vec_max<T>(u[k]));
-            }
+            };
+            if (phase == 0) read(std::true_type());
+            else read(std::false_type());
             float2 e = make_float2(s, 0.f);
 #pragma unroll
             for (int k = 0; k < kVecs; ++k) {
@@ -629,38 +677,44 @@ __global__ void __launch_bounds__(Tile<T>::kThreads, Tile<T>::kCtas) rules_kerne
             }
         } else {
             T *orow = static_cast<T *>(a.out) + w.out_off + s0;
-            const bool ovec = ((uintptr_t)orow & 15u) == 0;
+            const uint32_t ophase = (uint32_t)(uintptr_t)orow & 15u;
             const bool constant = w.nan_row || w.ignored;
+            auto pass = [&](auto aligned) {
+                constexpr bool kAligned = decltype(aligned)::value;
 #pragma unroll
-            for (int k = 0; k < kVecs; ++k) {
-                const int o = k * kThreads + tid, n = width - o * kVec;
-                if (n > 0) {
-                    uint4 u = reinterpret_cast<const uint4 *>(st)[o];
-                    float v[kVec];
-                    Elem<T>::unpack(u, v);
+                for (int k = 0; k < kVecs; ++k) {
+                    const int o = k * kThreads + tid, n = width - o * kVec;
+                    uint4 u = make_uint4(0u, 0u, 0u, 0u);
+                    if (n > 0) {
+                        u = staged_vec<kAligned>(buffer, phase, o);
+                        float v[kVec];
+                        Elem<T>::unpack(u, v);
 #pragma unroll
-                    for (int i = 0; i < kVec; i += 2) {
-                        float2 d = make_float2(v[i], v[i + 1]);
-                        if constexpr (kOp == kLogpBwd) {
-                            d = __fadd2_rn(__ffma2_rn(d, f2(w.inv_t), f2(-w.m)), f2(-w.log_s));
-                            if (Scaled<T>::kUnit != 1.f) d = __fmul2_rn(d, f2(Scaled<T>::kUnit));
-                            d = scaled_exp2<T>(d);
+                        for (int i = 0; i < kVec; i += 2) {
+                            float2 d = make_float2(v[i], v[i + 1]);
+                            if constexpr (kOp == kLogpBwd) {
+                                d = __fadd2_rn(__ffma2_rn(d, f2(w.inv_t), f2(-w.m)), f2(-w.log_s));
+                                if (Scaled<T>::kUnit != 1.f) d = __fmul2_rn(d, f2(Scaled<T>::kUnit));
+                                d = scaled_exp2<T>(d);
+                            }
+                            d = __fmul2_rn(d, f2(w.scale));
+                            v[i] = d.x;
+                            v[i + 1] = d.y;
                         }
-                        d = __fmul2_rn(d, f2(w.scale));
-                        v[i] = d.x;
-                        v[i + 1] = d.y;
-                    }
-                    if (constant) {
+                        if (constant) {
 #pragma unroll
-                        for (int i = 0; i < kVec; ++i) v[i] = w.nan_row ? qnan() : 0.f;
+                            for (int i = 0; i < kVec; ++i) v[i] = w.nan_row ? qnan() : 0.f;
+                        }
+                        u = Elem<T>::pack(v);
+                        const uint32_t on = allow.b[k / 4] >> (8 * (k % 4)) & L::kAll;
+                        if (on != L::kAll && !constant)
+                            u = keep_vec<T>(u, on, kOp == kProcFwd ? minus_inf_bits<T>() : 0u, sm.keep_words);
                     }
-                    u = Elem<T>::pack(v);
-                    const uint32_t on = allow.b[k / 4] >> (8 * (k % 4)) & Tile<T>::kAll;
-                    if (on != Tile<T>::kAll && !constant)
-                        u = keep_vec<T>(u, on, kOp == kProcFwd ? minus_inf_bits<T>() : 0u, sm.keep_words);
-                    store_vec(orow + o * kVec, u, n, ovec);
+                    store_vec<kAligned>(orow + o * kVec, u, n, ophase);
                 }
-            }
+            };
+            if (phase == 0 && ophase == 0) pass(std::true_type());
+            else pass(std::false_type());
             __syncthreads();                              // the vector pass's stores come before the walk's
             if (listed) {
                 walk([&](int l) {
@@ -740,22 +794,24 @@ rules_join_kernel(const PartialRec *__restrict__ parts, int K, int64_t N, float 
     logp[r] = ignored ? 0.f : lost || (rf & (kRowNanInf | kRowEmpty)) ? qnan() : (float)(((double)zt - (double)M) - log_s);
 }
 
-int64_t rule_slices(int64_t V) { return (V + Tile<float>::kWidth - 1) / Tile<float>::kWidth; }
+// slices (records) of the ruled logprobs' forward
+int64_t rule_slices(int64_t V) { return (V + Tile<float, kRuleThreads>::kWidth - 1) / Tile<float, kRuleThreads>::kWidth; }
 
-template <typename T, int kOp>
+template <typename T, int kOp, int kN = kRuleThreads>
 static cudaError_t launch_rules_t(RuleKernelArgs k, cudaStream_t stream) {
+    using L = Tile<T, kN>;
     // resident CTAs per SM for each number of tables and capacity of row_ids, asked once per device
     static std::atomic<int> resident[64][3][5];
-    k.n_slices = (k.V + Tile<T>::kWidth - 1) / Tile<T>::kWidth;
+    k.n_slices = (k.V + L::kWidth - 1) / L::kWidth;
     const int n_tables = k.q.bias_spans ? 2 : k.q.spans ? 1 : 0;
     // Room for twice the average row's ids: long histories take shared memory from other CTAs, but going
     // through 16384 ids for every slice takes longer than the slice.
     int step = 0;
     if (k.q.spans)
-        while (step < 4 && (int64_t)(kRowIdsLeast << step) * k.N < 2 * k.q.n_ids) ++step;
+        while (step < 4 && (int64_t)(kRowIdsLeast << step) * k.N < k.q.n_ids) ++step;
     static_assert(kRowIdsLeast << 4 == kRowIdsMost, "five capacities");
     k.row_ids = k.q.spans ? kRowIdsLeast << step : 0;
-    auto bytes = [](int tables, int ids) { return (int)sizeof(RuleSmem<T>) + tables * Tile<T>::kWidth * 4 + ids * 2; };
+    auto bytes = [](int tables, int ids) { return (int)sizeof(RuleSmem<L>) + tables * L::kWidth * 4 + ids * 2; };
     const int smem = bytes(n_tables, k.row_ids);
     int dev = 0, sms = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -763,16 +819,16 @@ static cudaError_t launch_rules_t(RuleKernelArgs k, cudaStream_t stream) {
     std::atomic<int> &known = resident[dev & 63][n_tables][step];
     int per_sm = known.load(std::memory_order_relaxed);
     if (!per_sm) {
-        e = cudaFuncSetAttribute(rules_kernel<T, kOp>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes(2, kRowIdsMost));
+        e = cudaFuncSetAttribute(rules_kernel<T, kOp, kN>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes(2, kRowIdsMost));
         if (e == cudaSuccess)
-            e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, rules_kernel<T, kOp>, Tile<T>::kThreads, smem);
+            e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, rules_kernel<T, kOp, kN>, L::kThreads, smem);
         if (e != cudaSuccess) return e;
         per_sm = per_sm < 1 ? 1 : per_sm;
         known.store(per_sm, std::memory_order_relaxed);
     }
     if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
     const int64_t total = k.N * k.n_slices, most = (int64_t)sms * per_sm;
-    return launch_pdl(rules_kernel<T, kOp>, dim3((unsigned)(total < most ? total : most)), dim3(Tile<T>::kThreads),
+    return launch_pdl(rules_kernel<T, kOp, kN>, dim3((unsigned)(total < most ? total : most)), dim3(L::kThreads),
                       (size_t)smem, stream, k);
 }
 
@@ -783,6 +839,9 @@ static cudaError_t launch_rules(const RuleArgs &a) {
                      static_cast<PartialRec *>(a.parts), a.err, 0};
     // no rule that reads the ids: the spans are not looked at
     if (!k.q.repetition && !k.q.frequency && !k.q.presence) k.q.spans = nullptr;
+    if (kOp == kProcFwd && k.q.spans && k.q.n_ids > Tile<float, kRuleThreads>::kWidth * k.N)
+        return a.bf16 ? launch_rules_t<__nv_bfloat16, kProcFwd, kRuleThreadsLong>(k, a.stream)
+                      : launch_rules_t<float, kProcFwd, kRuleThreadsLong>(k, a.stream);
     return a.bf16 ? launch_rules_t<__nv_bfloat16, kOp>(k, a.stream) : launch_rules_t<float, kOp>(k, a.stream);
 }
 
@@ -795,9 +854,8 @@ cudaError_t launch_processed_logprobs_bwd(const RuleArgs &a) { return launch_rul
 cudaError_t launch_processed_logprobs_fwd(const RuleArgs &a, float *logp, void *stats) {
     cudaError_t e = launch_rules<kLogpFwd>(a);
     if (e != cudaSuccess) return e;
-    const int width = a.bf16 ? Tile<__nv_bfloat16>::kWidth : Tile<float>::kWidth;
     return launch_pdl(rules_join_kernel, dim3((unsigned)((a.N + kJoinWarps - 1) / kJoinWarps)), dim3(kJoinWarps * 32), 0,
-                      a.stream, static_cast<const PartialRec *>(a.parts), (int)((a.V + width - 1) / width), a.N, logp,
+                      a.stream, static_cast<const PartialRec *>(a.parts), (int)rule_slices(a.V), a.N, logp,
                       static_cast<RowStat *>(stats), a.err);
 }
 
