@@ -407,6 +407,40 @@ def test_streams_and_graphs():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("n_ids", [20000, 100000, 3000000, 9000000])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_many_rows_of_few_ids(dtype, n_ids):
+    """More tiles than run at once, rows with and without a history in turn, ids far apart in a long list."""
+    N, V = 1500, 8200
+    g = torch.Generator(device="cuda").manual_seed(1)
+    x = torch.randn(N, V, generator=g, device="cuda").to(dtype)
+    ids = torch.full((n_ids,), -1, dtype=torch.int64, device="cuda")
+    at = torch.arange(0, N, 7, device="cuda")
+    first = at * (n_ids // N)
+    for k, v in enumerate((5, 5, 8199)):
+        ids[first + k] = v
+    spans = torch.zeros(N, 3, dtype=torch.int64, device="cuda")
+    spans[at, 0], spans[at, 2] = first, 3
+    two = torch.full((N,), 2.0, device="cuda")
+    rules = vp.logits_rules(ids=ids, spans=spans, frequency=two, temperature=two)
+    z = x.float().clone()
+    z[at, 5] -= 4
+    z[at, 8199] -= 2
+    z /= 2                                                        # exact: a power of two
+    assert torch.equal(vp.vp_logits_process_fwd(x, rules), z.to(dtype))
+    targets = torch.full((N,), 5, dtype=torch.int64, device="cuda")
+    logp, stats = vp.vp_processed_logprobs_fwd(x, rules, targets)
+    ref = torch.log_softmax(z.double(), 1)
+    assert (logp.double() - ref[:, 5]).abs().max() < U * (16 * 8 + 62 + 16)
+    one = torch.ones(N, device="cuda")
+    dx = vp.vp_processed_logprobs_bwd(x, rules, targets, stats, one).double()
+    g64 = -ref.exp()
+    g64[:, 5] = -torch.expm1(ref[:, 5])
+    g64 /= 2
+    assert ((dx - g64).abs() - (half_step(dtype) + U * 220) * g64.abs() - 2.0 ** -126).max() <= 0
+
+
+@pytest.mark.gpu
 @pytest.mark.slow
 def test_offsets_past_32_bits():
     """Rows that begin past 2^31 elements, and a history list whose last ids do."""

@@ -65,6 +65,21 @@ __device__ __forceinline__ int64_t quant_place(int64_t groups, int &chunk0) {
     return r;
 }
 
+// The largest |x| of 8 columns as the bits of an fp32 value; NaN wins.
+__device__ __forceinline__ uint32_t octet_amax(const uint4 (&u)[1]) {
+    const __nv_bfloat162 *p = reinterpret_cast<const __nv_bfloat162 *>(u);
+    const __nv_bfloat162 m = __hmax2_nan(__hmax2_nan(__habs2(p[0]), __habs2(p[1])), __hmax2_nan(__habs2(p[2]), __habs2(p[3])));
+    const uint32_t w = *reinterpret_cast<const uint32_t *>(&m);
+    return max(w << 16, w & 0xffff0000u);                  // bit patterns without sign order like the values, NaN highest
+}
+__device__ __forceinline__ uint32_t octet_amax(const uint4 (&u)[2]) {
+    const uint32_t *w = reinterpret_cast<const uint32_t *>(u);
+    uint32_t m = 0u;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = max(m, w[i] & 0x7fffffffu);
+    return m;
+}
+
 // A lane takes 8 consecutive columns of a chunk: a block is four lanes, its
 // maximum two shuffles away. The scale comes from the maximum's exponent bits (E:
 // the scale byte is E - 2, at least 0), so x / scale is exact. Rows N .. the next
@@ -104,21 +119,24 @@ mxfp4_quantize_kernel(const T *__restrict__ x, Rows rows, int64_t N, int64_t n_r
         const int chunk = chunk0 + k, c = chunk * kQChunk + lane * 8;
         if (chunk * kQChunk >= D) break;                   // uniform in the warp
         const bool valid = r < N && c < D;
-        float v[8];
-#pragma unroll
-        for (int i = 0; i < kVecs; ++i) Elem<T>::unpack(u[k][i], v + i * Elem<T>::kVec);
-        uint32_t amax = 0;                                 // bit patterns of |x| order like the values, NaN highest
-#pragma unroll
-        for (int i = 0; i < 8; ++i) amax = max(amax, __float_as_uint(v[i]) & 0x7fffffffu);
+        uint32_t amax = octet_amax(u[k]);
         amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
         amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
         const uint32_t e = amax >> 23;
         const uint32_t byte = e == 255u ? 255u : e > 2u ? e - 2u : 0u;
         if (valid) {
-            const float inv = __uint_as_float((254u - min(byte, 253u)) << 23);   // 2^(127 - byte)
+            float v[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = byte == 255u ? 0.f : v[i] * inv;
-            *reinterpret_cast<uint32_t *>(codes + r * (D / 2) + (c >> 1)) = e2m1x8(v);
+            for (int i = 0; i < kVecs; ++i) Elem<T>::unpack(u[k][i], v + i * Elem<T>::kVec);
+            const float2 inv = f2(__uint_as_float((254u - min(byte, 253u)) << 23));   // 2^(127 - byte)
+#pragma unroll
+            for (int i = 0; i < 8; i += 2) {
+                const float2 p = __fmul2_rn(make_float2(v[i], v[i + 1]), inv);
+                v[i] = p.x;
+                v[i + 1] = p.y;
+            }
+            const uint32_t code = e2m1x8(v);
+            *reinterpret_cast<uint32_t *>(codes + r * (D / 2) + (c >> 1)) = byte == 255u ? 0u : code;
         }
         uint32_t word = valid ? byte << (8 * ((lane >> 2) & 3)) : 0u;
         word |= __shfl_xor_sync(0xffffffffu, word, 4);

@@ -45,17 +45,17 @@ constexpr uint32_t kPromptBit = 0x80000000u;
 
 enum RuleOp { kProcFwd = 0, kProcBwd = 1, kLogpFwd = 2, kLogpBwd = 3 };
 
-// A tile's threads and size. Measured on GB300 at 4096 x 75968 bf16 with 1000 ids a
-// row (us, forward / backward of the ruled logprobs): 4 vectors a thread, five CTAs
-// an SM 336 / 268; 8 vectors, three CTAs 364 / 302; 256 threads with 4 vectors,
-// three CTAs 382 / 325. fp32 (2048 rows): 8 vectors 300 / 247, 4 vectors 343 / 320.
+// A tile's threads and size. Measured on GB300 at 8192 x 75968 bf16 with 1000 ids a
+// row (us, forward / backward of the ruled logprobs): 4096 columns and five CTAs an
+// SM 646 / 632, six 665 / 632, seven 697 / 611; 8192 columns and four CTAs 886 / 732.
+// fp32, 1024 rows: four CTAs 147 / 136, three 161 / 149.
 template <typename E, int kN> struct Tile {
     using T = E;
     static constexpr int kThreads = kN, kWarps = kThreads / 32;
     static constexpr int kVec = Elem<T>::kVec;                // columns of a 16-byte vector
     static constexpr int kWidth = 4096;                       // columns of a tile
     static constexpr int kVecs = kWidth / kVec / kThreads;    // vectors of a thread
-    static constexpr int kCtas = kThreads > 128 || sizeof(T) == 4 ? 3 : 5;   // of an SM
+    static constexpr int kCtas = kThreads > 128 ? 3 : sizeof(T) == 4 ? 4 : 5;   // of an SM, if their shared memory fits
     static constexpr int kWords = kWidth / 32;                // words of the bitmap
     static constexpr uint32_t kAll = kVec == 8 ? 0xffu : 0xfu;
 };
@@ -179,6 +179,7 @@ struct RuleKernelArgs {
     PartialRec *parts;
     int32_t *err;
     int row_ids;              // capacity of the list of a row's ids
+    bool narrow;              // occurrences counted in 15 bits: fewer ids than that in all
 };
 
 // The rules of one row, read and checked when a CTA comes to it, and what else
@@ -282,14 +283,14 @@ __device__ __forceinline__ float2 scaled_exp2(float2 t) {
 }
 
 // Columns of a vector whose bit in `on` is clear become `off` (the bits of a
-// value, twice for bf16). bf16 takes the vector's keep words from a table of all
-// bytes in shared memory.
+// value, twice for bf16). bf16 takes the vector's keep words, two for each four bits,
+// from a table in shared memory.
 template <typename T>
-__device__ __forceinline__ uint4 keep_vec(uint4 u, uint32_t on, uint32_t off, const uint4 *keep_words) {
+__device__ __forceinline__ uint4 keep_vec(uint4 u, uint32_t on, uint32_t off, const uint2 *keep_words) {
     if (sizeof(T) == 2) {
-        const uint4 k = keep_words[on];
-        return make_uint4((u.x & k.x) | (off & ~k.x), (u.y & k.y) | (off & ~k.y), (u.z & k.z) | (off & ~k.z),
-                          (u.w & k.w) | (off & ~k.w));
+        const uint2 k = keep_words[on & 15u], l = keep_words[on >> 4];
+        return make_uint4((u.x & k.x) | (off & ~k.x), (u.y & k.y) | (off & ~k.y), (u.z & l.x) | (off & ~l.x),
+                          (u.w & l.y) | (off & ~l.y));
     }
     return make_uint4(on & 1u ? u.x : off, on & 2u ? u.y : off, on & 4u ? u.z : off, on & 8u ? u.w : off);
 }
@@ -317,11 +318,25 @@ constexpr int kListed = 512, kSegment = 64, kRowIdsLeast = 2048, kRowIdsMost = 3
 // the tile's largest, so that the order they are found in does not matter.
 constexpr float kFixed = 281474976710656.f;   // 2^48
 
+__device__ __forceinline__ float redux_max(float v) {      // NaN is passed over
+    float m;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(v));
+    return m;
+}
+
+// Sum over the warp of integers below 2^58 - 2^53.
+__device__ __forceinline__ unsigned long long redux_sum(unsigned long long v) {
+    const uint32_t lo = __reduce_add_sync(0xffffffffu, (uint32_t)v & 0x7ffffffu);
+    const uint32_t hi = __reduce_add_sync(0xffffffffu, (uint32_t)(v >> 27));
+    return ((unsigned long long)hi << 27) + lo;
+}
+
 template <class L>
 struct RuleSmem {
     using T = typename L::T;
     T stage[2][L::kWidth + L::kVec];                      // a tile, and its phase
-    uint4 keep_words[sizeof(T) == 2 ? 256 : 1];
+    uint2 keep_words[16];
+    alignas(16) uint8_t allowed[2][L::kWidth / 8];        // the tile's mask bits
     uint64_t full[2];
     unsigned long long listed_sum[2][L::kWarps];
     uint32_t touched[L::kWords];
@@ -339,25 +354,20 @@ __global__ void __launch_bounds__(Tile<T, kN>::kThreads, Tile<T, kN>::kCtas) rul
     constexpr int kThreads = L::kThreads, kVec = L::kVec, kVecs = L::kVecs, kSlice = L::kWidth,
                   kWords = L::kWords, kWarps = L::kWarps;
     RuleSmem<L> &sm = *reinterpret_cast<RuleSmem<L> *>(smem_raw);
-    uint32_t *const counts = reinterpret_cast<uint32_t *>(smem_raw + sizeof(RuleSmem<L>)), *const entries = counts + kSlice;
+    uint32_t *const counts = reinterpret_cast<uint32_t *>(smem_raw + sizeof(RuleSmem<L>)), *const entries = counts + (a.q.spans ? a.narrow ? kSlice / 2 : kSlice : 0);
     // column of the slice, bit 15: prompt
-    uint16_t *const row_ids = reinterpret_cast<uint16_t *>(counts + (a.q.bias_spans ? 2 : a.q.spans ? 1 : 0) * kSlice);
+    uint16_t *const row_ids = reinterpret_cast<uint16_t *>(entries + (a.q.bias_spans ? kSlice : 0));
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint8_t *const touched8 = reinterpret_cast<const uint8_t *>(sm.touched);
     const bool tabled = a.q.spans != nullptr, biased = a.q.bias_spans != nullptr;
 
     // the tables are cleared once; a tile clears what it touched
     for (int i = tid; i < kWords; i += kThreads) sm.touched[i] = 0u;
-    for (int i = tid; i < (biased ? 2 : tabled ? 1 : 0) * (kSlice / 4); i += kThreads)
+    for (int i = tid; i < (int)(entries - counts + (biased ? kSlice : 0)) / 4; i += kThreads)
         reinterpret_cast<uint4 *>(counts)[i] = make_uint4(0u, 0u, 0u, 0u);
-    if (sizeof(T) == 2)
-        for (int b = tid; b < 256; b += kThreads) {
-            uint32_t k[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                k[i] = (b >> (2 * i) & 1 ? 0xffffu : 0u) | (b >> (2 * i + 1) & 1 ? 0xffff0000u : 0u);
-            sm.keep_words[b] = make_uint4(k[0], k[1], k[2], k[3]);
-        }
+    if (tid < 16)
+        sm.keep_words[tid] = make_uint2((tid & 1 ? 0xffffu : 0u) | (tid & 2 ? 0xffff0000u : 0u),
+                                        (tid & 4 ? 0xffffu : 0u) | (tid & 8 ? 0xffff0000u : 0u));
     if (tid < 2) sm.n_listed[tid] = 0u;
     if (tid == 0) {
         mbar_init(&sm.full[0], 1);
@@ -515,8 +525,14 @@ __global__ void __launch_bounds__(Tile<T, kN>::kThreads, Tile<T, kN>::kCtas) rul
                 if (kOp == kProcBwd) asm volatile("prefetch.global.L2 [%0];" ::"l"(xrow + c));
             };
             auto enter = [&](uint32_t c, bool prompt) {
-                if (prompt) atomicOr(&counts[c], kPromptBit);
-                else atomicAdd(&counts[c], 1u);
+                if (a.narrow) {
+                    const uint32_t sh = (c & 1) * 16;
+                    if (prompt) atomicOr(&counts[c >> 1], 0x8000u << sh);
+                    else atomicAdd(&counts[c >> 1], 1u << sh);
+                } else {
+                    if (prompt) atomicOr(&counts[c], kPromptBit);
+                    else atomicAdd(&counts[c], 1u);
+                }
                 mark(c);
             };
             if (tid == 0 && target >= 0) mark((uint32_t)target);
@@ -540,7 +556,22 @@ __global__ void __launch_bounds__(Tile<T, kN>::kThreads, Tile<T, kN>::kCtas) rul
             if (!mbar_wait(&sm.full[buf], parity >> buf & 1u)) arrived = false;
             parity ^= 1u << buf;
         }
-        if (listed) __syncthreads();                      // the tables, and what other threads copied
+        if (listed) {
+            if (w.mask) {                                 // this thread's mask bits, for the walk
+#pragma unroll
+                for (int k = 0; k < kVecs; ++k) {
+                    const uint32_t b = allow.b[k / 4] >> (8 * (k % 4)) & Tile<T, kN>::kAll;
+                    const int o = k * kThreads + tid;
+                    if (kVec == 8) {
+                        sm.allowed[buf][o] = (uint8_t)b;
+                    } else {                              // four bits each: a pair of lanes makes a byte
+                        const uint32_t both = b | __shfl_down_sync(0xffffffffu, b, 1) << 4;
+                        if (!(tid & 1)) sm.allowed[buf][o >> 1] = (uint8_t)both;
+                    }
+                }
+            }
+            __syncthreads();                              // the tables, and what other threads copied
+        }
         const uint32_t n_listed = listed ? sm.n_listed[buf] : 0u;
         // f(column) for each listed column, by some thread
         auto walk = [&](auto f) {
@@ -564,8 +595,14 @@ __global__ void __launch_bounds__(Tile<T, kN>::kThreads, Tile<T, kN>::kCtas) rul
         auto ruled = [&](int l, float x, float &f, bool last) {
             uint32_t c = 0u;
             if (tabled) {
-                c = counts[l];
-                if (last) counts[l] = 0u;
+                if (a.narrow) {
+                    uint16_t *const h = reinterpret_cast<uint16_t *>(counts) + l;
+                    c = (*h & 0x7fffu) | (uint32_t)(*h >> 15) << 31;
+                    if (last) *h = 0;
+                } else {
+                    c = counts[l];
+                    if (last) counts[l] = 0u;
+                }
             }
             const uint32_t n = c & ~kPromptBit;
             f = c == 0u ? 1.f : x > 0.f ? w.inv_rep : w.rep;
@@ -578,7 +615,7 @@ __global__ void __launch_bounds__(Tile<T, kN>::kThreads, Tile<T, kN>::kCtas) rul
             }
             return v;
         };
-        auto allowed = [&](int l) { return !w.mask || (__ldg(w.mask + ((s0 + l) >> 3)) >> (l & 7) & 1); };
+        auto allowed = [&](int l) { return !w.mask || (sm.allowed[buf][l >> 3] >> (l & 7) & 1); };
 
         if constexpr (kOp == kLogpFwd) {
             // Exponentials of u (v - top) / T, top the largest v before the temperature:
@@ -626,11 +663,11 @@ __global__ void __launch_bounds__(Tile<T, kN>::kThreads, Tile<T, kN>::kCtas) rul
                     e = __fadd2_rn(e, scaled_exp2<T>(__fmul2_rn(__fadd2_rn(make_float2(v[i], v[i + 1]), f2(-top)), f2(c1))));
             }
             s = e.x + e.y;
-            const float wtop = warp_max(top);
+            const float wtop = redux_max(top);
             s *= Scaled<T>::exp((top - wtop) * c1);
 #pragma unroll
             for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
-            if (listed) ltop = warp_max(ltop);
+            if (listed) ltop = redux_max(ltop);
             if (lane == 0) {
                 sm.red_top[buf][warp] = wtop;
                 sm.red_all[buf][warp] = fmaxf(wtop, ltop);
@@ -643,8 +680,7 @@ __global__ void __launch_bounds__(Tile<T, kN>::kThreads, Tile<T, kN>::kCtas) rul
             if (listed) {
                 unsigned long long sum = 0ull;
                 walk([&](int l) { sum += __float2ull_rn(Scaled<T>::exp((listed_value(l, true) - m) * c1) * kFixed); });
-#pragma unroll
-                for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+                sum = redux_sum(sum);                     // a lane's: at most 32 columns, each at most 2^48
                 if (lane == 0) sm.listed_sum[buf][warp] = sum;
                 if (n_listed > (uint32_t)kListed) __syncthreads();   // the walk reads every word of the bitmap
                 clear();
@@ -800,26 +836,30 @@ int64_t rule_slices(int64_t V) { return (V + Tile<float, kRuleThreads>::kWidth -
 template <typename T, int kOp, int kN = kRuleThreads>
 static cudaError_t launch_rules_t(RuleKernelArgs k, cudaStream_t stream) {
     using L = Tile<T, kN>;
-    // resident CTAs per SM for each number of tables and capacity of row_ids, asked once per device
-    static std::atomic<int> resident[64][3][5];
+    // resident CTAs per SM for each choice of tables and capacity of row_ids, asked once per device
+    static std::atomic<int> resident[64][6][5];
     k.n_slices = (k.V + L::kWidth - 1) / L::kWidth;
-    const int n_tables = k.q.bias_spans ? 2 : k.q.spans ? 1 : 0;
-    // Room for twice the average row's ids: long histories take shared memory from other CTAs, but going
+    // fewer than 2^15 ids in all (a training batch's sequences): no id occurs more often
+    k.narrow = k.q.n_ids < 0x8000;
+    const int tables = (k.q.spans ? k.narrow ? 1 : 2 : 0) + (k.q.bias_spans ? 3 : 0);
+    // Room for the average row's ids: long histories take shared memory from other CTAs, but going
     // through 16384 ids for every slice takes longer than the slice.
     int step = 0;
     if (k.q.spans)
         while (step < 4 && (int64_t)(kRowIdsLeast << step) * k.N < k.q.n_ids) ++step;
     static_assert(kRowIdsLeast << 4 == kRowIdsMost, "five capacities");
     k.row_ids = k.q.spans ? kRowIdsLeast << step : 0;
-    auto bytes = [](int tables, int ids) { return (int)sizeof(RuleSmem<L>) + tables * L::kWidth * 4 + ids * 2; };
-    const int smem = bytes(n_tables, k.row_ids);
+    auto bytes = [](int tables, int ids) {
+        return (int)sizeof(RuleSmem<L>) + (tables % 3) * L::kWidth * 2 + (tables / 3) * L::kWidth * 4 + ids * 2;
+    };
+    const int smem = bytes(tables, k.row_ids);
     int dev = 0, sms = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
-    std::atomic<int> &known = resident[dev & 63][n_tables][step];
+    std::atomic<int> &known = resident[dev & 63][tables][step];
     int per_sm = known.load(std::memory_order_relaxed);
     if (!per_sm) {
-        e = cudaFuncSetAttribute(rules_kernel<T, kOp, kN>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes(2, kRowIdsMost));
+        e = cudaFuncSetAttribute(rules_kernel<T, kOp, kN>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes(5, kRowIdsMost));
         if (e == cudaSuccess)
             e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, rules_kernel<T, kOp, kN>, L::kThreads, smem);
         if (e != cudaSuccess) return e;
@@ -836,7 +876,7 @@ template <int kOp>
 static cudaError_t launch_rules(const RuleArgs &a) {
     RuleKernelArgs k{a.x, a.dy, a.out, a.N, 0, a.vocab_start, (int)a.V, Rows{a.R, a.s_o, a.s_i},
                      Rows{a.R, a.out_s_o, a.out_s_i}, a.rules, a.targets, static_cast<const RowStat *>(a.stats), a.g,
-                     static_cast<PartialRec *>(a.parts), a.err, 0};
+                     static_cast<PartialRec *>(a.parts), a.err, 0, false};
     // no rule that reads the ids: the spans are not looked at
     if (!k.q.repetition && !k.q.frequency && !k.q.presence) k.q.spans = nullptr;
     if (kOp == kProcFwd && k.q.spans && k.q.n_ids > Tile<float, kRuleThreads>::kWidth * k.N)
