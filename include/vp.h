@@ -665,8 +665,9 @@ typedef struct vp_logits_rules {
  * be x itself (same pointer and strides); it must not overlap x otherwise.
  * Argument errors as the forward calls above; a rules pointer NULL where
  * another needs it (spans without ids, bias spans without entries): VP_ERR_NULL;
- * n_masks < 1, a mask row shorter than V bits (mask_stride < ceil(V / 32) with
- * more than one row), or fewer mask rows than N without mask_rows: VP_ERR_SHAPE. */
+ * vocab_start < 0: VP_ERR_ARG (negative ids are padding); n_masks < 1, a mask
+ * row shorter than V bits (mask_stride < ceil(V / 32) with more than one row), or
+ * fewer mask rows than N without mask_rows: VP_ERR_SHAPE. */
 VP_API vp_status vp_logits_process_fwd(const void *x, int dtype, int64_t N, int64_t V, int64_t R, int64_t s_o,
                                        int64_t s_i, int64_t vocab_start, const vp_logits_rules *rules, void *y,
                                        int64_t y_s_o, int64_t y_s_i, int32_t *err_word, vp_stream stream);
@@ -675,7 +676,7 @@ VP_API vp_status vp_logits_process_fwd(const void *x, int dtype, int64_t N, int6
  * where x_j > 0, rep elsewhere) for an id of the history and 1 for others; 0
  * where the mask does not allow j, whatever dy holds. The penalties' and
  * biases' own values get no gradient. dy and dx contiguous [N, V], dx may be
- * dy. x is read only at ids of the history. */
+ * dy but must not overlap x. x is read only at ids of the row's lists. */
 VP_API vp_status vp_logits_process_bwd(const void *x, int dtype, int64_t N, int64_t V, int64_t R, int64_t s_o,
                                        int64_t s_i, int64_t vocab_start, const vp_logits_rules *rules,
                                        const void *dy, void *dx, int32_t *err_word, vp_stream stream);
@@ -694,7 +695,7 @@ VP_API vp_status vp_processed_logprobs_fwd(const void *x, int dtype, int64_t N, 
 /* dx_j = grad_out f_j / temperature (onehot_j - p_j), p the softmax of y from
  * the forward's records; 0 where masked, a zero row for an ignored target, a
  * NaN row where the forward's logp was NaN. dx contiguous [N, V] in the dtype
- * of x; dx may be x when x is contiguous. */
+ * of x; dx may be x when x is contiguous, and must not overlap it otherwise. */
 VP_API vp_status vp_processed_logprobs_bwd(const void *x, int dtype, int64_t N, int64_t V, int64_t R, int64_t s_o,
                                            int64_t s_i, int64_t vocab_start, const vp_logits_rules *rules,
                                            const int64_t *targets, const vp_rowstat *stats, const float *grad_out,

@@ -441,6 +441,105 @@ def test_many_rows_of_few_ids(dtype, n_ids):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("uniform", [True, False])
+def test_long_shared_histories(dtype, uniform):
+    """Several slices of a row for one CTA, more ids and listed columns than its lists hold, all four calls."""
+    N, V, L, start = 400, 20001, 6000, 3
+    g = torch.Generator(device="cuda").manual_seed(2)
+    x = (torch.randn(N, V, generator=g, device="cuda") * 3).to(dtype)
+    u = torch.rand(L + N, generator=g, device="cuda")
+    ids = ((u if uniform else u ** 4) * (V + 9)).long()                       # a few outside the columns
+    r = torch.arange(N, device="cuda")
+    n_prompt, n_total = torch.full_like(r, 2500), L + r // 2
+    n_total[::9] = 0
+    n_prompt[::9] = 0
+    spans = torch.stack((torch.zeros_like(r), n_prompt, n_total), 1)
+    at = torch.arange(L + N, device="cuda")
+    local = ids - start
+    ok = (local >= 0) & (local < V)
+
+    def counts(first, last):                                                  # of ids[first[r]:last[r]] in each row
+        use = ok[None, :] & (at[None, :] >= first[:, None]) & (at[None, :] < last[:, None])
+        return torch.zeros(N, V, dtype=torch.float64, device="cuda").scatter_add_(
+            1, local.clamp(0, V - 1).expand(N, -1), use.double())
+
+    c_p, c_o = counts(torch.zeros_like(r), n_prompt), counts(n_prompt, n_total)
+    # powers of two: every product and quotient is exact, a count's product too
+    rules = vp.logits_rules(ids=ids, spans=spans.contiguous(), repetition=torch.full((N,), 2.0, device="cuda"),
+                            frequency=torch.full((N,), 2.0 ** -6, device="cuda"),
+                            presence=torch.full((N,), 0.25, device="cuda"), temperature=torch.full((N,), 0.5, device="cuda"))
+    f = torch.where(c_p + c_o > 0, torch.where(x > 0, 0.5, 2.0), 1.0).double()
+    z = 2 * (x.double() * f - c_o * 2.0 ** -6 - 0.25 * (c_o > 0))
+    M = 2 * ((x.double() * f).abs() + c_o * 2.0 ** -6 + 0.25)
+    y = vp.vp_logits_process_fwd(x, rules, vocab_start=start)
+    assert ((y.double() - z).abs() - 8 * U * M - half_step(dtype) * z.abs()).max() <= 0
+    dy = torch.randn(N, V, generator=g, device="cuda").to(dtype)
+    dx = vp.vp_logits_process_bwd(x, rules, dy, vocab_start=start)
+    assert torch.equal(dx, (dy.double() * f * 2).to(dtype))
+    t = torch.randint(0, V, (N,), generator=g, device="cuda")
+    logp, stats = vp.vp_processed_logprobs_fwd(x, rules, t + start, vocab_start=start)
+    again = vp.vp_processed_logprobs_fwd(x, rules, t + start, vocab_start=start)
+    assert torch.equal(logp, again[0]) and torch.equal(stats, again[1])       # whoever finds a column first
+    ref = torch.log_softmax(z, 1)
+    lp = ref.gather(1, t[:, None])[:, 0]
+    tol = U * (16 * M.amax(1) + 62 + lp.abs())
+    assert ((logp.double() - lp).abs() - tol).max() <= 0
+    grad = torch.randn(N, generator=g, device="cuda")
+    dx = vp.vp_processed_logprobs_bwd(x, rules, t + start, stats, grad, vocab_start=start)
+    p = ref.exp()
+    e = (-p).scatter_(1, t[:, None], -torch.expm1(lp)[:, None])
+    scale = 2 * f * grad.double()[:, None]
+    off = (dx.double() - scale * e).abs()
+    assert (off - scale.abs() * p * (tol[:, None] + 8 * U) - (6 * U + half_step(dtype)) * (scale * e).abs()
+            - scale.abs() * 2.0 ** -126).max() <= 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("n", [32766, 32767, 32768, 70001])
+def test_one_id_many_times(n):
+    """Occurrences around the widths they are counted in."""
+    x = torch.zeros(2, 5000, device="cuda")
+    ids = torch.full((n,), 4321, dtype=torch.int64, device="cuda")
+    spans = torch.tensor([[0, 0, n], [0, n, n]], device="cuda")               # all output; all prompt
+    rules = vp.logits_rules(ids=ids, spans=spans, frequency=torch.full((2,), 2.0 ** -4, device="cuda"),
+                            presence=torch.full((2,), 8.0, device="cuda"))
+    y = vp.vp_logits_process_fwd(x, rules)
+    assert float(y[0, 4321]) == -n / 16 - 8 and int((y != 0).sum()) == 1
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_rows_of_a_batch(dtype):
+    """[B, T, V] views with two strides, odd V, outputs with strides of their own."""
+    B, T, V = 3, 4, 2051
+    full = torch.randn(B, T + 1, V + 2, device="cuda").to(dtype)
+    x = full[:, :-1, 1:V + 1]
+    flat = x.reshape(B * T, V)
+    cpu, q, targets, grad = make(B * T, V, dtype, 31, L=40, nb=4, masks=3)
+    rules = to_gpu(q)
+    ref = vp.vp_logits_process_fwd(flat, rules)
+    assert torch.equal(vp.vp_logits_process_fwd(x, rules).view(B * T, V), ref)
+    out = torch.full((T, B, V + 7), 9.0, device="cuda").to(dtype)             # rows of another order
+    y = out.transpose(0, 1)[:, :, 3:V + 3]
+    vp.vp_logits_process_fwd(x, rules, y=y)
+    assert torch.equal(y.reshape(B * T, V), ref) and (out[:, :, :3] == 9).all() and (out[:, :, V + 3:] == 9).all()
+    tg, gg = targets.cuda(), grad.cuda()
+    logp, st = vp.vp_processed_logprobs_fwd(x, rules, tg)
+    one, st1 = vp.vp_processed_logprobs_fwd(flat, rules, tg)
+    assert torch.equal(logp.view(torch.int32), one.view(torch.int32))
+    assert torch.equal(vp.vp_processed_logprobs_bwd(x, rules, tg, st, gg).view(torch.int16),
+                       vp.vp_processed_logprobs_bwd(flat, rules, tg, st1, gg).view(torch.int16))
+    dy = torch.randn(B * T, V, device="cuda").to(dtype)
+    assert torch.equal(vp.vp_logits_process_bwd(x, rules, dy), vp.vp_logits_process_bwd(flat, rules, dy))
+    buf = dy.clone()
+    assert torch.equal(vp.vp_logits_process_bwd(x, rules, buf, dx=buf), vp.vp_logits_process_bwd(flat, rules, dy))
+    held = flat.clone()
+    assert torch.equal(vp.vp_processed_logprobs_bwd(held, rules, tg, st1, gg, dx=held).view(torch.int16),
+                       vp.vp_processed_logprobs_bwd(flat, rules, tg, st1, gg).view(torch.int16))
+
+
+@pytest.mark.gpu
 @pytest.mark.slow
 def test_offsets_past_32_bits():
     """Rows that begin past 2^31 elements, and a history list whose last ids do."""
@@ -487,6 +586,7 @@ def test_entry_points_check_arguments_on_the_host():
     assert fwd(row=(FAKE, 1, 4, 16, 4, 0, -1, 0)) == ERR_LAYOUT
     assert fwd(y_s_i=-16) == ERR_LAYOUT
     assert fwd(rules=None) == ERR_NULL and fwd(y=None) == ERR_NULL
+    assert fwd(row=(FAKE, 1, 4, 16, 4, 0, 16, -1)) == ERR_ARG                        # vocab_start
     assert fwd(y=FAKE_ODD) == ERR_ALIGN and fwd(err=FAKE_ODD) == ERR_ALIGN
     assert fwd(row=(None, 1, 0, 16, 4, 0, 16, 0), rules=None, y=None) == OK          # N = 0
     assert fwd(rules_struct(spans=P, n_ids=3)) == ERR_NULL                           # spans without ids

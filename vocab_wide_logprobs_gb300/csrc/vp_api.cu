@@ -678,8 +678,9 @@ namespace {
 
 int64_t mask_words(int64_t V) { return (V + 31) / 32; }
 
-vp_status check_rules(const vp_logits_rules *q, int64_t N, int64_t V, vp::RuleSet *out) {
+vp_status check_rules(const vp_logits_rules *q, int64_t N, int64_t V, int64_t vocab_start, vp::RuleSet *out) {
     if (!q) return VP_ERR_NULL;
+    if (vocab_start < 0) return VP_ERR_ARG;   // negative ids are padding
     if (q->spans) {
         if (q->n_ids < 0) return VP_ERR_SHAPE;
         if (q->n_ids > 0 && !q->ids) return VP_ERR_NULL;
@@ -719,7 +720,7 @@ vp_status vp_logits_process_fwd(const void *x, int dtype, int64_t N, int64_t V, 
     if (!aligned(x, es) || !aligned(y, es) || !aligned(err_word, 4)) return VP_ERR_ALIGN;
     vp::RuleArgs a{x, nullptr, y, dtype == VP_BF16, N, V, R, s_o, s_i, y_s_o, y_s_i, vocab_start, {}, nullptr, nullptr,
                    nullptr, nullptr, err_word, (cudaStream_t)stream};
-    if ((st = check_rules(rules, N, V, &a.rules)) != VP_OK) return st;
+    if ((st = check_rules(rules, N, V, vocab_start, &a.rules)) != VP_OK) return st;
     if ((st = check_device()) != VP_OK) return st;
     return launched(vp::launch_process_fwd(a));
 }
@@ -735,7 +736,7 @@ vp_status vp_logits_process_bwd(const void *x, int dtype, int64_t N, int64_t V, 
     if (!aligned(x, es) || !aligned(dy, es) || !aligned(dx, es) || !aligned(err_word, 4)) return VP_ERR_ALIGN;
     vp::RuleArgs a{x, dy, dx, dtype == VP_BF16, N, V, R, s_o, s_i, 0, 0, vocab_start, {}, nullptr, nullptr, nullptr,
                    nullptr, err_word, (cudaStream_t)stream};
-    if ((st = check_rules(rules, N, V, &a.rules)) != VP_OK) return st;
+    if ((st = check_rules(rules, N, V, vocab_start, &a.rules)) != VP_OK) return st;
     if ((st = check_device()) != VP_OK) return st;
     return launched(vp::launch_process_bwd(a));
 }
@@ -759,7 +760,7 @@ vp_status vp_processed_logprobs_fwd(const void *x, int dtype, int64_t N, int64_t
     if (workspace_bytes < vp_processed_logprobs_workspace_size(N, V)) return VP_ERR_ARG;
     vp::RuleArgs a{x, nullptr, nullptr, dtype == VP_BF16, N, V, R, s_o, s_i, 0, 0, vocab_start, {}, targets, nullptr,
                    nullptr, workspace, err_word, (cudaStream_t)stream};
-    if ((st = check_rules(rules, N, V, &a.rules)) != VP_OK) return st;
+    if ((st = check_rules(rules, N, V, vocab_start, &a.rules)) != VP_OK) return st;
     if ((st = check_device()) != VP_OK) return st;
     return launched(vp::launch_processed_logprobs_fwd(a, logp, stats));
 }
@@ -778,7 +779,7 @@ vp_status vp_processed_logprobs_bwd(const void *x, int dtype, int64_t N, int64_t
         return VP_ERR_ALIGN;
     vp::RuleArgs a{x, nullptr, dx, dtype == VP_BF16, N, V, R, s_o, s_i, 0, 0, vocab_start, {}, targets, stats,
                    grad_out, nullptr, err_word, (cudaStream_t)stream};
-    if ((st = check_rules(rules, N, V, &a.rules)) != VP_OK) return st;
+    if ((st = check_rules(rules, N, V, vocab_start, &a.rules)) != VP_OK) return st;
     if ((st = check_device()) != VP_OK) return st;
     return launched(vp::launch_processed_logprobs_bwd(a));
 }

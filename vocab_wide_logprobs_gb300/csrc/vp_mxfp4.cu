@@ -68,9 +68,10 @@ __device__ __forceinline__ int64_t quant_place(int64_t groups, int &chunk0) {
 // The largest |x| of 8 columns as the bits of an fp32 value; NaN wins.
 __device__ __forceinline__ uint32_t octet_amax(const uint4 (&u)[1]) {
     const __nv_bfloat162 *p = reinterpret_cast<const __nv_bfloat162 *>(u);
-    const __nv_bfloat162 m = __hmax2_nan(__hmax2_nan(__habs2(p[0]), __habs2(p[1])), __hmax2_nan(__habs2(p[2]), __habs2(p[3])));
+    const __nv_bfloat162 a = __hmax2_nan(__habs2(p[0]), __habs2(p[1])), b = __hmax2_nan(__habs2(p[2]), __habs2(p[3]));
+    const __nv_bfloat162 m = __hmax2_nan(a, b);
     const uint32_t w = *reinterpret_cast<const uint32_t *>(&m);
-    return max(w << 16, w & 0xffff0000u);                  // bit patterns without sign order like the values, NaN highest
+    return max(w << 16, w & 0xffff0000u);                  // bit patterns without sign order like the values
 }
 __device__ __forceinline__ uint32_t octet_amax(const uint4 (&u)[2]) {
     const uint32_t *w = reinterpret_cast<const uint32_t *>(u);

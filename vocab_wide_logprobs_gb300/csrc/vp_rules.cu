@@ -9,9 +9,10 @@
 //   y = allowed(j) ? z / T : -inf
 //   f = dy/dx = allowed(j) ? (c_p + c_o > 0 ? (x > 0 ? 1 / rep : rep) : 1) / T : 0
 //
-// Shape. A tile is a slice of 4096 columns of one row; a CTA works through consecutive tiles (a row's slices follow one another, its
-// rules are read once). One bulk copy brings the next tile to shared memory
-// while this one is worked on. Thread t owns the 16-byte vectors t, t + kThreads,
+// Shape. A tile is a slice of 4096 columns of one row; a CTA works through
+// consecutive tiles (a row's slices follow one another, its rules are read once).
+// One bulk copy brings the next tile to shared memory while this one is worked on.
+// Thread t owns the 16-byte vectors t, t + kThreads,
 // ... of a tile. Of the ids the CTA builds tables for the tile: a word per
 // column with the number of output occurrences and a prompt bit, a word with
 // the last bias entry, and a bit per column that is set where either is.
@@ -82,7 +83,8 @@ struct TileSource {
     const T *p;
     uint32_t phase;
     int first, last, width;   // columns [first, last) are whole blocks
-    __device__ __forceinline__ TileSource(const T *src, int w) : p(src), phase((uint32_t)(uintptr_t)src & 15u), width(w) {
+    __device__ __forceinline__ TileSource(const T *src, int w)
+        : p(src), phase((uint32_t)(uintptr_t)src & 15u), width(w) {
         first = min(w, (int)(((16u - phase) & 15u) / sizeof(T)));
         last = first + (w - first) / Elem<T>::kVec * Elem<T>::kVec;
     }
@@ -154,7 +156,8 @@ __device__ __forceinline__ void store_vec(T *p, const uint4 &u, int n, uint32_t 
     before.y = __shfl_up_sync(0xffffffffu, u.y, 1);
     before.z = __shfl_up_sync(0xffffffffu, u.z, 1);
     before.w = __shfl_up_sync(0xffffffffu, u.w, 1);
-    const int lane = threadIdx.x & 31, split = (int)((16u - phase) / sizeof(T));   // columns of the block that begins here
+    const int lane = threadIdx.x & 31;
+    const int split = (int)((16u - phase) / sizeof(T));   // this vector's columns in the block that begins before it
     const bool whole = n >= kVec, block = whole && lane > 0;
     if (block) stg_stream(reinterpret_cast<char *>(p) - phase, bytes_at(before, u, 16u - phase));
     // the next vector's block is not stored where it is not whole or in another warp
@@ -348,13 +351,15 @@ struct RuleSmem {
 };
 
 template <typename T, int kOp, int kN>
-__global__ void __launch_bounds__(Tile<T, kN>::kThreads, Tile<T, kN>::kCtas) rules_kernel(const __grid_constant__ RuleKernelArgs a) {
+__global__ void __launch_bounds__(Tile<T, kN>::kThreads, Tile<T, kN>::kCtas)
+rules_kernel(const __grid_constant__ RuleKernelArgs a) {
     extern __shared__ __align__(16) uint8_t smem_raw[];
     using L = Tile<T, kN>;
     constexpr int kThreads = L::kThreads, kVec = L::kVec, kVecs = L::kVecs, kSlice = L::kWidth,
                   kWords = L::kWords, kWarps = L::kWarps;
     RuleSmem<L> &sm = *reinterpret_cast<RuleSmem<L> *>(smem_raw);
-    uint32_t *const counts = reinterpret_cast<uint32_t *>(smem_raw + sizeof(RuleSmem<L>)), *const entries = counts + (a.q.spans ? a.narrow ? kSlice / 2 : kSlice : 0);
+    uint32_t *const counts = reinterpret_cast<uint32_t *>(smem_raw + sizeof(RuleSmem<L>));
+    uint32_t *const entries = counts + (a.q.spans ? a.narrow ? kSlice / 2 : kSlice : 0);
     // column of the slice, bit 15: prompt
     uint16_t *const row_ids = reinterpret_cast<uint16_t *>(entries + (a.q.bias_spans ? kSlice : 0));
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -411,7 +416,7 @@ __global__ void __launch_bounds__(Tile<T, kN>::kThreads, Tile<T, kN>::kCtas) rul
 #pragma unroll
         for (int k = 0; k < (kVecs + 3) / 4; ++k) m.b[k] = w.mask ? 0u : 0x01010101u * L::kAll;
         if (w.mask) {
-            const int o = (sl * kSlice + tid * kVec) >> 3, n = (a.V + 7) >> 3, sh = kVec == 8 ? 0 : (tid & 1) * 4;
+            const int o = (sl * kSlice + tid * kVec) >> 3, n = (a.V - 1) / 8 + 1, sh = kVec == 8 ? 0 : (tid & 1) * 4;
 #pragma unroll
             for (int k = 0; k < kVecs; ++k) {
                 const int at = o + k * (kThreads * kVec / 8);
@@ -560,7 +565,7 @@ __global__ void __launch_bounds__(Tile<T, kN>::kThreads, Tile<T, kN>::kCtas) rul
             if (w.mask) {                                 // this thread's mask bits, for the walk
 #pragma unroll
                 for (int k = 0; k < kVecs; ++k) {
-                    const uint32_t b = allow.b[k / 4] >> (8 * (k % 4)) & Tile<T, kN>::kAll;
+                    const uint32_t b = allow.b[k / 4] >> (8 * (k % 4)) & L::kAll;
                     const int o = k * kThreads + tid;
                     if (kVec == 8) {
                         sm.allowed[buf][o] = (uint8_t)b;
@@ -644,7 +649,8 @@ __global__ void __launch_bounds__(Tile<T, kN>::kThreads, Tile<T, kN>::kCtas) rul
                     if (n > 0) {
                         u[k] = staged_vec<decltype(aligned)::value>(buffer, phase, o);
                         uint32_t on = allow.b[k / 4] >> (8 * (k % 4)) & L::kAll;
-                        if (listed) on &= kVec == 8 ? ~(uint32_t)touched8[o] : ~((uint32_t)touched8[o >> 1] >> ((tid & 1) * 4));
+                        if (listed)
+                            on &= ~(kVec == 8 ? (uint32_t)touched8[o] : (uint32_t)touched8[o >> 1] >> ((tid & 1) * 4));
                         if (n < kVec) on &= (1u << n) - 1u;
                         if (on != L::kAll) u[k] = keep_vec<T>(u[k], on, off, sm.keep_words);
                     }
@@ -659,8 +665,10 @@ __global__ void __launch_bounds__(Tile<T, kN>::kThreads, Tile<T, kN>::kCtas) rul
                 float v[kVec];
                 Elem<T>::unpack(u[k], v);
 #pragma unroll
-                for (int i = 0; i < kVec; i += 2)
-                    e = __fadd2_rn(e, scaled_exp2<T>(__fmul2_rn(__fadd2_rn(make_float2(v[i], v[i + 1]), f2(-top)), f2(c1))));
+                for (int i = 0; i < kVec; i += 2) {
+                    const float2 d = __fadd2_rn(make_float2(v[i], v[i + 1]), f2(-top));
+                    e = __fadd2_rn(e, scaled_exp2<T>(__fmul2_rn(d, f2(c1))));
+                }
             }
             s = e.x + e.y;
             const float wtop = redux_max(top);
@@ -827,18 +835,22 @@ rules_join_kernel(const PartialRec *__restrict__ parts, int K, int64_t N, float 
     if (lost) rf |= kRowBadTarget;
     store_rowstat(stats + r, M, log_s, 0.0, rf);
     if (lost && err) atomicOr(err, VP_ERRBIT_TARGET_);
-    logp[r] = ignored ? 0.f : lost || (rf & (kRowNanInf | kRowEmpty)) ? qnan() : (float)(((double)zt - (double)M) - log_s);
+    const bool bad = lost || (rf & (kRowNanInf | kRowEmpty)) != 0u;
+    logp[r] = ignored ? 0.f : bad ? qnan() : (float)(((double)zt - (double)M) - log_s);
 }
 
 // slices (records) of the ruled logprobs' forward
-int64_t rule_slices(int64_t V) { return (V + Tile<float, kRuleThreads>::kWidth - 1) / Tile<float, kRuleThreads>::kWidth; }
+int64_t rule_slices(int64_t V) {
+    constexpr int64_t width = Tile<float, kRuleThreads>::kWidth;
+    return (V + width - 1) / width;
+}
 
 template <typename T, int kOp, int kN = kRuleThreads>
 static cudaError_t launch_rules_t(RuleKernelArgs k, cudaStream_t stream) {
     using L = Tile<T, kN>;
     // resident CTAs per SM for each choice of tables and capacity of row_ids, asked once per device
     static std::atomic<int> resident[64][6][5];
-    k.n_slices = (k.V + L::kWidth - 1) / L::kWidth;
+    k.n_slices = ((int64_t)k.V + L::kWidth - 1) / L::kWidth;
     // fewer than 2^15 ids in all (a training batch's sequences): no id occurs more often
     k.narrow = k.q.n_ids < 0x8000;
     const int tables = (k.q.spans ? k.narrow ? 1 : 2 : 0) + (k.q.bias_spans ? 3 : 0);
@@ -859,9 +871,9 @@ static cudaError_t launch_rules_t(RuleKernelArgs k, cudaStream_t stream) {
     std::atomic<int> &known = resident[dev & 63][tables][step];
     int per_sm = known.load(std::memory_order_relaxed);
     if (!per_sm) {
-        e = cudaFuncSetAttribute(rules_kernel<T, kOp, kN>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes(5, kRowIdsMost));
-        if (e == cudaSuccess)
-            e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, rules_kernel<T, kOp, kN>, L::kThreads, smem);
+        const auto kernel = rules_kernel<T, kOp, kN>;
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes(5, kRowIdsMost));
+        if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, L::kThreads, smem);
         if (e != cudaSuccess) return e;
         per_sm = per_sm < 1 ? 1 : per_sm;
         known.store(per_sm, std::memory_order_relaxed);
