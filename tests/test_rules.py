@@ -347,6 +347,30 @@ def test_rows_do_not_depend_on_the_batch(dtype):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("V", [9000, 9001])
+def test_rows_do_not_depend_on_where_they_begin(dtype, V):
+    N = 6
+    x, q, targets, grad = make(N, V, dtype, 12, L=60, nb=5, masks=3)
+    rules, tg, gg = to_gpu(q), targets.cuda(), grad.cuda()
+    bits = torch.int32 if dtype == torch.float32 else torch.int16
+    first = None
+    for offset in (0, 1, 3, 8):
+        for gap in (0, 1, 4, 16):
+            room = torch.full((offset + N * (V + gap),), float("nan"), dtype=dtype, device="cuda")
+            xg = room[offset:].view(N, V + gap)[:, :V]
+            xg.copy_(x)
+            y = vp.vp_logits_process_fwd(xg, rules)
+            logp, stats = vp.vp_processed_logprobs_fwd(xg, rules, tg)
+            dx = vp.vp_processed_logprobs_bwd(xg, rules, tg, stats, gg)
+            dy = vp.vp_logits_process_bwd(xg, rules, dx)
+            got = [y.view(bits), logp.view(torch.int32), stats.view(torch.int32), dx.view(bits), dy.view(bits)]
+            if first is None:
+                first = got
+            assert all(torch.equal(a, b) for a, b in zip(got, first)), (offset, gap)
+
+
+@pytest.mark.gpu
 def test_no_rules_are_the_plain_logprobs():
     N, V = 5, 9001
     x, _, targets, grad = make(N, V, torch.bfloat16, 2)

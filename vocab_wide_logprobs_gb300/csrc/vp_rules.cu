@@ -12,11 +12,11 @@
 // Shape. A tile is a slice of 4096 columns of one row; a CTA works through
 // consecutive tiles (a row's slices follow one another, its rules are read once).
 // One bulk copy brings the next tile to shared memory while this one is worked on.
-// Thread t owns the 16-byte vectors t, t + kThreads,
-// ... of a tile. Of the ids the CTA builds tables for the tile: a word per
-// column with the number of output occurrences and a prompt bit, a word with
-// the last bias entry, and a bit per column that is set where either is.
-// Integer atomics only, so the order of the ids does not matter.
+// Thread t owns the 16-byte vectors t, t + kThreads, ... of a tile. Of the ids the
+// CTA builds tables for the tile: a word per column (half a word where fewer than
+// 2^15 ids are given) with the number of output occurrences and a prompt bit, a
+// word with the last bias entry, and a bit per column that is set where either
+// is. Integer atomics only, so the order of the ids does not matter.
 //   - The vector pass treats every column as if no list named it: a few packed
 //     instructions per vector, one byte (fp32: four bits) of the mask for each.
 //   - The columns that a list names (a few in a hundred) and the target are
@@ -47,9 +47,10 @@ constexpr uint32_t kPromptBit = 0x80000000u;
 enum RuleOp { kProcFwd = 0, kProcBwd = 1, kLogpFwd = 2, kLogpBwd = 3 };
 
 // A tile's threads and size. Measured on GB300 at 8192 x 75968 bf16 with 1000 ids a
-// row (us, forward / backward of the ruled logprobs): 4096 columns and five CTAs an
-// SM 646 / 632, six 665 / 632, seven 697 / 611; 8192 columns and four CTAs 886 / 732.
-// fp32, 1024 rows: four CTAs 147 / 136, three 161 / 149.
+// row (us, forward / backward of the ruled logprobs): five CTAs an SM 584 / 562, four
+// 720 / 575, six 673 / 570, seven 675 / 554. Tiles of 8192 columns with four CTAs took
+// 1.37 and 1.16 times as long as these. fp32, 1024 rows: four CTAs 134 / 123, three
+// 149 / 134, five 145 / 128.
 template <typename E, int kN> struct Tile {
     using T = E;
     static constexpr int kThreads = kN, kWarps = kThreads / 32;
@@ -198,7 +199,11 @@ struct RowRules {
     bool ignored;             // no target (logprobs)
     bool nan_row;             // the row's outputs are NaN
     float m, log_s, scale;    // logprobs backward: log p = (v / T - m) - log_s; scale = -g / T. Elsewhere scale = 1 / T
-    int64_t x_off, out_off;   // the row's first element in x (dy) and in the output
+    // The row's first element in x and in the output: offsets from the kernel's arguments, so that the
+    // compiler sees global memory. The ruled logprobs' forward keeps an address of x instead: 71
+    // registers rather than 96, 8192 x 75968 bf16 in 585 us rather than 705.
+    int64_t x_off, out_off;
+    const void *x;
 };
 
 __device__ __forceinline__ bool span_ok(int64_t first, int64_t n, int64_t total) {
@@ -206,7 +211,7 @@ __device__ __forceinline__ bool span_ok(int64_t first, int64_t n, int64_t total)
     return first >= 0 && n >= 0 && n <= 0x7fffffff && n <= total && first <= total - n;
 }
 
-template <int kOp>
+template <typename T, int kOp>
 __device__ RowRules row_rules(const RuleKernelArgs &a, int64_t r) {
     const RuleSet &q = a.q;
     RowRules w{};
@@ -248,6 +253,7 @@ __device__ RowRules row_rules(const RuleKernelArgs &a, int64_t r) {
     w.nan_row = !w.ok;
     w.scale = w.inv_t;
     w.x_off = a.xrows.off(r);
+    w.x = static_cast<const T *>(a.x) + w.x_off;
     w.out_off = kOp == kProcFwd ? a.orows.off(r) : r * a.V;
     if (kOp >= kLogpFwd) {
         const int64_t tg = a.targets[r], tl = tg - a.vocab_start;
@@ -350,7 +356,7 @@ struct RuleSmem {
     // counts [kWidth], with a bias list entries [kWidth], then the row's ids follow
 };
 
-template <typename T, int kOp, int kN>
+template <typename T, int kOp, int kN, bool kAligned>
 __global__ void __launch_bounds__(Tile<T, kN>::kThreads, Tile<T, kN>::kCtas)
 rules_kernel(const __grid_constant__ RuleKernelArgs a) {
     extern __shared__ __align__(16) uint8_t smem_raw[];
@@ -388,26 +394,30 @@ rules_kernel(const __grid_constant__ RuleKernelArgs a) {
     int64_t r = tile / a.n_slices;
     int slice = (int)(tile - r * a.n_slices);
     const uint64_t policy = policy_evict_first();
-    // bit b: buffer b's last tile came as a bulk copy; the parity of the phase that such a copy completes next
-    uint32_t bulk = 0u, parity = 0u;
+    uint32_t parity = 0u, copied = 0u;                   // bit b: of the phase that buffer b's next copy completes; used
     bool arrived = true, fresh = true, sorted = false;   // fresh: the CTA's first tile of this row
     int seg0 = 0;                                        // ... was this slice
 
-    // brings a tile of a row's logits (dy for the gradient of the rules)
-    auto source = [&](const RowRules &w, int sl) {
-        const int s0 = sl * kSlice;
-        return TileSource<T>((kOp == kProcBwd ? static_cast<const T *>(a.dy) + w.out_off
-                                              : static_cast<const T *>(a.x) + w.x_off) + s0, min(kSlice, a.V - s0));
-    };
+    // brings a tile of a row to a buffer; what to know of it there
+    struct Staged { uint32_t phase; bool bulk; };
     auto stage = [&](int buf, const RowRules &w, int sl) {
-        const TileSource<T> t = source(w, sl);
-        bulk = (bulk & ~(1u << buf)) | ((uint32_t)t.bulk() << buf);
-        if (t.bulk() && tid == 0) {
-            const uint32_t bytes = (uint32_t)(t.last - t.first) * (uint32_t)sizeof(T);
+        const int s0 = sl * kSlice, width = min(kSlice, a.V - s0);
+        const T *p = s0 + (kOp == kLogpFwd   ? static_cast<const T *>(w.x)
+                           : kOp == kProcBwd ? static_cast<const T *>(a.dy) + w.out_off
+                                             : static_cast<const T *>(a.x) + w.x_off);
+        auto copy = [&](T *to, const T *from, int n) {
+            const uint32_t bytes = (uint32_t)n * (uint32_t)sizeof(T);
             mbar_arrive_expect_tx(&sm.full[buf], bytes);
-            bulk_g2s(t.at(sm.stage[buf], t.first), t.p + t.first, bytes, &sm.full[buf], policy);
+            bulk_g2s(to, from, bytes, &sm.full[buf], policy);
+        };
+        if (kAligned && width == kSlice) {                // whole blocks and no edges
+            if (tid == 0) copy(sm.stage[buf], p, kSlice);
+            return Staged{0u, true};
         }
+        const TileSource<T> t(p, width);
+        if (tid == 0 && t.bulk()) copy(t.at(sm.stage[buf], t.first), t.p + t.first, t.last - t.first);
         stage_edges<L>(t, sm.stage[buf]);
+        return Staged{t.phase, t.bulk()};
     };
     // this thread's mask bits of a tile, vector k in byte k % 4 of word k / 4
     struct Allow { uint32_t b[(kVecs + 3) / 4]; };
@@ -425,9 +435,9 @@ rules_kernel(const __grid_constant__ RuleKernelArgs a) {
         }
         return m;
     };
-    RowRules w = row_rules<kOp>(a, r), next_w = w;
+    RowRules w = row_rules<T, kOp>(a, r), next_w = w;
     __syncthreads();                                     // the barriers are set up, the tables clear
-    stage(0, w, slice);
+    Staged staged = stage(0, w, slice);
     Allow allow = mask_bits(w, slice);
 
     for (int buf = 0; tile < end; ++tile, buf ^= 1) {
@@ -435,7 +445,7 @@ rules_kernel(const __grid_constant__ RuleKernelArgs a) {
         const int width = min(kSlice, a.V - s0);          // columns of this slice
         const T *xrow = static_cast<const T *>(a.x) + w.x_off + s0;
         const T *const buffer = sm.stage[buf];
-        const uint32_t phase = source(w, slice).phase;
+        const uint32_t phase = kAligned ? 0u : staged.phase;
         const T *const st = buffer + phase / sizeof(T);   // column 0
         if (!w.ok && slice == 0 && tid == 0 && a.err) atomicOr(a.err, VP_ERRBIT_RULES_);
         // the target's column in this slice, if it lies here
@@ -445,11 +455,16 @@ rules_kernel(const __grid_constant__ RuleKernelArgs a) {
         const bool row_ends = slice + 1 == a.n_slices;
         const int next_slice = row_ends ? 0 : slice + 1;
         Allow next_allow = allow;
-        const bool bulked = bulk >> buf & 1u;
+        Staged next_staged = staged;
         if (tile + 1 < end) {
-            if (row_ends) next_w = row_rules<kOp>(a, r + 1);
-            stage(buf ^ 1, row_ends ? next_w : w, next_slice);
-            next_allow = mask_bits(row_ends ? next_w : w, next_slice);
+            if (row_ends) {
+                next_w = row_rules<T, kOp>(a, r + 1);
+                next_staged = stage(buf ^ 1, next_w, 0);
+                next_allow = mask_bits(next_w, 0);
+            } else {
+                next_staged = stage(buf ^ 1, w, next_slice);
+                next_allow = mask_bits(w, next_slice);
+            }
         }
 
         // f(column past base, index) for the ids of the row's history whose columns lie below reach;
@@ -557,9 +572,10 @@ rules_kernel(const __grid_constant__ RuleKernelArgs a) {
                 mark((uint32_t)l);
             }
         }
-        if (bulked) {
+        if (staged.bulk) {
             if (!mbar_wait(&sm.full[buf], parity >> buf & 1u)) arrived = false;
             parity ^= 1u << buf;
+            copied |= 1u << buf;
         }
         if (listed) {
             if (w.mask) {                                 // this thread's mask bits, for the walk
@@ -640,14 +656,15 @@ rules_kernel(const __grid_constant__ RuleKernelArgs a) {
                 if (l == target) sm.target_z[buf] = v * w.inv_t;
             });
             uint4 u[kVecs];
-            auto read = [&](auto aligned) {
+            auto read = [&](auto whole) {                 // whole: a tile of full width
+                constexpr bool kWhole = decltype(whole)::value;
 #pragma unroll
                 for (int k = 0; k < kVecs; ++k) {
-                    const int o = k * kThreads + tid, n = width - o * kVec;
+                    const int o = k * kThreads + tid, n = kWhole ? kVec : width - o * kVec;
                     const uint32_t off = minus_inf_bits<T>();
                     u[k] = make_uint4(off, off, off, off);
                     if (n > 0) {
-                        u[k] = staged_vec<decltype(aligned)::value>(buffer, phase, o);
+                        u[k] = staged_vec<kAligned>(buffer, phase, o);
                         uint32_t on = allow.b[k / 4] >> (8 * (k % 4)) & L::kAll;
                         if (listed)
                             on &= ~(kVec == 8 ? (uint32_t)touched8[o] : (uint32_t)touched8[o >> 1] >> ((tid & 1) * 4));
@@ -657,7 +674,7 @@ rules_kernel(const __grid_constant__ RuleKernelArgs a) {
                     top = fmaxf(top, vec_max<T>(u[k]));
                 }
             };
-            if (phase == 0) read(std::true_type());
+            if (kAligned && width == kSlice) read(std::bool_constant<kAligned>());
             else read(std::false_type());
             float2 e = make_float2(s, 0.f);
 #pragma unroll
@@ -723,11 +740,11 @@ rules_kernel(const __grid_constant__ RuleKernelArgs a) {
             T *orow = static_cast<T *>(a.out) + w.out_off + s0;
             const uint32_t ophase = (uint32_t)(uintptr_t)orow & 15u;
             const bool constant = w.nan_row || w.ignored;
-            auto pass = [&](auto aligned) {
-                constexpr bool kAligned = decltype(aligned)::value;
+            auto pass = [&](auto whole) {                 // whole: a tile of full width
+                constexpr bool kWhole = decltype(whole)::value;
 #pragma unroll
                 for (int k = 0; k < kVecs; ++k) {
-                    const int o = k * kThreads + tid, n = width - o * kVec;
+                    const int o = k * kThreads + tid, n = kWhole ? kVec : width - o * kVec;
                     uint4 u = make_uint4(0u, 0u, 0u, 0u);
                     if (n > 0) {
                         u = staged_vec<kAligned>(buffer, phase, o);
@@ -757,7 +774,7 @@ rules_kernel(const __grid_constant__ RuleKernelArgs a) {
                     store_vec<kAligned>(orow + o * kVec, u, n, ophase);
                 }
             };
-            if (phase == 0 && ophase == 0) pass(std::true_type());
+            if (kAligned && width == kSlice) pass(std::bool_constant<kAligned>());
             else pass(std::false_type());
             __syncthreads();                              // the vector pass's stores come before the walk's
             if (listed) {
@@ -787,12 +804,13 @@ rules_kernel(const __grid_constant__ RuleKernelArgs a) {
             fresh = true;
         }
         allow = next_allow;
+        staged = next_staged;
         slice = next_slice;
     }
     if (!arrived) {                                       // a copy was late: flagged, and awaited once more
         atomicOr(&g_linear_fault, 1u);
         for (int b = 0; b < 2; ++b)
-            if (bulk >> b & 1u) mbar_wait(&sm.full[b], (parity >> b & 1u) ^ 1u);
+            if (copied >> b & 1u) mbar_wait(&sm.full[b], (parity >> b & 1u) ^ 1u);
     }
 }
 
@@ -845,7 +863,7 @@ int64_t rule_slices(int64_t V) {
     return (V + width - 1) / width;
 }
 
-template <typename T, int kOp, int kN = kRuleThreads>
+template <typename T, int kOp, int kN, bool kAligned>
 static cudaError_t launch_rules_t(RuleKernelArgs k, cudaStream_t stream) {
     using L = Tile<T, kN>;
     // resident CTAs per SM for each choice of tables and capacity of row_ids, asked once per device
@@ -871,7 +889,7 @@ static cudaError_t launch_rules_t(RuleKernelArgs k, cudaStream_t stream) {
     std::atomic<int> &known = resident[dev & 63][tables][step];
     int per_sm = known.load(std::memory_order_relaxed);
     if (!per_sm) {
-        const auto kernel = rules_kernel<T, kOp, kN>;
+        const auto kernel = rules_kernel<T, kOp, kN, kAligned>;
         e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes(5, kRowIdsMost));
         if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, L::kThreads, smem);
         if (e != cudaSuccess) return e;
@@ -880,8 +898,33 @@ static cudaError_t launch_rules_t(RuleKernelArgs k, cudaStream_t stream) {
     }
     if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
     const int64_t total = k.N * k.n_slices, most = (int64_t)sms * per_sm;
-    return launch_pdl(rules_kernel<T, kOp, kN>, dim3((unsigned)(total < most ? total : most)), dim3(L::kThreads),
+    return launch_pdl(rules_kernel<T, kOp, kN, kAligned>, dim3((unsigned)(total < most ? total : most)), dim3(L::kThreads),
                       (size_t)smem, stream, k);
+}
+
+// Whether every row of a matrix begins at a 16-byte boundary.
+template <typename T>
+static bool rows_aligned(const void *p, int64_t N, const Rows &rows) {
+    const auto whole = [](int64_t stride) { return stride * (int64_t)sizeof(T) % 16 == 0; };
+    return (uintptr_t)p % 16 == 0 && (rows.R < 2 || N < 2 || whole(rows.s_i)) && (rows.R >= N || whole(rows.s_o));
+}
+
+// Rows that all begin at 16-byte boundaries have a kernel of their own, without the
+// shifts and with no check per vector in tiles of full width (us, 8192 x 75968 bf16
+// with 1000 ids a row, forward / backward of the ruled logprobs: 584 / 562; with a
+// check per vector 605 / 628, with the choice made tile by tile in one kernel
+// 648 / 632). 1024 x 75967, off the boundaries: 104 / 161, in one kernel 110 / 152.
+template <typename T, int kOp>
+static cudaError_t launch_rules_t(const RuleKernelArgs &k, cudaStream_t stream) {
+    const Rows packed{1, k.V, 0};
+    const bool aligned = rows_aligned<T>(kOp == kProcBwd ? k.dy : k.x, k.N, kOp == kProcBwd ? packed : k.xrows) &&
+                         (kOp == kLogpFwd || rows_aligned<T>(k.out, k.N, kOp == kProcFwd ? k.orows : packed));
+    if constexpr (kOp == kProcFwd)
+        if (k.q.spans && k.q.n_ids > Tile<T, kRuleThreads>::kWidth * k.N)
+            return aligned ? launch_rules_t<T, kOp, kRuleThreadsLong, true>(k, stream)
+                           : launch_rules_t<T, kOp, kRuleThreadsLong, false>(k, stream);
+    return aligned ? launch_rules_t<T, kOp, kRuleThreads, true>(k, stream)
+                   : launch_rules_t<T, kOp, kRuleThreads, false>(k, stream);
 }
 
 template <int kOp>
@@ -891,9 +934,6 @@ static cudaError_t launch_rules(const RuleArgs &a) {
                      static_cast<PartialRec *>(a.parts), a.err, 0, false};
     // no rule that reads the ids: the spans are not looked at
     if (!k.q.repetition && !k.q.frequency && !k.q.presence) k.q.spans = nullptr;
-    if (kOp == kProcFwd && k.q.spans && k.q.n_ids > Tile<float, kRuleThreads>::kWidth * k.N)
-        return a.bf16 ? launch_rules_t<__nv_bfloat16, kProcFwd, kRuleThreadsLong>(k, a.stream)
-                      : launch_rules_t<float, kProcFwd, kRuleThreadsLong>(k, a.stream);
     return a.bf16 ? launch_rules_t<__nv_bfloat16, kOp>(k, a.stream) : launch_rules_t<float, kOp>(k, a.stream);
 }
 
