@@ -57,16 +57,20 @@ template <typename E, int kN> struct Tile {
     static constexpr int kVec = Elem<T>::kVec;                // columns of a 16-byte vector
     static constexpr int kWidth = 4096;                       // columns of a tile
     static constexpr int kVecs = kWidth / kVec / kThreads;    // vectors of a thread
-    static constexpr int kCtas = kThreads > 128 ? 3 : sizeof(T) == 4 ? 4 : 5;   // of an SM, if their shared memory fits
+    static constexpr int kCtas = kThreads > 256 ? 1 : kThreads > 128 ? 3 : sizeof(T) == 4 ? 4 : 5;   // of an SM, if their shared memory fits
     static constexpr int kWords = kWidth / 32;                // words of the bitmap
     static constexpr uint32_t kAll = kVec == 8 ? 0xffu : 0xfu;
 };
 constexpr int kRuleThreads = 128;
 // Rules on logits whose histories are longer than a tile: going through the ids is
 // most of the work, and four warps are few for it (64 x 151936 fp32 with up to 16384
-// ids a row: 97 us with 128 threads, 81 with 256; one row with 32768 ids: 58 and 38;
-// 1024 x 75968 bf16 with 1000 ids: 91 and 113).
+// ids a row: 97 us with 128 threads, 81 with 256; 1024 x 75968 bf16 with 1000 ids: 91
+// and 113).
 constexpr int kRuleThreadsLong = 256;
+// ... of so few rows with histories that every tile has an SM of its own (us, one row
+// of 151936 bf16, ids of the row: 700: 11 with 512 threads and 11 with 128; 4000: 13
+// and 20; 32768: 23, and 36 with 256; 131072: 51 and 92).
+constexpr int kRuleThreadsFew = 512;
 
 __device__ __forceinline__ float to_float(float v) { return v; }
 __device__ __forceinline__ float to_float(__nv_bfloat16 v) { return __bfloat162float(v); }
@@ -598,6 +602,10 @@ rules_kernel(const __grid_constant__ RuleKernelArgs a) {
         auto walk = [&](auto f) {
             if (n_listed <= (uint32_t)kListed) {
                 for (uint32_t i = tid; i < n_listed; i += kThreads) f((int)sm.listed[i]);
+            } else if (kThreads > kRuleThreads) {         // long histories fill tiles: neighbouring lanes, neighbouring columns
+#pragma unroll 4
+                for (int i = warp; i < kWords; i += kWarps)
+                    if (sm.touched[i] >> lane & 1u) f(i * 32 + lane);
             } else {
                 for (int i = tid; i < kWords; i += kThreads)
                     for (uint32_t bits = sm.touched[i]; bits; bits &= bits - 1) f(i * 32 + __ffs(bits) - 1);
@@ -919,10 +927,18 @@ static cudaError_t launch_rules_t(const RuleKernelArgs &k, cudaStream_t stream) 
     const Rows packed{1, k.V, 0};
     const bool aligned = rows_aligned<T>(kOp == kProcBwd ? k.dy : k.x, k.N, kOp == kProcBwd ? packed : k.xrows) &&
                          (kOp == kLogpFwd || rows_aligned<T>(k.out, k.N, kOp == kProcFwd ? k.orows : packed));
-    if constexpr (kOp == kProcFwd)
+    if constexpr (kOp == kProcFwd) {
+        int dev = 0, sms = 0;
+        cudaError_t e = cudaGetDevice(&dev);
+        if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+        if (e != cudaSuccess) return e;
+        if (k.q.spans && k.N <= sms / rule_slices(k.V))
+            return aligned ? launch_rules_t<T, kOp, kRuleThreadsFew, true>(k, stream)
+                           : launch_rules_t<T, kOp, kRuleThreadsFew, false>(k, stream);
         if (k.q.spans && k.q.n_ids > Tile<T, kRuleThreads>::kWidth * k.N)
             return aligned ? launch_rules_t<T, kOp, kRuleThreadsLong, true>(k, stream)
                            : launch_rules_t<T, kOp, kRuleThreadsLong, false>(k, stream);
+    }
     return aligned ? launch_rules_t<T, kOp, kRuleThreads, true>(k, stream)
                    : launch_rules_t<T, kOp, kRuleThreads, false>(k, stream);
 }
