@@ -520,6 +520,40 @@ def test_long_shared_histories(dtype, uniform):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("V", [20000, 20001])
+@pytest.mark.parametrize("N", [3, 60])
+def test_long_histories_of_their_own(N, V, dtype):
+    """Rows of up to 9000 ids, most of them in the first slices: a few rows, and more tiles than run at once."""
+    L = 9000
+    g = torch.Generator(device="cuda").manual_seed(3)
+    x = (torch.randn(N, V, generator=g, device="cuda") * 3).to(dtype)
+    ids = (torch.rand(N, L, generator=g, device="cuda") ** 4 * (V + 9)).long()   # a few outside the columns
+    n_total = torch.randint(0, L + 1, (N,), generator=g, device="cuda")
+    n_total[0], n_total[1] = L, 0
+    n_prompt = n_total // 3
+    row = torch.arange(N, device="cuda")
+    spans = torch.stack((row * L, n_prompt, n_total), 1)
+    at = torch.arange(L, device="cuda")[None, :]
+
+    def counts(first, last):
+        use = (at >= first[:, None]) & (at < last[:, None]) & (ids < V)
+        return torch.zeros(N, V, dtype=torch.float64, device="cuda").scatter_add_(1, ids.clamp(max=V - 1), use.double())
+
+    c_p, c_o = counts(torch.zeros_like(n_prompt), n_prompt), counts(n_prompt, n_total)
+    assert int((c_o[0, :4096] > 0).sum()) > 512                               # a tile with more of them than its list holds
+    rules = vp.logits_rules(ids=ids.view(-1), spans=spans, repetition=torch.full((N,), 2.0, device="cuda"),
+                            frequency=torch.full((N,), 2.0 ** -6, device="cuda"),
+                            presence=torch.full((N,), 0.25, device="cuda"), temperature=torch.full((N,), 0.5, device="cuda"))
+    f = torch.where(c_p + c_o > 0, torch.where(x > 0, 0.5, 2.0), 1.0).double()
+    z = 2 * (x.double() * f - c_o * 2.0 ** -6 - 0.25 * (c_o > 0))
+    M = 2 * ((x.double() * f).abs() + c_o * 2.0 ** -6 + 0.25)
+    y = vp.vp_logits_process_fwd(x, rules)
+    assert ((y.double() - z).abs() - 8 * U * M - half_step(dtype) * z.abs()).max() <= 0
+    assert torch.equal(y, vp.vp_logits_process_fwd(x, rules))
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("n", [32766, 32767, 32768, 70001])
 def test_one_id_many_times(n):
     """Occurrences around the widths they are counted in."""
