@@ -96,6 +96,20 @@ def test_quantize_bit_for_bit(shape, dtype):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_quantize_does_not_depend_on_where_rows_begin(dtype):
+    N, D = 13, 1088
+    x = inputs(N, D, dtype, 77).cuda()
+    ref = vp.vp_mxfp4_quantize(x)
+    for offset in (1, 4, 8, 16):
+        for gap in (0, 4, 8, 13, 16):
+            room = torch.full((offset + N * (D + gap),), math.nan, dtype=dtype, device="cuda")
+            view = room[offset:].view(N, D + gap)[:, :D]
+            view.copy_(x)
+            assert all(torch.equal(a, b) for a, b in zip(vp.vp_mxfp4_quantize(view), ref)), (offset, gap)
+
+
+@pytest.mark.gpu
 def test_quantize_rows_of_a_batch():
     """[B, T, D] rows with two strides, and caller's buffers."""
     x = torch.randn(3, 6, 128).to(torch.bfloat16).cuda()
