@@ -697,6 +697,19 @@ def test_rules_are_checked_when_they_are_made():
     assert status(lambda: R(mask_rows=torch.zeros(4, dtype=i64))) == ERR_NULL
 
 
+def test_rules_reach_the_fields_of_the_struct():
+    f, i = torch.float32, torch.int64
+    t = {k: torch.zeros(n, dtype=d) for k, n, d in (
+        ("ids", 5, i), ("spans", (2, 3), i), ("repetition", 2, f), ("frequency", 2, f), ("presence", 2, f), ("bias_ids", 4, i),
+        ("bias_values", 4, f), ("bias_spans", (2, 2), i), ("mask", (3, 7), torch.int32), ("mask_rows", 2, i),
+        ("temperature", 2, f))}
+    q = vp.logits_rules(**t).struct
+    assert all(getattr(q, k) == v.data_ptr() for k, v in t.items())
+    assert (q.n_ids, q.n_bias, q.n_masks, q.mask_stride) == (5, 4, 3, 7)
+    q = vp.logits_rules().struct
+    assert not any(getattr(q, k) for k, _ in q._fields_)
+
+
 def test_calls_check_the_rules_and_tensors():
     x = torch.zeros(4, 64)
     t, g, st = torch.zeros(4, dtype=torch.int64), torch.zeros(4), vp.rowstats(4, "cpu")
