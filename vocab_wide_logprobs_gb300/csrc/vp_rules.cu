@@ -472,7 +472,9 @@ rules_kernel(const __grid_constant__ RuleKernelArgs a) {
         }
 
         // f(column past base, index) for the ids of the row's history whose columns lie below reach;
-        // 16 ids of a thread on their way at once
+        // 8 to 16 ids of a thread on their way at once. How many decides the registers of the whole kernel,
+        // and with them its CTAs on an SM (8192 x 75968 bf16, ruled logprobs: forward with 16 ids 70
+        // registers and 575 us, with 8 ids 96 and 662; backward with 16 ids 94 and 558, with 8 ids 80 and 515)
         auto each = [&](uint64_t base, uint64_t reach, auto f) {
             const uint32_t head = min(w.n_total, (uint32_t)((uintptr_t)w.ids >> 3 & 1u));   // to a 16-byte boundary
             const uint32_t pairs = (w.n_total - head) / 2u;
@@ -480,7 +482,7 @@ rules_kernel(const __grid_constant__ RuleKernelArgs a) {
                 const uint64_t l = id - base;             // negative ids come out far above any reach
                 if (l < reach) f((uint32_t)l, i);
             };
-            constexpr uint32_t kUnroll = 8;
+            constexpr uint32_t kUnroll = kThreads > kRuleThreads ? 8 : kOp == kLogpBwd ? 4 : kOp == kProcFwd ? 6 : 8;
             const ulonglong2 *const p = reinterpret_cast<const ulonglong2 *>(w.ids + head);
 #pragma unroll 1
             for (uint32_t i0 = tid; i0 < pairs; i0 += kUnroll * kThreads) {
@@ -559,11 +561,12 @@ rules_kernel(const __grid_constant__ RuleKernelArgs a) {
                 }
                 mark(c);
             };
-            if (tid == 0 && target >= 0) mark((uint32_t)target);
+            if (tid == kThreads - 1 && target >= 0) mark((uint32_t)target);
             if (sorted) {
                 const int k = slice - seg0;
                 const uint32_t to = sm.segment[k];
-                for (uint32_t i = (k ? sm.segment[k - 1] : 0u) + tid; i < to; i += kThreads)
+                // from the second warp on: the first is late, it has issued the next tile's copy
+                for (uint32_t i = (k ? sm.segment[k - 1] : 0u) + (tid + kThreads - 32) % kThreads; i < to; i += kThreads)
                     enter(row_ids[i] & 0x7fffu, row_ids[i] >> 15);
             } else {
                 each(base, (uint64_t)width, [&](uint32_t l, uint32_t i) { enter(l, i < w.n_prompt); });
@@ -720,7 +723,7 @@ rules_kernel(const __grid_constant__ RuleKernelArgs a) {
                 if (tid == 0) sm.n_listed[buf] = 0u;
                 __syncthreads();                          // the sum is whole, the tables are clear
             }
-            if (tid == 0) {
+            if (tid == kThreads - 1) {                    // of a warp that short lists leave idle
                 float t = 0.f;
 #pragma unroll
                 for (int i = 0; i < kWarps; ++i) t += sm.red_s[buf][i] * Scaled<T>::exp((sm.red_top[buf][i] - m) * c1);
