@@ -47,10 +47,12 @@ constexpr uint32_t kPromptBit = 0x80000000u;
 enum RuleOp { kProcFwd = 0, kProcBwd = 1, kLogpFwd = 2, kLogpBwd = 3 };
 
 // A tile's threads and size. Measured on GB300 at 8192 x 75968 bf16 with 1000 ids a
-// row (us, forward / backward of the ruled logprobs): five CTAs an SM 584 / 562, four
-// 720 / 575, six 673 / 570, seven 675 / 554. Tiles of 8192 columns with four CTAs took
-// 1.37 and 1.16 times as long as these. fp32, 1024 rows: four CTAs 134 / 123, three
-// 149 / 134, five 145 / 128.
+// row (us, forward / backward of the ruled logprobs): now 573 / 506. Compared with 16
+// ids of a thread on their way in both: five CTAs an SM 584 / 562, four 720 / 575, six
+// 673 / 570, seven 675 / 554. Five is what the registers are held to; the kernels come
+// out with fewer and run up to seven. Tiles of 8192 columns with four CTAs took 1.37
+// and 1.16 times as long. fp32, 1024 rows: four CTAs 134 / 123, three 149 / 134, five
+// 145 / 128.
 template <typename E, int kN> struct Tile {
     using T = E;
     static constexpr int kThreads = kN, kWarps = kThreads / 32;
@@ -472,9 +474,10 @@ rules_kernel(const __grid_constant__ RuleKernelArgs a) {
         }
 
         // f(column past base, index) for the ids of the row's history whose columns lie below reach;
-        // 8 to 16 ids of a thread on their way at once. How many decides the registers of the whole kernel,
+        // 6 to 16 ids of a thread on their way at once. How many decides the registers of the whole kernel,
         // and with them its CTAs on an SM (8192 x 75968 bf16, ruled logprobs: forward with 16 ids 70
-        // registers and 575 us, with 8 ids 96 and 662; backward with 16 ids 94 and 558, with 8 ids 80 and 515)
+        // registers and 575 us, with 8 ids 96 and 662; backward with 16 ids 94 and 558, with 8 ids 80 and 515, with
+        // 6 ids 78 and 506)
         auto each = [&](uint64_t base, uint64_t reach, auto f) {
             const uint32_t head = min(w.n_total, (uint32_t)((uintptr_t)w.ids >> 3 & 1u));   // to a 16-byte boundary
             const uint32_t pairs = (w.n_total - head) / 2u;
@@ -482,7 +485,7 @@ rules_kernel(const __grid_constant__ RuleKernelArgs a) {
                 const uint64_t l = id - base;             // negative ids come out far above any reach
                 if (l < reach) f((uint32_t)l, i);
             };
-            constexpr uint32_t kUnroll = kThreads > kRuleThreads ? 8 : kOp == kLogpBwd ? 4 : kOp == kProcFwd ? 6 : 8;
+            constexpr uint32_t kUnroll = kThreads > kRuleThreads ? 8 : kOp == kLogpBwd ? 3 : kOp == kProcFwd ? 6 : 8;
             const ulonglong2 *const p = reinterpret_cast<const ulonglong2 *>(w.ids + head);
 #pragma unroll 1
             for (uint32_t i0 = tid; i0 < pairs; i0 += kUnroll * kThreads) {
@@ -922,9 +925,10 @@ static bool rows_aligned(const void *p, int64_t N, const Rows &rows) {
 
 // Rows that all begin at 16-byte boundaries have a kernel of their own, without the
 // shifts and with no check per vector in tiles of full width (us, 8192 x 75968 bf16
-// with 1000 ids a row, forward / backward of the ruled logprobs: 584 / 562; with a
-// check per vector 605 / 628, with the choice made tile by tile in one kernel
-// 648 / 632). 1024 x 75967, off the boundaries: 104 / 161, in one kernel 110 / 152.
+// with 1000 ids a row, forward / backward of the ruled logprobs, 16 ids of a thread on
+// their way in both: 584 / 562; with a check per vector 605 / 628, with the choice
+// made tile by tile in one kernel 648 / 632). 1024 x 75967, off the boundaries: 104 /
+// 161, in one kernel 110 / 152; now 104 / 142.
 template <typename T, int kOp>
 static cudaError_t launch_rules_t(const RuleKernelArgs &k, cudaStream_t stream) {
     const Rows packed{1, k.V, 0};
