@@ -26,8 +26,11 @@
 //     vector instead had nearly every warp go through the slow path for a lane
 //     or two.
 // The walk clears the entries that it has read, so the tables are zero again.
-// Of a row whose slices a CTA has several of, the ids are sorted by slice first:
-// going through all of them for every slice cost more than everything else.
+// Of a row whose slices a CTA has several of, the ids are counted by slice and then
+// sorted by slice, for as many slices at a time as the list in shared memory holds:
+// going through all of them for every slice cost more than everything else, with long
+// histories most of all (2048 x 75968 bf16, histories of 16384 to 17407 ids: processing
+// 556 us, 1134 with only those rows sorted whose ids all fit).
 //
 // The ruled logprobs' forward writes one vp_partial record per (slice, row),
 // as a vocabulary shard would, and rules_join_kernel joins a row's slices.
@@ -47,7 +50,7 @@ constexpr uint32_t kPromptBit = 0x80000000u;
 enum RuleOp { kProcFwd = 0, kProcBwd = 1, kLogpFwd = 2, kLogpBwd = 3 };
 
 // A tile's threads and size. Measured on GB300 at 8192 x 75968 bf16 with 1000 ids a
-// row (us, forward / backward of the ruled logprobs): now 573 / 506. Compared with 16
+// row (us, forward / backward of the ruled logprobs): now 587 / 511. Compared with 16
 // ids of a thread on their way in both: five CTAs an SM 584 / 562, four 720 / 575, six
 // 673 / 570, seven 675 / 554. Five is what the registers are held to; the kernels come
 // out with fewer and run up to seven. Tiles of 8192 columns with four CTAs took 1.37
@@ -76,6 +79,19 @@ constexpr int kRuleThreadsFew = 512;
 
 __device__ __forceinline__ float to_float(float v) { return v; }
 __device__ __forceinline__ float to_float(__nv_bfloat16 v) { return __bfloat162float(v); }
+
+// The CTAs of an SM that the registers are held to, and the pairs of ids of a thread on
+// their way at once. Together they decide what registers a kernel comes out with, and
+// so how many CTAs run: measured op by op (8192 x 75968 bf16 with 1000 ids a row, us:
+// ruled logprobs' forward with 6 pairs 587, 5 601, 7 706, 8 619; backward with 2 pairs
+// and 7 CTAs 511, 4 and 7 517, 3 and 5 543, 2 and 5 575. 1024 x 75967, processing with
+// 6 pairs 110, 8 116, 5 125).
+template <typename T, int kOp, int kN> constexpr int rule_ctas() {
+    return kOp == kLogpBwd && sizeof(T) == 2 ? 7 : Tile<T, kN>::kCtas;
+}
+template <int kOp, int kN> constexpr uint32_t rule_pairs() {
+    return kN > kRuleThreads || kOp == kProcBwd ? 8 : kOp == kLogpBwd ? 2 : 6;
+}
 
 // Orders this thread's earlier stores to shared memory before later bulk copies there.
 __device__ __forceinline__ void fence_async_proxy() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
@@ -325,9 +341,8 @@ template <typename T> __device__ __forceinline__ float vec_max(const uint4 &u) {
 }
 
 // Listed columns of a tile that are kept as a list; with more of them the bitmap
-// is walked instead. A CTA that has several slices of a row sorts the row's ids among
-// them by slice, if the slices are at most kSegment and the ids no more than a
-// capacity that the launch chooses.
+// is walked instead. A CTA that has several slices of a row, at most kSegment, sorts the
+// row's ids among them by slice, into a list whose capacity the launch chooses.
 constexpr int kListed = 512, kSegment = 64, kRowIdsLeast = 2048, kRowIdsMost = 32768;
 // The listed columns' exponentials are summed as integers, in units of 2^-48 of
 // the tile's largest, so that the order they are found in does not matter.
@@ -357,13 +372,15 @@ struct RuleSmem {
     uint32_t touched[L::kWords];
     float red_top[2][L::kWarps], red_all[2][L::kWarps], red_s[2][L::kWarps], target_z[2];
     uint32_t n_listed[2];
+    int seg_n;                                            // counted slices
+    uint32_t seg_first;                                   // row_ids[0] is the id of this number, of the counted ones
     uint32_t segment[kSegment + 1];                       // where a slice's ids begin in row_ids; counters before that
     uint16_t listed[kListed];
     // counts [kWidth], with a bias list entries [kWidth], then the row's ids follow
 };
 
 template <typename T, int kOp, int kN, bool kAligned>
-__global__ void __launch_bounds__(Tile<T, kN>::kThreads, Tile<T, kN>::kCtas)
+__global__ void __launch_bounds__(Tile<T, kN>::kThreads, (rule_ctas<T, kOp, kN>()))
 rules_kernel(const __grid_constant__ RuleKernelArgs a) {
     extern __shared__ __align__(16) uint8_t smem_raw[];
     using L = Tile<T, kN>;
@@ -402,7 +419,7 @@ rules_kernel(const __grid_constant__ RuleKernelArgs a) {
     const uint64_t policy = policy_evict_first();
     uint32_t parity = 0u, copied = 0u;                   // bit b: of the phase that buffer b's next copy completes; used
     bool arrived = true, fresh = true, sorted = false;   // fresh: the CTA's first tile of this row
-    int seg0 = 0;                                        // ... was this slice
+    int seg0 = 0, seg_to = -1;                           // ... was this slice; row_ids holds ids up to the seg_to-th from it, -1: none
 
     // brings a tile of a row to a buffer; what to know of it there
     struct Staged { uint32_t phase; bool bulk; };
@@ -474,10 +491,7 @@ rules_kernel(const __grid_constant__ RuleKernelArgs a) {
         }
 
         // f(column past base, index) for the ids of the row's history whose columns lie below reach;
-        // 6 to 16 ids of a thread on their way at once. How many decides the registers of the whole kernel,
-        // and with them its CTAs on an SM (8192 x 75968 bf16, ruled logprobs: forward with 16 ids 70
-        // registers and 575 us, with 8 ids 96 and 662; backward with 16 ids 94 and 558, with 8 ids 80 and 515, with
-        // 6 ids 78 and 506)
+        // 4 to 16 ids of a thread on their way at once
         auto each = [&](uint64_t base, uint64_t reach, auto f) {
             const uint32_t head = min(w.n_total, (uint32_t)((uintptr_t)w.ids >> 3 & 1u));   // to a 16-byte boundary
             const uint32_t pairs = (w.n_total - head) / 2u;
@@ -485,7 +499,7 @@ rules_kernel(const __grid_constant__ RuleKernelArgs a) {
                 const uint64_t l = id - base;             // negative ids come out far above any reach
                 if (l < reach) f((uint32_t)l, i);
             };
-            constexpr uint32_t kUnroll = kThreads > kRuleThreads ? 8 : kOp == kLogpBwd ? 3 : kOp == kProcFwd ? 6 : 8;
+            constexpr uint32_t kUnroll = rule_pairs<kOp, kN>();
             const ulonglong2 *const p = reinterpret_cast<const ulonglong2 *>(w.ids + head);
 #pragma unroll 1
             for (uint32_t i0 = tid; i0 < pairs; i0 += kUnroll * kThreads) {
@@ -507,18 +521,21 @@ rules_kernel(const __grid_constant__ RuleKernelArgs a) {
         };
         const uint64_t base = (uint64_t)a.vocab_start + (uint64_t)s0;
 
-        // ---- a row that this CTA has several slices of: its ids are sorted by slice once
+        // ---- a row that this CTA has several slices of: its ids are counted by slice once, and sorted by
+        // slice for as many slices at a time as row_ids has room for
         if (fresh) {
             fresh = false;
             seg0 = slice;
-            const int64_t left = end - tile;
-            const int slices = (int)min(left, a.n_slices - (int64_t)slice);
-            sorted = w.n_total > 0u && slices > 1 && slices <= kSegment;
-            if (sorted) {
-                const uint64_t reach = (uint64_t)min((int64_t)slices * kSlice, (int64_t)a.V - s0);
+            seg_to = -1;
+            sorted = false;
+            const int seg_n = (int)min(end - tile, a.n_slices - (int64_t)slice);
+            if (w.n_total != 0u && seg_n > 1 && seg_n <= kSegment) {
+                seg_to = 0;
+                if (tid == 0) sm.seg_n = seg_n;
                 for (int i = tid; i <= kSegment; i += kThreads) sm.segment[i] = 0u;
                 __syncthreads();
-                each(base, reach, [&](uint32_t l, uint32_t) { atomicAdd(&sm.segment[l / kSlice + 1], 1u); });
+                each(base, (uint64_t)min((int64_t)seg_n * kSlice, (int64_t)a.V - s0),
+                     [&](uint32_t l, uint32_t) { atomicAdd(&sm.segment[l / kSlice + 1], 1u); });
                 __syncthreads();
                 if (warp == 0) {                          // counts to beginnings
                     uint32_t lo = sm.segment[1 + lane], hi = sm.segment[33 + lane];
@@ -532,14 +549,27 @@ rules_kernel(const __grid_constant__ RuleKernelArgs a) {
                     sm.segment[33 + lane] = hi;
                 }
                 __syncthreads();
-                sorted = sm.segment[kSegment] <= (uint32_t)a.row_ids;   // no cursor below is this one
-                if (sorted) {                             // the beginnings move to the ends as the ids are placed
-                    each(base, reach, [&](uint32_t l, uint32_t i) {
-                        const uint32_t at = atomicAdd(&sm.segment[l / kSlice], 1u);
-                        row_ids[at] = (uint16_t)(l % kSlice | (i < w.n_prompt ? 0x8000u : 0u));
-                    });
-                    __syncthreads();
-                }
+            }
+        }
+        const int k = slice - seg0;
+        if (k == seg_to) {
+            // The next slices whose ids fit: none are placed yet, so segment holds their beginnings. Where not
+            // even one slice's fit, its ids are gone through for itself.
+            const uint32_t first = sm.segment[k], last = first + (uint32_t)a.row_ids;
+#pragma unroll 1
+            for (const int n = sm.seg_n; seg_to < n && sm.segment[seg_to + 1] <= last; ++seg_to) {}
+            sorted = seg_to > k;
+            __syncthreads();
+            if (sorted) {                                 // the beginnings move to the ends as the ids are placed
+                if (tid == 0) sm.seg_first = first;
+                each(base, (uint64_t)min((int64_t)(seg_to - k) * kSlice, (int64_t)a.V - s0), [&](uint32_t l, uint32_t i) {
+                    const uint32_t at = atomicAdd(&sm.segment[k + l / kSlice], 1u) - first;
+                    row_ids[at] = (uint16_t)(l % kSlice | (i < w.n_prompt ? 0x8000u : 0u));
+                });
+                __syncthreads();
+            } else {
+                if (tid == 0) sm.segment[k] = sm.segment[k + 1];
+                ++seg_to;
             }
         }
 
@@ -566,10 +596,11 @@ rules_kernel(const __grid_constant__ RuleKernelArgs a) {
             };
             if (tid == kThreads - 1 && target >= 0) mark((uint32_t)target);
             if (sorted) {
-                const int k = slice - seg0;
-                const uint32_t to = sm.segment[k];
+                // row_ids begins with the first of these slices, whose own beginning is the end of the one before
+                const uint32_t first = sm.seg_first, to = sm.segment[k] - first;
                 // from the second warp on: the first is late, it has issued the next tile's copy
-                for (uint32_t i = (k ? sm.segment[k - 1] : 0u) + (tid + kThreads - 32) % kThreads; i < to; i += kThreads)
+                for (uint32_t i = (k ? sm.segment[k - 1] - first : 0u) + (tid + kThreads - 32) % kThreads; i < to;
+                     i += kThreads)
                     enter(row_ids[i] & 0x7fffu, row_ids[i] >> 15);
             } else {
                 each(base, (uint64_t)width, [&](uint32_t l, uint32_t i) { enter(l, i < w.n_prompt); });
@@ -928,7 +959,7 @@ static bool rows_aligned(const void *p, int64_t N, const Rows &rows) {
 // with 1000 ids a row, forward / backward of the ruled logprobs, 16 ids of a thread on
 // their way in both: 584 / 562; with a check per vector 605 / 628, with the choice
 // made tile by tile in one kernel 648 / 632). 1024 x 75967, off the boundaries: 104 /
-// 161, in one kernel 110 / 152; now 104 / 142.
+// 161, in one kernel 110 / 152; now 107 / 149.
 template <typename T, int kOp>
 static cudaError_t launch_rules_t(const RuleKernelArgs &k, cudaStream_t stream) {
     const Rows packed{1, k.V, 0};
