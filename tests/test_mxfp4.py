@@ -155,6 +155,19 @@ def test_product_against_64_bits(shape, dtype):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("shape", [(513, 20001, 320), (700, 13001, 832), (20, 60001, 192), (50, 60001, 576), (100, 60001, 192)])
+def test_several_tiles_for_each_pair_and_cta(shape, dtype):
+    """More tiles than run at once, two or three times over: both accumulators, their shared columns and the ring go round."""
+    mats = product_case(*shape, seed=sum(shape))
+    bufs = gpu(mats)
+    y = vp.vp_linear_mxfp4_fwd(*bufs, dtype=dtype)
+    check_product(y, mats, dtype)
+    assert torch.equal(vp.vp_linear_mxfp4_fwd(*bufs, dtype=dtype).view(torch.int16), y.view(torch.int16))
+    assert vp.vp_fault_status() == 0
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("N", [1, 20, 200, 513])
 def test_product_of_quantised_matrices(N):
     g = torch.Generator().manual_seed(N)

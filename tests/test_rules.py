@@ -553,6 +553,99 @@ def test_long_histories_of_their_own(N, V, dtype):
     assert torch.equal(y, vp.vp_logits_process_fwd(x, rules))
 
 
+def by_row(q, name, default):
+    return default if q.get(name) is None else q[name].double()[:, None]
+
+
+def ruled_rows(x, q, rows):
+    """(z, f, M) of some rows as plain_row has them, on x's device; vocab_start 0 and no repeated bias ids."""
+    V = x.shape[1]
+    q = {k: t if k in ("ids", "bias_ids", "bias_values", "mask") else t[rows] for k, t in q.items() if t is not None}
+    x = x[rows].double()
+    rep, T = by_row(q, "repetition", 1.0), by_row(q, "temperature", 1.0)
+    freq, pres = by_row(q, "frequency", 0.0), by_row(q, "presence", 0.0)
+    c_p, c_o, bias = (torch.zeros_like(x) for _ in range(3))
+    for i, (first, n_prompt, n_total) in enumerate(q["spans"].tolist()):
+        ids = q["ids"][first:first + n_total]
+        for counts, part in ((c_p, ids[:n_prompt]), (c_o, ids[n_prompt:])):
+            part = part[(part >= 0) & (part < V)]
+            counts[i].scatter_add_(0, part, torch.ones_like(part, dtype=torch.float64))
+    if "bias_spans" in q:
+        for i, (first, n) in enumerate(q["bias_spans"].tolist()):
+            ids, values = q["bias_ids"][first:first + n], q["bias_values"][first:first + n].double()
+            bias[i, ids] = values
+    f = torch.where(c_p + c_o > 0, torch.where(x > 0, 1 / rep, rep), torch.ones_like(x))
+    z = x * f
+    M = z.abs() + freq.abs() * c_o + pres.abs() * (c_o > 0) + bias.abs()
+    z = (z - freq * c_o - pres * (c_o > 0) + bias) / T
+    f, M = f / T, M / T
+    if "mask" in q:
+        bits = torch.arange(V, device=x.device)
+        for i, m in enumerate(q["mask_rows"].tolist()):
+            if m >= 0:
+                banned = (q["mask"][m].long()[bits // 32] >> (bits % 32) & 1) == 0
+                z[i, banned], f[i, banned], M[i, banned] = -math.inf, 0.0, 0.0
+    return z, f, M
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("N, V", [(3, 140003), (1000, 151936), (1200, 262208)])
+def test_rows_of_many_slices(N, V, dtype):
+    """More slices than the join has lanes (a few rows), more than 32 and more than 64 of a row for one CTA.
+
+    The tolerances are those above with log V + 1 < 14: u (16 M + 64 + |logp|) for a logprob."""
+    L, nb = 500, 20
+    g = torch.Generator(device="cuda").manual_seed(V + N)
+    x = (torch.randn(N, V, generator=g, device="cuda") * 3).to(dtype)
+    u = torch.rand(N * L, generator=g, device="cuda")
+    row = torch.arange(N, device="cuda")
+    n_total = torch.randint(0, L + 1, (N,), generator=g, device="cuda")
+    words = torch.randint(-2 ** 31, 2 ** 31, (2, -(-V // 32)), generator=g, device="cuda").to(torch.int32)
+    q = dict(ids=(torch.where(u < 0.5, u * 2, (u - 0.5) ** 3 * 8) * V).long().clamp(max=V - 1),
+             spans=torch.stack((row * L, n_total // 3, n_total), 1),
+             repetition=1 + torch.rand(N, generator=g, device="cuda"),
+             frequency=torch.rand(N, generator=g, device="cuda"), presence=torch.rand(N, generator=g, device="cuda"),
+             temperature=0.5 + torch.rand(N, generator=g, device="cuda"),
+             bias_ids=(row[:, None] * 17 + torch.arange(nb, device="cuda") * (V // nb)).view(-1) % V,
+             bias_values=torch.randn(N * nb, generator=g, device="cuda"),
+             bias_spans=torch.stack((row * nb, torch.full_like(row, nb)), 1),
+             mask=words, mask_rows=torch.randint(-1, 2, (N,), generator=g, device="cuda"))
+    targets = torch.randint(0, V, (N,), generator=g, device="cuda")
+    targets[::3] = q["ids"].view(N, L)[::3, 0]                                # some of them listed
+    grad = torch.randn(N, generator=g, device="cuda")
+    dy = torch.randn(N, V, generator=g, device="cuda").to(dtype)
+    rules, h = vp.logits_rules(**q), half_step(dtype)
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    y = vp.vp_logits_process_fwd(x, rules, err_word=err)
+    dz = vp.vp_logits_process_bwd(x, rules, dy, err_word=err)
+    logp, stats = vp.vp_processed_logprobs_fwd(x, rules, targets, err_word=err)
+    dx = vp.vp_processed_logprobs_bwd(x, rules, targets, stats, grad, err_word=err)
+    assert int(err) == 0 and vp.vp_fault_status() == 0
+    for r0 in range(0, N, 50):
+        rows = slice(r0, r0 + 50)
+        z, f, M = ruled_rows(x, q, rows)
+        kept = torch.isfinite(z)
+        assert torch.equal(y[rows].isneginf(), ~kept) and not y[rows].isnan().any()
+        off = (y[rows].double() - z).abs() - 8 * U * M - h * z.abs()
+        assert off[kept].max() <= 0
+        ref = dy[rows].double() * f
+        assert ((dz[rows].double() - ref).abs() - (4 * U + h) * ref.abs()).max() <= 2.0 ** -133
+        lse = torch.logsumexp(z, 1)
+        t = targets[rows, None]
+        lp = z.gather(1, t)[:, 0] - lse
+        fine = torch.isfinite(lp)                                             # a masked target's is -inf
+        tol = U * (16 * M.amax(1) + 64 + torch.where(fine, lp.abs(), 0.0))
+        got = logp[rows].double()
+        assert (got[~fine] == -math.inf).all() and ((got - lp).abs() - tol)[fine].max() <= 0
+        p = torch.exp(z - lse[:, None])
+        e = (-p).scatter_(1, t, -torch.expm1(lp)[:, None])
+        scale = f * grad[rows].double()[:, None]
+        ref = torch.where(f == 0, 0.0, scale * e)
+        off = (dx[rows].double() - ref).abs() - scale.abs() * (p * (tol[:, None] + 8 * U) + 2.0 ** -126)
+        assert (off - (6 * U + h) * ref.abs()).max() <= 2.0 ** -133
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("n", [32766, 32767, 32768, 70001])
 def test_one_id_many_times(n):
