@@ -6,10 +6,15 @@ derives from the logits before anything reaches the library: element count,
 dtype, device and contiguity. Every case here is refused on the host, before
 the library is called, so these tests run anywhere (CPU tensors suffice).
 """
+import ast
+import inspect
+import types
+
 import pytest
 import torch
 
 import vocab_wide_logprobs_gb300 as vp
+from vocab_wide_logprobs_gb300 import api
 
 N, V = 6, 40
 
@@ -75,3 +80,33 @@ def test_linear_arguments_are_checked():
     assert _status(lambda: vp.vp_linear_kl_bwd(h, W, h, W, vp.KL_REVERSE, st, st, g, outs=outs)) == 2
     assert _status(lambda: vp.vp_linear_jsd_bwd(h, W, h, W, 0.5, st, st, g, outs=outs[:3])) == 7
     assert _status(lambda: vp.vp_linear_logp_fwd_noalloc(h, W, t, logp=torch.empty(N + 2))) == 2
+
+
+def test_tensors_of_another_device_than_the_current_are_refused(monkeypatch):
+    """The library launches on the current device: with tensors of another one it would read that one's addresses here."""
+    asked = []
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda i: asked.append(i) or 0)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda *a: types.SimpleNamespace(cuda_stream=0))
+    there, here = (types.SimpleNamespace(is_cuda=True, device=torch.device("cuda", i)) for i in (1, 0))
+    assert _status(lambda: api._queue(there.device)) == 4
+    assert _status(lambda: api._stream(there)) == 4
+    assert api._queue(here.device) == 0 and asked == [0]
+    api._stream(here)
+    # nor do the two halves of a call's arguments come from different devices
+    a, b = torch.zeros(N, V), torch.zeros(N, V, device="meta")
+    h, W = torch.zeros(N, 64, dtype=torch.bfloat16), torch.zeros(V, 64, dtype=torch.bfloat16)
+    assert _status(lambda: vp.vp_kl_fwd(a, b)) == 4
+    assert _status(lambda: vp.vp_linear_entropy_fwd(h, W.to("meta"))) == 4
+    assert _status(lambda: vp.vp_linear_kl_fwd(h, W, h.to("meta"), W.to("meta"))) == 4
+
+
+def test_every_call_asks_for_its_stream_with_a_tensor():
+    """No entry point takes the current device's stream without naming the tensors that it is for."""
+    tree = ast.parse(inspect.getsource(api))
+    calls = [n for n in ast.walk(tree) if isinstance(n, ast.Call)]
+    streams = [n for n in calls if isinstance(n.func, ast.Name) and n.func.id in ("_stream", "_queue")]
+    assert len(streams) > 30 and all(len(n.args) == 1 for n in streams)
+    launches = [n for n in calls if isinstance(n.func, ast.Name) and n.func.id == "_check"
+                and "fault" not in ast.unparse(n) and "row_split" not in ast.unparse(n)]
+    assert launches and all(any(s in ast.walk(n) for s in streams) for n in launches)

@@ -91,7 +91,17 @@ def _ptr(t):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
-def _stream():
+def _on_current(device):
+    """The library launches on the current device, where another device's addresses mean nothing."""
+    current = torch._C._cuda_getDevice()
+    if device.index != current:
+        raise VPError(4, f"tensors on {device}, but the current device is cuda:{current}")
+
+
+def _stream(like):
+    """The current stream, for a call on tensors like this one."""
+    if like.is_cuda:
+        _on_current(like.device)
     return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
 
 
@@ -139,8 +149,8 @@ def _parts_arg(parts, n_records: int, like):
 
 
 def _same_layout(a: torch.Tensor, b: torch.Tensor):
-    if a.shape != b.shape or a.stride() != b.stride() or a.dtype != b.dtype:
-        raise VPError(4, "A and B must share shape, strides and dtype")
+    if a.shape != b.shape or a.stride() != b.stride() or a.dtype != b.dtype or a.device != b.device:
+        raise VPError(4, "A and B must share shape, strides, dtype and device")
 
 
 def vp_logprobs_fwd(x, targets, vocab_start: int = 0, err_word=None, logp=None, stats=None):
@@ -150,7 +160,7 @@ def vp_logprobs_fwd(x, targets, vocab_start: int = 0, err_word=None, logp=None, 
     logp = _f32(N, x) if logp is None else logp
     stats = rowstats(N, x.device) if stats is None else stats
     _check(_lib.lib().vp_logprobs_fwd(_ptr(x), _dtype_code(x), N, V, R, s_o, s_i, vocab_start, _ptr(targets),
-                                      _ptr(logp), _ptr(stats), _ptr(err_word), _stream()), "vp_logprobs_fwd")
+                                      _ptr(logp), _ptr(stats), _ptr(err_word), _stream(x)), "vp_logprobs_fwd")
     return logp, stats
 
 
@@ -161,7 +171,7 @@ def vp_logprobs_bwd(x, targets, stats, grad, vocab_start: int = 0, err_word=None
     _arg(dx, N * V, x.dtype, x, "dx")
     dx = torch.empty((N, V), dtype=x.dtype, device=x.device) if dx is None else dx
     _check(_lib.lib().vp_logprobs_bwd(_ptr(x), _dtype_code(x), N, V, R, s_o, s_i, vocab_start, _ptr(targets),
-                                      _ptr(stats), _ptr(grad), _ptr(dx), _ptr(err_word), _stream()),
+                                      _ptr(stats), _ptr(grad), _ptr(dx), _ptr(err_word), _stream(x)),
            "vp_logprobs_bwd")
     return dx
 
@@ -181,7 +191,7 @@ def vp_logprobs_topk_fwd(x, targets, vocab_start: int = 0, err_word=None, logp=N
     logp = torch.empty((N, K), dtype=torch.float32, device=x.device) if logp is None else logp
     stats = rowstats(N, x.device) if stats is None else stats
     _check(_lib.lib().vp_logprobs_topk_fwd(_ptr(x), _dtype_code(x), N, V, R, s_o, s_i, vocab_start, _ptr(targets), K,
-                                           _ptr(logp), _ptr(stats), _ptr(err_word), _stream()), "vp_logprobs_topk_fwd")
+                                           _ptr(logp), _ptr(stats), _ptr(err_word), _stream(x)), "vp_logprobs_topk_fwd")
     return logp, stats
 
 
@@ -194,7 +204,7 @@ def vp_logprobs_topk_bwd(x, targets, stats, grad, vocab_start: int = 0, err_word
     _arg(dx, N * V, x.dtype, x, "dx")
     dx = torch.empty((N, V), dtype=x.dtype, device=x.device) if dx is None else dx
     _check(_lib.lib().vp_logprobs_topk_bwd(_ptr(x), _dtype_code(x), N, V, R, s_o, s_i, vocab_start, _ptr(targets), K,
-                                           _ptr(stats), _ptr(grad), _ptr(dx), _ptr(err_word), _stream()),
+                                           _ptr(stats), _ptr(grad), _ptr(dx), _ptr(err_word), _stream(x)),
            "vp_logprobs_topk_bwd")
     return dx
 
@@ -205,7 +215,7 @@ def vp_entropy_fwd(x, H=None, stats=None):
     _row_args(x, N, stats=(stats,), outs=(H,))
     H = _f32(N, x) if H is None else H
     stats = rowstats(N, x.device) if stats is None else stats
-    _check(_lib.lib().vp_entropy_fwd(_ptr(x), _dtype_code(x), N, V, R, s_o, s_i, _ptr(H), _ptr(stats), _stream()),
+    _check(_lib.lib().vp_entropy_fwd(_ptr(x), _dtype_code(x), N, V, R, s_o, s_i, _ptr(H), _ptr(stats), _stream(x)),
            "vp_entropy_fwd")
     return H, stats
 
@@ -216,7 +226,7 @@ def vp_entropy_bwd(x, stats, grad, dx=None):
     _arg(dx, N * V, x.dtype, x, "dx")
     dx = torch.empty((N, V), dtype=x.dtype, device=x.device) if dx is None else dx
     _check(_lib.lib().vp_entropy_bwd(_ptr(x), _dtype_code(x), N, V, R, s_o, s_i, _ptr(stats), _ptr(grad),
-                                     _ptr(dx), _stream()), "vp_entropy_bwd")
+                                     _ptr(dx), _stream(x)), "vp_entropy_bwd")
     return dx
 
 
@@ -229,7 +239,7 @@ def vp_kl_fwd(a, b, direction: int = KL_REVERSE, kl=None, stats_a=None, stats_b=
     stats_a = rowstats(N, a.device) if stats_a is None else stats_a
     stats_b = rowstats(N, a.device) if stats_b is None else stats_b
     _check(_lib.lib().vp_kl_fwd(_ptr(a), _ptr(b), _dtype_code(a), N, V, R, s_o, s_i, int(direction), _ptr(kl),
-                                _ptr(stats_a), _ptr(stats_b), _stream()), "vp_kl_fwd")
+                                _ptr(stats_a), _ptr(stats_b), _stream(a)), "vp_kl_fwd")
     return kl, stats_a, stats_b
 
 
@@ -247,7 +257,7 @@ def vp_kl_bwd(a, b, direction, stats_a, stats_b, grad, want_da=True, want_db=Tru
     da = da if want_da else None
     db = db if want_db else None
     _check(_lib.lib().vp_kl_bwd(_ptr(a), _ptr(b), _dtype_code(a), N, V, R, s_o, s_i, int(direction),
-                                _ptr(stats_a), _ptr(stats_b), _ptr(grad), _ptr(da), _ptr(db), _stream()),
+                                _ptr(stats_a), _ptr(stats_b), _ptr(grad), _ptr(da), _ptr(db), _stream(a)),
            "vp_kl_bwd")
     return da, db
 
@@ -263,7 +273,7 @@ def vp_jsd_fwd(a, b, beta: float = 0.5, jsd=None, stats_a=None, stats_b=None):
     stats_a = rowstats(N, a.device) if stats_a is None else stats_a
     stats_b = rowstats(N, a.device) if stats_b is None else stats_b
     _check(_lib.lib().vp_jsd_fwd(_ptr(a), _ptr(b), _dtype_code(a), N, V, R, s_o, s_i, float(beta), _ptr(jsd),
-                                 _ptr(stats_a), _ptr(stats_b), _stream()), "vp_jsd_fwd")
+                                 _ptr(stats_a), _ptr(stats_b), _stream(a)), "vp_jsd_fwd")
     return jsd, stats_a, stats_b
 
 
@@ -281,7 +291,7 @@ def vp_jsd_bwd(a, b, beta, stats_a, stats_b, grad, want_da=True, want_db=True, d
     da = da if want_da else None
     db = db if want_db else None
     _check(_lib.lib().vp_jsd_bwd(_ptr(a), _ptr(b), _dtype_code(a), N, V, R, s_o, s_i, float(beta), _ptr(stats_a),
-                                 _ptr(stats_b), _ptr(grad), _ptr(da), _ptr(db), _stream()), "vp_jsd_bwd")
+                                 _ptr(stats_b), _ptr(grad), _ptr(da), _ptr(db), _stream(a)), "vp_jsd_bwd")
     return da, db
 
 
@@ -298,6 +308,8 @@ def vp_linear_logp_fwd(hidden, weight, targets, vocab_start: int = 0, err_word=N
         raise VPError(3, "vp_linear_logp_fwd takes bf16 hidden and weight")
     if not (hidden.is_contiguous() and weight.is_contiguous()) or hidden.dim() != 2 or weight.dim() != 2:
         raise VPError(4, "hidden and weight must be contiguous 2-D tensors")
+    if hidden.device != weight.device:
+        raise VPError(4, f"hidden on {hidden.device}, weight on {weight.device}")
     N, D = hidden.shape
     V = weight.shape[0]
     if weight.shape[1] != D:
@@ -311,7 +323,7 @@ def vp_linear_logp_fwd(hidden, weight, targets, vocab_start: int = 0, err_word=N
     _check(_lib.lib().vp_linear_logp_fwd(_ptr(hidden), _ptr(weight), N, V, D, vocab_start, _ptr(targets),
                                          _ptr(logp), _ptr(stats), _ptr(workspace),
                                          workspace.numel() * workspace.element_size(), _ptr(err_word),
-                                         _stream()), "vp_linear_logp_fwd")
+                                         _stream(hidden)), "vp_linear_logp_fwd")
     return logp, stats
 
 
@@ -339,7 +351,7 @@ def vp_linear_logp_bwd(hidden, weight, targets, stats, grad, vocab_start: int = 
     _check(_lib.lib().vp_linear_logp_bwd(_ptr(hidden), _ptr(weight), N, V, D, vocab_start, _ptr(targets),
                                          _ptr(stats), _ptr(grad), _ptr(dhidden), _ptr(dW), _precision(precision),
                                          _ptr(workspace), workspace.numel() * workspace.element_size(),
-                                         _ptr(err_word), _stream()),
+                                         _ptr(err_word), _stream(hidden)),
            "vp_linear_logp_bwd")
     return dhidden, dW
 
@@ -351,12 +363,14 @@ def vp_linear_logp_fwd_noalloc(hidden, weight, targets, vocab_start: int = 0, er
         raise VPError(3, "vp_linear_logp_fwd_noalloc takes bf16 hidden and weight")
     if not (hidden.is_contiguous() and weight.is_contiguous()) or hidden.dim() != 2 or weight.dim() != 2:
         raise VPError(4, "hidden and weight must be contiguous 2-D tensors")
+    if hidden.device != weight.device:
+        raise VPError(4, f"hidden on {hidden.device}, weight on {weight.device}")
     N, V, D = _linear_model(hidden, weight, "vp_linear_logp_fwd_noalloc")
     _row_args(hidden, N, targets=targets, stats=(stats,), err_word=err_word, outs=(logp,))
     logp = _f32(N, hidden) if logp is None else logp
     stats = rowstats(N, hidden.device) if stats is None else stats
     _check(_lib.lib().vp_linear_logp_fwd_noalloc(_ptr(hidden), _ptr(weight), N, V, D, vocab_start, _ptr(targets),
-                                                 _ptr(logp), _ptr(stats), _ptr(err_word), _stream()),
+                                                 _ptr(logp), _ptr(stats), _ptr(err_word), _stream(hidden)),
            "vp_linear_logp_fwd_noalloc")
     return logp, stats
 
@@ -369,6 +383,8 @@ def _linear_model(hidden, weight, what):
         raise VPError(3, f"{what} takes bf16 hidden and weight")
     if not (hidden.is_contiguous() and weight.is_contiguous()) or hidden.dim() != 2 or weight.dim() != 2:
         raise VPError(4, "hidden and weight must be contiguous 2-D tensors")
+    if hidden.device != weight.device:
+        raise VPError(4, f"hidden on {hidden.device}, weight on {weight.device}")
     if weight.shape[1] != hidden.shape[1]:
         raise VPError(2, "hidden and weight disagree on D")
     return hidden.shape[0], weight.shape[0], hidden.shape[1]
@@ -413,13 +429,13 @@ def _same_bytes(dst, src):
 
 def vp_upload(dst, src):
     """Copy a (page-locked) host tensor into a device tensor of the same size, on the current stream."""
-    _check(_lib.lib().vp_upload(_ptr(dst), _ptr(src), _same_bytes(dst, src), _stream()), "vp_upload")
+    _check(_lib.lib().vp_upload(_ptr(dst), _ptr(src), _same_bytes(dst, src), _stream(dst)), "vp_upload")
     return dst
 
 
 def vp_download(dst, src):
     """Copy a device tensor into a (page-locked) host tensor of the same size, on the current stream."""
-    _check(_lib.lib().vp_download(_ptr(dst), _ptr(src), _same_bytes(dst, src), _stream()), "vp_download")
+    _check(_lib.lib().vp_download(_ptr(dst), _ptr(src), _same_bytes(dst, src), _stream(src)), "vp_download")
     return dst
 
 
@@ -440,7 +456,8 @@ def vp_linear_entropy_fwd(hidden, weight, H=None, stats=None, workspace=None):
     if workspace is None:
         workspace = _workspace(_lib.lib().vp_linear_entropy_workspace_size(N, V, D), hidden)
     _check(_lib.lib().vp_linear_entropy_fwd(_ptr(hidden), _ptr(weight), N, V, D, _ptr(H), _ptr(stats),
-                                            _ptr(workspace), workspace.numel(), _stream()), "vp_linear_entropy_fwd")
+                                            _ptr(workspace), workspace.numel(), _stream(hidden)),
+           "vp_linear_entropy_fwd")
     return H, stats
 
 
@@ -458,7 +475,7 @@ def vp_linear_entropy_bwd(hidden, weight, stats, grad, want_dhidden=True, want_d
         workspace = _workspace(_lib.lib().vp_linear_entropy_bwd_workspace_size(N, V, D), hidden)
     _check(_lib.lib().vp_linear_entropy_bwd(_ptr(hidden), _ptr(weight), N, V, D, _ptr(stats), _ptr(grad),
                                             _ptr(dhidden), _ptr(dW), _precision(precision), _ptr(workspace),
-                                            workspace.numel(), _stream()),
+                                            workspace.numel(), _stream(hidden)),
            "vp_linear_entropy_bwd")
     return dhidden, dW
 
@@ -468,6 +485,8 @@ def _two_models(ha, wa, hb, wb, what):
     Nb, Vb, Db = _linear_model(hb, wb, what)
     if (Nb, Vb) != (N, V):
         raise VPError(2, "the two models disagree on N or V")
+    if ha.device != hb.device:
+        raise VPError(4, f"the two models are on {ha.device} and {hb.device}")
     return N, V, Da, Db
 
 
@@ -483,7 +502,7 @@ def vp_linear_kl_fwd(ha, wa, hb, wb, direction: int = KL_REVERSE, kl=None, stats
     if workspace is None:
         workspace = _workspace(_lib.lib().vp_linear_kl_workspace_size(N, V), ha)
     _check(_lib.lib().vp_linear_kl_fwd(_ptr(ha), _ptr(wa), _ptr(hb), _ptr(wb), N, V, Da, Db, int(direction), _ptr(kl),
-                                       _ptr(stats_a), _ptr(stats_b), _ptr(workspace), workspace.numel(), _stream()),
+                                       _ptr(stats_a), _ptr(stats_b), _ptr(workspace), workspace.numel(), _stream(ha)),
            "vp_linear_kl_fwd")
     return kl, stats_a, stats_b
 
@@ -506,7 +525,7 @@ def vp_linear_kl_bwd(ha, wa, hb, wb, direction, stats_a, stats_b, grad, want=(Tr
         workspace = _workspace(_lib.lib().vp_linear_kl_bwd_workspace_size(N, V, Da, Db), ha)
     _check(_lib.lib().vp_linear_kl_bwd(_ptr(ha), _ptr(wa), _ptr(hb), _ptr(wb), N, V, Da, Db, int(direction),
                                        _ptr(stats_a), _ptr(stats_b), _ptr(grad), *[_ptr(o) for o in outs],
-                                       _precision(precision), _ptr(workspace), workspace.numel(), _stream()),
+                                       _precision(precision), _ptr(workspace), workspace.numel(), _stream(ha)),
            "vp_linear_kl_bwd")
     return tuple(outs)
 
@@ -523,7 +542,7 @@ def vp_linear_jsd_fwd(ha, wa, hb, wb, beta: float = 0.5, jsd=None, stats_a=None,
         workspace = _workspace(_lib.lib().vp_linear_jsd_workspace_size(N, V), ha)
     _check(_lib.lib().vp_linear_jsd_fwd(_ptr(ha), _ptr(wa), _ptr(hb), _ptr(wb), N, V, Da, Db, float(beta),
                                         _ptr(jsd), _ptr(stats_a), _ptr(stats_b), _ptr(workspace), workspace.numel(),
-                                        _stream()), "vp_linear_jsd_fwd")
+                                        _stream(ha)), "vp_linear_jsd_fwd")
     return jsd, stats_a, stats_b
 
 
@@ -545,7 +564,7 @@ def vp_linear_jsd_bwd(ha, wa, hb, wb, beta, stats_a, stats_b, grad, want=(True, 
         workspace = _workspace(_lib.lib().vp_linear_jsd_bwd_workspace_size(N, V, Da, Db), ha)
     _check(_lib.lib().vp_linear_jsd_bwd(_ptr(ha), _ptr(wa), _ptr(hb), _ptr(wb), N, V, Da, Db, float(beta),
                                         _ptr(stats_a), _ptr(stats_b), _ptr(grad), *[_ptr(o) for o in outs],
-                                        _precision(precision), _ptr(workspace), workspace.numel(), _stream()),
+                                        _precision(precision), _ptr(workspace), workspace.numel(), _stream(ha)),
            "vp_linear_jsd_bwd")
     return tuple(outs)
 
@@ -560,7 +579,7 @@ def vp_logprobs_partial(x, targets, vocab_start: int = 0, parts=None):
     _parts_arg(parts, N, x)
     parts = partials(N, x.device) if parts is None else parts
     _check(_lib.lib().vp_logprobs_partial(_ptr(x), _dtype_code(x), N, V, R, s_o, s_i, vocab_start, _ptr(targets),
-                                          _ptr(parts), _stream()), "vp_logprobs_partial")
+                                          _ptr(parts), _stream(x)), "vp_logprobs_partial")
     return parts
 
 
@@ -569,7 +588,7 @@ def vp_entropy_partial(x, parts=None):
     N, V, R, s_o, s_i = rows_of(x)
     _parts_arg(parts, N, x)
     parts = partials(N, x.device) if parts is None else parts
-    _check(_lib.lib().vp_entropy_partial(_ptr(x), _dtype_code(x), N, V, R, s_o, s_i, _ptr(parts), _stream()),
+    _check(_lib.lib().vp_entropy_partial(_ptr(x), _dtype_code(x), N, V, R, s_o, s_i, _ptr(parts), _stream(x)),
            "vp_entropy_partial")
     return parts
 
@@ -581,7 +600,7 @@ def vp_kl_partial(a, b, direction: int = KL_REVERSE, parts=None):
     _parts_arg(parts, N, a)
     parts = partials(N, a.device) if parts is None else parts
     _check(_lib.lib().vp_kl_partial(_ptr(a), _ptr(b), _dtype_code(a), N, V, R, s_o, s_i, int(direction),
-                                    _ptr(parts), _stream()), "vp_kl_partial")
+                                    _ptr(parts), _stream(a)), "vp_kl_partial")
     return parts
 
 
@@ -598,7 +617,7 @@ def vp_logprobs_merge(parts, err_word=None, logp=None, stats=None):
     _row_args(parts, N, stats=(stats,), err_word=err_word, outs=(logp,))
     logp = _f32(N, parts) if logp is None else logp
     stats = rowstats(N, parts.device) if stats is None else stats
-    _check(_lib.lib().vp_logprobs_merge(_ptr(parts), K, N, _ptr(logp), _ptr(stats), _ptr(err_word), _stream()),
+    _check(_lib.lib().vp_logprobs_merge(_ptr(parts), K, N, _ptr(logp), _ptr(stats), _ptr(err_word), _stream(parts)),
            "vp_logprobs_merge")
     return logp, stats
 
@@ -609,7 +628,7 @@ def vp_entropy_merge(parts, H=None, stats=None):
     _row_args(parts, N, stats=(stats,), outs=(H,))
     H = _f32(N, parts) if H is None else H
     stats = rowstats(N, parts.device) if stats is None else stats
-    _check(_lib.lib().vp_entropy_merge(_ptr(parts), K, N, _ptr(H), _ptr(stats), _stream()), "vp_entropy_merge")
+    _check(_lib.lib().vp_entropy_merge(_ptr(parts), K, N, _ptr(H), _ptr(stats), _stream(parts)), "vp_entropy_merge")
     return H, stats
 
 
@@ -621,7 +640,7 @@ def vp_kl_merge(parts, direction: int = KL_REVERSE, kl=None, stats_a=None, stats
     stats_a = rowstats(N, parts.device) if stats_a is None else stats_a
     stats_b = rowstats(N, parts.device) if stats_b is None else stats_b
     _check(_lib.lib().vp_kl_merge(_ptr(parts), K, N, int(direction), _ptr(kl), _ptr(stats_a), _ptr(stats_b),
-                                  _stream()), "vp_kl_merge")
+                                  _stream(parts)), "vp_kl_merge")
     return kl, stats_a, stats_b
 
 
@@ -650,7 +669,7 @@ def vp_linear_logp_partial(hidden, weight, targets, vocab_start: int = 0, parts=
     if workspace is None:
         workspace = _workspace(_lib.lib().vp_linear_logp_workspace_size(N, V, D), hidden)
     _check(_lib.lib().vp_linear_logp_partial(_ptr(hidden), _ptr(weight), N, V, D, vocab_start, _ptr(targets),
-                                             _ptr(parts), _ptr(workspace), workspace.numel(), _stream()),
+                                             _ptr(parts), _ptr(workspace), workspace.numel(), _stream(hidden)),
            "vp_linear_logp_partial")
     return parts
 
@@ -663,7 +682,7 @@ def vp_linear_entropy_partial(hidden, weight, parts=None, workspace=None):
     if workspace is None:
         workspace = _workspace(_lib.lib().vp_linear_entropy_workspace_size(N, V, D), hidden)
     _check(_lib.lib().vp_linear_entropy_partial(_ptr(hidden), _ptr(weight), N, V, D, _ptr(parts), _ptr(workspace),
-                                                workspace.numel(), _stream()), "vp_linear_entropy_partial")
+                                                workspace.numel(), _stream(hidden)), "vp_linear_entropy_partial")
     return parts
 
 
@@ -675,7 +694,7 @@ def vp_linear_kl_partial(ha, wa, hb, wb, direction: int = KL_REVERSE, parts=None
     if workspace is None:
         workspace = _workspace(_lib.lib().vp_linear_kl_workspace_size(N, V), ha)
     _check(_lib.lib().vp_linear_kl_partial(_ptr(ha), _ptr(wa), _ptr(hb), _ptr(wb), N, V, Da, Db, int(direction),
-                                           _ptr(parts), _ptr(workspace), workspace.numel(), _stream()),
+                                           _ptr(parts), _ptr(workspace), workspace.numel(), _stream(ha)),
            "vp_linear_kl_partial")
     return parts
 
@@ -807,6 +826,7 @@ def _addr(t):
 
 
 def _queue(device):
+    _on_current(device)
     return torch._C._cuda_getCurrentRawStream(device.index)
 
 
@@ -938,8 +958,8 @@ def vp_mxfp4_dequantize(codes, scales, dtype=torch.bfloat16, out=None):
     _arg(out, N * D, dtype, codes, "out")
     _on_gpu(codes)
     out = torch.empty((N, D), dtype=dtype, device=codes.device) if out is None else out
-    _check(_handle().vp_mxfp4_dequantize(_addr(codes), _addr(scales), N, D, _DTYPES[dtype], _addr(out), _queue(codes.device)),
-           "vp_mxfp4_dequantize")
+    _check(_handle().vp_mxfp4_dequantize(_addr(codes), _addr(scales), N, D, _DTYPES[dtype], _addr(out),
+                                         _queue(codes.device)), "vp_mxfp4_dequantize")
     return out
 
 
