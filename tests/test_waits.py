@@ -1,0 +1,99 @@
+"""What a kernel waits for before it leaves early (csrc/vp_waits.h), against a model of the barriers.
+
+The header is plain C++: it is compiled for the host here, and its answers are
+played through on a model of an mbarrier, for every state that a pair of CTAs
+can be in when one of them gives up. Nothing of this runs on a GPU.
+"""
+import ctypes
+import os
+import subprocess
+
+import pytest
+
+import vocab_wide_logprobs_gb300 as vp
+
+CSRC = os.path.join(os.path.dirname(vp.__file__), "csrc")
+NOTHING, ALL, NO_PEER, NO_LEADER = range(4)
+
+
+@pytest.fixture(scope="module")
+def header(tmp_path_factory):
+    at = tmp_path_factory.mktemp("waits")
+    source = at / "waits.cpp"
+    source.write_text('#include "vp_waits.h"\n'
+                      'extern "C" uint32_t late(uint32_t s, uint32_t a, uint32_t b, uint32_t n) {\n'
+                      '    const vp::LateStage l = vp::late_stage(s, a, b, n);\n'
+                      '    return l.owed << 1 | l.parity;\n}\n')
+    subprocess.run(["g++", "-std=c++17", "-Wall", "-Werror", "-shared", "-fPIC", f"-I{CSRC}", str(source), "-o",
+                    str(at / "waits.so")], check=True)
+    return ctypes.CDLL(str(at / "waits.so"))
+
+
+class Barrier:
+    """An mbarrier of one arrival: a phase ends when the arrival and all its bytes have come."""
+
+    def __init__(self):
+        self.phase, self.pending, self.tx = 0, 1, 0
+
+    def arm(self, tx):
+        assert self.pending == 1, "armed twice in a phase"
+        self.pending, self.tx = 0, self.tx + tx
+        self.turn()
+
+    def land(self, tx):
+        self.tx -= tx
+        self.turn()
+
+    def turn(self):
+        if self.pending == 0 and self.tx == 0:
+            self.phase, self.pending = self.phase + 1, 1
+
+    def done(self, parity):
+        return self.phase & 1 != parity
+
+
+@pytest.mark.parametrize("n", [1, 3, 6, 10])
+def test_every_copy_in_flight_is_awaited(header, n):
+    """Both CTAs at every pair of counts, each copy under way or landed: the wait ends when the last has landed."""
+    for used in range(3 * n + 1):                                    # fills whose both halves were used
+        for leader in range(used, used + n + 1):                     # a stage is filled again only after that
+            for peer in range(used, used + n + 1):
+                for late in range(2):                                # of what is not used: all landed, all under way
+                    bars, flying = [Barrier() for _ in range(n)], []
+                    for f in range(max(leader, peer)):
+                        for mine, tx in ((leader, "leader"), (peer, "peer")):
+                            if f >= mine:
+                                continue
+                            if tx == "leader":
+                                bars[f % n].arm(2)
+                            if f >= used and late:
+                                flying.append(f % n)
+                            else:
+                                bars[f % n].land(1)
+                    plans = [divmod(header.late(s, leader, peer, n), 2) for s in range(n)]
+                    for s, (owed, _) in enumerate(plans):
+                        assert (owed == NOTHING) == (s >= max(leader, peer))
+                        assert owed != NOTHING or s not in flying
+                        if owed == NO_PEER:
+                            bars[s].land(1)
+                        if owed == NO_LEADER:
+                            bars[s].arm(1)
+                    for s, (owed, parity) in enumerate(plans):
+                        assert owed == NOTHING or bars[s].done(parity) == (s not in flying)
+                    for s in flying:
+                        bars[s].land(1)
+                    assert all(owed == NOTHING or bars[s].done(parity) for s, (owed, parity) in enumerate(plans))
+
+
+def test_the_stage_that_is_waited_for_is_among_them(header):
+    """The one whose copy is late holds up everything behind it: the producer stops right before filling it again."""
+    assert header.late(2, 8, 8, 6) >> 1 == ALL                       # fill 8 would be stage 2's second
+    assert header.late(2, 8, 9, 6) >> 1 == NO_LEADER and header.late(2, 9, 8, 6) >> 1 == NO_PEER
+
+
+def test_the_kernels_with_rings_ask():
+    """The MXFP4 product, of one CTA and of pairs: on every way out."""
+    with open(os.path.join(CSRC, "vp_mxfp4.cu")) as f:
+        kernels = f.read().split("template <int kNT, typename T>\n__global__")[1].split("template <typename T>\n__global__")
+    for kernel in kernels:
+        assert "late_stage(" in kernel and "bars.done" in kernel

@@ -16,6 +16,7 @@
 #include "vp_gemm_host.cuh"
 #include "vp_launch.h"
 #include "vp_umma.cuh"
+#include "vp_waits.h"
 
 namespace vp {
 
@@ -352,7 +353,7 @@ struct StageCount {
 
 template <int kNT>
 struct Mxfp4Bars {
-    uint64_t full[x_stages(kNT)], empty[x_stages(kNT)], acc_full[2], acc_empty[2];
+    uint64_t full[x_stages(kNT)], empty[x_stages(kNT)], acc_full[2], acc_empty[2], done;   // done: every MMA
     uint32_t tmem_base;
 };
 
@@ -380,6 +381,7 @@ linear_mxfp4_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_const
             mbar_init(&bars.acc_full[b], 1);
             mbar_init(&bars.acc_empty[b], kXThreads - 64);
         }
+        mbar_init(&bars.done, 1);
         fence_mbar_init();
         prefetch_tensormap(&tm_w);
         prefetch_tensormap(&tm_x);
@@ -395,17 +397,14 @@ linear_mxfp4_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_const
         if (elect_one()) {
             const uint64_t pol_w = l2_policy(n_tb > 1 ? 2 : 1), pol_x = l2_policy(2);
             StageCount at;
-            uint32_t it = 0;                             // stages begun, up to kStages
+            uint32_t fills = 0;
             bool ok = true;
             for (int64_t tile = blockIdx.x; tile < n_tiles && ok; tile += gridDim.x) {
                 const int vb = (int)(tile / n_tb), tb = (int)(tile - (int64_t)vb * n_tb);
                 for (int kb = 0; kb < n_k; ++kb, at.next(kStages)) {
                     const uint32_t st = at.st;
-                    if (it == (uint32_t)kStages) {
-                        if (!mbar_wait(&bars.empty[st], at.phase ^ 1)) { ok = false; break; }
-                    } else {
-                        ++it;
-                    }
+                    if (fills >= (uint32_t)kStages && !mbar_wait(&bars.empty[st], at.phase ^ 1)) { ok = false; break; }
+                    ++fills;
                     uint8_t *a = smem + st * kStageBytes, *b = a + kXAStage, *sa = b + kNT * kXRow, *sb = sa + kXSStage;
                     const uint32_t sbytes = 512u * (uint32_t)min(2, n_kt - 2 * kb);
                     mbar_arrive_expect_tx(&bars.full[st], kXAStage + kNT * kXRow + 2 * sbytes);
@@ -416,15 +415,12 @@ linear_mxfp4_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_const
                              pol_x);
                 }
             }
-            if (!ok) {
-                atomicOr(&g_linear_fault, 1u);
-                // the copies in flight land before the CTA gives up its shared memory: every other
-                // stage's last one (this stage's are in use or done)
-                for (uint32_t i = 0; i < it; ++i) {
-                    if (i == at.st) continue;
-                    mbar_wait(&bars.full[i], i < at.st ? at.phase : at.phase ^ 1);
-                }
+            // every copy lands before the CTA gives up its shared memory, whoever gave up
+            for (uint32_t i = 0; i < (uint32_t)kStages; ++i) {
+                const LateStage l = late_stage(i, fills, fills, kStages);
+                if (l.owed != kOwedNothing && !mbar_wait(&bars.full[i], l.parity)) { ok = false; break; }
             }
+            if (!ok) atomicOr(&g_linear_fault, 1u);
         }
     } else if (warp == 1) {
         if (elect_one()) {
@@ -462,6 +458,8 @@ linear_mxfp4_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_const
                 }
                 umma_commit(&bars.acc_full[buf]);
             }
+            umma_commit(&bars.done);                     // tensor memory is given back after the last MMA
+            if (!mbar_wait(&bars.done, 0)) ok = false;
             if (!ok) atomicOr(&g_linear_fault, 2u);
         }
     } else {
@@ -524,9 +522,30 @@ constexpr int kYOverlap = kYT - (int)kYAcc1;
 static_assert(kYAcc1 == 112 && kYOverlap == 144, "the epilogue's reads are written for these");
 
 struct PairMxfp4Bars {
-    uint64_t full[kYStages], empty[kYStages], acc_full[2], shared_free;
+    uint64_t full[kYStages], empty[kYStages], acc_full[2], shared_free, done;   // done: every MMA (leader's)
     uint32_t tmem_base;
+    uint32_t fills;                                       // stages that this CTA has filled
+    uint32_t gave_up;                                     // a wait of either CTA ran out; the same in both at the end
 };
+
+// A bounded wait ran out: flagged for the host and, before they leave, for both CTAs.
+__device__ __forceinline__ void pair_gives_up(PairMxfp4Bars &bars, uint32_t bit) {
+    atomicOr(&g_linear_fault, bit);
+    st_cluster_u32(cluster_addr(&bars.gave_up, 0), 1u);
+    st_cluster_u32(cluster_addr(&bars.gave_up, 1), 1u);
+}
+
+// Then the leader waits for the copies of both CTAs that are still under way.
+__device__ __forceinline__ void pair_drain(PairMxfp4Bars &bars) {
+    const uint32_t peer = ld_cluster_u32(cluster_addr(&bars.fills, 1));
+    for (uint32_t i = 0; i < (uint32_t)kYStages; ++i) {
+        const LateStage l = late_stage(i, bars.fills, peer, kYStages);
+        if (l.owed == kOwedNothing) continue;
+        if (l.owed == kOwedNoPeer) mbar_complete_tx(&bars.full[i], kYStageBytes);
+        if (l.owed == kOwedNoLeader) mbar_arrive_expect_tx(&bars.full[i], kYStageBytes);
+        if (!mbar_wait_cluster(&bars.full[i], l.parity)) break;
+    }
+}
 
 __device__ __forceinline__ void umma_mxf4_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
                                                uint32_t sfa, uint32_t sfb, uint32_t accumulate) {
@@ -537,6 +556,12 @@ __device__ __forceinline__ void umma_mxf4_pair(uint32_t d_tmem, uint64_t adesc, 
             d_tmem),
         "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
         : "memory");
+}
+
+// Arrive once on a barrier of this CTA when the pair MMAs issued so far by this thread have completed.
+__device__ __forceinline__ void umma_commit_pair_here(uint64_t *bar) {
+    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
+                 : "memory");
 }
 
 // In both CTAs, from the same place of each one's shared memory.
@@ -566,6 +591,8 @@ linear_mxfp4_pair_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_
         mbar_init(&bars.acc_full[0], 1);
         mbar_init(&bars.acc_full[1], 1);
         mbar_init(&bars.shared_free, 2 * (kXThreads - 64));   // the epilogue threads of both CTAs
+        mbar_init(&bars.done, 1);
+        bars.gave_up = 0u;
         fence_mbar_init();
         prefetch_tensormap(&tm_w);
         prefetch_tensormap(&tm_x);
@@ -584,14 +611,15 @@ linear_mxfp4_pair_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_
         if (elect_one()) {
             const uint64_t keep = l2_policy(2);
             StageCount at;
-            bool ok = true, again = false;               // again: the ring has been filled once
+            uint32_t fills = 0;
+            bool ok = true;
             for (int64_t tile = pair; tile < n_tiles && ok; tile += n_pairs) {
                 const int vp = (int)(tile / n_tb), tb = (int)(tile - (int64_t)vp * n_tb);
                 const int wb = 2 * vp + (int)rank;
                 for (int kb = 0; kb < n_k; ++kb, at.next(kYStages)) {
                     const uint32_t st = at.st;
-                    if (again && !mbar_wait_cluster(&bars.empty[st], at.phase ^ 1)) { ok = false; break; }
-                    again = again || st == kYStages - 1;
+                    if (fills >= kYStages && !mbar_wait_cluster(&bars.empty[st], at.phase ^ 1)) { ok = false; break; }
+                    ++fills;
                     uint8_t *a = smem + st * kYStageBytes, *b = a + kXAStage, *sa = b + kYBStage, *sb = sa + kXSStage;
                     const uint32_t fb = cluster_addr(&bars.full[st], 0);
                     if (rank == 0) mbar_arrive_expect_tx(&bars.full[st], 2 * kYStageBytes);
@@ -602,7 +630,13 @@ linear_mxfp4_pair_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_
                     tma_load_2d_pair(sb + kXSStage, &tm_xs, kb * (kXSStage / 4), 2 * tb + 1, fb, keep);
                 }
             }
-            if (!ok) atomicOr(&g_linear_fault, 1u);
+            // every stage is used before the CTA leaves: its copies have landed, and the arrival that says so
+            for (uint32_t i = 0; i < (uint32_t)kYStages && ok; ++i) {
+                const LateStage l = late_stage(i, fills, fills, kYStages);
+                if (l.owed != kOwedNothing && !mbar_wait_cluster(&bars.empty[i], l.parity)) ok = false;
+            }
+            bars.fills = fills;
+            if (!ok) pair_gives_up(bars, 1u);
         }
     } else if (warp == 1) {
         // ---------------- MMA issuer (leader only) ----------------
@@ -643,7 +677,9 @@ linear_mxfp4_pair_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_
                 }
                 umma_commit_pair(&bars.acc_full[j & 1]);
             }
-            if (!ok) atomicOr(&g_linear_fault, 2u);
+            umma_commit_pair_here(&bars.done);           // tensor memory is given back after the last MMA
+            if (!mbar_wait(&bars.done, 0)) ok = false;
+            if (!ok) pair_gives_up(bars, 2u);
         }
     } else {
         // ---------------- epilogue (both CTAs) ----------------
@@ -656,7 +692,7 @@ linear_mxfp4_pair_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_
             const int64_t t0 = (int64_t)tb * kYT, v = (int64_t)(2 * vp + (int)rank) * kXM + q * 32 + lane;
             if (ok && !mbar_wait_cluster(&bars.acc_full[j & 1], (j >> 1) & 1)) {
                 ok = false;
-                atomicOr(&g_linear_fault, 4u);
+                pair_gives_up(bars, 4u);
             }
             tc_fence_after();
             const bool all = __all_sync(0xffffffffu, ok);
@@ -701,7 +737,12 @@ linear_mxfp4_pair_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_
     }
     tc_fence_before();
     __syncthreads();
-    cluster_sync();                                      // no arrival or copy still targets either CTA
+    cluster_sync();                                      // no arrival or copy still targets either CTA,
+    if (bars.gave_up) {                                  // but where a wait ran out
+        if (rank == 0 && threadIdx.x == 0) pair_drain(bars);
+        __syncthreads();
+        cluster_sync();
+    }
     tc_fence_after();
     if (warp == 1) tmem_dealloc_pair(tmem, 512);
 }
