@@ -6,6 +6,7 @@ can be in when one of them gives up. Nothing of this runs on a GPU.
 """
 import ctypes
 import os
+import re
 import subprocess
 
 import pytest
@@ -97,3 +98,11 @@ def test_the_kernels_with_rings_ask():
         kernels = f.read().split("template <int kNT, typename T>\n__global__")[1].split("template <typename T>\n__global__")
     for kernel in kernels:
         assert "late_stage(" in kernel and "bars.done" in kernel
+
+
+def test_a_part_of_a_tile_is_not_handed_to_the_epilogue():
+    """A stage that never came ends the MMAs of its tile: the accumulator is announced only when it is whole."""
+    with open(os.path.join(CSRC, "vp_mxfp4.cu")) as f:
+        lines = [line.split("//")[0].strip() for line in f]
+    at = [i for i, line in enumerate(lines) if re.match(r"umma_commit(_pair)?\(&bars\.acc_full", line)]
+    assert len(at) == 2 and all(lines[i - 1] == "if (!ok) break;" for i in at)

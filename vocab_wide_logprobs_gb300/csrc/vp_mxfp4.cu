@@ -456,6 +456,7 @@ linear_mxfp4_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_const
                     umma_commit(&bars.empty[at.st]);
                     at.next(kStages);
                 }
+                if (!ok) break;                          // a part of a tile is no tile
                 umma_commit(&bars.acc_full[buf]);
             }
             umma_commit(&bars.done);                     // tensor memory is given back after the last MMA
@@ -675,6 +676,7 @@ linear_mxfp4_pair_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_
                     umma_commit_pair(&bars.empty[at.st]);
                     at.next(kYStages);
                 }
+                if (!ok) break;                          // a part of a tile is no tile
                 umma_commit_pair(&bars.acc_full[j & 1]);
             }
             umma_commit_pair_here(&bars.done);           // tensor memory is given back after the last MMA
