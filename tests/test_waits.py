@@ -24,7 +24,8 @@ def header(tmp_path_factory):
     source.write_text('#include "vp_waits.h"\n'
                       'extern "C" uint32_t late(uint32_t s, uint32_t a, uint32_t b, uint32_t n) {\n'
                       '    const vp::LateStage l = vp::late_stage(s, a, b, n);\n'
-                      '    return l.owed << 1 | l.parity;\n}\n')
+                      '    return l.owed << 1 | l.parity;\n}\n'
+                      'extern "C" uint32_t next(uint32_t p, uint32_t b) { return vp::next_phase(p, b); }\n')
     subprocess.run(["g++", "-std=c++17", "-Wall", "-Werror", "-shared", "-fPIC", f"-I{CSRC}", str(source), "-o",
                     str(at / "waits.so")], check=True)
     return ctypes.CDLL(str(at / "waits.so"))
@@ -106,3 +107,72 @@ def test_a_part_of_a_tile_is_not_handed_to_the_epilogue():
         lines = [line.split("//")[0].strip() for line in f]
     at = [i for i, line in enumerate(lines) if re.match(r"umma_commit(_pair)?\(&bars\.acc_full", line)]
     assert len(at) == 2 and all(lines[i - 1] == "if (!ok) break;" for i in at)
+
+
+def tiles_of_a_cta(header, copied, late, sees, stops=True):
+    """The rules' loop over tiles: the thread that begins the copies and another one.
+
+    copied[i]: tile i comes by a bulk copy. The late-th lands while it is waited for; sees: which of the two threads'
+    waits ended all the same. Returns how many waits ran out in all."""
+    bars = [Barrier(), Barrier()]
+    arrived, parity, ran_out, flying = [True, True], [0, 0], 0, set()
+
+    def stage(i):
+        if copied[i] and (arrived[0] or not stops):
+            bars[i % 2].arm(1)
+            flying.add(i)
+
+    def lands(but=None):
+        for i in flying - {but}:
+            bars[i % 2].land(1)
+            flying.discard(i)
+
+    stage(0)
+    for i in range(len(copied)):
+        buf = i % 2
+        if i + 1 < len(copied):
+            stage(i + 1)
+        if i == late:
+            first = [t for t in range(2) if not sees[t]]
+        else:
+            lands(but=late if late is not None and i < late else None)
+            first = []
+        for t in first + [t for t in range(2) if t not in first]:
+            if i == late and t not in first:
+                lands()
+            if not copied[i] or not (arrived[t] or not stops):
+                continue
+            if not bars[buf].done(header.next(parity[t], buf)):
+                ran_out += 1
+                arrived[t] = False
+                assert stops or t
+                waits = [(buf, header.next(parity[t], buf))]
+                if i + 1 < len(copied) and copied[i + 1]:
+                    waits.append((buf ^ 1, header.next(parity[t], buf ^ 1)))
+                if t == 0:                                           # the thread that began them sees all land
+                    assert {b for b, _ in waits} == {k % 2 for k in flying}
+                    lands()
+                    assert all(bars[b].done(p) for b, p in waits)
+            parity[t] ^= 1 << buf
+    assert not flying                                                # nothing is under way at the end
+    return ran_out
+
+
+def test_a_late_tile_of_the_rules(header):
+    """No barrier is armed in an open phase, all copies land before the CTA ends, and few waits run out on the way."""
+    for k in range(128):
+        copied = [bool(k >> i & 1) for i in range(7)]
+        assert tiles_of_a_cta(header, copied, late=None, sees=(True, True)) == 0
+        for late in (i for i in range(7) if copied[i]):
+            for sees in ((True, True), (True, False), (False, True), (False, False)):
+                ran_out = tiles_of_a_cta(header, copied, late, sees)
+                assert ran_out <= 2 and (ran_out > 0 or all(sees))
+    with pytest.raises(AssertionError):                              # going on as if nothing had happened
+        tiles_of_a_cta(header, [True] * 7, 2, (False, False), stops=False)
+
+
+def test_the_rules_stop_their_copies():
+    with open(os.path.join(CSRC, "vp_rules.cu")) as f:
+        source = f.read()
+    assert len(re.findall(r"if \(tid == 0 && arrived[^)]*\)?\)? copy\(", source)) == 2
+    assert "if (staged.bulk && arrived) {" in source and "next_phase(parity, buf ^ 1)" in source

@@ -42,6 +42,7 @@
 #include "vp_gemm_host.cuh"
 #include "vp_launch.h"
 #include "vp_tma.cuh"
+#include "vp_waits.h"
 
 namespace vp {
 
@@ -417,7 +418,7 @@ rules_kernel(const __grid_constant__ RuleKernelArgs a) {
     int64_t r = tile / a.n_slices;
     int slice = (int)(tile - r * a.n_slices);
     const uint64_t policy = policy_evict_first();
-    uint32_t parity = 0u, copied = 0u;                   // bit b: of the phase that buffer b's next copy completes; used
+    uint32_t parity = 0u;                                // next_phase
     bool arrived = true, fresh = true, sorted = false;   // fresh: the CTA's first tile of this row
     int seg0 = 0, seg_to = -1;                           // ... was this slice; row_ids holds ids up to the seg_to-th from it, -1: none
 
@@ -434,11 +435,11 @@ rules_kernel(const __grid_constant__ RuleKernelArgs a) {
             bulk_g2s(to, from, bytes, &sm.full[buf], policy);
         };
         if (kAligned && width == kSlice) {                // whole blocks and no edges
-            if (tid == 0) copy(sm.stage[buf], p, kSlice);
+            if (tid == 0 && arrived) copy(sm.stage[buf], p, kSlice);
             return Staged{0u, true};
         }
         const TileSource<T> t(p, width);
-        if (tid == 0 && t.bulk()) copy(t.at(sm.stage[buf], t.first), t.p + t.first, t.last - t.first);
+        if (tid == 0 && arrived && t.bulk()) copy(t.at(sm.stage[buf], t.first), t.p + t.first, t.last - t.first);
         stage_edges<L>(t, sm.stage[buf]);
         return Staged{t.phase, t.bulk()};
     };
@@ -613,10 +614,17 @@ rules_kernel(const __grid_constant__ RuleKernelArgs a) {
                 mark((uint32_t)l);
             }
         }
-        if (staged.bulk) {
-            if (!mbar_wait(&sm.full[buf], parity >> buf & 1u)) arrived = false;
+        if (staged.bulk && arrived) {
+            if (!mbar_wait(&sm.full[buf], next_phase(parity, buf))) {
+                // Late: flagged, and this thread waits for no later tile. The first one begins no more copies
+                // (the barrier's arrival is spent, its phase open) and sees those under way land before it goes
+                // on, so that the CTA keeps its shared memory until then. What it computes from here on is void.
+                arrived = false;
+                atomicOr(&g_linear_fault, 1u);
+                mbar_wait(&sm.full[buf], next_phase(parity, buf));
+                if (tile + 1 < end && next_staged.bulk) mbar_wait(&sm.full[buf ^ 1], next_phase(parity, buf ^ 1));
+            }
             parity ^= 1u << buf;
-            copied |= 1u << buf;
         }
         if (listed) {
             if (w.mask) {                                 // this thread's mask bits, for the walk
@@ -851,11 +859,6 @@ rules_kernel(const __grid_constant__ RuleKernelArgs a) {
         allow = next_allow;
         staged = next_staged;
         slice = next_slice;
-    }
-    if (!arrived) {                                       // a copy was late: flagged, and awaited once more
-        atomicOr(&g_linear_fault, 1u);
-        for (int b = 0; b < 2; ++b)
-            if (copied >> b & 1u) mbar_wait(&sm.full[b], (parity >> b & 1u) ^ 1u);
     }
 }
 

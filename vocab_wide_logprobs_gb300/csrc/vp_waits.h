@@ -36,4 +36,10 @@ VP_HOST_DEVICE LateStage late_stage(uint32_t stage, uint32_t leader, uint32_t pe
     return LateStage{a == b ? kOwedAll : a > b ? kOwedNoPeer : kOwedNoLeader, (last - 1) & 1u};
 }
 
+// Two buffers that bulk copies fill in turn, each with a barrier of its own: bit b of
+// `parity` is that of the phase which the next wait for buffer b is for, and flips with
+// every wait, whether it ended or ran out. After one that ran out its phase is still
+// open and the arrival on it spent, so no copy may be begun on that barrier again.
+VP_HOST_DEVICE uint32_t next_phase(uint32_t parity, uint32_t b) { return parity >> b & 1u; }
+
 }  // namespace vp
