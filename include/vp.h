@@ -756,9 +756,11 @@ VP_API vp_status vp_download(void *dst_host, const void *src_device, size_t byte
  * and, when `clear` is non-zero, resets it. The word is non-zero only if a
  * kernel's bounded wait on its copy pipeline gave up (bits 0-1: the forward
  * scans' producer / consumers; bits 2-4: the fused-linear GEMMs' and the MXFP4
- * product's producer / MMA / epilogue); that kernel then skipped its outputs and
- * returned instead of spinning. The rules' kernels set bit 0 and go on to their
- * end: their outputs are then not to be used. Unlike every other call, this one synchronises with the device.
+ * product's producer / MMA / epilogue; bit 5: the rules' kernels). Such a kernel
+ * skips the outputs that it has not got the inputs of and returns instead of
+ * spinning; the rules' kernels go on to their end. Either way what the calls of
+ * that kind have written since the word was last read is not to be used. Unlike
+ * every other call, this one synchronises with the device.
  * (No counterpart on the pages: a safety net of this implementation.) */
 VP_API vp_status vp_fault_status(uint32_t *value, int clear);
 

@@ -25,7 +25,8 @@ def header(tmp_path_factory):
                       'extern "C" uint32_t late(uint32_t s, uint32_t a, uint32_t b, uint32_t n) {\n'
                       '    const vp::LateStage l = vp::late_stage(s, a, b, n);\n'
                       '    return l.owed << 1 | l.parity;\n}\n'
-                      'extern "C" uint32_t next(uint32_t p, uint32_t b) { return vp::next_phase(p, b); }\n')
+                      'extern "C" uint32_t next(uint32_t p, uint32_t b) { return vp::next_phase(p, b); }\n'
+                      'extern "C" uint32_t word(uint32_t s, uint32_t l, uint32_t r) { return vp::fault_word(s, l, r); }\n')
     subprocess.run(["g++", "-std=c++17", "-Wall", "-Werror", "-shared", "-fPIC", f"-I{CSRC}", str(source), "-o",
                     str(at / "waits.so")], check=True)
     return ctypes.CDLL(str(at / "waits.so"))
@@ -176,3 +177,12 @@ def test_the_rules_stop_their_copies():
         source = f.read()
     assert len(re.findall(r"if \(tid == 0 && arrived[^)]*\)?\)? copy\(", source)) == 2
     assert "if (staged.bulk && arrived) {" in source and "next_phase(parity, buf ^ 1)" in source
+
+
+def test_the_fault_word_says_whose_outputs_are_void(header):
+    words = {(scans, products, rules): header.word(scans, products, rules)
+             for scans in range(4) for products in range(8) for rules in range(2)}
+    assert len(set(words.values())) == len(words) and words[0, 0, 0] == 0
+    assert words[1, 0, 0] == 1 and words[0, 4, 0] == 16 and words[0, 0, 1] == 32
+    with open(os.path.join(CSRC, "vp_api.cu")) as f:
+        assert "vp::fault_word(" in f.read()

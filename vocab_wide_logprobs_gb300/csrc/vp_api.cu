@@ -11,6 +11,7 @@
 
 #include "vp.h"
 #include "vp_launch.h"
+#include "vp_waits.h"
 
 static_assert(sizeof(vp_rowstat) == 32, "vp_rowstat is 32 bytes");
 static_assert(sizeof(vp_partial) == 40, "vp_partial is 40 bytes");
@@ -590,7 +591,7 @@ vp_status vp_fault_status(uint32_t *value, int clear) {
         vp::read_linear_mxfp4_fault(&d, clear != 0) != cudaSuccess ||
         vp::read_rules_fault(&e, clear != 0) != cudaSuccess)
         return VP_ERR_LAUNCH;
-    *value = a | e | ((b | c | d) << 2);
+    *value = vp::fault_word(a, b | c | d, e);
     return VP_OK;
 }
 

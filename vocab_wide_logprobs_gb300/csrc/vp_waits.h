@@ -42,4 +42,11 @@ VP_HOST_DEVICE LateStage late_stage(uint32_t stage, uint32_t leader, uint32_t pe
 // open and the arrival on it spent, so no copy may be begun on that barrier again.
 VP_HOST_DEVICE uint32_t next_phase(uint32_t parity, uint32_t b) { return parity >> b & 1u; }
 
+// The fault word that a caller reads (vp_fault_status in include/vp.h), of the words of
+// the forward scans, of the matrix products and of the rules' kernels: bits of their
+// own, so that it says whose outputs are void.
+VP_HOST_DEVICE uint32_t fault_word(uint32_t scans, uint32_t products, uint32_t rules) {
+    return scans | products << 2 | (rules ? 32u : 0u);
+}
+
 }  // namespace vp
