@@ -259,6 +259,41 @@ def test_gradients_against_differences():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("V", [5003, 12288])
+def test_a_common_offset_does_not_reach_the_logprob(dtype, V):
+    """Peaked rows of logits around 10^4, temperatures that are no powers of two: the target's ruled logit is rounded
+    where the maximum's is, and what either rounding takes away has to come back.
+
+    Without penalties a column's value before the temperature is exact, so is its distance t to the row's largest, and
+    what is left of the offset is the relative rounding of 1 / T and of the product, twice u of the distances: as in the
+    tolerance above with E_p |t| < log V + 1 < 11, a logprob is off by u (2 (|logp| + 11) + 22 + 4 + 32 + |logp|)."""
+    N = 64
+    g = torch.Generator(device="cuda").manual_seed(V)
+    row = torch.arange(N, device="cuda")
+    x = torch.randn(N, V, generator=g, device="cuda") + 1e4 * (1 - 2 * (row % 2))[:, None]
+    best = torch.randint(0, V, (N,), generator=g, device="cuda")
+    x[row, best] += 30 * torch.rand(N, generator=g, device="cuda")
+    x = x.to(dtype)
+    T = 0.3 + torch.rand(N, generator=g, device="cuda")
+    T[0] = 0.7
+    rules = vp.logits_rules(temperature=T)
+    z = x.double() / T.double()[:, None]
+    lse = torch.logsumexp(z, 1)
+    for targets in (best, torch.randint(0, V, (N,), generator=g, device="cuda"), x.float().argmax(1)):
+        logp, stats = vp.vp_processed_logprobs_fwd(x, rules, targets)
+        lp = z.gather(1, targets[:, None])[:, 0] - lse
+        tol = U * (3 * lp.abs() + 80)
+        assert ((logp.double() - lp).abs() - tol).max() <= 0
+        # the gradient's p of the target is the logprob's
+        dx = vp.vp_processed_logprobs_bwd(x, rules, targets, stats, torch.ones(N, device="cuda")).double()
+        got = dx.gather(1, targets[:, None])[:, 0] * T.double()
+        want = -torch.expm1(lp)
+        tol = torch.exp(lp) * (tol + 8 * U) + (6 * U + half_step(dtype)) * want.abs() + 2.0 ** -126
+        assert ((got - want).abs() - tol).max() <= 0
+
+
+@pytest.mark.gpu
 def test_masked_places_hide_what_they_hold():
     """NaN, infinities and the type's lowest value under the mask change nothing; a row left empty is NaN."""
     N, V = 4, 300

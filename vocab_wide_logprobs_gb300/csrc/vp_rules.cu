@@ -371,7 +371,7 @@ struct RuleSmem {
     uint64_t full[2];
     unsigned long long listed_sum[2][L::kWarps];
     uint32_t touched[L::kWords];
-    float red_top[2][L::kWarps], red_all[2][L::kWarps], red_s[2][L::kWarps], target_z[2];
+    float red_top[2][L::kWarps], red_all[2][L::kWarps], red_s[2][L::kWarps], target_v[2];
     uint32_t n_listed[2];
     int seg_n;                                            // counted slices
     uint32_t seg_first;                                   // row_ids[0] is the id of this number, of the counted ones
@@ -706,7 +706,7 @@ rules_kernel(const __grid_constant__ RuleKernelArgs a) {
                 const float v = listed_value(l, false);
                 if (!(v < pinf())) s = qnan();
                 ltop = fmaxf(ltop, v);
-                if (l == target) sm.target_z[buf] = v * w.inv_t;
+                if (l == target) sm.target_v[buf] = v;
             });
             uint4 u[kVecs];
             auto read = [&](auto whole) {                 // whole: a tile of full width
@@ -786,8 +786,11 @@ rules_kernel(const __grid_constant__ RuleKernelArgs a) {
                     const float d = fmaf(m, w.inv_t, -mz);
                     t *= fabsf(d) < 1e-3f ? fmaf(d, fmaf(0.5f, d, 1.f), 1.f) : expf(d);
                 }
-                a.parts[(int64_t)slice * a.N + r] =
-                    PartialRec{mz, kNegBig, (double)t, 0.0, 0.0, target >= 0 ? sm.target_z[buf] : 0.f, flags};
+                // ... and the target's is kept beside it: without either a common offset of the logits would reach the
+                // logprob (10^4 at a temperature of 0.7: 5e-4)
+                const float v = target >= 0 ? sm.target_v[buf] : 0.f, zt = v * w.inv_t;
+                const float rest = fabsf(zt) < pinf() ? fmaf(v, w.inv_t, -zt) : 0.f;
+                a.parts[(int64_t)slice * a.N + r] = PartialRec{mz, kNegBig, (double)t, 0.0, (double)rest, zt, flags};
             }
         } else {
             T *orow = static_cast<T *>(a.out) + w.out_off + s0;
@@ -874,18 +877,23 @@ rules_join_kernel(const PartialRec *__restrict__ parts, int K, int64_t N, float 
     const int64_t r = (int64_t)blockIdx.x * kJoinWarps + (threadIdx.x >> 5);
     const int lane = threadIdx.x & 31;
     if (r >= N) return;   // warp-uniform
-    float M = kNegBig, zt = 0.f;
+    float M = kNegBig, zt = 0.f, rest = 0.f;             // the target's ruled logit: zt + rest
     uint32_t flags = 0u;
     for (int k = lane; k < K; k += 32) {
         const PartialRec &p = parts[(int64_t)k * N + r];
         M = fmaxf(M, p.m);
         flags |= p.flags;
-        if (p.flags & kPartHasTarget) zt = p.z_t;
+        if (p.flags & kPartHasTarget) {
+            zt = p.z_t;
+            rest = (float)p.W;
+        }
     }
     M = warp_max(M);
     const unsigned holders = __ballot_sync(0xffffffffu, (flags & kPartHasTarget) != 0u);   // one slice at most
     flags = __reduce_or_sync(0xffffffffu, flags);
-    zt = __shfl_sync(0xffffffffu, zt, holders ? __ffs(holders) - 1 : 0);
+    const int holder = holders ? __ffs(holders) - 1 : 0;
+    zt = __shfl_sync(0xffffffffu, zt, holder);
+    rest = __shfl_sync(0xffffffffu, rest, holder);
     double S = 0.0;
     for (int k = lane; k < K; k += 32) {
         const PartialRec &p = parts[(int64_t)k * N + r];
@@ -902,7 +910,7 @@ rules_join_kernel(const PartialRec *__restrict__ parts, int K, int64_t N, float 
     store_rowstat(stats + r, M, log_s, 0.0, rf);
     if (lost && err) atomicOr(err, VP_ERRBIT_TARGET_);
     const bool bad = lost || (rf & (kRowNanInf | kRowEmpty)) != 0u;
-    logp[r] = ignored ? 0.f : bad ? qnan() : (float)(((double)zt - (double)M) - log_s);
+    logp[r] = ignored ? 0.f : bad ? qnan() : (float)(((double)zt - (double)M) + (double)rest - log_s);
 }
 
 // slices (records) of the ruled logprobs' forward
