@@ -627,7 +627,8 @@ VP_API vp_status vp_linear_kl_partial(const void *ha, const void *wa, const void
  *   v in the row's bias list:  z = z + bias(v), the last entry of v counting
  *   z = z / temperature[r]
  *   y = z where the mask allows the column, -inf elsewhere (whatever x holds)
- * in fp32, y rounded once to the dtype of the logits.
+ * in fp32, y rounded once to the dtype of the logits. The quotients are products
+ * with the rounded reciprocals, so they may be off by a step of fp32.
  *   ids, spans  spans[r] = {first, n_prompt, n_total}: row r's history is
  *               ids[first .. first + n_total), the first n_prompt of them the
  *               prompt. Rows may share ids (the rows of a sequence are
@@ -636,7 +637,7 @@ VP_API vp_status vp_linear_kl_partial(const void *ha, const void *wa, const void
  *               skipped. spans NULL: no history.
  *   repetition, frequency, presence, temperature
  *               one float per row, each array NULL for 1, 0, 0 and 1.
- *               repetition and temperature must be finite and > 0.
+ *               repetition and temperature must be finite and at least 2^-127.
  *   bias_*      bias_spans[r] = {first, n}: entries bias_ids[first ..) and
  *               bias_values[first ..). Values may be -inf. NULL: no biases.
  *   mask        n_masks rows of 32-bit words, mask_stride words apart; bit

@@ -365,6 +365,41 @@ def test_rows_out_of_range_are_data_errors(dtype):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("name", ["temperature", "repetition"])
+def test_divisors_whose_reciprocals_do_not_fit_are_data_errors(name, dtype):
+    """The kernels multiply by reciprocals: below 2^-127 these have no room, and 0 times infinity is not 0."""
+    V, least = 200, 2.0 ** -127
+    fine = [least, 2.0 ** -126, 1e-30, 1.0, torch.finfo(torch.float32).max]
+    bad = [least - 2.0 ** -149, 2.0 ** -128, 1e-39, 2.0 ** -149, 0.0, -1.0, math.inf, math.nan]
+    N = len(fine) + len(bad)
+    value = torch.tensor(fine + bad, dtype=torch.float64).float()
+    x = torch.zeros(N, V, dtype=dtype)                                        # all of it is seen: 0 / anything is 0
+    q = dict(ids=torch.arange(V), spans=torch.tensor([[0, 0, V]]).repeat(N, 1), repetition=torch.ones(N))
+    q[name] = value
+    rules, xg, tg = to_gpu(q), x.cuda(), torch.full((N,), 3, device="cuda")
+    seen = []
+
+    def run(call):
+        err = torch.zeros(1, dtype=torch.int32, device="cuda")
+        out = call(err)
+        seen.append(int(err))
+        return out
+
+    ok = torch.tensor([True] * len(fine) + [False] * len(bad), device="cuda")
+    y = run(lambda e: vp.vp_logits_process_fwd(xg, rules, err_word=e))
+    assert torch.isnan(y[~ok]).all() and not y[ok].any()
+    logp, stats = run(lambda e: vp.vp_processed_logprobs_fwd(xg, rules, tg, err_word=e))
+    assert torch.isnan(logp[~ok]).all() and (logp[ok] + math.log(V)).abs().max() <= U * 80
+    run(lambda e: vp.vp_logits_process_bwd(xg, rules, torch.ones_like(xg), err_word=e))
+    # gradients: a small upstream one, so that its product with the reciprocal fits
+    dx = run(lambda e: vp.vp_processed_logprobs_bwd(xg, rules, tg, stats, torch.full((N,), 2.0 ** -20, device="cuda"),
+                                                    err_word=e))
+    assert torch.isnan(dx[~ok]).all() and torch.isfinite(dx[ok]).all()
+    assert seen == [vp.ERRBIT_RULES] * 4
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 def test_rows_do_not_depend_on_the_batch(dtype):
     N, V = 37, 20000
     x, q, targets, grad = make(N, V, dtype, 9, L=60, nb=5, masks=3)

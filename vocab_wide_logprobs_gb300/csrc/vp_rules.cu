@@ -4,9 +4,9 @@
 //
 // Row r, column j (id v = vocab_start + j), c_p and c_o the occurrences of v
 // among the row's prompt and output ids:
-//   z = x;                       c_p + c_o > 0:  z = z > 0 ? z / rep : z * rep
+//   z = x;                       c_p + c_o > 0:  z = z > 0 ? z (1 / rep) : z rep
 //   c_o > 0:  z -= freq c_o + pres;     v in the bias list:  z += bias(v)
-//   y = allowed(j) ? z / T : -inf
+//   y = allowed(j) ? z (1 / T) : -inf
 //   f = dy/dx = allowed(j) ? (c_p + c_o > 0 ? (x > 0 ? 1 / rep : rep) : 1) / T : 0
 //
 // Shape. A tile is a slice of 4096 columns of one row; a CTA works through
@@ -229,6 +229,10 @@ struct RowRules {
     const void *x;
 };
 
+// What z is divided by is multiplied by as its fp32 reciprocal, which has to fit (from
+// 2^-127 on: also its product with log2 e); at most half a step more than a quotient.
+__device__ __forceinline__ bool divisor_ok(float d) { return d >= 0x1p-127f && d < pinf(); }
+
 __device__ __forceinline__ bool span_ok(int64_t first, int64_t n, int64_t total) {
     // n < 2^31: occurrences are counted in 31 bits
     return first >= 0 && n >= 0 && n <= 0x7fffffff && n <= total && first <= total - n;
@@ -249,7 +253,7 @@ __device__ RowRules row_rules(const RuleKernelArgs &a, int64_t r) {
         if (q.repetition) {
             w.rep = q.repetition[r];
             w.inv_rep = 1.f / w.rep;
-            w.ok = w.ok && w.rep > 0.f && w.rep < pinf();
+            w.ok = w.ok && divisor_ok(w.rep);
         }
         if (q.frequency) w.freq = q.frequency[r];
         if (q.presence) w.pres = q.presence[r];
@@ -263,7 +267,7 @@ __device__ RowRules row_rules(const RuleKernelArgs &a, int64_t r) {
     }
     if (q.temperature) {
         const float t = q.temperature[r];
-        w.ok = w.ok && t > 0.f && t < pinf();
+        w.ok = w.ok && divisor_ok(t);
         w.inv_t = 1.f / t;
     }
     if (q.mask) {
