@@ -400,6 +400,38 @@ def test_divisors_whose_reciprocals_do_not_fit_are_data_errors(name, dtype):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_spans_are_checked_without_penalties_too(dtype):
+    """Spans that no penalty reads change nothing, but one that is out of range is a data error all the same."""
+    N, V = 5, 9000
+    x, q, targets, grad = make(N, V, dtype, 41, L=12, drop=("repetition", "frequency", "presence"))
+    xg, tg, gg, dy = x.cuda(), targets.cuda(), grad.cuda(), torch.randn(N, V).to(dtype).cuda()
+
+    def run(rules):
+        err = torch.zeros(1, dtype=torch.int32, device="cuda")
+        logp, stats = vp.vp_processed_logprobs_fwd(xg, rules, tg, err_word=err)
+        errs, outs = [int(err)], [logp]
+        for call in (lambda e: vp.vp_logits_process_fwd(xg, rules, err_word=e),
+                     lambda e: vp.vp_logits_process_bwd(xg, rules, dy, err_word=e),
+                     lambda e: vp.vp_processed_logprobs_bwd(xg, rules, tg, stats, gg, err_word=e)):
+            err.zero_()
+            outs.append(call(err))
+            errs.append(int(err))
+        return outs, errs
+
+    ref, errs = run(vp.logits_rules(temperature=q["temperature"].cuda()))
+    assert errs == [0] * 4
+    got, errs = run(to_gpu(q))
+    assert errs == [0] * 4 and all(torch.equal(a, b) for a, b in zip(got, ref))
+    q["spans"][1] = torch.tensor([q["ids"].numel() - 1, 0, 2])
+    q["spans"][3] = torch.tensor([0, 3, 2])
+    got, errs = run(to_gpu(q))
+    assert errs == [vp.ERRBIT_RULES] * 4
+    for a, b in zip(got, ref):
+        assert torch.isnan(a[[1, 3]]).all() and torch.equal(a[[0, 2, 4]], b[[0, 2, 4]])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 def test_rows_do_not_depend_on_the_batch(dtype):
     N, V = 37, 20000
     x, q, targets, grad = make(N, V, dtype, 9, L=60, nb=5, masks=3)

@@ -205,6 +205,7 @@ struct RuleKernelArgs {
     const float *g;
     PartialRec *parts;
     int32_t *err;
+    bool tabled;              // a penalty reads the ids; without one the spans are only checked
     int row_ids;              // capacity of the list of a row's ids
     bool narrow;              // occurrences counted in 15 bits: fewer ids than that in all
 };
@@ -249,7 +250,7 @@ __device__ RowRules row_rules(const RuleKernelArgs &a, int64_t r) {
         w.ok = span_ok(first, n, q.n_ids) && n_prompt >= 0 && n_prompt <= n;
         w.ids = q.ids + first;
         w.n_prompt = (uint32_t)n_prompt;
-        w.n_total = (uint32_t)n;
+        w.n_total = a.tabled ? (uint32_t)n : 0u;
         if (q.repetition) {
             w.rep = q.repetition[r];
             w.inv_rep = 1.f / w.rep;
@@ -393,12 +394,12 @@ rules_kernel(const __grid_constant__ RuleKernelArgs a) {
                   kWords = L::kWords, kWarps = L::kWarps;
     RuleSmem<L> &sm = *reinterpret_cast<RuleSmem<L> *>(smem_raw);
     uint32_t *const counts = reinterpret_cast<uint32_t *>(smem_raw + sizeof(RuleSmem<L>));
-    uint32_t *const entries = counts + (a.q.spans ? a.narrow ? kSlice / 2 : kSlice : 0);
+    uint32_t *const entries = counts + (a.tabled ? a.narrow ? kSlice / 2 : kSlice : 0);
     // column of the slice, bit 15: prompt
     uint16_t *const row_ids = reinterpret_cast<uint16_t *>(entries + (a.q.bias_spans ? kSlice : 0));
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint8_t *const touched8 = reinterpret_cast<const uint8_t *>(sm.touched);
-    const bool tabled = a.q.spans != nullptr, biased = a.q.bias_spans != nullptr;
+    const bool biased = a.q.bias_spans != nullptr;
 
     // the tables are cleared once; a tile clears what it touched
     for (int i = tid; i < kWords; i += kThreads) sm.touched[i] = 0u;
@@ -672,7 +673,7 @@ rules_kernel(const __grid_constant__ RuleKernelArgs a) {
         // v before the temperature, and f, of a listed column l from x; clears the column's entries if told to
         auto ruled = [&](int l, float x, float &f, bool last) {
             uint32_t c = 0u;
-            if (tabled) {
+            if (a.tabled) {
                 if (a.narrow) {
                     uint16_t *const h = reinterpret_cast<uint16_t *>(counts) + l;
                     c = (*h & 0x7fffu) | (uint32_t)(*h >> 15) << 31;
@@ -931,14 +932,14 @@ static cudaError_t launch_rules_t(RuleKernelArgs k, cudaStream_t stream) {
     k.n_slices = ((int64_t)k.V + L::kWidth - 1) / L::kWidth;
     // fewer than 2^15 ids in all (a training batch's sequences): no id occurs more often
     k.narrow = k.q.n_ids < 0x8000;
-    const int tables = (k.q.spans ? k.narrow ? 1 : 2 : 0) + (k.q.bias_spans ? 3 : 0);
+    const int tables = (k.tabled ? k.narrow ? 1 : 2 : 0) + (k.q.bias_spans ? 3 : 0);
     // Room for the average row's ids: long histories take shared memory from other CTAs, but going
     // through 16384 ids for every slice takes longer than the slice.
     int step = 0;
-    if (k.q.spans)
+    if (k.tabled)
         while (step < 4 && (int64_t)(kRowIdsLeast << step) * k.N < k.q.n_ids) ++step;
     static_assert(kRowIdsLeast << 4 == kRowIdsMost, "five capacities");
-    k.row_ids = k.q.spans ? kRowIdsLeast << step : 0;
+    k.row_ids = k.tabled ? kRowIdsLeast << step : 0;
     auto bytes = [](int tables, int ids) {
         return (int)sizeof(RuleSmem<L>) + (tables % 3) * L::kWidth * 2 + (tables / 3) * L::kWidth * 4 + ids * 2;
     };
@@ -985,10 +986,10 @@ static cudaError_t launch_rules_t(const RuleKernelArgs &k, cudaStream_t stream) 
         cudaError_t e = cudaGetDevice(&dev);
         if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
         if (e != cudaSuccess) return e;
-        if (k.q.spans && k.N <= sms / rule_slices(k.V))
+        if (k.tabled && k.N <= sms / rule_slices(k.V))
             return aligned ? launch_rules_t<T, kOp, kRuleThreadsFew, true>(k, stream)
                            : launch_rules_t<T, kOp, kRuleThreadsFew, false>(k, stream);
-        if (k.q.spans && k.q.n_ids > Tile<T, kRuleThreads>::kWidth * k.N)
+        if (k.tabled && k.q.n_ids > Tile<T, kRuleThreads>::kWidth * k.N)
             return aligned ? launch_rules_t<T, kOp, kRuleThreadsLong, true>(k, stream)
                            : launch_rules_t<T, kOp, kRuleThreadsLong, false>(k, stream);
     }
@@ -1000,9 +1001,8 @@ template <int kOp>
 static cudaError_t launch_rules(const RuleArgs &a) {
     RuleKernelArgs k{a.x, a.dy, a.out, a.N, 0, a.vocab_start, (int)a.V, Rows{a.R, a.s_o, a.s_i},
                      Rows{a.R, a.out_s_o, a.out_s_i}, a.rules, a.targets, static_cast<const RowStat *>(a.stats), a.g,
-                     static_cast<PartialRec *>(a.parts), a.err, 0, false};
-    // no rule that reads the ids: the spans are not looked at
-    if (!k.q.repetition && !k.q.frequency && !k.q.presence) k.q.spans = nullptr;
+                     static_cast<PartialRec *>(a.parts), a.err,
+                     a.rules.spans && (a.rules.repetition || a.rules.frequency || a.rules.presence), 0, false};
     return a.bf16 ? launch_rules_t<__nv_bfloat16, kOp>(k, a.stream) : launch_rules_t<float, kOp>(k, a.stream);
 }
 
