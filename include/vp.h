@@ -646,7 +646,9 @@ VP_API vp_status vp_linear_kl_partial(const void *ha, const void *wa, const void
  *               uses mask row r (n_masks >= N). mask NULL: all allowed.
  * A row whose spans, mask row, repetition or temperature are out of range is a
  * data error: its outputs (and gradients) are NaN and VP_ERRBIT_RULES is OR-ed
- * into *err_word; nothing outside the arrays is read. */
+ * into *err_word; nothing outside the arrays is read. (A row without a target
+ * has no logprob to be wrong: its logp stays 0 and its gradient a zero row, as
+ * for a NaN row of vp_logprobs_fwd; the bit is set all the same.) */
 typedef struct vp_logits_rules {
     const int64_t *ids;
     int64_t n_ids;

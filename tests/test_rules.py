@@ -432,6 +432,30 @@ def test_spans_are_checked_without_penalties_too(dtype):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_rows_without_a_target_are_zero_whatever_their_rules(dtype):
+    """Padding: a negative target with NaN logits or rules out of range gives 0 and a zero row, as in the plain logprobs."""
+    N, V = 6, 5000
+    x, q, targets, grad = make(N, V, dtype, 43, L=12)
+    targets[1:5] = -1
+    q["temperature"][1], q["repetition"][2], q["spans"][3, 0] = 0.0, math.nan, -4
+    x[4, 17] = math.nan
+    rules, xg, tg = to_gpu(q), x.cuda(), targets.cuda()
+    for call, bit in ((lambda e: vp.vp_processed_logprobs_fwd(xg, rules, tg, err_word=e), vp.ERRBIT_RULES),
+                      (lambda e: vp.vp_logprobs_fwd(xg, tg, err_word=e), 0)):
+        err = torch.zeros(1, dtype=torch.int32, device="cuda")
+        logp, stats = call(err)
+        assert int(err) == bit and not logp[1:5].any() and torch.isfinite(logp[[0, 5]]).all()
+        if bit:
+            err.zero_()
+            dx = vp.vp_processed_logprobs_bwd(xg, rules, tg, stats, grad.cuda(), err_word=err)
+            assert int(err) == bit
+        else:
+            dx = vp.vp_logprobs_bwd(xg, tg, stats, grad.cuda())
+        assert not dx[1:5].any() and torch.isfinite(dx[[0, 5]]).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 def test_rows_do_not_depend_on_the_batch(dtype):
     N, V = 37, 20000
     x, q, targets, grad = make(N, V, dtype, 9, L=60, nb=5, masks=3)
