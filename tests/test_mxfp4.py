@@ -241,6 +241,32 @@ def test_streams_and_graphs():
     assert torch.equal(out, want) and vp.vp_fault_status() == 0
 
 
+@pytest.mark.gpu
+@pytest.mark.slow
+@pytest.mark.parametrize("shape", [(1, 2 ** 31 - 100), (2 ** 31 - 100, 1)])
+def test_as_many_rows_as_the_calls_take(shape):
+    """Row counts that a tile's worth more would carry past 31 bits, of W for single CTAs and of x for the pairs."""
+    N, V = shape
+    if torch.cuda.mem_get_info()[0] < 100 << 30:
+        pytest.skip("needs 100 GB")
+    few = product_case(1, 1, 64, seed=1)
+    long, short = torch.zeros(2 ** 31 - 100, 32, dtype=torch.uint8, device="cuda"), gpu(few)[:2]
+    scales = torch.full((vp.vp_mxfp4_scale_bytes(2 ** 31 - 100, 64),), 127, dtype=torch.uint8, device="cuda")
+    at = torch.tensor([0, 127, 128, 2 ** 30 + 3, 2 ** 31 - 356, 2 ** 31 - 129, 2 ** 31 - 101], device="cuda")
+    long[at] = torch.randint(0, 256, (at.numel(), 32), dtype=torch.uint8, device="cuda")
+    y = torch.full((N, V), math.nan, dtype=torch.bfloat16, device="cuda")
+    big = (long, scales)
+    args = (*short, *big) if N == 1 else (*big, *short)
+    vp.vp_linear_mxfp4_fwd(*args, y=y)
+    y = y.view(-1)
+    codes = torch.stack((long[at] % 16, long[at] // 16), 2).view(-1, 64).cpu().long()
+    values = plain_values(codes, torch.full((at.numel(), 2), 127)) @ plain_values(*few[0])[0]
+    assert (y[at].cpu().double() - values).abs().max() <= 2.0 ** -8 * values.abs().max() + 3 * 2.0 ** -23 * 36 * 64 * 8
+    y[at] = 0
+    assert not y.any()
+    assert vp.vp_fault_status() == 0
+
+
 # ---------------------------------------------------------------------------
 # refusals (CPU)
 # ---------------------------------------------------------------------------

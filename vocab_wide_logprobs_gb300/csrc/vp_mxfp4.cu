@@ -368,7 +368,7 @@ linear_mxfp4_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_const
     __shared__ Mxfp4Bars<kNT> bars;
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int n_vb = (V + kXM - 1) / kXM, n_tb = (N + kNT - 1) / kNT;
+    const int n_vb = (V - 1) / kXM + 1, n_tb = (N - 1) / kNT + 1;   // N and V have up to 31 bits
     const int64_t n_tiles = (int64_t)n_vb * n_tb;
     const int n_k = (D + kXK - 1) / kXK, n_kt = (D + 127) / 128;
 
@@ -580,7 +580,7 @@ linear_mxfp4_pair_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_rank();
-    const int n_vp = (V + 2 * kXM - 1) / (2 * kXM), n_tb = (N + kYT - 1) / kYT;
+    const int n_vp = (V - 1) / (2 * kXM) + 1, n_tb = (N - 1) / kYT + 1;   // N and V have up to 31 bits
     const int64_t n_tiles = (int64_t)n_vp * n_tb, pair = blockIdx.x >> 1, n_pairs = gridDim.x >> 1;
     const int n_k = (D + kXK - 1) / kXK, n_kt = (D + 127) / 128;
 
