@@ -83,15 +83,16 @@ __device__ __forceinline__ float to_float(__nv_bfloat16 v) { return __bfloat162f
 
 // The CTAs of an SM that the registers are held to, and the pairs of ids of a thread on
 // their way at once. Together they decide what registers a kernel comes out with, and
-// so how many CTAs run: measured op by op (8192 x 75968 bf16 with 1000 ids a row, us:
-// ruled logprobs' forward with 6 pairs 587, 5 601, 7 706, 8 619; backward with 2 pairs
-// and 7 CTAs 511, 4 and 7 517, 3 and 5 543, 2 and 5 575. 1024 x 75967, processing with
-// 6 pairs 110, 8 116, 5 125).
-template <typename T, int kOp, int kN> constexpr int rule_ctas() {
-    return kOp == kLogpBwd && sizeof(T) == 2 ? 7 : Tile<T, kN>::kCtas;
+// so how many CTAs run: measured op by op, and again whenever the kernel changes. The
+// ruled logprobs' backward (8192 x 75968 bf16 with 1000 ids a row, us): 7 CTAs and 3
+// pairs 513, 2 pairs 525, 4 547; 6 and 2 546; 5 and 2 556. Off the boundaries (1024 x
+// 75967): 5 and 2 143, 7 and 2 155, 7 and 3 159. Processing there: 5 and 6 114, with 3
+// to 5 pairs or 6 to 7 CTAs 136 to 142.
+template <typename T, int kOp, int kN, bool kAligned> constexpr int rule_ctas() {
+    return kOp == kLogpBwd && sizeof(T) == 2 && kAligned ? 7 : Tile<T, kN>::kCtas;
 }
-template <int kOp, int kN> constexpr uint32_t rule_pairs() {
-    return kN > kRuleThreads || kOp == kProcBwd ? 8 : kOp == kLogpBwd ? 2 : 6;
+template <int kOp, int kN, bool kAligned> constexpr uint32_t rule_pairs() {
+    return kN > kRuleThreads || kOp == kProcBwd ? 8 : kOp == kLogpBwd ? kAligned ? 3 : 2 : 6;
 }
 
 // Orders this thread's earlier stores to shared memory before later bulk copies there.
@@ -386,7 +387,7 @@ struct RuleSmem {
 };
 
 template <typename T, int kOp, int kN, bool kAligned>
-__global__ void __launch_bounds__(Tile<T, kN>::kThreads, (rule_ctas<T, kOp, kN>()))
+__global__ void __launch_bounds__(Tile<T, kN>::kThreads, (rule_ctas<T, kOp, kN, kAligned>()))
 rules_kernel(const __grid_constant__ RuleKernelArgs a) {
     extern __shared__ __align__(16) uint8_t smem_raw[];
     using L = Tile<T, kN>;
@@ -505,7 +506,7 @@ rules_kernel(const __grid_constant__ RuleKernelArgs a) {
                 const uint64_t l = id - base;             // negative ids come out far above any reach
                 if (l < reach) f((uint32_t)l, i);
             };
-            constexpr uint32_t kUnroll = rule_pairs<kOp, kN>();
+            constexpr uint32_t kUnroll = rule_pairs<kOp, kN, kAligned>();
             const ulonglong2 *const p = reinterpret_cast<const ulonglong2 *>(w.ids + head);
 #pragma unroll 1
             for (uint32_t i0 = tid; i0 < pairs; i0 += kUnroll * kThreads) {
