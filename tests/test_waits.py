@@ -94,20 +94,17 @@ def test_the_stage_that_is_waited_for_is_among_them(header):
     assert header.late(2, 8, 9, 6) >> 1 == NO_LEADER and header.late(2, 9, 8, 6) >> 1 == NO_PEER
 
 
-def test_the_kernels_with_rings_ask():
-    """The MXFP4 product, of one CTA and of pairs: on every way out."""
-    with open(os.path.join(CSRC, "vp_mxfp4.cu")) as f:
-        kernels = f.read().split("template <int kNT, typename T>\n__global__")[1].split("template <typename T>\n__global__")
-    for kernel in kernels:
-        assert "late_stage(" in kernel and "bars.done" in kernel
-
-
-def test_a_part_of_a_tile_is_not_handed_to_the_epilogue():
-    """A stage that never came ends the MMAs of its tile: the accumulator is announced only when it is whole."""
-    with open(os.path.join(CSRC, "vp_mxfp4.cu")) as f:
-        lines = [line.split("//")[0].strip() for line in f]
-    at = [i for i, line in enumerate(lines) if re.match(r"umma_commit(_pair)?\(&bars\.acc_full", line)]
-    assert len(at) == 2 and all(lines[i - 1] == "if (!ok) break;" for i in at)
+@pytest.mark.parametrize("name", ["vp_mxfp4.cu", "vp_gemm.cuh"])
+def test_the_kernels_with_rings_ask(name):
+    """The products of one CTA and of pairs, on every way out; and an accumulator is announced only when it is whole."""
+    with open(os.path.join(CSRC, name)) as f:
+        single, pair = re.split(r"\n\w*_pair_kernel\(const", f.read())
+    assert "late_stage(" in single and "umma_commit(&bars.done);" in single
+    assert "pair_ring_used<" in pair and "pair_ends<" in pair and "umma_commit_pair_here(&bars.done);" in pair
+    for kernel in (single, pair):
+        lines = [line.split("//")[0].strip() for line in kernel.splitlines()]
+        at = [i for i, line in enumerate(lines) if re.match(r"umma_commit(_pair)?\(&bars\.acc_full", line)]
+        assert len(at) == 1 and lines[at[0] - 1] == "if (!ok) break;"
 
 
 def tiles_of_a_cta(header, copied, late, sees, stops=True):

@@ -15,7 +15,9 @@
 #include "vp_device.cuh"
 #include "vp_gemm_host.cuh"
 #include "vp_launch.h"
+#include "vp_pair.cuh"
 #include "vp_umma.cuh"
+#include "vp_waits.h"
 
 namespace vp {
 
@@ -31,7 +33,7 @@ constexpr int kDualEpiCols = 128;
 constexpr uint32_t kLTmemCols = 2 * kLBN;          // two accumulators
 
 struct LinearBars {
-    uint64_t full[kLStages], empty[kLStages], acc_full[2], acc_empty[2];
+    uint64_t full[kLStages], empty[kLStages], acc_full[2], acc_empty[2], done;   // done: every MMA
     uint32_t tmem_base;
 };
 
@@ -88,6 +90,7 @@ umma_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant
             mbar_init(&bars.acc_full[b], 1);
             mbar_init(&bars.acc_empty[b], kLThreads - 64);   // every epilogue thread
         }
+        mbar_init(&bars.done, 1);
         fence_mbar_init();
         prefetch_tensormap(&tm_a);
         prefetch_tensormap(&tm_b);
@@ -134,6 +137,11 @@ umma_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant
                     }
                 }
             }
+            // every copy lands before the CTA gives up its shared memory, whoever gave up
+            for (uint32_t i = 0; i < (uint32_t)kLStages; ++i) {
+                const LateStage l = late_stage(i, it, it, kLStages);
+                if (l.owed != kOwedNothing && !mbar_wait(&bars.full[i], l.parity)) { ok = false; break; }
+            }
             if (!ok) atomicOr(&g_linear_fault, 1u);
         }
     } else if (warp == 1) {
@@ -163,8 +171,11 @@ umma_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant
                     }
                     umma_commit(&bars.empty[st]);       // frees the stage once these MMAs are done
                 }
+                if (!ok) break;                         // a part of a tile is no tile
                 umma_commit(&bars.acc_full[buf]);       // the accumulator is complete
             }
+            umma_commit(&bars.done);                    // tensor memory is given back after the last MMA
+            if (!mbar_wait(&bars.done, 0)) ok = false;
             if (!ok) atomicOr(&g_linear_fault, 2u);
         }
     } else {
@@ -236,8 +247,8 @@ constexpr int kPStageBytes = kPAStage + kPBStage;       // 32 KB
 constexpr int kPSmemBytes = kPStages * kPStageBytes + 1024;
 
 struct PairBars {
-    uint64_t full[kPStages], empty[kPStages], acc_full[2], acc_empty[2];
-    uint32_t tmem_base;
+    uint64_t full[kPStages], empty[kPStages], acc_full[2], acc_empty[2], done;
+    uint32_t tmem_base, fills, gave_up;
 };
 
 constexpr int kPairDualRegsLaunch = 168, kPairDualRegsLow = 56, kPairDualRegsHigh = 224;
@@ -274,6 +285,8 @@ umma_gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_con
             mbar_init(&bars.acc_full[b], 1);
             mbar_init(&bars.acc_empty[b], 2 * kEpiThreads);   // the epilogue threads of both CTAs
         }
+        mbar_init(&bars.done, 1);
+        bars.gave_up = 0u;
         fence_mbar_init();
         prefetch_tensormap(&tm_a);
         prefetch_tensormap(&tm_b);
@@ -328,7 +341,8 @@ umma_gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_con
                     }
                 }
             }
-            if (!ok) atomicOr(&g_linear_fault, 1u);
+            bars.fills = it;
+            if (!ok || !pair_ring_used<kPStages>(bars, it)) pair_gives_up(bars, 1u);
         }
     } else if (warp == 1) {
         // ---------------- MMA issuer (leader only) ----------------
@@ -361,10 +375,13 @@ umma_gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_con
                         }
                         umma_commit_pair(&bars.empty[st]);   // frees the stage in both CTAs
                     }
+                    if (!ok) break;                          // a part of a tile is no tile
                     umma_commit_pair(&bars.acc_full[buf]);   // the accumulator (product) is complete
                 }
             }
-            if (!ok) atomicOr(&g_linear_fault, 2u);
+            umma_commit_pair_here(&bars.done);               // tensor memory is given back after the last MMA
+            if (!mbar_wait(&bars.done, 0)) ok = false;
+            if (!ok) pair_gives_up(bars, 2u);
         }
     }
     } else {
@@ -385,7 +402,7 @@ umma_gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_con
                 const int ncol = min(kDualEpiCols, Nn - c0);
                 if (ok && !mbar_wait_cluster(&bars.acc_full[0], j & 1)) {
                     ok = false;
-                    atomicOr(&g_linear_fault, 4u);
+                    pair_gives_up(bars, 4u);
                 }
                 tc_fence_after();
                 const uint32_t ta = tmem + half * kDualEpiCols + lanes;
@@ -395,7 +412,7 @@ umma_gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_con
                 mbar_arrive_cluster(cluster_addr(&bars.acc_empty[0], 0));   // the next first product may start
                 if (ok && !mbar_wait_cluster(&bars.acc_full[1], j & 1)) {
                     ok = false;
-                    atomicOr(&g_linear_fault, 4u);
+                    pair_gives_up(bars, 4u);
                 }
                 tc_fence_after();
                 if (__all_sync(0xffffffffu, ok) && ncol > 0) epi(mb * kLBM + r_in, c0, ncol, x, ta + kLBN);
@@ -405,7 +422,7 @@ umma_gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_con
                 const uint32_t buf = j & 1;
                 if (ok && !mbar_wait_cluster(&bars.acc_full[buf], (j >> 1) & 1)) {
                     ok = false;
-                    atomicOr(&g_linear_fault, 4u);
+                    pair_gives_up(bars, 4u);
                 }
                 tc_fence_after();
                 if (__all_sync(0xffffffffu, ok))
@@ -417,7 +434,7 @@ umma_gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_con
     }
     tc_fence_before();
     __syncthreads();
-    cluster_sync();                                      // no arrival or copy still targets either CTA
+    pair_ends<kPStages, kPStageBytes>(bars, rank);
     tc_fence_after();
     if (warp == 1) tmem_dealloc_pair(tmem, kLTmemCols);
 }

@@ -15,6 +15,7 @@
 #include "vp_device.cuh"
 #include "vp_gemm_host.cuh"
 #include "vp_launch.h"
+#include "vp_pair.cuh"
 #include "vp_umma.cuh"
 #include "vp_waits.h"
 
@@ -523,30 +524,9 @@ constexpr int kYOverlap = kYT - (int)kYAcc1;
 static_assert(kYAcc1 == 112 && kYOverlap == 144, "the epilogue's reads are written for these");
 
 struct PairMxfp4Bars {
-    uint64_t full[kYStages], empty[kYStages], acc_full[2], shared_free, done;   // done: every MMA (leader's)
-    uint32_t tmem_base;
-    uint32_t fills;                                       // stages that this CTA has filled
-    uint32_t gave_up;                                     // a wait of either CTA ran out; the same in both at the end
+    uint64_t full[kYStages], empty[kYStages], acc_full[2], shared_free, done;
+    uint32_t tmem_base, fills, gave_up;
 };
-
-// A bounded wait ran out: flagged for the host and, before they leave, for both CTAs.
-__device__ __forceinline__ void pair_gives_up(PairMxfp4Bars &bars, uint32_t bit) {
-    atomicOr(&g_linear_fault, bit);
-    st_cluster_u32(cluster_addr(&bars.gave_up, 0), 1u);
-    st_cluster_u32(cluster_addr(&bars.gave_up, 1), 1u);
-}
-
-// Then the leader waits for the copies of both CTAs that are still under way.
-__device__ __forceinline__ void pair_drain(PairMxfp4Bars &bars) {
-    const uint32_t peer = ld_cluster_u32(cluster_addr(&bars.fills, 1));
-    for (uint32_t i = 0; i < (uint32_t)kYStages; ++i) {
-        const LateStage l = late_stage(i, bars.fills, peer, kYStages);
-        if (l.owed == kOwedNothing) continue;
-        if (l.owed == kOwedNoPeer) mbar_complete_tx(&bars.full[i], kYStageBytes);
-        if (l.owed == kOwedNoLeader) mbar_arrive_expect_tx(&bars.full[i], kYStageBytes);
-        if (!mbar_wait_cluster(&bars.full[i], l.parity)) break;
-    }
-}
 
 __device__ __forceinline__ void umma_mxf4_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
                                                uint32_t sfa, uint32_t sfb, uint32_t accumulate) {
@@ -557,12 +537,6 @@ __device__ __forceinline__ void umma_mxf4_pair(uint32_t d_tmem, uint64_t adesc, 
             d_tmem),
         "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
         : "memory");
-}
-
-// Arrive once on a barrier of this CTA when the pair MMAs issued so far by this thread have completed.
-__device__ __forceinline__ void umma_commit_pair_here(uint64_t *bar) {
-    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
-                 : "memory");
 }
 
 // In both CTAs, from the same place of each one's shared memory.
@@ -631,13 +605,8 @@ linear_mxfp4_pair_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_
                     tma_load_2d_pair(sb + kXSStage, &tm_xs, kb * (kXSStage / 4), 2 * tb + 1, fb, keep);
                 }
             }
-            // every stage is used before the CTA leaves: its copies have landed, and the arrival that says so
-            for (uint32_t i = 0; i < (uint32_t)kYStages && ok; ++i) {
-                const LateStage l = late_stage(i, fills, fills, kYStages);
-                if (l.owed != kOwedNothing && !mbar_wait_cluster(&bars.empty[i], l.parity)) ok = false;
-            }
             bars.fills = fills;
-            if (!ok) pair_gives_up(bars, 1u);
+            if (!ok || !pair_ring_used<kYStages>(bars, fills)) pair_gives_up(bars, 1u);
         }
     } else if (warp == 1) {
         // ---------------- MMA issuer (leader only) ----------------
@@ -739,12 +708,7 @@ linear_mxfp4_pair_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_
     }
     tc_fence_before();
     __syncthreads();
-    cluster_sync();                                      // no arrival or copy still targets either CTA,
-    if (bars.gave_up) {                                  // but where a wait ran out
-        if (rank == 0 && threadIdx.x == 0) pair_drain(bars);
-        __syncthreads();
-        cluster_sync();
-    }
+    pair_ends<kYStages, kYStageBytes>(bars, rank);
     tc_fence_after();
     if (warp == 1) tmem_dealloc_pair(tmem, 512);
 }
