@@ -1,6 +1,6 @@
-// vp_gemm_host.cuh -- what the translation units with tensor-core kernels share
-// on the host: the fault word of their bounded waits and the driver's tensor-map
-// encoder.
+// vp_gemm_host.cuh -- what the translation units with tensor-core kernels and the
+// rules' share: the fault word of their bounded waits, and on the host the driver's
+// tensor-map encoder.
 #pragma once
 
 #include <cuda.h>
@@ -12,7 +12,7 @@
 
 namespace vp {
 
-// Set when a bounded wait of the linear kernels gave up.
+// Set when a bounded wait of this translation unit's kernels gave up.
 static __device__ uint32_t g_linear_fault;   // one per translation unit
 
 // Reads (and optionally clears) this translation unit's fault word.

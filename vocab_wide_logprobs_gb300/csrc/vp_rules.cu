@@ -50,13 +50,11 @@ constexpr uint32_t kPromptBit = 0x80000000u;
 
 enum RuleOp { kProcFwd = 0, kProcBwd = 1, kLogpFwd = 2, kLogpBwd = 3 };
 
-// A tile's threads and size. Measured on GB300 at 8192 x 75968 bf16 with 1000 ids a
-// row (us, forward / backward of the ruled logprobs): now 587 / 511. Compared with 16
-// ids of a thread on their way in both: five CTAs an SM 584 / 562, four 720 / 575, six
-// 673 / 570, seven 675 / 554. Five is what the registers are held to; the kernels come
-// out with fewer and run up to seven. Tiles of 8192 columns with four CTAs took 1.37
-// and 1.16 times as long. fp32, 1024 rows: four CTAs 134 / 123, three 149 / 134, five
-// 145 / 128.
+// A tile's threads and size. Five CTAs an SM (fp32: four) are what the registers are
+// held to; the kernels come out with fewer and run up to eight. Ruled logprobs' forward
+// on GB300, us, 8192 x 75968 bf16 with 1000 ids a row: five 591, four 710, six 679,
+// seven and eight 691; 1024 x 75968 fp32: four 136, three 153, five 151. (Tiles of 8192
+// columns, tried when the kernel was new, took 1.37 times as long.)
 template <typename E, int kN> struct Tile {
     using T = E;
     static constexpr int kThreads = kN, kWarps = kThreads / 32;
@@ -225,8 +223,8 @@ struct RowRules {
     bool nan_row;             // the row's outputs are NaN
     float m, log_s, scale;    // logprobs backward: log p = (v / T - m) - log_s; scale = -g / T. Elsewhere scale = 1 / T
     // The row's first element in x and in the output: offsets from the kernel's arguments, so that the
-    // compiler sees global memory. The ruled logprobs' forward keeps an address of x instead: 71
-    // registers rather than 96, 8192 x 75968 bf16 in 585 us rather than 705.
+    // compiler sees global memory. The ruled logprobs' forward keeps an address of x instead: off the
+    // boundaries 64 registers rather than 96, 1024 x 75967 bf16 in 108 us rather than 126 (at them the same).
     int64_t x_off, out_off;
     const void *x;
 };
@@ -973,10 +971,10 @@ static bool rows_aligned(const void *p, int64_t N, const Rows &rows) {
 
 // Rows that all begin at 16-byte boundaries have a kernel of their own, without the
 // shifts and with no check per vector in tiles of full width (us, 8192 x 75968 bf16
-// with 1000 ids a row, forward / backward of the ruled logprobs, 16 ids of a thread on
-// their way in both: 584 / 562; with a check per vector 605 / 628, with the choice
-// made tile by tile in one kernel 648 / 632). 1024 x 75967, off the boundaries: 104 /
-// 161, in one kernel 110 / 152; now 107 / 149.
+// with 1000 ids a row, forward / backward of the ruled logprobs: 591 / 513; when the
+// kernel was split, with 16 ids of a thread on their way, 584 / 562 against 605 / 628
+// with a check per vector and 648 / 632 with the choice made tile by tile in one
+// kernel). 1024 x 75968 and 75967, the latter off the boundaries: 89 / 77 and 108 / 143.
 template <typename T, int kOp>
 static cudaError_t launch_rules_t(const RuleKernelArgs &k, cudaStream_t stream) {
     const Rows packed{1, k.V, 0};
