@@ -743,6 +743,105 @@ VP_API vp_status vp_linear_mxfp4_fwd(const uint8_t *x_codes, const uint8_t *x_sc
                                      vp_stream stream);
 
 /* ------------------------------------------------------------------------ */
+/* Softmax cross entropy as a training loss: label smoothing, z-loss and      */
+/* soft-capped logits (no counterpart on the pages: the loss of the same      */
+/* softmax that logprobs, entropy and KL are taken of)                        */
+/* ------------------------------------------------------------------------ */
+/* For row r with logits x and target t:
+ *   z_j  = x_j, or softcap tanh(x_j / softcap) where softcap > 0
+ *   lse  = log sum_j exp(z_j)
+ *   loss = lse - (1 - label_smoothing) z_t - label_smoothing mean_j(z_j) + z_loss lse^2
+ *   dx_j = grad_out (p_j (1 + 2 z_loss lse) - (1 - label_smoothing) [j = t] - label_smoothing / V)
+ *          (1 - (z_j / softcap)^2),   p = softmax(z)
+ * in fp32 (the row's finish in fp64), loss as fp32 [N]. label_smoothing in [0, 1],
+ * z_loss in [0, 1e30], softcap 0 (none) or in [1e-30, 1e30]; others: VP_ERR_ARG.
+ * Targets, records and data errors as vp_logprobs_fwd: a negative target gives loss 0
+ * and a zero gradient row, one outside the shard NaN and VP_ERRBIT_TARGET. A NaN logit
+ * gives NaN, and without a cap +inf and an all -inf row do too; a capped logit of +-inf is
+ * +-softcap, with gradient 0. A masked (-inf) column has p = 0; with label smoothing it makes
+ * the loss +inf, while the gradient stays that of the formula. workspace: 8-byte aligned,
+ * vp_cross_entropy_workspace_size(N, V) bytes. A row's result does not depend on N. */
+VP_API size_t vp_cross_entropy_workspace_size(int64_t N, int64_t V);
+VP_API vp_status vp_cross_entropy_fwd(const void *x, int dtype, int64_t N, int64_t V, int64_t R, int64_t s_o,
+                                      int64_t s_i, int64_t vocab_start, double label_smoothing, double z_loss,
+                                      double softcap, const int64_t *targets, float *loss, vp_rowstat *stats,
+                                      void *workspace, size_t workspace_bytes, int32_t *err_word, vp_stream stream);
+
+/* The gradient with respect to x from the forward's records, with the forward's options. dx
+ * contiguous [N, V] in the dtype of x; dx may be x when x is contiguous, and must not overlap it
+ * otherwise. vocab_total: columns of the whole vocabulary where x is a shard of it and the
+ * records come from vp_cross_entropy_merge; 0 for V, else at least V (VP_ERR_SHAPE). */
+VP_API vp_status vp_cross_entropy_bwd(const void *x, int dtype, int64_t N, int64_t V, int64_t R, int64_t s_o,
+                                      int64_t s_i, int64_t vocab_start, int64_t vocab_total, double label_smoothing,
+                                      double z_loss, double softcap, const int64_t *targets, const vp_rowstat *stats,
+                                      const float *grad_out, void *dx, int32_t *err_word, vp_stream stream);
+
+/* The shard's records for a vocabulary split over shards (the flow of the sharded forms above):
+ * vp_partial with m, S, z_t and flags as vp_logprobs_partial over z, W = sum_j (z_j - m) and
+ * S_b = the shard's number of columns. parts 8-byte aligned, workspace as the forward's. */
+VP_API vp_status vp_cross_entropy_partial(const void *x, int dtype, int64_t N, int64_t V, int64_t R, int64_t s_o,
+                                          int64_t s_i, int64_t vocab_start, double softcap, const int64_t *targets,
+                                          vp_partial *parts, void *workspace, size_t workspace_bytes,
+                                          vp_stream stream);
+
+/* Merges K >= 1 shards' records (K * N, shard-major) into the losses and records of the whole
+ * rows; targets' errors and VP_ROW_SHARDED as vp_logprobs_merge. The shards hold below 2^32
+ * columns together. */
+VP_API vp_status vp_cross_entropy_merge(const vp_partial *parts, int64_t K, int64_t N, double label_smoothing,
+                                        double z_loss, float *loss, vp_rowstat *stats, int32_t *err_word,
+                                        vp_stream stream);
+
+/* The same of the logits hidden . weight^T, which exist only tile by tile on the tensor cores
+ * (hidden, weight, workspaces' alignment, VP_GRAD_* and the sharded flow as for the fused linear
+ * logp): hidden bf16 [N, D], weight bf16 [V, D], D a multiple of 64. The backward writes dhidden
+ * bf16 [N, D] and dW bf16 [V, D] (either may be NULL, not both); with N = 0 it writes zeros to dW.
+ * A row without valid statistics makes its dhidden row and all of dW NaN. */
+VP_API size_t vp_linear_cross_entropy_workspace_size(int64_t N, int64_t V, int64_t D);
+VP_API vp_status vp_linear_cross_entropy_fwd(const void *hidden, const void *weight, int64_t N, int64_t V, int64_t D,
+                                             int64_t vocab_start, double label_smoothing, double z_loss,
+                                             double softcap, const int64_t *targets, float *loss, vp_rowstat *stats,
+                                             void *workspace, size_t workspace_bytes, int32_t *err_word,
+                                             vp_stream stream);
+VP_API vp_status vp_linear_cross_entropy_partial(const void *hidden, const void *weight, int64_t N, int64_t V,
+                                                 int64_t D, int64_t vocab_start, double softcap,
+                                                 const int64_t *targets, vp_partial *parts, void *workspace,
+                                                 size_t workspace_bytes, vp_stream stream);
+VP_API size_t vp_linear_cross_entropy_bwd_workspace_size(int64_t N, int64_t V, int64_t D);
+VP_API vp_status vp_linear_cross_entropy_bwd(const void *hidden, const void *weight, int64_t N, int64_t V, int64_t D,
+                                             int64_t vocab_start, int64_t vocab_total, double label_smoothing,
+                                             double z_loss, double softcap, const int64_t *targets,
+                                             const vp_rowstat *stats, const float *grad_out, void *dhidden, void *dW,
+                                             int precision, void *workspace, size_t workspace_bytes,
+                                             int32_t *err_word, vp_stream stream);
+
+/* ------------------------------------------------------------------------ */
+/* The vocabulary's table as an embedding (no counterpart on the pages: the    */
+/* other end of a model whose head is the same table)                         */
+/* ------------------------------------------------------------------------ */
+/* out[n] = scale * table[ids[n] - vocab_start], in fp32 and rounded once to out_dtype. table: V
+ * rows of D elements, row_stride apart; out: contiguous [N, D]. ids int64 [N]: a negative one
+ * (padding) gives a zero row. One outside [vocab_start, vocab_start + V) is a data error (a NaN row
+ * and VP_ERRBIT_TARGET), or where sharded is not 0 a row of another shard: zeros, so that the
+ * shards' outputs add up. */
+VP_API vp_status vp_embedding_fwd(const void *table, int dtype, int64_t V, int64_t D, int64_t row_stride,
+                                  const int64_t *ids, int64_t N, int64_t vocab_start, int sharded, double scale,
+                                  void *out, int out_dtype, int32_t *err_word, vp_stream stream);
+
+/* dW[v] = scale * sum of dy[n] over the tokens n with ids[n] - vocab_start = v, summed in fp32 in an
+ * order that follows from the ids alone (the same result every time) and rounded once to out_dtype;
+ * accumulate not 0: that is added to what dW holds, before the rounding (the gradient of a head
+ * that is the same table), and rows without tokens are left as they are. dy: N rows of D elements with
+ * the rows' two strides as for logits; dW: contiguous [V, D]. Tokens of padding and of other shards
+ * count nowhere; those of a data error neither, and set VP_ERRBIT_TARGET. N = 0 writes zeros, or
+ * nothing where it accumulates. workspace: 256-byte aligned, vp_embedding_bwd_workspace_size(N, V, D)
+ * bytes. */
+VP_API size_t vp_embedding_bwd_workspace_size(int64_t N, int64_t V, int64_t D);
+VP_API vp_status vp_embedding_bwd(const void *dy, int dtype, int64_t N, int64_t D, int64_t R, int64_t s_o, int64_t s_i,
+                                  const int64_t *ids, int64_t V, int64_t vocab_start, int sharded, double scale,
+                                  void *dW, int out_dtype, int accumulate, void *workspace, size_t workspace_bytes,
+                                  int32_t *err_word, vp_stream stream);
+
+/* ------------------------------------------------------------------------ */
 /* Misc                                                                      */
 /* ------------------------------------------------------------------------ */
 

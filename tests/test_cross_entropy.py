@@ -1,0 +1,543 @@
+"""Cross entropy with label smoothing, z-loss and capped logits, of logits and of hidden . W^T, against the definition in
+64 bits.
+
+Tolerances (u = 2^-24, h = half a step of the output's type, per row with g the upstream gradient):
+  logits    a capped logit takes a rounded quotient, tanh (3e-7) and a rounded product: off by 8 u |z|; of hidden . W^T,
+            a tensor-core step adds 16 products to the running sum and drops up to a step of 2 u of the largest: off by
+            d = (D / 16 + 1) 2 u sum |h w|. A capped logit's own d is no larger, since |dz/dx| <= 1.
+  p         the argument's rounding (|log p| + 2) u, two more of log S, the base-2 exponential 3 u, S's own relative
+            error (at most 40 additions of a thread and 6 u of its terms): p (64 + 2 |log p|) u, and p 2 d
+  loss      log S as S: 64 u; m, z_t: 2 u of themselves and d; the mean: 40 additions and two roundings of
+            mean |z - m|; zeta lse^2 follows lse; h |loss|
+  dx        g slope (dp (1 + 2 zeta |lse|) + 8 u (p (1 + 2 zeta |lse|) + [j = t] + e / V)) + 32 u |dx| (the slope:
+            16 u absolute where it is over 2 / 3, 20 u relative elsewhere) + 6 u |x / c| |dx| + h |dx|: the slope is about
+            4 e^a, a = -2 |x / c|, and a carries three roundings (1 / c, the product with x, that with log2(e)), which
+            are 3 u |a| = 6 u |x / c| of e^a
+  dhidden, dW: every term's dz off as dx without h, by 2^-16 of itself as a pair of bf16 values (2^-8 as one), and the
+            sum over K terms by (K / 16 + 2) 2 u of the sum of magnitudes; h of the result
+"""
+import ctypes
+import math
+
+import pytest
+import torch
+
+import vocab_wide_logprobs_gb300 as vp
+from vocab_wide_logprobs_gb300 import _lib
+
+OK, ERR_NULL, ERR_SHAPE, ERR_DTYPE, ERR_LAYOUT, ERR_ALIGN, ERR_LAUNCH, ERR_ARG, ERR_DEVICE = range(9)
+U = 2.0 ** -24
+BF16, F32 = torch.bfloat16, torch.float32
+
+
+def plain(x, targets, smooth=0.0, zeta=0.0, cap=0.0, start=0):
+    """Losses of fp64 logits from the definition; differentiable."""
+    z = cap * torch.tanh(x / cap) if cap else x
+    lse = torch.logsumexp(z, 1)
+    t = (targets - start).clamp(min=0)
+    loss = lse - (1 - smooth) * z.gather(1, t[:, None])[:, 0] + zeta * lse ** 2
+    if smooth:
+        loss = loss - smooth * z.mean(1)
+    return torch.where(targets >= 0, loss, 0.0)
+
+
+def plain_grad(x, targets, g, smooth=0.0, zeta=0.0, cap=0.0, start=0, total=None):
+    """dx of sum g loss by the formula, and what its tolerance is made of."""
+    V = x.shape[1]
+    z = cap * torch.tanh(x / cap) if cap else x
+    slope = 1 / torch.cosh(x / cap) ** 2 if cap else torch.ones_like(x)
+    lse = torch.logsumexp(z, 1, keepdim=True)
+    lp = z - lse
+    p = torch.exp(lp)
+    onehot = torch.zeros_like(x).scatter_(1, (targets - start).clamp(min=0)[:, None], 1.0)
+    gr = torch.where(targets >= 0, g.double(), 0.0)[:, None]
+    share = smooth / (total or V)
+    a = 1 + 2 * zeta * lse
+    dz = gr * (p * a - (1 - smooth) * onehot - share)
+    # without cancellation at a target that carries its row
+    exact = gr * (torch.expm1(lp) + 2 * zeta * lse * p + smooth - share)
+    dz = torch.where(onehot > 0, exact, dz)
+    z, lp = z.clamp(-1e30, 1e30), lp.clamp(min=-1e4)
+    off = gr.abs() * slope * (p * (64 + 2 * lp.abs()) * U * a.abs() + 8 * U * (p * a.abs() + onehot + share))
+    far = 6 * U * (x / cap).abs().clamp(max=1e4) if cap else 0.0
+    return dz * slope, off + (32 * U + far) * (dz * slope).abs(), gr.abs() * slope * p * a.abs() * 2, z, lse
+
+
+def loss_tol(x, ref, targets, smooth, zeta, cap, d):
+    z = cap * torch.tanh(x / cap) if cap else x
+    fin = torch.where(torch.isfinite(z), z, 0.0)
+    m, lse = z.amax(1), torch.logsumexp(z, 1).abs()
+    d = d + (8 * U * fin.abs().amax(1) if cap else 0.0)
+    zt = z.gather(1, targets.clamp(min=0)[:, None])[:, 0]
+    zt = torch.where(torch.isfinite(zt), zt, 0.0)
+    mean = torch.where(torch.isfinite(z), (z - m[:, None]).abs(), 0.0).mean(1)
+    base = 64 * U + 3 * d + 4 * U * (m.abs() + (zt - m).abs()) + smooth * 48 * U * mean
+    return base * (1 + 2 * zeta * lse) + 4 * U * zeta * lse ** 2 + U * ref.abs().nan_to_num(posinf=0.0)
+
+
+def near(got, ref, tol, what):
+    got = got.double().cpu()
+    assert torch.equal(torch.isnan(got), torch.isnan(ref)), f"{what}: NaN elsewhere"
+    assert torch.equal(torch.isinf(got), torch.isinf(ref)), f"{what}: inf elsewhere"
+    fine = torch.isfinite(ref)
+    over = torch.where(fine, (got - ref).abs() - tol, torch.zeros_like(ref))
+    assert over.max() <= 0, f"{what}: {float(over.max()):.2e} over its tolerance"
+
+
+def rows(N, V, dtype, seed, sigma=3.0, offset=0.0):
+    g = torch.Generator().manual_seed(seed)
+    x = (torch.randn(N, V, generator=g) * sigma + offset).to(dtype)
+    targets = torch.randint(0, V, (N,), generator=g)
+    targets[torch.rand(N, generator=g) < 0.15] = -1
+    targets[0] = V - 1
+    return x, targets, torch.randn(N, generator=g)
+
+
+OPTIONS = [dict(), dict(smooth=0.1, zeta=1e-4), dict(cap=30.0), dict(smooth=1.0), dict(smooth=0.2, zeta=1e-2, cap=4.0)]
+
+
+def kw(o):
+    names = {"smooth": "label_smoothing", "zeta": "z_loss", "cap": "softcap", "start": "vocab_start"}
+    return {names[k]: v for k, v in o.items()}
+
+
+def check_logits(x, targets, g, o, xg=None, dtype=None):
+    xg = x.cuda() if xg is None else xg
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    loss, stats = vp.vp_cross_entropy_fwd(xg, targets.cuda(), err_word=err, **kw(o))
+    dx = vp.vp_cross_entropy_bwd(xg, targets.cuda(), stats, g.cuda(), err_word=err, **kw(o))
+    x64 = x.double()
+    s, z, c = o.get("smooth", 0.0), o.get("zeta", 0.0), o.get("cap", 0.0)
+    ref = plain(x64, targets, s, z, c, o.get("start", 0))
+    near(loss, ref, loss_tol(x64, ref, targets - o.get("start", 0), s, z, c, 0.0), "loss")
+    d, off, per_d, zz, _ = plain_grad(x64, targets, g, s, z, c, o.get("start", 0))
+    if c:
+        off = off + per_d * 8 * U * zz.abs().amax(1, keepdim=True)
+    near(dx, d, off + torch.finfo(x.dtype).eps / 2 * d.abs(), "dx")
+    assert int(err) == 0 and dx.dtype == x.dtype
+    return loss, stats, dx
+
+
+# --------------------------------------------------------------------------- the reference itself
+@pytest.mark.parametrize("o", OPTIONS)
+def test_formula_is_the_derivative(o):
+    """The formula against autograd of the definition and against central differences."""
+    x, targets, g = rows(5, 13, F32, 3)
+    x = x.double().requires_grad_()
+    s, z, c = o.get("smooth", 0.0), o.get("zeta", 0.0), o.get("cap", 0.0)
+    (plain(x, targets, s, z, c) * g).sum().backward()
+    d = plain_grad(x.detach(), targets, g, s, z, c)[0]
+    assert torch.allclose(x.grad, d, rtol=1e-12, atol=1e-14)
+    step = 1e-5
+    for j in range(13):
+        e = torch.zeros(13, dtype=torch.float64)
+        e[j] = step
+        diff = (plain(x.detach() + e, targets, s, z, c) - plain(x.detach() - e, targets, s, z, c)) / (2 * step) * g
+        assert torch.allclose(diff, d[:, j], rtol=1e-6, atol=1e-9)
+
+
+# --------------------------------------------------------------------------- logits
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("o", OPTIONS)
+@pytest.mark.parametrize("shape", [(1, 1), (3, 5), (2, 31), (7, 4096), (5, 8192), (4, 8193), (3, 20011), (40, 1000)])
+def test_logits(shape, o, dtype):
+    check_logits(*rows(*shape, dtype, sum(shape)), o)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_logits_wide_values_and_offsets(dtype):
+    """A common offset, near-certain rows, capped logits far out, values around the split of the tanh."""
+    x, targets, g = rows(6, 9001, dtype, 5, offset=200.0)
+    check_logits(x, targets, g, dict(smooth=0.1))
+    x, targets, g = rows(6, 9001, dtype, 6)
+    x[torch.arange(6), targets.clamp(min=0)] = 40.0
+    check_logits(x, targets, g, dict())
+    check_logits(x, targets, g, dict(zeta=1e-4, smooth=0.1))
+    x, targets, g = rows(6, 9001, dtype, 7, sigma=60.0)
+    check_logits(x, targets, g, dict(cap=15.0, smooth=0.1, zeta=1e-3))
+    x = torch.linspace(-2, 2, 6 * 1024).reshape(6, 1024).to(dtype) * 15.0
+    check_logits(x, torch.arange(6) * 100, g, dict(cap=15.0))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_logits_where_rows_begin(dtype):
+    """Rows at any offset from a 16-byte boundary, [B, T, V] views with two strides, and dx in place."""
+    x, targets, g = rows(12, 8231, dtype, 9)
+    for offset, gap in ((1, 0), (3, 5), (4, 4), (8, 1), (0, 8)):
+        room = torch.full((offset + 12 * (8231 + gap),), math.nan, dtype=dtype, device="cuda")
+        view = room[offset:].view(12, 8231 + gap)[:, :8231]
+        view.copy_(x)
+        check_logits(x, targets, g, dict(smooth=0.1), xg=view)
+    full = torch.full((3, 5, 8231), math.nan, dtype=dtype, device="cuda")
+    full[:, :-1] = x.view(3, 4, 8231).cuda()
+    _, stats, dx = check_logits(x, targets, g, dict(cap=20.0), xg=full[:, :-1])
+    for first in (0, 1):                                             # a base on a 16-byte boundary and one off it
+        room = torch.empty(12 * 8231 + 1, dtype=dtype, device="cuda")
+        inplace = room[first:first + 12 * 8231].view(12, 8231)
+        inplace.copy_(x)
+        loss, stats = vp.vp_cross_entropy_fwd(inplace, targets.cuda(), softcap=20.0)
+        ref = vp.vp_cross_entropy_bwd(inplace, targets.cuda(), stats, g.cuda(), softcap=20.0)
+        got = vp.vp_cross_entropy_bwd(inplace, targets.cuda(), stats, g.cuda(), softcap=20.0, dx=inplace)
+        assert got.data_ptr() == inplace.data_ptr() and torch.equal(got, ref)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("fill", ["inf", "lowest"])
+def test_masked_columns(dtype, fill):
+    x, targets, g = rows(8, 9001, dtype, 11)
+    low = -math.inf if fill == "inf" else torch.finfo(dtype).min
+    keep = torch.rand(8, 9001, generator=torch.Generator().manual_seed(1)) < 0.5
+    keep[torch.arange(8), targets.clamp(min=0)] = True
+    keep[2, 1:] = False                                              # one column left
+    keep[2, 0] = True
+    targets[2], targets[3] = 0, 4500
+    keep[3, :4500], keep[3, 4501:] = False, False                    # and in another slice
+    keep[3, 4500] = True
+    x = torch.where(keep, x, torch.tensor(low, dtype=dtype))
+    check_logits(x, targets, g, dict())
+    if fill == "inf":
+        # smoothing wants some of every column: infinite losses, finite gradients
+        loss, stats, _ = check_logits(x, targets, g, dict(smooth=0.1))
+        assert torch.isinf(loss[targets.cuda() >= 0]).all()
+        # a cap makes -inf the number -cap
+        check_logits(x, targets, g, dict(cap=20.0, smooth=0.1))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_rows_with_nothing_or_with_nan(dtype):
+    x, _, g = rows(7, 5003, dtype, 13)
+    x[1] = -math.inf
+    x[2, 4000] = math.nan
+    x[3, 17] = math.inf
+    x[4, 5002] = math.nan
+    targets = torch.tensor([5, 5, 5, 5, -1, 4000, 17])
+    loss, stats = vp.vp_cross_entropy_fwd(x.cuda(), targets.cuda(), label_smoothing=0.1)
+    dx = vp.vp_cross_entropy_bwd(x.cuda(), targets.cuda(), stats, g.cuda(), label_smoothing=0.1)
+    assert torch.isnan(loss).tolist() == [False, True, True, True, False, False, False]
+    assert loss[4] == 0 and (dx[4] == 0).all()
+    assert torch.isnan(dx[1:4]).all() and torch.isfinite(dx[5:]).all() and torch.isfinite(dx[0]).all()
+    flags = vp.decode_rowstats(stats)["flags"].tolist()
+    assert flags == [0, vp.ROW_EMPTY, vp.ROW_NANINF, vp.ROW_NANINF, vp.ROW_NANINF, 0, 0]
+    # under a cap an infinity is a number, a NaN is not
+    loss, stats = vp.vp_cross_entropy_fwd(x.cuda(), targets.cuda(), softcap=10.0)
+    dx = vp.vp_cross_entropy_bwd(x.cuda(), targets.cuda(), stats, g.cuda(), softcap=10.0)
+    assert torch.isnan(loss).tolist() == [False, False, True, False, False, False, False]
+    assert (dx[1] == 0).all() and dx[3, 17] == 0 and torch.isfinite(dx[3]).all() and torch.isnan(dx[2]).all()
+    assert abs(float(loss[1]) - math.log(5003)) < 1e-4
+
+
+@pytest.mark.gpu
+def test_targets_outside_the_shard():
+    x, _, g = rows(5, 700, BF16, 15)
+    targets = torch.tensor([700, 1399, 1400, 699, -7])
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    loss, stats = vp.vp_cross_entropy_fwd(x.cuda(), targets.cuda(), vocab_start=700, err_word=err)
+    assert int(err) == vp.ERRBIT_TARGET and torch.isnan(loss).tolist() == [False, False, True, True, False]
+    err.zero_()
+    dx = vp.vp_cross_entropy_bwd(x.cuda(), targets.cuda(), stats, g.cuda(), vocab_start=700, err_word=err)
+    assert int(err) == vp.ERRBIT_TARGET and torch.isnan(dx[2:4]).all() and (dx[4] == 0).all()
+    ref = plain_grad(x.double()[:2], targets[:2], g[:2], start=700)[0]
+    assert torch.allclose(dx[:2].double().cpu(), ref, rtol=2.0 ** -7, atol=1e-6)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_a_row_does_not_depend_on_the_batch(dtype):
+    x, targets, g = (t.cuda() for t in rows(70, 9008, dtype, 17, sigma=12.0))
+    o = dict(label_smoothing=0.1, z_loss=1e-3, softcap=25.0)
+    loss, stats = vp.vp_cross_entropy_fwd(x, targets, **o)
+    dx = vp.vp_cross_entropy_bwd(x, targets, stats, g, **o)
+    for i in (0, 1, 37, 69):
+        k = slice(i, i + 1)
+        one, st = vp.vp_cross_entropy_fwd(x[k], targets[k], **o)
+        assert torch.equal(one, loss[k]) and torch.equal(st, stats[k])
+        assert torch.equal(vp.vp_cross_entropy_bwd(x[k], targets[k], st, g[k], **o), dx[k])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("o", OPTIONS)
+def test_shards_merge_to_the_whole(dtype, o):
+    x, targets, g = rows(9, 6001, dtype, 19)
+    cuts = [0, 1, 2500, 2531, 6001]
+    s, z, c = o.get("smooth", 0.0), o.get("zeta", 0.0), o.get("cap", 0.0)
+    shards = [x[:, a:b].contiguous().cuda() for a, b in zip(cuts, cuts[1:])]
+    parts = torch.stack([vp.vp_cross_entropy_partial(p, targets.cuda(), softcap=c, vocab_start=a)
+                         for p, a in zip(shards, cuts)])
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    loss, stats = vp.vp_cross_entropy_merge(parts, label_smoothing=s, z_loss=z, err_word=err)
+    ref = plain(x.double(), targets, s, z, c)
+    near(loss, ref, loss_tol(x.double(), ref, targets, s, z, c, 0.0), "merged loss")
+    d, off, per_d, zz, _ = plain_grad(x.double(), targets, g, s, z, c)
+    if c:
+        off = off + per_d * 8 * U * zz.abs().amax(1, keepdim=True)
+    dx = torch.cat([vp.vp_cross_entropy_bwd(p, targets.cuda(), stats, g.cuda(), vocab_start=a, vocab_total=6001,
+                                            err_word=err, **kw(o)) for p, a in zip(shards, cuts)], 1)
+    near(dx, d, off + torch.finfo(dtype).eps / 2 * d.abs(), "sharded dx")
+    assert int(err) == 0
+    # a target that no shard holds
+    loss, _ = vp.vp_cross_entropy_merge(parts[:2], label_smoothing=s, z_loss=z, err_word=err)
+    held = (targets < 2500).cuda()
+    assert torch.equal(torch.isnan(loss), ~held) and int(err) == vp.ERRBIT_TARGET
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_merged_masked_shards(dtype):
+    """A shard of nothing but -inf, and a row of nothing at all."""
+    x, targets, g = rows(4, 900, dtype, 21)
+    x[1, 300:600] = -math.inf
+    x[2] = -math.inf
+    targets[:] = torch.tensor([5, 700, 3, -1])
+    parts = torch.stack([vp.vp_cross_entropy_partial(x[:, a:a + 300].cuda(), targets.cuda(), vocab_start=a)
+                         for a in (0, 300, 600)])
+    for s in (0.0, 0.1):
+        loss, stats = vp.vp_cross_entropy_merge(parts, label_smoothing=s)
+        ref = plain(x.double(), targets, s)
+        ref[2] = math.nan
+        near(loss, ref, loss_tol(x.double(), ref, targets, s, 0.0, 0.0, 0.0).nan_to_num(), f"smooth {s}")
+
+
+# --------------------------------------------------------------------------- hidden . W^T
+def model(N, V, D, seed, sigma=2.5):
+    g = torch.Generator().manual_seed(seed)
+    h = torch.randn(N, D, generator=g).to(BF16)
+    w = (torch.randn(V, D, generator=g) * sigma / math.sqrt(D)).to(BF16)
+    targets = torch.randint(0, V, (N,), generator=g)
+    targets[torch.rand(N, generator=g) < 0.1] = -1
+    targets[0] = V - 1
+    return h, w, targets, torch.randn(N, generator=g)
+
+
+def check_linear(h, w, targets, g, o, precision=vp.GRAD_EXACT, total=None, start=0):
+    D, (N, V) = h.shape[1], (h.shape[0], w.shape[0])
+    s, z, c = o.get("smooth", 0.0), o.get("zeta", 0.0), o.get("cap", 0.0)
+    hg, wg, tg = h.cuda(), w.cuda(), targets.cuda()
+    loss, stats = vp.vp_linear_cross_entropy_fwd(hg, wg, tg, **kw(o))
+    dh, dw = vp.vp_linear_cross_entropy_bwd(hg, wg, tg, stats, g.cuda(), precision=precision, **kw(o))
+    h64, w64 = h.double(), w.double()
+    x, size = h64 @ w64.t(), h64.abs() @ w64.abs().t()
+    d = (D / 16 + 1) * 2 * U * size.amax(1)
+    ref = plain(x, targets, s, z, c, o.get("start", 0))
+    near(loss, ref, loss_tol(x, ref, targets - o.get("start", 0), s, z, c, d), "loss")
+    dz, off, per_d, zz, _ = plain_grad(x, targets, g, s, z, c, o.get("start", 0))
+    d = d[:, None] + (8 * U * zz.abs().amax(1, keepdim=True) if c else 0.0)
+    # a logit off by d moves the cap's slope by at most |slope'| d <= d / c of itself
+    off = off + per_d * d + (dz.abs() * d / c if c else 0.0)
+    pair = 2.0 ** -16 if precision == vp.GRAD_EXACT else 2.0 ** -8
+    off = off + pair * dz.abs()
+    half = torch.finfo(BF16).eps / 2
+    for got, ref, tol, what in (
+            (dh, dz @ w64, off @ w64.abs() + (V / 16 + 2) * 2 * U * (dz.abs() @ w64.abs()), "dhidden"),
+            (dw, dz.t() @ h64, off.t() @ h64.abs() + (N / 16 + 2) * 2 * U * (dz.abs().t() @ h64.abs()), "dW")):
+        near(got, ref, tol + half * ref.abs(), what)
+    return loss, stats, dh, dw
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("o", OPTIONS)
+@pytest.mark.parametrize("shape", [(1, 1, 64), (3, 200, 64), (130, 700, 128), (257, 1025, 192), (64, 5003, 512)])
+def test_linear(shape, o):
+    check_linear(*model(*shape, sum(shape)), o)
+
+
+@pytest.mark.gpu
+def test_linear_fast_precision_and_single_outputs():
+    h, w, targets, g = model(300, 1500, 256, 31)
+    o = dict(smooth=0.1, zeta=1e-4, cap=10.0)
+    check_linear(h, w, targets, g, o, precision=vp.GRAD_FAST)
+    _, stats, dh, dw = check_linear(h, w, targets, g, o)
+    args = (h.cuda(), w.cuda(), targets.cuda(), stats, g.cuda())
+    a, none = vp.vp_linear_cross_entropy_bwd(*args, want_dW=False, **kw(o))
+    assert none is None and torch.equal(a, dh)
+    none, b = vp.vp_linear_cross_entropy_bwd(*args, want_dhidden=False, **kw(o))
+    assert none is None and torch.equal(b, dw)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("N, V", [(4, 40000), (8200, 300)])
+def test_linear_several_pieces(N, V):
+    """More vocabulary than one piece of the backward (32768 columns), and more rows than its first limit."""
+    check_linear(*model(N, V, 64, 33), dict(smooth=0.1, zeta=1e-4))
+
+
+@pytest.mark.gpu
+def test_linear_near_certain_rows():
+    h, w, targets, g = model(40, 900, 128, 35, sigma=1.0)
+    used = targets >= 0
+    w[targets[used]] = (h[used].float() * 0.3).to(BF16)              # logits of about 38 at the targets
+    check_linear(h, w, targets, g, dict())
+    check_linear(h, w, targets, g, dict(cap=30.0, smooth=0.1))
+
+
+@pytest.mark.gpu
+def test_linear_bad_rows():
+    h, w, targets, g = model(6, 300, 64, 37)
+    h[1, 3] = math.nan
+    targets[:] = torch.tensor([5, 5, -1, 300, 7, 299])
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    args = (h.cuda(), w.cuda(), targets.cuda())
+    loss, stats = vp.vp_linear_cross_entropy_fwd(*args, err_word=err, label_smoothing=0.1)
+    assert torch.isnan(loss).tolist() == [False, True, False, True, False, False] and int(err) == vp.ERRBIT_TARGET
+    err.zero_()
+    dh, dw = vp.vp_linear_cross_entropy_bwd(*args, stats, g.cuda(), err_word=err, label_smoothing=0.1)
+    assert int(err) == vp.ERRBIT_TARGET and torch.isnan(dw).all()
+    assert torch.isnan(dh[[1, 3]]).all() and torch.isfinite(dh[[0, 4, 5]]).all() and (dh[2] == 0).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("o", OPTIONS)
+def test_linear_shards(o):
+    h, w, targets, g = model(150, 1000, 128, 39)
+    s, z, c = o.get("smooth", 0.0), o.get("zeta", 0.0), o.get("cap", 0.0)
+    cuts = [0, 300, 301, 1000]
+    hg, tg = h.cuda(), targets.cuda()
+    ws = [w[a:b].contiguous().cuda() for a, b in zip(cuts, cuts[1:])]
+    parts = torch.stack([vp.vp_linear_cross_entropy_partial(hg, p, tg, softcap=c, vocab_start=a)
+                         for p, a in zip(ws, cuts)])
+    loss, stats = vp.vp_cross_entropy_merge(parts, label_smoothing=s, z_loss=z)
+    whole, wstats = vp.vp_linear_cross_entropy_fwd(hg, w.cuda(), tg, **kw(o))
+    x = h.double() @ w.double().t()
+    ref = plain(x, targets, s, z, c)
+    near(loss, ref, loss_tol(x, ref, targets, s, z, c, (128 / 16 + 1) * 2 * U * (h.double().abs() @ w.double().abs().t()).amax(1)),
+         "merged")
+    got = [vp.vp_linear_cross_entropy_bwd(hg, p, tg, stats, g.cuda(), vocab_start=a, vocab_total=1000, **kw(o))
+           for p, a in zip(ws, cuts)]
+    dh, dw = vp.vp_linear_cross_entropy_bwd(hg, w.cuda(), tg, wstats, g.cuda(), **kw(o))
+    # the same products; records that differ in their last bits, and four roundings of dhidden instead of one
+    assert torch.allclose(torch.cat([b for _, b in got]).double(), dw.double(), rtol=2.0 ** -6, atol=1e-5)
+    assert torch.allclose(sum(a.double() for a, _ in got), dh.double(), rtol=2.0 ** -6,
+                          atol=2.0 ** -7 * float(max(a.abs().max() for a, _ in got)))
+
+
+# --------------------------------------------------------------------------- streams, graphs, buffers
+@pytest.mark.gpu
+def test_another_stream_and_a_captured_step():
+    h, w, targets, g = (t.cuda() for t in model(96, 1300, 128, 41))
+    x = (h.float() @ w.float().t()).to(BF16)
+    o = dict(label_smoothing=0.1, z_loss=1e-4, softcap=12.0)
+
+    def step():
+        a, st = vp.vp_cross_entropy_fwd(x, targets, **o)
+        b, sl = vp.vp_linear_cross_entropy_fwd(h, w, targets, **o)
+        return (a, vp.vp_cross_entropy_bwd(x, targets, st, g, **o), b,
+                *vp.vp_linear_cross_entropy_bwd(h, w, targets, sl, g, **o))
+
+    ref = step()
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        got = step()
+    torch.cuda.current_stream().wait_stream(side)
+    assert all(torch.equal(a, b) for a, b in zip(got, ref))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step()
+    h.mul_(0.5)
+    x.copy_((h.float() @ w.float().t()).to(BF16))
+    targets.copy_(targets.roll(1))
+    for _ in range(2):
+        graph.replay()
+    assert all(torch.equal(a, b) for a, b in zip(out, step()))
+    assert vp.vp_fault_status() == 0
+
+
+@pytest.mark.gpu
+def test_callers_buffers_and_nothing_behind_them():
+    x, targets, g = (t.cuda() for t in rows(10, 5001, BF16, 43))
+    loss, stats = torch.full((11,), 7.0, device="cuda"), torch.full((11, 8), 7.0, device="cuda")
+    work = torch.full((vp.vp_cross_entropy_workspace_size(10, 5001) + 64,), 99, dtype=torch.uint8, device="cuda")
+    ref, rst = vp.vp_cross_entropy_fwd(x, targets, label_smoothing=0.1)
+    vp.vp_cross_entropy_fwd(x, targets, label_smoothing=0.1, loss=loss[:10], stats=stats[:10], workspace=work[:-64])
+    assert torch.equal(loss[:10], ref) and torch.equal(stats[:10], rst)
+    assert (loss[10:] == 7).all() and (stats[10:] == 7).all() and (work[-64:] == 99).all()
+    dx = torch.full((11, 5001), 7.0, dtype=BF16, device="cuda")
+    vp.vp_cross_entropy_bwd(x, targets, stats[:10], g, label_smoothing=0.1, dx=dx[:10])
+    assert (dx[10:] == 7).all()
+    h, w, t, gg = (v.cuda() for v in model(20, 600, 64, 44))
+    loss, st = vp.vp_linear_cross_entropy_fwd(h, w, t)
+    dh, dw = torch.full((21, 64), 7.0, dtype=BF16, device="cuda"), torch.full((601, 64), 7.0, dtype=BF16, device="cuda")
+    vp.vp_linear_cross_entropy_bwd(h, w, t, st, gg, dhidden=dh[:20], dW=dw[:600])
+    assert (dh[20:] == 7).all() and (dw[600:] == 7).all() and not (dw[:600] == 7).all()
+
+
+@pytest.mark.gpu
+def test_no_rows():
+    none = torch.empty(0, dtype=torch.int64, device="cuda")
+    loss, stats = vp.vp_cross_entropy_fwd(torch.empty(0, 50, device="cuda"), none)
+    assert loss.shape == (0,) and vp.vp_cross_entropy_bwd(torch.empty(0, 50, device="cuda"), none, stats, loss).shape == (0, 50)
+    h, w = torch.empty(0, 64, dtype=BF16, device="cuda"), torch.ones(50, 64, dtype=BF16, device="cuda")
+    loss, stats = vp.vp_linear_cross_entropy_fwd(h, w, none)
+    dh, dw = vp.vp_linear_cross_entropy_bwd(h, w, none, stats, loss)
+    assert dh.shape == (0, 64) and (dw == 0).all()                   # a sum over no rows
+
+
+# --------------------------------------------------------------------------- refusals (no GPU needed)
+FAKE, ODD = ctypes.c_void_p(0x100000), ctypes.c_void_p(0x100001)
+BIG = ctypes.c_size_t(1 << 40)
+
+
+def fwd(dtype=1, N=4, V=16, smooth=0.0, z=0.0, cap=0.0, targets=FAKE, loss=FAKE, stats=FAKE, work=FAKE, size=BIG):
+    return _lib.lib().vp_cross_entropy_fwd(FAKE, dtype, N, V, 4, 0, V, 0, smooth, z, cap, targets, loss, stats, work, size,
+                                           None, None)
+
+
+def test_refusals_of_the_library():
+    lib = _lib.lib()
+    nan, inf = math.nan, math.inf
+    for bad in (dict(smooth=-0.1), dict(smooth=1.1), dict(smooth=nan), dict(z=-1.0), dict(z=nan), dict(z=inf),
+                dict(cap=-1.0), dict(cap=nan), dict(cap=inf), dict(cap=1e-40), dict(size=ctypes.c_size_t(16))):
+        assert fwd(**bad) == ERR_ARG, bad
+    assert fwd(dtype=2) == ERR_DTYPE and fwd(V=0) == ERR_SHAPE and fwd(N=-1) == ERR_SHAPE
+    for name in ("targets", "loss", "stats", "work"):
+        assert fwd(**{name: None}) == ERR_NULL and fwd(**{name: ODD}) == ERR_ALIGN
+    assert fwd(N=0, targets=None, loss=None, stats=None, work=None) == OK
+    bwd = lambda total=0, dx=FAKE, smooth=0.0: lib.vp_cross_entropy_bwd(
+        FAKE, 1, 4, 16, 4, 0, 16, 0, total, smooth, 0.0, 0.0, FAKE, FAKE, FAKE, dx, None, None)
+    assert bwd(total=15) == ERR_SHAPE and bwd(dx=None) == ERR_NULL and bwd(dx=ODD) == ERR_ALIGN and bwd(smooth=2.0) == ERR_ARG
+    part = lambda parts=FAKE, cap=0.0, work=FAKE: lib.vp_cross_entropy_partial(
+        FAKE, 1, 4, 16, 4, 0, 16, 0, cap, FAKE, parts, work, BIG, None)
+    assert part(parts=None) == ERR_NULL and part(parts=ODD) == ERR_ALIGN and part(cap=-1.0) == ERR_ARG
+    merge = lambda K=2, smooth=0.0, loss=FAKE: lib.vp_cross_entropy_merge(FAKE, K, 4, smooth, 0.0, loss, FAKE, None, None)
+    assert merge(K=0) == ERR_SHAPE and merge(smooth=-1.0) == ERR_ARG and merge(loss=None) == ERR_NULL
+    lin = lambda D=64, loss=FAKE, work=FAKE, size=BIG, cap=0.0: lib.vp_linear_cross_entropy_fwd(
+        FAKE, FAKE, 4, 16, D, 0, 0.0, 0.0, cap, FAKE, loss, FAKE, work, size, None, None)
+    assert lin(D=96) == ERR_SHAPE and lin(loss=None) == ERR_NULL and lin(cap=nan) == ERR_ARG
+    assert lin(work=ctypes.c_void_p(0x100010)) == ERR_ALIGN and lin(size=ctypes.c_size_t(8)) == ERR_ARG
+    back = lambda dh=FAKE, dw=FAKE, p=0, total=0, N=4, size=BIG: lib.vp_linear_cross_entropy_bwd(
+        FAKE, FAKE, N, 16, 64, 0, total, 0.0, 0.0, 0.0, FAKE, FAKE, FAKE, dh, dw, p, FAKE, size, None, None)
+    assert back(dh=None, dw=None) == ERR_ARG and back(p=3) == ERR_ARG and back(total=3) == ERR_SHAPE
+    assert back(dw=ODD) == ERR_ALIGN and back(N=0, dw=None) == OK and back(size=ctypes.c_size_t(8)) == ERR_ARG
+    assert lib.vp_linear_cross_entropy_partial(FAKE, FAKE, 4, 16, 64, 0, 0.0, FAKE, None, FAKE, BIG, None) == ERR_NULL
+    assert lib.vp_cross_entropy_workspace_size(-1, 5) == 0 and lib.vp_linear_cross_entropy_workspace_size(4, 5, 65) == 0
+
+
+def test_refusals_of_the_binding():
+    def status(fn):
+        with pytest.raises(vp.VPError) as e:
+            fn()
+        return e.value.status
+
+    N, V = 6, 40
+    x, t, g, st = torch.zeros(N, V), torch.zeros(N, dtype=torch.int64), torch.zeros(N), vp.rowstats(N, "cpu")
+    assert status(lambda: vp.vp_cross_entropy_fwd(x, t.int())) == 3
+    assert status(lambda: vp.vp_cross_entropy_fwd(x, t[:-1])) == 2
+    assert status(lambda: vp.vp_cross_entropy_fwd(x, t, loss=torch.empty(N + 1))) == 2
+    assert status(lambda: vp.vp_cross_entropy_fwd(x.half(), t)) == 3
+    assert status(lambda: vp.vp_cross_entropy_fwd(x.t(), torch.zeros(V, dtype=torch.int64))) == 4
+    assert status(lambda: vp.vp_cross_entropy_fwd(x, t)) == 8                                # not on a GPU
+    assert status(lambda: vp.vp_cross_entropy_bwd(x, t, st, g, dx=torch.empty(N, V, dtype=BF16))) == 3
+    assert status(lambda: vp.vp_cross_entropy_bwd(x, t, st, torch.zeros(2 * N)[::2])) == 4
+    assert status(lambda: vp.vp_cross_entropy_partial(x, t, parts=vp.partials(N - 1, "cpu"))) == 2
+    assert status(lambda: vp.vp_cross_entropy_merge(vp.partials(N, "cpu"))) == 2
+    h, w = torch.zeros(N, 64, dtype=BF16), torch.zeros(V, 64, dtype=BF16)
+    assert status(lambda: vp.vp_linear_cross_entropy_fwd(h.float(), w, t)) == 3
+    assert status(lambda: vp.vp_linear_cross_entropy_fwd(h, w[:, :32], t)) in (2, 4)
+    assert status(lambda: vp.vp_linear_cross_entropy_bwd(h, w, t, st, g, dW=torch.empty(V, 65, dtype=BF16))) == 2
+    assert status(lambda: vp.vp_linear_cross_entropy_bwd(h, w, t, st, g, dhidden=h.float())) == 3

@@ -14,7 +14,7 @@ from . import build as _build
 _lock = threading.Lock()
 _handle = None
 
-P, I64, I32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int
+P, I64, I32, F64 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_double
 
 # name -> argument types (all return int status unless noted)
 SIGNATURES = {
@@ -56,6 +56,16 @@ SIGNATURES = {
     "vp_mxfp4_quantize": [P, I32, I64, I64, I64, I64, I64, P, P, P],
     "vp_mxfp4_dequantize": [P, P, I64, I64, I32, P, P],
     "vp_linear_mxfp4_fwd": [P, P, P, P, I64, I64, I64, I32, P, P],
+    "vp_cross_entropy_fwd": [P, I32, I64, I64, I64, I64, I64, I64, F64, F64, F64, P, P, P, P, ctypes.c_size_t, P, P],
+    "vp_cross_entropy_bwd": [P, I32, I64, I64, I64, I64, I64, I64, I64, F64, F64, F64, P, P, P, P, P, P],
+    "vp_cross_entropy_partial": [P, I32, I64, I64, I64, I64, I64, I64, F64, P, P, P, ctypes.c_size_t, P],
+    "vp_cross_entropy_merge": [P, I64, I64, F64, F64, P, P, P, P],
+    "vp_linear_cross_entropy_fwd": [P, P, I64, I64, I64, I64, F64, F64, F64, P, P, P, P, ctypes.c_size_t, P, P],
+    "vp_linear_cross_entropy_partial": [P, P, I64, I64, I64, I64, F64, P, P, P, ctypes.c_size_t, P],
+    "vp_linear_cross_entropy_bwd": [P, P, I64, I64, I64, I64, I64, F64, F64, F64, P, P, P, P, P, I32, P,
+                                    ctypes.c_size_t, P, P],
+    "vp_embedding_fwd": [P, I32, I64, I64, I64, P, I64, I64, I32, F64, P, I32, P, P],
+    "vp_embedding_bwd": [P, I32, I64, I64, I64, I64, I64, P, I64, I64, I32, F64, P, I32, I32, P, ctypes.c_size_t, P, P],
 }
 
 
@@ -94,7 +104,11 @@ def lib():
                                ("vp_linear_jsd_workspace_size", [I64, I64]),
                                ("vp_linear_jsd_bwd_workspace_size", [I64, I64, I64, I64]),
                                ("vp_processed_logprobs_workspace_size", [I64, I64]),
-                               ("vp_mxfp4_scale_bytes", [I64, I64])):
+                               ("vp_mxfp4_scale_bytes", [I64, I64]),
+                               ("vp_cross_entropy_workspace_size", [I64, I64]),
+                               ("vp_linear_cross_entropy_workspace_size", [I64, I64, I64]),
+                               ("vp_linear_cross_entropy_bwd_workspace_size", [I64, I64, I64]),
+                               ("vp_embedding_bwd_workspace_size", [I64, I64, I64])):
                 fn = getattr(h, name)
                 fn.argtypes = args
                 fn.restype = ctypes.c_size_t

@@ -977,3 +977,206 @@ def vp_linear_mxfp4_fwd(x_codes, x_scales, w_codes, w_scales, dtype=torch.bfloat
     _check(_handle().vp_linear_mxfp4_fwd(_addr(x_codes), _addr(x_scales), _addr(w_codes), _addr(w_scales), N, V, D,
                                           _DTYPES[dtype], _addr(y), _queue(x_codes.device)), "vp_linear_mxfp4_fwd")
     return y
+
+
+# ---------------------------------------------------------------------------
+# Cross entropy as a training loss, and the table as an embedding
+# ---------------------------------------------------------------------------
+def _bytes_arg(workspace, like):
+    """A caller's workspace; the library checks its size and alignment."""
+    if workspace is not None and (workspace.device != like.device or not workspace.is_contiguous()):
+        raise VPError(4, f"workspace: needs contiguous bytes on {like.device}")
+
+
+def _nbytes(workspace):
+    return workspace.numel() * workspace.element_size()
+
+
+def vp_cross_entropy_workspace_size(N: int, V: int) -> int:
+    return int(_handle().vp_cross_entropy_workspace_size(N, V))
+
+
+def vp_cross_entropy_fwd(x, targets, label_smoothing: float = 0.0, z_loss: float = 0.0, softcap: float = 0.0,
+                         vocab_start: int = 0, err_word=None, loss=None, stats=None, workspace=None):
+    """Softmax cross entropy per row with label smoothing, z_loss * lse^2 and logits capped at softcap tanh(x / softcap)
+    (0: no cap). Returns (loss fp32 [N], stats)."""
+    N, V, R, s_o, s_i = rows_of(x)
+    _row_args(x, N, targets=targets, stats=(stats,), err_word=err_word, outs=(loss,))
+    _bytes_arg(workspace, x)
+    code = _dtype_code(x)
+    _on_gpu(x)
+    loss = _f32(N, x) if loss is None else loss
+    stats = rowstats(N, x.device) if stats is None else stats
+    if workspace is None:
+        workspace = _workspace(_handle().vp_cross_entropy_workspace_size(N, V), x)
+    _check(_handle().vp_cross_entropy_fwd(_addr(x), code, N, V, R, s_o, s_i, vocab_start, label_smoothing, z_loss,
+                                          softcap, _addr(targets), _addr(loss), _addr(stats), _addr(workspace),
+                                          _nbytes(workspace), _addr(err_word), _queue(x.device)), "vp_cross_entropy_fwd")
+    return loss, stats
+
+
+def vp_cross_entropy_bwd(x, targets, stats, grad, label_smoothing: float = 0.0, z_loss: float = 0.0,
+                         softcap: float = 0.0, vocab_start: int = 0, vocab_total: int = 0, err_word=None, dx=None):
+    """Gradient of sum_r grad[r] loss[r] with respect to x: dx, contiguous [N, V] in the dtype of x (dx=x works in place
+    where x is contiguous). vocab_total: columns of the whole vocabulary where x is a shard of it."""
+    N, V, R, s_o, s_i = rows_of(x)
+    _row_args(x, N, targets=targets, stats=(stats,), grad=grad, err_word=err_word)
+    _arg(dx, N * V, x.dtype, x, "dx")
+    code = _dtype_code(x)
+    _on_gpu(x)
+    dx = torch.empty((N, V), dtype=x.dtype, device=x.device) if dx is None else dx
+    _check(_handle().vp_cross_entropy_bwd(_addr(x), code, N, V, R, s_o, s_i, vocab_start, vocab_total, label_smoothing,
+                                          z_loss, softcap, _addr(targets), _addr(stats), _addr(grad), _addr(dx),
+                                          _addr(err_word), _queue(x.device)), "vp_cross_entropy_bwd")
+    return dx
+
+
+def vp_cross_entropy_partial(x, targets, softcap: float = 0.0, vocab_start: int = 0, parts=None, workspace=None):
+    """Per-row cross-entropy records over the shard x (columns vocab_start .. vocab_start + V)."""
+    N, V, R, s_o, s_i = rows_of(x)
+    _row_args(x, N, targets=targets)
+    _parts_arg(parts, N, x)
+    _bytes_arg(workspace, x)
+    code = _dtype_code(x)
+    _on_gpu(x)
+    parts = partials(N, x.device) if parts is None else parts
+    if workspace is None:
+        workspace = _workspace(_handle().vp_cross_entropy_workspace_size(N, V), x)
+    _check(_handle().vp_cross_entropy_partial(_addr(x), code, N, V, R, s_o, s_i, vocab_start, softcap, _addr(targets),
+                                              _addr(parts), _addr(workspace), _nbytes(workspace), _queue(x.device)),
+           "vp_cross_entropy_partial")
+    return parts
+
+
+def vp_cross_entropy_merge(parts, label_smoothing: float = 0.0, z_loss: float = 0.0, err_word=None, loss=None,
+                           stats=None):
+    """Merges [K, N] shard records (shard-major) into (loss fp32 [N], stats) for the whole rows."""
+    K, N = _gathered(parts)
+    _row_args(parts, N, stats=(stats,), err_word=err_word, outs=(loss,))
+    _on_gpu(parts)
+    loss = _f32(N, parts) if loss is None else loss
+    stats = rowstats(N, parts.device) if stats is None else stats
+    _check(_handle().vp_cross_entropy_merge(_addr(parts), K, N, label_smoothing, z_loss, _addr(loss), _addr(stats),
+                                            _addr(err_word), _queue(parts.device)), "vp_cross_entropy_merge")
+    return loss, stats
+
+
+def vp_linear_cross_entropy_workspace_size(N: int, V: int, D: int) -> int:
+    return int(_handle().vp_linear_cross_entropy_workspace_size(N, V, D))
+
+
+def vp_linear_cross_entropy_bwd_workspace_size(N: int, V: int, D: int) -> int:
+    return int(_handle().vp_linear_cross_entropy_bwd_workspace_size(N, V, D))
+
+
+def vp_linear_cross_entropy_fwd(hidden, weight, targets, label_smoothing: float = 0.0, z_loss: float = 0.0,
+                                softcap: float = 0.0, vocab_start: int = 0, err_word=None, loss=None, stats=None,
+                                workspace=None):
+    """vp_cross_entropy_fwd of hidden @ weight^T without materialising the logits. hidden: bf16 [N, D], weight: bf16
+    [V, D] (contiguous). Returns (loss fp32 [N], stats)."""
+    N, V, D = _linear_model(hidden, weight, "vp_linear_cross_entropy_fwd")
+    _row_args(hidden, N, targets=targets, stats=(stats,), err_word=err_word, outs=(loss,))
+    _bytes_arg(workspace, hidden)
+    _on_gpu(hidden)
+    loss = _f32(N, hidden) if loss is None else loss
+    stats = rowstats(N, hidden.device) if stats is None else stats
+    if workspace is None:
+        workspace = _workspace(_handle().vp_linear_cross_entropy_workspace_size(N, V, D), hidden)
+    _check(_handle().vp_linear_cross_entropy_fwd(_addr(hidden), _addr(weight), N, V, D, vocab_start, label_smoothing,
+                                                 z_loss, softcap, _addr(targets), _addr(loss), _addr(stats),
+                                                 _addr(workspace), _nbytes(workspace), _addr(err_word),
+                                                 _queue(hidden.device)), "vp_linear_cross_entropy_fwd")
+    return loss, stats
+
+
+def vp_linear_cross_entropy_partial(hidden, weight, targets, softcap: float = 0.0, vocab_start: int = 0, parts=None,
+                                    workspace=None):
+    """Per-row cross-entropy records over the vocabulary shard held by weight (rows vocab_start .. + V of the head)."""
+    N, V, D = _linear_model(hidden, weight, "vp_linear_cross_entropy_partial")
+    _row_args(hidden, N, targets=targets)
+    _parts_arg(parts, N, hidden)
+    _bytes_arg(workspace, hidden)
+    _on_gpu(hidden)
+    parts = partials(N, hidden.device) if parts is None else parts
+    if workspace is None:
+        workspace = _workspace(_handle().vp_linear_cross_entropy_workspace_size(N, V, D), hidden)
+    _check(_handle().vp_linear_cross_entropy_partial(_addr(hidden), _addr(weight), N, V, D, vocab_start, softcap,
+                                                     _addr(targets), _addr(parts), _addr(workspace), _nbytes(workspace),
+                                                     _queue(hidden.device)), "vp_linear_cross_entropy_partial")
+    return parts
+
+
+def vp_linear_cross_entropy_bwd(hidden, weight, targets, stats, grad, label_smoothing: float = 0.0,
+                                z_loss: float = 0.0, softcap: float = 0.0, vocab_start: int = 0, vocab_total: int = 0,
+                                want_dhidden=True, want_dW=True, err_word=None, dhidden=None, dW=None, workspace=None,
+                                precision: int = None):
+    """Gradients of sum_r grad[r] loss[r]: (dhidden bf16 [N, D] or None, dW bf16 [V, D] or None); precision as
+    vp_linear_logp_bwd."""
+    N, V, D = _linear_model(hidden, weight, "vp_linear_cross_entropy_bwd")
+    _row_args(hidden, N, targets=targets, stats=(stats,), grad=grad, err_word=err_word)
+    _arg(dhidden if want_dhidden else None, N * D, torch.bfloat16, hidden, "dhidden")
+    _arg(dW if want_dW else None, V * D, torch.bfloat16, hidden, "dW")
+    _bytes_arg(workspace, hidden)
+    _on_gpu(hidden)
+    dhidden = (torch.empty((N, D), dtype=torch.bfloat16, device=hidden.device) if dhidden is None else dhidden) \
+        if want_dhidden else None
+    dW = (torch.empty((V, D), dtype=torch.bfloat16, device=hidden.device) if dW is None else dW) if want_dW else None
+    if workspace is None:
+        workspace = _workspace(_handle().vp_linear_cross_entropy_bwd_workspace_size(N, V, D), hidden)
+    _check(_handle().vp_linear_cross_entropy_bwd(_addr(hidden), _addr(weight), N, V, D, vocab_start, vocab_total,
+                                                 label_smoothing, z_loss, softcap, _addr(targets), _addr(stats),
+                                                 _addr(grad), _addr(dhidden), _addr(dW), _precision(precision),
+                                                 _addr(workspace), _nbytes(workspace), _addr(err_word),
+                                                 _queue(hidden.device)), "vp_linear_cross_entropy_bwd")
+    return dhidden, dW
+
+
+def vp_embedding_fwd(weight, ids, scale: float = 1.0, vocab_start: int = 0, sharded: bool = False, dtype=None,
+                     err_word=None, out=None):
+    """scale * weight[ids - vocab_start], [*ids.shape, D] in dtype (weight's by default). weight: [V, D] with any row
+    stride; ids int64, contiguous: negative ones are padding (zero rows); with sharded, those of other shards too."""
+    if weight.dim() != 2:
+        raise VPError(2, f"weight must be [V, D], got {tuple(weight.shape)}")
+    V, D, _, _, stride = rows_of(weight)
+    dtype = weight.dtype if dtype is None else dtype
+    if dtype not in _DTYPES:
+        raise VPError(3, f"dtype {dtype}")
+    N, code = ids.numel(), _dtype_code(weight)
+    _arg(ids, N, torch.int64, weight, "ids")
+    _arg(out, N * D, dtype, weight, "out")
+    _arg(err_word, 1, torch.int32, weight, "err_word")
+    _on_gpu(weight)
+    out = torch.empty((*ids.shape, D), dtype=dtype, device=weight.device) if out is None else out
+    _check(_handle().vp_embedding_fwd(_addr(weight), code, V, D, stride, _addr(ids), N, vocab_start, int(sharded), scale,
+                                      _addr(out), _DTYPES[dtype], _addr(err_word), _queue(weight.device)),
+           "vp_embedding_fwd")
+    return out
+
+
+def vp_embedding_bwd_workspace_size(N: int, V: int, D: int) -> int:
+    return int(_handle().vp_embedding_bwd_workspace_size(N, V, D))
+
+
+def vp_embedding_bwd(dy, ids, V: int, scale: float = 1.0, vocab_start: int = 0, sharded: bool = False, dtype=None,
+                     err_word=None, dW=None, accumulate: bool = False, workspace=None):
+    """Gradient of vp_embedding_fwd with respect to its table of V rows: dW [V, D] in dtype (dy's, or dW's where it is
+    passed). dy: [N, D] or [B, T, D] rows, one for each id. accumulate: added to what the passed dW holds."""
+    N, D, R, s_o, s_i = rows_of(dy)
+    dtype = (dy.dtype if dW is None else dW.dtype) if dtype is None else dtype
+    if dtype not in _DTYPES:
+        raise VPError(3, f"dtype {dtype}")
+    if accumulate and dW is None:
+        raise VPError(1, "accumulate needs a dW to add to")
+    code = _dtype_code(dy)
+    _arg(ids, N, torch.int64, dy, "ids")
+    _arg(dW, V * D, dtype, dy, "dW")
+    _arg(err_word, 1, torch.int32, dy, "err_word")
+    _bytes_arg(workspace, dy)
+    _on_gpu(dy)
+    dW = torch.empty((V, D), dtype=dtype, device=dy.device) if dW is None else dW
+    if workspace is None:
+        workspace = _workspace(_handle().vp_embedding_bwd_workspace_size(N, V, D), dy)
+    _check(_handle().vp_embedding_bwd(_addr(dy), code, N, D, R, s_o, s_i, _addr(ids), V, vocab_start, int(sharded), scale,
+                                      _addr(dW), _DTYPES[dtype], int(accumulate), _addr(workspace), _nbytes(workspace),
+                                      _addr(err_word), _queue(dy.device)), "vp_embedding_bwd")
+    return dW

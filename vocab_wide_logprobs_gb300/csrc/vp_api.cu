@@ -585,13 +585,14 @@ vp_status vp_fault_status(uint32_t *value, int clear) {
     if (!value) return VP_ERR_NULL;
     vp_status st = check_device();
     if (st != VP_OK) return st;
-    uint32_t a = 0, b = 0, c = 0, d = 0, e = 0;
+    uint32_t a = 0, b = 0, c = 0, d = 0, e = 0, f = 0;
     if (vp::read_fault(&a, clear != 0) != cudaSuccess || vp::read_linear_logp_fault(&b, clear != 0) != cudaSuccess ||
         vp::read_linear_ent_kl_fault(&c, clear != 0) != cudaSuccess ||
         vp::read_linear_mxfp4_fault(&d, clear != 0) != cudaSuccess ||
-        vp::read_rules_fault(&e, clear != 0) != cudaSuccess)
+        vp::read_rules_fault(&e, clear != 0) != cudaSuccess ||
+        vp::read_linear_ce_fault(&f, clear != 0) != cudaSuccess)
         return VP_ERR_LAUNCH;
-    *value = vp::fault_word(a, b | c | d, e);
+    *value = vp::fault_word(a, b | c | d | f, e);
     return VP_OK;
 }
 
@@ -833,4 +834,259 @@ vp_status vp_linear_mxfp4_fwd(const uint8_t *x_codes, const uint8_t *x_scales, c
     if (st != VP_OK) return st;
     vp::LinearMxfp4Args a{x_codes, x_scales, w_codes, w_scales, N, V, D, y, dtype == VP_BF16, (cudaStream_t)stream};
     return launched(vp::launch_linear_mxfp4(a));
+}
+
+// ---------------------------------------------------------------------------
+// Cross entropy
+// ---------------------------------------------------------------------------
+namespace {
+
+vp_status ce_options(double label_smoothing, double z_loss, double softcap, int64_t V, int64_t vocab_total,
+                     vp::CeOptions *out) {
+    if (!(label_smoothing >= 0.0 && label_smoothing <= 1.0)) return VP_ERR_ARG;
+    if (!(z_loss >= 0.0 && z_loss <= 1e30)) return VP_ERR_ARG;
+    if (!(softcap == 0.0 || (softcap >= 1e-30 && softcap <= 1e30))) return VP_ERR_ARG;
+    if (vocab_total != 0 && vocab_total < V) return VP_ERR_SHAPE;
+    *out = vp::CeOptions{label_smoothing, z_loss, softcap, vocab_total ? vocab_total : V};
+    return VP_OK;
+}
+
+vp::CeArgs ce_args(const void *x, int dtype, int64_t N, int64_t V, int64_t R, int64_t s_o, int64_t s_i,
+                   int64_t vocab_start, const vp::CeOptions &opt, const int64_t *targets, vp_stream stream) {
+    return vp::CeArgs{x, dtype == VP_BF16, N, V, R, s_o, s_i, vocab_start, opt, targets, (cudaStream_t)stream};
+}
+
+}  // namespace
+
+size_t vp_cross_entropy_workspace_size(int64_t N, int64_t V) {
+    if (N < 0 || N > kMaxRowsPerLaunch || V < 1 || V > kMaxV) return 0;
+    return (size_t)vp::ce_workspace_bytes(false, N, V);   // fp32 rows have the more slices
+}
+
+vp_status vp_cross_entropy_fwd(const void *x, int dtype, int64_t N, int64_t V, int64_t R, int64_t s_o, int64_t s_i,
+                               int64_t vocab_start, double label_smoothing, double z_loss, double softcap,
+                               const int64_t *targets, float *loss, vp_rowstat *stats, void *workspace,
+                               size_t workspace_bytes, int32_t *err_word, vp_stream stream) {
+    vp::CeOptions opt;
+    vp_status st = check_rows(dtype, N, V, R, s_o, s_i);
+    if (st != VP_OK) return st;
+    if ((st = ce_options(label_smoothing, z_loss, softcap, V, 0, &opt)) != VP_OK) return st;
+    if (N == 0) return VP_OK;
+    if (!x || !targets || !loss || !stats || !workspace) return VP_ERR_NULL;
+    if (!aligned(x, elem_size(dtype)) || !aligned(targets, 8) || !aligned(loss, 4) || !aligned(stats, 16) ||
+        !aligned(workspace, 8) || !aligned(err_word, 4))
+        return VP_ERR_ALIGN;
+    if (workspace_bytes < vp_cross_entropy_workspace_size(N, V)) return VP_ERR_ARG;
+    if ((st = check_device()) != VP_OK) return st;
+    vp::CeArgs a = ce_args(x, dtype, N, V, R, s_o, s_i, vocab_start, opt, targets, stream);
+    a.loss = loss;
+    a.stats = stats;
+    a.workspace = workspace;
+    a.err = err_word;
+    return launched(vp::launch_ce_fwd(a));
+}
+
+vp_status vp_cross_entropy_bwd(const void *x, int dtype, int64_t N, int64_t V, int64_t R, int64_t s_o, int64_t s_i,
+                               int64_t vocab_start, int64_t vocab_total, double label_smoothing, double z_loss,
+                               double softcap, const int64_t *targets, const vp_rowstat *stats, const float *grad_out,
+                               void *dx, int32_t *err_word, vp_stream stream) {
+    vp::CeOptions opt;
+    vp_status st = check_rows(dtype, N, V, R, s_o, s_i);
+    if (st != VP_OK) return st;
+    if ((st = ce_options(label_smoothing, z_loss, softcap, V, vocab_total, &opt)) != VP_OK) return st;
+    if (N == 0) return VP_OK;
+    if (!x || !targets || !stats || !grad_out || !dx) return VP_ERR_NULL;
+    const size_t es = elem_size(dtype);
+    if (!aligned(x, es) || !aligned(dx, es) || !aligned(targets, 8) || !aligned(stats, 16) ||
+        !aligned(grad_out, 4) || !aligned(err_word, 4))
+        return VP_ERR_ALIGN;
+    if ((st = check_device()) != VP_OK) return st;
+    vp::CeArgs a = ce_args(x, dtype, N, V, R, s_o, s_i, vocab_start, opt, targets, stream);
+    a.stats = const_cast<vp_rowstat *>(stats);
+    a.g = grad_out;
+    a.dx = dx;
+    a.err = err_word;
+    return launched(vp::launch_ce_bwd(a));
+}
+
+vp_status vp_cross_entropy_partial(const void *x, int dtype, int64_t N, int64_t V, int64_t R, int64_t s_o, int64_t s_i,
+                                   int64_t vocab_start, double softcap, const int64_t *targets, vp_partial *parts,
+                                   void *workspace, size_t workspace_bytes, vp_stream stream) {
+    vp::CeOptions opt;
+    vp_status st = check_rows(dtype, N, V, R, s_o, s_i);
+    if (st != VP_OK) return st;
+    if ((st = ce_options(0.0, 0.0, softcap, V, 0, &opt)) != VP_OK) return st;
+    if (N == 0) return VP_OK;
+    if (!x || !targets || !parts || !workspace) return VP_ERR_NULL;
+    if (!aligned(x, elem_size(dtype)) || !aligned(targets, 8) || !aligned(parts, 8) || !aligned(workspace, 8))
+        return VP_ERR_ALIGN;
+    if (workspace_bytes < vp_cross_entropy_workspace_size(N, V)) return VP_ERR_ARG;
+    if ((st = check_device()) != VP_OK) return st;
+    vp::CeArgs a = ce_args(x, dtype, N, V, R, s_o, s_i, vocab_start, opt, targets, stream);
+    a.parts = parts;
+    a.workspace = workspace;
+    return launched(vp::launch_ce_fwd(a));
+}
+
+vp_status vp_cross_entropy_merge(const vp_partial *parts, int64_t K, int64_t N, double label_smoothing, double z_loss,
+                                 float *loss, vp_rowstat *stats, int32_t *err_word, vp_stream stream) {
+    vp::CeOptions opt;
+    vp_status st = check_merge(parts, K, N);
+    if (st != VP_OK) return st;
+    if ((st = ce_options(label_smoothing, z_loss, 0.0, 1, 0, &opt)) != VP_OK) return st;
+    if (N == 0) return VP_OK;
+    if (!loss || !stats) return VP_ERR_NULL;
+    if (!aligned(loss, 4) || !aligned(stats, 16) || !aligned(err_word, 4)) return VP_ERR_ALIGN;
+    if ((st = check_device()) != VP_OK) return st;
+    vp::CeArgs a = ce_args(nullptr, VP_F32, N, 1, 1, 0, 0, 0, opt, nullptr, stream);
+    a.loss = loss;
+    a.stats = stats;
+    a.err = err_word;
+    return launched(vp::launch_ce_merge(a, parts, K));
+}
+
+size_t vp_linear_cross_entropy_workspace_size(int64_t N, int64_t V, int64_t D) {
+    return linear_dims_ok(N, V, D) ? vp::linear_ce_workspace_bytes(N, V) : 0;
+}
+
+size_t vp_linear_cross_entropy_bwd_workspace_size(int64_t N, int64_t V, int64_t D) {
+    return linear_dims_ok(N, V, D) ? vp::linear_ce_bwd_workspace_bytes(N, V, D) : 0;
+}
+
+static vp_status linear_ce_fwd(const void *hidden, const void *weight, int64_t N, int64_t V, int64_t D,
+                               int64_t vocab_start, double label_smoothing, double z_loss, double softcap,
+                               const int64_t *targets, float *loss, vp_rowstat *stats, vp_partial *parts,
+                               void *workspace, size_t workspace_bytes, int32_t *err_word, vp_stream stream) {
+    vp::CeOptions opt;
+    if (!linear_dims_ok(N, V, D)) return VP_ERR_SHAPE;
+    vp_status st = ce_options(label_smoothing, z_loss, softcap, V, 0, &opt);
+    if (st != VP_OK) return st;
+    if (N == 0) return VP_OK;
+    if (!hidden || !weight || !targets || !(parts || (loss && stats)) || !workspace) return VP_ERR_NULL;
+    if (!aligned(hidden, 16) || !aligned(weight, 16) || !aligned(targets, 8) || !aligned(loss, 4) ||
+        !aligned(stats, 16) || !aligned(parts, 8) || !aligned(workspace, 256) || !aligned(err_word, 4))
+        return VP_ERR_ALIGN;
+    if (workspace_bytes < vp::linear_ce_workspace_bytes(N, V)) return VP_ERR_ARG;
+    if ((st = check_device()) != VP_OK) return st;
+    vp::CeArgs a = ce_args(nullptr, VP_BF16, N, V, 1, 0, 0, vocab_start, opt, targets, stream);
+    a.hidden = hidden;
+    a.weight = weight;
+    a.D = D;
+    a.loss = loss;
+    a.stats = stats;
+    a.parts = parts;
+    a.workspace = workspace;
+    a.err = err_word;
+    return launched(vp::launch_linear_ce_fwd(a));
+}
+
+vp_status vp_linear_cross_entropy_fwd(const void *hidden, const void *weight, int64_t N, int64_t V, int64_t D,
+                                      int64_t vocab_start, double label_smoothing, double z_loss, double softcap,
+                                      const int64_t *targets, float *loss, vp_rowstat *stats, void *workspace,
+                                      size_t workspace_bytes, int32_t *err_word, vp_stream stream) {
+    return linear_ce_fwd(hidden, weight, N, V, D, vocab_start, label_smoothing, z_loss, softcap, targets, loss, stats,
+                         nullptr, workspace, workspace_bytes, err_word, stream);
+}
+
+vp_status vp_linear_cross_entropy_partial(const void *hidden, const void *weight, int64_t N, int64_t V, int64_t D,
+                                          int64_t vocab_start, double softcap, const int64_t *targets,
+                                          vp_partial *parts, void *workspace, size_t workspace_bytes,
+                                          vp_stream stream) {
+    if (linear_dims_ok(N, V, D) && N > 0 && !parts) return VP_ERR_NULL;
+    return linear_ce_fwd(hidden, weight, N, V, D, vocab_start, 0.0, 0.0, softcap, targets, nullptr, nullptr, parts,
+                         workspace, workspace_bytes, nullptr, stream);
+}
+
+vp_status vp_linear_cross_entropy_bwd(const void *hidden, const void *weight, int64_t N, int64_t V, int64_t D,
+                                      int64_t vocab_start, int64_t vocab_total, double label_smoothing, double z_loss,
+                                      double softcap, const int64_t *targets, const vp_rowstat *stats,
+                                      const float *grad_out, void *dhidden, void *dW, int precision, void *workspace,
+                                      size_t workspace_bytes, int32_t *err_word, vp_stream stream) {
+    vp::CeOptions opt;
+    if (!linear_dims_ok(N, V, D)) return VP_ERR_SHAPE;
+    if (!dhidden && !dW) return VP_ERR_ARG;
+    if (!precision_ok(precision)) return VP_ERR_ARG;
+    vp_status st = ce_options(label_smoothing, z_loss, softcap, V, vocab_total, &opt);
+    if (st != VP_OK) return st;
+    if (N == 0 && !dW) return VP_OK;
+    if (!aligned(dhidden, 16) || !aligned(dW, 16)) return VP_ERR_ALIGN;
+    if (N == 0) {                                          // a sum over no rows
+        if ((st = check_device()) != VP_OK) return st;
+        return launched(cudaMemsetAsync(dW, 0, (size_t)V * D * 2, (cudaStream_t)stream));
+    }
+    if (!hidden || !weight || !targets || !stats || !grad_out || !workspace) return VP_ERR_NULL;
+    if (!aligned(hidden, 16) || !aligned(weight, 16) || !aligned(targets, 8) || !aligned(stats, 16) ||
+        !aligned(grad_out, 4) || !aligned(workspace, 256) || !aligned(err_word, 4))
+        return VP_ERR_ALIGN;
+    if (workspace_bytes < vp::linear_ce_bwd_workspace_bytes(N, V, D)) return VP_ERR_ARG;
+    if ((st = check_device()) != VP_OK) return st;
+    vp::CeArgs a = ce_args(nullptr, VP_BF16, N, V, 1, 0, 0, vocab_start, opt, targets, stream);
+    a.hidden = hidden;
+    a.weight = weight;
+    a.D = D;
+    a.stats = const_cast<vp_rowstat *>(stats);
+    a.g = grad_out;
+    a.dhidden = dhidden;
+    a.dW = dW;
+    a.precision = precision;
+    a.workspace = workspace;
+    a.err = err_word;
+    return launched(vp::launch_linear_ce_bwd(a));
+}
+
+// ---------------------------------------------------------------------------
+// Embedding
+// ---------------------------------------------------------------------------
+namespace {
+bool dtype_ok(int dtype) { return dtype == VP_F32 || dtype == VP_BF16; }
+bool embedding_dims_ok(int64_t N, int64_t V, int64_t D) {
+    return N >= 0 && N <= kMaxRowsPerLaunch && V >= 1 && V < kMaxV && D >= 1 && D <= (1 << 20);
+}
+}  // namespace
+
+vp_status vp_embedding_fwd(const void *table, int dtype, int64_t V, int64_t D, int64_t row_stride, const int64_t *ids,
+                           int64_t N, int64_t vocab_start, int sharded, double scale, void *out, int out_dtype,
+                           int32_t *err_word, vp_stream stream) {
+    if (!dtype_ok(dtype) || !dtype_ok(out_dtype)) return VP_ERR_DTYPE;
+    if (!embedding_dims_ok(N, V, D)) return VP_ERR_SHAPE;
+    if (row_stride < 0) return VP_ERR_LAYOUT;
+    if (N == 0) return VP_OK;
+    if (!table || !ids || !out) return VP_ERR_NULL;
+    if (!aligned(table, elem_size(dtype)) || !aligned(out, elem_size(out_dtype)) || !aligned(ids, 8) ||
+        !aligned(err_word, 4))
+        return VP_ERR_ALIGN;
+    vp_status st = check_device();
+    if (st != VP_OK) return st;
+    vp::EmbeddingArgs a{table, dtype == VP_BF16, out_dtype == VP_BF16, N, V, D, 1, 0, row_stride, vocab_start, ids,
+                        (float)scale, sharded != 0, out, false, err_word, nullptr, (cudaStream_t)stream};
+    return launched(vp::launch_embedding_fwd(a));
+}
+
+size_t vp_embedding_bwd_workspace_size(int64_t N, int64_t V, int64_t D) {
+    return embedding_dims_ok(N, V, D) ? vp::embedding_bwd_workspace_bytes(N, V, D) : 0;
+}
+
+vp_status vp_embedding_bwd(const void *dy, int dtype, int64_t N, int64_t D, int64_t R, int64_t s_o, int64_t s_i,
+                           const int64_t *ids, int64_t V, int64_t vocab_start, int sharded, double scale, void *dW,
+                           int out_dtype, int accumulate, void *workspace, size_t workspace_bytes, int32_t *err_word,
+                           vp_stream stream) {
+    if (!dtype_ok(dtype) || !dtype_ok(out_dtype)) return VP_ERR_DTYPE;
+    if (!embedding_dims_ok(N, V, D) || R < 1) return VP_ERR_SHAPE;
+    if (s_o < 0 || s_i < 0) return VP_ERR_LAYOUT;
+    if (N == 0 && accumulate) return VP_OK;
+    if (!dW) return VP_ERR_NULL;
+    if (!aligned(dW, elem_size(out_dtype))) return VP_ERR_ALIGN;
+    vp_status st;
+    if (N == 0) {                                          // a sum over no tokens
+        if ((st = check_device()) != VP_OK) return st;
+        return launched(cudaMemsetAsync(dW, 0, (size_t)V * D * elem_size(out_dtype), (cudaStream_t)stream));
+    }
+    if (!dy || !ids || !workspace) return VP_ERR_NULL;
+    if (!aligned(dy, elem_size(dtype)) || !aligned(ids, 8) || !aligned(workspace, 256) || !aligned(err_word, 4))
+        return VP_ERR_ALIGN;
+    if (workspace_bytes < vp::embedding_bwd_workspace_bytes(N, V, D)) return VP_ERR_ARG;
+    if ((st = check_device()) != VP_OK) return st;
+    vp::EmbeddingArgs a{dy, dtype == VP_BF16, out_dtype == VP_BF16, N, V, D, R, s_o, s_i, vocab_start, ids,
+                        (float)scale, sharded != 0, dW, accumulate != 0, err_word, workspace, (cudaStream_t)stream};
+    return launched(vp::launch_embedding_bwd(a));
 }

@@ -1,0 +1,446 @@
+// vp_embedding.cu -- rows of the vocabulary's table for token ids, and the table's gradient.
+//
+//   forward   y_n = s W[id_n]; an id < 0 (padding) or of another shard gives a zero row
+//   backward  dW[v] = s sum_{n: id_n = v} dy_n, or that added to what dW holds
+//
+// Forward: a warp for a piece of 32 x 4 vectors of 8 columns of one row, so that the four
+//   loads of a lane are on their way together. Bound: DRAM bytes.
+// Backward, three launches:
+//   1. token_sort_kernel: the tokens in the order of their ids (and of their positions
+//      among equal ids). Each CTA owns a range of ids and goes over all N ids twice, once to
+//      count and once to place its own: no CTA waits for another, no atomic decides an order.
+//      The ids come from L2, 8 bytes for each CTA and token against 2 D or 4 D of dy.
+//   2. table_grad_kernel: windows of the sorted tokens, each summed in fp32 in order; a
+//      run of one id that lies in a window is written at once, the ends of runs that cross
+//      windows are left as fp32 partial sums. More CTAs write zeros to rows no token asks for.
+//   3. table_join_kernel: the partial sums of such runs, in the order of the windows, as
+//      double-floats.
+//   Every sum's order follows from the ids alone, so the result is the same every time, and
+//   an id that takes half of a batch is spread over as many CTAs as it has windows.
+//   Bound: DRAM bytes of dy and dW.
+#include "vp_device.cuh"
+#include "vp_launch.h"
+
+namespace vp {
+
+constexpr int kEmbVec = 8;   // columns of a vector: 16 bytes of bf16, 32 of fp32
+
+// Columns c .. c + 7 (vectors) or c, c + step, .. (single elements) of a row, as fp32.
+template <typename T, bool kVector>
+__device__ __forceinline__ void load8(const T *row, int c, int step, int D, float (&v)[kEmbVec]) {
+    if constexpr (kVector) {
+        if constexpr (sizeof(T) == 2) {
+            Elem<T>::unpack(ldg_stream(row + c), v);
+        } else {
+            const uint4 a = ldg_stream(row + c), b = ldg_stream(row + c + 4);
+            v[0] = __uint_as_float(a.x); v[1] = __uint_as_float(a.y); v[2] = __uint_as_float(a.z); v[3] = __uint_as_float(a.w);
+            v[4] = __uint_as_float(b.x); v[5] = __uint_as_float(b.y); v[6] = __uint_as_float(b.z); v[7] = __uint_as_float(b.w);
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < kEmbVec; ++e) v[e] = c + e * step < D ? Elem<T>::load1(row + c + e * step) : 0.f;
+    }
+}
+
+template <typename T, bool kVector>
+__device__ __forceinline__ void store8(T *row, int c, int step, int D, const float (&v)[kEmbVec]) {
+    if constexpr (kVector) {
+        if constexpr (sizeof(T) == 2) {
+            stg_stream(row + c, Elem<T>::pack(v));
+        } else {
+            stg_stream(row + c, Elem<float>::pack(v));
+            stg_stream(row + c + 4, Elem<float>::pack(v + 4));
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < kEmbVec; ++e)
+            if (c + e * step < D) Elem<T>::store1(row + c + e * step, v[e]);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Forward
+// ---------------------------------------------------------------------------
+constexpr int kEmbThreads = 128, kEmbUnroll = 4;
+constexpr int kEmbPiece = 32 * kEmbUnroll * kEmbVec;   // columns of a warp's piece
+
+template <typename TI, typename TO, bool kVector>
+__global__ void __launch_bounds__(kEmbThreads)
+embedding_fwd_kernel(const TI *__restrict__ table, int64_t pitch, int V, int D, const int64_t *__restrict__ ids,
+                     int64_t vocab_start, float scale, bool sharded, TO *__restrict__ out, int32_t *__restrict__ err,
+                     int pieces, int64_t total) {
+    pdl_enter<true>();   // no global access before this
+    const int lane = threadIdx.x & 31;
+    const int64_t step = (int64_t)gridDim.x * (kEmbThreads / 32);
+    for (int64_t i = (int64_t)blockIdx.x * (kEmbThreads / 32) + (threadIdx.x >> 5); i < total; i += step) {
+        const int64_t n = i / pieces;
+        const int c0 = (int)(i - n * pieces) * kEmbPiece;
+        const int64_t id = ids[n], local = id - vocab_start;
+        const bool here = id >= 0 && local >= 0 && local < V;
+        const bool wrong = id >= 0 && !here && !sharded;
+        if (wrong && err && c0 == 0 && lane == 0) atomicOr(err, VP_ERRBIT_TARGET_);
+        const TI *row = table + (here ? local : 0) * pitch;
+        TO *dst = out + n * (int64_t)D;
+        float v[kEmbUnroll][kEmbVec];
+#pragma unroll
+        for (int k = 0; k < kEmbUnroll; ++k) {
+            const int c = kVector ? c0 + (k * 32 + lane) * kEmbVec : c0 + k * 32 * kEmbVec + lane;
+            if (here && c < D) load8<TI, kVector>(row, c, 32, D, v[k]);
+        }
+#pragma unroll
+        for (int k = 0; k < kEmbUnroll; ++k) {
+            const int c = kVector ? c0 + (k * 32 + lane) * kEmbVec : c0 + k * 32 * kEmbVec + lane;
+            if (c >= D) continue;
+#pragma unroll
+            for (int e = 0; e < kEmbVec; ++e) v[k][e] = here ? v[k][e] * scale : wrong ? qnan() : 0.f;
+            store8<TO, kVector>(dst, c, 32, D, v[k]);
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Backward
+// ---------------------------------------------------------------------------
+constexpr int kSortThreads = 1024, kSortWarps = kSortThreads / 32;
+constexpr int kSortMaxBins = 1024;               // ids of a CTA's range: a thread each in the scan, 128 KB of counters
+
+// The tokens of the shard in the order of their ids: rows[k] and positions[k] of the k-th,
+// first[v] .. first[v + 1] those of row v. CTA b owns the rows from b * bins on. A warp goes
+// over the same stretch of positions in both passes, so its counters, made offsets by the scan
+// (row by row, and warp by warp within a row), place its tokens behind those of earlier stretches.
+__global__ void __launch_bounds__(kSortThreads)
+token_sort_kernel(const int64_t *__restrict__ ids, int64_t N, int V, int64_t vocab_start, bool sharded, int bins,
+                  int *__restrict__ first, int *__restrict__ rows, int *__restrict__ positions,
+                  int32_t *__restrict__ err) {
+    extern __shared__ uint32_t counts[];         // [kSortWarps][bins]
+    __shared__ uint32_t s_sum[kSortWarps];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    for (int i = tid; i < kSortWarps * bins; i += kSortThreads) counts[i] = 0u;
+    __syncthreads();
+    pdl_enter<false>();
+    const int64_t lo = (int64_t)blockIdx.x * bins;
+    const int64_t stretch = ((N + kSortWarps - 1) / kSortWarps + 31) & ~(int64_t)31;
+    const int64_t p0 = min(N, warp * stretch), p1 = min(N, p0 + stretch);
+    uint32_t *mine = counts + warp * bins;
+    uint32_t below = 0;
+    bool wrong = false;
+    for (int64_t p = p0 + lane; p < p1; p += 32) {
+        const int64_t id = ids[p], local = id - vocab_start;
+        if (id < 0) continue;
+        if (local < 0 || local >= V) {
+            wrong = true;
+            continue;
+        }
+        if (local < lo) ++below;
+        else if (local < lo + bins) atomicAdd(&mine[local - lo], 1u);
+    }
+    if (wrong && !sharded && err && blockIdx.x == 0) atomicOr(err, VP_ERRBIT_TARGET_);
+    below = __reduce_add_sync(0xffffffffu, below);
+    if (lane == 0) s_sum[warp] = below;
+    __syncthreads();
+    uint32_t base = __reduce_add_sync(0xffffffffu, s_sum[lane]);
+    __syncthreads();
+
+    // thread t has row lo + t: its tokens, then the offsets of its warps' counters
+    uint32_t n = 0;
+    if (tid < bins)
+        for (int w = 0; w < kSortWarps; ++w) n += counts[w * bins + tid];
+    uint32_t scan = n;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const uint32_t o = __shfl_up_sync(0xffffffffu, scan, d);
+        if (lane >= d) scan += o;
+    }
+    if (lane == 31) s_sum[warp] = scan;
+    __syncthreads();
+    const uint32_t sums = s_sum[lane];
+    base += __reduce_add_sync(0xffffffffu, lane < warp ? sums : 0u) + scan - n;
+    if (tid < bins) {
+        if (lo + tid <= V) first[lo + tid] = (int)base;
+        if (tid == bins - 1 && lo + bins >= V) first[V] = (int)(base + n);
+        for (int w = 0; w < kSortWarps; ++w) {
+            const uint32_t c = counts[w * bins + tid];
+            counts[w * bins + tid] = base;
+            base += c;
+        }
+    }
+    __syncthreads();
+
+    for (int64_t q = p0; q < p1; q += 32) {
+        const int64_t p = q + lane;
+        const int64_t id = p < p1 ? ids[p] : -1, local = id - vocab_start;
+        const bool own = id >= 0 && local >= lo && local < lo + bins && local < V;
+        if (!__any_sync(0xffffffffu, own)) continue;
+        const uint32_t bin = own ? (uint32_t)(local - lo) : 0xffffffffu;
+        const uint32_t peers = __match_any_sync(0xffffffffu, bin);
+        const uint32_t before = __popc(peers & ((1u << lane) - 1u));
+        uint32_t at = 0;
+        if (own) at = mine[bin] + before;
+        __syncwarp();
+        if (own) {
+            if (before == 0) mine[bin] += __popc(peers);
+            rows[at] = (int)local;
+            positions[at] = (int)p;
+        }
+        __syncwarp();
+    }
+}
+
+constexpr int kGradThreads = 256;
+constexpr int kGradMaxWindow = 64;
+
+struct TableGrad {
+    int64_t N;
+    int V, D, window, n_windows, col_blocks;
+    Rows dy_rows;
+    float scale;
+    const int *first, *rows, *positions;
+    float *partial;             // [n_windows][2][D]: what belongs to a run begun in an earlier window, and
+                                // what belongs to one that goes on in later ones
+};
+
+// The row of table, its new value from the sum.
+template <typename TO, bool kVector, bool kAdd>
+__device__ __forceinline__ void finish8(TO *dst, int c, int step, int D, float scale, float (&v)[kEmbVec]) {
+    if constexpr (kAdd) {
+        float o[kEmbVec];
+        if constexpr (kVector && sizeof(TO) == 2) {
+            const uint4 u = *reinterpret_cast<const uint4 *>(dst + c);
+            Elem<TO>::unpack(u, o);
+        } else {
+#pragma unroll
+            for (int e = 0; e < kEmbVec; ++e) {
+                const int k = kVector ? c + e : c + e * step;
+                o[e] = kVector || k < D ? (float)dst[k] : 0.f;
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < kEmbVec; ++e) v[e] = fmaf(v[e], scale, o[e]);
+    } else {
+#pragma unroll
+        for (int e = 0; e < kEmbVec; ++e) v[e] *= scale;
+    }
+    store8<TO, kVector>(dst, c, step, D, v);
+}
+
+template <typename TI, typename TO, bool kVector, bool kAdd>
+__global__ void __launch_bounds__(kGradThreads)
+table_grad_kernel(const TI *__restrict__ dy, const TableGrad a, TO *__restrict__ dW, int fill_rows) {
+    __shared__ int s_row[kGradMaxWindow];
+    __shared__ int64_t s_off[kGradMaxWindow];
+    const int tid = threadIdx.x, nt = blockDim.x;
+    pdl_enter<false>();
+    const int total = a.first[a.V];              // tokens of this shard
+    int64_t b = blockIdx.x;
+    const int64_t n_sum = (int64_t)a.n_windows * a.col_blocks;
+    if (b >= n_sum) {
+        // zeros for rows that no token asks for
+        if constexpr (!kAdd) {
+            const int64_t v0 = (b - n_sum) * fill_rows, v1 = min((int64_t)a.V, v0 + fill_rows);
+            const float zero[kEmbVec] = {};
+            for (int64_t v = v0; v < v1; ++v) {
+                if (a.first[v + 1] != a.first[v]) continue;
+                TO *dst = dW + v * (int64_t)a.D;
+                if (kVector) for (int c = tid * kEmbVec; c < a.D; c += nt * kEmbVec) store8<TO, true>(dst, c, 1, a.D, zero);
+                else for (int c = tid; c < a.D; c += nt) Elem<TO>::store1(dst + c, 0.f);
+            }
+        }
+        return;
+    }
+    const int w = (int)(b / a.col_blocks), cb = (int)(b - (int64_t)w * a.col_blocks);
+    const int64_t k0 = (int64_t)w * a.window, k1 = min((int64_t)total, k0 + a.window);
+    if (k0 >= k1) return;
+    for (int i = tid; i < (int)(k1 - k0); i += nt) {
+        s_row[i] = a.rows[k0 + i];
+        s_off[i] = a.dy_rows.off(a.positions[k0 + i]);
+    }
+    __syncthreads();
+    const int c = cb * nt * kEmbVec + (kVector ? tid * kEmbVec : tid), step = nt;
+    if (c >= a.D) return;
+    const int count = (int)(k1 - k0);
+    float sum[kEmbVec] = {};
+    constexpr int kAhead = 4;
+    for (int i = 0; i < count; i += kAhead) {
+        float v[kAhead][kEmbVec];
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k)
+            if (i + k < count) load8<TI, kVector>(dy + s_off[i + k], c, step, a.D, v[k]);
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            if (i + k >= count) break;
+#pragma unroll
+            for (int e = 0; e < kEmbVec; ++e) sum[e] += v[k][e];
+            const int row = s_row[i + k];
+            if (i + k + 1 < count && s_row[i + k + 1] == row) continue;
+            // the run ends here, or the window does
+            const bool begun_before = a.first[row] < k0, goes_on = a.first[row + 1] > k1;
+            if (begun_before || goes_on) {
+                float *part = a.partial + ((int64_t)w * 2 + (begun_before ? 0 : 1)) * a.D;
+                if (kVector) {
+                    *reinterpret_cast<float4 *>(part + c) = make_float4(sum[0], sum[1], sum[2], sum[3]);
+                    *reinterpret_cast<float4 *>(part + c + 4) = make_float4(sum[4], sum[5], sum[6], sum[7]);
+                } else {
+                    store8<float, false>(part, c, step, a.D, sum);
+                }
+            } else {
+                finish8<TO, kVector, kAdd>(dW + row * (int64_t)a.D, c, step, a.D, a.scale, sum);
+            }
+#pragma unroll
+            for (int e = 0; e < kEmbVec; ++e) sum[e] = 0.f;
+        }
+    }
+}
+
+// A CTA for each window and 32 columns: where a run begins in the window and goes on, eight
+// warps add its partial sums, warp j those of windows w + j, w + j + 8, ..; then one adds the eight.
+constexpr int kJoinWarps = 8;
+template <typename TO, bool kAdd>
+__global__ void __launch_bounds__(kJoinWarps * 32)
+table_join_kernel(const TableGrad a, TO *__restrict__ dW) {
+    __shared__ DF s_sum[kJoinWarps][32];
+    pdl_enter<false>();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int w = blockIdx.x;
+    const int64_t total = a.first[a.V];
+    const int64_t k1 = (int64_t)(w + 1) * a.window;
+    if (k1 >= total) return;                                          // nothing behind this window
+    const int row = a.rows[k1 - 1];
+    if (a.first[row] < k1 - a.window || a.first[row + 1] <= k1) return;   // begun earlier, or ends here
+    const int last = (a.first[row + 1] - 1) / a.window;
+    for (int c0 = blockIdx.y * 32; c0 < a.D; c0 += gridDim.y * 32) {
+        const int c = c0 + lane;
+        DF sum{0.f, 0.f};
+        if (c < a.D)
+            for (int u = w + warp; u <= last; u += kJoinWarps)
+                df_add(sum, a.partial[((int64_t)u * 2 + (u == w ? 1 : 0)) * a.D + c]);
+        s_sum[warp][lane] = sum;
+        __syncthreads();
+        if (warp == 0 && c < a.D) {
+            for (int j = 1; j < kJoinWarps; ++j) df_add(sum, s_sum[j][lane]);
+            TO *dst = dW + row * (int64_t)a.D + c;
+            const float s = sum.hi + sum.lo;
+            Elem<TO>::store1(dst, kAdd ? fmaf(s, a.scale, (float)*dst) : s * a.scale);
+        }
+        __syncthreads();
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Host side
+// ---------------------------------------------------------------------------
+namespace {
+
+int sm_count() {
+    int dev = 0, sms = 0;
+    cudaGetDevice(&dev);
+    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    return sms > 0 ? sms : 1;
+}
+
+// Tokens of a window: enough windows for a few CTAs on every SM, and as long as that allows, since
+// a window costs up to two partial rows.
+int grad_window(int64_t N) {
+    int w = 8;
+    while (w < kGradMaxWindow && N > (int64_t)w * 256) w *= 2;
+    return w;
+}
+
+struct GradLayout {
+    size_t rows, positions, partial, total;
+};
+GradLayout grad_layout(int64_t N, int64_t V, int64_t D) {
+    auto up = [](size_t x) { return (x + 255) & ~(size_t)255; };
+    const int64_t windows = (N + grad_window(N) - 1) / grad_window(N);
+    GradLayout L;
+    L.rows = up((size_t)(V + 1) * 4);
+    L.positions = L.rows + up((size_t)N * 4);
+    L.partial = L.positions + up((size_t)N * 4);
+    L.total = L.partial + (size_t)windows * 2 * D * 4;
+    return L;
+}
+
+template <typename TI, typename TO>
+cudaError_t embedding_fwd(const EmbeddingArgs &a) {
+    const TI *x = static_cast<const TI *>(a.x);
+    TO *out = static_cast<TO *>(a.out);
+    const bool vector = a.D % kEmbVec == 0 && (uintptr_t)x % 16 == 0 && (uintptr_t)out % 16 == 0 &&
+                        a.s_i * sizeof(TI) % 16 == 0;
+    const int pieces = (int)((a.D + kEmbPiece - 1) / kEmbPiece);
+    const int64_t total = a.N * pieces, ctas = (total + kEmbThreads / 32 - 1) / (kEmbThreads / 32);
+    auto go = [&](auto kernel) {
+        return launch_pdl(kernel, dim3((unsigned)(ctas < 2147483647 ? ctas : 2147483647)), dim3(kEmbThreads), 0, a.stream,
+                          x, a.s_i, (int)a.V, (int)a.D, a.ids, a.vocab_start, a.scale, a.sharded, out, a.err, pieces, total);
+    };
+    return vector ? go(embedding_fwd_kernel<TI, TO, true>) : go(embedding_fwd_kernel<TI, TO, false>);
+}
+
+template <typename TI, typename TO>
+cudaError_t embedding_bwd(const EmbeddingArgs &a) {
+    const TI *dy = static_cast<const TI *>(a.x);
+    TO *dW = static_cast<TO *>(a.out);
+    const GradLayout L = grad_layout(a.N, a.V, a.D);
+    uint8_t *ws = static_cast<uint8_t *>(a.workspace);
+    int *first = reinterpret_cast<int *>(ws), *rows = reinterpret_cast<int *>(ws + L.rows),
+        *positions = reinterpret_cast<int *>(ws + L.positions);
+    // rows of a CTA's range in the sort: the table over the SMs, within what the counters have room for
+    const int sms = sm_count();
+    int64_t bins = (a.V + sms - 1) / sms;
+    bins = bins < 32 ? 32 : bins > kSortMaxBins ? kSortMaxBins : bins;
+    const size_t smem = (size_t)kSortWarps * bins * 4;
+    cudaError_t e = cudaFuncSetAttribute(token_sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         kSortWarps * kSortMaxBins * 4);
+    if (e != cudaSuccess) return e;
+    e = launch_pdl(token_sort_kernel, dim3((unsigned)((a.V + bins - 1) / bins)), dim3(kSortThreads), smem, a.stream,
+                   a.ids, a.N, (int)a.V, a.vocab_start, a.sharded, (int)bins, first, rows, positions, a.err);
+    if (e != cudaSuccess) return e;
+
+    const bool vector = a.D % kEmbVec == 0 && (uintptr_t)dy % 16 == 0 && (uintptr_t)dW % 16 == 0 &&
+                        a.s_i * sizeof(TI) % 16 == 0 && a.s_o * sizeof(TI) % 16 == 0;
+    const int threads = (int)(a.D >= kGradThreads * kEmbVec ? kGradThreads : ((a.D + kEmbVec - 1) / kEmbVec + 31) / 32 * 32);
+    TableGrad g;
+    g.N = a.N;
+    g.V = (int)a.V;
+    g.D = (int)a.D;
+    g.window = grad_window(a.N);
+    g.n_windows = (int)((a.N + g.window - 1) / g.window);
+    g.col_blocks = (int)((a.D + threads * kEmbVec - 1) / (threads * kEmbVec));
+    g.dy_rows = Rows{a.R, a.s_o, a.s_i};
+    g.scale = a.scale;
+    g.first = first;
+    g.rows = rows;
+    g.positions = positions;
+    g.partial = reinterpret_cast<float *>(ws + L.partial);
+    // about 64 KB of zeros for a CTA
+    const int64_t row_bytes = a.D * (int64_t)sizeof(TO);
+    const int fill_rows = (int)(row_bytes >= 65536 ? 1 : 65536 / row_bytes);
+    const int64_t fill_ctas = a.accumulate ? 0 : (a.V + fill_rows - 1) / fill_rows;
+    const int64_t ctas = (int64_t)g.n_windows * g.col_blocks + fill_ctas;
+    if (ctas > 2147483647) return cudaErrorInvalidValue;
+    auto go = [&](auto kernel) {
+        return launch_pdl(kernel, dim3((unsigned)ctas), dim3(threads), 0, a.stream, dy, g, dW, fill_rows);
+    };
+    e = vector ? (a.accumulate ? go(table_grad_kernel<TI, TO, true, true>) : go(table_grad_kernel<TI, TO, true, false>))
+               : (a.accumulate ? go(table_grad_kernel<TI, TO, false, true>) : go(table_grad_kernel<TI, TO, false, false>));
+    if (e != cudaSuccess || g.n_windows < 2) return e;
+    const dim3 grid((unsigned)(g.n_windows - 1), (unsigned)((a.D + 31) / 32 < 64 ? (a.D + 31) / 32 : 64));
+    return a.accumulate ? launch_pdl(table_join_kernel<TO, true>, grid, dim3(kJoinWarps * 32), 0, a.stream, g, dW)
+                        : launch_pdl(table_join_kernel<TO, false>, grid, dim3(kJoinWarps * 32), 0, a.stream, g, dW);
+}
+
+}  // namespace
+
+size_t embedding_bwd_workspace_bytes(int64_t N, int64_t V, int64_t D) { return grad_layout(N, V, D).total; }
+
+cudaError_t launch_embedding_fwd(const EmbeddingArgs &a) {
+    if (a.x_bf16)
+        return a.out_bf16 ? embedding_fwd<__nv_bfloat16, __nv_bfloat16>(a) : embedding_fwd<__nv_bfloat16, float>(a);
+    return a.out_bf16 ? embedding_fwd<float, __nv_bfloat16>(a) : embedding_fwd<float, float>(a);
+}
+
+cudaError_t launch_embedding_bwd(const EmbeddingArgs &a) {
+    if (a.x_bf16)
+        return a.out_bf16 ? embedding_bwd<__nv_bfloat16, __nv_bfloat16>(a) : embedding_bwd<__nv_bfloat16, float>(a);
+    return a.out_bf16 ? embedding_bwd<float, __nv_bfloat16>(a) : embedding_bwd<float, float>(a);
+}
+
+}  // namespace vp

@@ -245,6 +245,59 @@ cudaError_t launch_mxfp4_dequantize(const Mxfp4DequantArgs &a);
 cudaError_t launch_linear_mxfp4(const LinearMxfp4Args &a);
 cudaError_t read_linear_mxfp4_fault(uint32_t *value, bool clear);
 
+// Cross entropy: of logits x (rows of V), or of hidden . weight^T.
+struct CeOptions {
+    double smooth, zeta, cap;     // label smoothing, z-loss, cap on the logits (0: none)
+    int64_t vocab_total;          // columns of the whole vocabulary
+};
+struct CeArgs {
+    const void *x;                // logits
+    bool bf16;
+    int64_t N, V, R, s_o, s_i, vocab_start;
+    CeOptions opt;
+    const int64_t *targets;
+    cudaStream_t stream;
+    float *loss = nullptr;        // forward: fp32 [N]
+    void *stats = nullptr;        // vp_rowstat [N]: written by the forward, read by the backward
+    void *parts = nullptr;        // forward: vp_partial [N], the shard's records instead of loss and stats
+    const float *g = nullptr;     // backward: upstream gradient of the losses, fp32 [N]
+    void *dx = nullptr;           // backward: contiguous [N, V]
+    int32_t *err = nullptr;
+    void *workspace = nullptr;
+    // the linear form, bf16 row-major
+    const void *hidden = nullptr, *weight = nullptr;   // [N, D], [V, D]
+    int64_t D = 0;
+    void *dhidden = nullptr, *dW = nullptr;            // either may be NULL
+    int precision = 0;            // VP_GRAD_EXACT or VP_GRAD_FAST (as LinearBwdArgs)
+};
+int64_t ce_workspace_bytes(bool bf16, int64_t N, int64_t V);
+size_t linear_ce_workspace_bytes(int64_t N, int64_t V);
+size_t linear_ce_bwd_workspace_bytes(int64_t N, int64_t V, int64_t D);
+cudaError_t launch_ce_fwd(const CeArgs &a);
+cudaError_t launch_ce_merge(const CeArgs &a, const void *parts, int64_t K);   // gathered [K, N] records
+cudaError_t launch_ce_bwd(const CeArgs &a);
+cudaError_t launch_linear_ce_fwd(const CeArgs &a);
+cudaError_t launch_linear_ce_bwd(const CeArgs &a);
+cudaError_t read_linear_ce_fault(uint32_t *value, bool clear);
+
+// Embedding: rows of the table [V, D] for token ids, and the table's gradient.
+struct EmbeddingArgs {
+    const void *x;                // the table (row r at r * s_i), or dy (N rows with two strides)
+    bool x_bf16, out_bf16;
+    int64_t N, V, D, R, s_o, s_i, vocab_start;
+    const int64_t *ids;
+    float scale;
+    bool sharded;                 // ids outside the shard belong to another one
+    void *out;                    // rows [N, D], or the table's gradient [V, D], contiguous
+    bool accumulate;              // the gradient is added to what out holds
+    int32_t *err;
+    void *workspace;
+    cudaStream_t stream;
+};
+size_t embedding_bwd_workspace_bytes(int64_t N, int64_t V, int64_t D);
+cudaError_t launch_embedding_fwd(const EmbeddingArgs &a);
+cudaError_t launch_embedding_bwd(const EmbeddingArgs &a);
+
 cudaError_t launch_logprobs_fwd(const StatsArgs &a);
 cudaError_t launch_entropy_fwd(const StatsArgs &a);
 cudaError_t launch_logprobs_topk_fwd(const StatsArgs &a);
