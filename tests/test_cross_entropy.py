@@ -209,6 +209,27 @@ def test_masked_columns(dtype, fill):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("V", [700, 20000])
+def test_rows_of_a_types_ends(dtype, V):
+    """Rows of nothing but the type's lowest value (uniform, as the definition has it), and one-hot rows that span the
+    type: nothing overflows on the way."""
+    low, high = torch.finfo(dtype).min, torch.finfo(dtype).max
+    x = torch.full((4, V), low, dtype=dtype)
+    x[1, V - 3], x[2, 5], x[3, ::2] = high, 0.0, high
+    targets, g = torch.tensor([7, V - 3, 5, 0]), torch.tensor([1.0, -2.0, 0.5, 3.0])
+    loss, stats = vp.vp_cross_entropy_fwd(x.cuda(), targets.cuda())
+    ref = torch.tensor([math.log(V), 0.0, 0.0, math.log((V + 1) // 2)], dtype=torch.float64)
+    assert torch.allclose(loss.double().cpu(), ref, rtol=1e-6, atol=1e-6)
+    dx = vp.vp_cross_entropy_bwd(x.cuda(), targets.cuda(), stats, g.cuda()).double().cpu()
+    d = torch.zeros(4, V, dtype=torch.float64)
+    d[0], d[3, ::2] = 1.0 / V, 3.0 / ((V + 1) // 2)
+    d[0, 7] -= 1.0
+    d[3, 0] -= 3.0
+    assert torch.allclose(dx, d, rtol=torch.finfo(dtype).eps, atol=1e-7)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [F32, BF16])
 def test_rows_with_nothing_or_with_nan(dtype):
     x, _, g = rows(7, 5003, dtype, 13)
     x[1] = -math.inf

@@ -31,54 +31,120 @@ struct CeRules {
 constexpr float kCeScale = 5.9604644775390625e-08f;
 constexpr double kCeUnscale = 16777216.0;
 
-// t = tanh(y) and slope = 1 - t^2. Below 5/8: y (1 + s P(s)), s = y^2, P of degree 4 by
-// interpolation of tanh(y) / y at Chebyshev points (relative error 7.3e-8, all roundings
-// included); above: (1 - e) / (1 + e) and 4 e / (1 + e)^2 with e = e^{-2 |y|}, which do
-// not cancel there (relative error about 3e-7). A value takes its formula whatever its
-// neighbours are: the vote only spares a warp the second one when none of its values needs it.
+// z = c t and slope = 1 - t^2, t = tanh(y), y = x / c, of n (even) values. Below |y| = 5/8:
+// t = y (1 + s P(s)), s = y^2, P of degree 4 by interpolation of tanh(y) / y at Chebyshev
+// points (relative error 7.3e-8, all roundings included); above: (1 - e) / (1 + e) and
+// 4 e / (1 + e)^2 with e = e^{-2 |y|}, which do not cancel there (about 3e-7). A value takes
+// its formula whatever its neighbours are: the vote only spares a warp the second one when
+// none of its values needs it. Pairs of values go through f32x2 instructions.
 constexpr float kTanhSplit = 0.625f;
-template <int n>
-__device__ __forceinline__ void soft_cap(const CeRules &q, const float (&x)[n], float (&z)[n], float *slope) {
-    bool far = false;
-    float y[n];
+template <int n, bool kSlope>
+__device__ __forceinline__ void soft_cap(const CeRules &q, float (&x)[n], float (&slope)[n]) {
+    static_assert(n % 2 == 0, "pairs");
+    float far = 0.f;
+    float2 y[n / 2];
 #pragma unroll
-    for (int i = 0; i < n; ++i) {
-        y[i] = x[i] * q.inv_cap;
-        const float s = y[i] * y[i];
-        float p = fmaf(s, -0.005657135043293238f, 0.020588191226124763f);
-        p = fmaf(s, p, -0.05372010916471481f);
-        p = fmaf(s, p, 0.13331113755702972f);
-        p = fmaf(s, p, -0.3333325982093811f);
-        const float t = fmaf(y[i] * s, p, y[i]);
-        z[i] = t * q.cap;
-        if (slope) slope[i] = fmaf(-t, t, 1.f);
-        far |= !(fabsf(y[i]) < kTanhSplit);
+    for (int i = 0; i < n / 2; ++i) {
+        y[i] = __fmul2_rn(make_float2(x[2 * i], x[2 * i + 1]), f2(q.inv_cap));
+        far = fmaxf(far, fmaxf(fabsf(y[i].x), fabsf(y[i].y)));
+        const float2 s = __fmul2_rn(y[i], y[i]);
+        float2 p = __ffma2_rn(s, f2(-0.005657135043293238f), f2(0.020588191226124763f));
+        p = __ffma2_rn(s, p, f2(-0.05372010916471481f));
+        p = __ffma2_rn(s, p, f2(0.13331113755702972f));
+        p = __ffma2_rn(s, p, f2(-0.3333325982093811f));
+        const float2 t = __ffma2_rn(__fmul2_rn(y[i], s), p, y[i]);
+        const float2 z = __fmul2_rn(t, f2(q.cap));
+        x[2 * i] = z.x;
+        x[2 * i + 1] = z.y;
+        if (kSlope) {
+            const float2 m = __ffma2_rn(__fmul2_rn(t, f2(-1.f)), t, f2(1.f));
+            slope[2 * i] = m.x;
+            slope[2 * i + 1] = m.y;
+        }
     }
-    if (__any_sync(__activemask(), far)) {
+    if (__any_sync(__activemask(), far >= kTanhSplit)) {
 #pragma unroll
         for (int i = 0; i < n; ++i) {
+            const float v = i % 2 ? y[i / 2].y : y[i / 2].x;
             float e, r;
-            asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(fabsf(y[i]) * (-2.f * kLog2e)));
+            asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(fabsf(v) * (-2.f * kLog2e)));
             asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
-            if (!(fabsf(y[i]) < kTanhSplit)) {
-                z[i] = copysignf((1.f - e) * r, y[i]) * q.cap;
-                if (slope) slope[i] = 4.f * e * r * r;
+            if (fabsf(v) >= kTanhSplit) {
+                x[i] = copysignf((1.f - e) * r, v) * q.cap;
+                if (kSlope) slope[i] = 4.f * e * r * r;
             }
         }
     }
 }
-
-// g (a p - e / V), a = 1 + a1: a column's gradient before the cap's slope. At the target
-// 1 - e is taken away in a form that does not cancel as p -> 1: p - 1 = e^{log p} - 1.
-__device__ __forceinline__ float ce_grad(const CeRules &q, float p, float a1, float g) {
-    return g * fmaf(a1, p, p - q.share);
+template <int n>
+__device__ __forceinline__ void soft_cap(const CeRules &q, float (&x)[n]) {
+    float none[n];
+    soft_cap<n, false>(q, x, none);
 }
-__device__ __forceinline__ float ce_grad_target(const CeRules &q, float p, float lp, float a1, float g) {
+__device__ __forceinline__ float soft_cap1(const CeRules &q, float x, float *slope = nullptr) {
+    float v[2] = {x, 0.f}, m[2];
+    soft_cap<2, true>(q, v, m);
+    if (slope) *slope = m[0];
+    return v[0];
+}
+
+// Exponentials against a centre k: e^{z - k} = 2^{z l - c} f with l = fl(log2 e), c = fl(k l), so that
+// one FMA makes the argument of the hardware's 2^x. z l is exact inside the FMA, and f = 2^{c - k l}
+// takes back what rounding k l did to every term alike; left over is (z - k) (log2 e - l), 2e-8 of
+// z - k, and the argument's own rounding. Beyond |k| = 2^100 (rows of a type's lowest value, say)
+// floats lie so far apart that z is k or has no weight: l = 1 and c = k serve, and cannot overflow.
+struct ExpCentre {
+    float l, c, f;
+};
+constexpr float kFarCentre = 1.2676506002282294e30f;
+__device__ __forceinline__ ExpCentre exp_centre(float k) {
+    if (fabsf(k) >= kFarCentre) return {1.f, k, 1.f};
+    const float c = k * kLog2e;
+    return {kLog2e, c, fmaf(fmaf(k, kLog2e, -c), -0.6931471805599453f, 1.f)};
+}
+// k = a + b + b_lo, b >= 0 a row's log S
+__device__ __forceinline__ ExpCentre exp_centre(float a, float b, float b_lo) {
+    if (fabsf(a) >= kFarCentre) return {1.f, a, expf(-(b + b_lo))};
+    const float pa = a * kLog2e, ea = fmaf(a, kLog2e, -pa);
+    const float pb = b * kLog2e, eb = fmaf(b_lo, kLog2e, fmaf(b, 1.925963033500011e-08f, fmaf(b, kLog2e, -pb)));
+    const DF s = two_sum(pa, pb);
+    return {kLog2e, s.hi, fmaf(s.lo + (ea + eb), -0.6931471805599453f, 1.f)};
+}
+__device__ __forceinline__ float ex2_approx(float a) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(a));
+    return y;
+}
+// 2^{z l - c}
+__device__ __forceinline__ float ce_exp(const ExpCentre &k, float z) { return ex2_approx(fmaf(z, k.l, -k.c)); }
+__device__ __forceinline__ float2 ce_exp2(const ExpCentre &k, float2 z) {
+    const float2 a = __ffma2_rn(z, f2(k.l), f2(-k.c));
+    return make_float2(ex2_approx(a.x), ex2_approx(a.y));
+}
+
+// Constants of a row's gradient: dz = ga 2^{z l - c} - gs for every column but the target's.
+struct CeGradRow {
+    ExpCentre k;
+    float ga, gs, g, a1, m, logS_hi, logS_lo;
+};
+__device__ __forceinline__ CeGradRow ce_grad_row(const CeRules &q, const RowStat &s, float g) {
+    const ExpCentre k = exp_centre(s.m, s.logS_hi, s.logS_lo);
+    const float a1 = 2.f * q.zeta * (s.m + (s.logS_hi + s.logS_lo));
+    return {k, g * (1.f + a1) * k.f, g * q.share, g, a1, s.m, s.logS_hi, s.logS_lo};
+}
+__device__ __forceinline__ float2 ce_grad2(const CeGradRow &r, float2 z) {
+    return __ffma2_rn(f2(r.ga), ce_exp2(r.k, z), f2(-r.gs));
+}
+// The target's column: 1 - e is taken away in a form that does not cancel as p -> 1,
+// p - 1 = e^{log p} - 1.
+__device__ __forceinline__ float ce_grad_target(const CeRules &q, const CeGradRow &r, float z) {
+    const DF l = df_sub(df_diff(z, r.m), r.logS_hi, r.logS_lo);
+    const float lp = l.hi + l.lo, p = exp_split(l.hi, l.lo);
     const float pm1 = lp > -0.5f ? expm1_small(lp) : p - 1.f;
-    return g * (pm1 + fmaf(a1, p, q.smooth - q.share));
+    return r.g * (pm1 + fmaf(r.a1, p, q.smooth - q.share));
 }
 
-// What a row's pieces come to.
+// What a piece of a row, or the whole of it, comes to.
 struct CeRow {
     float M;
     DF S, W;              // W times 2^-24
@@ -89,59 +155,74 @@ struct CeRow {
 };
 constexpr uint32_t kCeMinusInf = 1u << 30;
 
-// Pieces of a row: vp_partial records, at [k * sk + r * sr].
-struct CePieces {
-    const PartialRec *parts;
-    int64_t sk, sr;
-    __device__ __forceinline__ float max_of(int64_t r, int k) const { return parts[k * sk + r * sr].m; }
+// o, whose maximum is M, and a piece of n columns with maximum m, sum S and sum W (times 2^-24)
+__device__ __forceinline__ void ce_add(CeRow &o, float m, DF S, DF W, uint32_t n) {
+    if (S.hi != S.hi) o.flags |= kPartNanInf;
+    else if (S.hi > 0.f) {
+        const float a = expf(m - o.M);
+        df_add(o.S, a * S.hi);
+        df_add(o.S, a * S.lo);
+    }
+    if (W.hi == W.hi) {
+        df_add(o.W, W);
+        df_add(o.W, (float)n * fmaf(o.M, -kCeScale, m * kCeScale));
+    }
+    o.n += n;
+}
+
+// A slice of a row of logits: 32 bytes.
+struct CeSlice {
+    float m, S, S_lo, W, W_lo, zt;
+    uint32_t flags, n;
+};
+struct CeSlices {
+    const CeSlice *slices;      // [N][K]
+    int K;
+    __device__ __forceinline__ float max_of(int64_t r, int k) const { return slices[r * K + k].m; }
     __device__ __forceinline__ float target(int64_t, float zt) const { return zt; }
-    __device__ __forceinline__ void add(int64_t r, int k, float M, CeRow &o) const {
-        const PartialRec p = parts[k * sk + r * sr];
-        o.flags |= p.flags;
-        if (p.flags & kPartHasTarget) {
-            ++o.owners;
-            o.zt = p.z_t;
-        }
-        const float S = (float)p.S;
-        if (S != S) o.flags |= kPartNanInf;
-        else if (S > 0.f) {
-            const float a = expf(p.m - M);
-            df_add(o.S, a * S);
-            df_add(o.S, a * (float)(p.S - (double)S));
-        }
-        // S_b: the piece's columns
-        const double W = p.W * (1.0 / kCeUnscale);
-        if (W == -INFINITY) o.flags |= kCeMinusInf;
-        else if (W == W) {
-            const float hi = (float)W, d = fmaf(M, -kCeScale, p.m * kCeScale);
-            df_add(o.W, hi);
-            df_add(o.W, (float)(W - (double)hi));
-            df_add(o.W, (float)p.S_b * d);
-        }
-        o.n += (uint32_t)p.S_b;
+    __device__ __forceinline__ void add(int64_t r, int k, CeRow &o) const {
+        const uint4 *p = reinterpret_cast<const uint4 *>(slices + r * K + k);
+        const uint4 a = p[0], b = p[1];
+        o.flags |= b.z;
+        if (b.z & kPartHasTarget) o.zt = __uint_as_float(b.y), ++o.owners;
+        ce_add(o, __uint_as_float(a.x), {__uint_as_float(a.y), __uint_as_float(a.z)},
+               {__uint_as_float(a.w), __uint_as_float(b.x)}, b.w);
     }
 };
 
-// Pieces of a row that one GEMM tile of 256 columns left: (m, S, sum z, -), and the target's
-// logit in an array of its own.
+// vp_partial records of gathered shards: [K][N].
+struct CeShards {
+    const PartialRec *parts;
+    int64_t N;
+    __device__ __forceinline__ float max_of(int64_t r, int k) const { return parts[k * N + r].m; }
+    __device__ __forceinline__ float target(int64_t, float zt) const { return zt; }
+    __device__ __forceinline__ void add(int64_t r, int k, CeRow &o) const {
+        const PartialRec p = parts[k * N + r];
+        o.flags |= p.flags;
+        if (p.flags & kPartHasTarget) o.zt = p.z_t, ++o.owners;
+        const double W = p.W / kCeUnscale;
+        if (W == -INFINITY) o.flags |= kCeMinusInf;
+        ce_add(o, p.m, df_from(p.S), W == -INFINITY ? DF{0.f, 0.f} : df_from(W), (uint32_t)p.S_b);   // S_b: its columns
+    }
+};
+
+// What one GEMM tile of 256 columns left of a row: (m, S, sum of z, -), and the target's logit
+// in an array of its own.
 struct CeTiles {
     const float4 *tiles;        // [N][n_t]
     const float *zt;            // [N]
     int n_t, V;
     __device__ __forceinline__ float max_of(int64_t r, int k) const { return tiles[r * n_t + k].x; }
     __device__ __forceinline__ float target(int64_t r, float) const { return zt[r]; }
-    __device__ __forceinline__ void add(int64_t r, int k, float M, CeRow &o) const {
+    __device__ __forceinline__ void add(int64_t r, int k, CeRow &o) const {
         const float4 p = tiles[r * n_t + k];
-        if (p.y != p.y) o.flags |= kPartNanInf;
-        else if (p.y > 0.f) df_add(o.S, p.y * expf(p.x - M));
         const int n = min(256, V - 256 * k);
         const float w = p.z * kCeScale;
         if (w == -INFINITY) o.flags |= kCeMinusInf;
-        else if (w == w) {
-            df_add(o.W, w);
-            df_add(o.W, -(float)n * (M * kCeScale));
-        }
-        o.n += (uint32_t)n;
+        // sum of (z - m) = sum of z - n m
+        DF W{w == -INFINITY ? 0.f : w, 0.f};
+        if (w == w) df_add(W, -(float)n * (p.x * kCeScale));
+        ce_add(o, p.x, {p.y, 0.f}, W, (uint32_t)n);
     }
 };
 
@@ -165,39 +246,45 @@ struct CeJoinArgs {
     double smooth, zeta;
 };
 
-// One warp for four rows, a lane for every 32nd piece, in a fixed order; then one lane for
-// each of the CTA's 32 rows takes the logarithm in 64 bits: a whole warp's worth of that narrow
-// pipe for 32 rows, not for one.
-constexpr int kCeJoinRows = 32;
-enum CeJoin { kCeLoss, kCeRecords, kCeShards };   // losses; the shard's records; losses of gathered shards
-template <class Src, CeJoin kind>
-__global__ void __launch_bounds__(256)
+// kLanes lanes for a row, each for every kLanes-th piece in a fixed order; then one lane for each
+// of the CTA's rows takes the logarithm in 64 bits, a warp's worth of that narrow pipe for up to
+// 32 rows and not for one. 8 lanes where a row has up to 32 pieces, 32 lanes beyond.
+constexpr int kCeJoinThreads = 256;
+enum CeJoin { kCeLoss, kCeRecords, kCeGathered };   // losses; the shard's records; losses of gathered shards
+template <class Src, CeJoin kind, int kLanes>
+__global__ void __launch_bounds__(kCeJoinThreads)
 ce_join_kernel(const Src src, int K, const CeJoinArgs a) {
-    __shared__ CeRow rows[kCeJoinRows];
+    constexpr int kRows = kCeJoinThreads / kLanes;
+    static_assert(kRows <= 32, "a lane for each row");
+    __shared__ CeRow rows[kRows];
     pdl_enter<false>();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int64_t r0 = (int64_t)blockIdx.x * kCeJoinRows;
-    for (int i = 0; i < 4; ++i) {
-        const int64_t r = r0 + warp * 4 + i;
-        if (r >= a.N) break;
+    const int64_t r0 = (int64_t)blockIdx.x * kRows;
+    {
+        const int i = threadIdx.x / kLanes, k0 = threadIdx.x % kLanes;
+        const int64_t r = r0 + i < a.N ? r0 + i : a.N - 1;     // a lane without a row of its own votes along
         CeRow o{kNegBig, {0.f, 0.f}, {0.f, 0.f}, 0.f, 0u, 0, 0u};
-        for (int k = lane; k < K; k += 32) o.M = fmaxf(o.M, src.max_of(r, k));
-        o.M = warp_max(o.M);
-        for (int k = lane; k < K; k += 32) src.add(r, k, o.M, o);
-        const unsigned holders = __ballot_sync(0xffffffffu, o.owners > 0);
-        o.zt = __shfl_sync(0xffffffffu, o.zt, holders ? __ffs(holders) - 1 : 0);
-        o.owners = __reduce_add_sync(0xffffffffu, o.owners);
-        o.flags = __reduce_or_sync(0xffffffffu, o.flags);
+#pragma unroll 4
+        for (int k = k0; k < K; k += kLanes) o.M = fmaxf(o.M, src.max_of(r, k));
 #pragma unroll
-        for (int m = 16; m > 0; m >>= 1) {
+        for (int m = kLanes / 2; m > 0; m >>= 1) o.M = fmaxf(o.M, __shfl_xor_sync(0xffffffffu, o.M, m));
+#pragma unroll 4
+        for (int k = k0; k < K; k += kLanes) src.add(r, k, o);
+#pragma unroll
+        for (int m = kLanes / 2; m > 0; m >>= 1) {
+            const int owners = __shfl_xor_sync(0xffffffffu, o.owners, m);
+            const float zt = __shfl_xor_sync(0xffffffffu, o.zt, m);
+            if (owners > o.owners) o.zt = zt;
+            o.owners += owners;
+            o.flags |= __shfl_xor_sync(0xffffffffu, o.flags, m);
+            o.n += __shfl_xor_sync(0xffffffffu, o.n, m);
             df_add(o.S, shfl_xor(o.S, m));
             df_add(o.W, shfl_xor(o.W, m));
         }
-        o.n = __reduce_add_sync(0xffffffffu, o.n);
-        if (lane == 0) rows[warp * 4 + i] = o;
+        if (k0 == 0) rows[i] = o;
     }
     __syncthreads();
-    if (warp != 0 || r0 + lane >= a.N) return;
+    if (warp != 0 || lane >= kRows || r0 + lane >= a.N) return;
     const int64_t r = r0 + lane;
     const CeRow o = rows[lane];
     const double S = df_value(o.S);
@@ -205,7 +292,7 @@ ce_join_kernel(const Src src, int K, const CeJoinArgs a) {
     const bool nan = (o.flags & kPartNanInf) || S != S;
     bool ignored, bad;
     float zt = o.zt;
-    if (kind == kCeShards) {
+    if (kind == kCeGathered) {
         ignored = (o.flags & kPartIgnored) != 0;
         bad = !ignored && o.owners != 1;
     } else {
@@ -226,7 +313,7 @@ ce_join_kernel(const Src src, int K, const CeJoinArgs a) {
     else if (S == 0.0) flags |= kRowEmpty;
     const double logS = log(nan ? (double)qnan() : S), lse = (double)o.M + logS;
     const bool broken = flags != 0;
-    if (kind == kCeShards) flags |= kRowSharded | (bad ? kRowBadTarget : 0u);
+    if (kind == kCeGathered) flags |= kRowSharded | (bad ? kRowBadTarget : 0u);
     store_rowstat(a.stats + r, o.M, logS, 0.0, flags);
     if (bad && a.err) atomicOr(a.err, VP_ERRBIT_TARGET_);
     double loss = logS + a.zeta * lse * lse;
@@ -238,14 +325,20 @@ ce_join_kernel(const Src src, int K, const CeJoinArgs a) {
 // A row's K pieces made its loss and record, or the shard's record (a.parts), or, of gathered
 // shards, the whole row's loss and record.
 template <class Src>
-static cudaError_t launch_ce_join(const Src &src, int K, const CeArgs &a, bool shards) {
+static cudaError_t launch_ce_join(const Src &src, int K, const CeArgs &a) {
     const CeJoinArgs j{a.N, a.V, a.vocab_start, a.targets, a.loss, static_cast<RowStat *>(a.stats), a.err,
                        static_cast<PartialRec *>(a.parts), a.opt.smooth, a.opt.zeta};
-    const dim3 grid((unsigned)((a.N + kCeJoinRows - 1) / kCeJoinRows));
-    if (a.parts) return launch_pdl(ce_join_kernel<Src, kCeRecords>, grid, dim3(256), 0, a.stream, src, K, j);
-    if constexpr (std::is_same<Src, CePieces>::value)
-        if (shards) return launch_pdl(ce_join_kernel<Src, kCeShards>, grid, dim3(256), 0, a.stream, src, K, j);
-    return launch_pdl(ce_join_kernel<Src, kCeLoss>, grid, dim3(256), 0, a.stream, src, K, j);
+    auto go = [&](auto kernel, int lanes) {
+        const int64_t rows = kCeJoinThreads / lanes;
+        return launch_pdl(kernel, dim3((unsigned)((a.N + rows - 1) / rows)), dim3(kCeJoinThreads), 0, a.stream, src, K, j);
+    };
+    if constexpr (std::is_same<Src, CeShards>::value) {
+        return go(ce_join_kernel<Src, kCeGathered, 8>, 8);
+    } else {
+        if (a.parts)
+            return K <= 32 ? go(ce_join_kernel<Src, kCeRecords, 8>, 8) : go(ce_join_kernel<Src, kCeRecords, 32>, 32);
+        return K <= 32 ? go(ce_join_kernel<Src, kCeLoss, 8>, 8) : go(ce_join_kernel<Src, kCeLoss, 32>, 32);
+    }
 }
 
 }  // namespace vp

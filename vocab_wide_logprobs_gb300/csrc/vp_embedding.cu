@@ -18,6 +18,8 @@
 //   Every sum's order follows from the ids alone, so the result is the same every time, and
 //   an id that takes half of a batch is spread over as many CTAs as it has windows.
 //   Bound: DRAM bytes of dy and dW.
+#include <algorithm>
+
 #include "vp_device.cuh"
 #include "vp_launch.h"
 
@@ -104,36 +106,63 @@ embedding_fwd_kernel(const TI *__restrict__ table, int64_t pitch, int V, int D, 
 constexpr int kSortThreads = 1024, kSortWarps = kSortThreads / 32;
 constexpr int kSortMaxBins = 1024;               // ids of a CTA's range: a thread each in the scan, 128 KB of counters
 
+constexpr int kSortAhead = 8;                    // ids of a lane on their way at once
+constexpr int kStash = 256;                      // own tokens that a warp remembers for the second pass
+constexpr uint32_t kStashSpan = 1u << 22;        // and how long a stretch they can come from (10 + 22 bits)
+static_assert(kSortMaxBins <= 1 << 10, "a bin's 10 bits");
+
 // The tokens of the shard in the order of their ids: rows[k] and positions[k] of the k-th,
-// first[v] .. first[v + 1] those of row v. CTA b owns the rows from b * bins on. A warp goes
-// over the same stretch of positions in both passes, so its counters, made offsets by the scan
-// (row by row, and warp by warp within a row), place its tokens behind those of earlier stretches.
+// first[v] .. first[v + 1] those of row v. CTA b owns the rows from b * bins on. A warp places the
+// tokens of the stretch of positions that it has counted, so its counters, made offsets by the scan
+// (row by row, and warp by warp within a row), put them behind those of earlier stretches. While it
+// counts it notes its own tokens; only a warp with more of them than it can note reads its stretch again.
 __global__ void __launch_bounds__(kSortThreads)
 token_sort_kernel(const int64_t *__restrict__ ids, int64_t N, int V, int64_t vocab_start, bool sharded, int bins,
                   int *__restrict__ first, int *__restrict__ rows, int *__restrict__ positions,
                   int32_t *__restrict__ err) {
-    extern __shared__ uint32_t counts[];         // [kSortWarps][bins]
+    extern __shared__ uint32_t counts[];         // [kSortWarps][bins], then [kSortWarps][kStash]
     __shared__ uint32_t s_sum[kSortWarps];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     for (int i = tid; i < kSortWarps * bins; i += kSortThreads) counts[i] = 0u;
     __syncthreads();
     pdl_enter<false>();
-    const int64_t lo = (int64_t)blockIdx.x * bins;
+    const uint32_t lo = blockIdx.x * (uint32_t)bins;
     const int64_t stretch = ((N + kSortWarps - 1) / kSortWarps + 31) & ~(int64_t)31;
     const int64_t p0 = min(N, warp * stretch), p1 = min(N, p0 + stretch);
-    uint32_t *mine = counts + warp * bins;
-    uint32_t below = 0;
+    uint32_t *mine = counts + warp * bins, *stash = counts + kSortWarps * bins + warp * kStash;
+    uint32_t below = 0, noted = 0;               // noted: the same in every lane
     bool wrong = false;
-    for (int64_t p = p0 + lane; p < p1; p += 32) {
-        const int64_t id = ids[p], local = id - vocab_start;
-        if (id < 0) continue;
-        if (local < 0 || local >= V) {
-            wrong = true;
-            continue;
+
+    // each(bin, position) of the warp's own tokens in the order of their positions, by whole warps
+    auto scan_stretch = [&](auto each, bool count) {
+        for (int64_t q = p0; q < p1; q += 32 * kSortAhead) {
+            int64_t id[kSortAhead];
+#pragma unroll
+            for (int k = 0; k < kSortAhead; ++k) id[k] = q + k * 32 + lane < p1 ? ids[q + k * 32 + lane] : -1;
+#pragma unroll
+            for (int k = 0; k < kSortAhead; ++k) {
+                const int64_t local = id[k] - vocab_start;
+                const bool here = id[k] >= 0 && local >= 0 && local < V;
+                const uint32_t bin = here ? (uint32_t)local - lo : 0xffffffffu;
+                if (count) {
+                    wrong |= id[k] >= 0 && !here;
+                    below += here && (uint32_t)local < lo;
+                }
+                const uint32_t own = __ballot_sync(0xffffffffu, bin < (uint32_t)bins);
+                if (own) each(own, bin, q + k * 32 + lane);
+            }
         }
-        if (local < lo) ++below;
-        else if (local < lo + bins) atomicAdd(&mine[local - lo], 1u);
-    }
+    };
+    scan_stretch(
+        [&](uint32_t own, uint32_t bin, int64_t p) {
+            if (own >> lane & 1) {
+                atomicAdd(&mine[bin], 1u);
+                const uint32_t at = noted + __popc(own & ((1u << lane) - 1u));
+                if (at < kStash) stash[at] = bin << 22 | ((uint32_t)(p - p0) & (kStashSpan - 1));
+            }
+            noted += __popc(own);
+        },
+        true);
     if (wrong && !sharded && err && blockIdx.x == 0) atomicOr(err, VP_ERRBIT_TARGET_);
     below = __reduce_add_sync(0xffffffffu, below);
     if (lane == 0) s_sum[warp] = below;
@@ -156,8 +185,9 @@ token_sort_kernel(const int64_t *__restrict__ ids, int64_t N, int V, int64_t voc
     const uint32_t sums = s_sum[lane];
     base += __reduce_add_sync(0xffffffffu, lane < warp ? sums : 0u) + scan - n;
     if (tid < bins) {
-        if (lo + tid <= V) first[lo + tid] = (int)base;
-        if (tid == bins - 1 && lo + bins >= V) first[V] = (int)(base + n);
+        const int64_t row = (int64_t)lo + tid;
+        if (row <= V) first[row] = (int)base;
+        if (tid == bins - 1 && row + 1 >= V) first[V] = (int)(base + n);
         for (int w = 0; w < kSortWarps; ++w) {
             const uint32_t c = counts[w * bins + tid];
             counts[w * bins + tid] = base;
@@ -166,28 +196,33 @@ token_sort_kernel(const int64_t *__restrict__ ids, int64_t N, int V, int64_t voc
     }
     __syncthreads();
 
-    for (int64_t q = p0; q < p1; q += 32) {
-        const int64_t p = q + lane;
-        const int64_t id = p < p1 ? ids[p] : -1, local = id - vocab_start;
-        const bool own = id >= 0 && local >= lo && local < lo + bins && local < V;
-        if (!__any_sync(0xffffffffu, own)) continue;
-        const uint32_t bin = own ? (uint32_t)(local - lo) : 0xffffffffu;
-        const uint32_t peers = __match_any_sync(0xffffffffu, bin);
+    auto place = [&](uint32_t own, uint32_t bin, int64_t p) {
+        const bool is_own = own >> lane & 1;
+        const uint32_t peers = __match_any_sync(0xffffffffu, is_own ? bin : 0xffffffffu);
         const uint32_t before = __popc(peers & ((1u << lane) - 1u));
         uint32_t at = 0;
-        if (own) at = mine[bin] + before;
+        if (is_own) at = mine[bin] + before;
         __syncwarp();
-        if (own) {
+        if (is_own) {
             if (before == 0) mine[bin] += __popc(peers);
-            rows[at] = (int)local;
+            rows[at] = (int)(lo + bin);
             positions[at] = (int)p;
         }
         __syncwarp();
+    };
+    if (noted <= kStash && stretch <= (int64_t)kStashSpan) {
+        for (uint32_t i = 0; i < noted; i += 32) {
+            const uint32_t e = i + lane < noted ? stash[i + lane] : 0u;
+            place(__ballot_sync(0xffffffffu, i + lane < noted), e >> 22, p0 + (e & (kStashSpan - 1)));
+        }
+    } else {
+        scan_stretch(place, false);
     }
 }
 
 constexpr int kGradThreads = 256;
 constexpr int kGradMaxWindow = 64;
+constexpr int kFillBytes = 256, kFillMaxRows = 1024;     // zeros of a thread, and rows of a CTA, at most
 
 struct TableGrad {
     int64_t N;
@@ -195,6 +230,7 @@ struct TableGrad {
     Rows dy_rows;
     float scale;
     const int *first, *rows, *positions;
+    int *until;                 // [n_windows]: the window where the run that begins in one and goes on ends, or 0
     float *partial;             // [n_windows][2][D]: what belongs to a run begun in an earlier window, and
                                 // what belongs to one that goes on in later ones
 };
@@ -223,32 +259,52 @@ __device__ __forceinline__ void finish8(TO *dst, int c, int step, int D, float s
     store8<TO, kVector>(dst, c, step, D, v);
 }
 
+template <typename T>
+__device__ __forceinline__ void zero_fill(T *p, int64_t n, int tid, int nt) {
+    const int64_t head = min(n, (int64_t)((16 - (uintptr_t)p % 16) % 16 / sizeof(T)));
+    constexpr int kPer = 16 / sizeof(T);
+    const int64_t vecs = (n - head) / kPer, tail = head + vecs * kPer;
+    if (tid < head) Elem<T>::store1(p + tid, 0.f);
+    for (int64_t i = tid; i < vecs; i += nt) stg_stream(p + head + i * kPer, make_uint4(0, 0, 0, 0));
+    if (tid < n - tail) Elem<T>::store1(p + tail + tid, 0.f);
+}
+
 template <typename TI, typename TO, bool kVector, bool kAdd>
 __global__ void __launch_bounds__(kGradThreads)
 table_grad_kernel(const TI *__restrict__ dy, const TableGrad a, TO *__restrict__ dW, int fill_rows) {
     __shared__ int s_row[kGradMaxWindow];
     __shared__ int64_t s_off[kGradMaxWindow];
+    __shared__ bool s_asked[kFillMaxRows];
     const int tid = threadIdx.x, nt = blockDim.x;
     pdl_enter<false>();
     const int total = a.first[a.V];              // tokens of this shard
-    int64_t b = blockIdx.x;
+    const int64_t b = blockIdx.x;
     const int64_t n_sum = (int64_t)a.n_windows * a.col_blocks;
     if (b >= n_sum) {
         // zeros for rows that no token asks for
         if constexpr (!kAdd) {
             const int64_t v0 = (b - n_sum) * fill_rows, v1 = min((int64_t)a.V, v0 + fill_rows);
-            const float zero[kEmbVec] = {};
-            for (int64_t v = v0; v < v1; ++v) {
-                if (a.first[v + 1] != a.first[v]) continue;
-                TO *dst = dW + v * (int64_t)a.D;
-                if (kVector) for (int c = tid * kEmbVec; c < a.D; c += nt * kEmbVec) store8<TO, true>(dst, c, 1, a.D, zero);
-                else for (int c = tid; c < a.D; c += nt) Elem<TO>::store1(dst + c, 0.f);
+            for (int64_t v = v0 + tid; v < v1; v += nt) s_asked[v - v0] = a.first[v + 1] != a.first[v];
+            __syncthreads();
+            for (int64_t v = v0; v < v1;) {
+                int64_t end = v;                 // rows v .. end lie behind one another
+                while (end < v1 && !s_asked[end - v0]) ++end;
+                zero_fill(dW + v * a.D, (end - v) * a.D, tid, nt);
+                v = end + 1;
             }
         }
         return;
     }
     const int w = (int)(b / a.col_blocks), cb = (int)(b - (int64_t)w * a.col_blocks);
     const int64_t k0 = (int64_t)w * a.window, k1 = min((int64_t)total, k0 + a.window);
+    if (cb == 0 && tid == 0) {
+        int until = 0;
+        if (k1 < total && k0 < k1) {
+            const int row = a.rows[k1 - 1], end = a.first[row + 1];
+            if (a.first[row] >= k0 && end > k1) until = (end - 1) / a.window;
+        }
+        a.until[w] = until;
+    }
     if (k0 >= k1) return;
     for (int i = tid; i < (int)(k1 - k0); i += nt) {
         s_row[i] = a.rows[k0 + i];
@@ -291,35 +347,53 @@ table_grad_kernel(const TI *__restrict__ dy, const TableGrad a, TO *__restrict__
     }
 }
 
-// A CTA for each window and 32 columns: where a run begins in the window and goes on, eight
-// warps add its partial sums, warp j those of windows w + j, w + j + 8, ..; then one adds the eight.
-constexpr int kJoinWarps = 8;
-template <typename TO, bool kAdd>
-__global__ void __launch_bounds__(kJoinWarps * 32)
+// A CTA for each window and 512 columns, four each for a thread: where a run begins in the window and
+// goes on, four groups of threads add its partial sums, group j those of windows w + j, w + j + 4, ..;
+// then one adds the four.
+constexpr int kJoinThreads = 512, kJoinLanes = 128, kJoinGroups = kJoinThreads / kJoinLanes, kJoinAhead = 4;
+template <typename TO, bool kVector, bool kAdd>
+__global__ void __launch_bounds__(kJoinThreads)
 table_join_kernel(const TableGrad a, TO *__restrict__ dW) {
-    __shared__ DF s_sum[kJoinWarps][32];
+    __shared__ DF s_sum[kJoinGroups][kJoinLanes][4];
     pdl_enter<false>();
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int w = blockIdx.x;
-    const int64_t total = a.first[a.V];
-    const int64_t k1 = (int64_t)(w + 1) * a.window;
-    if (k1 >= total) return;                                          // nothing behind this window
-    const int row = a.rows[k1 - 1];
-    if (a.first[row] < k1 - a.window || a.first[row + 1] <= k1) return;   // begun earlier, or ends here
-    const int last = (a.first[row + 1] - 1) / a.window;
-    for (int c0 = blockIdx.y * 32; c0 < a.D; c0 += gridDim.y * 32) {
-        const int c = c0 + lane;
-        DF sum{0.f, 0.f};
-        if (c < a.D)
-            for (int u = w + warp; u <= last; u += kJoinWarps)
-                df_add(sum, a.partial[((int64_t)u * 2 + (u == w ? 1 : 0)) * a.D + c]);
-        s_sum[warp][lane] = sum;
+    const int group = threadIdx.x / kJoinLanes, lane = threadIdx.x % kJoinLanes;
+    const int w = blockIdx.x, until = a.until[w];
+    if (until == 0) return;
+    const int row = a.rows[(int64_t)(w + 1) * a.window - 1];
+    for (int c0 = blockIdx.y * kJoinLanes * 4; c0 < a.D; c0 += gridDim.y * kJoinLanes * 4) {
+        const int c = kVector ? c0 + 4 * lane : c0 + lane, step = kVector ? 1 : kJoinLanes;
+        DF sum[4] = {};
+        for (int u0 = w + group; u0 <= until; u0 += kJoinGroups * kJoinAhead) {
+            float v[kJoinAhead][4];
+#pragma unroll
+            for (int k = 0; k < kJoinAhead; ++k) {
+                const int u = u0 + k * kJoinGroups;
+                const float *part = a.partial + ((int64_t)u * 2 + (u == w ? 1 : 0)) * a.D + c;
+                if (kVector) {
+                    const float4 f = u <= until && c < a.D ? *reinterpret_cast<const float4 *>(part) : make_float4(0.f, 0.f, 0.f, 0.f);
+                    v[k][0] = f.x; v[k][1] = f.y; v[k][2] = f.z; v[k][3] = f.w;
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) v[k][e] = u <= until && c + e * step < a.D ? part[e * step] : 0.f;
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < kJoinAhead; ++k)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) df_add(sum[e], v[k][e]);
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s_sum[group][lane][e] = sum[e];
         __syncthreads();
-        if (warp == 0 && c < a.D) {
-            for (int j = 1; j < kJoinWarps; ++j) df_add(sum, s_sum[j][lane]);
-            TO *dst = dW + row * (int64_t)a.D + c;
-            const float s = sum.hi + sum.lo;
-            Elem<TO>::store1(dst, kAdd ? fmaf(s, a.scale, (float)*dst) : s * a.scale);
+        if (group == 0) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                if (c + e * step >= a.D) break;
+                for (int j = 1; j < kJoinGroups; ++j) df_add(sum[e], s_sum[j][lane][e]);
+                TO *dst = dW + row * (int64_t)a.D + c + e * step;
+                const float s = sum[e].hi + sum[e].lo;
+                Elem<TO>::store1(dst, kAdd ? fmaf(s, a.scale, (float)*dst) : s * a.scale);
+            }
         }
         __syncthreads();
     }
@@ -346,7 +420,7 @@ int grad_window(int64_t N) {
 }
 
 struct GradLayout {
-    size_t rows, positions, partial, total;
+    size_t rows, positions, until, partial, total;
 };
 GradLayout grad_layout(int64_t N, int64_t V, int64_t D) {
     auto up = [](size_t x) { return (x + 255) & ~(size_t)255; };
@@ -354,7 +428,8 @@ GradLayout grad_layout(int64_t N, int64_t V, int64_t D) {
     GradLayout L;
     L.rows = up((size_t)(V + 1) * 4);
     L.positions = L.rows + up((size_t)N * 4);
-    L.partial = L.positions + up((size_t)N * 4);
+    L.until = L.positions + up((size_t)N * 4);
+    L.partial = L.until + up((size_t)windows * 4);
     L.total = L.partial + (size_t)windows * 2 * D * 4;
     return L;
 }
@@ -386,9 +461,9 @@ cudaError_t embedding_bwd(const EmbeddingArgs &a) {
     const int sms = sm_count();
     int64_t bins = (a.V + sms - 1) / sms;
     bins = bins < 32 ? 32 : bins > kSortMaxBins ? kSortMaxBins : bins;
-    const size_t smem = (size_t)kSortWarps * bins * 4;
+    const size_t smem = (size_t)kSortWarps * (bins + kStash) * 4;
     cudaError_t e = cudaFuncSetAttribute(token_sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         kSortWarps * kSortMaxBins * 4);
+                                         kSortWarps * (kSortMaxBins + kStash) * 4);
     if (e != cudaSuccess) return e;
     e = launch_pdl(token_sort_kernel, dim3((unsigned)((a.V + bins - 1) / bins)), dim3(kSortThreads), smem, a.stream,
                    a.ids, a.N, (int)a.V, a.vocab_start, a.sharded, (int)bins, first, rows, positions, a.err);
@@ -409,10 +484,10 @@ cudaError_t embedding_bwd(const EmbeddingArgs &a) {
     g.first = first;
     g.rows = rows;
     g.positions = positions;
+    g.until = reinterpret_cast<int *>(ws + L.until);
     g.partial = reinterpret_cast<float *>(ws + L.partial);
-    // about 64 KB of zeros for a CTA
     const int64_t row_bytes = a.D * (int64_t)sizeof(TO);
-    const int fill_rows = (int)(row_bytes >= 65536 ? 1 : 65536 / row_bytes);
+    const int fill_rows = (int)std::clamp<int64_t>((int64_t)kFillBytes * threads / row_bytes, 1, kFillMaxRows);
     const int64_t fill_ctas = a.accumulate ? 0 : (a.V + fill_rows - 1) / fill_rows;
     const int64_t ctas = (int64_t)g.n_windows * g.col_blocks + fill_ctas;
     if (ctas > 2147483647) return cudaErrorInvalidValue;
@@ -422,9 +497,13 @@ cudaError_t embedding_bwd(const EmbeddingArgs &a) {
     e = vector ? (a.accumulate ? go(table_grad_kernel<TI, TO, true, true>) : go(table_grad_kernel<TI, TO, true, false>))
                : (a.accumulate ? go(table_grad_kernel<TI, TO, false, true>) : go(table_grad_kernel<TI, TO, false, false>));
     if (e != cudaSuccess || g.n_windows < 2) return e;
-    const dim3 grid((unsigned)(g.n_windows - 1), (unsigned)((a.D + 31) / 32 < 64 ? (a.D + 31) / 32 : 64));
-    return a.accumulate ? launch_pdl(table_join_kernel<TO, true>, grid, dim3(kJoinWarps * 32), 0, a.stream, g, dW)
-                        : launch_pdl(table_join_kernel<TO, false>, grid, dim3(kJoinWarps * 32), 0, a.stream, g, dW);
+    const int64_t blocks = (a.D + kJoinLanes * 4 - 1) / (kJoinLanes * 4);
+    auto join = [&](auto kernel) {
+        return launch_pdl(kernel, dim3((unsigned)(g.n_windows - 1), (unsigned)std::min<int64_t>(blocks, 65535)),
+                          dim3(kJoinThreads), 0, a.stream, g, dW);
+    };
+    return vector ? (a.accumulate ? join(table_join_kernel<TO, true, true>) : join(table_join_kernel<TO, true, false>))
+                  : (a.accumulate ? join(table_join_kernel<TO, false, true>) : join(table_join_kernel<TO, false, false>));
 }
 
 }  // namespace

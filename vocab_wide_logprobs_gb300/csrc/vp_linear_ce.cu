@@ -35,7 +35,7 @@ struct CeEpi {
             tmem_ld32(taddr + c * 32, v);
             const int n = ncol - c * 32;                 // columns of the vocabulary left
             if (n <= 0) continue;
-            if (kCap) soft_cap(q, v, v, nullptr);
+            if (kCap) soft_cap(q, v);
             float cm = kNegBig;
 #pragma unroll
             for (int i = 0; i < 32; i += 2) {
@@ -48,16 +48,14 @@ struct CeEpi {
                 cm = fmaxf(cm, fmaxf(v[i], v[i + 1]));
             }
             if (cm > m) {
-                S *= exp2f((m - cm) * kLog2e);
+                S *= ex2_approx((m - cm) * kLog2e);
                 m = cm;
             }
-            float s0 = 0.f, s1 = 0.f;
+            float2 s2 = f2(0.f);
+            const ExpCentre k = exp_centre(m);
 #pragma unroll
-            for (int i = 0; i < 32; i += 2) {
-                s0 += ex2_fast((v[i] - m) * kLog2e);
-                s1 += ex2_fast((v[i + 1] - m) * kLog2e);
-            }
-            S += s0 + s1;
+            for (int i = 0; i < 32; i += 2) s2 = __fadd2_rn(s2, ce_exp2(k, make_float2(v[i], v[i + 1])));
+            S = fmaf(s2.x + s2.y, k.f, S);
         }
         if (!valid) return;
         tiles[(int64_t)row * n_t + col0 / kLBN] = make_float4(m, S, Z0 + Z1, 0.f);
@@ -87,25 +85,35 @@ struct DzCeEpi {
         int mode = (s.flags & (kRowNanInf | kRowEmpty | kRowBadTarget)) || outside ? 2 : 0;   // 1 zeros, 2 NaN
         if (tg < 0) mode = 1;
         if (valid && outside && err && col0 == 0 && v0 == 0) atomicOr(err, VP_ERRBIT_TARGET_);
-        const int64_t tcol = tl - v0 - col0;               // target column within this tile
-        const float gr = valid ? g[row] : 0.f;
-        const float a1 = 2.f * q.zeta * (s.m + (s.logS_hi + s.logS_lo));
+        const int64_t tl0 = tg >= 0 ? tl : -1;
+        const int64_t tcol = tl0 - v0 - col0;               // target column within this tile
+        const CeGradRow gr = ce_grad_row(q, s, valid ? g[row] : 0.f);
 #pragma unroll 1
         for (int c = 0; c < kLBN / 32; ++c) {
             float v[32], slope[32];
             tmem_ld32(taddr + c * 32, v);
-            if (kCap) soft_cap(q, v, v, slope);
+            if (kCap) soft_cap<32, true>(q, v, slope);
+            const int64_t at = tcol - c * 32;
+            float zt = 0.f;
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) {
+                if (i == at) zt = v[i];
+                if (i + 1 == at) zt = v[i + 1];
+                float2 d = ce_grad2(gr, make_float2(v[i], v[i + 1]));
+                v[i] = d.x;
+                v[i + 1] = d.y;
+            }
+            if (at >= 0 && at < 32) {
+                const float d = ce_grad_target(q, gr, zt);
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                    if (i == at) v[i] = d;
+            }
 #pragma unroll
             for (int i = 0; i < 32; ++i) {
-                const int col = c * 32 + i;
-                const float lp = (v[i] - s.m) - s.logS_hi;
-                const float p = ex2_fast(lp * kLog2e);
-                float x = ce_grad(q, p, a1, gr);
-                if (col == tcol) x = ce_grad_target(q, p, lp - s.logS_lo, a1, gr);
-                if (kCap) x *= slope[i];
-                if (mode == 1 || col >= ncol) x = 0.f;
-                else if (mode == 2) x = qnan();
-                v[i] = x;
+                if (kCap) v[i] *= slope[i];
+                if (mode == 1 || c * 32 + i >= ncol) v[i] = 0.f;
+                else if (mode == 2) v[i] = qnan();
             }
             if (valid) store_dz(dz + (int64_t)row * ldz + col0 + c * 32, v, lo_off);
         }
@@ -138,7 +146,7 @@ cudaError_t launch_linear_ce_fwd(const CeArgs &a) {
                               ? gemm(CeEpi<true>{(int)a.N, n_t, a.vocab_start, a.targets, q, tiles, tgt})
                               : gemm(CeEpi<false>{(int)a.N, n_t, a.vocab_start, a.targets, q, tiles, tgt});
     if (e != cudaSuccess) return e;
-    return launch_ce_join(CeTiles{tiles, tgt, n_t, (int)a.V}, n_t, a, false);
+    return launch_ce_join(CeTiles{tiles, tgt, n_t, (int)a.V}, n_t, a);
 }
 
 struct CeBwdLayout {
