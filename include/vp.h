@@ -795,7 +795,17 @@ VP_API vp_status vp_cross_entropy_merge(const vp_partial *parts, int64_t K, int6
  * (hidden, weight, workspaces' alignment, VP_GRAD_* and the sharded flow as for the fused linear
  * logp): hidden bf16 [N, D], weight bf16 [V, D], D a multiple of 64. The backward writes dhidden
  * bf16 [N, D] and dW bf16 [V, D] (either may be NULL, not both); with N = 0 it writes zeros to dW.
- * A row without valid statistics makes its dhidden row and all of dW NaN. */
+ * A row without valid statistics makes its dhidden row and all of dW NaN. Beside VP_GRAD_EXACT and
+ * VP_GRAD_FAST it takes
+ *   VP_GRAD_MIXED  dz as a pair hi + lo where it counts: the gradient GEMMs add the second halves of
+ *                  those k-blocks that hold a value over 1/16 of its row's |grad_out| (1 - p_t +
+ *                  label_smoothing), a target's among them. What the smaller values can add up to in
+ *                  dhidden is a third of what rounding the output adds, relative to the row's scale; a
+ *                  dW row of a column that is no row's target is that of VP_GRAD_FAST. About 6 to 7
+ *                  N V D flops for 10 of VP_GRAD_EXACT.
+ * How dhidden's sum is split over SMs follows from N, V and D, so its last bits may differ between
+ * batch sizes, and under VP_GRAD_MIXED with the rows beside it. */
+#define VP_GRAD_MIXED 2
 VP_API size_t vp_linear_cross_entropy_workspace_size(int64_t N, int64_t V, int64_t D);
 VP_API vp_status vp_linear_cross_entropy_fwd(const void *hidden, const void *weight, int64_t N, int64_t V, int64_t D,
                                              int64_t vocab_start, double label_smoothing, double z_loss,

@@ -6,7 +6,7 @@ function names: it turns torch tensors into pointers, sizes and strides and
 calls the C functions. There is no CPU fallback: every call raises if the
 library cannot be built or loaded, or if no sm_103 device is present.
 """
-from .api import (ERRBIT_RULES, ERRBIT_TARGET, GRAD_EXACT, GRAD_FAST, KL_FORWARD, KL_REVERSE, PART_HAS_TARGET,
+from .api import (ERRBIT_RULES, ERRBIT_TARGET, GRAD_EXACT, GRAD_FAST, GRAD_MIXED, KL_FORWARD, KL_REVERSE, PART_HAS_TARGET,
                  PART_IGNORED, PART_MISMATCH, PART_NANINF, PART_NANINF_B, ROW_BADTARGET, ROW_EMPTY, ROW_MISMATCH,
                  ROW_NANINF, ROW_SHARDED, LogitsRules, VPError, decode_partials, decode_rowstats, logits_rules,
                  partials, rows_of, rowstats, vp_cross_entropy_bwd, vp_cross_entropy_fwd, vp_cross_entropy_merge,
@@ -27,7 +27,7 @@ from .api import (ERRBIT_RULES, ERRBIT_TARGET, GRAD_EXACT, GRAD_FAST, KL_FORWARD
                  vp_processed_logprobs_fwd, vp_processed_logprobs_workspace_size, vp_set_row_split, vp_status_string,
                  vp_upload, vp_version)
 
-__all__ = ["ERRBIT_RULES", "ERRBIT_TARGET", "GRAD_EXACT", "GRAD_FAST", "KL_FORWARD", "KL_REVERSE", "PART_HAS_TARGET",
+__all__ = ["ERRBIT_RULES", "ERRBIT_TARGET", "GRAD_EXACT", "GRAD_FAST", "GRAD_MIXED", "KL_FORWARD", "KL_REVERSE", "PART_HAS_TARGET",
            "PART_IGNORED", "PART_MISMATCH", "PART_NANINF", "PART_NANINF_B", "ROW_BADTARGET", "ROW_EMPTY",
            "ROW_MISMATCH", "ROW_NANINF", "ROW_SHARDED", "LogitsRules", "VPError", "decode_partials",
            "decode_rowstats", "logits_rules", "partials", "rows_of", "rowstats", "vp_cross_entropy_bwd",

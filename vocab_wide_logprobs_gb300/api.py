@@ -24,6 +24,7 @@ from . import _lib
 F32, BF16 = 0, 1
 KL_REVERSE, KL_FORWARD = 0, 1
 GRAD_EXACT, GRAD_FAST = 0, 1   # precision of the fused linear backwards (VP_GRAD_EXACT / VP_GRAD_FAST)
+GRAD_MIXED = 2                 # and of the fused linear cross entropy's (VP_GRAD_MIXED)
 ERRBIT_TARGET = 1
 ERRBIT_RULES = 2               # a row's rules are out of range (VP_ERRBIT_RULES)
 ROW_NANINF, ROW_EMPTY, ROW_MISMATCH, ROW_SHARDED, ROW_BADTARGET = 1, 2, 4, 8, 16
@@ -1110,8 +1111,8 @@ def vp_linear_cross_entropy_bwd(hidden, weight, targets, stats, grad, label_smoo
                                 z_loss: float = 0.0, softcap: float = 0.0, vocab_start: int = 0, vocab_total: int = 0,
                                 want_dhidden=True, want_dW=True, err_word=None, dhidden=None, dW=None, workspace=None,
                                 precision: int = None):
-    """Gradients of sum_r grad[r] loss[r]: (dhidden bf16 [N, D] or None, dW bf16 [V, D] or None); precision as
-    vp_linear_logp_bwd."""
+    """Gradients of sum_r grad[r] loss[r]: (dhidden bf16 [N, D] or None, dW bf16 [V, D] or None). precision: GRAD_MIXED
+    (default: dz as a bf16 pair where a value counts in its row), GRAD_EXACT (everywhere) or GRAD_FAST (nowhere)."""
     N, V, D = _linear_model(hidden, weight, "vp_linear_cross_entropy_bwd")
     _row_args(hidden, N, targets=targets, stats=(stats,), grad=grad, err_word=err_word)
     _arg(dhidden if want_dhidden else None, N * D, torch.bfloat16, hidden, "dhidden")
@@ -1125,7 +1126,7 @@ def vp_linear_cross_entropy_bwd(hidden, weight, targets, stats, grad, label_smoo
         workspace = _workspace(_handle().vp_linear_cross_entropy_bwd_workspace_size(N, V, D), hidden)
     _check(_handle().vp_linear_cross_entropy_bwd(_addr(hidden), _addr(weight), N, V, D, vocab_start, vocab_total,
                                                  label_smoothing, z_loss, softcap, _addr(targets), _addr(stats),
-                                                 _addr(grad), _addr(dhidden), _addr(dW), _precision(precision),
+                                                 _addr(grad), _addr(dhidden), _addr(dW), GRAD_MIXED if precision is None else int(precision),
                                                  _addr(workspace), _nbytes(workspace), _addr(err_word),
                                                  _queue(hidden.device)), "vp_linear_cross_entropy_bwd")
     return dhidden, dW

@@ -1005,7 +1005,7 @@ vp_status vp_linear_cross_entropy_bwd(const void *hidden, const void *weight, in
     vp::CeOptions opt;
     if (!linear_dims_ok(N, V, D)) return VP_ERR_SHAPE;
     if (!dhidden && !dW) return VP_ERR_ARG;
-    if (!precision_ok(precision)) return VP_ERR_ARG;
+    if (!precision_ok(precision) && precision != VP_GRAD_MIXED) return VP_ERR_ARG;
     vp_status st = ce_options(label_smoothing, z_loss, softcap, V, vocab_total, &opt);
     if (st != VP_OK) return st;
     if (N == 0 && !dW) return VP_OK;

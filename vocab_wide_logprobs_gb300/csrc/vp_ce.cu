@@ -14,7 +14,8 @@
 namespace vp {
 
 constexpr int kCeThreads = 256;
-constexpr int kCeFwdVecs = 8, kCeGradVecs = 4;   // vectors of a thread
+constexpr int kCeFwdVecs = 8;                    // vectors of a thread
+constexpr int ce_grad_vecs(bool cap) { return cap ? 8 : 4; }
 
 static int64_t ce_slices(bool bf16, int vecs, int64_t V) {
     const int64_t per = (int64_t)kCeThreads * vecs * (bf16 ? 8 : 4);
@@ -56,7 +57,7 @@ __device__ __forceinline__ float vec_max(const uint4 &u, float m) {
 
 // kSum: with the sum of the centred logits, which only label smoothing asks for
 template <typename T, bool kCap, bool kSum>
-__global__ void __launch_bounds__(kCeThreads)
+__global__ void __launch_bounds__(kCeThreads, 4)
 ce_fwd_kernel(const T *__restrict__ x, int V, Rows rows, const CeRules q, const int64_t *__restrict__ targets,
               int64_t vocab_start, int n_slices, int64_t total, CeSlice *__restrict__ slices) {
     constexpr int kVec = Elem<T>::kVec, kWarps = kCeThreads / 32, kCeVecs = kCeFwdVecs, kCeSliceVecs = kCeThreads * kCeVecs;
@@ -174,11 +175,11 @@ ce_fwd_kernel(const T *__restrict__ x, int V, Rows rows, const CeRules q, const 
 }
 
 template <typename T, bool kCap>
-__global__ void __launch_bounds__(kCeThreads)
+__global__ void __launch_bounds__(kCeThreads, kCap ? 4 : 1)
 ce_grad_kernel(const T *x, int V, Rows rows, const CeRules q, const RowStat *__restrict__ stats,
                const float *__restrict__ g_in, const int64_t *__restrict__ targets, int64_t vocab_start, T *dx,
                int32_t *__restrict__ err, int n_slices, int64_t total) {
-    constexpr int kVec = Elem<T>::kVec, kCeVecs = kCeGradVecs, kCeSliceVecs = kCeThreads * kCeVecs;
+    constexpr int kVec = Elem<T>::kVec, kCeVecs = ce_grad_vecs(kCap), kCeSliceVecs = kCeThreads * kCeVecs;
     const int tid = threadIdx.x;
     pdl_enter<true>();   // no global access before this
     for (int64_t tile = blockIdx.x; tile < total; tile += gridDim.x) {
@@ -280,7 +281,7 @@ cudaError_t launch_ce_merge(const CeArgs &a, const void *parts, int64_t K) {
 }
 
 cudaError_t launch_ce_bwd(const CeArgs &a) {
-    const int slices = (int)ce_slices(a.bf16, kCeGradVecs, a.V);
+    const int slices = (int)ce_slices(a.bf16, ce_grad_vecs(a.opt.cap > 0.0), a.V);
     const int64_t total = a.N * slices;
     const CeRules q = ce_rules(a.opt);
     const Rows rows{a.R, a.s_o, a.s_i};

@@ -57,9 +57,8 @@ __device__ __forceinline__ void soft_cap(const CeRules &q, float (&x)[n], float 
         x[2 * i] = z.x;
         x[2 * i + 1] = z.y;
         if (kSlope) {
-            const float2 m = __ffma2_rn(__fmul2_rn(t, f2(-1.f)), t, f2(1.f));
-            slope[2 * i] = m.x;
-            slope[2 * i + 1] = m.y;
+            slope[2 * i] = fmaf(-t.x, t.x, 1.f);
+            slope[2 * i + 1] = fmaf(-t.y, t.y, 1.f);
         }
     }
     if (__any_sync(__activemask(), far >= kTanhSplit)) {
@@ -314,7 +313,9 @@ ce_join_kernel(const Src src, int K, const CeJoinArgs a) {
     const double logS = log(nan ? (double)qnan() : S), lse = (double)o.M + logS;
     const bool broken = flags != 0;
     if (kind == kCeGathered) flags |= kRowSharded | (bad ? kRowBadTarget : 0u);
-    store_rowstat(a.stats + r, o.M, logS, 0.0, flags);
+    // c: log p of the target, by which the backward knows the scale of the row's gradient
+    const double lpt = ((double)zt - (double)o.M) - logS;
+    store_rowstat(a.stats + r, o.M, logS, ignored || bad || broken ? 0.0 : fmax(lpt, -1e30), flags);
     if (bad && a.err) atomicOr(a.err, VP_ERRBIT_TARGET_);
     double loss = logS + a.zeta * lse * lse;
     if (a.smooth < 1.0) loss -= (1.0 - a.smooth) * ((double)zt - (double)o.M);

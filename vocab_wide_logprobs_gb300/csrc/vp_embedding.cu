@@ -235,27 +235,23 @@ struct TableGrad {
                                 // what belongs to one that goes on in later ones
 };
 
-// The row of table, its new value from the sum.
-template <typename TO, bool kVector, bool kAdd>
-__device__ __forceinline__ void finish8(TO *dst, int c, int step, int D, float scale, float (&v)[kEmbVec]) {
-    if constexpr (kAdd) {
-        float o[kEmbVec];
-        if constexpr (kVector && sizeof(TO) == 2) {
-            const uint4 u = *reinterpret_cast<const uint4 *>(dst + c);
-            Elem<TO>::unpack(u, o);
-        } else {
+// What the columns of a table row hold, and their new value from the sum.
+template <typename TO, bool kVector>
+__device__ __forceinline__ void load_old(const TO *row, int c, int step, int D, float (&o)[kEmbVec]) {
+    if constexpr (kVector) {
 #pragma unroll
-            for (int e = 0; e < kEmbVec; ++e) {
-                const int k = kVector ? c + e : c + e * step;
-                o[e] = kVector || k < D ? (float)dst[k] : 0.f;
-            }
-        }
-#pragma unroll
-        for (int e = 0; e < kEmbVec; ++e) v[e] = fmaf(v[e], scale, o[e]);
+        for (int h = 0; h < (int)(kEmbVec * sizeof(TO) / 16); ++h)
+            Elem<TO>::unpack(*reinterpret_cast<const uint4 *>(row + c + h * Elem<TO>::kVec), o + h * Elem<TO>::kVec);
     } else {
 #pragma unroll
-        for (int e = 0; e < kEmbVec; ++e) v[e] *= scale;
+        for (int e = 0; e < kEmbVec; ++e) o[e] = c + e * step < D ? (float)row[c + e * step] : 0.f;
     }
+}
+template <typename TO, bool kVector, bool kAdd>
+__device__ __forceinline__ void finish8(TO *dst, int c, int step, int D, float scale, float (&v)[kEmbVec],
+                                        const float (&o)[kEmbVec]) {
+#pragma unroll
+    for (int e = 0; e < kEmbVec; ++e) v[e] = kAdd ? fmaf(v[e], scale, o[e]) : v[e] * scale;
     store8<TO, kVector>(dst, c, step, D, v);
 }
 
@@ -317,10 +313,15 @@ table_grad_kernel(const TI *__restrict__ dy, const TableGrad a, TO *__restrict__
     float sum[kEmbVec] = {};
     constexpr int kAhead = 4;
     for (int i = 0; i < count; i += kAhead) {
-        float v[kAhead][kEmbVec];
+        // the tokens' rows, and with them what the rows of the table hold whose runs end here
+        float v[kAhead][kEmbVec], old[kAdd ? kAhead : 1][kEmbVec];
 #pragma unroll
-        for (int k = 0; k < kAhead; ++k)
-            if (i + k < count) load8<TI, kVector>(dy + s_off[i + k], c, step, a.D, v[k]);
+        for (int k = 0; k < kAhead; ++k) {
+            if (i + k >= count) break;
+            load8<TI, kVector>(dy + s_off[i + k], c, step, a.D, v[k]);
+            if (kAdd && (i + k + 1 == count || s_row[i + k + 1] != s_row[i + k]))
+                load_old<TO, kVector>(dW + s_row[i + k] * (int64_t)a.D, c, step, a.D, old[k]);
+        }
 #pragma unroll
         for (int k = 0; k < kAhead; ++k) {
             if (i + k >= count) break;
@@ -339,7 +340,7 @@ table_grad_kernel(const TI *__restrict__ dy, const TableGrad a, TO *__restrict__
                     store8<float, false>(part, c, step, a.D, sum);
                 }
             } else {
-                finish8<TO, kVector, kAdd>(dW + row * (int64_t)a.D, c, step, a.D, a.scale, sum);
+                finish8<TO, kVector, kAdd>(dW + row * (int64_t)a.D, c, step, a.D, a.scale, sum, old[kAdd ? k : 0]);
             }
 #pragma unroll
             for (int e = 0; e < kEmbVec; ++e) sum[e] = 0.f;

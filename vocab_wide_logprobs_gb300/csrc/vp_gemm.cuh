@@ -257,12 +257,35 @@ static_assert(4 * kPairDualRegsLow + 8 * kPairDualRegsHigh == 12 * kPairDualRegs
 __host__ __device__ constexpr int pair_threads(bool dual) { return dual ? 12 * 32 : kLThreads; }
 __host__ __device__ constexpr int pair_epi_first_warp(bool dual) { return dual ? 4 : 2; }
 
-template <class Epi, bool kAMn = false, bool kBMn = false, bool kDual = false, bool kChain = false>
+// What a tile's sum goes over. Whole: all of K (and, chained, all of the second product's K). Split: an output
+// tile's k-blocks are shared out over `splits` tiles, whose sums the epilogue keeps apart (it is told which),
+// so that few output tiles with a long K fill the GPU; and a chained second product takes only the k-blocks
+// that a list names for the tile's rows (no list: all of them).
+struct WholeK {
+    static constexpr bool kSplit = false;
+};
+struct SplitK {
+    static constexpr bool kSplit = true;
+    int splits;
+    const int *count, *list;   // [n_mp], [n_mp][pitch]: the second product's k-blocks of a row block
+    int pitch;
+};
+// The k-blocks of one tile: k0 .. k1 of the first product, then l0 .. l1 of the second's list.
+struct TileK {
+    int k0, k1, l0, l1;
+};
+__device__ __forceinline__ TileK tile_k(const SplitK &p, int split, int n_k, int n_k2) {
+    auto share = [&](int n, int i) { return (int)((int64_t)n * i / p.splits); };
+    return {share(n_k, split), share(n_k, split + 1), share(n_k2, split), share(n_k2, split + 1)};
+}
+
+template <class Epi, bool kAMn = false, bool kBMn = false, bool kDual = false, bool kChain = false, class Ks = WholeK>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair_threads(kDual), 1)
 umma_gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
                       const __grid_constant__ CUtensorMap tm_a2, const __grid_constant__ CUtensorMap tm_b2, int M,
-                      int Nn, int K, int K2, int group_m, int l2hints, const Epi epi) {
+                      int Nn, int K, int K2, int group_m, int l2hints, const Epi epi, const Ks ks) {
     static_assert(!kDual || (!kAMn && !kBMn), "the dual form takes K-major operands");
+    static_assert(!(kDual && Ks::kSplit), "split sums are of one product");
     static_assert(!(kDual && kChain), "one second product at a time");
     extern __shared__ uint8_t smem_raw[];
     __shared__ PairBars bars;
@@ -270,7 +293,9 @@ umma_gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_con
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_rank();
     const int n_mp = (M + 2 * kLBM - 1) / (2 * kLBM), n_nb = (Nn + kLBN - 1) / kLBN;
-    const int64_t n_tiles = (int64_t)n_mp * n_nb;
+    const int64_t n_out = (int64_t)n_mp * n_nb;          // tiles of the output
+    int64_t n_tiles = n_out;
+    if constexpr (Ks::kSplit) n_tiles *= ks.splits;
     const int n_k = (K + kLBK - 1) / kLBK;
     const int n_k2 = (kDual || kChain) ? (K2 + kLBK - 1) / kLBK : 0;   // k-blocks of the second product
     const int64_t pair = blockIdx.x >> 1, n_pairs = gridDim.x >> 1;
@@ -312,19 +337,30 @@ umma_gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_con
             bool ok = true;
             for (int64_t tile = pair; tile < n_tiles && ok; tile += n_pairs) {
                 int mp, nb;
-                tile_coords(tile, n_mp, n_nb, group_m, mp, nb);
+                tile_coords(Ks::kSplit ? tile % n_out : tile, n_mp, n_nb, group_m, mp, nb);
                 const int mb = 2 * mp + (int)rank;
                 const int nrow = nb * kLBN + (int)rank * kPBHalf;
-                for (int kb = 0; kb < n_k + n_k2; ++kb, ++it) {
+                int n_first = n_k, n_all = n_k + n_k2;   // k-blocks of the tile's first product, and of both
+                TileK tk{0, n_k, 0, n_k2};
+                const int *list = nullptr;
+                if constexpr (Ks::kSplit) {
+                    if (kChain && ks.count) list = ks.list + (int64_t)mp * ks.pitch;
+                    tk = tile_k(ks, (int)(tile / n_out), n_k, kChain && ks.count ? __ldg(ks.count + mp) : n_k2);
+                    n_first = tk.k1 - tk.k0;
+                    n_all = n_first + tk.l1 - tk.l0;
+                }
+                for (int kb = 0; kb < n_all; ++kb, ++it) {
                     const uint32_t st = it % kPStages, use = it / kPStages;
                     if (use > 0 && !mbar_wait_cluster(&bars.empty[st], (use - 1) & 1)) { ok = false; break; }
                     uint8_t *a = smem + st * kPStageBytes;
                     const uint32_t fb = cluster_addr(&bars.full[st], 0);
                     if (rank == 0) mbar_arrive_expect_tx(&bars.full[st], 2 * kPStageBytes);
                     // k-blocks past n_k belong to the second product (its own maps)
-                    const bool second = (kDual || kChain) && kb >= n_k;
+                    const bool second = (kDual || kChain) && kb >= n_first;
                     const CUtensorMap *ma = second ? &tm_a2 : &tm_a, *mbm = second ? &tm_b2 : &tm_b;
-                    const int kc = (second ? kb - n_k : kb) * kLBK;
+                    int kc = (second ? kb - n_first + tk.l0 : kb + tk.k0) * kLBK;
+                    if constexpr (Ks::kSplit)
+                        if (second && list) kc = __ldg(list + kb - n_first + tk.l0) * kLBK;
                     if (kAMn) {
 #pragma unroll
                         for (int i = 0; i < kLBM / 64; ++i)
@@ -359,7 +395,14 @@ umma_gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_con
                     tc_fence_after();
                     const uint32_t d = tmem + buf * kLBN;
                     // a chained second product accumulates into the same accumulator
-                    const int nkb = kChain ? n_k + n_k2 : p ? n_k2 : n_k;
+                    int nkb = kChain ? n_k + n_k2 : p ? n_k2 : n_k;
+                    if constexpr (Ks::kSplit) {
+                        int mp, nb;
+                        tile_coords(Ks::kSplit ? tile % n_out : tile, n_mp, n_nb, group_m, mp, nb);
+                        const TileK tk = tile_k(ks, (int)(tile / n_out), n_k,
+                                                kChain && ks.count ? __ldg(ks.count + mp) : n_k2);
+                        nkb = tk.k1 - tk.k0 + tk.l1 - tk.l0;
+                    }
                     for (int kb = 0; kb < nkb; ++kb, ++it) {
                         const uint32_t st = it % kPStages;
                         if (!mbar_wait(&bars.full[st], (it / kPStages) & 1)) { ok = false; break; }
@@ -395,7 +438,7 @@ umma_gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_con
         bool ok = true;
         for (int64_t tile = pair; tile < n_tiles; tile += n_pairs, ++j) {
             int mp, nb;
-            tile_coords(tile, n_mp, n_nb, group_m, mp, nb);
+            tile_coords(Ks::kSplit ? tile % n_out : tile, n_mp, n_nb, group_m, mp, nb);
             const int mb = 2 * mp + (int)rank;
             if constexpr (kDual) {
                 const int c0 = nb * kLBN + half * kDualEpiCols;
@@ -425,8 +468,13 @@ umma_gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_con
                     pair_gives_up(bars, 4u);
                 }
                 tc_fence_after();
-                if (__all_sync(0xffffffffu, ok))
-                    epi(mb * kLBM + r_in, nb * kLBN, min(kLBN, Nn - nb * kLBN), tmem + buf * kLBN + lanes);
+                if (__all_sync(0xffffffffu, ok)) {
+                    const uint32_t acc = tmem + buf * kLBN + lanes;
+                    if constexpr (Ks::kSplit)
+                        epi(mb * kLBM + r_in, nb * kLBN, min(kLBN, Nn - nb * kLBN), acc, (int)(tile / n_out));
+                    else
+                        epi(mb * kLBM + r_in, nb * kLBN, min(kLBN, Nn - nb * kLBN), acc);
+                }
                 tc_fence_before();
                 mbar_arrive_cluster(cluster_addr(&bars.acc_empty[buf], 0));
             }
@@ -622,15 +670,15 @@ static cudaError_t launch_gemm(const CUtensorMap &ta, const CUtensorMap &tb, int
 // CTA-pair form (umma_gemm_pair_kernel): K-major B maps need boxes of 128 rows
 // (kPBHalf); MN-major maps are the same 64 x 64 boxes as for one CTA. group_m
 // counts 256-row pair blocks; <= 0 picks about 32 MB of A per group.
-template <class Epi, bool kAMn, bool kBMn, bool kDual, bool kChain = false>
+template <class Epi, bool kAMn, bool kBMn, bool kDual, bool kChain = false, class Ks = WholeK>
 static cudaError_t launch_gemm_pair_impl(const CUtensorMap &ta, const CUtensorMap &tb, const CUtensorMap &ta2,
                                         const CUtensorMap &tb2, int M, int Nn, int K, int K2, const Epi &epi,
-                                        cudaStream_t stream, int group_m, int l2hints) {
+                                        cudaStream_t stream, int group_m, int l2hints, const Ks &ks = Ks()) {
     static std::atomic<uint64_t> attr_done{0};
     int dev = 0;
     cudaGetDevice(&dev);
     if (!(attr_done.load() & (1ull << (dev & 63)))) {
-        cudaError_t e = cudaFuncSetAttribute(umma_gemm_pair_kernel<Epi, kAMn, kBMn, kDual, kChain>,
+        cudaError_t e = cudaFuncSetAttribute(umma_gemm_pair_kernel<Epi, kAMn, kBMn, kDual, kChain, Ks>,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize, kPSmemBytes);
         if (e != cudaSuccess) return e;
         if (kDual) {
@@ -638,7 +686,7 @@ static cudaError_t launch_gemm_pair_impl(const CUtensorMap &ta, const CUtensorMa
             // kPairDualRegsLaunch registers a thread; with fewer, setmaxnreg.inc
             // would wait for registers that do not exist, so refuse instead
             cudaFuncAttributes fa;
-            if ((e = cudaFuncGetAttributes(&fa, umma_gemm_pair_kernel<Epi, kAMn, kBMn, kDual, kChain>)) != cudaSuccess)
+            if ((e = cudaFuncGetAttributes(&fa, umma_gemm_pair_kernel<Epi, kAMn, kBMn, kDual, kChain, Ks>)) != cudaSuccess)
                 return e;
             if (fa.numRegs != kPairDualRegsLaunch) return cudaErrorInvalidConfiguration;
         }
@@ -647,14 +695,15 @@ static cudaError_t launch_gemm_pair_impl(const CUtensorMap &ta, const CUtensorMa
     int sms = 0;
     cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     const int n_mp = (M + 2 * kLBM - 1) / (2 * kLBM);
-    const int64_t n_tiles = (int64_t)n_mp * ((Nn + kLBN - 1) / kLBN);
+    int64_t n_tiles = (int64_t)n_mp * ((Nn + kLBN - 1) / kLBN);
+    if constexpr (Ks::kSplit) n_tiles *= ks.splits;
     const int64_t pairs = std::max(1, sms / 2);
     const unsigned grid = (unsigned)(2 * (n_tiles < pairs ? n_tiles : pairs));
     if (group_m <= 0)   // about 32 MB of A (both products' A tiles in the dual form) per m-group
         group_m = (int)std::max<int64_t>(1, ((int64_t)32 << 20) / ((int64_t)2 * kLBM * (K + (kDual ? K2 : 0)) * 2));
     if (group_m > n_mp) group_m = n_mp;
-    umma_gemm_pair_kernel<Epi, kAMn, kBMn, kDual, kChain><<<grid, pair_threads(kDual), kPSmemBytes, stream>>>(
-        ta, tb, ta2, tb2, M, Nn, K, K2, group_m, l2hints, epi);
+    umma_gemm_pair_kernel<Epi, kAMn, kBMn, kDual, kChain, Ks><<<grid, pair_threads(kDual), kPSmemBytes, stream>>>(
+        ta, tb, ta2, tb2, M, Nn, K, K2, group_m, l2hints, epi, ks);
     return cudaGetLastError();
 }
 template <class Epi, bool kAMn = false, bool kBMn = false>

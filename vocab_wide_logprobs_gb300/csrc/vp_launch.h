@@ -11,6 +11,7 @@ constexpr int VP_ERRBIT_TARGET_ = 1;  // same value as VP_ERRBIT_TARGET in inclu
 constexpr int VP_ERRBIT_RULES_ = 2;   // same value as VP_ERRBIT_RULES
 constexpr int VP_GRAD_EXACT_ = 0;     // same values as VP_GRAD_EXACT / VP_GRAD_FAST in include/vp.h
 constexpr int VP_GRAD_FAST_ = 1;
+constexpr int VP_GRAD_MIXED_ = 2;     // the linear cross entropy's (VP_GRAD_MIXED)
 
 struct StatsArgs {
     const void *x;
@@ -268,7 +269,7 @@ struct CeArgs {
     const void *hidden = nullptr, *weight = nullptr;   // [N, D], [V, D]
     int64_t D = 0;
     void *dhidden = nullptr, *dW = nullptr;            // either may be NULL
-    int precision = 0;            // VP_GRAD_EXACT or VP_GRAD_FAST (as LinearBwdArgs)
+    int precision = 0;            // VP_GRAD_EXACT, VP_GRAD_FAST or VP_GRAD_MIXED
 };
 int64_t ce_workspace_bytes(bool bf16, int64_t N, int64_t V);
 size_t linear_ce_workspace_bytes(int64_t N, int64_t V);

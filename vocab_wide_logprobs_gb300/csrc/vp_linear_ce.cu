@@ -63,8 +63,36 @@ struct CeEpi {
     }
 };
 
+// A warp's 32 rows of 64 bf16 columns to global memory, row `first` + i from lane i's eight vectors, through
+// shared memory: eight lanes then write a row's 128 bytes at once. Straight from the lanes every store would
+// touch half a sector of each of 32 rows (dW of 75968 x 4096 from 16 tokens took 256 us, its bytes are 92).
+__device__ __forceinline__ void store_rows64(uint4 *stage, const uint4 (&v)[8], __nv_bfloat16 *dst, int64_t ld, int first,
+                                             int M) {
+    const int lane = threadIdx.x & 31;
+    __syncwarp();                                        // the last rows have been read
+#pragma unroll
+    for (int j = 0; j < 8; ++j) stage[lane * 8 + (j ^ (lane & 7))] = v[j];
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int r = 4 * i + lane / 8, j = lane % 8;
+        if (first + r < M) stg_stream(dst + r * ld + 8 * j, stage[r * 8 + (j ^ (r & 7))]);
+    }
+}
+constexpr int kStageVecs = 32 * 8;                       // of each epilogue warp: 4 KB
+
+// Which values of dz the mixed precision carries as a pair. One bf16 value is off by up to 2^-8 of
+// itself, so what the values up to a threshold of a row add to the error of dhidden is 2^-8 sqrt(sum of
+// their squares) |W|, and with a threshold of t times the row's own scale s (for a cross entropy the values
+// add up to about 2 s, s = |g| (1 - p_t), through the cap's slope at the target) that is below
+// 2^-8 sqrt(2 t) s |W|: for t = 1/16 about a third of what the output's own rounding adds. The larger values
+// of a row, its target's first of all, are pairs. Which 32 x 64 pieces of dz hold one is noted, and the
+// gradient GEMMs take the second halves of no other k-blocks.
+constexpr float kPairShare = 1.f / 16.f;
+constexpr int kFlagRows = 32, kFlagCols = 64;
+
 // dz of a 256-column tile of the piece that starts at shard column v0, as bf16 (and, with
-// lo_off != 0, what that rounding took away as a second one: store_dz).
+// lo_off != 0, what that rounding took away as a second one).
 template <bool kCap>
 struct DzCeEpi {
     int N, V, v0, ldz;
@@ -76,6 +104,7 @@ struct DzCeEpi {
     __nv_bfloat16 *dz;
     int32_t *err;
     int64_t lo_off;
+    uint8_t *flags;     // [N / 32][ldz / 64], or NULL: no notes
     __device__ __forceinline__ void operator()(int row, int col0, int ncol, uint32_t taddr) const {
         const bool valid = row < N;
         const RowStat s = load_rowstat(stats + (valid ? row : 0));
@@ -85,37 +114,76 @@ struct DzCeEpi {
         int mode = (s.flags & (kRowNanInf | kRowEmpty | kRowBadTarget)) || outside ? 2 : 0;   // 1 zeros, 2 NaN
         if (tg < 0) mode = 1;
         if (valid && outside && err && col0 == 0 && v0 == 0) atomicOr(err, VP_ERRBIT_TARGET_);
-        const int64_t tl0 = tg >= 0 ? tl : -1;
-        const int64_t tcol = tl0 - v0 - col0;               // target column within this tile
+        const int64_t tcol = tg >= 0 ? tl - v0 - col0 : -1;   // target column within this tile
         const CeGradRow gr = ce_grad_row(q, s, valid ? g[row] : 0.f);
+        // the record's c is log p of the target
+        float limit = kPairShare * fabsf(gr.g) * fmaxf(q.smooth - expm1f(s.c_hi), 9.5367431640625e-07f);
+        if (kCap) {
+            const float zt = (s.m + s.logS_hi + s.c_hi) * q.inv_cap;
+            limit *= fmaxf(fmaf(-zt, zt, 1.f), 9.5367431640625e-07f);
+        }
+        __shared__ uint4 stage[kLThreads / 32 - 2][kStageVecs];
+        uint4 *mine = stage[(threadIdx.x >> 5) & 3];
+        const int first = row - (threadIdx.x & 31);           // the warp's first row
 #pragma unroll 1
-        for (int c = 0; c < kLBN / 32; ++c) {
-            float v[32], slope[32];
-            tmem_ld32(taddr + c * 32, v);
-            if (kCap) soft_cap<32, true>(q, v, slope);
-            const int64_t at = tcol - c * 32;
-            float zt = 0.f;
+        for (int c = 0; c < kLBN / 64; ++c) {
+            uint4 hi[8], lo[8];
+            float most = 0.f;                                 // of the row's 64 columns
 #pragma unroll
-            for (int i = 0; i < 32; i += 2) {
-                if (i == at) zt = v[i];
-                if (i + 1 == at) zt = v[i + 1];
-                float2 d = ce_grad2(gr, make_float2(v[i], v[i + 1]));
-                v[i] = d.x;
-                v[i + 1] = d.y;
-            }
-            if (at >= 0 && at < 32) {
-                const float d = ce_grad_target(q, gr, zt);
+            for (int half = 0; half < 2; ++half) {
+                const int c0 = c * 64 + half * 32;
+                float v[32], slope[32];
+                tmem_ld32(taddr + c0, v);
+                if (kCap) soft_cap<32, true>(q, v, slope);
+                const int64_t at = tcol - c0;
+                float zt = 0.f;
 #pragma unroll
-                for (int i = 0; i < 32; ++i)
-                    if (i == at) v[i] = d;
-            }
+                for (int i = 0; i < 32; i += 2) {
+                    if (i == at) zt = v[i];
+                    if (i + 1 == at) zt = v[i + 1];
+                    const float2 d = ce_grad2(gr, make_float2(v[i], v[i + 1]));
+                    v[i] = d.x;
+                    v[i + 1] = d.y;
+                }
+                if (at >= 0 && at < 32) {
+                    const float d = ce_grad_target(q, gr, zt);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
-                if (kCap) v[i] *= slope[i];
-                if (mode == 1 || c * 32 + i >= ncol) v[i] = 0.f;
-                else if (mode == 2) v[i] = qnan();
+                    for (int i = 0; i < 32; ++i)
+                        if (i == at) v[i] = d;
+                }
+                if (kCap) {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) v[i] *= slope[i];
+                }
+                if (mode || c0 + 32 > ncol) {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) v[i] = mode == 1 || c0 + i >= ncol ? 0.f : mode == 2 ? qnan() : v[i];
+                }
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    uint32_t h[4], l[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float x0 = v[8 * k + 2 * i], x1 = v[8 * k + 2 * i + 1];
+                        most = fmaxf(most, fmaxf(fabsf(x0), fabsf(x1)));
+                        const __nv_bfloat162 b = __floats2bfloat162_rn(x0, x1);
+                        h[i] = *reinterpret_cast<const uint32_t *>(&b);
+                        // what the rounding took away (exact in fp32), itself rounded
+                        const __nv_bfloat162 r = __floats2bfloat162_rn(x0 - __low2float(b), x1 - __high2float(b));
+                        l[i] = *reinterpret_cast<const uint32_t *>(&r);
+                    }
+                    hi[half * 4 + k] = make_uint4(h[0], h[1], h[2], h[3]);
+                    lo[half * 4 + k] = make_uint4(l[0], l[1], l[2], l[3]);
+                }
             }
-            if (valid) store_dz(dz + (int64_t)row * ldz + col0 + c * 32, v, lo_off);
+            __nv_bfloat16 *dst = dz + (int64_t)first * ldz + col0 + c * 64;
+            store_rows64(mine, hi, dst, ldz, first, N);
+            if (lo_off) store_rows64(mine, lo, dst + lo_off, ldz, first, N);
+            if (flags) {
+                const bool pair = __any_sync(0xffffffffu, valid && most > limit);
+                if ((row & 31) == 0 && valid)
+                    flags[(int64_t)(row / kFlagRows) * (ldz / kFlagCols) + (col0 + c * 64) / kFlagCols] = pair;
+            }
         }
     }
 };
@@ -140,7 +208,7 @@ cudaError_t launch_linear_ce_fwd(const CeArgs &a) {
     float *tgt = reinterpret_cast<float *>(ws + L.tgt);
     const CeRules q = ce_rules(a.opt);
     auto gemm = [&](const auto &epi) {
-        return launch_logits_gemm(a.hidden, a.weight, (int)a.N, (int)a.V, (int)a.D, epi, a.stream, kFwdPairs);
+        return launch_logits_gemm(a.hidden, a.weight, (int)a.N, (int)a.V, (int)a.D, epi, a.stream, true);
     };
     const cudaError_t e = q.cap > 0.f
                               ? gemm(CeEpi<true>{(int)a.N, n_t, a.vocab_start, a.targets, q, tiles, tgt})
@@ -149,46 +217,216 @@ cudaError_t launch_linear_ce_fwd(const CeArgs &a) {
     return launch_ce_join(CeTiles{tiles, tgt, n_t, (int)a.V}, n_t, a);
 }
 
-struct CeBwdLayout {
-    size_t dz, acc, total;
+// From the notes, the k-blocks whose second halves the gradient GEMMs take: for each 256 rows of dz the
+// 64-column blocks (dhidden), and for each 256 columns the 64-row blocks (dW), in order. One CTA for a list.
+__global__ void __launch_bounds__(256)
+pair_list_kernel(const uint8_t *__restrict__ flags, int row_groups, int pitch, int col_groups, int n_rows, int *__restrict__ count,
+                 int *__restrict__ list, int pitch_rows, int pitch_cols) {
+    __shared__ uint32_t s_n[8];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const bool by_rows = (int)blockIdx.x < n_rows;
+    const int b = by_rows ? blockIdx.x : blockIdx.x - n_rows;
+    const int n = by_rows ? col_groups : (row_groups + 1) / 2;
+    int *out = list + (by_rows ? (int64_t)b * pitch_rows : (int64_t)n_rows * pitch_rows + (int64_t)b * pitch_cols);
+    uint32_t done = 0;
+    for (int k0 = 0; k0 < n; k0 += 256) {
+        const int k = k0 + tid;
+        bool any = false;
+        if (k < n) {
+            // 8 groups of rows and one of columns, or 2 and 4 (one word: the pitch is a multiple of 4)
+            const int r0 = by_rows ? 8 * b : 2 * k;
+            uint32_t seen = 0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                if (r0 + i >= row_groups || (!by_rows && i >= 2)) continue;
+                const uint8_t *f = flags + (int64_t)(r0 + i) * pitch;
+                seen |= by_rows ? f[k] : *reinterpret_cast<const uint32_t *>(f + 4 * b);
+            }
+            any = seen != 0;
+        }
+        const uint32_t votes = __ballot_sync(0xffffffffu, any);
+        if (lane == 0) s_n[warp] = __popc(votes);
+        __syncthreads();
+        uint32_t before = done;
+        for (int w = 0; w < 8; ++w) {
+            if (w < warp) before += s_n[w];
+            done += s_n[w];
+        }
+        if (any) out[before + __popc(votes & ((1u << lane) - 1u))] = k;
+        __syncthreads();
+    }
+    if (tid == 0) count[blockIdx.x] = (int)done;
+}
+
+// dhidden's tiles: the sum over a share of the k-blocks, kept apart for each share.
+struct SplitAccEpi {
+    int M, ld;
+    bool first;
+    float *acc;          // [splits][M][ld]
+    __device__ __forceinline__ void operator()(int row, int col0, int ncol, uint32_t taddr, int split) const {
+        AccEpi{M, ld, first, acc + (int64_t)split * M * ld, nullptr}(row, col0, ncol, taddr);
+    }
 };
-static CeBwdLayout ce_bwd_layout(int64_t N, int64_t V, int64_t D) {
-    const int64_t vc = chunk_cols(N, V);
+// dW's tiles, rounded; ld is a multiple of 64.
+struct StoreRowsEpi {
+    int M, ld;
+    int64_t row0;
+    __nv_bfloat16 *out;
+    __device__ __forceinline__ void operator()(int row, int col0, int ncol, uint32_t taddr, int) const {
+        __shared__ uint4 stage[kLThreads / 32 - 2][kStageVecs];
+        uint4 *mine = stage[(threadIdx.x >> 5) & 3];
+        const int first = row - (threadIdx.x & 31);
+#pragma unroll 1
+        for (int c = 0; c < ncol; c += 64) {
+            uint4 v[8];
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                float f[32];
+                tmem_ld32(taddr + c + half * 32, f);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) v[half * 4 + k] = Elem<__nv_bfloat16>::pack(f + 8 * k);
+            }
+            store_rows64(mine, v, out + (row0 + first) * (int64_t)ld + col0 + c, ld, first, M);
+        }
+    }
+};
+
+// The shares' sums, added in order and rounded once.
+__global__ void __launch_bounds__(256)
+split_sum_kernel(const float *__restrict__ acc, int64_t n, int splits, __nv_bfloat16 *__restrict__ out) {
+    const int64_t i = 8 * ((int64_t)blockIdx.x * 256 + threadIdx.x);   // n is a multiple of 64
+    if (i >= n) return;
+    float v[8] = {};
+    for (int s = 0; s < splits; ++s) {
+        const float4 a = *reinterpret_cast<const float4 *>(acc + s * n + i), b = *reinterpret_cast<const float4 *>(acc + s * n + i + 4);
+        v[0] += a.x; v[1] += a.y; v[2] += a.z; v[3] += a.w;
+        v[4] += b.x; v[5] += b.y; v[6] += b.z; v[7] += b.w;
+    }
+    *reinterpret_cast<uint4 *>(out + i) = Elem<__nv_bfloat16>::pack(v);
+}
+
+// Columns of the vocabulary a piece: dz twice over near 1 GB, so that few rows take the whole vocabulary at
+// once; 8192 at least.
+static int64_t ce_piece(int64_t N, int64_t V) {
+    const int64_t fit = ((int64_t)1 << 28) / N / 256 * 256, all = (V + 255) / 256 * 256;
+    return std::min(all, std::clamp<int64_t>(fit, 8192, 1 << 22));
+}
+
+// Shares of dhidden's k-blocks: its output tiles are few where N and D are, and the GPU's pairs of SMs then
+// stand still. The waves of tiles that a split makes, counted in whole tiles, with 1 % of them for
+// each share's sums, which are written and read once more.
+static int ce_splits(int64_t N, int64_t piece, int64_t D, int pairs) {
+    const int64_t tiles = ((N + 255) / 256) * ((D + 255) / 256);
+    int best = 1;
+    double least = 1e30;
+    for (int s = 1; s <= 16 && s <= piece / 512; ++s) {
+        const double cost = (double)((tiles * s + pairs - 1) / pairs) / s + 0.01 * s;
+        if (cost < least) least = cost, best = s;
+    }
+    return best;
+}
+
+struct CeBwdLayout {
+    size_t dz, acc, flags, count, list, total;
+    int64_t vc;
+    int splits, row_groups, col_groups, n_rows, n_cols, pitch_rows, pitch_cols;
+};
+static CeBwdLayout ce_bwd_layout(int64_t N, int64_t V, int64_t D, int pairs) {
     CeBwdLayout L;
+    L.vc = ce_piece(N, V);
+    L.splits = ce_splits(N, L.vc, D, pairs);
+    L.row_groups = (int)((N + kFlagRows - 1) / kFlagRows);
+    L.col_groups = (int)(L.vc / kFlagCols);
+    L.n_rows = (int)((N + 255) / 256);
+    L.n_cols = (int)(L.vc / 256);
+    L.pitch_rows = L.col_groups;
+    L.pitch_cols = (L.row_groups + 1) / 2;
     L.dz = 0;
-    L.acc = up256((size_t)2 * N * vc * 2);
-    L.total = L.acc + up256((size_t)N * D * 4);
+    L.acc = up256((size_t)2 * N * L.vc * 2);
+    L.flags = L.acc + up256((size_t)L.splits * N * D * 4);
+    L.count = L.flags + up256((size_t)L.row_groups * L.col_groups);
+    L.list = L.count + up256((size_t)(L.n_rows + L.n_cols) * 4);
+    L.total = L.list + up256(((size_t)L.n_rows * L.pitch_rows + (size_t)L.n_cols * L.pitch_cols) * 4);
     return L;
 }
-size_t linear_ce_bwd_workspace_bytes(int64_t N, int64_t V, int64_t D) { return ce_bwd_layout(N, V, D).total; }
+static int sm_pairs() {
+    int dev = 0, sms = 0;
+    cudaGetDevice(&dev);
+    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    return std::max(1, sms / 2);
+}
+size_t linear_ce_bwd_workspace_bytes(int64_t N, int64_t V, int64_t D) {
+    return N ? ce_bwd_layout(N, V, D, sm_pairs()).total : 0;
+}
 
 cudaError_t launch_linear_ce_bwd(const CeArgs &a) {
-    const CeBwdLayout L = ce_bwd_layout(a.N, a.V, a.D);
-    const int64_t vc = chunk_cols(a.N, a.V);
+    const CeBwdLayout L = ce_bwd_layout(a.N, a.V, a.D, sm_pairs());
+    const int64_t vc = L.vc;
     uint8_t *ws = static_cast<uint8_t *>(a.workspace);
     __nv_bfloat16 *dz = reinterpret_cast<__nv_bfloat16 *>(ws + L.dz);
-    const int64_t lo_off = a.precision == VP_GRAD_EXACT_ ? a.N * vc : 0;   // dz_lo follows dz_hi
-    float *acc = a.dhidden ? reinterpret_cast<float *>(ws + L.acc) : nullptr;
+    const bool chain = a.precision != VP_GRAD_FAST_, mixed = a.precision == VP_GRAD_MIXED_;
+    const __nv_bfloat16 *dz_lo = dz + a.N * vc;            // behind dz_hi
+    float *acc = reinterpret_cast<float *>(ws + L.acc);
+    uint8_t *flags = mixed ? ws + L.flags : nullptr;
+    int *count = reinterpret_cast<int *>(ws + L.count), *list = reinterpret_cast<int *>(ws + L.list);
+    const SplitK of_rows{L.splits, mixed ? count : nullptr, list, L.pitch_rows};
+    const SplitK of_cols{1, mixed ? count + L.n_rows : nullptr, list + (int64_t)L.n_rows * L.pitch_rows, L.pitch_cols};
     const __nv_bfloat16 *h = static_cast<const __nv_bfloat16 *>(a.hidden);
     const __nv_bfloat16 *W = static_cast<const __nv_bfloat16 *>(a.weight);
     const RowStat *stats = static_cast<const RowStat *>(a.stats);
     const int N = (int)a.N, V = (int)a.V, D = (int)a.D;
     const CeRules q = ce_rules(a.opt);
     cudaError_t e;
-    CUtensorMap tm_h_mn;
-    if (!make_map_mn(&tm_h_mn, h, N, D, D)) return cudaErrorInvalidValue;
+    CUtensorMap tm_h;
+    if (!make_map_mn(&tm_h, h, N, D, D)) return cudaErrorInvalidValue;
     for (int64_t v0 = 0; v0 < V; v0 += vc) {
         const int nv = (int)(V - v0 < vc ? V - v0 : vc);
         auto gemm = [&](const auto &epi) {
-            return launch_logits_gemm(h, W + v0 * D, N, nv, D, epi, a.stream, kGemmPairs);
+            return launch_logits_gemm(h, W + v0 * D, N, nv, D, epi, a.stream, true);
         };
-        e = q.cap > 0.f ? gemm(DzCeEpi<true>{N, V, (int)v0, (int)vc, a.vocab_start, a.targets, q, stats, a.g, dz, a.err, lo_off})
-                        : gemm(DzCeEpi<false>{N, V, (int)v0, (int)vc, a.vocab_start, a.targets, q, stats, a.g, dz, a.err, lo_off});
+        const int64_t lo_off = chain ? a.N * vc : 0;
+        e = q.cap > 0.f ? gemm(DzCeEpi<true>{N, V, (int)v0, (int)vc, a.vocab_start, a.targets, q, stats, a.g, dz, a.err, lo_off, flags})
+                        : gemm(DzCeEpi<false>{N, V, (int)v0, (int)vc, a.vocab_start, a.targets, q, stats, a.g, dz, a.err, lo_off, flags});
         if (e != cudaSuccess) return e;
-        e = chunk_gradient_gemms(tm_h_mn, W, N, D, v0, nv, vc, dz, lo_off ? dz + lo_off : nullptr, acc,
-                                 static_cast<__nv_bfloat16 *>(a.dhidden), static_cast<__nv_bfloat16 *>(a.dW), v0 + vc >= V,
-                                 a.stream);
-        if (e != cudaSuccess) return e;
+        if (mixed) {
+            const int cols = (nv + 63) / 64, tiles = (nv + 255) / 256;
+            pair_list_kernel<<<L.n_rows + tiles, 256, 0, a.stream>>>(flags, L.row_groups, L.col_groups, cols, L.n_rows, count,
+                                                                     list, L.pitch_rows, L.pitch_cols);
+            if ((e = cudaGetLastError()) != cudaSuccess) return e;
+        }
+        auto product = [&](auto kinds, const CUtensorMap &ta, const CUtensorMap &tb, const CUtensorMap &ta2, int M, int Nn,
+                           int K, const auto &epi, int group, const SplitK &ks) {
+            using Epi = std::decay_t<decltype(epi)>;
+            constexpr bool kAMn = decltype(kinds)::value;
+            return chain ? launch_gemm_pair_impl<Epi, kAMn, true, false, true>(ta, tb, ta2, tb, M, Nn, K, K, epi, a.stream,
+                                                                              (group + 1) / 2, kHintK2, ks)
+                         : launch_gemm_pair_impl<Epi, kAMn, true, false, false>(ta, tb, ta, tb, M, Nn, K, 0, epi, a.stream,
+                                                                               (group + 1) / 2, kHintK2, ks);
+        };
+        if (a.dhidden) {
+            CUtensorMap ta, ta2, tb;
+            if (!make_map(&ta, dz, N, nv, vc, kLBM) || !make_map(&ta2, dz_lo, N, nv, vc, kLBM) ||
+                !make_map_mn(&tb, W + v0 * D, nv, D, D))
+                return cudaErrorInvalidValue;
+            // a short last piece has fewer k-blocks than there are shares; their sums stay as they are
+            SplitK ks = of_rows;
+            ks.splits = std::min(ks.splits, (nv + kLBK - 1) / kLBK);
+            e = product(std::false_type(), ta, tb, ta2, N, D, nv, SplitAccEpi{N, D, v0 == 0, acc}, kGradGroupM, ks);
+            if (e != cudaSuccess) return e;
+        }
+        if (a.dW) {
+            CUtensorMap ta, ta2;
+            if (!make_map_mn(&ta, dz, N, nv, vc) || !make_map_mn(&ta2, dz_lo, N, nv, vc)) return cudaErrorInvalidValue;
+            e = product(std::true_type(), ta, tm_h, ta2, nv, D, N,
+                        StoreRowsEpi{nv, D, v0, static_cast<__nv_bfloat16 *>(a.dW)}, kWGroupM, of_cols);
+            if (e != cudaSuccess) return e;
+        }
+    }
+    if (a.dhidden) {
+        const int64_t n = a.N * a.D;
+        split_sum_kernel<<<(unsigned)((n / 8 + 255) / 256), 256, 0, a.stream>>>(acc, n, L.splits,
+                                                                               static_cast<__nv_bfloat16 *>(a.dhidden));
+        return cudaGetLastError();
     }
     return cudaSuccess;
 }
