@@ -844,7 +844,7 @@ VP_API vp_status vp_embedding_fwd(const void *table, int dtype, int64_t V, int64
  * the rows' two strides as for logits; dW: contiguous [V, D]. Tokens of padding and of other shards
  * count nowhere; those of a data error neither, and set VP_ERRBIT_TARGET. N = 0 writes zeros, or
  * nothing where it accumulates. workspace: 256-byte aligned, vp_embedding_bwd_workspace_size(N, V, D)
- * bytes. */
+ * bytes; NULL where that is 0 (few tokens, or sizes that are not taken). */
 VP_API size_t vp_embedding_bwd_workspace_size(int64_t N, int64_t V, int64_t D);
 VP_API vp_status vp_embedding_bwd(const void *dy, int dtype, int64_t N, int64_t D, int64_t R, int64_t s_o, int64_t s_i,
                                   const int64_t *ids, int64_t V, int64_t vocab_start, int sharded, double scale,

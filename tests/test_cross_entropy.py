@@ -269,8 +269,10 @@ def test_targets_outside_the_shard():
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("dtype", [F32, BF16])
-def test_a_row_does_not_depend_on_the_batch(dtype):
-    x, targets, g = (t.cuda() for t in rows(70, 9008, dtype, 17, sigma=12.0))
+@pytest.mark.parametrize("N, V", [(70, 25008), (700, 1000)])
+def test_a_row_does_not_depend_on_the_batch(N, V, dtype):
+    """Neither joined out of several slices nor finished where it is summed (few short rows) or not (many)."""
+    x, targets, g = (t.cuda() for t in rows(N, V, dtype, 17, sigma=12.0))
     o = dict(label_smoothing=0.1, z_loss=1e-3, softcap=25.0)
     loss, stats = vp.vp_cross_entropy_fwd(x, targets, **o)
     dx = vp.vp_cross_entropy_bwd(x, targets, stats, g, **o)

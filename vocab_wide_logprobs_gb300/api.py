@@ -1176,8 +1176,10 @@ def vp_embedding_bwd(dy, ids, V: int, scale: float = 1.0, vocab_start: int = 0, 
     _on_gpu(dy)
     dW = torch.empty((V, D), dtype=dtype, device=dy.device) if dW is None else dW
     if workspace is None:
-        workspace = _workspace(_handle().vp_embedding_bwd_workspace_size(N, V, D), dy)
+        need = _handle().vp_embedding_bwd_workspace_size(N, V, D)
+        workspace = _workspace(need, dy) if need else None
     _check(_handle().vp_embedding_bwd(_addr(dy), code, N, D, R, s_o, s_i, _addr(ids), V, vocab_start, int(sharded), scale,
-                                      _addr(dW), _DTYPES[dtype], int(accumulate), _addr(workspace), _nbytes(workspace),
-                                      _addr(err_word), _queue(dy.device)), "vp_embedding_bwd")
+                                      _addr(dW), _DTYPES[dtype], int(accumulate), _addr(workspace),
+                                      0 if workspace is None else _nbytes(workspace), _addr(err_word), _queue(dy.device)),
+           "vp_embedding_bwd")
     return dW

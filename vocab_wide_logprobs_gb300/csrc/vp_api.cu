@@ -1081,10 +1081,11 @@ vp_status vp_embedding_bwd(const void *dy, int dtype, int64_t N, int64_t D, int6
         if ((st = check_device()) != VP_OK) return st;
         return launched(cudaMemsetAsync(dW, 0, (size_t)V * D * elem_size(out_dtype), (cudaStream_t)stream));
     }
-    if (!dy || !ids || !workspace) return VP_ERR_NULL;
+    const size_t need = vp::embedding_bwd_workspace_bytes(N, V, D);
+    if (!dy || !ids || (need && !workspace)) return VP_ERR_NULL;
     if (!aligned(dy, elem_size(dtype)) || !aligned(ids, 8) || !aligned(workspace, 256) || !aligned(err_word, 4))
         return VP_ERR_ALIGN;
-    if (workspace_bytes < vp::embedding_bwd_workspace_bytes(N, V, D)) return VP_ERR_ARG;
+    if (workspace_bytes < need) return VP_ERR_ARG;
     if ((st = check_device()) != VP_OK) return st;
     vp::EmbeddingArgs a{dy, dtype == VP_BF16, out_dtype == VP_BF16, N, V, D, R, s_o, s_i, vocab_start, ids,
                         (float)scale, sharded != 0, dW, accumulate != 0, err_word, workspace, (cudaStream_t)stream};

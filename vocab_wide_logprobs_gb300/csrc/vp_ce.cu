@@ -15,6 +15,7 @@ namespace vp {
 
 constexpr int kCeThreads = 256;
 constexpr int kCeFwdVecs = 8;                    // vectors of a thread
+constexpr int64_t kCeFewRows = 608;              // four for each SM
 constexpr int ce_grad_vecs(bool cap) { return cap ? 8 : 4; }
 
 static int64_t ce_slices(bool bf16, int vecs, int64_t V) {
@@ -59,7 +60,8 @@ __device__ __forceinline__ float vec_max(const uint4 &u, float m) {
 template <typename T, bool kCap, bool kSum>
 __global__ void __launch_bounds__(kCeThreads, 4)
 ce_fwd_kernel(const T *__restrict__ x, int V, Rows rows, const CeRules q, const int64_t *__restrict__ targets,
-              int64_t vocab_start, int n_slices, int64_t total, CeSlice *__restrict__ slices) {
+              int64_t vocab_start, int n_slices, int64_t total, CeSlice *__restrict__ slices, bool whole,
+              const CeJoinArgs join) {
     constexpr int kVec = Elem<T>::kVec, kWarps = kCeThreads / 32, kCeVecs = kCeFwdVecs, kCeSliceVecs = kCeThreads * kCeVecs;
     __shared__ float s_max[kWarps];
     __shared__ DF s_S[kWarps], s_W[kWarps];
@@ -166,9 +168,16 @@ ce_fwd_kernel(const T *__restrict__ x, int V, Rows rows, const CeRules q, const 
                           (has_target ? kPartHasTarget : 0u) | (minus_inf ? kCeMinusInf : 0u),
                           (uint32_t)(max(v1 - v0, 0) * kVec + extra)};
                 if (!(S_all < INFINITY)) o.S = qnan(), o.S_lo = 0.f;     // a NaN, or +inf without a cap
-                uint4 *dst = reinterpret_cast<uint4 *>(slices + tile);
-                dst[0] = reinterpret_cast<const uint4 *>(&o)[0];
-                dst[1] = reinterpret_cast<const uint4 *>(&o)[1];
+                if (whole) {
+                    CeRow c{m, {0.f, 0.f}, {0.f, 0.f}, 0.f, 0u, 0, 0u};
+                    ce_add(c, {o.m, {o.S, o.S_lo}, {o.W, o.W_lo}, o.zt, o.flags, o.n});
+                    if (join.parts) ce_finish<kCeRecords>(c, r, join);
+                    else ce_finish<kCeLoss>(c, r, join);
+                } else {
+                    uint4 *dst = reinterpret_cast<uint4 *>(slices + tile);
+                    dst[0] = reinterpret_cast<const uint4 *>(&o)[0];
+                    dst[1] = reinterpret_cast<const uint4 *>(&o)[1];
+                }
             }
         }
     }
@@ -264,14 +273,18 @@ static cudaError_t ce_fwd(const CeArgs &a) {
     const int64_t total = a.N * n_slices;
     const CeRules q = ce_rules(a.opt);
     CeSlice *work = static_cast<CeSlice *>(a.workspace);
+    // Rows of one slice are finished where they are summed, the same way, but for so many rows that the
+    // logarithms in 64 bits, one CTA's at a time, cost more than a launch that takes 32 at once.
+    const bool whole = n_slices == 1 && a.N <= kCeFewRows;
     auto go = [&](auto kernel) {
         return launch_pdl(kernel, dim3(ce_grid(total)), dim3(kCeThreads), 0, a.stream, static_cast<const T *>(a.x),
-                          (int)a.V, Rows{a.R, a.s_o, a.s_i}, q, a.targets, a.vocab_start, n_slices, total, work);
+                          (int)a.V, Rows{a.R, a.s_o, a.s_i}, q, a.targets, a.vocab_start, n_slices, total, work, whole,
+                          ce_join_args(a));
     };
     const bool sum = a.parts || q.smooth > 0.f;      // a shard's records are merged with any smoothing
     const cudaError_t e = q.cap > 0.f ? (sum ? go(ce_fwd_kernel<T, true, true>) : go(ce_fwd_kernel<T, true, false>))
                                       : (sum ? go(ce_fwd_kernel<T, false, true>) : go(ce_fwd_kernel<T, false, false>));
-    return e != cudaSuccess ? e : launch_ce_join(CeSlices{work, n_slices}, n_slices, a);
+    return e != cudaSuccess || whole ? e : launch_ce_join(CeSlices{work, n_slices}, n_slices, a);
 }
 
 cudaError_t launch_ce_fwd(const CeArgs &a) { return a.bf16 ? ce_fwd<__nv_bfloat16>(a) : ce_fwd<float>(a); }

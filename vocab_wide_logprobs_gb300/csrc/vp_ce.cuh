@@ -154,19 +154,38 @@ struct CeRow {
 };
 constexpr uint32_t kCeMinusInf = 1u << 30;
 
-// o, whose maximum is M, and a piece of n columns with maximum m, sum S and sum W (times 2^-24)
-__device__ __forceinline__ void ce_add(CeRow &o, float m, DF S, DF W, uint32_t n) {
-    if (S.hi != S.hi) o.flags |= kPartNanInf;
-    else if (S.hi > 0.f) {
-        const float a = expf(m - o.M);
-        df_add(o.S, a * S.hi);
-        df_add(o.S, a * S.lo);
+// A piece of a row as its record says it: n columns, the largest m, sum S and sum W (times 2^-24).
+struct CePiece {
+    float m;
+    DF S, W;
+    float zt;
+    uint32_t flags, n;
+};
+
+// o's centre moved up to M
+__device__ __forceinline__ void ce_recentre(CeRow &o, float M) {
+    if (M == o.M) return;
+    const float a = expf(o.M - M);
+    o.S.hi *= a;
+    o.S.lo *= a;
+    df_add(o.W, (float)o.n * fmaf(M, -kCeScale, o.M * kCeScale));
+    o.M = M;
+}
+// o and a piece whose maximum is not above o's
+__device__ __forceinline__ void ce_add(CeRow &o, const CePiece &p) {
+    o.flags |= p.flags;
+    if (p.flags & kPartHasTarget) o.zt = p.zt, ++o.owners;
+    if (p.S.hi != p.S.hi) o.flags |= kPartNanInf;
+    else if (p.S.hi > 0.f) {
+        const float a = expf(p.m - o.M);
+        df_add(o.S, a * p.S.hi);
+        df_add(o.S, a * p.S.lo);
     }
-    if (W.hi == W.hi) {
-        df_add(o.W, W);
-        df_add(o.W, (float)n * fmaf(o.M, -kCeScale, m * kCeScale));
+    if (p.W.hi == p.W.hi) {
+        df_add(o.W, p.W);
+        df_add(o.W, (float)p.n * fmaf(o.M, -kCeScale, p.m * kCeScale));
     }
-    o.n += n;
+    o.n += p.n;
 }
 
 // A slice of a row of logits: 32 bytes.
@@ -177,15 +196,12 @@ struct CeSlice {
 struct CeSlices {
     const CeSlice *slices;      // [N][K]
     int K;
-    __device__ __forceinline__ float max_of(int64_t r, int k) const { return slices[r * K + k].m; }
     __device__ __forceinline__ float target(int64_t, float zt) const { return zt; }
-    __device__ __forceinline__ void add(int64_t r, int k, CeRow &o) const {
+    __device__ __forceinline__ CePiece piece(int64_t r, int k) const {
         const uint4 *p = reinterpret_cast<const uint4 *>(slices + r * K + k);
         const uint4 a = p[0], b = p[1];
-        o.flags |= b.z;
-        if (b.z & kPartHasTarget) o.zt = __uint_as_float(b.y), ++o.owners;
-        ce_add(o, __uint_as_float(a.x), {__uint_as_float(a.y), __uint_as_float(a.z)},
-               {__uint_as_float(a.w), __uint_as_float(b.x)}, b.w);
+        return {__uint_as_float(a.x), {__uint_as_float(a.y), __uint_as_float(a.z)},
+                {__uint_as_float(a.w), __uint_as_float(b.x)}, __uint_as_float(b.y), b.z, b.w};
     }
 };
 
@@ -193,15 +209,13 @@ struct CeSlices {
 struct CeShards {
     const PartialRec *parts;
     int64_t N;
-    __device__ __forceinline__ float max_of(int64_t r, int k) const { return parts[k * N + r].m; }
     __device__ __forceinline__ float target(int64_t, float zt) const { return zt; }
-    __device__ __forceinline__ void add(int64_t r, int k, CeRow &o) const {
+    __device__ __forceinline__ CePiece piece(int64_t r, int k) const {
         const PartialRec p = parts[k * N + r];
-        o.flags |= p.flags;
-        if (p.flags & kPartHasTarget) o.zt = p.z_t, ++o.owners;
         const double W = p.W / kCeUnscale;
-        if (W == -INFINITY) o.flags |= kCeMinusInf;
-        ce_add(o, p.m, df_from(p.S), W == -INFINITY ? DF{0.f, 0.f} : df_from(W), (uint32_t)p.S_b);   // S_b: its columns
+        const bool minus_inf = W == -INFINITY;
+        return {p.m, df_from(p.S), minus_inf ? DF{0.f, 0.f} : df_from(W), p.z_t,
+                p.flags | (minus_inf ? kCeMinusInf : 0u), (uint32_t)p.S_b};          // S_b: its columns
     }
 };
 
@@ -211,17 +225,15 @@ struct CeTiles {
     const float4 *tiles;        // [N][n_t]
     const float *zt;            // [N]
     int n_t, V;
-    __device__ __forceinline__ float max_of(int64_t r, int k) const { return tiles[r * n_t + k].x; }
     __device__ __forceinline__ float target(int64_t r, float) const { return zt[r]; }
-    __device__ __forceinline__ void add(int64_t r, int k, CeRow &o) const {
+    __device__ __forceinline__ CePiece piece(int64_t r, int k) const {
         const float4 p = tiles[r * n_t + k];
         const int n = min(256, V - 256 * k);
         const float w = p.z * kCeScale;
-        if (w == -INFINITY) o.flags |= kCeMinusInf;
-        // sum of (z - m) = sum of z - n m
-        DF W{w == -INFINITY ? 0.f : w, 0.f};
-        if (w == w) df_add(W, -(float)n * (p.x * kCeScale));
-        ce_add(o, p.x, {p.y, 0.f}, W, (uint32_t)n);
+        const bool minus_inf = w == -INFINITY;
+        DF W{minus_inf ? 0.f : w, 0.f};
+        if (w == w) df_add(W, -(float)n * (p.x * kCeScale));                         // sum of (z - m)
+        return {p.x, {p.y, 0.f}, W, 0.f, minus_inf ? kCeMinusInf : 0u, (uint32_t)n};
     }
 };
 
@@ -245,52 +257,15 @@ struct CeJoinArgs {
     double smooth, zeta;
 };
 
-// kLanes lanes for a row, each for every kLanes-th piece in a fixed order; then one lane for each
-// of the CTA's rows takes the logarithm in 64 bits, a warp's worth of that narrow pipe for up to
-// 32 rows and not for one. 8 lanes where a row has up to 32 pieces, 32 lanes beyond.
-constexpr int kCeJoinThreads = 256;
 enum CeJoin { kCeLoss, kCeRecords, kCeGathered };   // losses; the shard's records; losses of gathered shards
-template <class Src, CeJoin kind, int kLanes>
-__global__ void __launch_bounds__(kCeJoinThreads)
-ce_join_kernel(const Src src, int K, const CeJoinArgs a) {
-    constexpr int kRows = kCeJoinThreads / kLanes;
-    static_assert(kRows <= 32, "a lane for each row");
-    __shared__ CeRow rows[kRows];
-    pdl_enter<false>();
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int64_t r0 = (int64_t)blockIdx.x * kRows;
-    {
-        const int i = threadIdx.x / kLanes, k0 = threadIdx.x % kLanes;
-        const int64_t r = r0 + i < a.N ? r0 + i : a.N - 1;     // a lane without a row of its own votes along
-        CeRow o{kNegBig, {0.f, 0.f}, {0.f, 0.f}, 0.f, 0u, 0, 0u};
-#pragma unroll 4
-        for (int k = k0; k < K; k += kLanes) o.M = fmaxf(o.M, src.max_of(r, k));
-#pragma unroll
-        for (int m = kLanes / 2; m > 0; m >>= 1) o.M = fmaxf(o.M, __shfl_xor_sync(0xffffffffu, o.M, m));
-#pragma unroll 4
-        for (int k = k0; k < K; k += kLanes) src.add(r, k, o);
-#pragma unroll
-        for (int m = kLanes / 2; m > 0; m >>= 1) {
-            const int owners = __shfl_xor_sync(0xffffffffu, o.owners, m);
-            const float zt = __shfl_xor_sync(0xffffffffu, o.zt, m);
-            if (owners > o.owners) o.zt = zt;
-            o.owners += owners;
-            o.flags |= __shfl_xor_sync(0xffffffffu, o.flags, m);
-            o.n += __shfl_xor_sync(0xffffffffu, o.n, m);
-            df_add(o.S, shfl_xor(o.S, m));
-            df_add(o.W, shfl_xor(o.W, m));
-        }
-        if (k0 == 0) rows[i] = o;
-    }
-    __syncthreads();
-    if (warp != 0 || lane >= kRows || r0 + lane >= a.N) return;
-    const int64_t r = r0 + lane;
-    const CeRow o = rows[lane];
+
+// A row's loss and record, or the shard's record.
+template <CeJoin kind>
+__device__ __forceinline__ void ce_finish(const CeRow &o, int64_t r, const CeJoinArgs &a) {
     const double S = df_value(o.S);
     const double W = (o.flags & kCeMinusInf) ? -INFINITY : df_value(o.W) * kCeUnscale;
     const bool nan = (o.flags & kPartNanInf) || S != S;
     bool ignored, bad;
-    float zt = o.zt;
     if (kind == kCeGathered) {
         ignored = (o.flags & kPartIgnored) != 0;
         bad = !ignored && o.owners != 1;
@@ -298,8 +273,8 @@ ce_join_kernel(const Src src, int K, const CeJoinArgs a) {
         const int64_t t = a.targets[r], loc = t - a.vocab_start;
         ignored = t < 0;
         bad = !ignored && (loc < 0 || loc >= a.V);
-        zt = ignored || bad ? 0.f : src.target(r, zt);
     }
+    const float zt = ignored || bad ? 0.f : o.zt;
     if (kind == kCeRecords) {
         uint32_t pf = nan ? kPartNanInf : 0u;
         if (ignored) pf |= kPartIgnored;
@@ -323,12 +298,69 @@ ce_join_kernel(const Src src, int K, const CeJoinArgs a) {
     a.loss[r] = ignored ? 0.f : (bad || broken) ? qnan() : (float)loss;
 }
 
+// kLanes lanes for a row, each for every kLanes-th piece in a fixed order, four at once; then one
+// lane for each of the CTA's rows takes the logarithm in 64 bits, a warp's worth of that narrow
+// pipe for up to 32 rows and not for one. 8 lanes where a row has up to 32 pieces, 32 lanes beyond.
+constexpr int kCeJoinThreads = 256, kCeJoinAhead = 4;
+template <class Src, CeJoin kind, int kLanes>
+__global__ void __launch_bounds__(kCeJoinThreads)
+ce_join_kernel(const Src src, int K, const CeJoinArgs a) {
+    constexpr int kRows = kCeJoinThreads / kLanes;
+    static_assert(kRows <= 32, "a lane for each row");
+    __shared__ CeRow rows[kRows];
+    pdl_enter<true>();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t r0 = (int64_t)blockIdx.x * kRows;
+    const int mine = threadIdx.x / kLanes, k0 = threadIdx.x % kLanes;
+    const int64_t row = r0 + mine < a.N ? r0 + mine : a.N - 1;   // a lane without a row of its own goes along
+    CeRow o{kNegBig, {0.f, 0.f}, {0.f, 0.f}, 0.f, 0u, 0, 0u};
+    for (int k = k0; k < K; k += kLanes * kCeJoinAhead) {
+        CePiece p[kCeJoinAhead];
+        float M = o.M;
+#pragma unroll
+        for (int i = 0; i < kCeJoinAhead; ++i)
+            if (k + i * kLanes < K) p[i] = src.piece(row, k + i * kLanes);
+#pragma unroll
+        for (int i = 0; i < kCeJoinAhead; ++i)
+            if (k + i * kLanes < K) M = fmaxf(M, p[i].m);
+        ce_recentre(o, M);
+#pragma unroll
+        for (int i = 0; i < kCeJoinAhead; ++i)
+            if (k + i * kLanes < K) ce_add(o, p[i]);
+    }
+    float M = o.M;
+#pragma unroll
+    for (int m = kLanes / 2; m > 0; m >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, m));
+    ce_recentre(o, M);
+#pragma unroll
+    for (int m = kLanes / 2; m > 0; m >>= 1) {
+        const int owners = __shfl_xor_sync(0xffffffffu, o.owners, m);
+        const float zt = __shfl_xor_sync(0xffffffffu, o.zt, m);
+        if (owners > o.owners) o.zt = zt;
+        o.owners += owners;
+        o.flags |= __shfl_xor_sync(0xffffffffu, o.flags, m);
+        o.n += __shfl_xor_sync(0xffffffffu, o.n, m);
+        df_add(o.S, shfl_xor(o.S, m));
+        df_add(o.W, shfl_xor(o.W, m));
+    }
+    if (k0 == 0) rows[mine] = o;
+    __syncthreads();
+    if (warp != 0 || lane >= kRows || r0 + lane >= a.N) return;
+    o = rows[lane];
+    if (kind != kCeGathered && a.targets[r0 + lane] >= 0) o.zt = src.target(r0 + lane, o.zt);
+    ce_finish<kind>(o, r0 + lane, a);
+}
+
+static CeJoinArgs ce_join_args(const CeArgs &a) {
+    return {a.N, a.V, a.vocab_start, a.targets, a.loss, static_cast<RowStat *>(a.stats), a.err,
+            static_cast<PartialRec *>(a.parts), a.opt.smooth, a.opt.zeta};
+}
+
 // A row's K pieces made its loss and record, or the shard's record (a.parts), or, of gathered
 // shards, the whole row's loss and record.
 template <class Src>
 static cudaError_t launch_ce_join(const Src &src, int K, const CeArgs &a) {
-    const CeJoinArgs j{a.N, a.V, a.vocab_start, a.targets, a.loss, static_cast<RowStat *>(a.stats), a.err,
-                       static_cast<PartialRec *>(a.parts), a.opt.smooth, a.opt.zeta};
+    const CeJoinArgs j = ce_join_args(a);
     auto go = [&](auto kernel, int lanes) {
         const int64_t rows = kCeJoinThreads / lanes;
         return launch_pdl(kernel, dim3((unsigned)((a.N + rows - 1) / rows)), dim3(kCeJoinThreads), 0, a.stream, src, K, j);

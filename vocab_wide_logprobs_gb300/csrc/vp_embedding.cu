@@ -5,7 +5,7 @@
 //
 // Forward: a warp for a piece of 32 x 4 vectors of 8 columns of one row, so that the four
 //   loads of a lane are on their way together. Bound: DRAM bytes.
-// Backward, three launches:
+// Backward of more than 128 tokens, three launches (up to there one: table_grad_few_kernel):
 //   1. token_sort_kernel: the tokens in the order of their ids (and of their positions
 //      among equal ids). Each CTA owns a range of ids and goes over all N ids twice, once to
 //      count and once to place its own: no CTA waits for another, no atomic decides an order.
@@ -19,6 +19,7 @@
 //   an id that takes half of a batch is spread over as many CTAs as it has windows.
 //   Bound: DRAM bytes of dy and dW.
 #include <algorithm>
+#include <atomic>
 
 #include "vp_device.cuh"
 #include "vp_launch.h"
@@ -264,6 +265,16 @@ __device__ __forceinline__ void zero_fill(T *p, int64_t n, int tid, int nt) {
     for (int64_t i = tid; i < vecs; i += nt) stg_stream(p + head + i * kPer, make_uint4(0, 0, 0, 0));
     if (tid < n - tail) Elem<T>::store1(p + tail + tid, 0.f);
 }
+// Zeros to the rows v0 .. v1 of a table that no token asks for, runs of them at once.
+template <typename T>
+__device__ __forceinline__ void fill_unasked(T *dW, int D, int64_t v0, int64_t v1, const bool *asked, int tid, int nt) {
+    for (int64_t v = v0; v < v1;) {
+        int64_t end = v;
+        while (end < v1 && !asked[end - v0]) ++end;
+        zero_fill(dW + v * D, (end - v) * D, tid, nt);
+        v = end + 1;
+    }
+}
 
 template <typename TI, typename TO, bool kVector, bool kAdd>
 __global__ void __launch_bounds__(kGradThreads)
@@ -282,12 +293,7 @@ table_grad_kernel(const TI *__restrict__ dy, const TableGrad a, TO *__restrict__
             const int64_t v0 = (b - n_sum) * fill_rows, v1 = min((int64_t)a.V, v0 + fill_rows);
             for (int64_t v = v0 + tid; v < v1; v += nt) s_asked[v - v0] = a.first[v + 1] != a.first[v];
             __syncthreads();
-            for (int64_t v = v0; v < v1;) {
-                int64_t end = v;                 // rows v .. end lie behind one another
-                while (end < v1 && !s_asked[end - v0]) ++end;
-                zero_fill(dW + v * a.D, (end - v) * a.D, tid, nt);
-                v = end + 1;
-            }
+            fill_unasked(dW, a.D, v0, v1, s_asked, tid, nt);
         }
         return;
     }
@@ -346,6 +352,80 @@ table_grad_kernel(const TI *__restrict__ dy, const TableGrad a, TO *__restrict__
             for (int e = 0; e < kEmbVec; ++e) sum[e] = 0.f;
         }
     }
+}
+
+// Few tokens: one launch. A CTA for each token and 8 columns of each of its threads: where no earlier token
+// has the same id, it sums the rows of all that have it, in order. More CTAs write zeros, as above.
+constexpr int kFewTokens = 128;
+template <typename TI, typename TO, bool kVector, bool kAdd>
+__global__ void __launch_bounds__(kGradThreads)
+table_grad_few_kernel(const TI *__restrict__ dy, const TableGrad a, const int64_t *__restrict__ ids, int64_t vocab_start,
+                      bool sharded, TO *__restrict__ dW, int32_t *__restrict__ err, int fill_rows) {
+    __shared__ int s_row[kFewTokens], s_list[kFewTokens];
+    __shared__ uint32_t s_same[kFewTokens / 32];
+    __shared__ bool s_asked[kFillMaxRows];
+    const int tid = threadIdx.x, nt = blockDim.x, N = (int)a.N;
+    pdl_enter<false>();
+    for (int i = tid; i < N; i += nt) {
+        const int64_t id = ids[i], local = id - vocab_start;
+        const bool here = id >= 0 && local >= 0 && local < a.V;
+        s_row[i] = here ? (int)local : -1;
+        if (id >= 0 && !here && !sharded && err && blockIdx.x == 0) atomicOr(err, VP_ERRBIT_TARGET_);
+    }
+    const int64_t b = blockIdx.x, n_sum = (int64_t)N * a.col_blocks;
+    if (b >= n_sum) {
+        if constexpr (!kAdd) {
+            const int64_t v0 = (b - n_sum) * fill_rows, v1 = min((int64_t)a.V, v0 + fill_rows);
+            for (int v = tid; v < (int)(v1 - v0); v += nt) s_asked[v] = false;
+            __syncthreads();
+            for (int i = tid; i < N; i += nt)
+                if (s_row[i] >= v0 && s_row[i] < v1) s_asked[s_row[i] - v0] = true;
+            __syncthreads();
+            fill_unasked(dW, a.D, v0, v1, s_asked, tid, nt);
+        }
+        return;
+    }
+    __syncthreads();
+    const int i = (int)(b / a.col_blocks), cb = (int)(b - (int64_t)i * a.col_blocks);
+    const int row = s_row[i];
+    if (row < 0) return;
+    // which tokens have this id, a bit each
+    for (int k = tid; k < (N + 31) / 32 * 32; k += nt) {         // by whole warps: nt is a multiple of 32
+        const uint32_t same = __ballot_sync(0xffffffffu, k < N && s_row[k] == row);
+        if (k % 32 == 0) s_same[k / 32] = same;
+    }
+    __syncthreads();
+    int before = 0, count = 0;
+    for (int w = 0; w < (N + 31) / 32; ++w) {
+        if (w < i / 32) before += __popc(s_same[w]);
+        count += __popc(s_same[w]);
+    }
+    if (before || s_same[i / 32] & ((1u << (i & 31)) - 1u)) return;   // an earlier token's CTA has it
+    for (int k = tid; k < N; k += nt)
+        if (s_row[k] == row) {
+            int at = __popc(s_same[k / 32] & ((1u << (k & 31)) - 1u));
+            for (int w = 0; w < k / 32; ++w) at += __popc(s_same[w]);
+            s_list[at] = k;
+        }
+    __syncthreads();
+    const int c = cb * nt * kEmbVec + (kVector ? tid * kEmbVec : tid), step = nt;
+    if (c >= a.D) return;
+    float sum[kEmbVec] = {}, old[kEmbVec];
+    TO *dst = dW + row * (int64_t)a.D;
+    if (kAdd) load_old<TO, kVector>(dst, c, step, a.D, old);
+    constexpr int kAhead = 4;
+    for (int k0 = 0; k0 < count; k0 += kAhead) {
+        float v[kAhead][kEmbVec];
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k)
+            if (k0 + k < count) load8<TI, kVector>(dy + a.dy_rows.off(s_list[k0 + k]), c, step, a.D, v[k]);
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k)
+            if (k0 + k < count)
+#pragma unroll
+                for (int e = 0; e < kEmbVec; ++e) sum[e] += v[k][e];
+    }
+    finish8<TO, kVector, kAdd>(dst, c, step, a.D, a.scale, sum, old);
 }
 
 // A CTA for each window and 512 columns, four each for a thread: where a run begins in the window and
@@ -454,6 +534,27 @@ template <typename TI, typename TO>
 cudaError_t embedding_bwd(const EmbeddingArgs &a) {
     const TI *dy = static_cast<const TI *>(a.x);
     TO *dW = static_cast<TO *>(a.out);
+    const bool vector = a.D % kEmbVec == 0 && (uintptr_t)dy % 16 == 0 && (uintptr_t)dW % 16 == 0 &&
+                        a.s_i * sizeof(TI) % 16 == 0 && a.s_o * sizeof(TI) % 16 == 0;
+    const int threads = (int)(a.D >= kGradThreads * kEmbVec ? kGradThreads : ((a.D + kEmbVec - 1) / kEmbVec + 31) / 32 * 32);
+    const int64_t row_bytes = a.D * (int64_t)sizeof(TO);
+    const int fill_rows = (int)std::clamp<int64_t>((int64_t)kFillBytes * threads / row_bytes, 1, kFillMaxRows);
+    const int64_t fill_ctas = a.accumulate ? 0 : (a.V + fill_rows - 1) / fill_rows;
+    TableGrad g{};
+    g.N = a.N;
+    g.V = (int)a.V;
+    g.D = (int)a.D;
+    g.col_blocks = (int)((a.D + threads * kEmbVec - 1) / (threads * kEmbVec));
+    g.dy_rows = Rows{a.R, a.s_o, a.s_i};
+    g.scale = a.scale;
+    if (a.N <= kFewTokens) {
+        auto few = [&](auto kernel) {
+            return launch_pdl(kernel, dim3((unsigned)(a.N * g.col_blocks + fill_ctas)), dim3(threads), 0, a.stream, dy, g,
+                              a.ids, a.vocab_start, a.sharded, dW, a.err, fill_rows);
+        };
+        return vector ? (a.accumulate ? few(table_grad_few_kernel<TI, TO, true, true>) : few(table_grad_few_kernel<TI, TO, true, false>))
+                      : (a.accumulate ? few(table_grad_few_kernel<TI, TO, false, true>) : few(table_grad_few_kernel<TI, TO, false, false>));
+    }
     const GradLayout L = grad_layout(a.N, a.V, a.D);
     uint8_t *ws = static_cast<uint8_t *>(a.workspace);
     int *first = reinterpret_cast<int *>(ws), *rows = reinterpret_cast<int *>(ws + L.rows),
@@ -463,33 +564,28 @@ cudaError_t embedding_bwd(const EmbeddingArgs &a) {
     int64_t bins = (a.V + sms - 1) / sms;
     bins = bins < 32 ? 32 : bins > kSortMaxBins ? kSortMaxBins : bins;
     const size_t smem = (size_t)kSortWarps * (bins + kStash) * 4;
-    cudaError_t e = cudaFuncSetAttribute(token_sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         kSortWarps * (kSortMaxBins + kStash) * 4);
-    if (e != cudaSuccess) return e;
+    // the counters' room, asked for once on each device
+    static std::atomic<uint64_t> attr_done{0};
+    int dev = 0;
+    cudaGetDevice(&dev);
+    cudaError_t e;
+    if (!(attr_done.load() & (1ull << (dev & 63)))) {
+        e = cudaFuncSetAttribute(token_sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 kSortWarps * (kSortMaxBins + kStash) * 4);
+        if (e != cudaSuccess) return e;
+        attr_done.fetch_or(1ull << (dev & 63));
+    }
     e = launch_pdl(token_sort_kernel, dim3((unsigned)((a.V + bins - 1) / bins)), dim3(kSortThreads), smem, a.stream,
                    a.ids, a.N, (int)a.V, a.vocab_start, a.sharded, (int)bins, first, rows, positions, a.err);
     if (e != cudaSuccess) return e;
 
-    const bool vector = a.D % kEmbVec == 0 && (uintptr_t)dy % 16 == 0 && (uintptr_t)dW % 16 == 0 &&
-                        a.s_i * sizeof(TI) % 16 == 0 && a.s_o * sizeof(TI) % 16 == 0;
-    const int threads = (int)(a.D >= kGradThreads * kEmbVec ? kGradThreads : ((a.D + kEmbVec - 1) / kEmbVec + 31) / 32 * 32);
-    TableGrad g;
-    g.N = a.N;
-    g.V = (int)a.V;
-    g.D = (int)a.D;
     g.window = grad_window(a.N);
     g.n_windows = (int)((a.N + g.window - 1) / g.window);
-    g.col_blocks = (int)((a.D + threads * kEmbVec - 1) / (threads * kEmbVec));
-    g.dy_rows = Rows{a.R, a.s_o, a.s_i};
-    g.scale = a.scale;
     g.first = first;
     g.rows = rows;
     g.positions = positions;
     g.until = reinterpret_cast<int *>(ws + L.until);
     g.partial = reinterpret_cast<float *>(ws + L.partial);
-    const int64_t row_bytes = a.D * (int64_t)sizeof(TO);
-    const int fill_rows = (int)std::clamp<int64_t>((int64_t)kFillBytes * threads / row_bytes, 1, kFillMaxRows);
-    const int64_t fill_ctas = a.accumulate ? 0 : (a.V + fill_rows - 1) / fill_rows;
     const int64_t ctas = (int64_t)g.n_windows * g.col_blocks + fill_ctas;
     if (ctas > 2147483647) return cudaErrorInvalidValue;
     auto go = [&](auto kernel) {
@@ -509,7 +605,9 @@ cudaError_t embedding_bwd(const EmbeddingArgs &a) {
 
 }  // namespace
 
-size_t embedding_bwd_workspace_bytes(int64_t N, int64_t V, int64_t D) { return grad_layout(N, V, D).total; }
+size_t embedding_bwd_workspace_bytes(int64_t N, int64_t V, int64_t D) {
+    return N <= kFewTokens ? 0 : grad_layout(N, V, D).total;
+}
 
 cudaError_t launch_embedding_fwd(const EmbeddingArgs &a) {
     if (a.x_bf16)

@@ -11,6 +11,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <type_traits>
 
 #include "vp_device.cuh"
 #include "vp_gemm_host.cuh"
@@ -257,6 +258,18 @@ static_assert(4 * kPairDualRegsLow + 8 * kPairDualRegsHigh == 12 * kPairDualRegs
 __host__ __device__ constexpr int pair_threads(bool dual) { return dual ? 12 * 32 : kLThreads; }
 __host__ __device__ constexpr int pair_epi_first_warp(bool dual) { return dual ? 4 : 2; }
 
+// Epilogues that declare kPdl belong to kernels that are launched with programmatic stream serialization
+// (vp_device.cuh): a kernel sets its barriers and tensor memory up while the stream's previous one
+// finishes, and lets the next one do so from its start, since every CTA of these grids is resident at once.
+template <class Epi, class = void>
+struct PdlOf {
+    static constexpr bool value = false;
+};
+template <class Epi>
+struct PdlOf<Epi, std::void_t<decltype(Epi::kPdl)>> {
+    static constexpr bool value = Epi::kPdl;
+};
+
 // What a tile's sum goes over. Whole: all of K (and, chained, all of the second product's K). Split: an output
 // tile's k-blocks are shared out over `splits` tiles, whose sums the epilogue keeps apart (it is told which),
 // so that few output tiles with a long K fill the GPU; and a chained second product takes only the k-blocks
@@ -325,6 +338,7 @@ umma_gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_con
     cluster_sync();                                      // barriers and TMEM ready in both CTAs
     tc_fence_after();
     const uint32_t tmem = bars.tmem_base;
+    if constexpr (PdlOf<Epi>::value) pdl_enter<true>();  // no global access before this
 
     if (warp < pair_epi_first_warp(kDual)) {
     // warpgroup 0 in the dual form (TMA, MMA and two idle warps)
@@ -702,6 +716,10 @@ static cudaError_t launch_gemm_pair_impl(const CUtensorMap &ta, const CUtensorMa
     if (group_m <= 0)   // about 32 MB of A (both products' A tiles in the dual form) per m-group
         group_m = (int)std::max<int64_t>(1, ((int64_t)32 << 20) / ((int64_t)2 * kLBM * (K + (kDual ? K2 : 0)) * 2));
     if (group_m > n_mp) group_m = n_mp;
+    if constexpr (PdlOf<Epi>::value)
+        return launch_pdl(umma_gemm_pair_kernel<Epi, kAMn, kBMn, kDual, kChain, Ks>, dim3(grid),
+                          dim3(pair_threads(kDual)), kPSmemBytes, stream, ta, tb, ta2, tb2, M, Nn, K, K2, group_m, l2hints,
+                          epi, ks);
     umma_gemm_pair_kernel<Epi, kAMn, kBMn, kDual, kChain, Ks><<<grid, pair_threads(kDual), kPSmemBytes, stream>>>(
         ta, tb, ta2, tb2, M, Nn, K, K2, group_m, l2hints, epi, ks);
     return cudaGetLastError();

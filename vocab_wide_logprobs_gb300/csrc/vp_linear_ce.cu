@@ -32,6 +32,7 @@ __device__ __forceinline__ void scale_all(float (&v)[32], float s) {
 
 template <bool kCap>
 struct CeEpi {
+    static constexpr bool kPdl = true;
     int N, n_t;
     float scale;        // cut_off(D)
     int64_t vocab_start;
@@ -112,6 +113,7 @@ constexpr int kFlagRows = 32, kFlagCols = 64;
 // lo_off != 0, what that rounding took away as a second one).
 template <bool kCap>
 struct DzCeEpi {
+    static constexpr bool kPdl = true;
     int N, V, v0, ldz;
     float scale;        // cut_off(D)
     int64_t vocab_start;
@@ -242,6 +244,7 @@ __global__ void __launch_bounds__(256)
 pair_list_kernel(const uint8_t *__restrict__ flags, int row_groups, int pitch, int col_groups, int n_rows, int *__restrict__ count,
                  int *__restrict__ list, int pitch_rows, int pitch_cols) {
     __shared__ uint32_t s_n[8];
+    pdl_enter<true>();   // no global access before this
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const bool by_rows = (int)blockIdx.x < n_rows;
     const int b = by_rows ? blockIdx.x : blockIdx.x - n_rows;
@@ -279,6 +282,7 @@ pair_list_kernel(const uint8_t *__restrict__ flags, int row_groups, int pitch, i
 
 // dhidden's tiles: the sum over a share of the k-blocks, kept apart for each share.
 struct SplitAccEpi {
+    static constexpr bool kPdl = true;
     int M, ld;
     bool first;
     float *acc;          // [splits][M][ld]
@@ -288,6 +292,7 @@ struct SplitAccEpi {
 };
 // dW's tiles, rounded; ld is a multiple of 64.
 struct StoreRowsEpi {
+    static constexpr bool kPdl = true;
     int M, ld;
     int64_t row0;
     __nv_bfloat16 *out;
@@ -313,6 +318,7 @@ struct StoreRowsEpi {
 // The shares' sums, added in order and rounded once.
 __global__ void __launch_bounds__(256)
 split_sum_kernel(const float *__restrict__ acc, int64_t n, int splits, __nv_bfloat16 *__restrict__ out) {
+    pdl_enter<true>();   // no global access before this
     const int64_t i = 8 * ((int64_t)blockIdx.x * 256 + threadIdx.x);   // n is a multiple of 64
     if (i >= n) return;
     float v[8] = {};
@@ -409,9 +415,9 @@ cudaError_t launch_linear_ce_bwd(const CeArgs &a) {
         if (e != cudaSuccess) return e;
         if (mixed) {
             const int cols = (nv + 63) / 64, tiles = (nv + 255) / 256;
-            pair_list_kernel<<<L.n_rows + tiles, 256, 0, a.stream>>>(flags, L.row_groups, L.col_groups, cols, L.n_rows, count,
-                                                                     list, L.pitch_rows, L.pitch_cols);
-            if ((e = cudaGetLastError()) != cudaSuccess) return e;
+            e = launch_pdl(pair_list_kernel, dim3(L.n_rows + tiles), dim3(256), 0, a.stream, flags, L.row_groups, L.col_groups,
+                           cols, L.n_rows, count, list, L.pitch_rows, L.pitch_cols);
+            if (e != cudaSuccess) return e;
         }
         auto product = [&](auto kinds, const CUtensorMap &ta, const CUtensorMap &tb, const CUtensorMap &ta2, int M, int Nn,
                            int K, const auto &epi, int group, const SplitK &ks) {
@@ -443,9 +449,8 @@ cudaError_t launch_linear_ce_bwd(const CeArgs &a) {
     }
     if (a.dhidden) {
         const int64_t n = a.N * a.D;
-        split_sum_kernel<<<(unsigned)((n / 8 + 255) / 256), 256, 0, a.stream>>>(acc, n, L.splits,
-                                                                               static_cast<__nv_bfloat16 *>(a.dhidden));
-        return cudaGetLastError();
+        return launch_pdl(split_sum_kernel, dim3((unsigned)((n / 8 + 255) / 256)), dim3(256), 0, a.stream, acc, n, L.splits,
+                          static_cast<__nv_bfloat16 *>(a.dhidden));
     }
     return cudaSuccess;
 }
