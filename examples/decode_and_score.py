@@ -1,9 +1,10 @@
-"""Decode with a 4-bit head and rules on the logits, then score the rollout under the same rules.
+"""Decode with a 4-bit head and rules on the logits, score the rollout under the same rules, then learn from it.
 
 A stand-in model (the hidden state of a token is its embedding) drives the calls as a rollout worker and a
 trainer make them:
 
   decode, one token for each sequence a step
+      vp_embedding_fwd        the tokens' rows of the embedding
       vp_mxfp4_quantize       the hidden states
       vp_linear_mxfp4_fwd     times the head, kept in MXFP4: logits
       vp_logits_process_fwd   penalties for repeated tokens, biases, a grammar mask, a temperature (in place)
@@ -11,6 +12,10 @@ trainer make them:
   score, all tokens of all sequences at once
       vp_mxfp4_quantize, vp_linear_mxfp4_fwd    the same logits, row (b, t) of sequence b's prefix
       vp_processed_logprobs_fwd / _bwd          logprobs of the drawn tokens and the gradient of their sum
+  learn, all tokens at once, with the embedding as the head (a tied model)
+      vp_embedding_fwd                          hidden states
+      vp_linear_cross_entropy_fwd / _bwd        the loss and its gradients, the logits never stored
+      vp_embedding_bwd                          the lookup's gradient, added to the head's
 
     python examples/decode_and_score.py
 """
@@ -31,6 +36,17 @@ def grammar(V, words, device, generator):
     allowed[1, :V] = torch.rand(V, generator=generator, device=device) < 0.8
     bits = (allowed.view(2, words, 32).long() << torch.arange(32, device=device)).sum(-1)
     return torch.where(bits >= 1 << 31, bits - (1 << 32), bits).to(torch.int32)
+
+
+def learn(table, ids, targets, scale, label_smoothing=0.1, z_loss=1e-4, softcap=30.0):
+    """The mean loss of a tied model, scale * table[ids] . table^T, that is to predict the targets, and the gradient of its table."""
+    rules = dict(label_smoothing=label_smoothing, z_loss=z_loss, softcap=softcap)
+    hidden = vp.vp_embedding_fwd(table, ids, scale=scale)
+    loss, stats = vp.vp_linear_cross_entropy_fwd(hidden, table, targets, **rules)
+    grad = torch.full_like(loss, 1 / loss.numel())
+    dhidden, dtable = vp.vp_linear_cross_entropy_bwd(hidden, table, targets, stats, grad, **rules)
+    vp.vp_embedding_bwd(dhidden, ids, table.shape[0], scale=scale, dW=dtable, accumulate=True)
+    return loss.mean(), dtable
 
 
 def run(B=4, prompt=24, steps=16, V=5003, D=512, device="cuda", seed=0):
@@ -57,7 +73,8 @@ def run(B=4, prompt=24, steps=16, V=5003, D=512, device="cuda", seed=0):
                                **{k: v[sequence] for k, v in per_sequence.items()})
 
     def logits(tokens):
-        return vp.vp_linear_mxfp4_fwd(*vp.vp_mxfp4_quantize(embedding[tokens]), *head, dtype=torch.float32)
+        hidden = vp.vp_embedding_fwd(embedding, tokens.contiguous())
+        return vp.vp_linear_mxfp4_fwd(*vp.vp_mxfp4_quantize(hidden), *head, dtype=torch.float32)
 
     drawn_logp = torch.empty(B, steps, dtype=torch.float64, device=device)
     for t in range(steps):
@@ -75,11 +92,15 @@ def run(B=4, prompt=24, steps=16, V=5003, D=512, device="cuda", seed=0):
     q, targets = rules(sequence, step), ids[sequence, prompt + step].contiguous()
     logp, stats = vp.vp_processed_logprobs_fwd(x, q, targets, err_word=err)
     dx = vp.vp_processed_logprobs_bwd(x, q, targets, stats, torch.ones_like(logp), err_word=err)
-    return dict(ids=ids, drawn_logp=drawn_logp.view(-1), logp=logp, dx=dx, err=int(err), fault=vp.vp_fault_status())
+    seen = ids[sequence, prompt + step - 1].contiguous()
+    loss, dtable = learn(embedding, seen, targets, D ** -0.5)
+    return dict(ids=ids, drawn_logp=drawn_logp.view(-1), logp=logp, dx=dx, err=int(err), fault=vp.vp_fault_status(),
+                table=embedding, seen=seen, targets=targets, loss=loss, dtable=dtable)
 
 
 if __name__ == "__main__":
     out = run()
     print(f"drew {out['logp'].numel()} tokens: mean logprob {out['logp'].mean():.4f}, "
           f"largest difference to the logprobs at decode {(out['logp'] - out['drawn_logp']).abs().max():.1e}, "
-          f"gradient rms {out['dx'].float().square().mean().sqrt():.3e}")
+          f"gradient rms {out['dx'].float().square().mean().sqrt():.3e}; "
+          f"loss of the tied model {out['loss']:.4f}, its table's gradient rms {out['dtable'].float().square().mean().sqrt():.3e}")

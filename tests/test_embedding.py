@@ -285,6 +285,24 @@ def test_a_tied_model_learns_from_both_ends():
     assert all(torch.equal(a, b) for a, b in zip(out, tied_step(wg, ig, tg, scale, gg, **rules)))
 
 
+@pytest.mark.gpu
+def test_the_example_learns():
+    """The example's rollout, learnt from: its loss and its table's gradient against the definition in 64 bits."""
+    from examples import decode_and_score
+    out = decode_and_score.run(B=3, prompt=9, steps=8, V=1003, D=128)
+    w64 = out["table"].double().cpu().requires_grad_()
+    seen, targets = out["seen"].cpu(), out["targets"].cpu()
+    z = 30 * torch.tanh((w64[seen] * 128 ** -0.5) @ w64.t() / 30)
+    lse = torch.logsumexp(z, 1)
+    loss = (lse - 0.9 * z.gather(1, targets[:, None])[:, 0] - 0.1 * z.mean(1) + 1e-4 * lse ** 2).mean()
+    loss.backward()
+    loss = float(loss.detach())
+    assert abs(float(out["loss"]) - loss) < 2e-5 * loss and out["fault"] == 0
+    # three roundings to bf16 (dhidden, the head's part, the sum), each half a step of magnitudes that may cancel
+    lim = 3 * 2.0 ** -8 * (w64.grad.abs() + w64.grad.abs().amax(1, keepdim=True) / 4)
+    assert ((out["dtable"].double().cpu() - w64.grad).abs() - lim - 2e-7).max() <= 0
+
+
 # --------------------------------------------------------------------------- refusals (no GPU needed)
 FAKE, ODD = ctypes.c_void_p(0x100000), ctypes.c_void_p(0x100001)
 BIG = ctypes.c_size_t(1 << 40)

@@ -1138,18 +1138,21 @@ def vp_embedding_fwd(weight, ids, scale: float = 1.0, vocab_start: int = 0, shar
     stride; ids int64, contiguous: negative ones are padding (zero rows); with sharded, those of other shards too."""
     if weight.dim() != 2:
         raise VPError(2, f"weight must be [V, D], got {tuple(weight.shape)}")
-    V, D, _, _, stride = rows_of(weight)
-    dtype = weight.dtype if dtype is None else dtype
+    (V, D), (stride, unit), device = weight.shape, weight.stride(), weight.device
+    if D > 1 and unit != 1:
+        raise VPError(4, "weight needs a unit stride along D")
+    N, code, dtype = ids.numel(), _dtype_code(weight), weight.dtype if dtype is None else dtype
     if dtype not in _DTYPES:
         raise VPError(3, f"dtype {dtype}")
-    N, code = ids.numel(), _dtype_code(weight)
     _arg(ids, N, torch.int64, weight, "ids")
-    _arg(out, N * D, dtype, weight, "out")
     _arg(err_word, 1, torch.int32, weight, "err_word")
+    if out is not None:
+        _arg(out, N * D, dtype, weight, "out")
     _on_gpu(weight)
-    out = torch.empty((*ids.shape, D), dtype=dtype, device=weight.device) if out is None else out
-    _check(_handle().vp_embedding_fwd(_addr(weight), code, V, D, stride, _addr(ids), N, vocab_start, int(sharded), scale,
-                                      _addr(out), _DTYPES[dtype], _addr(err_word), _queue(weight.device)),
+    if out is None:
+        out = torch.empty((*ids.shape, D), dtype=dtype, device=device)
+    _check(_handle().vp_embedding_fwd(weight.data_ptr(), code, V, D, stride, ids.data_ptr(), N, vocab_start, int(sharded),
+                                      scale, out.data_ptr(), _DTYPES[dtype], _addr(err_word), _queue(device)),
            "vp_embedding_fwd")
     return out
 

@@ -300,17 +300,22 @@ struct StoreRowsEpi {
         __shared__ uint4 stage[kLThreads / 32 - 2][kStageVecs];
         uint4 *mine = stage[(threadIdx.x >> 5) & 3];
         const int first = row - (threadIdx.x & 31);
-#pragma unroll 1
-        for (int c = 0; c < ncol; c += 64) {
+        // a chunk's columns come out of TMEM while the one before is stored
+        uint32_t f[2][32];
+        tmem_ld32_issue(taddr, f[0]);
+        tmem_ld32_issue(taddr + 32, f[1]);
+        tmem_wait_ld();
+#pragma unroll
+        for (int c = 0; c < kLBN; c += 64) {
             uint4 v[8];
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                float f[32];
-                tmem_ld32(taddr + c + half * 32, f);
-#pragma unroll
-                for (int k = 0; k < 4; ++k) v[half * 4 + k] = Elem<__nv_bfloat16>::pack(f + 8 * k);
+            for (int k = 0; k < 8; ++k) v[k] = Elem<__nv_bfloat16>::pack(reinterpret_cast<const float *>(f[k / 4]) + 8 * (k % 4));
+            if (c + 64 < kLBN) {
+                tmem_ld32_issue(taddr + c + 64, f[0]);
+                tmem_ld32_issue(taddr + c + 96, f[1]);
             }
-            store_rows64(mine, v, out + (row0 + first) * (int64_t)ld + col0 + c, ld, first, M);
+            if (c < ncol) store_rows64(mine, v, out + (row0 + first) * (int64_t)ld + col0 + c, ld, first, M);
+            if (c + 64 < kLBN) tmem_wait_ld();
         }
     }
 };
