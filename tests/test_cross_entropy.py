@@ -172,6 +172,14 @@ def test_logits_where_rows_begin(dtype):
         view = room[offset:].view(12, 8231 + gap)[:, :8231]
         view.copy_(x)
         check_logits(x, targets, g, dict(smooth=0.1), xg=view)
+    for V in (9, 17, 33, 8192 + 15):                                 # rows of a few vectors, and of a slice and some
+        x2, t2, g2 = rows(9, V, dtype, V)
+        for offset, gap in ((0, 1), (5, 2), (2, 3), (7, 8)):
+            room = torch.full((offset + 9 * (V + gap),), math.nan, dtype=dtype, device="cuda")
+            view = room[offset:].view(9, V + gap)[:, :V]
+            view.copy_(x2)
+            check_logits(x2, t2, g2, dict(cap=9.0, zeta=1e-3), xg=view)
+            check_logits(x2, t2, g2, dict(smooth=0.2), xg=view)
     full = torch.full((3, 5, 8231), math.nan, dtype=dtype, device="cuda")
     full[:, :-1] = x.view(3, 4, 8231).cuda()
     _, stats, dx = check_logits(x, targets, g, dict(cap=20.0), xg=full[:, :-1])
@@ -281,6 +289,18 @@ def test_a_row_does_not_depend_on_the_batch(N, V, dtype):
         one, st = vp.vp_cross_entropy_fwd(x[k], targets[k], **o)
         assert torch.equal(one, loss[k]) and torch.equal(st, stats[k])
         assert torch.equal(vp.vp_cross_entropy_bwd(x[k], targets[k], st, g[k], **o), dx[k])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("V", [1000, 9000])
+def test_a_linear_row_does_not_depend_on_the_batch(V):
+    """Its loss and record: few rows and many, of pieces for eight lanes and for all of a CTA."""
+    h, w, targets, _ = (t.cuda() for t in model(1500, V, 64, 18))
+    o = dict(label_smoothing=0.1, z_loss=1e-3, softcap=25.0)
+    loss, stats = vp.vp_linear_cross_entropy_fwd(h, w, targets, **o)
+    for k in (slice(0, 1), slice(3, 4), slice(700, 900), slice(1499, 1500), slice(100, 1400)):
+        one, st = vp.vp_linear_cross_entropy_fwd(h[k], w, targets[k], **o)
+        assert torch.equal(one, loss[k]) and torch.equal(st, stats[k])
 
 
 @pytest.mark.gpu

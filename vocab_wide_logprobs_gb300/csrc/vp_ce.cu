@@ -43,6 +43,21 @@ __device__ __forceinline__ int64_t row_offset(const Rows &rows, int64_t r) {
     return r < rows.R ? r * rows.s_i : rows.off(r);
 }
 
+// Bytes b .. b + 15 of two vectors behind one another, b a multiple of 2.
+__device__ __forceinline__ uint4 shifted(const uint4 &x, const uint4 &y, uint32_t b) {
+    uint32_t w[5];                                       // from word b / 4 on
+    switch (b >> 2) {                                    // the same for a whole row
+        case 0: w[0] = x.x; w[1] = x.y; w[2] = x.z; w[3] = x.w; w[4] = y.x; break;
+        case 1: w[0] = x.y; w[1] = x.z; w[2] = x.w; w[3] = y.x; w[4] = y.y; break;
+        case 2: w[0] = x.z; w[1] = x.w; w[2] = y.x; w[3] = y.y; w[4] = y.z; break;
+        default: w[0] = x.w; w[1] = y.x; w[2] = y.y; w[3] = y.z; w[4] = y.w; break;
+    }
+    if (b & 2)
+        return make_uint4(__funnelshift_r(w[0], w[1], 16), __funnelshift_r(w[1], w[2], 16), __funnelshift_r(w[2], w[3], 16),
+                          __funnelshift_r(w[3], w[4], 16));
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
 // The largest of the values of a vector (NaN left out, as fmaxf does).
 template <typename T>
 __device__ __forceinline__ float vec_max(const uint4 &u, float m) {
@@ -56,11 +71,12 @@ __device__ __forceinline__ float vec_max(const uint4 &u, float m) {
     }
 }
 
-// kSum: with the sum of the centred logits, which only label smoothing asks for
-template <typename T, bool kCap, bool kSum>
+// kSum: with the sum of the centred logits, which only label smoothing asks for. kWhole: rows of one slice, finished
+// here (a kernel of its own: the 64-bit logarithm would take registers from the sums).
+template <typename T, bool kCap, bool kSum, bool kWhole>
 __global__ void __launch_bounds__(kCeThreads, 4)
 ce_fwd_kernel(const T *__restrict__ x, int V, Rows rows, const CeRules q, const int64_t *__restrict__ targets,
-              int64_t vocab_start, int n_slices, int64_t total, CeSlice *__restrict__ slices, bool whole,
+              int64_t vocab_start, int n_slices, int64_t total, CeSlice *__restrict__ slices,
               const CeJoinArgs join) {
     constexpr int kVec = Elem<T>::kVec, kWarps = kCeThreads / 32, kCeVecs = kCeFwdVecs, kCeSliceVecs = kCeThreads * kCeVecs;
     __shared__ float s_max[kWarps];
@@ -168,7 +184,7 @@ ce_fwd_kernel(const T *__restrict__ x, int V, Rows rows, const CeRules q, const 
                           (has_target ? kPartHasTarget : 0u) | (minus_inf ? kCeMinusInf : 0u),
                           (uint32_t)(max(v1 - v0, 0) * kVec + extra)};
                 if (!(S_all < INFINITY)) o.S = qnan(), o.S_lo = 0.f;     // a NaN, or +inf without a cap
-                if (whole) {
+                if constexpr (kWhole) {
                     CeRow c{m, {0.f, 0.f}, {0.f, 0.f}, 0.f, 0u, 0, 0u};
                     ce_add(c, {o.m, {o.S, o.S_lo}, {o.W, o.W_lo}, o.zt, o.flags, o.n});
                     if (join.parts) ce_finish<kCeRecords>(c, r, join);
@@ -183,8 +199,22 @@ ce_fwd_kernel(const T *__restrict__ x, int V, Rows rows, const CeRules q, const 
     }
 }
 
-template <typename T, bool kCap>
-__global__ void __launch_bounds__(kCeThreads, kCap ? 4 : 1)
+// dx may be x, so the gradient's loads are ordinary ones, not those of read-only memory. A thread reads an element
+// before it writes it, and no other thread reads it.
+__device__ __forceinline__ uint4 load_own(const void *p) {
+    uint4 r;
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+                 : "l"(p)
+                 : "memory");
+    return r;
+}
+__device__ __forceinline__ float load_own1(const float *p) { return *p; }
+__device__ __forceinline__ float load_own1(const __nv_bfloat16 *p) { return __bfloat162float(*p); }
+
+// kSame: every row of the input lies as its row of the output modulo 16 bytes
+template <typename T, bool kCap, bool kSame>
+__global__ void __launch_bounds__(kCeThreads, kCap ? 4 : 5)
 ce_grad_kernel(const T *x, int V, Rows rows, const CeRules q, const RowStat *__restrict__ stats,
                const float *__restrict__ g_in, const int64_t *__restrict__ targets, int64_t vocab_start, T *dx,
                int32_t *__restrict__ err, int n_slices, int64_t total) {
@@ -198,12 +228,13 @@ ce_grad_kernel(const T *x, int V, Rows rows, const CeRules q, const RowStat *__r
         T *out = dx + r * (int64_t)V;
         const int hin = head_count(in, V), hout = head_count(out, V);
         const int v0 = s * kCeSliceVecs;
-        const int v1 = hin == hout ? min((V - hin) / kVec, v0 + kCeSliceVecs) : 0;
+        const bool same = kSame || hin == hout;
+        const int v1 = same ? min((V - hin) / kVec, v0 + kCeSliceVecs) : 0;
         uint4 u[kCeVecs];
 #pragma unroll
         for (int k = 0; k < kCeVecs; ++k) {
             const int i = v0 + tid + k * kCeThreads;
-            if (i < v1) u[k] = ldg_stream(reinterpret_cast<const uint4 *>(in + hin) + i);
+            if (i < v1) u[k] = load_own(reinterpret_cast<const uint4 *>(in + hin) + i);
         }
         const RowStat st = load_rowstat(stats + r);
         int mode = (st.flags & (kRowNanInf | kRowEmpty | kRowBadTarget)) ? 2 : 0;   // 1 zeros, 2 NaN
@@ -221,46 +252,66 @@ ce_grad_kernel(const T *x, int V, Rows rows, const CeRules q, const RowStat *__r
         const float constant = mode == 1 ? 0.f : qnan();
 
         auto one = [&](int j) {
-            float z = Elem<T>::load1(in + j), slope = 1.f;
+            float z = load_own1(in + j), slope = 1.f;
             if (kCap) z = soft_cap1(q, z, &slope);
             float d = j == loc ? ce_grad_target(q, row, z) : ce_grad2(row, make_float2(z, 0.f)).x;
             if (kCap) d *= slope;
             Elem<T>::store1(out + j, mode ? constant : d);
         };
-        if (hin == hout) {
+        // the gradients of a vector of columns from j0 on
+        auto vector = [&](const uint4 &raw, int j0) {
+            float z[kVec], slope[kVec], d[kVec];
+            Elem<T>::unpack(raw, z);
+            if (kCap) soft_cap<kVec, true>(q, z, slope);
+#pragma unroll
+            for (int e = 0; e < kVec; e += 2) {
+                float2 v = ce_grad2(row, make_float2(z[e], z[e + 1]));
+                if (kCap) v = __fmul2_rn(v, make_float2(slope[e], slope[e + 1]));
+                d[e] = v.x;
+                d[e + 1] = v.y;
+            }
+            const uint32_t at = (uint32_t)(loc - j0);          // the target's place in this vector
+            if (at < (uint32_t)kVec) {
+#pragma unroll
+                for (int e = 0; e < kVec; ++e)
+                    if (e == (int)at) d[e] = ce_grad_target(q, row, z[e]) * (kCap ? slope[e] : 1.f);
+            }
+            if (mode) {
+#pragma unroll
+                for (int e = 0; e < kVec; ++e) d[e] = constant;
+            }
+            return Elem<T>::pack(d);
+        };
+        if (same) {
             const int tail0 = hin + (V - hin) / kVec * kVec;
             if (s == 0 && tid < hin + V - tail0) one(tid < hin ? tid : tail0 + tid - hin);
             uint4 *vout = reinterpret_cast<uint4 *>(out + hin);
 #pragma unroll
             for (int k = 0; k < kCeVecs; ++k) {
                 const int i = v0 + tid + k * kCeThreads;
-                if (i < v1) {
-                    float z[kVec], slope[kVec], d[kVec];
-                    Elem<T>::unpack(u[k], z);
-                    if (kCap) soft_cap<kVec, true>(q, z, slope);
-#pragma unroll
-                    for (int e = 0; e < kVec; e += 2) {
-                        float2 v = ce_grad2(row, make_float2(z[e], z[e + 1]));
-                        if (kCap) v = __fmul2_rn(v, make_float2(slope[e], slope[e + 1]));
-                        d[e] = v.x;
-                        d[e + 1] = v.y;
-                    }
-                    const uint32_t at = (uint32_t)(loc - hin - i * kVec);      // the target's place in this vector
-                    if (at < (uint32_t)kVec) {
-#pragma unroll
-                        for (int e = 0; e < kVec; ++e)
-                            if (e == (int)at) d[e] = ce_grad_target(q, row, z[e]) * (kCap ? slope[e] : 1.f);
-                    }
-                    if (mode) {
-#pragma unroll
-                        for (int e = 0; e < kVec; ++e) d[e] = constant;
-                    }
-                    stg_stream(vout + i, Elem<T>::pack(d));
+                if (i < v1) stg_stream(vout + i, vector(u[k], hin + i * kVec));
+            }
+        } else if constexpr (!kSame) {
+            // Input and output rows lie differently modulo 16 bytes (an odd vocabulary out of padded rows): whole
+            // vectors of the output, each out of the two of the input that its columns lie in. The first and last ones,
+            // whose two would reach out of the row, go column by column, as do the ends.
+            const int nv = (V - hout) / kVec, o1 = min(nv, v0 + kCeSliceVecs);
+            const uint32_t b = (uint32_t)((uintptr_t)(in + hout) & 15u);
+            const uint4 *base = reinterpret_cast<const uint4 *>(reinterpret_cast<const uint8_t *>(in + hout) - b);
+            const uint4 *first = reinterpret_cast<const uint4 *>(in), *last = reinterpret_cast<const uint4 *>(in + V);
+            const int tail0 = hout + nv * kVec;
+            if (s == 0 && tid < hout + V - tail0) one(tid < hout ? tid : tail0 + tid - hout);
+            uint4 *vout = reinterpret_cast<uint4 *>(out + hout);
+#pragma unroll 2
+            for (int k = 0; k < kCeVecs; ++k) {
+                const int i = v0 + tid + k * kCeThreads;
+                if (i >= o1) break;
+                if (base + i < first || base + i + 2 > last) {
+                    for (int e = 0; e < kVec; ++e) one(hout + i * kVec + e);
+                } else {
+                    vout[i] = vector(shifted(__ldg(base + i), __ldg(base + i + 1), b), hout + i * kVec);
                 }
             }
-        } else {   // input and output rows lie differently modulo 16 bytes
-            const int64_t e0 = (int64_t)s * kCeSliceVecs * kVec, e1 = min((int64_t)V, e0 + (int64_t)kCeSliceVecs * kVec);
-            for (int64_t j = e0 + tid; j < e1; j += kCeThreads) one((int)j);
         }
     }
 }
@@ -278,12 +329,17 @@ static cudaError_t ce_fwd(const CeArgs &a) {
     const bool whole = n_slices == 1 && a.N <= kCeFewRows;
     auto go = [&](auto kernel) {
         return launch_pdl(kernel, dim3(ce_grid(total)), dim3(kCeThreads), 0, a.stream, static_cast<const T *>(a.x),
-                          (int)a.V, Rows{a.R, a.s_o, a.s_i}, q, a.targets, a.vocab_start, n_slices, total, work, whole,
+                          (int)a.V, Rows{a.R, a.s_o, a.s_i}, q, a.targets, a.vocab_start, n_slices, total, work,
                           ce_join_args(a));
     };
     const bool sum = a.parts || q.smooth > 0.f;      // a shard's records are merged with any smoothing
-    const cudaError_t e = q.cap > 0.f ? (sum ? go(ce_fwd_kernel<T, true, true>) : go(ce_fwd_kernel<T, true, false>))
-                                      : (sum ? go(ce_fwd_kernel<T, false, true>) : go(ce_fwd_kernel<T, false, false>));
+    auto pick = [&](auto cap, auto summed) {
+        constexpr bool kCap = decltype(cap)::value, kSum = decltype(summed)::value;
+        return whole ? go(ce_fwd_kernel<T, kCap, kSum, true>) : go(ce_fwd_kernel<T, kCap, kSum, false>);
+    };
+    const std::true_type yes;
+    const std::false_type no;
+    const cudaError_t e = q.cap > 0.f ? (sum ? pick(yes, yes) : pick(yes, no)) : (sum ? pick(no, yes) : pick(no, no));
     return e != cudaSuccess || whole ? e : launch_ce_join(CeSlices{work, n_slices}, n_slices, a);
 }
 
@@ -306,8 +362,15 @@ cudaError_t launch_ce_bwd(const CeArgs &a) {
     const __nv_bfloat16 *xb = static_cast<const __nv_bfloat16 *>(a.x);
     float *df = static_cast<float *>(a.dx);
     __nv_bfloat16 *db = static_cast<__nv_bfloat16 *>(a.dx);
-    return a.bf16 ? (q.cap > 0.f ? go(ce_grad_kernel<__nv_bfloat16, true>, xb, db) : go(ce_grad_kernel<__nv_bfloat16, false>, xb, db))
-                  : (q.cap > 0.f ? go(ce_grad_kernel<float, true>, xf, df) : go(ce_grad_kernel<float, false>, xf, df));
+    const int64_t es = a.bf16 ? 2 : 4;
+    const bool same = ((uintptr_t)a.x - (uintptr_t)a.dx) % 16 == 0 && (a.s_i - a.V) * es % 16 == 0 &&
+                      (a.R >= a.N || (a.s_o - a.R * a.V) * es % 16 == 0);
+    auto pick = [&](auto tag, auto *x, auto *dx) {
+        using T = std::remove_reference_t<decltype(tag)>;
+        return q.cap > 0.f ? (same ? go(ce_grad_kernel<T, true, true>, x, dx) : go(ce_grad_kernel<T, true, false>, x, dx))
+                           : (same ? go(ce_grad_kernel<T, false, true>, x, dx) : go(ce_grad_kernel<T, false, false>, x, dx));
+    };
+    return a.bf16 ? pick(__nv_bfloat16(), xb, db) : pick(float(), xf, df);
 }
 
 }  // namespace vp

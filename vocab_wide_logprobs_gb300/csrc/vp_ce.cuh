@@ -219,8 +219,9 @@ struct CeShards {
     }
 };
 
-// What one GEMM tile of 256 columns left of a row: (m, S, sum of z, -), and the target's logit
+// What a GEMM's epilogue left of 128 columns of a row: (m, S, sum of z, -), and the target's logit
 // in an array of its own.
+constexpr int kCeTileCols = 128;
 struct CeTiles {
     const float4 *tiles;        // [N][n_t]
     const float *zt;            // [N]
@@ -228,7 +229,7 @@ struct CeTiles {
     __device__ __forceinline__ float target(int64_t r, float) const { return zt[r]; }
     __device__ __forceinline__ CePiece piece(int64_t r, int k) const {
         const float4 p = tiles[r * n_t + k];
-        const int n = min(256, V - 256 * k);
+        const int n = min(kCeTileCols, V - kCeTileCols * k);
         const float w = p.z * kCeScale;
         const bool minus_inf = w == -INFINITY;
         DF W{minus_inf ? 0.f : w, 0.f};
@@ -298,55 +299,74 @@ __device__ __forceinline__ void ce_finish(const CeRow &o, int64_t r, const CeJoi
     a.loss[r] = ignored ? 0.f : (bad || broken) ? qnan() : (float)loss;
 }
 
-// kLanes lanes for a row, each for every kLanes-th piece in a fixed order, four at once; then one
-// lane for each of the CTA's rows takes the logarithm in 64 bits, a warp's worth of that narrow
-// pipe for up to 32 rows and not for one. 8 lanes where a row has up to 32 pieces, 32 lanes beyond.
-constexpr int kCeJoinThreads = 256, kCeJoinAhead = 4;
+// kLanes lanes for a row, each for every kLanes-th piece in a fixed order, four at once: 8 lanes where a row has
+// up to 32 pieces, beyond that the CTA's 256, for `per` rows one after the other. Then one lane for each of
+// the CTA's rows takes the logarithm in 64 bits, a warp's worth of that narrow pipe for all of them and not
+// for one. Lanes and order follow from the number of pieces alone; how many rows a CTA has does not change
+// a row's result: one where there are few rows (16 rows of 594 pieces: 19 us with a warp for a row, 8 us so),
+// eight where there are many.
+constexpr int kCeJoinThreads = 256, kCeJoinAhead = 4, kCeJoinMany = 8;
 template <class Src, CeJoin kind, int kLanes>
 __global__ void __launch_bounds__(kCeJoinThreads)
-ce_join_kernel(const Src src, int K, const CeJoinArgs a) {
-    constexpr int kRows = kCeJoinThreads / kLanes;
-    static_assert(kRows <= 32, "a lane for each row");
-    __shared__ CeRow rows[kRows];
+ce_join_kernel(const Src src, int K, int per, const CeJoinArgs a) {
+    static_assert(kLanes == 8 || kLanes == kCeJoinThreads, "within a warp, or the whole CTA");
+    constexpr int kWarpLanes = kLanes < 32 ? kLanes : 32, kParts = kLanes / kWarpLanes;   // warps of a row
+    constexpr int kSide = kCeJoinThreads / kLanes;                                        // rows side by side
+    __shared__ CeRow rows[kLanes == 8 ? kSide : kCeJoinMany * kParts];
     pdl_enter<true>();
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int64_t r0 = (int64_t)blockIdx.x * kRows;
-    const int mine = threadIdx.x / kLanes, k0 = threadIdx.x % kLanes;
-    const int64_t row = r0 + mine < a.N ? r0 + mine : a.N - 1;   // a lane without a row of its own goes along
-    CeRow o{kNegBig, {0.f, 0.f}, {0.f, 0.f}, 0.f, 0u, 0, 0u};
-    for (int k = k0; k < K; k += kLanes * kCeJoinAhead) {
-        CePiece p[kCeJoinAhead];
+    const int lane = threadIdx.x & 31, k0 = threadIdx.x % kLanes;
+    const int n_rows = kSide * per;
+    const int64_t r0 = (int64_t)blockIdx.x * n_rows;
+    for (int t = 0; t < per; ++t) {
+        const int mine = t * kSide + threadIdx.x / kLanes;
+        const int64_t row = r0 + mine < a.N ? r0 + mine : a.N - 1;   // a lane without a row of its own goes along
+        CeRow o{kNegBig, {0.f, 0.f}, {0.f, 0.f}, 0.f, 0u, 0, 0u};
+        for (int k = k0; k < K; k += kLanes * kCeJoinAhead) {
+            CePiece p[kCeJoinAhead];
+            float M = o.M;
+#pragma unroll
+            for (int i = 0; i < kCeJoinAhead; ++i)
+                if (k + i * kLanes < K) p[i] = src.piece(row, k + i * kLanes);
+#pragma unroll
+            for (int i = 0; i < kCeJoinAhead; ++i)
+                if (k + i * kLanes < K) M = fmaxf(M, p[i].m);
+            ce_recentre(o, M);
+#pragma unroll
+            for (int i = 0; i < kCeJoinAhead; ++i)
+                if (k + i * kLanes < K) ce_add(o, p[i]);
+        }
         float M = o.M;
 #pragma unroll
-        for (int i = 0; i < kCeJoinAhead; ++i)
-            if (k + i * kLanes < K) p[i] = src.piece(row, k + i * kLanes);
-#pragma unroll
-        for (int i = 0; i < kCeJoinAhead; ++i)
-            if (k + i * kLanes < K) M = fmaxf(M, p[i].m);
+        for (int m = kWarpLanes / 2; m > 0; m >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, m));
         ce_recentre(o, M);
 #pragma unroll
-        for (int i = 0; i < kCeJoinAhead; ++i)
-            if (k + i * kLanes < K) ce_add(o, p[i]);
+        for (int m = kWarpLanes / 2; m > 0; m >>= 1) {
+            const int owners = __shfl_xor_sync(0xffffffffu, o.owners, m);
+            const float zt = __shfl_xor_sync(0xffffffffu, o.zt, m);
+            if (owners > o.owners) o.zt = zt;
+            o.owners += owners;
+            o.flags |= __shfl_xor_sync(0xffffffffu, o.flags, m);
+            o.n += __shfl_xor_sync(0xffffffffu, o.n, m);
+            df_add(o.S, shfl_xor(o.S, m));
+            df_add(o.W, shfl_xor(o.W, m));
+        }
+        if (threadIdx.x % kWarpLanes == 0) rows[mine * kParts + threadIdx.x % kLanes / 32] = o;
     }
-    float M = o.M;
-#pragma unroll
-    for (int m = kLanes / 2; m > 0; m >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, m));
-    ce_recentre(o, M);
-#pragma unroll
-    for (int m = kLanes / 2; m > 0; m >>= 1) {
-        const int owners = __shfl_xor_sync(0xffffffffu, o.owners, m);
-        const float zt = __shfl_xor_sync(0xffffffffu, o.zt, m);
-        if (owners > o.owners) o.zt = zt;
-        o.owners += owners;
-        o.flags |= __shfl_xor_sync(0xffffffffu, o.flags, m);
-        o.n += __shfl_xor_sync(0xffffffffu, o.n, m);
-        df_add(o.S, shfl_xor(o.S, m));
-        df_add(o.W, shfl_xor(o.W, m));
-    }
-    if (k0 == 0) rows[mine] = o;
     __syncthreads();
-    if (warp != 0 || lane >= kRows || r0 + lane >= a.N) return;
-    o = rows[lane];
+    if (threadIdx.x >= n_rows || r0 + lane >= a.N) return;               // n_rows is 32 at most
+    CeRow o = rows[lane * kParts];
+    for (int w = 1; w < kParts; ++w) {                                   // the row's warps, in order
+        CeRow p = rows[lane * kParts + w];
+        const float top = fmaxf(o.M, p.M);
+        ce_recentre(o, top);
+        ce_recentre(p, top);
+        if (p.owners > o.owners) o.zt = p.zt;
+        o.owners += p.owners;
+        o.flags |= p.flags;
+        o.n += p.n;
+        df_add(o.S, p.S);
+        df_add(o.W, p.W);
+    }
     if (kind != kCeGathered && a.targets[r0 + lane] >= 0) o.zt = src.target(r0 + lane, o.zt);
     ce_finish<kind>(o, r0 + lane, a);
 }
@@ -361,16 +381,17 @@ static CeJoinArgs ce_join_args(const CeArgs &a) {
 template <class Src>
 static cudaError_t launch_ce_join(const Src &src, int K, const CeArgs &a) {
     const CeJoinArgs j = ce_join_args(a);
-    auto go = [&](auto kernel, int lanes) {
-        const int64_t rows = kCeJoinThreads / lanes;
-        return launch_pdl(kernel, dim3((unsigned)((a.N + rows - 1) / rows)), dim3(kCeJoinThreads), 0, a.stream, src, K, j);
+    const bool whole = K > 32;                    // the CTA for a row
+    const int per = whole && a.N > 1216 ? kCeJoinMany : 1;   // eight CTAs on every SM take 1216 rows at once
+    const int rows = whole ? per : kCeJoinThreads / 8;
+    auto go = [&](auto kernel) {
+        return launch_pdl(kernel, dim3((unsigned)((a.N + rows - 1) / rows)), dim3(kCeJoinThreads), 0, a.stream, src, K, per, j);
     };
     if constexpr (std::is_same<Src, CeShards>::value) {
-        return go(ce_join_kernel<Src, kCeGathered, 8>, 8);
+        return whole ? go(ce_join_kernel<Src, kCeGathered, kCeJoinThreads>) : go(ce_join_kernel<Src, kCeGathered, 8>);
     } else {
-        if (a.parts)
-            return K <= 32 ? go(ce_join_kernel<Src, kCeRecords, 8>, 8) : go(ce_join_kernel<Src, kCeRecords, 32>, 32);
-        return K <= 32 ? go(ce_join_kernel<Src, kCeLoss, 8>, 8) : go(ce_join_kernel<Src, kCeLoss, 32>, 32);
+        if (a.parts) return whole ? go(ce_join_kernel<Src, kCeRecords, kCeJoinThreads>) : go(ce_join_kernel<Src, kCeRecords, 8>);
+        return whole ? go(ce_join_kernel<Src, kCeLoss, kCeJoinThreads>) : go(ce_join_kernel<Src, kCeLoss, 8>);
     }
 }
 

@@ -255,7 +255,12 @@ struct PairBars {
 constexpr int kPairDualRegsLaunch = 168, kPairDualRegsLow = 56, kPairDualRegsHigh = 224;
 static_assert(4 * kPairDualRegsLow + 8 * kPairDualRegsHigh == 12 * kPairDualRegsLaunch,
               "the epilogue warpgroups take exactly what warpgroup 0 gives up");
-__host__ __device__ constexpr int pair_threads(bool dual) { return dual ? 12 * 32 : kLThreads; }
+// Wide epilogues: eight warps, two per TMEM lane quarter, one 128-column half of the tile each (a tile with a short
+// K is done before four warps have gone through 256 columns).
+constexpr int kWideEpiCols = 128, kWideEpiWarps = 8;
+__host__ __device__ constexpr int pair_threads(bool dual, bool wide = false) {
+    return dual ? 12 * 32 : wide ? 64 + 32 * kWideEpiWarps : kLThreads;
+}
 __host__ __device__ constexpr int pair_epi_first_warp(bool dual) { return dual ? 4 : 2; }
 
 // Epilogues that declare kPdl belong to kernels that are launched with programmatic stream serialization
@@ -268,6 +273,16 @@ struct PdlOf {
 template <class Epi>
 struct PdlOf<Epi, std::void_t<decltype(Epi::kPdl)>> {
     static constexpr bool value = Epi::kPdl;
+};
+
+// Epilogues that declare kWide are called by eight warps, for 128 columns at a time.
+template <class Epi, class = void>
+struct WideOf {
+    static constexpr bool value = false;
+};
+template <class Epi>
+struct WideOf<Epi, std::void_t<decltype(Epi::kWide)>> {
+    static constexpr bool value = Epi::kWide;
 };
 
 // What a tile's sum goes over. Whole: all of K (and, chained, all of the second product's K). Split: an output
@@ -293,12 +308,14 @@ __device__ __forceinline__ TileK tile_k(const SplitK &p, int split, int n_k, int
 }
 
 template <class Epi, bool kAMn = false, bool kBMn = false, bool kDual = false, bool kChain = false, class Ks = WholeK>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair_threads(kDual), 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair_threads(kDual, WideOf<Epi>::value), 1)
 umma_gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
                       const __grid_constant__ CUtensorMap tm_a2, const __grid_constant__ CUtensorMap tm_b2, int M,
                       int Nn, int K, int K2, int group_m, int l2hints, const Epi epi, const Ks ks) {
     static_assert(!kDual || (!kAMn && !kBMn), "the dual form takes K-major operands");
     static_assert(!(kDual && Ks::kSplit), "split sums are of one product");
+    constexpr bool kWide = WideOf<Epi>::value;
+    static_assert(!(kDual && kWide), "the dual form has its own halves");
     static_assert(!(kDual && kChain), "one second product at a time");
     extern __shared__ uint8_t smem_raw[];
     __shared__ PairBars bars;
@@ -312,7 +329,7 @@ umma_gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_con
     const int n_k = (K + kLBK - 1) / kLBK;
     const int n_k2 = (kDual || kChain) ? (K2 + kLBK - 1) / kLBK : 0;   // k-blocks of the second product
     const int64_t pair = blockIdx.x >> 1, n_pairs = gridDim.x >> 1;
-    constexpr int kEpiThreads = pair_threads(kDual) - 32 * pair_epi_first_warp(kDual);
+    constexpr int kEpiThreads = pair_threads(kDual, kWide) - 32 * pair_epi_first_warp(kDual);
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < kPStages; ++s) {
@@ -446,7 +463,7 @@ umma_gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_con
         if constexpr (kDual) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kPairDualRegsHigh));
         const int q = warp & 3;
         const int r_in = q * 32 + lane;
-        const int half = kDual ? (warp - 4) >> 2 : 0;   // dual form: the warp's 128-column half
+        const int half = kDual ? (warp - 4) >> 2 : kWide ? (warp - 2) >> 2 : 0;   // the warp's 128-column half
         const uint32_t lanes = (uint32_t)(q * 32) << 16;
         uint32_t j = 0;
         bool ok = true;
@@ -483,11 +500,13 @@ umma_gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_con
                 }
                 tc_fence_after();
                 if (__all_sync(0xffffffffu, ok)) {
-                    const uint32_t acc = tmem + buf * kLBN + lanes;
-                    if constexpr (Ks::kSplit)
-                        epi(mb * kLBM + r_in, nb * kLBN, min(kLBN, Nn - nb * kLBN), acc, (int)(tile / n_out));
-                    else
-                        epi(mb * kLBM + r_in, nb * kLBN, min(kLBN, Nn - nb * kLBN), acc);
+                    constexpr int kCols = kWide ? kWideEpiCols : kLBN;
+                    const int c0 = nb * kLBN + half * kWideEpiCols, ncol = min(kCols, Nn - c0);
+                    const uint32_t acc = tmem + buf * kLBN + half * kWideEpiCols + lanes;
+                    if (!kWide || ncol > 0) {
+                        if constexpr (Ks::kSplit) epi(mb * kLBM + r_in, c0, ncol, acc, (int)(tile / n_out));
+                        else epi(mb * kLBM + r_in, c0, ncol, acc);
+                    }
                 }
                 tc_fence_before();
                 mbar_arrive_cluster(cluster_addr(&bars.acc_empty[buf], 0));
@@ -718,9 +737,10 @@ static cudaError_t launch_gemm_pair_impl(const CUtensorMap &ta, const CUtensorMa
     if (group_m > n_mp) group_m = n_mp;
     if constexpr (PdlOf<Epi>::value)
         return launch_pdl(umma_gemm_pair_kernel<Epi, kAMn, kBMn, kDual, kChain, Ks>, dim3(grid),
-                          dim3(pair_threads(kDual)), kPSmemBytes, stream, ta, tb, ta2, tb2, M, Nn, K, K2, group_m, l2hints,
+                          dim3(pair_threads(kDual, WideOf<Epi>::value)), kPSmemBytes, stream, ta, tb, ta2, tb2, M, Nn, K, K2, group_m, l2hints,
                           epi, ks);
-    umma_gemm_pair_kernel<Epi, kAMn, kBMn, kDual, kChain, Ks><<<grid, pair_threads(kDual), kPSmemBytes, stream>>>(
+    umma_gemm_pair_kernel<Epi, kAMn, kBMn, kDual, kChain, Ks>
+        <<<grid, pair_threads(kDual, WideOf<Epi>::value), kPSmemBytes, stream>>>(
         ta, tb, ta2, tb2, M, Nn, K, K2, group_m, l2hints, epi, ks);
     return cudaGetLastError();
 }

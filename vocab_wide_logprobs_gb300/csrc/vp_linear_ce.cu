@@ -32,9 +32,10 @@ __device__ __forceinline__ void scale_all(float (&v)[32], float s) {
 
 template <bool kCap>
 struct CeEpi {
-    static constexpr bool kPdl = true;
+    static constexpr bool kPdl = true, kWide = true;
     int N, n_t;
     float scale;        // cut_off(D)
+    bool sum;           // the sum of the logits, which only label smoothing asks for
     int64_t vocab_start;
     const int64_t *targets;
     CeRules q;
@@ -45,26 +46,34 @@ struct CeEpi {
         const int64_t tg = valid ? targets[row] : -1;
         const int64_t t = tg - vocab_start - col0;
         const int tloc = (tg >= 0 && t >= 0 && t < ncol) ? (int)t : -1;
-        float m = kNegBig, S = 0.f, zt = 0.f, Z0 = 0.f, Z1 = 0.f;
+        float m = kNegBig, S = 0.f, zt = 0.f;
+        float2 Z = f2(0.f);
 #pragma unroll 1
-        for (int c = 0; c < kLBN / 32; ++c) {
+        for (int c = 0; c < kWideEpiCols / 32; ++c) {
             float v[32];
             tmem_ld32(taddr + c * 32, v);
             const int n = ncol - c * 32;                 // columns of the vocabulary left
             if (n <= 0) continue;
             scale_all(v, scale);
             if (kCap) soft_cap(q, v);
-            float cm = kNegBig;
+            if ((uint32_t)(tloc - c * 32) < 32u) {
 #pragma unroll
-            for (int i = 0; i < 32; i += 2) {
-                if (c * 32 + i == tloc) zt = v[i];
-                if (c * 32 + i + 1 == tloc) zt = v[i + 1];
-                Z0 += i < n ? v[i] : 0.f;
-                Z1 += i + 1 < n ? v[i + 1] : 0.f;
-                if (i >= n) v[i] = -INFINITY;
-                if (i + 1 >= n) v[i + 1] = -INFINITY;
-                cm = fmaxf(cm, fmaxf(v[i], v[i + 1]));
+                for (int i = 0; i < 32; ++i)
+                    if (c * 32 + i == tloc) zt = v[i];
             }
+            if (n < 32) {
+#pragma unroll
+                for (int i = 0; i < 32; ++i) {
+                    Z.x += i < n ? v[i] : 0.f;
+                    if (i >= n) v[i] = -INFINITY;
+                }
+            } else if (sum) {
+#pragma unroll
+                for (int i = 0; i < 32; i += 2) Z = __fadd2_rn(Z, make_float2(v[i], v[i + 1]));
+            }
+            float cm = m;
+#pragma unroll
+            for (int i = 0; i < 32; ++i) cm = fmaxf(cm, v[i]);
             if (cm > m) {
                 S *= ex2_approx((m - cm) * kLog2e);
                 m = cm;
@@ -76,28 +85,39 @@ struct CeEpi {
             S = fmaf(s2.x + s2.y, k.f, S);
         }
         if (!valid) return;
-        tiles[(int64_t)row * n_t + col0 / kLBN] = make_float4(m, S, Z0 + Z1, 0.f);
+        tiles[(int64_t)row * n_t + col0 / kCeTileCols] = make_float4(m, S, Z.x + Z.y, 0.f);
         if (tloc >= 0) tgt[row] = zt;
     }
 };
 
-// A warp's 32 rows of 64 bf16 columns to global memory, row `first` + i from lane i's eight vectors, through
-// shared memory: eight lanes then write a row's 128 bytes at once. Straight from the lanes every store would
-// touch half a sector of each of 32 rows (dW of 75968 x 4096 from 16 tokens took 256 us, its bytes are 92).
-__device__ __forceinline__ void store_rows64(uint4 *stage, const uint4 (&v)[8], __nv_bfloat16 *dst, int64_t ld, int first,
-                                             int M) {
+// A warp's 32 rows of kVecs 16-byte vectors, row i in lane i, turned in shared memory so that kVecs lanes have a
+// row's vectors behind one another: use(row, vector, value). Straight from the lanes every store would touch half a
+// sector of each of 32 rows (dW of 75968 x 4096 from 16 tokens took 256 us, its bytes are 92; now 150). The
+// vectors' places are swapped by row so that neither side meets a bank twice.
+constexpr int kStageVecs = 32 * 8;                       // of each epilogue warp: 4 KB
+template <int kVecs, class Use>
+__device__ __forceinline__ void turn_rows(uint4 *stage, const uint4 (&v)[kVecs], Use use) {
+    static_assert(kVecs == 4 || kVecs == 8, "64 or 128 bytes of a row");
     const int lane = threadIdx.x & 31;
+    auto at = [](int r, int j) { return r * kVecs + (j ^ (kVecs == 8 ? r & 7 : (r >> 1) & 3)); };
     __syncwarp();                                        // the last rows have been read
 #pragma unroll
-    for (int j = 0; j < 8; ++j) stage[lane * 8 + (j ^ (lane & 7))] = v[j];
+    for (int j = 0; j < kVecs; ++j) stage[at(lane, j)] = v[j];
     __syncwarp();
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const int r = 4 * i + lane / 8, j = lane % 8;
-        if (first + r < M) stg_stream(dst + r * ld + 8 * j, stage[r * 8 + (j ^ (r & 7))]);
+    for (int i = 0; i < kVecs; ++i) {
+        const int r = (32 / kVecs) * i + lane / kVecs, j = lane % kVecs;
+        use(r, j, stage[at(r, j)]);
     }
 }
-constexpr int kStageVecs = 32 * 8;                       // of each epilogue warp: 4 KB
+// .. and to the rows `first` .. of a bf16 matrix
+template <int kVecs>
+__device__ __forceinline__ void store_rows(uint4 *stage, const uint4 (&v)[kVecs], __nv_bfloat16 *dst, int64_t ld, int first,
+                                           int M) {
+    turn_rows(stage, v, [&](int r, int j, const uint4 &x) {
+        if (first + r < M) stg_stream(dst + r * ld + 8 * j, x);
+    });
+}
 
 // Which values of dz the mixed precision carries as a pair. One bf16 value is off by up to 2^-8 of
 // itself, so what the values up to a threshold of a row add to the error of dhidden is 2^-8 sqrt(sum of
@@ -113,7 +133,7 @@ constexpr int kFlagRows = 32, kFlagCols = 64;
 // lo_off != 0, what that rounding took away as a second one).
 template <bool kCap>
 struct DzCeEpi {
-    static constexpr bool kPdl = true;
+    static constexpr bool kPdl = true, kWide = true;
     int N, V, v0, ldz;
     float scale;        // cut_off(D)
     int64_t vocab_start;
@@ -142,72 +162,85 @@ struct DzCeEpi {
             const float zt = (s.m + s.logS_hi + s.c_hi) * q.inv_cap;
             limit *= fmaxf(fmaf(-zt, zt, 1.f), 9.5367431640625e-07f);
         }
-        __shared__ uint4 stage[kLThreads / 32 - 2][kStageVecs];
-        uint4 *mine = stage[(threadIdx.x >> 5) & 3];
+        __shared__ uint4 stage[kWideEpiWarps][kStageVecs];
+        uint4 *mine = stage[(threadIdx.x >> 5) - 2];
         const int first = row - (threadIdx.x & 31);           // the warp's first row
+        float most = 0.f;                                     // of the row's 64 columns
 #pragma unroll 1
-        for (int c = 0; c < kLBN / 64; ++c) {
-            uint4 hi[8], lo[8];
-            float most = 0.f;                                 // of the row's 64 columns
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                const int c0 = c * 64 + half * 32;
-                float v[32], slope[32];
-                tmem_ld32(taddr + c0, v);
-                scale_all(v, scale);
-                if (kCap) soft_cap<32, true>(q, v, slope);
-                const int64_t at = tcol - c0;
+        for (int c = 0; c < kWideEpiCols; c += 32) {
+            float v[32], slope[32];
+            tmem_ld32(taddr + c, v);
+            scale_all(v, scale);
+            if (kCap) soft_cap<32, true>(q, v, slope);
+            const uint32_t at = tcol >= 0 && tcol < kWideEpiCols ? (uint32_t)((int)tcol - c) : 32u;
+            float dt = 0.f;                                   // the target's column
+            if (at < 32u) {
                 float zt = 0.f;
 #pragma unroll
+                for (int i = 0; i < 32; ++i)
+                    if (i == (int)at) zt = v[i];
+                dt = ce_grad_target(q, gr, zt);
+            }
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) {
+                const float2 d = ce_grad2(gr, make_float2(v[i], v[i + 1]));
+                v[i] = d.x;
+                v[i + 1] = d.y;
+            }
+            if (at < 32u) {
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                    if (i == (int)at) v[i] = dt;
+            }
+            if (kCap) {
+#pragma unroll
                 for (int i = 0; i < 32; i += 2) {
-                    if (i == at) zt = v[i];
-                    if (i + 1 == at) zt = v[i + 1];
-                    const float2 d = ce_grad2(gr, make_float2(v[i], v[i + 1]));
+                    const float2 d = __fmul2_rn(make_float2(v[i], v[i + 1]), make_float2(slope[i], slope[i + 1]));
                     v[i] = d.x;
                     v[i + 1] = d.y;
                 }
-                if (at >= 0 && at < 32) {
-                    const float d = ce_grad_target(q, gr, zt);
+            }
+            if (mode || c + 32 > ncol) {
 #pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        if (i == at) v[i] = d;
-                }
-                if (kCap) {
+                for (int i = 0; i < 32; ++i) v[i] = mode == 1 || c + i >= ncol ? 0.f : mode == 2 ? qnan() : v[i];
+            }
+            uint4 hi[4];
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) v[i] *= slope[i];
-                }
-                if (mode || c0 + 32 > ncol) {
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) v[i] = mode == 1 || c0 + i >= ncol ? 0.f : mode == 2 ? qnan() : v[i];
-                }
+            for (int k = 0; k < 4; ++k) hi[k] = Elem<__nv_bfloat16>::pack(v + 8 * k);
+            __nv_bfloat16 *dst = dz + (int64_t)first * ldz + col0 + c;
+            store_rows(mine, hi, dst, ldz, first, N);
+            if (lo_off) {
+                uint4 lo[4];
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                    uint32_t h[4], l[4];
+                    float h[8];                               // what the rounding took away is exact in fp32
+                    Elem<__nv_bfloat16>::unpack(hi[k], h);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float x0 = v[8 * k + 2 * i], x1 = v[8 * k + 2 * i + 1];
-                        most = fmaxf(most, fmaxf(fabsf(x0), fabsf(x1)));
-                        const __nv_bfloat162 b = __floats2bfloat162_rn(x0, x1);
-                        h[i] = *reinterpret_cast<const uint32_t *>(&b);
-                        // what the rounding took away (exact in fp32), itself rounded
-                        const __nv_bfloat162 r = __floats2bfloat162_rn(x0 - __low2float(b), x1 - __high2float(b));
-                        l[i] = *reinterpret_cast<const uint32_t *>(&r);
+                    for (int i = 0; i < 8; ++i) {
+                        most = fmaxf(most, fabsf(v[8 * k + i]));
+                        h[i] = v[8 * k + i] - h[i];
                     }
-                    hi[half * 4 + k] = make_uint4(h[0], h[1], h[2], h[3]);
-                    lo[half * 4 + k] = make_uint4(l[0], l[1], l[2], l[3]);
+                    lo[k] = Elem<__nv_bfloat16>::pack(h);
                 }
+                store_rows(mine, lo, dst + lo_off, ldz, first, N);
             }
-            __nv_bfloat16 *dst = dz + (int64_t)first * ldz + col0 + c * 64;
-            store_rows64(mine, hi, dst, ldz, first, N);
-            if (lo_off) store_rows64(mine, lo, dst + lo_off, ldz, first, N);
-            if (flags) {
+            if (flags && c % 64) {
                 const bool pair = __any_sync(0xffffffffu, valid && most > limit);
                 if ((row & 31) == 0 && valid)
-                    flags[(int64_t)(row / kFlagRows) * (ldz / kFlagCols) + (col0 + c * 64) / kFlagCols] = pair;
+                    flags[(int64_t)(row / kFlagRows) * (ldz / kFlagCols) + (col0 + c) / kFlagCols] = pair;
+                most = 0.f;
             }
         }
     }
 };
+
+// The logits of hidden rows [N, D] and rows of W [nv, D], on CTA pairs.
+template <class Epi>
+static cudaError_t ce_logits_gemm(const void *h, const void *w, int N, int nv, int D, const Epi &epi, cudaStream_t stream) {
+    CUtensorMap ta, tb;
+    if (!make_map(&ta, h, N, D, D, kLBM) || !make_map(&tb, w, nv, D, D, kPBHalf)) return cudaErrorInvalidValue;
+    return launch_gemm_pair<Epi>(ta, tb, N, nv, D, epi, stream, 0, kHintLogits);
+}
 
 struct CeFwdLayout {
     size_t tiles, tgt, total;
@@ -215,7 +248,7 @@ struct CeFwdLayout {
 static CeFwdLayout ce_fwd_layout(int64_t N, int64_t V) {
     CeFwdLayout L;
     L.tiles = 0;
-    L.tgt = up256((size_t)N * ((V + kLBN - 1) / kLBN) * sizeof(float4));
+    L.tgt = up256((size_t)N * ((V + kCeTileCols - 1) / kCeTileCols) * sizeof(float4));
     L.total = L.tgt + up256((size_t)N * sizeof(float));
     return L;
 }
@@ -223,17 +256,17 @@ size_t linear_ce_workspace_bytes(int64_t N, int64_t V) { return ce_fwd_layout(N,
 
 cudaError_t launch_linear_ce_fwd(const CeArgs &a) {
     const CeFwdLayout L = ce_fwd_layout(a.N, a.V);
-    const int n_t = (int)((a.V + kLBN - 1) / kLBN);
+    const int n_t = (int)((a.V + kCeTileCols - 1) / kCeTileCols);
     uint8_t *ws = static_cast<uint8_t *>(a.workspace);
     float4 *tiles = reinterpret_cast<float4 *>(ws + L.tiles);
     float *tgt = reinterpret_cast<float *>(ws + L.tgt);
     const CeRules q = ce_rules(a.opt);
     auto gemm = [&](const auto &epi) {
-        return launch_logits_gemm(a.hidden, a.weight, (int)a.N, (int)a.V, (int)a.D, epi, a.stream, true);
+        return ce_logits_gemm(a.hidden, a.weight, (int)a.N, (int)a.V, (int)a.D, epi, a.stream);
     };
     const cudaError_t e = q.cap > 0.f
-                              ? gemm(CeEpi<true>{(int)a.N, n_t, cut_off(a.D), a.vocab_start, a.targets, q, tiles, tgt})
-                              : gemm(CeEpi<false>{(int)a.N, n_t, cut_off(a.D), a.vocab_start, a.targets, q, tiles, tgt});
+                              ? gemm(CeEpi<true>{(int)a.N, n_t, cut_off(a.D), a.parts || q.smooth > 0.f, a.vocab_start, a.targets, q, tiles, tgt})
+                              : gemm(CeEpi<false>{(int)a.N, n_t, cut_off(a.D), a.parts || q.smooth > 0.f, a.vocab_start, a.targets, q, tiles, tgt});
     if (e != cudaSuccess) return e;
     return launch_ce_join(CeTiles{tiles, tgt, n_t, (int)a.V}, n_t, a);
 }
@@ -255,8 +288,11 @@ pair_list_kernel(const uint8_t *__restrict__ flags, int row_groups, int pitch, i
         const int k = k0 + tid;
         bool any = false;
         if (k < n) {
-            // 8 groups of rows and one of columns, or 2 and 4 (one word: the pitch is a multiple of 4)
+            // 8 groups of rows and one of columns, or 2 and 4 (one word: the pitch is a multiple of 4; the last may
+            // hold groups behind the vocabulary, which nothing has written)
             const int r0 = by_rows ? 8 * b : 2 * k;
+            const int in_word = col_groups - 4 * b;
+            const uint32_t mask = by_rows || in_word >= 4 ? 0xffffffffu : (1u << (8 * in_word)) - 1u;
             uint32_t seen = 0;
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
@@ -264,7 +300,7 @@ pair_list_kernel(const uint8_t *__restrict__ flags, int row_groups, int pitch, i
                 const uint8_t *f = flags + (int64_t)(r0 + i) * pitch;
                 seen |= by_rows ? f[k] : *reinterpret_cast<const uint32_t *>(f + 4 * b);
             }
-            any = seen != 0;
+            any = (seen & mask) != 0;
         }
         const uint32_t votes = __ballot_sync(0xffffffffu, any);
         if (lane == 0) s_n[warp] = __popc(votes);
@@ -280,25 +316,48 @@ pair_list_kernel(const uint8_t *__restrict__ flags, int row_groups, int pitch, i
     if (tid == 0) count[blockIdx.x] = (int)done;
 }
 
-// dhidden's tiles: the sum over a share of the k-blocks, kept apart for each share.
+// dhidden's tiles: the sum over a share of the k-blocks, kept apart for each share; ld is a multiple of 64.
 struct SplitAccEpi {
-    static constexpr bool kPdl = true;
+    static constexpr bool kPdl = true, kWide = true;
     int M, ld;
     bool first;
     float *acc;          // [splits][M][ld]
     __device__ __forceinline__ void operator()(int row, int col0, int ncol, uint32_t taddr, int split) const {
-        AccEpi{M, ld, first, acc + (int64_t)split * M * ld, nullptr}(row, col0, ncol, taddr);
+        __shared__ uint4 stage[kWideEpiWarps][kStageVecs];
+        uint4 *mine = stage[(threadIdx.x >> 5) - 2];
+        const int top = row - (int)(threadIdx.x & 31);
+#pragma unroll 1
+        for (int c = 0; c < ncol; c += 32) {
+            float v[32];
+            tmem_ld32(taddr + c, v);
+            uint4 u[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) u[j] = Elem<float>::pack(v + 4 * j);
+            float *dst = acc + ((int64_t)split * M + top) * ld + col0 + c;
+            turn_rows(mine, u, [&](int r, int j, const uint4 &x) {
+                if (top + r >= M) return;
+                uint4 *p = reinterpret_cast<uint4 *>(dst + (int64_t)r * ld + 4 * j);
+                float f[4], o[4];
+                Elem<float>::unpack(x, f);
+                if (!first) {
+                    Elem<float>::unpack(*p, o);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) f[k] += o[k];
+                }
+                *p = Elem<float>::pack(f);
+            });
+        }
     }
 };
 // dW's tiles, rounded; ld is a multiple of 64.
 struct StoreRowsEpi {
-    static constexpr bool kPdl = true;
+    static constexpr bool kPdl = true, kWide = true;
     int M, ld;
     int64_t row0;
     __nv_bfloat16 *out;
     __device__ __forceinline__ void operator()(int row, int col0, int ncol, uint32_t taddr, int) const {
-        __shared__ uint4 stage[kLThreads / 32 - 2][kStageVecs];
-        uint4 *mine = stage[(threadIdx.x >> 5) & 3];
+        __shared__ uint4 stage[kWideEpiWarps][kStageVecs];
+        uint4 *mine = stage[(threadIdx.x >> 5) - 2];
         const int first = row - (threadIdx.x & 31);
         // a chunk's columns come out of TMEM while the one before is stored
         uint32_t f[2][32];
@@ -306,16 +365,16 @@ struct StoreRowsEpi {
         tmem_ld32_issue(taddr + 32, f[1]);
         tmem_wait_ld();
 #pragma unroll
-        for (int c = 0; c < kLBN; c += 64) {
+        for (int c = 0; c < kWideEpiCols; c += 64) {
             uint4 v[8];
 #pragma unroll
             for (int k = 0; k < 8; ++k) v[k] = Elem<__nv_bfloat16>::pack(reinterpret_cast<const float *>(f[k / 4]) + 8 * (k % 4));
-            if (c + 64 < kLBN) {
+            if (c + 64 < kWideEpiCols) {
                 tmem_ld32_issue(taddr + c + 64, f[0]);
                 tmem_ld32_issue(taddr + c + 96, f[1]);
             }
-            if (c < ncol) store_rows64(mine, v, out + (row0 + first) * (int64_t)ld + col0 + c, ld, first, M);
-            if (c + 64 < kLBN) tmem_wait_ld();
+            if (c < ncol) store_rows(mine, v, out + (row0 + first) * (int64_t)ld + col0 + c, ld, first, M);
+            if (c + 64 < kWideEpiCols) tmem_wait_ld();
         }
     }
 };
@@ -412,7 +471,7 @@ cudaError_t launch_linear_ce_bwd(const CeArgs &a) {
     for (int64_t v0 = 0; v0 < V; v0 += vc) {
         const int nv = (int)(V - v0 < vc ? V - v0 : vc);
         auto gemm = [&](const auto &epi) {
-            return launch_logits_gemm(h, W + v0 * D, N, nv, D, epi, a.stream, true);
+            return ce_logits_gemm(h, W + v0 * D, N, nv, D, epi, a.stream);
         };
         const int64_t lo_off = chain ? a.N * vc : 0;
         e = q.cap > 0.f ? gemm(DzCeEpi<true>{N, V, (int)v0, (int)vc, cut_off(D), a.vocab_start, a.targets, q, stats, a.g, dz, a.err, lo_off, flags})
