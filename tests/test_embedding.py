@@ -136,7 +136,7 @@ def test_gradient_widths(D, types):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("kind", ["zipf", "flat", "one", "sorted"])
-@pytest.mark.parametrize("N, V", [(2, 1), (8, 9), (128, 5003), (129, 77), (9, 8), (255, 33), (256, 5003), (2049, 5003), (5000, 160000),
+@pytest.mark.parametrize("N, V", [(2, 1), (8, 9), (128, 5003), (129, 77), (100, 90), (9, 8), (250, 33), (500, 5003), (2049, 5003), (5000, 160000),
                                   (20000, 300), (70000, 40)])
 def test_gradient_runs(N, V, kind):
     """Runs of one id within a window of tokens, at its ends, and over many windows; tables of more rows than the SMs have

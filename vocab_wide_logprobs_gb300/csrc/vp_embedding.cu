@@ -28,22 +28,42 @@ namespace vp {
 
 constexpr int kEmbVec = 8;   // columns of a vector: 16 bytes of bf16, 32 of fp32
 
-// Columns c .. c + 7 (vectors) or c, c + step, .. (single elements) of a row, as fp32.
+// Columns c .. c + 7 (vectors) or c, c + step, .. (single elements) of a row, as they lie in memory: a caller starts
+// several rows' loads before it takes the first one's values.
 template <typename T, bool kVector>
-__device__ __forceinline__ void load8(const T *row, int c, int step, int D, float (&v)[kEmbVec]) {
-    if constexpr (kVector) {
-        if constexpr (sizeof(T) == 2) {
-            Elem<T>::unpack(ldg_stream(row + c), v);
-        } else {
-            const uint4 a = ldg_stream(row + c), b = ldg_stream(row + c + 4);
-            v[0] = __uint_as_float(a.x); v[1] = __uint_as_float(a.y); v[2] = __uint_as_float(a.z); v[3] = __uint_as_float(a.w);
-            v[4] = __uint_as_float(b.x); v[5] = __uint_as_float(b.y); v[6] = __uint_as_float(b.z); v[7] = __uint_as_float(b.w);
-        }
-    } else {
+struct Row8 {
+    uint4 u[kVector ? kEmbVec * sizeof(T) / 16 : 1];
+    T e[kVector ? 1 : kEmbVec];
+    __device__ __forceinline__ void load(const T *row, int c, int step, int D) {
+        if constexpr (kVector) {
 #pragma unroll
-        for (int e = 0; e < kEmbVec; ++e) v[e] = c + e * step < D ? Elem<T>::load1(row + c + e * step) : 0.f;
+            for (int h = 0; h < (int)(kEmbVec * sizeof(T) / 16); ++h) u[h] = __ldg(reinterpret_cast<const uint4 *>(row + c + h * Elem<T>::kVec));
+        } else {
+#pragma unroll
+            for (int k = 0; k < kEmbVec; ++k) e[k] = c + k * step < D ? __ldg(row + c + k * step) : T(0.f);
+        }
     }
-}
+    // what a kernel also writes: not through the read-only path
+    __device__ __forceinline__ void load_own(const T *row, int c, int step, int D) {
+        if constexpr (kVector) {
+#pragma unroll
+            for (int h = 0; h < (int)(kEmbVec * sizeof(T) / 16); ++h)
+                u[h] = *reinterpret_cast<const uint4 *>(row + c + h * Elem<T>::kVec);
+        } else {
+#pragma unroll
+            for (int k = 0; k < kEmbVec; ++k) e[k] = c + k * step < D ? row[c + k * step] : T(0.f);
+        }
+    }
+    __device__ __forceinline__ void get(float (&v)[kEmbVec]) const {
+        if constexpr (kVector) {
+#pragma unroll
+            for (int h = 0; h < (int)(kEmbVec * sizeof(T) / 16); ++h) Elem<T>::unpack(u[h], v + h * Elem<T>::kVec);
+        } else {
+#pragma unroll
+            for (int k = 0; k < kEmbVec; ++k) v[k] = (float)e[k];
+        }
+    }
+};
 
 template <typename T, bool kVector>
 __device__ __forceinline__ void store8(T *row, int c, int step, int D, const float (&v)[kEmbVec]) {
@@ -84,19 +104,21 @@ embedding_fwd_kernel(const TI *__restrict__ table, int64_t pitch, int V, int D, 
         if (wrong && err && c0 == 0 && lane == 0) atomicOr(err, VP_ERRBIT_TARGET_);
         const TI *row = table + (here ? local : 0) * pitch;
         TO *dst = out + n * (int64_t)D;
-        float v[kEmbUnroll][kEmbVec];
+        Row8<TI, kVector> u[kEmbUnroll];
 #pragma unroll
         for (int k = 0; k < kEmbUnroll; ++k) {
             const int c = kVector ? c0 + (k * 32 + lane) * kEmbVec : c0 + k * 32 * kEmbVec + lane;
-            if (here && c < D) load8<TI, kVector>(row, c, 32, D, v[k]);
+            if (here && c < D) u[k].load(row, c, 32, D);
         }
 #pragma unroll
         for (int k = 0; k < kEmbUnroll; ++k) {
             const int c = kVector ? c0 + (k * 32 + lane) * kEmbVec : c0 + k * 32 * kEmbVec + lane;
             if (c >= D) continue;
+            float v[kEmbVec];
+            u[k].get(v);
 #pragma unroll
-            for (int e = 0; e < kEmbVec; ++e) v[k][e] = here ? v[k][e] * scale : wrong ? qnan() : 0.f;
-            store8<TO, kVector>(dst, c, 32, D, v[k]);
+            for (int e = 0; e < kEmbVec; ++e) v[e] = here ? v[e] * scale : wrong ? qnan() : 0.f;
+            store8<TO, kVector>(dst, c, 32, D, v);
         }
     }
 }
@@ -236,21 +258,12 @@ struct TableGrad {
                                 // what belongs to one that goes on in later ones
 };
 
-// What the columns of a table row hold, and their new value from the sum.
-template <typename TO, bool kVector>
-__device__ __forceinline__ void load_old(const TO *row, int c, int step, int D, float (&o)[kEmbVec]) {
-    if constexpr (kVector) {
-#pragma unroll
-        for (int h = 0; h < (int)(kEmbVec * sizeof(TO) / 16); ++h)
-            Elem<TO>::unpack(*reinterpret_cast<const uint4 *>(row + c + h * Elem<TO>::kVec), o + h * Elem<TO>::kVec);
-    } else {
-#pragma unroll
-        for (int e = 0; e < kEmbVec; ++e) o[e] = c + e * step < D ? (float)row[c + e * step] : 0.f;
-    }
-}
+// A table row's new value from the sum and, where it is added to, from what the row held.
 template <typename TO, bool kVector, bool kAdd>
 __device__ __forceinline__ void finish8(TO *dst, int c, int step, int D, float scale, float (&v)[kEmbVec],
-                                        const float (&o)[kEmbVec]) {
+                                        const Row8<TO, kVector> &old) {
+    float o[kEmbVec];
+    if (kAdd) old.get(o);
 #pragma unroll
     for (int e = 0; e < kEmbVec; ++e) v[e] = kAdd ? fmaf(v[e], scale, o[e]) : v[e] * scale;
     store8<TO, kVector>(dst, c, step, D, v);
@@ -319,20 +332,27 @@ table_grad_kernel(const TI *__restrict__ dy, const TableGrad a, TO *__restrict__
     float sum[kEmbVec] = {};
     constexpr int kAhead = 4;
     for (int i = 0; i < count; i += kAhead) {
-        // the tokens' rows, and with them what the rows of the table hold whose runs end here
-        float v[kAhead][kEmbVec], old[kAdd ? kAhead : 1][kEmbVec];
+        // the tokens' rows (the last one again behind the window), and with them what the rows of the table hold
+        // whose runs end here
+        Row8<TI, kVector> u[kAhead];
+        Row8<TO, kVector> old[kAdd ? kAhead : 1];
 #pragma unroll
-        for (int k = 0; k < kAhead; ++k) {
-            if (i + k >= count) break;
-            load8<TI, kVector>(dy + s_off[i + k], c, step, a.D, v[k]);
-            if (kAdd && (i + k + 1 == count || s_row[i + k + 1] != s_row[i + k]))
-                load_old<TO, kVector>(dW + s_row[i + k] * (int64_t)a.D, c, step, a.D, old[k]);
+        for (int k = 0; k < kAhead; ++k) u[k].load(dy + s_off[min(i + k, count - 1)], c, step, a.D);
+        if constexpr (kAdd) {
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) {
+                const int at = min(i + k, count - 1);
+                if (at + 1 == count || s_row[at + 1] != s_row[at])
+                    old[k].load_own(dW + s_row[at] * (int64_t)a.D, c, step, a.D);
+            }
         }
 #pragma unroll
         for (int k = 0; k < kAhead; ++k) {
             if (i + k >= count) break;
+            float v[kEmbVec];
+            u[k].get(v);
 #pragma unroll
-            for (int e = 0; e < kEmbVec; ++e) sum[e] += v[k][e];
+            for (int e = 0; e < kEmbVec; ++e) sum[e] += v[e];
             const int row = s_row[i + k];
             if (i + k + 1 < count && s_row[i + k + 1] == row) continue;
             // the run ends here, or the window does
@@ -354,17 +374,24 @@ table_grad_kernel(const TI *__restrict__ dy, const TableGrad a, TO *__restrict__
     }
 }
 
-// Few tokens: one launch. A CTA for each token and 8 columns of each of its threads: where no earlier token
-// has the same id, it sums the rows of all that have it, in order. More CTAs write zeros, as above.
+// Few tokens: one launch. A CTA for each token and 8 columns of each of 64 lanes (32 of a narrow table): where no
+// earlier token has the same id, its groups of lanes sum the rows of all that have it, group j those of the j-th,
+// (j + groups)-th, .. of them, and their sums are added in order. (One group of 256 lanes took half a microsecond
+// a token, since the compiler has no more than two of its rows on their way: 40 us for 55 tokens of one id among 256.)
+// More CTAs write zeros, as above.
+// Up to how many: of 128 tokens added to 50000 x 2048 bf16, 9 us with ids of their own, 13 with a third of them
+// alike, 23 with all alike, against 17 to 18 in three launches; of 256, 11, 19 and 40.
 constexpr int kFewTokens = 128;
 template <typename TI, typename TO, bool kVector, bool kAdd>
 __global__ void __launch_bounds__(kGradThreads)
 table_grad_few_kernel(const TI *__restrict__ dy, const TableGrad a, const int64_t *__restrict__ ids, int64_t vocab_start,
-                      bool sharded, TO *__restrict__ dW, int32_t *__restrict__ err, int fill_rows) {
-    __shared__ int s_row[kFewTokens], s_list[kFewTokens];
+                      bool sharded, TO *__restrict__ dW, int32_t *__restrict__ err, int fill_rows, int lanes) {
+    __shared__ int s_row[kFewTokens];
+    __shared__ int64_t s_off[kFewTokens];        // of the tokens that have the CTA's id, in order
     __shared__ uint32_t s_same[kFewTokens / 32];
     __shared__ bool s_asked[kFillMaxRows];
-    const int tid = threadIdx.x, nt = blockDim.x, N = (int)a.N;
+    __shared__ float s_sum[kGradThreads][kEmbVec + 1];
+    const int tid = threadIdx.x, nt = kGradThreads, N = (int)a.N;
     pdl_enter<false>();
     for (int i = tid; i < N; i += nt) {
         const int64_t id = ids[i], local = id - vocab_start;
@@ -405,26 +432,37 @@ table_grad_few_kernel(const TI *__restrict__ dy, const TableGrad a, const int64_
         if (s_row[k] == row) {
             int at = __popc(s_same[k / 32] & ((1u << (k & 31)) - 1u));
             for (int w = 0; w < k / 32; ++w) at += __popc(s_same[w]);
-            s_list[at] = k;
+            s_off[at] = a.dy_rows.off(k);
         }
     __syncthreads();
-    const int c = cb * nt * kEmbVec + (kVector ? tid * kEmbVec : tid), step = nt;
-    if (c >= a.D) return;
-    float sum[kEmbVec] = {}, old[kEmbVec];
+    const int group = tid / lanes, lane = tid % lanes, groups = nt / lanes;
+    const int c = cb * lanes * kEmbVec + (kVector ? lane * kEmbVec : lane), step = lanes;
+    const bool inside = c < a.D;
+    float sum[kEmbVec] = {};
+    Row8<TO, kVector> old;
     TO *dst = dW + row * (int64_t)a.D;
-    if (kAdd) load_old<TO, kVector>(dst, c, step, a.D, old);
+    if (kAdd && inside && group == 0) old.load_own(dst, c, step, a.D);
     constexpr int kAhead = 4;
-    for (int k0 = 0; k0 < count; k0 += kAhead) {
-        float v[kAhead][kEmbVec];
+    for (int k0 = group; inside && k0 < count; k0 += groups * kAhead) {
+        Row8<TI, kVector> u[kAhead];                             // the last row again behind the run
 #pragma unroll
-        for (int k = 0; k < kAhead; ++k)
-            if (k0 + k < count) load8<TI, kVector>(dy + a.dy_rows.off(s_list[k0 + k]), c, step, a.D, v[k]);
+        for (int k = 0; k < kAhead; ++k) u[k].load(dy + s_off[min(k0 + k * groups, count - 1)], c, step, a.D);
 #pragma unroll
-        for (int k = 0; k < kAhead; ++k)
-            if (k0 + k < count)
+        for (int k = 0; k < kAhead; ++k) {
+            float v[kEmbVec];
+            u[k].get(v);
 #pragma unroll
-                for (int e = 0; e < kEmbVec; ++e) sum[e] += v[k][e];
+            for (int e = 0; e < kEmbVec; ++e) sum[e] += k0 + k * groups < count ? v[e] : 0.f;
+        }
     }
+    if (group > 0)
+#pragma unroll
+        for (int e = 0; e < kEmbVec; ++e) s_sum[tid][e] = sum[e];
+    __syncthreads();
+    if (group > 0 || !inside) return;
+    for (int g = 1; g < min(groups, count); ++g)
+#pragma unroll
+        for (int e = 0; e < kEmbVec; ++e) sum[e] += s_sum[g * lanes + lane][e];
     finish8<TO, kVector, kAdd>(dst, c, step, a.D, a.scale, sum, old);
 }
 
@@ -548,9 +586,14 @@ cudaError_t embedding_bwd(const EmbeddingArgs &a) {
     g.dy_rows = Rows{a.R, a.s_o, a.s_i};
     g.scale = a.scale;
     if (a.N <= kFewTokens) {
+        const int lanes = a.D > 32 * kEmbVec ? 64 : 32;
+        g.col_blocks = (int)((a.D + lanes * kEmbVec - 1) / (lanes * kEmbVec));
+        const int rows = (int)std::clamp<int64_t>((int64_t)kFillBytes * kGradThreads / row_bytes, 1, kFillMaxRows);
+        const int64_t ctas = a.N * g.col_blocks + (a.accumulate ? 0 : (a.V + rows - 1) / rows);
+        if (ctas > 2147483647) return cudaErrorInvalidValue;
         auto few = [&](auto kernel) {
-            return launch_pdl(kernel, dim3((unsigned)(a.N * g.col_blocks + fill_ctas)), dim3(threads), 0, a.stream, dy, g,
-                              a.ids, a.vocab_start, a.sharded, dW, a.err, fill_rows);
+            return launch_pdl(kernel, dim3((unsigned)ctas), dim3(kGradThreads), 0, a.stream, dy, g, a.ids, a.vocab_start,
+                              a.sharded, dW, a.err, rows, lanes);
         };
         return vector ? (a.accumulate ? few(table_grad_few_kernel<TI, TO, true, true>) : few(table_grad_few_kernel<TI, TO, true, false>))
                       : (a.accumulate ? few(table_grad_few_kernel<TI, TO, false, true>) : few(table_grad_few_kernel<TI, TO, false, false>));
