@@ -298,12 +298,50 @@ struct SplitK {
     const int *count, *list;   // [n_mp], [n_mp][pitch]: the second product's k-blocks of a row block
     int pitch;
 };
+// Which share of which output tile a tile is. In 32 bits wherever the number of tiles allows: one thread alone
+// needs some hundred nanoseconds for a division in 64, and the MMA thread's tensor pipe stands still meanwhile
+// (1.5 us a tile at first, a fifth of dW's time at 1024 rows).
+struct SplitTile {
+    int split, mp, nb;
+};
+__device__ __forceinline__ SplitTile split_tile(int64_t tile, int64_t n_tiles, int64_t n_out, int n_mp, int n_nb,
+                                                int group_m) {
+    SplitTile t;
+    if (n_tiles <= 0x7fffffff) {
+        const uint32_t n = (uint32_t)n_out, per_group = (uint32_t)group_m * (uint32_t)n_nb;
+        t.split = (int)((uint32_t)tile / n);
+        const uint32_t w = (uint32_t)tile - (uint32_t)t.split * n, g = w / per_group, in = w - g * per_group;
+        const uint32_t first = g * (uint32_t)group_m, gm = min((uint32_t)group_m, (uint32_t)n_mp - first);
+        t.nb = (int)(in / gm);
+        t.mp = (int)(first + in - (uint32_t)t.nb * gm);
+    } else {
+        t.split = (int)(tile / n_out);
+        tile_coords(tile % n_out, n_mp, n_nb, group_m, t.mp, t.nb);
+    }
+    return t;
+}
+// How many of the second product's k-blocks a row block has. A thread asks for the next tile's number while it
+// works on one: waiting for it would cost a memory latency for every tile.
+__device__ __forceinline__ int listed_blocks(const SplitK &p, int mp, int n_k2) {
+    return p.count ? __ldg(p.count + mp) : n_k2;
+}
+// A list's entries from `at` on, four at once, clamped to the list's `n`.
+struct ListAhead {
+    int e[4];
+    __device__ __forceinline__ void load(const int *list, int at, int n) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) e[i] = __ldg(list + min(at + i, n - 1));
+    }
+    __device__ __forceinline__ int get(int i) const { return i < 2 ? (i ? e[1] : e[0]) : (i == 2 ? e[2] : e[3]); }
+};
 // The k-blocks of one tile: k0 .. k1 of the first product, then l0 .. l1 of the second's list.
 struct TileK {
     int k0, k1, l0, l1;
 };
 __device__ __forceinline__ TileK tile_k(const SplitK &p, int split, int n_k, int n_k2) {
-    auto share = [&](int n, int i) { return (int)((int64_t)n * i / p.splits); };
+    if (p.splits == 1) return {0, n_k, 0, n_k2};
+    // 16 shares of 2^25 blocks at most: 32 bits
+    auto share = [&](int n, int i) { return (int)((uint32_t)n * (uint32_t)i / (uint32_t)p.splits); };
     return {share(n_k, split), share(n_k, split + 1), share(n_k2, split), share(n_k2, split + 1)};
 }
 
@@ -366,20 +404,38 @@ umma_gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_con
             const uint64_t pol_a = l2_policy(l2hints & 3), pol_b = l2_policy((l2hints >> 2) & 3);
             uint32_t it = 0;
             bool ok = true;
+            SplitTile at{}, at_next{};
+            int blocks_next = n_k2;
+            if constexpr (Ks::kSplit) {
+                if (pair < n_tiles) {
+                    at_next = split_tile(pair, n_tiles, n_out, n_mp, n_nb, group_m);
+                    if (kChain) blocks_next = listed_blocks(ks, at_next.mp, n_k2);
+                }
+            }
             for (int64_t tile = pair; tile < n_tiles && ok; tile += n_pairs) {
                 int mp, nb;
-                tile_coords(Ks::kSplit ? tile % n_out : tile, n_mp, n_nb, group_m, mp, nb);
-                const int mb = 2 * mp + (int)rank;
-                const int nrow = nb * kLBN + (int)rank * kPBHalf;
                 int n_first = n_k, n_all = n_k + n_k2;   // k-blocks of the tile's first product, and of both
                 TileK tk{0, n_k, 0, n_k2};
                 const int *list = nullptr;
+                ListAhead now{}, next{};                 // the list's entries, four on their way
                 if constexpr (Ks::kSplit) {
+                    at = at_next;
+                    mp = at.mp;
+                    nb = at.nb;
+                    tk = tile_k(ks, at.split, n_k, blocks_next);
+                    if (tile + n_pairs < n_tiles) {
+                        at_next = split_tile(tile + n_pairs, n_tiles, n_out, n_mp, n_nb, group_m);
+                        if (kChain) blocks_next = listed_blocks(ks, at_next.mp, n_k2);
+                    }
                     if (kChain && ks.count) list = ks.list + (int64_t)mp * ks.pitch;
-                    tk = tile_k(ks, (int)(tile / n_out), n_k, kChain && ks.count ? __ldg(ks.count + mp) : n_k2);
                     n_first = tk.k1 - tk.k0;
                     n_all = n_first + tk.l1 - tk.l0;
+                    if (list && tk.l1 > tk.l0) next.load(list, tk.l0, tk.l1);
+                } else {
+                    tile_coords(tile, n_mp, n_nb, group_m, mp, nb);
                 }
+                const int mb = 2 * mp + (int)rank;
+                const int nrow = nb * kLBN + (int)rank * kPBHalf;
                 for (int kb = 0; kb < n_all; ++kb, ++it) {
                     const uint32_t st = it % kPStages, use = it / kPStages;
                     if (use > 0 && !mbar_wait_cluster(&bars.empty[st], (use - 1) & 1)) { ok = false; break; }
@@ -390,8 +446,16 @@ umma_gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_con
                     const bool second = (kDual || kChain) && kb >= n_first;
                     const CUtensorMap *ma = second ? &tm_a2 : &tm_a, *mbm = second ? &tm_b2 : &tm_b;
                     int kc = (second ? kb - n_first + tk.l0 : kb + tk.k0) * kLBK;
-                    if constexpr (Ks::kSplit)
-                        if (second && list) kc = __ldg(list + kb - n_first + tk.l0) * kLBK;
+                    if constexpr (Ks::kSplit && kChain) {
+                        if (second && list) {
+                            const int i = kb - n_first;
+                            if (i % 4 == 0) {
+                                now = next;
+                                next.load(list, tk.l0 + i + 4, tk.l1);
+                            }
+                            kc = now.get(i % 4) * kLBK;
+                        }
+                    }
                     if (kAMn) {
 #pragma unroll
                         for (int i = 0; i < kLBM / 64; ++i)
@@ -417,6 +481,14 @@ umma_gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_con
             constexpr uint32_t idesc = umma_idesc_bf16(2 * kLBM, kLBN, kAMn, kBMn);
             uint32_t it = 0, j = 0;
             bool ok = true;
+            SplitTile at_next{};
+            int blocks_next = n_k2;
+            if constexpr (Ks::kSplit) {
+                if (pair < n_tiles) {
+                    at_next = split_tile(pair, n_tiles, n_out, n_mp, n_nb, group_m);
+                    if (kChain) blocks_next = listed_blocks(ks, at_next.mp, n_k2);
+                }
+            }
             for (int64_t tile = pair; tile < n_tiles && ok; tile += n_pairs, ++j) {
                 // product p of the dual form: accumulator columns p * 256 and
                 // barriers acc_full[p] / acc_empty[p]; otherwise buffer j & 1
@@ -427,12 +499,11 @@ umma_gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_con
                     const uint32_t d = tmem + buf * kLBN;
                     // a chained second product accumulates into the same accumulator
                     int nkb = kChain ? n_k + n_k2 : p ? n_k2 : n_k;
+                    bool next_unknown = false;
                     if constexpr (Ks::kSplit) {
-                        int mp, nb;
-                        tile_coords(Ks::kSplit ? tile % n_out : tile, n_mp, n_nb, group_m, mp, nb);
-                        const TileK tk = tile_k(ks, (int)(tile / n_out), n_k,
-                                                kChain && ks.count ? __ldg(ks.count + mp) : n_k2);
+                        const TileK tk = tile_k(ks, at_next.split, n_k, blocks_next);
                         nkb = tk.k1 - tk.k0 + tk.l1 - tk.l0;
+                        next_unknown = true;
                     }
                     for (int kb = 0; kb < nkb; ++kb, ++it) {
                         const uint32_t st = it % kPStages;
@@ -448,6 +519,13 @@ umma_gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_con
                             umma_bf16_pair(d, da, db, idesc, (kb | kk) != 0);
                         }
                         umma_commit_pair(&bars.empty[st]);   // frees the stage in both CTAs
+                        if constexpr (Ks::kSplit) {
+                            if (next_unknown && tile + n_pairs < n_tiles) {   // behind the first MMAs of this one
+                                at_next = split_tile(tile + n_pairs, n_tiles, n_out, n_mp, n_nb, group_m);
+                                if (kChain) blocks_next = listed_blocks(ks, at_next.mp, n_k2);
+                            }
+                            next_unknown = false;
+                        }
                     }
                     if (!ok) break;                          // a part of a tile is no tile
                     umma_commit_pair(&bars.acc_full[buf]);   // the accumulator (product) is complete
@@ -468,8 +546,15 @@ umma_gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_con
         uint32_t j = 0;
         bool ok = true;
         for (int64_t tile = pair; tile < n_tiles; tile += n_pairs, ++j) {
-            int mp, nb;
-            tile_coords(Ks::kSplit ? tile % n_out : tile, n_mp, n_nb, group_m, mp, nb);
+            int mp, nb, split = 0;
+            if constexpr (Ks::kSplit) {
+                const SplitTile t = split_tile(tile, n_tiles, n_out, n_mp, n_nb, group_m);
+                mp = t.mp;
+                nb = t.nb;
+                split = t.split;
+            } else {
+                tile_coords(tile, n_mp, n_nb, group_m, mp, nb);
+            }
             const int mb = 2 * mp + (int)rank;
             if constexpr (kDual) {
                 const int c0 = nb * kLBN + half * kDualEpiCols;
@@ -504,7 +589,7 @@ umma_gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_con
                     const int c0 = nb * kLBN + half * kWideEpiCols, ncol = min(kCols, Nn - c0);
                     const uint32_t acc = tmem + buf * kLBN + half * kWideEpiCols + lanes;
                     if (!kWide || ncol > 0) {
-                        if constexpr (Ks::kSplit) epi(mb * kLBM + r_in, c0, ncol, acc, (int)(tile / n_out));
+                        if constexpr (Ks::kSplit) epi(mb * kLBM + r_in, c0, ncol, acc, split);
                         else epi(mb * kLBM + r_in, c0, ncol, acc);
                     }
                 }
