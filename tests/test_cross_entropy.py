@@ -535,6 +535,27 @@ def test_another_stream_and_a_captured_step():
 
 
 @pytest.mark.gpu
+def test_two_streams_at_once():
+    a, b = (tuple(t.cuda() for t in model(200, 3000, 256, s)) for s in (46, 47))
+
+    def step(h, w, targets, g):
+        loss, st = vp.vp_linear_cross_entropy_fwd(h, w, targets, softcap=9.0)
+        dh, dw = vp.vp_linear_cross_entropy_bwd(h, w, targets, st, g, softcap=9.0)
+        return loss, dh, vp.vp_embedding_bwd(dh, targets, 3000, dW=dw, accumulate=True)
+
+    ref = step(*a), step(*b)
+    torch.cuda.synchronize()
+    streams = torch.cuda.Stream(), torch.cuda.Stream()
+    got = [[], []]
+    for _ in range(5):
+        for i, (stream, args) in enumerate(zip(streams, (a, b))):
+            with torch.cuda.stream(stream):
+                got[i].append(step(*args))
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, y) for i in (0, 1) for out in got[i] for x, y in zip(out, ref[i]))
+
+
+@pytest.mark.gpu
 def test_callers_buffers_and_nothing_behind_them():
     x, targets, g = (t.cuda() for t in rows(10, 5001, BF16, 43))
     loss, stats = torch.full((11,), 7.0, device="cuda"), torch.full((11, 8), 7.0, device="cuda")

@@ -7,8 +7,10 @@
 //   logit) and ce_join_kernel makes a row's records its loss. A single row is then spread
 //   over as many SMs as it has slices, and a row's arithmetic depends on V, its type and
 //   its address modulo 16 only.
-// Backward: slices of 1024 vectors, one read and one write; dx may be x.
-// Bound: DRAM bytes; with a cap on the logits the forward's issue slots.
+// Backward: slices of 1024 vectors (2048 with a cap), one read and one write; dx may be x.
+// Bound: DRAM bytes; with a cap on bf16 logits the issue slots, of which the cap takes some 6 a column.
+//   8192 x 75968 bf16, at 6.79 TB/s 183 and 367 us: forward 204, 213 to 225 with the sum that label smoothing asks
+//   for, backward 355; capped 335 and 434. 4096 x 75968 fp32: forward 181, backward 345.
 #include "vp_ce.cuh"
 
 namespace vp {

@@ -2,13 +2,16 @@
 // forward and backward on tcgen05 tensor cores (formulas: vp_ce.cuh; the GEMMs, their
 // order and their bounds: vp_gemm.cuh).
 //
-// Forward: tiles of 256 rows x 256 vocabulary rows; the epilogue reads a tile from TMEM, caps
-//   its logits, and leaves per row the tile's (max, sum of exponentials, sum of logits) and the
+// Forward: tiles of 256 rows x 256 vocabulary rows; eight epilogue warps read a tile from TMEM, cap its
+//   logits, and leave for each row and 128 columns (max, sum of exponentials, sum of logits) and the
 //   target's logit; ce_join_kernel makes them the row's loss. 2 N V D flops.
-// Backward, a piece of the vocabulary at a time: the piece's logits again, dz in the
-//   epilogue (through the cap's slope) as one or two bf16 values, then dhidden += dz . W_c and
-//   dW_c = dz^T . h. 6 N V D flops, 10 with dz as a pair.
-// Bound: the tensor cores, and the power they draw.
+// Backward, a piece of the vocabulary at a time: the piece's logits again, dz in the epilogue (through
+//   the cap's slope) as one or two bf16 values, then dhidden += dz . W_c and dW_c = dz^T . h. 6 N V D
+//   flops, 10 with dz as a pair everywhere, about 6.9 with a pair where it counts (the default).
+// Bound: the tensor cores, and the power they draw. 8192 x 75968 x 4096: forward 2.5 ms, backward 9.3 ms
+//   after a pause (1.9 and 1.6 PFLOP/s of the products that are made); 13.9 ms both, back to back under the
+//   power cap. Few rows: the bytes of W, read three times, and dW written (16 rows: 102, 107, 99 and 142 us, 92
+//   each at the copy rate). Short K (D of 512 and less): the epilogues' instructions.
 #include "vp_ce.cuh"
 #include "vp_gemm.cuh"
 #include "vp_stats.cuh"
@@ -129,7 +132,7 @@ __device__ __forceinline__ void store_rows(uint4 *stage, const uint4 (&v)[kVecs]
 constexpr float kPairShare = 1.f / 16.f;
 constexpr int kFlagRows = 32, kFlagCols = 64;
 
-// dz of a 256-column tile of the piece that starts at shard column v0, as bf16 (and, with
+// dz of 128 columns of a tile of the piece that starts at shard column v0, as bf16 (and, with
 // lo_off != 0, what that rounding took away as a second one).
 template <bool kCap>
 struct DzCeEpi {
@@ -349,6 +352,7 @@ struct SplitAccEpi {
         }
     }
 };
+
 // dW's tiles, rounded; ld is a multiple of 64.
 struct StoreRowsEpi {
     static constexpr bool kPdl = true, kWide = true;
@@ -402,7 +406,7 @@ static int64_t ce_piece(int64_t N, int64_t V) {
 }
 
 // Shares of dhidden's k-blocks: its output tiles are few where N and D are, and the GPU's pairs of SMs then
-// stand still. The waves of tiles that a split makes, counted in whole tiles, with 1 % of them for
+// stand still (1000 x 75968 x 2048, dz as a pair: 690 us with whole sums on 32 of 76 pairs, 340 with seven shares). The waves of tiles that a split makes, counted in whole tiles, with 1 % of them for
 // each share's sums, which are written and read once more.
 static int ce_splits(int64_t N, int64_t piece, int64_t D, int pairs) {
     const int64_t tiles = ((N + 255) / 256) * ((D + 255) / 256);
