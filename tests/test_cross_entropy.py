@@ -557,14 +557,15 @@ def test_two_streams_at_once():
 
 @pytest.mark.gpu
 def test_callers_buffers_and_nothing_behind_them():
-    x, targets, g = (t.cuda() for t in rows(10, 5001, BF16, 43))
+    x, targets, g = (t.cuda() for t in rows(10, 9001, F32, 43))
     loss, stats = torch.full((11,), 7.0, device="cuda"), torch.full((11, 8), 7.0, device="cuda")
-    work = torch.full((vp.vp_cross_entropy_workspace_size(10, 5001) + 64,), 99, dtype=torch.uint8, device="cuda")
+    need = vp.vp_cross_entropy_workspace_size(10, 9001)
+    work = torch.full((need + 64,), 99, dtype=torch.uint8, device="cuda")
     ref, rst = vp.vp_cross_entropy_fwd(x, targets, label_smoothing=0.1)
     vp.vp_cross_entropy_fwd(x, targets, label_smoothing=0.1, loss=loss[:10], stats=stats[:10], workspace=work[:-64])
     assert torch.equal(loss[:10], ref) and torch.equal(stats[:10], rst)
-    assert (loss[10:] == 7).all() and (stats[10:] == 7).all() and (work[-64:] == 99).all()
-    dx = torch.full((11, 5001), 7.0, dtype=BF16, device="cuda")
+    assert need and (loss[10:] == 7).all() and (stats[10:] == 7).all() and (work[-64:] == 99).all()
+    dx = torch.full((11, 9001), 7.0, device="cuda")
     vp.vp_cross_entropy_bwd(x, targets, stats[:10], g, label_smoothing=0.1, dx=dx[:10])
     assert (dx[10:] == 7).all()
     h, w, t, gg = (v.cuda() for v in model(20, 600, 64, 44))
@@ -590,7 +591,8 @@ FAKE, ODD = ctypes.c_void_p(0x100000), ctypes.c_void_p(0x100001)
 BIG = ctypes.c_size_t(1 << 40)
 
 
-def fwd(dtype=1, N=4, V=16, smooth=0.0, z=0.0, cap=0.0, targets=FAKE, loss=FAKE, stats=FAKE, work=FAKE, size=BIG):
+# wide enough to take a workspace: with one missing or short, nothing may be launched
+def fwd(dtype=1, N=4, V=20000, smooth=0.0, z=0.0, cap=0.0, targets=FAKE, loss=FAKE, stats=FAKE, work=FAKE, size=BIG):
     return _lib.lib().vp_cross_entropy_fwd(FAKE, dtype, N, V, 4, 0, V, 0, smooth, z, cap, targets, loss, stats, work, size,
                                            None, None)
 
@@ -609,8 +611,8 @@ def test_refusals_of_the_library():
         FAKE, 1, 4, 16, 4, 0, 16, 0, total, smooth, 0.0, 0.0, FAKE, FAKE, FAKE, dx, None, None)
     assert bwd(total=15) == ERR_SHAPE and bwd(dx=None) == ERR_NULL and bwd(dx=ODD) == ERR_ALIGN and bwd(smooth=2.0) == ERR_ARG
     part = lambda parts=FAKE, cap=0.0, work=FAKE: lib.vp_cross_entropy_partial(
-        FAKE, 1, 4, 16, 4, 0, 16, 0, cap, FAKE, parts, work, BIG, None)
-    assert part(parts=None) == ERR_NULL and part(parts=ODD) == ERR_ALIGN and part(cap=-1.0) == ERR_ARG
+        FAKE, 1, 4, 20000, 4, 0, 20000, 0, cap, FAKE, parts, work, BIG, None)
+    assert part(parts=None) == ERR_NULL and part(work=None) == ERR_NULL and part(parts=ODD) == ERR_ALIGN and part(cap=-1.0) == ERR_ARG
     merge = lambda K=2, smooth=0.0, loss=FAKE: lib.vp_cross_entropy_merge(FAKE, K, 4, smooth, 0.0, loss, FAKE, None, None)
     assert merge(K=0) == ERR_SHAPE and merge(smooth=-1.0) == ERR_ARG and merge(loss=None) == ERR_NULL
     lin = lambda D=64, loss=FAKE, work=FAKE, size=BIG, cap=0.0: lib.vp_linear_cross_entropy_fwd(

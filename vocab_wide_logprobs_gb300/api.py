@@ -990,7 +990,12 @@ def _bytes_arg(workspace, like):
 
 
 def _nbytes(workspace):
-    return workspace.numel() * workspace.element_size()
+    return 0 if workspace is None else workspace.numel() * workspace.element_size()
+
+
+def _needed(nbytes, like):
+    """A workspace, where the call takes one."""
+    return _workspace(nbytes, like) if nbytes else None
 
 
 def vp_cross_entropy_workspace_size(N: int, V: int) -> int:
@@ -1009,7 +1014,7 @@ def vp_cross_entropy_fwd(x, targets, label_smoothing: float = 0.0, z_loss: float
     loss = _f32(N, x) if loss is None else loss
     stats = rowstats(N, x.device) if stats is None else stats
     if workspace is None:
-        workspace = _workspace(_handle().vp_cross_entropy_workspace_size(N, V), x)
+        workspace = _needed(_handle().vp_cross_entropy_workspace_size(N, V), x)
     _check(_handle().vp_cross_entropy_fwd(_addr(x), code, N, V, R, s_o, s_i, vocab_start, label_smoothing, z_loss,
                                           softcap, _addr(targets), _addr(loss), _addr(stats), _addr(workspace),
                                           _nbytes(workspace), _addr(err_word), _queue(x.device)), "vp_cross_entropy_fwd")
@@ -1042,7 +1047,7 @@ def vp_cross_entropy_partial(x, targets, softcap: float = 0.0, vocab_start: int 
     _on_gpu(x)
     parts = partials(N, x.device) if parts is None else parts
     if workspace is None:
-        workspace = _workspace(_handle().vp_cross_entropy_workspace_size(N, V), x)
+        workspace = _needed(_handle().vp_cross_entropy_workspace_size(N, V), x)
     _check(_handle().vp_cross_entropy_partial(_addr(x), code, N, V, R, s_o, s_i, vocab_start, softcap, _addr(targets),
                                               _addr(parts), _addr(workspace), _nbytes(workspace), _queue(x.device)),
            "vp_cross_entropy_partial")
@@ -1179,10 +1184,8 @@ def vp_embedding_bwd(dy, ids, V: int, scale: float = 1.0, vocab_start: int = 0, 
     _on_gpu(dy)
     dW = torch.empty((V, D), dtype=dtype, device=dy.device) if dW is None else dW
     if workspace is None:
-        need = _handle().vp_embedding_bwd_workspace_size(N, V, D)
-        workspace = _workspace(need, dy) if need else None
+        workspace = _needed(_handle().vp_embedding_bwd_workspace_size(N, V, D), dy)
     _check(_handle().vp_embedding_bwd(_addr(dy), code, N, D, R, s_o, s_i, _addr(ids), V, vocab_start, int(sharded), scale,
-                                      _addr(dW), _DTYPES[dtype], int(accumulate), _addr(workspace),
-                                      0 if workspace is None else _nbytes(workspace), _addr(err_word), _queue(dy.device)),
-           "vp_embedding_bwd")
+                                      _addr(dW), _DTYPES[dtype], int(accumulate), _addr(workspace), _nbytes(workspace),
+                                      _addr(err_word), _queue(dy.device)), "vp_embedding_bwd")
     return dW

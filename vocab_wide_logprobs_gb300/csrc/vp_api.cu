@@ -872,11 +872,12 @@ vp_status vp_cross_entropy_fwd(const void *x, int dtype, int64_t N, int64_t V, i
     if (st != VP_OK) return st;
     if ((st = ce_options(label_smoothing, z_loss, softcap, V, 0, &opt)) != VP_OK) return st;
     if (N == 0) return VP_OK;
-    if (!x || !targets || !loss || !stats || !workspace) return VP_ERR_NULL;
+    const size_t need = vp_cross_entropy_workspace_size(N, V);
+    if (!x || !targets || !loss || !stats || (need && !workspace)) return VP_ERR_NULL;
     if (!aligned(x, elem_size(dtype)) || !aligned(targets, 8) || !aligned(loss, 4) || !aligned(stats, 16) ||
         !aligned(workspace, 8) || !aligned(err_word, 4))
         return VP_ERR_ALIGN;
-    if (workspace_bytes < vp_cross_entropy_workspace_size(N, V)) return VP_ERR_ARG;
+    if (workspace_bytes < need) return VP_ERR_ARG;
     if ((st = check_device()) != VP_OK) return st;
     vp::CeArgs a = ce_args(x, dtype, N, V, R, s_o, s_i, vocab_start, opt, targets, stream);
     a.loss = loss;
@@ -917,10 +918,11 @@ vp_status vp_cross_entropy_partial(const void *x, int dtype, int64_t N, int64_t 
     if (st != VP_OK) return st;
     if ((st = ce_options(0.0, 0.0, softcap, V, 0, &opt)) != VP_OK) return st;
     if (N == 0) return VP_OK;
-    if (!x || !targets || !parts || !workspace) return VP_ERR_NULL;
+    const size_t need = vp_cross_entropy_workspace_size(N, V);
+    if (!x || !targets || !parts || (need && !workspace)) return VP_ERR_NULL;
     if (!aligned(x, elem_size(dtype)) || !aligned(targets, 8) || !aligned(parts, 8) || !aligned(workspace, 8))
         return VP_ERR_ALIGN;
-    if (workspace_bytes < vp_cross_entropy_workspace_size(N, V)) return VP_ERR_ARG;
+    if (workspace_bytes < need) return VP_ERR_ARG;
     if ((st = check_device()) != VP_OK) return st;
     vp::CeArgs a = ce_args(x, dtype, N, V, R, s_o, s_i, vocab_start, opt, targets, stream);
     a.parts = parts;

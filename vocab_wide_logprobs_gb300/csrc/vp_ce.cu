@@ -25,8 +25,13 @@ static int64_t ce_slices(bool bf16, int vecs, int64_t V) {
     return (V + per - 1) / per;
 }
 
+// Few rows of one slice are finished where they are summed, the same way as in the join; of many the logarithms in 64
+// bits, one CTA's at a time, would cost more than a launch that takes 32 at once.
+static bool ce_whole(int64_t N, int n_slices) { return n_slices == 1 && N <= kCeFewRows; }
+
 int64_t ce_workspace_bytes(bool bf16, int64_t N, int64_t V) {
-    return N * ce_slices(bf16, kCeFwdVecs, V) * (int64_t)sizeof(CeSlice);
+    const int64_t n_slices = ce_slices(bf16, kCeFwdVecs, V);
+    return ce_whole(N, (int)n_slices) ? 0 : N * n_slices * (int64_t)sizeof(CeSlice);
 }
 
 // A tile's row and slice, and a row's offset, without 64-bit divisions where the sizes allow: a thread
@@ -326,9 +331,7 @@ static cudaError_t ce_fwd(const CeArgs &a) {
     const int64_t total = a.N * n_slices;
     const CeRules q = ce_rules(a.opt);
     CeSlice *work = static_cast<CeSlice *>(a.workspace);
-    // Rows of one slice are finished where they are summed, the same way, but for so many rows that the
-    // logarithms in 64 bits, one CTA's at a time, cost more than a launch that takes 32 at once.
-    const bool whole = n_slices == 1 && a.N <= kCeFewRows;
+    const bool whole = ce_whole(a.N, n_slices);
     auto go = [&](auto kernel) {
         return launch_pdl(kernel, dim3(ce_grid(total)), dim3(kCeThreads), 0, a.stream, static_cast<const T *>(a.x),
                           (int)a.V, Rows{a.R, a.s_o, a.s_i}, q, a.targets, a.vocab_start, n_slices, total, work,

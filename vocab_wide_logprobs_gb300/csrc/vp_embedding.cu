@@ -166,14 +166,15 @@ token_sort_kernel(const int64_t *__restrict__ ids, int64_t N, int V, int64_t voc
             for (int k = 0; k < kSortAhead; ++k) id[k] = q + k * 32 + lane < p1 ? ids[q + k * 32 + lane] : -1;
 #pragma unroll
             for (int k = 0; k < kSortAhead; ++k) {
+                // in the shard: no high half, and a low one below V (the loop's instructions are what the sort costs)
                 const int64_t local = id[k] - vocab_start;
-                const bool here = id[k] >= 0 && local >= 0 && local < V;
-                const uint32_t bin = here ? (uint32_t)local - lo : 0xffffffffu;
+                const bool here = id[k] >= 0 && (uint32_t)(local >> 32) == 0u && (uint32_t)local < (uint32_t)V;
+                const uint32_t bin = (uint32_t)local - lo;
                 if (count) {
-                    wrong |= id[k] >= 0 && !here;
-                    below += here && (uint32_t)local < lo;
+                    if (blockIdx.x == 0) wrong |= id[k] >= 0 && !here;
+                    if (here && (uint32_t)local < lo) ++below;
                 }
-                const uint32_t own = __ballot_sync(0xffffffffu, bin < (uint32_t)bins);
+                const uint32_t own = __ballot_sync(0xffffffffu, here && bin < (uint32_t)bins);
                 if (own) each(own, bin, q + k * 32 + lane);
             }
         }
