@@ -594,7 +594,10 @@ umma_gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_con
                     }
                 }
                 tc_fence_before();
-                mbar_arrive_cluster(cluster_addr(&bars.acc_empty[buf], 0));
+                // What the MMA warp waits for is that the accumulator has been read, which the loads' own waits have
+                // seen to. A release would hold the warp until its tile's stores are out as well: 1600 clocks a
+                // tile of dW from 16 rows, 142 us for its 75968 x 4096 against 96 without.
+                mbar_arrive_cluster_relaxed(cluster_addr(&bars.acc_empty[buf], 0));
             }
         }
     }

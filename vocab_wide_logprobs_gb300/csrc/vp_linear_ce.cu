@@ -10,7 +10,7 @@
 //   flops, 10 with dz as a pair everywhere, about 6.9 with a pair where it counts (the default).
 // Bound: the tensor cores, and the power they draw. 8192 x 75968 x 4096: forward 2.5 ms, backward 9.3 ms
 //   after a pause (1.9 and 1.6 PFLOP/s of the products that are made); 13.9 ms both, back to back under the
-//   power cap. Few rows: the bytes of W, read three times, and dW written (16 rows: 102, 107, 99 and 142 us, 92
+//   power cap. Few rows: the bytes of W, read three times, and dW written (16 rows: 102, 107, 99 and 96 us, 92
 //   each at the copy rate). Short K (D of 512 and less): the epilogues' instructions.
 #include "vp_ce.cuh"
 #include "vp_gemm.cuh"
@@ -95,7 +95,7 @@ struct CeEpi {
 
 // A warp's 32 rows of kVecs 16-byte vectors, row i in lane i, turned in shared memory so that kVecs lanes have a
 // row's vectors behind one another: use(row, vector, value). Straight from the lanes every store would touch half a
-// sector of each of 32 rows (dW of 75968 x 4096 from 16 tokens took 256 us, its bytes are 92; now 150). The
+// sector of each of 32 rows (dW of 75968 x 4096 from 16 tokens took 256 us so, 150 by whole lines; its bytes are 92). The
 // vectors' places are swapped by row so that neither side meets a bank twice.
 constexpr int kStageVecs = 32 * 8;                       // of each epilogue warp: 4 KB
 template <int kVecs, class Use>

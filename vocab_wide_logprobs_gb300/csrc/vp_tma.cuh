@@ -110,7 +110,8 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_bar) {
 
 // Arrival on an mbarrier of another CTA of the cluster, without a release
 // fence: for a "slot free" signal whose only prior accesses are shared-memory
-// reads whose values the caller has already consumed.
+// reads whose values the caller has already consumed, or tensor-memory loads
+// that it has waited for.
 __device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t cluster_bar) {
     asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
 }
