@@ -149,6 +149,36 @@ def test_gradient_runs(N, V, kind):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("N, D", [(600, 517), (600, 1032), (2600, 130), (2600, 2056), (30000, 13)])
+def test_gradient_of_long_runs(N, D):
+    """Runs over windows by the dozen, in narrow, wide and odd tables, beside short ones; warps of the sort that have more
+    tokens of one CTA than they note."""
+    V = 700
+    ids = make_ids(N, V, D)
+    ids[torch.rand(N, generator=torch.Generator().manual_seed(N)) < 0.4] = 7
+    ids[N // 3:N // 3 + N // 4] = 8
+    dy = rand(N, D, BF16)
+    check_grad(dy, ids, V, scale=0.7, dtype=F32)
+    check_grad(dy, ids, V, before=rand(V, D, BF16, 3))
+    whole = vp.vp_embedding_bwd(dy.cuda(), ids.cuda(), V)
+    assert torch.equal(whole, vp.vp_embedding_bwd(dy.cuda(), ids.cuda(), V))
+
+
+@pytest.mark.gpu
+def test_sorted_ids_of_every_size():
+    """Ids at the ends of 64 and of 32 bits, and shards that begin anywhere, in a batch that is sorted."""
+    N, V, D = 300, 77, 16
+    dy = rand(N, D, F32)
+    for start in (0, 5, 2 ** 32 - 30, 2 ** 62, 2 ** 63 - 1 - V):
+        ids = torch.full((N,), -1)
+        near = torch.arange(start - 40, min(start + V + 40, 2 ** 63 - 1))
+        ids[:len(near)] = near
+        ends = [-2 ** 63, -2 ** 63 + 1, -2, 0, 1, 2 ** 31, 2 ** 32, 2 ** 32 + 3, 2 ** 62, 2 ** 63 - 1]
+        ids[len(near):len(near) + len(ends)] = torch.tensor(ends)
+        check_grad(dy, ids, V, start=start, sharded=True)
+
+
+@pytest.mark.gpu
 def test_gradient_of_batches_and_views():
     V, D = 400, 136
     ids = make_ids(60, V, 3)

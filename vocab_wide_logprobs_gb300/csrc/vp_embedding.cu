@@ -7,10 +7,10 @@
 //   loads of a lane are on their way together. Bound: DRAM bytes (8192 rows of 4096, fp32 to bf16: 22 us; rows
 //   asked for again come from L2).
 // Backward of more than 128 tokens, three launches (up to there one: table_grad_few_kernel):
-//   1. token_sort_kernel: the tokens in the order of their ids (and of their positions
-//      among equal ids). Each CTA owns a range of ids, goes over all N ids and counts, notes and
+//   1. token_sort_kernel: the tokens of each id behind one another, in the order of their
+//      positions. Each CTA owns some of the ids, goes over all N and counts, notes and
 //      places its own: no CTA waits for another, no atomic decides an order. The ids come from
-//      L2, 8 bytes for each CTA and token against 2 D or 4 D of dy (8192 ids 8 us, 65536 20).
+//      L2, 8 bytes for each CTA and token against 2 D or 4 D of dy (8192 ids 8 us, 65536 19, 24 if skewed).
 //   2. table_grad_kernel: windows of the sorted tokens, each summed in fp32 in order; a
 //      run of one id that lies in a window is written at once, the ends of runs that cross
 //      windows are left as fp32 partial sums. More CTAs write zeros to rows no token asks for.
@@ -132,31 +132,50 @@ constexpr int kSortThreads = 1024, kSortWarps = kSortThreads / 32;
 constexpr int kSortMaxBins = 1024;               // ids of a CTA's range: a thread each in the scan, 128 KB of counters
 
 constexpr int kSortAhead = 8;                    // ids of a lane on their way at once
-constexpr int kStash = 256;                      // own tokens that a warp remembers for the second pass
+constexpr int kStash = 768;                      // own tokens that a warp remembers for the second pass, at most
 constexpr uint32_t kStashSpan = 1u << 22;        // and how long a stretch they can come from (10 + 22 bits)
 static_assert(kSortMaxBins <= 1 << 10, "a bin's 10 bits");
+static_assert(kSortWarps * (kSortMaxBins + kStash) * 4 <= 226 * 1024, "shared memory");
 
-// The tokens of the shard in the order of their ids: rows[k] and positions[k] of the k-th,
-// first[v] .. first[v + 1] those of row v. CTA b owns the rows from b * bins on. A warp places the
-// tokens of the stretch of positions that it has counted, so its counters, made offsets by the scan
-// (row by row, and warp by warp within a row), put them behind those of earlier stretches. While it
-// counts it notes its own tokens; only a warp with more of them than it can note reads its stretch again.
+// Quotients by d >= 2 of x < 2^31 without a division: the high half of x m, shifted by s, where 2^s < d <= 2^(s + 1)
+// and m = ceil(2^(32 + s) / d) < 2^32. m d exceeds 2^(32 + s) by less than d, so x m / 2^(32 + s) exceeds x / d by less than
+// x / 2^(32 + s) <= 1 / 2^(s + 1) <= 1 / d: too little to reach the next whole number.
+struct FastDiv {
+    uint32_t m, s, d;
+    explicit FastDiv(uint32_t by) : s(0), d(by) {
+        while (((uint64_t)2 << s) < by) ++s;
+        m = (uint32_t)((((uint64_t)1 << (32 + s)) + by - 1) / by);
+    }
+    __device__ __forceinline__ uint32_t div(uint32_t x) const { return __umulhi(x, m) >> s; }
+};
+
+// The tokens of the shard, those of one row behind one another in the order of their positions: rows[k] and
+// positions[k] of the k-th, spans[v].x .. spans[v].y - 1 those of row v. The rows go to the CTAs by turns, four neighbours at
+// once: frequent tokens often have neighbouring ids (the CTA of the 500 lowest had 43 % of the 65536 tokens of a skewed
+// batch and took 46 us, now 24), while neighbours written together are a little faster (one row at a time: 1 to 3 % of
+// the call). A warp places the tokens of the stretch of positions that it has counted, so its counters, made offsets by the
+// scan (row by row, and warp by warp within a row), put them behind those of earlier stretches. While it counts it notes
+// its own tokens; only a warp with more of them than it can note reads its stretch again (20 us of 65536 tokens).
+constexpr int kTurnBits = 2, kTurnRows = 1 << kTurnBits;
 __global__ void __launch_bounds__(kSortThreads)
 token_sort_kernel(const int64_t *__restrict__ ids, int64_t N, int V, int64_t vocab_start, bool sharded, int bins,
-                  int *__restrict__ first, int *__restrict__ rows, int *__restrict__ positions,
-                  int32_t *__restrict__ err) {
-    extern __shared__ uint32_t counts[];         // [kSortWarps][bins], then [kSortWarps][kStash]
+                  int stash_size, FastDiv by_ctas, int *__restrict__ n_tokens, int2 *__restrict__ spans, int *__restrict__ rows,
+                  int *__restrict__ positions, int32_t *__restrict__ err) {
+    extern __shared__ uint32_t counts[];         // [kSortWarps][bins], then [kSortWarps][stash_size]
     __shared__ uint32_t s_sum[kSortWarps];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     for (int i = tid; i < kSortWarps * bins; i += kSortThreads) counts[i] = 0u;
     __syncthreads();
     pdl_enter<false>();
-    const uint32_t lo = blockIdx.x * (uint32_t)bins;
     const int64_t stretch = ((N + kSortWarps - 1) / kSortWarps + 31) & ~(int64_t)31;
     const int64_t p0 = min(N, warp * stretch), p1 = min(N, p0 + stretch);
-    uint32_t *mine = counts + warp * bins, *stash = counts + kSortWarps * bins + warp * kStash;
+    uint32_t *mine = counts + warp * bins, *stash = counts + kSortWarps * bins + warp * stash_size;
+    const uint32_t n_stash = (uint32_t)stash_size;
     uint32_t below = 0, noted = 0;               // noted: the same in every lane
     bool wrong = false;
+    auto row_of = [](uint32_t bin) {             // of this CTA's
+        return ((int64_t)(bin >> kTurnBits) * gridDim.x + blockIdx.x) * kTurnRows + (bin & (kTurnRows - 1));
+    };
 
     // each(bin, position) of the warp's own tokens in the order of their positions, by whole warps
     auto scan_stretch = [&](auto each, bool count) {
@@ -169,12 +188,14 @@ token_sort_kernel(const int64_t *__restrict__ ids, int64_t N, int V, int64_t voc
                 // in the shard: no high half, and a low one below V (the loop's instructions are what the sort costs)
                 const int64_t local = id[k] - vocab_start;
                 const bool here = id[k] >= 0 && (uint32_t)(local >> 32) == 0u && (uint32_t)local < (uint32_t)V;
-                const uint32_t bin = (uint32_t)local - lo;
+                const uint32_t group = (uint32_t)local >> kTurnBits, turn = by_ctas.div(group);
+                const uint32_t bin = turn << kTurnBits | ((uint32_t)local & (kTurnRows - 1));
+                const int later = (int)(group - turn * by_ctas.d) - (int)blockIdx.x;   // CTAs from this one's
                 if (count) {
                     if (blockIdx.x == 0) wrong |= id[k] >= 0 && !here;
-                    if (here && (uint32_t)local < lo) ++below;
+                    if (here && later < 0) ++below;
                 }
-                const uint32_t own = __ballot_sync(0xffffffffu, here && bin < (uint32_t)bins);
+                const uint32_t own = __ballot_sync(0xffffffffu, here && later == 0);
                 if (own) each(own, bin, q + k * 32 + lane);
             }
         }
@@ -184,7 +205,7 @@ token_sort_kernel(const int64_t *__restrict__ ids, int64_t N, int V, int64_t voc
             if (own >> lane & 1) {
                 atomicAdd(&mine[bin], 1u);
                 const uint32_t at = noted + __popc(own & ((1u << lane) - 1u));
-                if (at < kStash) stash[at] = bin << 22 | ((uint32_t)(p - p0) & (kStashSpan - 1));
+                if (at < n_stash) stash[at] = bin << 22 | ((uint32_t)(p - p0) & (kStashSpan - 1));
             }
             noted += __popc(own);
         },
@@ -196,7 +217,7 @@ token_sort_kernel(const int64_t *__restrict__ ids, int64_t N, int V, int64_t voc
     uint32_t base = __reduce_add_sync(0xffffffffu, s_sum[lane]);
     __syncthreads();
 
-    // thread t has row lo + t: its tokens, then the offsets of its warps' counters
+    // thread t has the CTA's t-th row: its tokens, then the offsets of its warps' counters
     uint32_t n = 0;
     if (tid < bins)
         for (int w = 0; w < kSortWarps; ++w) n += counts[w * bins + tid];
@@ -210,10 +231,10 @@ token_sort_kernel(const int64_t *__restrict__ ids, int64_t N, int V, int64_t voc
     __syncthreads();
     const uint32_t sums = s_sum[lane];
     base += __reduce_add_sync(0xffffffffu, lane < warp ? sums : 0u) + scan - n;
+    if (tid == bins - 1 && blockIdx.x == gridDim.x - 1) *n_tokens = (int)(base + n);
     if (tid < bins) {
-        const int64_t row = (int64_t)lo + tid;
-        if (row <= V) first[row] = (int)base;
-        if (tid == bins - 1 && row + 1 >= V) first[V] = (int)(base + n);
+        const int64_t row = row_of((uint32_t)tid);
+        if (row < V) spans[row] = make_int2((int)base, (int)(base + n));
         for (int w = 0; w < kSortWarps; ++w) {
             const uint32_t c = counts[w * bins + tid];
             counts[w * bins + tid] = base;
@@ -231,12 +252,12 @@ token_sort_kernel(const int64_t *__restrict__ ids, int64_t N, int V, int64_t voc
         __syncwarp();
         if (is_own) {
             if (before == 0) mine[bin] += __popc(peers);
-            rows[at] = (int)(lo + bin);
+            rows[at] = (int)row_of(bin);
             positions[at] = (int)p;
         }
         __syncwarp();
     };
-    if (noted <= kStash && stretch <= (int64_t)kStashSpan) {
+    if (noted <= n_stash && stretch <= (int64_t)kStashSpan) {
         for (uint32_t i = 0; i < noted; i += 32) {
             const uint32_t e = i + lane < noted ? stash[i + lane] : 0u;
             place(__ballot_sync(0xffffffffu, i + lane < noted), e >> 22, p0 + (e & (kStashSpan - 1)));
@@ -255,8 +276,11 @@ struct TableGrad {
     int V, D, window, n_windows, col_blocks;
     Rows dy_rows;
     float scale;
-    const int *first, *rows, *positions;
-    int *until;                 // [n_windows]: the window where the run that begins in one and goes on ends, or 0
+    const int *n_tokens;        // of this shard
+    const int2 *spans;          // [V]: where a row's tokens begin and end
+    const int *rows, *positions;
+    int4 *runs;                 // [n_windows]: the run that goes on behind a window: its row, the window that it begins
+                                // in and the one that it ends in (0: none goes on)
     float *partial;             // [n_windows][2][D]: what belongs to a run begun in an earlier window, and
                                 // what belongs to one that goes on in later ones
 };
@@ -300,14 +324,14 @@ table_grad_kernel(const TI *__restrict__ dy, const TableGrad a, TO *__restrict__
     __shared__ bool s_asked[kFillMaxRows];
     const int tid = threadIdx.x, nt = blockDim.x;
     pdl_enter<false>();
-    const int total = a.first[a.V];              // tokens of this shard
+    const int total = *a.n_tokens;
     const int64_t b = blockIdx.x;
     const int64_t n_sum = (int64_t)a.n_windows * a.col_blocks;
     if (b >= n_sum) {
         // zeros for rows that no token asks for
         if constexpr (!kAdd) {
             const int64_t v0 = (b - n_sum) * fill_rows, v1 = min((int64_t)a.V, v0 + fill_rows);
-            for (int64_t v = v0 + tid; v < v1; v += nt) s_asked[v - v0] = a.first[v + 1] != a.first[v];
+            for (int64_t v = v0 + tid; v < v1; v += nt) s_asked[v - v0] = a.spans[v].x != a.spans[v].y;
             __syncthreads();
             fill_unasked(dW, a.D, v0, v1, s_asked, tid, nt);
         }
@@ -316,12 +340,13 @@ table_grad_kernel(const TI *__restrict__ dy, const TableGrad a, TO *__restrict__
     const int w = (int)(b / a.col_blocks), cb = (int)(b - (int64_t)w * a.col_blocks);
     const int64_t k0 = (int64_t)w * a.window, k1 = min((int64_t)total, k0 + a.window);
     if (cb == 0 && tid == 0) {
-        int until = 0;
+        int4 run = make_int4(0, 0, 0, 0);
         if (k1 < total && k0 < k1) {
-            const int row = a.rows[k1 - 1], end = a.first[row + 1];
-            if (a.first[row] >= k0 && end > k1) until = (end - 1) / a.window;
+            const int row = a.rows[k1 - 1];
+            const int2 span = a.spans[row];
+            if (span.y > k1) run = make_int4(row, span.x / a.window, (span.y - 1) / a.window, 0);
         }
-        a.until[w] = until;
+        a.runs[w] = run;
     }
     if (k0 >= k1) return;
     for (int i = tid; i < (int)(k1 - k0); i += nt) {
@@ -359,7 +384,8 @@ table_grad_kernel(const TI *__restrict__ dy, const TableGrad a, TO *__restrict__
             const int row = s_row[i + k];
             if (i + k + 1 < count && s_row[i + k + 1] == row) continue;
             // the run ends here, or the window does
-            const bool begun_before = a.first[row] < k0, goes_on = a.first[row + 1] > k1;
+            const int2 span = a.spans[row];
+            const bool begun_before = span.x < k0, goes_on = span.y > k1;
             if (begun_before || goes_on) {
                 float *part = a.partial + ((int64_t)w * 2 + (begun_before ? 0 : 1)) * a.D;
                 if (kVector) {
@@ -469,27 +495,24 @@ table_grad_few_kernel(const TI *__restrict__ dy, const TableGrad a, const int64_
     finish8<TO, kVector, kAdd>(dst, c, step, a.D, a.scale, sum, old);
 }
 
-// A CTA for each window and 512 columns, four each for a thread: where a run begins in the window and
-// goes on, four groups of threads add its partial sums, group j those of windows w + j, w + j + 4, ..;
-// then one adds the four.
-constexpr int kJoinThreads = 512, kJoinLanes = 128, kJoinGroups = kJoinThreads / kJoinLanes, kJoinAhead = 4;
-template <typename TO, bool kVector, bool kAdd>
-__global__ void __launch_bounds__(kJoinThreads)
-table_join_kernel(const TableGrad a, TO *__restrict__ dW) {
-    __shared__ DF s_sum[kJoinGroups][kJoinLanes][4];
-    pdl_enter<false>();
-    const int group = threadIdx.x / kJoinLanes, lane = threadIdx.x % kJoinLanes;
-    const int w = blockIdx.x, until = a.until[w];
-    if (until == 0) return;
-    const int row = a.rows[(int64_t)(w + 1) * a.window - 1];
-    for (int c0 = blockIdx.y * kJoinLanes * 4; c0 < a.D; c0 += gridDim.y * kJoinLanes * 4) {
-        const int c = kVector ? c0 + 4 * lane : c0 + lane, step = kVector ? 1 : kJoinLanes;
+// The partial sums of a run, by groups of threads, four columns each: group j adds those of its windows w + j,
+// w + j + groups, .., then a thread for each column adds the groups'. A run of a few windows is added by the CTAs of its first one, in four
+// groups, 512 columns a CTA; a longer one by those of all its windows, in sixteen, 128 columns a CTA (0.3 of 65536
+// tokens alike: 10 us; 42 where one window's CTAs added the run).
+constexpr int kJoinThreads = 512, kJoinAhead = 4, kJoinFew = 8;
+template <typename TO, bool kVector, bool kAdd, int kGroups>
+__device__ __forceinline__ void join_run(const TableGrad &a, TO *__restrict__ dW, const int4 &run, int slice, int slices,
+                                         DF (*s_sum)[4]) {
+    constexpr int kLanes = kJoinThreads / kGroups;
+    const int group = threadIdx.x / kLanes, lane = threadIdx.x % kLanes, w = run.y, until = run.z;
+    for (int c0 = slice * kLanes * 4; c0 < a.D; c0 += slices * kLanes * 4) {
+        const int c = kVector ? c0 + 4 * lane : c0 + lane, step = kVector ? 1 : kLanes;
         DF sum[4] = {};
-        for (int u0 = w + group; u0 <= until; u0 += kJoinGroups * kJoinAhead) {
+        for (int u0 = w + group; u0 <= until; u0 += kGroups * kJoinAhead) {
             float v[kJoinAhead][4];
 #pragma unroll
             for (int k = 0; k < kJoinAhead; ++k) {
-                const int u = u0 + k * kJoinGroups;
+                const int u = u0 + k * kGroups;
                 const float *part = a.partial + ((int64_t)u * 2 + (u == w ? 1 : 0)) * a.D + c;
                 if (kVector) {
                     const float4 f = u <= until && c < a.D ? *reinterpret_cast<const float4 *>(part) : make_float4(0.f, 0.f, 0.f, 0.f);
@@ -505,20 +528,32 @@ table_join_kernel(const TableGrad a, TO *__restrict__ dW) {
                 for (int e = 0; e < 4; ++e) df_add(sum[e], v[k][e]);
         }
 #pragma unroll
-        for (int e = 0; e < 4; ++e) s_sum[group][lane][e] = sum[e];
+        for (int e = 0; e < 4; ++e) s_sum[threadIdx.x][e] = sum[e];
         __syncthreads();
-        if (group == 0) {
+        // a thread for each column now
+        const int t = threadIdx.x, l = kVector ? t / 4 : t % kLanes, e = kVector ? t % 4 : t / kLanes;
+        if (t < kLanes * 4 && c0 + t < a.D) {
+            DF total = s_sum[l][e];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                if (c + e * step >= a.D) break;
-                for (int j = 1; j < kJoinGroups; ++j) df_add(sum[e], s_sum[j][lane][e]);
-                TO *dst = dW + row * (int64_t)a.D + c + e * step;
-                const float s = sum[e].hi + sum[e].lo;
-                Elem<TO>::store1(dst, kAdd ? fmaf(s, a.scale, (float)*dst) : s * a.scale);
-            }
+            for (int j = 1; j < kGroups; ++j) df_add(total, s_sum[j * kLanes + l][e]);
+            TO *dst = dW + run.x * (int64_t)a.D + c0 + t;
+            const float s = total.hi + total.lo;
+            Elem<TO>::store1(dst, kAdd ? fmaf(s, a.scale, (float)*dst) : s * a.scale);
         }
         __syncthreads();
     }
+}
+template <typename TO, bool kVector, bool kAdd>
+__global__ void __launch_bounds__(kJoinThreads, 3)
+table_join_kernel(const TableGrad a, TO *__restrict__ dW) {
+    __shared__ DF s_sum[kJoinThreads][4];
+    pdl_enter<false>();
+    const int w = blockIdx.x;
+    const int4 run = a.runs[w];
+    if (run.z - run.y >= kJoinFew)
+        join_run<TO, kVector, kAdd, 16>(a, dW, run, (w - run.y) * gridDim.y + blockIdx.y, (run.z - run.y) * gridDim.y, s_sum);
+    else if (run.z && w == run.y)
+        join_run<TO, kVector, kAdd, 4>(a, dW, run, blockIdx.y, gridDim.y, s_sum);
 }
 
 // ---------------------------------------------------------------------------
@@ -542,16 +577,17 @@ int grad_window(int64_t N) {
 }
 
 struct GradLayout {
-    size_t rows, positions, until, partial, total;
+    size_t n_tokens, rows, positions, runs, partial, total;
 };
 GradLayout grad_layout(int64_t N, int64_t V, int64_t D) {
     auto up = [](size_t x) { return (x + 255) & ~(size_t)255; };
     const int64_t windows = (N + grad_window(N) - 1) / grad_window(N);
-    GradLayout L;
-    L.rows = up((size_t)(V + 1) * 4);
+    GradLayout L;                                // the rows' spans first
+    L.n_tokens = up((size_t)V * sizeof(int2));
+    L.rows = L.n_tokens + 256;
     L.positions = L.rows + up((size_t)N * 4);
-    L.until = L.positions + up((size_t)N * 4);
-    L.partial = L.until + up((size_t)windows * 4);
+    L.runs = L.positions + up((size_t)N * 4);
+    L.partial = L.runs + up((size_t)windows * sizeof(int4));
     L.total = L.partial + (size_t)windows * 2 * D * 4;
     return L;
 }
@@ -603,13 +639,16 @@ cudaError_t embedding_bwd(const EmbeddingArgs &a) {
     }
     const GradLayout L = grad_layout(a.N, a.V, a.D);
     uint8_t *ws = static_cast<uint8_t *>(a.workspace);
-    int *first = reinterpret_cast<int *>(ws), *rows = reinterpret_cast<int *>(ws + L.rows),
+    int2 *spans = reinterpret_cast<int2 *>(ws);
+    int *n_tokens = reinterpret_cast<int *>(ws + L.n_tokens), *rows = reinterpret_cast<int *>(ws + L.rows),
         *positions = reinterpret_cast<int *>(ws + L.positions);
-    // rows of a CTA's range in the sort: the table over the SMs, within what the counters have room for
+    // rows of a CTA in the sort: the table over the SMs, within what the counters have room for
     const int sms = sm_count();
     int64_t bins = (a.V + sms - 1) / sms;
+    bins = (bins + kTurnRows - 1) / kTurnRows * kTurnRows;
     bins = bins < 32 ? 32 : bins > kSortMaxBins ? kSortMaxBins : bins;
-    const size_t smem = (size_t)kSortWarps * (bins + kStash) * 4;
+    const int stash = (int)std::min<int64_t>(kStash, (a.N + kSortWarps - 1) / kSortWarps + 31);
+    const size_t smem = (size_t)kSortWarps * (bins + stash) * 4;
     // the counters' room, asked for once on each device
     static std::atomic<uint64_t> attr_done{0};
     int dev = 0;
@@ -621,16 +660,18 @@ cudaError_t embedding_bwd(const EmbeddingArgs &a) {
         if (e != cudaSuccess) return e;
         attr_done.fetch_or(1ull << (dev & 63));
     }
-    e = launch_pdl(token_sort_kernel, dim3((unsigned)((a.V + bins - 1) / bins)), dim3(kSortThreads), smem, a.stream,
-                   a.ids, a.N, (int)a.V, a.vocab_start, a.sharded, (int)bins, first, rows, positions, a.err);
+    const unsigned sort_ctas = (unsigned)std::max<int64_t>(2, (a.V + bins - 1) / bins);
+    e = launch_pdl(token_sort_kernel, dim3(sort_ctas), dim3(kSortThreads), smem, a.stream, a.ids, a.N, (int)a.V,
+                   a.vocab_start, a.sharded, (int)bins, stash, FastDiv(sort_ctas), n_tokens, spans, rows, positions, a.err);
     if (e != cudaSuccess) return e;
 
     g.window = grad_window(a.N);
     g.n_windows = (int)((a.N + g.window - 1) / g.window);
-    g.first = first;
+    g.n_tokens = n_tokens;
+    g.spans = spans;
     g.rows = rows;
     g.positions = positions;
-    g.until = reinterpret_cast<int *>(ws + L.until);
+    g.runs = reinterpret_cast<int4 *>(ws + L.runs);
     g.partial = reinterpret_cast<float *>(ws + L.partial);
     const int64_t ctas = (int64_t)g.n_windows * g.col_blocks + fill_ctas;
     if (ctas > 2147483647) return cudaErrorInvalidValue;
@@ -640,7 +681,7 @@ cudaError_t embedding_bwd(const EmbeddingArgs &a) {
     e = vector ? (a.accumulate ? go(table_grad_kernel<TI, TO, true, true>) : go(table_grad_kernel<TI, TO, true, false>))
                : (a.accumulate ? go(table_grad_kernel<TI, TO, false, true>) : go(table_grad_kernel<TI, TO, false, false>));
     if (e != cudaSuccess || g.n_windows < 2) return e;
-    const int64_t blocks = (a.D + kJoinLanes * 4 - 1) / (kJoinLanes * 4);
+    const int64_t blocks = (a.D + kJoinThreads - 1) / kJoinThreads;
     auto join = [&](auto kernel) {
         return launch_pdl(kernel, dim3((unsigned)(g.n_windows - 1), (unsigned)std::min<int64_t>(blocks, 65535)),
                           dim3(kJoinThreads), 0, a.stream, g, dW);
