@@ -149,10 +149,10 @@ def test_gradient_runs(N, V, kind):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("N, D", [(600, 517), (600, 1032), (2600, 130), (2600, 2056), (30000, 13)])
+@pytest.mark.parametrize("N, D", [(600, 517), (600, 1032), (2600, 130), (2600, 2056), (30000, 13), (32767, 16), (32768, 16), (100001, 11)])
 def test_gradient_of_long_runs(N, D):
     """Runs over windows by the dozen, in narrow, wide and odd tables, beside short ones; warps of the sort that have more
-    tokens of one CTA than they note."""
+    tokens of one CTA than they note, batches just below and above those that are dealt out first."""
     V = 700
     ids = make_ids(N, V, D)
     ids[torch.rand(N, generator=torch.Generator().manual_seed(N)) < 0.4] = 7
@@ -165,9 +165,21 @@ def test_gradient_of_long_runs(N, D):
 
 
 @pytest.mark.gpu
-def test_sorted_ids_of_every_size():
+@pytest.mark.parametrize("V", [1, 5, 300, 131077, 1100000])
+def test_gradient_of_large_batches(V):
+    """Tables of fewer rows than the sort has CTAs, and of more than it can deal to: sums and order as of any other."""
+    N = 50000
+    ids, dy = make_ids(N, V, V, "flat"), rand(N, 8, BF16)
+    ids[::7] = V // 2
+    got = check_grad(dy, ids, V, dtype=F32)
+    assert torch.equal(got, vp.vp_embedding_bwd(dy.cuda(), ids.cuda(), V, dtype=F32))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("N", [300, 40000])
+def test_sorted_ids_of_every_size(N):
     """Ids at the ends of 64 and of 32 bits, and shards that begin anywhere, in a batch that is sorted."""
-    N, V, D = 300, 77, 16
+    V, D = 77, 16
     dy = rand(N, D, F32)
     for start in (0, 5, 2 ** 32 - 30, 2 ** 62, 2 ** 63 - 1 - V):
         ids = torch.full((N,), -1)
@@ -175,6 +187,7 @@ def test_sorted_ids_of_every_size():
         ids[:len(near)] = near
         ends = [-2 ** 63, -2 ** 63 + 1, -2, 0, 1, 2 ** 31, 2 ** 32, 2 ** 32 + 3, 2 ** 62, 2 ** 63 - 1]
         ids[len(near):len(near) + len(ends)] = torch.tensor(ends)
+        ids = ids[torch.randperm(N, generator=torch.Generator().manual_seed(N))]
         check_grad(dy, ids, V, start=start, sharded=True)
 
 

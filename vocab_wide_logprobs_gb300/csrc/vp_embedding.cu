@@ -6,11 +6,11 @@
 // Forward: a warp for a piece of 32 x 4 vectors of 8 columns of one row, so that the four
 //   loads of a lane are on their way together. Bound: DRAM bytes (8192 rows of 4096, fp32 to bf16: 22 us; rows
 //   asked for again come from L2).
-// Backward of more than 128 tokens, three launches (up to there one: table_grad_few_kernel):
+// Backward of more than 128 tokens, three or four launches (up to there one: table_grad_few_kernel):
 //   1. token_sort_kernel: the tokens of each id behind one another, in the order of their
 //      positions. Each CTA owns some of the ids, goes over all N and counts, notes and
-//      places its own: no CTA waits for another, no atomic decides an order. The ids come from
-//      L2, 8 bytes for each CTA and token against 2 D or 4 D of dy (8192 ids 8 us, 65536 19, 24 if skewed).
+//      places its own: no CTA waits for another, no atomic decides an order. From 32768 tokens on
+//      token_deal_kernel gives each CTA its own first (8192 ids 7 us, 65536 13, skewed ones 8 and 18).
 //   2. table_grad_kernel: windows of the sorted tokens, each summed in fp32 in order; a
 //      run of one id that lies in a window is written at once, the ends of runs that cross
 //      windows are left as fp32 partial sums. More CTAs write zeros to rows no token asks for.
@@ -131,7 +131,7 @@ embedding_fwd_kernel(const TI *__restrict__ table, int64_t pitch, int V, int D, 
 constexpr int kSortThreads = 1024, kSortWarps = kSortThreads / 32;
 constexpr int kSortMaxBins = 1024;               // ids of a CTA's range: a thread each in the scan, 128 KB of counters
 
-constexpr int kSortAhead = 8;                    // ids of a lane on their way at once
+constexpr int kSortAhead = 4;                    // ids of a lane on their way at once
 constexpr int kStash = 768;                      // own tokens that a warp remembers for the second pass, at most
 constexpr uint32_t kStashSpan = 1u << 22;        // and how long a stretch they can come from (10 + 22 bits)
 static_assert(kSortMaxBins <= 1 << 10, "a bin's 10 bits");
@@ -149,78 +149,34 @@ struct FastDiv {
     __device__ __forceinline__ uint32_t div(uint32_t x) const { return __umulhi(x, m) >> s; }
 };
 
-// The tokens of the shard, those of one row behind one another in the order of their positions: rows[k] and
-// positions[k] of the k-th, spans[v].x .. spans[v].y - 1 those of row v. The rows go to the CTAs by turns, four neighbours at
-// once: frequent tokens often have neighbouring ids (the CTA of the 500 lowest had 43 % of the 65536 tokens of a skewed
-// batch and took 46 us, now 24), while neighbours written together are a little faster (one row at a time: 1 to 3 % of
-// the call). A warp places the tokens of the stretch of positions that it has counted, so its counters, made offsets by the
-// scan (row by row, and warp by warp within a row), put them behind those of earlier stretches. While it counts it notes
-// its own tokens; only a warp with more of them than it can note reads its stretch again (20 us of 65536 tokens).
 constexpr int kTurnBits = 2, kTurnRows = 1 << kTurnBits;
-__global__ void __launch_bounds__(kSortThreads)
-token_sort_kernel(const int64_t *__restrict__ ids, int64_t N, int V, int64_t vocab_start, bool sharded, int bins,
-                  int stash_size, FastDiv by_ctas, int *__restrict__ n_tokens, int2 *__restrict__ spans, int *__restrict__ rows,
-                  int *__restrict__ positions, int32_t *__restrict__ err) {
-    extern __shared__ uint32_t counts[];         // [kSortWarps][bins], then [kSortWarps][stash_size]
-    __shared__ uint32_t s_sum[kSortWarps];
+// Where an id's row is: the CTA that owns it and its place there, or no row of the shard. The rows go to the CTAs by
+// turns, kTurnRows neighbours at once.
+struct Deal {
+    int64_t vocab_start;
+    int V;
+    FastDiv by_ctas;
+    __device__ __forceinline__ bool at(int64_t id, uint32_t &cta, uint32_t &bin) const {
+        const int64_t local = id - vocab_start;
+        const uint32_t group = (uint32_t)local >> kTurnBits, turn = by_ctas.div(group);
+        cta = group - turn * by_ctas.d;
+        bin = turn << kTurnBits | ((uint32_t)local & (kTurnRows - 1));
+        return id >= 0 && (uint32_t)(local >> 32) == 0u && (uint32_t)local < (uint32_t)V;   // no high half, a low one below V
+    }
+};
+
+// The warps' counters of thread t's column t < width, made offsets: of the column within all that `base` is in front of,
+// and within it warp by warp. begin and n: the column's own. By whole CTAs.
+struct Column {
+    uint32_t begin, n;
+};
+__device__ __forceinline__ Column column_offsets(uint32_t *counts, int width, uint32_t base, uint32_t *s_sum) {
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    for (int i = tid; i < kSortWarps * bins; i += kSortThreads) counts[i] = 0u;
-    __syncthreads();
-    pdl_enter<false>();
-    const int64_t stretch = ((N + kSortWarps - 1) / kSortWarps + 31) & ~(int64_t)31;
-    const int64_t p0 = min(N, warp * stretch), p1 = min(N, p0 + stretch);
-    uint32_t *mine = counts + warp * bins, *stash = counts + kSortWarps * bins + warp * stash_size;
-    const uint32_t n_stash = (uint32_t)stash_size;
-    uint32_t below = 0, noted = 0;               // noted: the same in every lane
-    bool wrong = false;
-    auto row_of = [](uint32_t bin) {             // of this CTA's
-        return ((int64_t)(bin >> kTurnBits) * gridDim.x + blockIdx.x) * kTurnRows + (bin & (kTurnRows - 1));
-    };
-
-    // each(bin, position) of the warp's own tokens in the order of their positions, by whole warps
-    auto scan_stretch = [&](auto each, bool count) {
-        for (int64_t q = p0; q < p1; q += 32 * kSortAhead) {
-            int64_t id[kSortAhead];
+    uint32_t c[kSortWarps], n = 0;
 #pragma unroll
-            for (int k = 0; k < kSortAhead; ++k) id[k] = q + k * 32 + lane < p1 ? ids[q + k * 32 + lane] : -1;
+    for (int w = 0; w < kSortWarps; ++w) c[w] = tid < width ? counts[w * width + tid] : 0u;
 #pragma unroll
-            for (int k = 0; k < kSortAhead; ++k) {
-                // in the shard: no high half, and a low one below V (the loop's instructions are what the sort costs)
-                const int64_t local = id[k] - vocab_start;
-                const bool here = id[k] >= 0 && (uint32_t)(local >> 32) == 0u && (uint32_t)local < (uint32_t)V;
-                const uint32_t group = (uint32_t)local >> kTurnBits, turn = by_ctas.div(group);
-                const uint32_t bin = turn << kTurnBits | ((uint32_t)local & (kTurnRows - 1));
-                const int later = (int)(group - turn * by_ctas.d) - (int)blockIdx.x;   // CTAs from this one's
-                if (count) {
-                    if (blockIdx.x == 0) wrong |= id[k] >= 0 && !here;
-                    if (here && later < 0) ++below;
-                }
-                const uint32_t own = __ballot_sync(0xffffffffu, here && later == 0);
-                if (own) each(own, bin, q + k * 32 + lane);
-            }
-        }
-    };
-    scan_stretch(
-        [&](uint32_t own, uint32_t bin, int64_t p) {
-            if (own >> lane & 1) {
-                atomicAdd(&mine[bin], 1u);
-                const uint32_t at = noted + __popc(own & ((1u << lane) - 1u));
-                if (at < n_stash) stash[at] = bin << 22 | ((uint32_t)(p - p0) & (kStashSpan - 1));
-            }
-            noted += __popc(own);
-        },
-        true);
-    if (wrong && !sharded && err && blockIdx.x == 0) atomicOr(err, VP_ERRBIT_TARGET_);
-    below = __reduce_add_sync(0xffffffffu, below);
-    if (lane == 0) s_sum[warp] = below;
-    __syncthreads();
-    uint32_t base = __reduce_add_sync(0xffffffffu, s_sum[lane]);
-    __syncthreads();
-
-    // thread t has the CTA's t-th row: its tokens, then the offsets of its warps' counters
-    uint32_t n = 0;
-    if (tid < bins)
-        for (int w = 0; w < kSortWarps; ++w) n += counts[w * bins + tid];
+    for (int w = 0; w < kSortWarps; ++w) n += c[w];
     uint32_t scan = n;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -231,19 +187,164 @@ token_sort_kernel(const int64_t *__restrict__ ids, int64_t N, int V, int64_t voc
     __syncthreads();
     const uint32_t sums = s_sum[lane];
     base += __reduce_add_sync(0xffffffffu, lane < warp ? sums : 0u) + scan - n;
-    if (tid == bins - 1 && blockIdx.x == gridDim.x - 1) *n_tokens = (int)(base + n);
-    if (tid < bins) {
-        const int64_t row = row_of((uint32_t)tid);
-        if (row < V) spans[row] = make_int2((int)base, (int)(base + n));
-        for (int w = 0; w < kSortWarps; ++w) {
-            const uint32_t c = counts[w * bins + tid];
-            counts[w * bins + tid] = base;
-            base += c;
-        }
+    const Column of{base, n};
+#pragma unroll
+    for (int w = 0; w < kSortWarps; ++w) {
+        if (tid < width) counts[w * width + tid] = base;
+        base += c[w];
     }
     __syncthreads();
+    return of;
+}
 
-    auto place = [&](uint32_t own, uint32_t bin, int64_t p) {
+// Many tokens: the ids of each slice of them dealt to their CTAs first, so that a CTA of the sort goes over its own
+// tokens alone. dealt[slice][..]: the slice's tokens by CTA and in order, their place at their CTA << 10 | their place in
+// the slice; starts[cta][slice]: where those of a CTA begin there (and, one further, end).
+constexpr int kSlice = kSortThreads;
+static_assert(kSlice <= 1 << 10, "a place's 10 bits");
+constexpr int kDealMaxCtas = kSortThreads;
+__global__ void __launch_bounds__(kSortThreads)
+token_deal_kernel(const int64_t *__restrict__ ids, int64_t N, Deal deal, bool sharded, uint32_t *__restrict__ dealt,
+                  uint16_t *__restrict__ starts, int32_t *__restrict__ err) {
+    extern __shared__ uint32_t counts[];         // [kSortWarps][CTAs of the sort]
+    __shared__ uint32_t s_sum[kSortWarps];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, width = (int)deal.by_ctas.d;
+    for (int i = tid; i < kSortWarps * width; i += kSortThreads) counts[i] = 0u;
+    __syncthreads();
+    pdl_enter<true>();
+    const int64_t slice = blockIdx.x, p = slice * kSlice + tid;
+    const int64_t id = p < N ? ids[p] : -1;
+    uint32_t cta, bin;
+    const bool here = deal.at(id, cta, bin);
+    if (id >= 0 && !here && !sharded && err) atomicOr(err, VP_ERRBIT_TARGET_);
+    const uint32_t peers = __match_any_sync(0xffffffffu, here ? cta : 0xffffffffu);
+    const uint32_t before = __popc(peers & ((1u << lane) - 1u));
+    if (here && before == 0) counts[warp * width + cta] = __popc(peers);
+    __syncthreads();
+    const Column of = column_offsets(counts, width, 0u, s_sum);
+    if (tid < width) starts[(int64_t)tid * gridDim.x + slice] = (uint16_t)of.begin;
+    if (tid == width - 1) starts[(int64_t)width * gridDim.x + slice] = (uint16_t)(of.begin + of.n);
+    if (here) dealt[slice * kSlice + counts[warp * width + cta] + before] = bin << 10 | (uint32_t)tid;
+}
+
+// The tokens of the shard, those of one row behind one another in the order of their positions: rows[k] and
+// positions[k] of the k-th, spans[v].x .. spans[v].y - 1 those of row v. Rows are dealt to the CTAs, since frequent tokens
+// often have neighbouring ids (with a range of ids for a CTA, that of the 500 lowest had 43 % of the 65536 tokens of a
+// skewed batch and took 46 us); neighbours written together are a little faster than one row at a time (1 to 3 % of the call).
+// A warp places the tokens of the stretch of positions that it has counted, so its counters, made offsets (row by
+// row, and warp by warp within a row), put them behind those of earlier stretches. While it counts it notes its own
+// tokens; only a warp with more of them than it can note reads its stretch again.
+// kDealt: of what token_deal_kernel has left. Otherwise every CTA goes over all ids, and the loop's instructions are what
+// that costs (13 of 19 us of 65536 tokens).
+template <bool kDealt>
+__global__ void __launch_bounds__(kSortThreads)
+token_sort_kernel(const int64_t *__restrict__ ids, int64_t N, Deal deal, bool sharded, int bins, int stash_size,
+                  const uint32_t *__restrict__ dealt, const uint16_t *__restrict__ starts, int *__restrict__ n_tokens,
+                  int2 *__restrict__ spans, int *__restrict__ rows, int *__restrict__ positions,
+                  int32_t *__restrict__ err) {
+    extern __shared__ uint32_t counts[];         // [kSortWarps][bins], then [kSortWarps][stash_size]
+    __shared__ uint32_t s_sum[kSortWarps];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    for (int i = tid; i < kSortWarps * bins; i += kSortThreads) counts[i] = 0u;
+    __syncthreads();
+    pdl_enter<false>();
+    const int64_t unit = kDealt ? kSlice : 32, units = (N + unit - 1) / unit;
+    const int64_t stretch = (units + kSortWarps - 1) / kSortWarps * unit;
+    const int64_t p0 = min(N, warp * stretch), p1 = min(N, p0 + stretch);
+    uint32_t *mine = counts + warp * bins, *stash = counts + kSortWarps * bins + warp * stash_size;
+    const uint32_t n_stash = (uint32_t)stash_size;
+    uint32_t below = 0, noted = 0;               // noted: the same in every lane
+    bool wrong = false;
+    auto row_of = [](uint32_t bin) {             // of this CTA's
+        return ((int64_t)(bin >> kTurnBits) * gridDim.x + blockIdx.x) * kTurnRows + (bin & (kTurnRows - 1));
+    };
+
+    // each(which lanes, bin, place in the stretch) of the warp's own tokens in the order of their positions, by whole
+    // warps; loads are on their way while those before are looked at
+    auto scan_stretch = [&](auto each, bool count) {
+        if constexpr (kDealt) {
+            const int s0 = (int)min(units, warp * (stretch / kSlice)), s1 = (int)min(units, s0 + stretch / kSlice);
+            for (int sb = s0; sb < s1; sb += 32) {
+                const int64_t at = (int64_t)blockIdx.x * units + sb + lane;
+                const uint32_t begin = sb + lane < s1 ? starts[at] : 0u, end = sb + lane < s1 ? starts[at + units] : 0u;
+                if (count) below += begin;
+                for (int j = 0; j < min(32, s1 - sb); j += kSortAhead) {
+                    uint32_t from[kSortAhead], len[kSortAhead], x[kSortAhead];
+#pragma unroll
+                    for (int k = 0; k < kSortAhead; ++k) {
+                        from[k] = __shfl_sync(0xffffffffu, begin, j + k);
+                        len[k] = __shfl_sync(0xffffffffu, end, j + k) - from[k];
+                        x[k] = lane < len[k] ? dealt[(int64_t)(sb + j + k) * kSlice + from[k] + lane] : 0u;
+                    }
+#pragma unroll
+                    for (int k = 0; k < kSortAhead; ++k) {
+                        const uint32_t *rest = dealt + (int64_t)(sb + j + k) * kSlice + from[k] + lane;
+                        const int at_slice = (sb + j + k - s0) * kSlice;
+                        auto look = [&](uint32_t i, uint32_t y) {
+                            if (i >= len[k]) return;
+                            each(__ballot_sync(0xffffffffu, i + lane < len[k]), y >> 10, at_slice + (int)(y & (kSlice - 1)));
+                        };
+                        look(0, x[k]);
+                        for (uint32_t i = 32; i < len[k]; i += 32 * kSortAhead) {      // a frequent token's CTA
+                            uint32_t y[kSortAhead];
+#pragma unroll
+                            for (int m = 0; m < kSortAhead; ++m) y[m] = i + m * 32 + lane < len[k] ? rest[i + m * 32] : 0u;
+#pragma unroll
+                            for (int m = 0; m < kSortAhead; ++m) look(i + m * 32, y[m]);
+                        }
+                    }
+                }
+            }
+        } else {
+            const int n = (int)(p1 - p0);
+            const int64_t *from = ids + p0 + lane;
+            int64_t id[kSortAhead], next[kSortAhead];
+            auto load = [&](int q) {
+#pragma unroll
+                for (int k = 0; k < kSortAhead; ++k) next[k] = q + k * 32 + lane < n ? from[q + k * 32] : -1;
+            };
+            load(0);
+            for (int q = 0; q < n; q += 32 * kSortAhead) {
+#pragma unroll
+                for (int k = 0; k < kSortAhead; ++k) id[k] = next[k];
+                load(q + 32 * kSortAhead);
+#pragma unroll
+                for (int k = 0; k < kSortAhead; ++k) {
+                    uint32_t cta, bin;
+                    const bool here = deal.at(id[k], cta, bin);
+                    if (count) {
+                        if (blockIdx.x == 0) wrong |= id[k] >= 0 && !here;
+                        if (here && cta < blockIdx.x) ++below;
+                    }
+                    const uint32_t own = __ballot_sync(0xffffffffu, here && cta == blockIdx.x);
+                    if (own) each(own, bin, q + k * 32 + lane);
+                }
+            }
+        }
+    };
+    scan_stretch(
+        [&](uint32_t own, uint32_t bin, int at_stretch) {
+            if (own >> lane & 1) {
+                atomicAdd(&mine[bin], 1u);
+                const uint32_t at = noted + __popc(own & ((1u << lane) - 1u));
+                if (at < n_stash) stash[at] = bin << 22 | ((uint32_t)at_stretch & (kStashSpan - 1));
+            }
+            noted += __popc(own);
+        },
+        true);
+    if (wrong && !sharded && err) atomicOr(err, VP_ERRBIT_TARGET_);
+    below = __reduce_add_sync(0xffffffffu, below);
+    if (lane == 0) s_sum[warp] = below;
+    __syncthreads();
+    const uint32_t base = __reduce_add_sync(0xffffffffu, s_sum[lane]);
+    __syncthreads();
+
+    // thread t has the CTA's t-th row
+    const Column of = column_offsets(counts, bins, base, s_sum);
+    if (tid == bins - 1 && blockIdx.x == gridDim.x - 1) *n_tokens = (int)(of.begin + of.n);
+    if (tid < bins && row_of((uint32_t)tid) < deal.V) spans[row_of((uint32_t)tid)] = make_int2((int)of.begin, (int)(of.begin + of.n));
+
+    auto place = [&](uint32_t own, uint32_t bin, int at_stretch) {
         const bool is_own = own >> lane & 1;
         const uint32_t peers = __match_any_sync(0xffffffffu, is_own ? bin : 0xffffffffu);
         const uint32_t before = __popc(peers & ((1u << lane) - 1u));
@@ -253,14 +354,14 @@ token_sort_kernel(const int64_t *__restrict__ ids, int64_t N, int V, int64_t voc
         if (is_own) {
             if (before == 0) mine[bin] += __popc(peers);
             rows[at] = (int)row_of(bin);
-            positions[at] = (int)p;
+            positions[at] = (int)p0 + at_stretch;
         }
         __syncwarp();
     };
     if (noted <= n_stash && stretch <= (int64_t)kStashSpan) {
         for (uint32_t i = 0; i < noted; i += 32) {
             const uint32_t e = i + lane < noted ? stash[i + lane] : 0u;
-            place(__ballot_sync(0xffffffffu, i + lane < noted), e >> 22, p0 + (e & (kStashSpan - 1)));
+            place(__ballot_sync(0xffffffffu, i + lane < noted), e >> 22, (int)(e & (kStashSpan - 1)));
         }
     } else {
         scan_stretch(place, false);
@@ -576,8 +677,13 @@ int grad_window(int64_t N) {
     return w;
 }
 
+// From how many tokens on they are dealt first (75968 rows; even ids to 0.3 of one id): of 262144, 10 us for that and 11 to 47
+// for the sort, against 58 to 145 by the sort alone; of 65536, 6 and 7 to 15 against 19 to 25; of 16384, 6 and 7 to 10 against
+// 9 to 11.
+constexpr int64_t kDealTokens = 32768;
+
 struct GradLayout {
-    size_t n_tokens, rows, positions, runs, partial, total;
+    size_t n_tokens, rows, positions, runs, dealt, starts, partial, total;
 };
 GradLayout grad_layout(int64_t N, int64_t V, int64_t D) {
     auto up = [](size_t x) { return (x + 255) & ~(size_t)255; };
@@ -587,7 +693,10 @@ GradLayout grad_layout(int64_t N, int64_t V, int64_t D) {
     L.rows = L.n_tokens + 256;
     L.positions = L.rows + up((size_t)N * 4);
     L.runs = L.positions + up((size_t)N * 4);
-    L.partial = L.runs + up((size_t)windows * sizeof(int4));
+    L.dealt = L.runs + up((size_t)windows * sizeof(int4));
+    const size_t slices = N >= kDealTokens ? (size_t)(N + kSlice - 1) / kSlice : 0;
+    L.starts = L.dealt + slices * kSlice * 4;
+    L.partial = L.starts + up(slices * (kDealMaxCtas + 1) * 2);
     L.total = L.partial + (size_t)windows * 2 * D * 4;
     return L;
 }
@@ -647,22 +756,40 @@ cudaError_t embedding_bwd(const EmbeddingArgs &a) {
     int64_t bins = (a.V + sms - 1) / sms;
     bins = (bins + kTurnRows - 1) / kTurnRows * kTurnRows;
     bins = bins < 32 ? 32 : bins > kSortMaxBins ? kSortMaxBins : bins;
-    const int stash = (int)std::min<int64_t>(kStash, (a.N + kSortWarps - 1) / kSortWarps + 31);
-    const size_t smem = (size_t)kSortWarps * (bins + stash) * 4;
     // the counters' room, asked for once on each device
     static std::atomic<uint64_t> attr_done{0};
     int dev = 0;
     cudaGetDevice(&dev);
     cudaError_t e;
     if (!(attr_done.load() & (1ull << (dev & 63)))) {
-        e = cudaFuncSetAttribute(token_sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 kSortWarps * (kSortMaxBins + kStash) * 4);
-        if (e != cudaSuccess) return e;
+        constexpr int most = kSortWarps * (kSortMaxBins + kStash) * 4;
+        if ((e = cudaFuncSetAttribute(token_sort_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, most)) != cudaSuccess ||
+            (e = cudaFuncSetAttribute(token_sort_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, most)) != cudaSuccess ||
+            (e = cudaFuncSetAttribute(token_deal_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                      kSortWarps * kDealMaxCtas * 4)) != cudaSuccess)
+            return e;
         attr_done.fetch_or(1ull << (dev & 63));
     }
     const unsigned sort_ctas = (unsigned)std::max<int64_t>(2, (a.V + bins - 1) / bins);
-    e = launch_pdl(token_sort_kernel, dim3(sort_ctas), dim3(kSortThreads), smem, a.stream, a.ids, a.N, (int)a.V,
-                   a.vocab_start, a.sharded, (int)bins, stash, FastDiv(sort_ctas), n_tokens, spans, rows, positions, a.err);
+    const bool deal_first = a.N >= kDealTokens && sort_ctas <= kDealMaxCtas;
+    // a warp notes its whole stretch, where that is short
+    const int64_t unit = deal_first ? kSlice : 32, stretch = ((a.N + unit - 1) / unit + kSortWarps - 1) / kSortWarps * unit;
+    const int stash = (int)std::min<int64_t>(kStash, stretch);
+    const size_t smem = (size_t)kSortWarps * (bins + stash) * 4;
+    const Deal deal{a.vocab_start, (int)a.V, FastDiv(sort_ctas)};
+    uint32_t *dealt = reinterpret_cast<uint32_t *>(ws + L.dealt);
+    uint16_t *starts = reinterpret_cast<uint16_t *>(ws + L.starts);
+    auto sort = [&](auto kernel) {
+        return launch_pdl(kernel, dim3(sort_ctas), dim3(kSortThreads), smem, a.stream, a.ids, a.N, deal, a.sharded, (int)bins,
+                          stash, dealt, starts, n_tokens, spans, rows, positions, a.err);
+    };
+    if (deal_first) {
+        e = launch_pdl(token_deal_kernel, dim3((unsigned)((a.N + kSlice - 1) / kSlice)), dim3(kSortThreads),
+                       (size_t)kSortWarps * sort_ctas * 4, a.stream, a.ids, a.N, deal, a.sharded, dealt, starts, a.err);
+        if (e == cudaSuccess) e = sort(token_sort_kernel<true>);
+    } else {
+        e = sort(token_sort_kernel<false>);
+    }
     if (e != cudaSuccess) return e;
 
     g.window = grad_window(a.N);
