@@ -195,6 +195,41 @@ def test_logits_where_rows_begin(dtype):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("vectors", [128, 512, 1024])
+def test_logits_at_the_ends_of_row_sizes(vectors, dtype):
+    """Rows that just fill the threads of one, two and four warps, and rows of a column more; few rows and many."""
+    full = vectors * (8 if dtype == BF16 else 4)
+    for V in (full - 1, full, full + 1):
+        for N in (3, 700):
+            x, targets, g = rows(N, V, dtype, V + N)
+            check_logits(x, targets, g, dict(cap=9.0, smooth=0.2) if V == full else dict(zeta=1e-3))
+    x, targets, g = rows(9, full, dtype, full)
+    for offset in (1, 6):
+        room = torch.full((offset + 9 * (full + 3),), math.nan, dtype=dtype, device="cuda")
+        view = room[offset:].view(9, full + 3)[:, :full]
+        view.copy_(x)
+        check_logits(x, targets, g, dict(smooth=0.1), xg=view)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_logits_of_many_short_rows(dtype):
+    """More rows than CTAs run at once, with rows to ignore among them; each as in a batch of its own, where it lies as it
+    does in the large one (a row's sums depend on its address modulo 16 bytes)."""
+    N, V = 11000, 70
+    x, targets, g = rows(N, V, dtype, 23, sigma=8.0)
+    xg = x.cuda()
+    loss, stats, dx = check_logits(x, targets, g, dict(smooth=0.1, zeta=1e-3), xg=xg)
+    o = dict(label_smoothing=0.1, z_loss=1e-3)
+    for i in (0, 4863, 4864, N - 5):
+        k = slice(i, i + 5)
+        one, st = vp.vp_cross_entropy_fwd(xg[k], targets[k].cuda(), **o)
+        assert torch.equal(one, loss[k]) and torch.equal(st.nan_to_num(7), stats[k].nan_to_num(7))
+        assert torch.equal(vp.vp_cross_entropy_bwd(xg[k], targets[k].cuda(), st, g[k].cuda(), **o), dx[k])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [F32, BF16])
 @pytest.mark.parametrize("fill", ["inf", "lowest"])
 def test_masked_columns(dtype, fill):
     x, targets, g = rows(8, 9001, dtype, 11)

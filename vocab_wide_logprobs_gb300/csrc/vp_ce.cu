@@ -1,7 +1,7 @@
 // vp_ce.cu -- softmax cross entropy of logits, forward and backward (formulas: vp_ce.cuh).
 //
 // Forward: one CTA for a slice of 2048 16-byte vectors of a row (16384 bf16 or 8192 fp32
-//   logits), read once into registers, eight loads of a thread on their way together. The
+//   logits; smaller CTAs for rows that they hold), read once into registers, eight loads of a thread on their way together. The
 //   slice's maximum is known before its first exponential, so nothing is rescaled; the
 //   CTA leaves a record (max, sum of exponentials, sum of centred logits, the target's
 //   logit) and ce_join_kernel makes a row's records its loss. A single row is then spread
@@ -11,17 +11,27 @@
 // Bound: DRAM bytes; with a cap on bf16 logits the issue slots, of which the cap takes some 6 a column.
 //   8192 x 75968 bf16, at 6.79 TB/s 183 and 367 us: forward 204, 213 to 225 with the sum that label smoothing asks
 //   for, backward 355; capped 335 and 434. 4096 x 75968 fp32: forward 181, backward 345.
+#include <algorithm>
+
 #include "vp_ce.cuh"
 
 namespace vp {
 
 constexpr int kCeThreads = 256;
 constexpr int kCeFwdVecs = 8;                    // vectors of a thread
+// Threads of a CTA: fewer for a row that they can hold, so that more rows are on their way on an SM than four. The
+// number depends on V alone, as the order of a row's sums does. Forward and backward against 256 threads, in us: 65536 x 256
+// bf16 43 + 22 against 212 + 120, 65536 x 2048 83 + 78 against 237 + 144, 65536 x 4096 fp32 168 + 302 against 245 + 301,
+// 16384 x 4100 bf16 40 + 46 against 66 + 49; few rows of 250 vectors, whose threads then have four, 6.7 against 5.4.
+static int ce_threads(bool bf16, int64_t V) {
+    const int64_t most = (V + (bf16 ? 7 : 3)) / (bf16 ? 8 : 4);       // vectors
+    return most <= 128 ? 32 : most <= 64 * kCeFwdVecs ? 64 : most <= 128 * kCeFwdVecs ? 128 : kCeThreads;
+}
 constexpr int64_t kCeFewRows = 608;              // four for each SM
 constexpr int ce_grad_vecs(bool cap) { return cap ? 8 : 4; }
 
 static int64_t ce_slices(bool bf16, int vecs, int64_t V) {
-    const int64_t per = (int64_t)kCeThreads * vecs * (bf16 ? 8 : 4);
+    const int64_t per = (int64_t)ce_threads(bf16, V) * vecs * (bf16 ? 8 : 4);
     return (V + per - 1) / per;
 }
 
@@ -80,12 +90,12 @@ __device__ __forceinline__ float vec_max(const uint4 &u, float m) {
 
 // kSum: with the sum of the centred logits, which only label smoothing asks for. kWhole: rows of one slice, finished
 // here (a kernel of its own: the 64-bit logarithm would take registers from the sums).
-template <typename T, bool kCap, bool kSum, bool kWhole>
-__global__ void __launch_bounds__(kCeThreads, 4)
+template <typename T, bool kCap, bool kSum, bool kWhole, int kThreads>
+__global__ void __launch_bounds__(kThreads, 1024 / kThreads)
 ce_fwd_kernel(const T *__restrict__ x, int V, Rows rows, const CeRules q, const int64_t *__restrict__ targets,
               int64_t vocab_start, int n_slices, int64_t total, CeSlice *__restrict__ slices,
               const CeJoinArgs join) {
-    constexpr int kVec = Elem<T>::kVec, kWarps = kCeThreads / 32, kCeVecs = kCeFwdVecs, kCeSliceVecs = kCeThreads * kCeVecs;
+    constexpr int kVec = Elem<T>::kVec, kWarps = kThreads / 32, kCeVecs = kCeFwdVecs, kCeSliceVecs = kThreads * kCeVecs;
     __shared__ float s_max[kWarps];
     __shared__ DF s_S[kWarps], s_W[kWarps];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -99,7 +109,7 @@ ce_fwd_kernel(const T *__restrict__ x, int V, Rows rows, const CeRules q, const 
         uint4 u[kCeVecs];
 #pragma unroll
         for (int k = 0; k < kCeVecs; ++k) {
-            const int i = v0 + tid + k * kCeThreads;
+            const int i = v0 + tid + k * kThreads;
             if (i < v1) u[k] = ldg_stream(reinterpret_cast<const uint4 *>(in + head) + i);
         }
         // the first slice also takes the elements before the first vector and behind the last
@@ -120,7 +130,7 @@ ce_fwd_kernel(const T *__restrict__ x, int V, Rows rows, const CeRules q, const 
         float m = kNegBig;
 #pragma unroll
         for (int k = 0; k < kCeVecs; ++k)
-            if (v0 + tid + k * kCeThreads < v1) m = vec_max<T>(u[k], m);
+            if (v0 + tid + k * kThreads < v1) m = vec_max<T>(u[k], m);
         if (tid < extra) m = fmaxf(m, ze);
         m = warp_max(m);
         if (lane == 0) s_max[warp] = m;
@@ -134,7 +144,7 @@ ce_fwd_kernel(const T *__restrict__ x, int V, Rows rows, const CeRules q, const 
         const float2 mw = f2(-m * kCeScale);
 #pragma unroll
         for (int k = 0; k < kCeVecs; ++k) {
-            if (v0 + tid + k * kCeThreads < v1) {
+            if (v0 + tid + k * kThreads < v1) {
                 float z[kVec];
                 Elem<T>::unpack(u[k], z);
                 if (kCap) soft_cap(q, z);
@@ -220,12 +230,12 @@ __device__ __forceinline__ float load_own1(const float *p) { return *p; }
 __device__ __forceinline__ float load_own1(const __nv_bfloat16 *p) { return __bfloat162float(*p); }
 
 // kSame: every row of the input lies as its row of the output modulo 16 bytes
-template <typename T, bool kCap, bool kSame>
-__global__ void __launch_bounds__(kCeThreads, kCap ? 4 : 5)
+template <typename T, bool kCap, bool kSame, int kThreads>
+__global__ void __launch_bounds__(kThreads, kThreads == 32 ? 32 : (kCap ? 4 : 5) * (kCeThreads / kThreads))
 ce_grad_kernel(const T *x, int V, Rows rows, const CeRules q, const RowStat *__restrict__ stats,
                const float *__restrict__ g_in, const int64_t *__restrict__ targets, int64_t vocab_start, T *dx,
                int32_t *__restrict__ err, int n_slices, int64_t total) {
-    constexpr int kVec = Elem<T>::kVec, kCeVecs = ce_grad_vecs(kCap), kCeSliceVecs = kCeThreads * kCeVecs;
+    constexpr int kVec = Elem<T>::kVec, kCeVecs = ce_grad_vecs(kCap), kCeSliceVecs = kThreads * kCeVecs;
     const int tid = threadIdx.x;
     pdl_enter<true>();   // no global access before this
     for (int64_t tile = blockIdx.x; tile < total; tile += gridDim.x) {
@@ -240,7 +250,7 @@ ce_grad_kernel(const T *x, int V, Rows rows, const CeRules q, const RowStat *__r
         uint4 u[kCeVecs];
 #pragma unroll
         for (int k = 0; k < kCeVecs; ++k) {
-            const int i = v0 + tid + k * kCeThreads;
+            const int i = v0 + tid + k * kThreads;
             if (i < v1) u[k] = load_own(reinterpret_cast<const uint4 *>(in + hin) + i);
         }
         const RowStat st = load_rowstat(stats + r);
@@ -295,7 +305,7 @@ ce_grad_kernel(const T *x, int V, Rows rows, const CeRules q, const RowStat *__r
             uint4 *vout = reinterpret_cast<uint4 *>(out + hin);
 #pragma unroll
             for (int k = 0; k < kCeVecs; ++k) {
-                const int i = v0 + tid + k * kCeThreads;
+                const int i = v0 + tid + k * kThreads;
                 if (i < v1) stg_stream(vout + i, vector(u[k], hin + i * kVec));
             }
         } else if constexpr (!kSame) {
@@ -311,7 +321,7 @@ ce_grad_kernel(const T *x, int V, Rows rows, const CeRules q, const RowStat *__r
             uint4 *vout = reinterpret_cast<uint4 *>(out + hout);
 #pragma unroll 2
             for (int k = 0; k < kCeVecs; ++k) {
-                const int i = v0 + tid + k * kCeThreads;
+                const int i = v0 + tid + k * kThreads;
                 if (i >= o1) break;
                 if (base + i < first || base + i + 2 > last) {
                     for (int e = 0; e < kVec; ++e) one(hout + i * kVec + e);
@@ -323,7 +333,18 @@ ce_grad_kernel(const T *x, int V, Rows rows, const CeRules q, const RowStat *__r
     }
 }
 
-static unsigned ce_grid(int64_t total) { return (unsigned)(total < 2147483647 ? total : 2147483647); }
+// CTAs of a call: one a slice, but of one warp no more than run at once, which then go from row to row: the GPU begins
+// about one a nanosecond (65536 x 256 bf16: 83 + 67 us with one for each row). Larger ones are slower so: their rows' loads
+// would no longer go on beside one another (65536 x 4096 bf16: 106 + 174 against 101 + 153).
+static unsigned ce_grid(int64_t total, int threads) {
+    if (threads == 32) {
+        int dev = 0, sms = 0;
+        cudaGetDevice(&dev);
+        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+        total = std::min<int64_t>(total, (int64_t)std::max(1, sms) * 32);
+    }
+    return (unsigned)(total < 2147483647 ? total : 2147483647);
+}
 
 template <typename T>
 static cudaError_t ce_fwd(const CeArgs &a) {
@@ -332,15 +353,23 @@ static cudaError_t ce_fwd(const CeArgs &a) {
     const CeRules q = ce_rules(a.opt);
     CeSlice *work = static_cast<CeSlice *>(a.workspace);
     const bool whole = ce_whole(a.N, n_slices);
+    const int threads = ce_threads(a.bf16, a.V);
     auto go = [&](auto kernel) {
-        return launch_pdl(kernel, dim3(ce_grid(total)), dim3(kCeThreads), 0, a.stream, static_cast<const T *>(a.x),
+        return launch_pdl(kernel, dim3(ce_grid(total, threads)), dim3(threads), 0, a.stream, static_cast<const T *>(a.x),
                           (int)a.V, Rows{a.R, a.s_o, a.s_i}, q, a.targets, a.vocab_start, n_slices, total, work,
                           ce_join_args(a));
     };
     const bool sum = a.parts || q.smooth > 0.f;      // a shard's records are merged with any smoothing
     auto pick = [&](auto cap, auto summed) {
         constexpr bool kCap = decltype(cap)::value, kSum = decltype(summed)::value;
-        return whole ? go(ce_fwd_kernel<T, kCap, kSum, true>) : go(ce_fwd_kernel<T, kCap, kSum, false>);
+        auto sized = [&](auto n) {
+            constexpr int kThreads = decltype(n)::value;
+            return whole ? go(ce_fwd_kernel<T, kCap, kSum, true, kThreads>) : go(ce_fwd_kernel<T, kCap, kSum, false, kThreads>);
+        };
+        return threads == 32    ? sized(std::integral_constant<int, 32>())
+               : threads == 64  ? sized(std::integral_constant<int, 64>())
+               : threads == 128 ? sized(std::integral_constant<int, 128>())
+                                : sized(std::integral_constant<int, kCeThreads>());
     };
     const std::true_type yes;
     const std::false_type no;
@@ -357,10 +386,11 @@ cudaError_t launch_ce_merge(const CeArgs &a, const void *parts, int64_t K) {
 cudaError_t launch_ce_bwd(const CeArgs &a) {
     const int slices = (int)ce_slices(a.bf16, ce_grad_vecs(a.opt.cap > 0.0), a.V);
     const int64_t total = a.N * slices;
+    const int threads = ce_threads(a.bf16, a.V);
     const CeRules q = ce_rules(a.opt);
     const Rows rows{a.R, a.s_o, a.s_i};
     auto go = [&](auto kernel, auto *x, auto *dx) {
-        return launch_pdl(kernel, dim3(ce_grid(total)), dim3(kCeThreads), 0, a.stream, x, (int)a.V, rows, q,
+        return launch_pdl(kernel, dim3(ce_grid(total, threads)), dim3(threads), 0, a.stream, x, (int)a.V, rows, q,
                           static_cast<const RowStat *>(a.stats), a.g, a.targets, a.vocab_start, dx, a.err, slices, total);
     };
     const float *xf = static_cast<const float *>(a.x);
@@ -372,8 +402,16 @@ cudaError_t launch_ce_bwd(const CeArgs &a) {
                       (a.R >= a.N || (a.s_o - a.R * a.V) * es % 16 == 0);
     auto pick = [&](auto tag, auto *x, auto *dx) {
         using T = std::remove_reference_t<decltype(tag)>;
-        return q.cap > 0.f ? (same ? go(ce_grad_kernel<T, true, true>, x, dx) : go(ce_grad_kernel<T, true, false>, x, dx))
-                           : (same ? go(ce_grad_kernel<T, false, true>, x, dx) : go(ce_grad_kernel<T, false, false>, x, dx));
+        auto wide = [&](auto cap, auto alike) {
+            constexpr bool kCap = decltype(cap)::value, kSame = decltype(alike)::value;
+            return threads == 32    ? go(ce_grad_kernel<T, kCap, kSame, 32>, x, dx)
+                   : threads == 64  ? go(ce_grad_kernel<T, kCap, kSame, 64>, x, dx)
+                   : threads == 128 ? go(ce_grad_kernel<T, kCap, kSame, 128>, x, dx)
+                                    : go(ce_grad_kernel<T, kCap, kSame, kCeThreads>, x, dx);
+        };
+        const std::true_type yes;
+        const std::false_type no;
+        return q.cap > 0.f ? (same ? wide(yes, yes) : wide(yes, no)) : (same ? wide(no, yes) : wide(no, no));
     };
     return a.bf16 ? pick(__nv_bfloat16(), xb, db) : pick(float(), xf, df);
 }
