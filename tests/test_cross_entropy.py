@@ -473,6 +473,14 @@ def test_linear_several_pieces(N, V, precision):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("precision", [vp.GRAD_MIXED, vp.GRAD_EXACT, vp.GRAD_FAST])
+@pytest.mark.parametrize("N, V, D", [(1023, 256, 64), (1024, 257, 192), (5000, 1100, 256), (20000, 50, 64)])
+def test_linear_small_vocabularies(N, V, D, precision):
+    """dW's few tiles, their rows shared out over many pairs of SMs, and just not."""
+    check_linear(*model(N, V, D, 37), dict(smooth=0.1, cap=20.0), precision=precision, where="cuda")
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("D", [512, 4096])
 def test_linear_losses_are_not_short(D):
     """The tensor cores' sums come out short, 2.4e-5 of a log-sum-exp at D = 4096; what is given back leaves the losses

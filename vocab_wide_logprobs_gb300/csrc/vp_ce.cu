@@ -234,8 +234,8 @@ template <typename T, bool kCap, bool kSame, int kThreads>
 __global__ void __launch_bounds__(kThreads, kThreads == 32 ? 32 : (kCap ? 4 : 5) * (kCeThreads / kThreads))
 ce_grad_kernel(const T *x, int V, Rows rows, const CeRules q, const RowStat *__restrict__ stats,
                const float *__restrict__ g_in, const int64_t *__restrict__ targets, int64_t vocab_start, T *dx,
-               int32_t *__restrict__ err, int n_slices, int64_t total) {
-    constexpr int kVec = Elem<T>::kVec, kCeVecs = ce_grad_vecs(kCap), kCeSliceVecs = kThreads * kCeVecs;
+               int32_t *__restrict__ err, int n_slices, int slice_vecs, int64_t total) {
+    constexpr int kVec = Elem<T>::kVec, kCeVecs = ce_grad_vecs(kCap);
     const int tid = threadIdx.x;
     pdl_enter<true>();   // no global access before this
     for (int64_t tile = blockIdx.x; tile < total; tile += gridDim.x) {
@@ -244,9 +244,9 @@ ce_grad_kernel(const T *x, int V, Rows rows, const CeRules q, const RowStat *__r
         const T *in = x + row_offset(rows, r);
         T *out = dx + r * (int64_t)V;
         const int hin = head_count(in, V), hout = head_count(out, V);
-        const int v0 = s * kCeSliceVecs;
+        const int v0 = s * slice_vecs;
         const bool same = kSame || hin == hout;
-        const int v1 = same ? min((V - hin) / kVec, v0 + kCeSliceVecs) : 0;
+        const int v1 = same ? min((V - hin) / kVec, v0 + slice_vecs) : 0;
         uint4 u[kCeVecs];
 #pragma unroll
         for (int k = 0; k < kCeVecs; ++k) {
@@ -312,7 +312,7 @@ ce_grad_kernel(const T *x, int V, Rows rows, const CeRules q, const RowStat *__r
             // Input and output rows lie differently modulo 16 bytes (an odd vocabulary out of padded rows): whole
             // vectors of the output, each out of the two of the input that its columns lie in. The first and last ones,
             // whose two would reach out of the row, go column by column, as do the ends.
-            const int nv = (V - hout) / kVec, o1 = min(nv, v0 + kCeSliceVecs);
+            const int nv = (V - hout) / kVec, o1 = min(nv, v0 + slice_vecs);
             const uint32_t b = (uint32_t)((uintptr_t)(in + hout) & 15u);
             const uint4 *base = reinterpret_cast<const uint4 *>(reinterpret_cast<const uint8_t *>(in + hout) - b);
             const uint4 *first = reinterpret_cast<const uint4 *>(in), *last = reinterpret_cast<const uint4 *>(in + V);
@@ -384,14 +384,19 @@ cudaError_t launch_ce_merge(const CeArgs &a, const void *parts, int64_t K) {
 }
 
 cudaError_t launch_ce_bwd(const CeArgs &a) {
-    const int slices = (int)ce_slices(a.bf16, ce_grad_vecs(a.opt.cap > 0.0), a.V);
-    const int64_t total = a.N * slices;
     const int threads = ce_threads(a.bf16, a.V);
+    // vectors of a thread: fewer where that leaves SMs without a slice (a gradient is the same in any slice; capped bf16, 107 x 30162
+    // out of odd rows 9.5 us against 11.7, 7 x 87716 3.8 against 4.7)
+    int vecs = ce_grad_vecs(a.opt.cap > 0.0);
+    while (vecs > 1 && a.N * ce_slices(a.bf16, vecs, a.V) < kCeFewRows) vecs /= 2;
+    const int slices = (int)ce_slices(a.bf16, vecs, a.V);
+    const int64_t total = a.N * slices;
     const CeRules q = ce_rules(a.opt);
     const Rows rows{a.R, a.s_o, a.s_i};
     auto go = [&](auto kernel, auto *x, auto *dx) {
         return launch_pdl(kernel, dim3(ce_grid(total, threads)), dim3(threads), 0, a.stream, x, (int)a.V, rows, q,
-                          static_cast<const RowStat *>(a.stats), a.g, a.targets, a.vocab_start, dx, a.err, slices, total);
+                          static_cast<const RowStat *>(a.stats), a.g, a.targets, a.vocab_start, dx, a.err, slices,
+                          threads * vecs, total);
     };
     const float *xf = static_cast<const float *>(a.x);
     const __nv_bfloat16 *xb = static_cast<const __nv_bfloat16 *>(a.x);

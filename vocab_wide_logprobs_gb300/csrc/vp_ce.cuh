@@ -300,7 +300,7 @@ __device__ __forceinline__ void ce_finish(const CeRow &o, int64_t r, const CeJoi
 }
 
 // kLanes lanes for a row, each for every kLanes-th piece in a fixed order, four at once: 8 lanes where a row has
-// up to 32 pieces, beyond that the CTA's 256, for `per` rows one after the other. Then one lane for each of
+// up to 32 pieces, a warp up to 256 (6427 rows of 33: 14 us, 32 with a CTA for each), beyond that the CTA's 256 lanes, for `per` rows one after the other. Then one lane for each of
 // the CTA's rows takes the logarithm in 64 bits, a warp's worth of that narrow pipe for all of them and not
 // for one. Lanes and order follow from the number of pieces alone; how many rows a CTA has does not change
 // a row's result: one where there are few rows (16 rows of 594 pieces: 19 us with a warp for a row, 8 us so),
@@ -309,10 +309,10 @@ constexpr int kCeJoinThreads = 256, kCeJoinAhead = 4, kCeJoinMany = 8;
 template <class Src, CeJoin kind, int kLanes>
 __global__ void __launch_bounds__(kCeJoinThreads)
 ce_join_kernel(const Src src, int K, int per, const CeJoinArgs a) {
-    static_assert(kLanes == 8 || kLanes == kCeJoinThreads, "within a warp, or the whole CTA");
+    static_assert(kLanes <= 32 || kLanes == kCeJoinThreads, "within a warp, or the whole CTA");
     constexpr int kWarpLanes = kLanes < 32 ? kLanes : 32, kParts = kLanes / kWarpLanes;   // warps of a row
     constexpr int kSide = kCeJoinThreads / kLanes;                                        // rows side by side
-    __shared__ CeRow rows[kLanes == 8 ? kSide : kCeJoinMany * kParts];
+    __shared__ CeRow rows[kLanes <= 32 ? kSide : kCeJoinMany * kParts];
     pdl_enter<true>();
     const int lane = threadIdx.x & 31, k0 = threadIdx.x % kLanes;
     const int n_rows = kSide * per;
@@ -381,17 +381,22 @@ static CeJoinArgs ce_join_args(const CeArgs &a) {
 template <class Src>
 static cudaError_t launch_ce_join(const Src &src, int K, const CeArgs &a) {
     const CeJoinArgs j = ce_join_args(a);
-    const bool whole = K > 32;                    // the CTA for a row
-    const int per = whole && a.N > 1216 ? kCeJoinMany : 1;   // eight CTAs on every SM take 1216 rows at once
-    const int rows = whole ? per : kCeJoinThreads / 8;
+    const int lanes = K <= 32 ? 8 : K <= 256 ? 32 : kCeJoinThreads;
+    const int per = lanes == kCeJoinThreads && a.N > 1216 ? kCeJoinMany : 1;   // eight CTAs on every SM take 1216 rows at once
+    const int rows = kCeJoinThreads / lanes * per;
     auto go = [&](auto kernel) {
         return launch_pdl(kernel, dim3((unsigned)((a.N + rows - 1) / rows)), dim3(kCeJoinThreads), 0, a.stream, src, K, per, j);
     };
+    auto sized = [&](auto k) {
+        constexpr CeJoin kind = decltype(k)::value;
+        return lanes == 8 ? go(ce_join_kernel<Src, kind, 8>)
+                          : lanes == 32 ? go(ce_join_kernel<Src, kind, 32>) : go(ce_join_kernel<Src, kind, kCeJoinThreads>);
+    };
     if constexpr (std::is_same<Src, CeShards>::value) {
-        return whole ? go(ce_join_kernel<Src, kCeGathered, kCeJoinThreads>) : go(ce_join_kernel<Src, kCeGathered, 8>);
+        return sized(std::integral_constant<CeJoin, kCeGathered>());
     } else {
-        if (a.parts) return whole ? go(ce_join_kernel<Src, kCeRecords, kCeJoinThreads>) : go(ce_join_kernel<Src, kCeRecords, 8>);
-        return whole ? go(ce_join_kernel<Src, kCeLoss, kCeJoinThreads>) : go(ce_join_kernel<Src, kCeLoss, 8>);
+        if (a.parts) return sized(std::integral_constant<CeJoin, kCeRecords>());
+        return sized(std::integral_constant<CeJoin, kCeLoss>());
     }
 }
 

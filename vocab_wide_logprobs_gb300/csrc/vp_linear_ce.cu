@@ -408,11 +408,13 @@ static int64_t ce_piece(int64_t N, int64_t V) {
 // Shares of dhidden's k-blocks: its output tiles are few where N and D are, and the GPU's pairs of SMs then
 // stand still (1000 x 75968 x 2048, dz as a pair: 690 us with whole sums on 32 of 76 pairs, 340 with seven shares). The waves of tiles that a split makes, counted in whole tiles, with 1 % of them for
 // each share's sums, which are written and read once more.
-static int ce_splits(int64_t N, int64_t piece, int64_t D, int pairs) {
-    const int64_t tiles = ((N + 255) / 256) * ((D + 255) / 256);
+// dW's tiles are few where V and D are (backward of 4392 x 1597 x 256: 84 us with
+// dW on 7 of 76 pairs, 50 with shares; 65536 x 256 x 1024: 883 and 261).
+static int ce_splits(int64_t rows, int64_t K, int64_t D, int pairs) {
+    const int64_t tiles = ((rows + 255) / 256) * ((D + 255) / 256);
     int best = 1;
     double least = 1e30;
-    for (int s = 1; s <= 16 && s <= piece / 512; ++s) {
+    for (int s = 1; s <= 16 && s <= K / 512; ++s) {
         const double cost = (double)((tiles * s + pairs - 1) / pairs) / s + 0.01 * s;
         if (cost < least) least = cost, best = s;
     }
@@ -420,14 +422,16 @@ static int ce_splits(int64_t N, int64_t piece, int64_t D, int pairs) {
 }
 
 struct CeBwdLayout {
-    size_t dz, acc, flags, count, list, total;
+    size_t dz, acc, acc_w, flags, count, list, total;
     int64_t vc;
-    int splits, row_groups, col_groups, n_rows, n_cols, pitch_rows, pitch_cols;
+    int splits, splits_w, row_groups, col_groups, n_rows, n_cols, pitch_rows, pitch_cols;
 };
 static CeBwdLayout ce_bwd_layout(int64_t N, int64_t V, int64_t D, int pairs) {
     CeBwdLayout L;
     L.vc = ce_piece(N, V);
     L.splits = ce_splits(N, L.vc, D, pairs);
+    // shares of dW only where its sums are small beside what they add up, and V is one piece
+    L.splits_w = L.vc >= V && 2 * ((V + 255) / 256) * ((D + 255) / 256) <= pairs ? ce_splits(V, N, D, pairs) : 1;
     L.row_groups = (int)((N + kFlagRows - 1) / kFlagRows);
     L.col_groups = (int)(L.vc / kFlagCols);
     L.n_rows = (int)((N + 255) / 256);
@@ -436,7 +440,8 @@ static CeBwdLayout ce_bwd_layout(int64_t N, int64_t V, int64_t D, int pairs) {
     L.pitch_cols = (L.row_groups + 1) / 2;
     L.dz = 0;
     L.acc = up256((size_t)2 * N * L.vc * 2);
-    L.flags = L.acc + up256((size_t)L.splits * N * D * 4);
+    L.acc_w = L.acc + up256((size_t)L.splits * N * D * 4);
+    L.flags = L.acc_w + (L.splits_w > 1 ? up256((size_t)L.splits_w * V * D * 4) : 0);
     L.count = L.flags + up256((size_t)L.row_groups * L.col_groups);
     L.list = L.count + up256((size_t)(L.n_rows + L.n_cols) * 4);
     L.total = L.list + up256(((size_t)L.n_rows * L.pitch_rows + (size_t)L.n_cols * L.pitch_cols) * 4);
@@ -463,7 +468,7 @@ cudaError_t launch_linear_ce_bwd(const CeArgs &a) {
     uint8_t *flags = mixed ? ws + L.flags : nullptr;
     int *count = reinterpret_cast<int *>(ws + L.count), *list = reinterpret_cast<int *>(ws + L.list);
     const SplitK of_rows{L.splits, mixed ? count : nullptr, list, L.pitch_rows};
-    const SplitK of_cols{1, mixed ? count + L.n_rows : nullptr, list + (int64_t)L.n_rows * L.pitch_rows, L.pitch_cols};
+    const SplitK of_cols{L.splits_w, mixed ? count + L.n_rows : nullptr, list + (int64_t)L.n_rows * L.pitch_rows, L.pitch_cols};
     const __nv_bfloat16 *h = static_cast<const __nv_bfloat16 *>(a.hidden);
     const __nv_bfloat16 *W = static_cast<const __nv_bfloat16 *>(a.weight);
     const RowStat *stats = static_cast<const RowStat *>(a.stats);
@@ -510,17 +515,21 @@ cudaError_t launch_linear_ce_bwd(const CeArgs &a) {
         if (a.dW) {
             CUtensorMap ta, ta2;
             if (!make_map_mn(&ta, dz, N, nv, vc) || !make_map_mn(&ta2, dz_lo, N, nv, vc)) return cudaErrorInvalidValue;
-            e = product(std::true_type(), ta, tm_h, ta2, nv, D, N,
-                        StoreRowsEpi{nv, D, v0, static_cast<__nv_bfloat16 *>(a.dW)}, kWGroupM, of_cols);
+            if (L.splits_w > 1)
+                e = product(std::true_type(), ta, tm_h, ta2, nv, D, N, SplitAccEpi{nv, D, true, reinterpret_cast<float *>(ws + L.acc_w)},
+                            kWGroupM, of_cols);
+            else
+                e = product(std::true_type(), ta, tm_h, ta2, nv, D, N,
+                            StoreRowsEpi{nv, D, v0, static_cast<__nv_bfloat16 *>(a.dW)}, kWGroupM, of_cols);
             if (e != cudaSuccess) return e;
         }
     }
-    if (a.dhidden) {
-        const int64_t n = a.N * a.D;
-        return launch_pdl(split_sum_kernel, dim3((unsigned)((n / 8 + 255) / 256)), dim3(256), 0, a.stream, acc, n, L.splits,
-                          static_cast<__nv_bfloat16 *>(a.dhidden));
-    }
-    return cudaSuccess;
+    auto sum = [&](size_t shares, int64_t n, int splits, void *out) {
+        return launch_pdl(split_sum_kernel, dim3((unsigned)((n / 8 + 255) / 256)), dim3(256), 0, a.stream,
+                          reinterpret_cast<const float *>(ws + shares), n, splits, static_cast<__nv_bfloat16 *>(out));
+    };
+    if (a.dW && L.splits_w > 1 && (e = sum(L.acc_w, a.V * a.D, L.splits_w, a.dW)) != cudaSuccess) return e;
+    return a.dhidden ? sum(L.acc, a.N * a.D, L.splits, a.dhidden) : cudaSuccess;
 }
 
 cudaError_t read_linear_ce_fault(uint32_t *value, bool clear) { return read_tu_fault(value, clear); }
