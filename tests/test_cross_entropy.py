@@ -481,6 +481,23 @@ def test_linear_small_vocabularies(N, V, D, precision):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("N, V, D", [(1100, 33000, 1024), (8200, 32800, 1024), (1030, 8201, 4160)])
+def test_linear_many_rows_of_large_tables(N, V, D):
+    """What dhidden's rows add of dz's second halves by themselves, in one piece of the vocabulary and in two; a row
+    without statistics takes no other row's part."""
+    h, w, targets, g = model(N, V, D, 39)
+    g[7] = 0.0
+    _, stats, dh, _ = check_linear(h, w, targets, g, dict(smooth=0.1, zeta=1e-4), where="cuda")
+    h[N - 3] = math.nan
+    o = dict(label_smoothing=0.1, z_loss=1e-4)
+    _, stats = vp.vp_linear_cross_entropy_fwd(h.cuda(), w.cuda(), targets.cuda(), **o)
+    got, _ = vp.vp_linear_cross_entropy_bwd(h.cuda(), w.cuda(), targets.cuda(), stats, g.cuda(), want_dW=False, **o)
+    rest = torch.arange(N, device="cuda") != N - 3
+    assert torch.equal(got[rest], dh.cuda()[rest])
+    assert targets[N - 3] < 0 or torch.isnan(got[N - 3]).all()
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("D", [512, 4096])
 def test_linear_losses_are_not_short(D):
     """The tensor cores' sums come out short, 2.4e-5 of a log-sum-exp at D = 4096; what is given back leaves the losses

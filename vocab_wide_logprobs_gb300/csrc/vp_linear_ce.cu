@@ -7,10 +7,9 @@
 //   target's logit; ce_join_kernel makes them the row's loss. 2 N V D flops.
 // Backward, a piece of the vocabulary at a time: the piece's logits again, dz in the epilogue (through
 //   the cap's slope) as one or two bf16 values, then dhidden += dz . W_c and dW_c = dz^T . h. 6 N V D
-//   flops, 10 with dz as a pair everywhere, about 6.9 with a pair where it counts (the default).
-// Bound: the tensor cores, and the power they draw. 8192 x 75968 x 4096: forward 2.5 ms, backward 9.3 ms
-//   after a pause (1.9 and 1.6 PFLOP/s of the products that are made); 13.9 ms both, back to back under the
-//   power cap. Few rows: the bytes of W, read three times, and dW written (16 rows: 102, 107, 99 and 96 us, 92
+//   flops, 10 with dz as a pair everywhere, 6.5 to 6.9 with a pair where it counts (the default).
+// Bound: the tensor cores, and the power they draw. 8192 x 75968 x 4096: forward 2.5 ms after
+//   a pause (1.9 PFLOP/s); back to back, under the power cap, backward 9.9 to 10.2 and both 13.3 ms (1.62 PFLOP/s). Few rows: the bytes of W, read three times, and dW written (16 rows: 102, 107, 99 and 96 us, 92
 //   each at the copy rate). Short K (D of 512 and less): the epilogues' instructions.
 #include "vp_ce.cuh"
 #include "vp_gemm.cuh"
@@ -148,6 +147,7 @@ struct DzCeEpi {
     int32_t *err;
     int64_t lo_off;
     uint8_t *flags;     // [N / 32][ldz / 64], or NULL: no notes
+    float *limits;      // [N]: from where on a row's values are pairs; or NULL
     __device__ __forceinline__ void operator()(int row, int col0, int ncol, uint32_t taddr) const {
         const bool valid = row < N;
         const RowStat s = load_rowstat(stats + (valid ? row : 0));
@@ -165,6 +165,7 @@ struct DzCeEpi {
             const float zt = (s.m + s.logS_hi + s.c_hi) * q.inv_cap;
             limit *= fmaxf(fmaf(-zt, zt, 1.f), 9.5367431640625e-07f);
         }
+        if (limits && valid && col0 == 0) limits[row] = limit;
         __shared__ uint4 stage[kWideEpiWarps][kStageVecs];
         uint4 *mine = stage[(threadIdx.x >> 5) - 2];
         const int first = row - (threadIdx.x & 31);           // the warp's first row
@@ -319,6 +320,79 @@ pair_list_kernel(const uint8_t *__restrict__ flags, int row_groups, int pitch, i
     if (tid == 0) count[blockIdx.x] = (int)done;
 }
 
+// dhidden's share of the second halves, without a GEMM: a row's values above its limit are few (those of a cross entropy add
+// up to about twice its scale, so some 32 at most, and one or two as a rule), so their second halves times their rows of W are
+// added to the row's sum as they are. A CTA for a row and 2048 columns: it goes through the row's noted blocks, 32 at a time,
+// in order, so a row's sum does not depend on the rows beside it.
+constexpr int kAddThreads = 256, kAddBlocks = 32;
+__global__ void __launch_bounds__(kAddThreads)
+pair_add_kernel(const __nv_bfloat16 *__restrict__ dz, int64_t lo_off, int ldz, const uint8_t *__restrict__ flags, int pitch,
+                int col_groups, const float *__restrict__ limits, const __nv_bfloat16 *__restrict__ W, int D,
+                float *__restrict__ acc) {
+    __shared__ int s_block[kAddThreads];
+    __shared__ uint32_t s_n[kAddThreads / 32];
+    __shared__ uint2 s_mask[kAddBlocks];
+    __shared__ float s_lo[kAddBlocks][kFlagCols];
+    pdl_enter<true>();   // no global access before this
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int64_t row = blockIdx.x;
+    const int d = (blockIdx.y * kAddThreads + tid) * 8;
+    const float limit = limits[row];
+    const uint8_t *f = flags + row / kFlagRows * pitch;
+    const __nv_bfloat16 *hi = dz + row * ldz;
+    float sum[8] = {};
+    bool some = false;                                   // the same for the CTA
+    for (int g0 = 0; g0 < col_groups; g0 += kAddThreads) {
+        const bool noted = g0 + tid < col_groups && f[g0 + tid];
+        const uint32_t votes = __ballot_sync(0xffffffffu, noted);
+        if (lane == 0) s_n[warp] = __popc(votes);
+        __syncthreads();
+        int before = __popc(votes & ((1u << lane) - 1u)), n = 0;
+        for (int w = 0; w < kAddThreads / 32; ++w) {
+            if (w < warp) before += s_n[w];
+            n += s_n[w];
+        }
+        if (noted) s_block[before] = g0 + tid;
+        __syncthreads();
+        for (int b0 = 0; b0 < n; b0 += kAddBlocks) {
+            const int nb = min(kAddBlocks, n - b0);
+            for (int b = warp; b < nb; b += kAddThreads / 32) {
+                const int64_t at = (int64_t)s_block[b0 + b] * kFlagCols + 2 * lane;
+                const uint32_t h = __ldg(reinterpret_cast<const uint32_t *>(hi + at)), l = __ldg(reinterpret_cast<const uint32_t *>(hi + lo_off + at));
+                float x, y;
+                Elem<__nv_bfloat16>::unpack2(h, x, y);
+                const uint32_t even = __ballot_sync(0xffffffffu, fabsf(x) > limit), odd = __ballot_sync(0xffffffffu, fabsf(y) > limit);
+                if (lane == 0) s_mask[b] = make_uint2(even, odd);
+                Elem<__nv_bfloat16>::unpack2(l, s_lo[b][2 * lane], s_lo[b][2 * lane + 1]);
+            }
+            __syncthreads();
+            for (int b = 0; b < nb; ++b) {
+                const uint2 mask = s_mask[b];
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    for (uint32_t m = half ? mask.y : mask.x; m; m &= m - 1) {
+                        const int e = 2 * (__ffs(m) - 1) + half;
+                        some = true;
+                        if (d >= D) continue;
+                        float w[8];
+                        Elem<__nv_bfloat16>::unpack(__ldg(reinterpret_cast<const uint4 *>(W + ((int64_t)s_block[b0 + b] * kFlagCols + e) * D + d)), w);
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) sum[k] = fmaf(s_lo[b][e], w[k], sum[k]);
+                    }
+                }
+            }
+            __syncthreads();
+        }
+    }
+    if (!some || d >= D) return;
+    float4 *p = reinterpret_cast<float4 *>(acc + row * D + d);
+    float4 a = p[0], b = p[1];
+    a.x += sum[0]; a.y += sum[1]; a.z += sum[2]; a.w += sum[3];
+    b.x += sum[4]; b.y += sum[5]; b.z += sum[6]; b.w += sum[7];
+    p[0] = a;
+    p[1] = b;
+}
+
 // dhidden's tiles: the sum over a share of the k-blocks, kept apart for each share; ld is a multiple of 64.
 struct SplitAccEpi {
     static constexpr bool kPdl = true, kWide = true;
@@ -421,8 +495,14 @@ static int ce_splits(int64_t rows, int64_t K, int64_t D, int pairs) {
     return best;
 }
 
+// Whether dhidden's second halves are added by pair_add_kernel, about 15 ns a row, and not by the GEMM, 2 V D flops a row
+// in those k-blocks that any of 256 rows notes (a quarter of 75968 columns, half of 20000). Backward, in us, so and
+// otherwise: 8192 x 75968 x 4096 10210 and 10680, 2048 x 32000 x 2048 645 and 708, 8192 x 20000 x 1024 1021 and 1028; but
+// 6427 x 4122 x 832 281 and 256, 256 x 32000 x 1024 102 and 97. Under a cap a row's values are not bounded by its scale: there the GEMM adds them.
+static bool ce_apart(int64_t N, int64_t V, int64_t D, double cap) { return cap <= 0.0 && N >= 1024 && V * D >= 1 << 25; }
+
 struct CeBwdLayout {
-    size_t dz, acc, acc_w, flags, count, list, total;
+    size_t dz, acc, acc_w, flags, limits, count, list, total;
     int64_t vc;
     int splits, splits_w, row_groups, col_groups, n_rows, n_cols, pitch_rows, pitch_cols;
 };
@@ -442,7 +522,8 @@ static CeBwdLayout ce_bwd_layout(int64_t N, int64_t V, int64_t D, int pairs) {
     L.acc = up256((size_t)2 * N * L.vc * 2);
     L.acc_w = L.acc + up256((size_t)L.splits * N * D * 4);
     L.flags = L.acc_w + (L.splits_w > 1 ? up256((size_t)L.splits_w * V * D * 4) : 0);
-    L.count = L.flags + up256((size_t)L.row_groups * L.col_groups);
+    L.limits = L.flags + up256((size_t)L.row_groups * L.col_groups);
+    L.count = L.limits + up256((size_t)N * 4);
     L.list = L.count + up256((size_t)(L.n_rows + L.n_cols) * 4);
     L.total = L.list + up256(((size_t)L.n_rows * L.pitch_rows + (size_t)L.n_cols * L.pitch_cols) * 4);
     return L;
@@ -466,6 +547,8 @@ cudaError_t launch_linear_ce_bwd(const CeArgs &a) {
     const __nv_bfloat16 *dz_lo = dz + a.N * vc;            // behind dz_hi
     float *acc = reinterpret_cast<float *>(ws + L.acc);
     uint8_t *flags = mixed ? ws + L.flags : nullptr;
+    const bool apart = mixed && a.dhidden && ce_apart(a.N, a.V, a.D, a.opt.cap);
+    float *limits = apart ? reinterpret_cast<float *>(ws + L.limits) : nullptr;
     int *count = reinterpret_cast<int *>(ws + L.count), *list = reinterpret_cast<int *>(ws + L.list);
     const SplitK of_rows{L.splits, mixed ? count : nullptr, list, L.pitch_rows};
     const SplitK of_cols{L.splits_w, mixed ? count + L.n_rows : nullptr, list + (int64_t)L.n_rows * L.pitch_rows, L.pitch_cols};
@@ -483,8 +566,8 @@ cudaError_t launch_linear_ce_bwd(const CeArgs &a) {
             return ce_logits_gemm(h, W + v0 * D, N, nv, D, epi, a.stream);
         };
         const int64_t lo_off = chain ? a.N * vc : 0;
-        e = q.cap > 0.f ? gemm(DzCeEpi<true>{N, V, (int)v0, (int)vc, cut_off(D), a.vocab_start, a.targets, q, stats, a.g, dz, a.err, lo_off, flags})
-                        : gemm(DzCeEpi<false>{N, V, (int)v0, (int)vc, cut_off(D), a.vocab_start, a.targets, q, stats, a.g, dz, a.err, lo_off, flags});
+        e = q.cap > 0.f ? gemm(DzCeEpi<true>{N, V, (int)v0, (int)vc, cut_off(D), a.vocab_start, a.targets, q, stats, a.g, dz, a.err, lo_off, flags, limits})
+                        : gemm(DzCeEpi<false>{N, V, (int)v0, (int)vc, cut_off(D), a.vocab_start, a.targets, q, stats, a.g, dz, a.err, lo_off, flags, limits});
         if (e != cudaSuccess) return e;
         if (mixed) {
             const int cols = (nv + 63) / 64, tiles = (nv + 255) / 256;
@@ -492,7 +575,7 @@ cudaError_t launch_linear_ce_bwd(const CeArgs &a) {
                            cols, L.n_rows, count, list, L.pitch_rows, L.pitch_cols);
             if (e != cudaSuccess) return e;
         }
-        auto product = [&](auto kinds, const CUtensorMap &ta, const CUtensorMap &tb, const CUtensorMap &ta2, int M, int Nn,
+        auto product = [&](auto kinds, bool chain, const CUtensorMap &ta, const CUtensorMap &tb, const CUtensorMap &ta2, int M, int Nn,
                            int K, const auto &epi, int group, const SplitK &ks) {
             using Epi = std::decay_t<decltype(epi)>;
             constexpr bool kAMn = decltype(kinds)::value;
@@ -509,17 +592,23 @@ cudaError_t launch_linear_ce_bwd(const CeArgs &a) {
             // a short last piece has fewer k-blocks than there are shares; their sums stay as they are
             SplitK ks = of_rows;
             ks.splits = std::min(ks.splits, (nv + kLBK - 1) / kLBK);
-            e = product(std::false_type(), ta, tb, ta2, N, D, nv, SplitAccEpi{N, D, v0 == 0, acc}, kGradGroupM, ks);
+            e = product(std::false_type(), chain && !apart, ta, tb, ta2, N, D, nv, SplitAccEpi{N, D, v0 == 0, acc}, kGradGroupM, ks);
             if (e != cudaSuccess) return e;
+            if (apart) {
+                e = launch_pdl(pair_add_kernel, dim3((unsigned)N, (unsigned)((D + 8 * kAddThreads - 1) / (8 * kAddThreads))),
+                               dim3(kAddThreads), 0, a.stream, dz, lo_off, (int)vc, flags, L.col_groups, (nv + kFlagCols - 1) / kFlagCols,
+                               limits, W + v0 * D, D, acc);
+                if (e != cudaSuccess) return e;
+            }
         }
         if (a.dW) {
             CUtensorMap ta, ta2;
             if (!make_map_mn(&ta, dz, N, nv, vc) || !make_map_mn(&ta2, dz_lo, N, nv, vc)) return cudaErrorInvalidValue;
             if (L.splits_w > 1)
-                e = product(std::true_type(), ta, tm_h, ta2, nv, D, N, SplitAccEpi{nv, D, true, reinterpret_cast<float *>(ws + L.acc_w)},
+                e = product(std::true_type(), chain, ta, tm_h, ta2, nv, D, N, SplitAccEpi{nv, D, true, reinterpret_cast<float *>(ws + L.acc_w)},
                             kWGroupM, of_cols);
             else
-                e = product(std::true_type(), ta, tm_h, ta2, nv, D, N,
+                e = product(std::true_type(), chain, ta, tm_h, ta2, nv, D, N,
                             StoreRowsEpi{nv, D, v0, static_cast<__nv_bfloat16 *>(a.dW)}, kWGroupM, of_cols);
             if (e != cudaSuccess) return e;
         }
