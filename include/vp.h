@@ -803,7 +803,7 @@ VP_API vp_status vp_cross_entropy_merge(const vp_partial *parts, int64_t K, int6
  *                  the values themselves. What the smaller values can add up to in
  *                  dhidden is a third of what rounding the output adds, relative to the row's scale; a
  *                  dW row of a column that is no row's target is that of VP_GRAD_FAST. About 6 to 7
- *                  N V D flops for 10 of VP_GRAD_EXACT.
+ *                  N V D flops for 10 of VP_GRAD_EXACT, which it is where weight and products are small.
  * How dhidden's sum is split over SMs follows from N, V and D, so its last bits may differ between
  * batch sizes, and under VP_GRAD_MIXED with the rows beside it. */
 #define VP_GRAD_MIXED 2

@@ -450,6 +450,14 @@ def test_linear(shape, o):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("o", OPTIONS)
+@pytest.mark.parametrize("shape", [(3, 70001, 64), (130, 20000, 256), (257, 8200, 576), (1500, 6000, 128)])
+def test_linear_larger_tables(shape, o):
+    """Tables and products from where on only the blocks of dz that count are summed as pairs."""
+    check_linear(*model(*shape, sum(shape)), o, where="cuda")
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("shape", [(300, 1500, 256), (700, 9000, 64), (17, 9000, 1024)])
 def test_linear_precisions_and_single_outputs(shape):
     h, w, targets, g = model(*shape, 31)

@@ -501,6 +501,11 @@ static int ce_splits(int64_t rows, int64_t K, int64_t D, int pairs) {
 // 6427 x 4122 x 832 281 and 256, 256 x 32000 x 1024 102 and 97. Under a cap a row's values are not bounded by its scale: there the GEMM adds them.
 static bool ce_apart(int64_t N, int64_t V, int64_t D, double cap) { return cap <= 0.0 && N >= 1024 && V * D >= 1 << 25; }
 
+// Whether the mixed precision looks for the blocks that count: finding them is a launch, which costs more than all
+// second halves where the table and the products are small (backward, in us, without and with: 64 x 5003 x 512 30 and 32,
+// 2000 x 2000 x 256 41 and 44; but 64 x 16000 x 512 45 and 42, 16 x 16000 x 512 44 and 38, where they read the table once more).
+static bool ce_lists(int64_t N, int64_t V, int64_t D) { return V * D > 1 << 22 || N * V * D > 1 << 30; }
+
 struct CeBwdLayout {
     size_t dz, acc, acc_w, flags, limits, count, list, total;
     int64_t vc;
@@ -543,7 +548,7 @@ cudaError_t launch_linear_ce_bwd(const CeArgs &a) {
     const int64_t vc = L.vc;
     uint8_t *ws = static_cast<uint8_t *>(a.workspace);
     __nv_bfloat16 *dz = reinterpret_cast<__nv_bfloat16 *>(ws + L.dz);
-    const bool chain = a.precision != VP_GRAD_FAST_, mixed = a.precision == VP_GRAD_MIXED_;
+    const bool chain = a.precision != VP_GRAD_FAST_, mixed = a.precision == VP_GRAD_MIXED_ && ce_lists(a.N, a.V, a.D);
     const __nv_bfloat16 *dz_lo = dz + a.N * vc;            // behind dz_hi
     float *acc = reinterpret_cast<float *>(ws + L.acc);
     uint8_t *flags = mixed ? ws + L.flags : nullptr;
