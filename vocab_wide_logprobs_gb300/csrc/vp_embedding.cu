@@ -669,11 +669,12 @@ int sm_count() {
     return sms > 0 ? sms : 1;
 }
 
-// Tokens of a window: enough windows for a few CTAs on every SM, and as long as that allows, since
-// a window costs up to two partial rows.
-int grad_window(int64_t N) {
+// Tokens of a window: as many as leave three CTAs for every SM, since a window costs up to two partial rows (20000 x 1024
+// bf16 into 151936 rows, 64 tokens and 313 CTAs: 81 us, 32 and 625: 72; 8192 x 4096, 32 and 512: 109, 8 and 2048: 111 to 117).
+int grad_window(int64_t N, int64_t D) {
+    const int64_t col_blocks = (D + kGradThreads * kEmbVec - 1) / (kGradThreads * kEmbVec);
     int w = 8;
-    while (w < kGradMaxWindow && N > (int64_t)w * 256) w *= 2;
+    while (w < kGradMaxWindow && N * col_blocks >= (int64_t)w * 2 * 500) w *= 2;
     return w;
 }
 
@@ -687,7 +688,7 @@ struct GradLayout {
 };
 GradLayout grad_layout(int64_t N, int64_t V, int64_t D) {
     auto up = [](size_t x) { return (x + 255) & ~(size_t)255; };
-    const int64_t windows = (N + grad_window(N) - 1) / grad_window(N);
+    const int64_t windows = (N + grad_window(N, D) - 1) / grad_window(N, D);
     GradLayout L;                                // the rows' spans first
     L.n_tokens = up((size_t)V * sizeof(int2));
     L.rows = L.n_tokens + 256;
@@ -792,7 +793,7 @@ cudaError_t embedding_bwd(const EmbeddingArgs &a) {
     }
     if (e != cudaSuccess) return e;
 
-    g.window = grad_window(a.N);
+    g.window = grad_window(a.N, a.D);
     g.n_windows = (int)((a.N + g.window - 1) / g.window);
     g.n_tokens = n_tokens;
     g.spans = spans;
