@@ -759,7 +759,7 @@ VP_API vp_status vp_linear_mxfp4_fwd(const uint8_t *x_codes, const uint8_t *x_sc
  * and a zero gradient row, one outside the shard NaN and VP_ERRBIT_TARGET. A NaN logit
  * gives NaN, and without a cap +inf and an all -inf row do too; a capped logit of +-inf is
  * +-softcap, with gradient 0. A masked (-inf) column has p = 0; with label smoothing it makes
- * the loss +inf, while the gradient stays that of the formula. workspace: 8-byte aligned,
+ * the loss +inf, while the gradient stays that of the formula. workspace: 16-byte aligned,
  * vp_cross_entropy_workspace_size(N, V) bytes, NULL where that is 0. A row's result does not depend on N. */
 VP_API size_t vp_cross_entropy_workspace_size(int64_t N, int64_t V);
 VP_API vp_status vp_cross_entropy_fwd(const void *x, int dtype, int64_t N, int64_t V, int64_t R, int64_t s_o,

@@ -695,6 +695,14 @@ def test_refusals_of_the_library():
     assert lib.vp_cross_entropy_workspace_size(-1, 5) == 0 and lib.vp_linear_cross_entropy_workspace_size(4, 5, 65) == 0
 
 
+def test_a_workspace_off_a_16_byte_boundary_is_refused():
+    """The slices' records are written and read 16 bytes at a time."""
+    eight = ctypes.c_void_p(0x100008)
+    assert fwd(work=eight) == ERR_ALIGN
+    assert _lib.lib().vp_cross_entropy_partial(FAKE, 1, 4, 20000, 4, 0, 20000, 0, 0.0, FAKE, FAKE, eight, BIG,
+                                               None) == ERR_ALIGN
+
+
 def test_refusals_of_the_binding():
     def status(fn):
         with pytest.raises(vp.VPError) as e:

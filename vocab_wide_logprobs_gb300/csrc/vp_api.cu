@@ -875,7 +875,7 @@ vp_status vp_cross_entropy_fwd(const void *x, int dtype, int64_t N, int64_t V, i
     const size_t need = vp_cross_entropy_workspace_size(N, V);
     if (!x || !targets || !loss || !stats || (need && !workspace)) return VP_ERR_NULL;
     if (!aligned(x, elem_size(dtype)) || !aligned(targets, 8) || !aligned(loss, 4) || !aligned(stats, 16) ||
-        !aligned(workspace, 8) || !aligned(err_word, 4))
+        !aligned(workspace, 16) || !aligned(err_word, 4))
         return VP_ERR_ALIGN;
     if (workspace_bytes < need) return VP_ERR_ARG;
     if ((st = check_device()) != VP_OK) return st;
@@ -920,7 +920,7 @@ vp_status vp_cross_entropy_partial(const void *x, int dtype, int64_t N, int64_t 
     if (N == 0) return VP_OK;
     const size_t need = vp_cross_entropy_workspace_size(N, V);
     if (!x || !targets || !parts || (need && !workspace)) return VP_ERR_NULL;
-    if (!aligned(x, elem_size(dtype)) || !aligned(targets, 8) || !aligned(parts, 8) || !aligned(workspace, 8))
+    if (!aligned(x, elem_size(dtype)) || !aligned(targets, 8) || !aligned(parts, 8) || !aligned(workspace, 16))
         return VP_ERR_ALIGN;
     if (workspace_bytes < need) return VP_ERR_ARG;
     if ((st = check_device()) != VP_OK) return st;

@@ -188,8 +188,8 @@ __device__ __forceinline__ void ce_add(CeRow &o, const CePiece &p) {
     o.n += p.n;
 }
 
-// A slice of a row of logits: 32 bytes.
-struct CeSlice {
+// A slice of a row of logits: 32 bytes, written and read 16 at a time.
+struct alignas(16) CeSlice {
     float m, S, S_lo, W, W_lo, zt;
     uint32_t flags, n;
 };
