@@ -253,6 +253,33 @@ def test_nan_stays_with_its_token(N):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("D", [40, 37])
+@pytest.mark.parametrize("N, V, share", [(3000, 100, 0.0), (3000, 50, 0.6), (100, 50, 0.5)])
+def test_infinities_of_runs_over_windows(N, V, share, D):
+    """Infinite sums as plain additions have them, whether an id's tokens lie in a few windows (30 of them), in many (1800) or
+    in a single launch (50): inf from one infinity or from finite values that overflow, NaN from two of opposite signs."""
+    hot = 20
+    ids = torch.arange(N) % V
+    ids[torch.rand(N, generator=torch.Generator().manual_seed(N)) < share] = hot
+    dy = rand(N, D, F32)
+    mine = (ids == hot).nonzero()[:, 0]
+    first, middle, last = int(mine[0]), int(mine[len(mine) // 2]), int(mine[-1])
+    dy[first, 0], dy[middle, 1], dy[last, 2] = math.inf, -math.inf, math.inf
+    dy[first, 3], dy[last, 3] = math.inf, -math.inf
+    dy[middle, 4] = math.nan
+    dy[mine, 5], dy[mine, 6] = 3e38, -3e38                           # two of them overflow
+    dy[first, 7], dy[last, 7] = math.inf, math.inf
+    dy[mine, 8] = 3e37                                               # twelve do, more than a window of eight has
+    for before in (None, rand(V, D, F32, 1)):
+        dW = None if before is None else before.cuda()
+        got = vp.vp_embedding_bwd(dy.cuda(), ids.cuda(), V, dW=dW, accumulate=before is not None).cpu()
+        inf = math.inf
+        assert got[hot, [0, 1, 2, 5, 6, 7, 8]].tolist() == [inf, -inf, inf, inf, -inf, inf, inf]
+        assert torch.isnan(got[hot, 3:5]).all() and torch.isfinite(got[hot, 9:]).all()
+        assert torch.isfinite(got[torch.arange(V) != hot]).all()
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("N", [40, 3000])
 def test_streams_graphs_and_workspaces(N):
     V, D = 3000, 256

@@ -638,7 +638,8 @@ __device__ __forceinline__ void join_run(const TableGrad &a, TO *__restrict__ dW
 #pragma unroll
             for (int j = 1; j < kGroups; ++j) df_add(total, s_sum[j * kLanes + l][e]);
             TO *dst = dW + run.x * (int64_t)a.D + c0 + t;
-            const float s = total.hi + total.lo;
+            // an infinite sum's low part is NaN (inf - inf), a finite one's is finite
+            const float s = isfinite(total.hi) ? total.hi + total.lo : total.hi;
             Elem<TO>::store1(dst, kAdd ? fmaf(s, a.scale, (float)*dst) : s * a.scale);
         }
         __syncthreads();
