@@ -274,6 +274,24 @@ def test_rows_of_a_types_ends(dtype, V):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("dtype", [F32, BF16])
+def test_sums_of_logits_past_the_largest_float(dtype):
+    """Half of 2^25 columns at either end of the type, with smoothing: their mean is a float, their sum is not, nor is what
+    2^24 of them add up to."""
+    V = 1 << 25
+    high = torch.finfo(dtype).max
+    x = torch.full((1, V), -high, dtype=dtype, device="cuda")
+    x[0, ::2] = high
+    targets = torch.tensor([4], device="cuda")
+    want = 0.1 * high + math.log(V // 2)                             # mean_j (m - z_j) is half of 2 high
+    loss, _ = vp.vp_cross_entropy_fwd(x, targets, label_smoothing=0.1)
+    assert abs(float(loss) - want) <= 1e-6 * want
+    parts = torch.stack([vp.vp_cross_entropy_partial(x[:, a:a + V // 2], targets, vocab_start=a) for a in (0, V // 2)])
+    loss, _ = vp.vp_cross_entropy_merge(parts, label_smoothing=0.1)
+    assert abs(float(loss) - want) <= 1e-6 * want
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [F32, BF16])
 def test_rows_with_nothing_or_with_nan(dtype):
     x, _, g = rows(7, 5003, dtype, 13)
     x[1] = -math.inf
@@ -517,6 +535,19 @@ def test_linear_losses_are_not_short(D):
     h = torch.zeros_like(h)
     h[torch.arange(200), torch.arange(200) * 7 % D] = 8.0
     check_linear(h, w, targets, torch.ones(200), dict())
+
+
+@pytest.mark.gpu
+def test_linear_sums_of_logits_past_the_largest_float():
+    """Logits of +-2^124, with smoothing: 128 of them add up to more than a float holds, their mean does not."""
+    h, w = torch.zeros(3, 64, dtype=BF16), torch.zeros(1000, 64, dtype=BF16)
+    h[:, 5] = torch.tensor([2.0 ** 60, -2.0 ** 60, 2.0 ** 10])
+    w[:, 5] = 2.0 ** 64
+    w[1::4, 5] = -2.0 ** 64
+    targets = torch.tensor([4, 5, 0])
+    loss, _ = vp.vp_linear_cross_entropy_fwd(h.cuda(), w.cuda(), targets.cuda(), label_smoothing=0.1)
+    ref = plain(h.double() @ w.double().t(), targets, 0.1)
+    assert torch.allclose(loss.double().cpu(), ref, rtol=1e-6)
 
 
 @pytest.mark.gpu

@@ -26,10 +26,10 @@ struct CeRules {
     float cap, inv_cap;          // c, 1 / c (cap 0: none)
 };
 
-// Sums W are carried times 2^-24: a row may span more than the largest float, and
-// the factor is exact for all that counts.
-constexpr float kCeScale = 5.9604644775390625e-08f;
-constexpr double kCeUnscale = 16777216.0;
+// Sums W and sums of logits are carried times 2^-33: below 2^32 columns that lie up to twice the
+// largest float apart do not overflow, and the factor is exact for all that counts.
+constexpr float kCeScale = 1.16415321826934814453125e-10f;
+constexpr double kCeUnscale = 8589934592.0;
 
 // z = c t and slope = 1 - t^2, t = tanh(y), y = x / c, of n (even) values. Below |y| = 5/8:
 // t = y (1 + s P(s)), s = y^2, P of degree 4 by interpolation of tanh(y) / y at Chebyshev
@@ -146,7 +146,7 @@ __device__ __forceinline__ float ce_grad_target(const CeRules &q, const CeGradRo
 // What a piece of a row, or the whole of it, comes to.
 struct CeRow {
     float M;
-    DF S, W;              // W times 2^-24
+    DF S, W;              // W times 2^-33
     float zt;
     uint32_t flags;       // VP_PART_* of the pieces; kCeMinusInf where W is -inf
     int owners;           // pieces that hold the target
@@ -154,7 +154,7 @@ struct CeRow {
 };
 constexpr uint32_t kCeMinusInf = 1u << 30;
 
-// A piece of a row as its record says it: n columns, the largest m, sum S and sum W (times 2^-24).
+// A piece of a row as its record says it: n columns, the largest m, sum S and sum W (times 2^-33).
 struct CePiece {
     float m;
     DF S, W;
@@ -219,8 +219,8 @@ struct CeShards {
     }
 };
 
-// What a GEMM's epilogue left of 128 columns of a row: (m, S, sum of z, -), and the target's logit
-// in an array of its own.
+// What a GEMM's epilogue left of 128 columns of a row: (m, S, sum of z times 2^-33, -), and the target's
+// logit in an array of its own.
 constexpr int kCeTileCols = 128;
 struct CeTiles {
     const float4 *tiles;        // [N][n_t]
@@ -230,10 +230,9 @@ struct CeTiles {
     __device__ __forceinline__ CePiece piece(int64_t r, int k) const {
         const float4 p = tiles[r * n_t + k];
         const int n = min(kCeTileCols, V - kCeTileCols * k);
-        const float w = p.z * kCeScale;
-        const bool minus_inf = w == -INFINITY;
-        DF W{minus_inf ? 0.f : w, 0.f};
-        if (w == w) df_add(W, -(float)n * (p.x * kCeScale));                         // sum of (z - m)
+        const bool minus_inf = p.z == -INFINITY;
+        DF W{minus_inf ? 0.f : p.z, 0.f};
+        if (p.z == p.z) df_add(W, -(float)n * (p.x * kCeScale));                         // sum of (z - m)
         return {p.x, {p.y, 0.f}, W, 0.f, minus_inf ? kCeMinusInf : 0u, (uint32_t)n};
     }
 };

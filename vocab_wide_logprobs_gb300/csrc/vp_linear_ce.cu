@@ -49,7 +49,7 @@ struct CeEpi {
         const int64_t t = tg - vocab_start - col0;
         const int tloc = (tg >= 0 && t >= 0 && t < ncol) ? (int)t : -1;
         float m = kNegBig, S = 0.f, zt = 0.f;
-        float2 Z = f2(0.f);
+        float2 Z = f2(0.f);                              // times 2^-33 (kCeScale)
 #pragma unroll 1
         for (int c = 0; c < kWideEpiCols / 32; ++c) {
             float v[32];
@@ -66,12 +66,12 @@ struct CeEpi {
             if (n < 32) {
 #pragma unroll
                 for (int i = 0; i < 32; ++i) {
-                    Z.x += i < n ? v[i] : 0.f;
+                    Z.x += i < n ? v[i] * kCeScale : 0.f;
                     if (i >= n) v[i] = -INFINITY;
                 }
             } else if (sum) {
 #pragma unroll
-                for (int i = 0; i < 32; i += 2) Z = __fadd2_rn(Z, make_float2(v[i], v[i + 1]));
+                for (int i = 0; i < 32; i += 2) Z = __ffma2_rn(make_float2(v[i], v[i + 1]), f2(kCeScale), Z);
             }
             float cm = m;
 #pragma unroll
