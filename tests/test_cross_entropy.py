@@ -524,6 +524,34 @@ def test_linear_many_rows_of_large_tables(N, V, D):
 
 
 @pytest.mark.gpu
+def test_dhidden_of_a_large_table_does_not_depend_on_the_rows_beside_it():
+    """A row with 16 values whose bf16 rounding crosses the row's limit for pairs: they are pairs whether or not a row of the
+    same block has one there. 17 equal logits of 18 among zeros and their target among them: p = (1 - m) / 17 with
+    m = 32751 e^-18 / 17 = 2.9e-5, the limit (1 + m / 16) / 17 for |g| = 1, so the 16 lie 3.1e-5 of themselves below it, and
+    with g / 17 = 1 + 0.75 2^-7 they round up over it."""
+    N, V, D = 1024, 32768, 1024
+    gen = torch.Generator().manual_seed(50)
+    heavy = torch.arange(17) * 1024 + 5
+    w = torch.randn(V, D, generator=gen).to(BF16)
+    w[:, 0] = 0.0
+    w[heavy, 0] = 18.0
+    h = torch.zeros(N, D, dtype=BF16)
+    h[:, 0] = 1.0
+    g = torch.ones(N)
+    g[5] = 17 * (1 + 0.75 / 128)
+    rest = []
+    for beside in (False, True):
+        targets = torch.full((N,), -1)
+        targets[5] = heavy[0]
+        if beside:
+            targets[6:22] = heavy[1:]
+        args = h.cuda(), w.cuda(), targets.cuda()
+        _, stats = vp.vp_linear_cross_entropy_fwd(*args)
+        rest.append(vp.vp_linear_cross_entropy_bwd(*args, stats, g.cuda(), want_dW=False)[0][5])
+    assert torch.equal(*rest)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("D", [512, 4096])
 def test_linear_losses_are_not_short(D):
     """The tensor cores' sums come out short, 2.4e-5 of a log-sum-exp at D = 4096; what is given back leaves the losses

@@ -125,8 +125,8 @@ __device__ __forceinline__ void store_rows(uint4 *stage, const uint4 (&v)[kVecs]
 // itself, so what the values up to a threshold of a row add to the error of dhidden is 2^-8 sqrt(sum of
 // their squares) |W|, and with a threshold of t times the row's own scale s (for a cross entropy the values
 // add up to about 2 s, s = |g| (1 - p_t), through the cap's slope at the target) that is below
-// 2^-8 sqrt(2 t) s |W|: for t = 1/16 about a third of what the output's own rounding adds. The larger values
-// of a row, its target's first of all, are pairs. Which 32 x 64 pieces of dz hold one is noted, and the
+// 2^-8 sqrt(2 t) s |W|: for t = 1/16 about a third of what the output's own rounding adds. The values of a
+// row whose first half is larger, its target's first of all, are pairs. Which 32 x 64 pieces of dz hold one is noted, and the
 // gradient GEMMs take the second halves of no other k-blocks.
 constexpr float kPairShare = 1.f / 16.f;
 constexpr int kFlagRows = 32, kFlagCols = 64;
@@ -221,7 +221,7 @@ struct DzCeEpi {
                     Elem<__nv_bfloat16>::unpack(hi[k], h);
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
-                        most = fmaxf(most, fabsf(v[8 * k + i]));
+                        most = fmaxf(most, fabsf(h[i]));  // as pair_add_kernel sees them
                         h[i] = v[8 * k + i] - h[i];
                     }
                     lo[k] = Elem<__nv_bfloat16>::pack(h);
