@@ -552,6 +552,45 @@ def test_dhidden_of_a_large_table_does_not_depend_on_the_rows_beside_it():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("N, V, D, zeta", [(1100, 33000, 1024, 1.0), (1100, 33000, 1024, 1e3), (300, 20000, 256, 1.0)])
+def test_linear_large_z_loss(N, V, D, zeta):
+    """A z-loss whose gradient, 1 + 2 zeta lse of the softmax, is most of the row's: against 64 bits, with the row's scale
+    times that factor, and in about the time of a small one (the values over the limit stay a few a row)."""
+    h, w, targets, g = (t.cuda() for t in model(N, V, D, 52))
+    loss, stats = vp.vp_linear_cross_entropy_fwd(h, w, targets, z_loss=zeta)
+    dh, dw = vp.vp_linear_cross_entropy_bwd(h, w, targets, stats, g, z_loss=zeta)
+    h64, w64 = h.double(), w.double()
+    x, size = h64 @ w64.t(), h64.abs() @ w64.abs().t()
+    d = (D / 16 + 1) * 2.25 * U * size.amax(1, keepdim=True)
+    ref = plain(x, targets, zeta=zeta)
+    near(loss, ref, loss_tol(x, ref, targets, 0.0, zeta, 0.0, d[:, 0]), "loss")
+    dz, off, per_d, _, lse = plain_grad(x, targets, g, zeta=zeta)
+    a = 1 + 2 * zeta * lse
+    # lse is off by d and its own rounding, and 2 zeta lse with it
+    off = off + per_d * d + g.double().abs()[:, None] * torch.exp(x - lse) * 2 * zeta * (d + 64 * U + 4 * U * lse.abs())
+    lpt = (x - lse).gather(1, targets.clamp(min=0)[:, None])
+    scale = g.double().abs()[:, None] * (-torch.expm1(lpt)).clamp(min=2.0 ** -20) * a.abs().clamp(min=1.0)
+    off = off + torch.where(dz.abs() > 1.01 / 16 * scale, 2.0 ** -16, 2.0 ** -8) * dz.abs()
+    half = torch.finfo(BF16).eps / 2
+    for got, ref, tol in ((dh, dz @ w64, off @ w64.abs() + (V / 16 + 2) * 2 * U * (dz.abs() @ w64.abs())),
+                          (dw, dz.t() @ h64, off.t() @ h64.abs() + (N / 16 + 2) * 2 * U * (dz.abs().t() @ h64.abs()))):
+        near(got, ref, tol + half * ref.abs(), f"zeta {zeta}")
+
+    def took(z):
+        times = []
+        for _ in range(4):
+            a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+            a.record()
+            vp.vp_linear_cross_entropy_bwd(h, w, targets, stats, g, z_loss=z)
+            b.record()
+            b.synchronize()
+            times.append(a.elapsed_time(b))
+        return min(times)
+
+    assert took(zeta) < 4 * took(0.0)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("D", [512, 4096])
 def test_linear_losses_are_not_short(D):
     """The tensor cores' sums come out short, 2.4e-5 of a log-sum-exp at D = 4096; what is given back leaves the losses
