@@ -795,8 +795,11 @@ VP_API vp_status vp_cross_entropy_merge(const vp_partial *parts, int64_t K, int6
  * (hidden, weight, workspaces' alignment, VP_GRAD_* and the sharded flow as for the fused linear
  * logp): hidden bf16 [N, D], weight bf16 [V, D], D a multiple of 64. The backward writes dhidden
  * bf16 [N, D] and dW bf16 [V, D] (either may be NULL, not both); with N = 0 it writes zeros to dW.
- * A row without valid statistics makes its dhidden row and all of dW NaN. Beside VP_GRAD_EXACT and
- * VP_GRAD_FAST it takes
+ * A row without valid statistics makes its dhidden row and all of dW NaN. The tensor cores cut each step's sum
+ * off towards zero, and the logits are given back what that comes to on average: the factor 1 + min(D, 16384) / 16 * 2^-26,
+ * the same in all of these calls and in no vp_linear_logp_* call. Logits of many terms of either sign are right on
+ * average to 1e-6 of themselves so (up to D = 16384; short by 4e-6 without at 4096); sums that are exact come out long by it, 4e-6 there and 1.5e-5 at most.
+ * Beside VP_GRAD_EXACT and VP_GRAD_FAST the backward takes
  *   VP_GRAD_MIXED  dz as a pair hi + lo where it counts: the gradient GEMMs add the second halves of
  *                  those k-blocks that hold a value whose hi is over 1/16 of its row's scale, |grad_out|
  *                  (1 - p_t + label_smoothing) max(1, |1 + 2 z_loss lse|), as a target's is unless the z-loss

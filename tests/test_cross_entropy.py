@@ -618,6 +618,22 @@ def test_linear_sums_of_logits_past_the_largest_float():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("D", [1024, 4096, 32768])
+def test_linear_logits_whose_sums_are_exact(D):
+    """One product each, of which nothing is cut off: what is given back all the same is D / 16 steps of 2^-26 of the logit,
+    of 16384 columns at most, to a quarter of itself and the rounding of the factor and the product (2 u)."""
+    h, w = torch.zeros(64, D, dtype=BF16), torch.zeros(1, D, dtype=BF16)
+    at = torch.arange(64) * (D // 64) + 3
+    h[torch.arange(64), at] = torch.randn(64, generator=torch.Generator().manual_seed(54)).to(BF16) * 30
+    w[0, at] = torch.randn(64, generator=torch.Generator().manual_seed(55)).to(BF16)
+    _, stats = vp.vp_linear_cross_entropy_fwd(h.cuda(), w.cuda(), torch.zeros(64, dtype=torch.int64, device="cuda"))
+    got = vp.decode_rowstats(stats)["m"].double().cpu()              # of one column, the logit
+    z = (h.double() @ w.double().t())[:, 0]
+    back = min(D, 16384) / 16 * 2.0 ** -26
+    assert ((got - z * (1 + back)).abs() <= (back / 4 + 2 * U) * z.abs()).all()
+
+
+@pytest.mark.gpu
 def test_linear_near_certain_rows():
     h, w, targets, g = model(40, 900, 128, 35, sigma=1.0)
     used = targets >= 0

@@ -19,10 +19,14 @@ namespace vp {
 
 // A tensor-core step adds 16 products to the running fp32 sum and cuts off what lies below its last
 // bit, towards zero, so a logit comes out short: over sums of independent terms by 2^-26 of itself a
-// step on average (measured on GB300: lse short by 2.7e-6, 1.2e-5 and 2.4e-5 at D = 512, 2048 and
-// 4096 with logits of variance 6.25, whose softmax-weighted mean is 6.25). The epilogues give that mean back;
-// it is within the bound of the steps themselves, 2^-23 of the running sum each, for any data.
-static float cut_off(int64_t D) { return 1.f + (float)(D / 16) * 1.490116119384765625e-08f; }
+// step on average (measured on GB300 as the slope of 98304 logits' errors: 0.86, 0.90, 0.96, 1.01, 1.03 and
+// 1.06 times 2^-26 a step at D = 512, 1024, .., 16384, the same to 1 % at variances of 1, 6.25, 25 and 100).
+// The epilogues give that mean back, for 16384 columns at most. It is a mean and no more: terms of one
+// sign lose 1.9 to 5.4 times as much, and a sum that nothing is cut off of (one product, say) comes out long by what is
+// given back, 2^-18 of itself at D = 4096 and 2^-16 at most. Either is within the bound of the steps themselves,
+// 2^-23 of the running sum each.
+constexpr int64_t kCutOffMostD = 16384;
+static float cut_off(int64_t D) { return 1.f + (float)(std::min(D, kCutOffMostD) / 16) * 1.490116119384765625e-08f; }
 __device__ __forceinline__ void scale_all(float (&v)[32], float s) {
 #pragma unroll
     for (int i = 0; i < 32; i += 2) {
