@@ -292,6 +292,26 @@ def test_sums_of_logits_past_the_largest_float(dtype):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("N, V", [(4, 700), (700, 1001), (6, 9001)])
+def test_a_masked_target(N, V, dtype):
+    """Its loss is infinite, its gradient what the formula says of p = 0; and a z-loss of 1."""
+    x, targets, g = rows(N, V, dtype, 57)
+    targets = targets.clamp(min=0)
+    x[torch.arange(0, N, 2), targets[::2]] = -math.inf
+    x[torch.arange(1, N, 4), targets[1::4]] = torch.finfo(dtype).min
+    for s, z in ((0.0, 0.0), (0.1, 0.0), (0.0, 1.0), (1.0, 1.0)):
+        loss, stats = vp.vp_cross_entropy_fwd(x.cuda(), targets.cuda(), label_smoothing=s, z_loss=z)
+        assert torch.isinf(loss[::2]).all() and torch.isfinite(loss[3::4]).all()
+        dx = vp.vp_cross_entropy_bwd(x.cuda(), targets.cuda(), stats, g.cuda(), label_smoothing=s, z_loss=z)
+        d, off, *_ = plain_grad(x.double(), targets, g, s, z)
+        r = torch.arange(N)
+        p0 = torch.isinf(x[r, targets])
+        d[r[p0], targets[p0]] = g.double()[p0] * -(1 - s + s / V)
+        near(dx, d, off + torch.finfo(dtype).eps / 2 * d.abs(), f"smooth {s}, zeta {z}")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [F32, BF16])
 def test_rows_with_nothing_or_with_nan(dtype):
     x, _, g = rows(7, 5003, dtype, 13)
     x[1] = -math.inf
@@ -591,6 +611,29 @@ def test_linear_large_z_loss(N, V, D, zeta):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("precision", [vp.GRAD_MIXED, vp.GRAD_FAST, vp.GRAD_EXACT])
+def test_linear_dW_of_columns_without_a_target(precision):
+    """Row by row of dW where no value need be a pair: roundings of dz to bf16 and of the result are spread over half a step
+    each, 2^-8 of the value at most and 2^-8 / sqrt(3) in the mean square, so the rows' squared errors add up to
+    2^-16 / 3 (sum dz^2 |h|^2 + |dW|^2), without the first term where dz is a pair; no row alone is off by four times that."""
+    h, w, targets, g = (t.cuda() for t in model(1100, 20000, 256, 56))
+    o = dict(label_smoothing=0.1, z_loss=1e-4)
+    _, stats = vp.vp_linear_cross_entropy_fwd(h, w, targets, **o)
+    _, dw = vp.vp_linear_cross_entropy_bwd(h, w, targets, stats, g, want_dhidden=False, precision=precision, **o)
+    h64 = h.double()
+    dz = plain_grad(h64 @ w.double().t(), targets, g, 0.1, 1e-4)[0]
+    ref = dz.t() @ h64
+    free = torch.ones(20000, dtype=torch.bool, device="cuda")
+    free[targets[targets >= 0]] = False
+    error = (dw.double() - ref).square().sum(1)[free]
+    allowed = ref.square().sum(1)
+    if precision != vp.GRAD_EXACT:
+        allowed = allowed + (dz.square() * h64.square().sum(1, keepdim=True)).sum(0)
+    allowed = 2.0 ** -16 / 3 * allowed[free]
+    assert error.sum() <= 1.1 * allowed.sum() and (error <= 16 * allowed).all()
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("D", [512, 4096])
 def test_linear_losses_are_not_short(D):
     """The tensor cores' sums come out short, 2.4e-5 of a log-sum-exp at D = 4096; what is given back leaves the losses
@@ -755,6 +798,33 @@ def test_callers_buffers_and_nothing_behind_them():
     dh, dw = torch.full((21, 64), 7.0, dtype=BF16, device="cuda"), torch.full((601, 64), 7.0, dtype=BF16, device="cuda")
     vp.vp_linear_cross_entropy_bwd(h, w, t, st, gg, dhidden=dh[:20], dW=dw[:600])
     assert (dh[20:] == 7).all() and (dw[600:] == 7).all() and not (dw[:600] == 7).all()
+
+
+@pytest.mark.gpu
+def test_buffers_at_their_least_alignment():
+    """Workspaces of the loss on any 16-byte boundary, of the fused forms on any of 256, records on any of 8."""
+    x, targets, g = (t.cuda() for t in rows(700, 9001, F32, 51))
+    ref, rst = vp.vp_cross_entropy_fwd(x, targets)
+    need = vp.vp_cross_entropy_workspace_size(700, 9001)
+    work = torch.empty(need + 16, dtype=torch.uint8, device="cuda")[16:]
+    assert work.data_ptr() % 32 == 16
+    loss, stats = vp.vp_cross_entropy_fwd(x, targets, workspace=work)
+    assert torch.equal(loss, ref) and torch.equal(stats, rst)
+    parts = vp.partials(701, "cuda")[1:]
+    assert parts.data_ptr() % 16 == 8
+    vp.vp_cross_entropy_partial(x, targets, parts=parts, workspace=work)
+    merged, _ = vp.vp_cross_entropy_merge(parts[None])
+    assert torch.allclose(merged, ref, rtol=1e-6)
+    h, w, t, gg = (v.cuda() for v in model(300, 9000, 128, 52))
+    ref, st = vp.vp_linear_cross_entropy_fwd(h, w, t)
+    dh, dw = vp.vp_linear_cross_entropy_bwd(h, w, t, st, gg)
+    for size, call, want in ((vp.vp_linear_cross_entropy_workspace_size(300, 9000, 128),
+                              lambda work: vp.vp_linear_cross_entropy_fwd(h, w, t, workspace=work), (ref, st)),
+                             (vp.vp_linear_cross_entropy_bwd_workspace_size(300, 9000, 128),
+                              lambda work: vp.vp_linear_cross_entropy_bwd(h, w, t, st, gg, workspace=work), (dh, dw))):
+        work = torch.empty(size + 256, dtype=torch.uint8, device="cuda")[256:]
+        assert work.data_ptr() % 512 == 256
+        assert all(torch.equal(a, b) for a, b in zip(call(work), want))
 
 
 @pytest.mark.gpu
