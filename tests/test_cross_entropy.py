@@ -310,6 +310,33 @@ def test_a_masked_target(N, V, dtype):
         near(dx, d, off + torch.finfo(dtype).eps / 2 * d.abs(), f"smooth {s}, zeta {z}")
 
 
+FAR = [1.2e4, -65504.0, 1e5, -1e6, 3e7, -1e8, -1e9, 2.0 ** 30, -2.0 ** 30, 2.0 ** 30 + 128, -3e9, 1e20, -1e30, 3e38]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("V", [700, 20000])
+def test_rows_far_from_zero(dtype, V):
+    """Rows of one value (all that a mask of -1e9 leaves, say) are uniform, and rows that lie close together around a far
+    value are what their differences say: z - m is exact, so neither the loss nor p knows the offset. Where the differences are of
+    64 and more, p below 2^-62 may come out 0."""
+    g = torch.linspace(-2, 3, len(FAR))
+    x = torch.tensor(FAR)[:, None].expand(-1, V).to(dtype).contiguous()
+    targets = torch.arange(len(FAR)) * 49 + 3
+    for spread in (0.0, 3.0):
+        if spread:
+            x = (x.double() + spread * torch.randn(len(FAR), V, generator=torch.Generator().manual_seed(V), dtype=torch.float64)).to(dtype)
+        for s in (0.0, 0.1):
+            loss, stats = vp.vp_cross_entropy_fwd(x.cuda(), targets.cuda(), label_smoothing=s)
+            dx = vp.vp_cross_entropy_bwd(x.cuda(), targets.cuda(), stats, g.cuda(), label_smoothing=s)
+            z = x.double() - x.double().amax(1, keepdim=True)
+            ref = plain(z, targets, s)
+            size = z.gather(1, targets[:, None])[:, 0].abs() + s * 24 * z.abs().mean(1)
+            near(loss, ref, 64 * U + 2 * U * size + U * ref.abs(), "loss")
+            d, off, *_ = plain_grad(z, targets, g, s)
+            near(dx, d, off + g.abs().double()[:, None] * 2.0 ** -62 + torch.finfo(dtype).eps / 2 * d.abs(), "dx")
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("dtype", [F32, BF16])
 def test_rows_with_nothing_or_with_nan(dtype):
@@ -674,6 +701,26 @@ def test_linear_logits_whose_sums_are_exact(D):
     z = (h.double() @ w.double().t())[:, 0]
     back = min(D, 16384) / 16 * 2.0 ** -26
     assert ((got - z * (1 + back)).abs() <= (back / 4 + 2 * U) * z.abs()).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("V", [1000, 70001])
+def test_linear_rows_far_from_zero(V):
+    """Rows of one far value: uniform, whatever the value. Row n takes column n of hidden and weight alone, so dW there is
+    dz times the hidden value, rounded (dz twice, as a pair or as one value: 2^-8 each)."""
+    N = 12
+    scale = torch.tensor([1.0, -1.0]).repeat(6) * 2.0 ** torch.arange(12, 36, 2)
+    h, w = torch.zeros(N, 64, dtype=BF16), torch.zeros(V, 64, dtype=BF16)
+    h[torch.arange(N), torch.arange(N)] = scale.to(BF16)
+    w[:, :N] = 1.3
+    targets, g = torch.arange(N) * 30 + 1, torch.linspace(1, 2, N)
+    loss, stats = vp.vp_linear_cross_entropy_fwd(h.cuda(), w.cuda(), targets.cuda())
+    assert torch.allclose(loss.double().cpu(), torch.full((N,), math.log(V), dtype=torch.float64), rtol=0, atol=64 * U + U * math.log(V))
+    _, dw = vp.vp_linear_cross_entropy_bwd(h.cuda(), w.cuda(), targets.cuda(), stats, g.cuda())
+    dz = (dw[:, :N].double().cpu() / scale).t()
+    ref = (g.double() / V)[:, None].repeat(1, V)
+    ref[torch.arange(N), targets] -= g.double()
+    assert ((dz - ref).abs() <= 2.1 * 2.0 ** -8 * ref.abs()).all()
 
 
 @pytest.mark.gpu

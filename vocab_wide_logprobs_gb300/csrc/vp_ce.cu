@@ -197,7 +197,7 @@ ce_fwd_kernel(const T *__restrict__ x, int V, Rows rows, const CeRules q, const 
                     if (kSum) df_add(Wd, s_W[w]);
                 }
                 const float S_all = Sd.hi * centre.f;
-                CeSlice o{m, S_all, fmaf(Sd.hi, centre.f, -S_all) + Sd.lo, Wd.hi, Wd.lo, zt,
+                CeSlice o{m, S_all, fmaf(Sd.hi, centre.f, -S_all) + Sd.lo * centre.f, Wd.hi, Wd.lo, zt,
                           (has_target ? kPartHasTarget : 0u) | (minus_inf ? kCeMinusInf : 0u),
                           (uint32_t)(max(v1 - v0, 0) * kVec + extra)};
                 if (!(S_all < INFINITY)) o.S = qnan(), o.S_lo = 0.f;     // a NaN, or +inf without a cap

@@ -87,32 +87,42 @@ __device__ __forceinline__ float soft_cap1(const CeRules &q, float x, float *slo
     return v[0];
 }
 
-// Exponentials against a centre k: e^{z - k} = 2^{z l - c} f with l = fl(log2 e), c = fl(k l), so that
-// one FMA makes the argument of the hardware's 2^x. z l is exact inside the FMA, and f = 2^{c - k l}
-// takes back what rounding k l did to every term alike; left over is (z - k) (log2 e - l), 2e-8 of
-// z - k, and the argument's own rounding. Beyond |k| = 2^100 (rows of a type's lowest value, say)
-// floats lie so far apart that z is k or has no weight: l = 1 and c = k serve, and cannot overflow.
-struct ExpCentre {
-    float l, c, f;
-};
-constexpr float kFarCentre = 1.2676506002282294e30f;
-__device__ __forceinline__ ExpCentre exp_centre(float k) {
-    if (fabsf(k) >= kFarCentre) return {1.f, k, 1.f};
-    const float c = k * kLog2e;
-    return {kLog2e, c, fmaf(fmaf(k, kLog2e, -c), -0.6931471805599453f, 1.f)};
-}
-// k = a + b + b_lo, b >= 0 a row's log S
-__device__ __forceinline__ ExpCentre exp_centre(float a, float b, float b_lo) {
-    if (fabsf(a) >= kFarCentre) return {1.f, a, expf(-(b + b_lo))};
-    const float pa = a * kLog2e, ea = fmaf(a, kLog2e, -pa);
-    const float pb = b * kLog2e, eb = fmaf(b_lo, kLog2e, fmaf(b, 1.925963033500011e-08f, fmaf(b, kLog2e, -pb)));
-    const DF s = two_sum(pa, pb);
-    return {kLog2e, s.hi, fmaf(s.lo + (ea + eb), -0.6931471805599453f, 1.f)};
-}
 __device__ __forceinline__ float ex2_approx(float a) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(a));
     return y;
+}
+
+// Exponentials against a centre k: e^{z - k} = 2^{z l - c} f with l = fl(log2 e), c = fl(k l), so that
+// one FMA makes the argument of the hardware's 2^x. z l is exact inside the FMA, and f = 2^{c - k l}
+// takes back what rounding k l did to every term alike; left over is (z - k) (log2 e - l), 2e-8 of
+// z - k, and the argument's own rounding. What rounding did is up to 64 at |k| = 2^30: no term is above 2^64
+// and f not below 2^-64. Beyond that (rows masked by the type's lowest value, say) floats lie 128 or more
+// apart, so z is k or has no weight: l = 2 and c = 2 k serve as well, or l = 1 where 2 k could overflow.
+struct ExpCentre {
+    float l, c, f;
+};
+constexpr float kFarCentre = 1073741824.f, kLargeCentre = 1.2676506002282294e30f;   // 2^30 and 2^100
+__device__ __forceinline__ ExpCentre far_centre(float k, float f) {
+    const float l = fabsf(k) < kLargeCentre ? 2.f : 1.f;
+    return {l, k * l, f};
+}
+// 2^-r, r what rounding a product took away: 1 - r ln 2 is off by r^2 / 4, 2^-24 up to 2^-11
+constexpr float kSmallDrift = 4.8828125e-4f;
+__device__ __forceinline__ ExpCentre exp_centre(float k) {
+    if (fabsf(k) > kFarCentre) return far_centre(k, 1.f);
+    const float c = k * kLog2e, r = fmaf(k, kLog2e, -c);
+    return {kLog2e, c, fabsf(r) <= kSmallDrift ? fmaf(r, -0.6931471805599453f, 1.f) : ex2_approx(-r)};
+}
+// k = a + b + b_lo, b >= 0 a row's log S: its exponential goes into f where the sum is rounded by much
+__device__ __forceinline__ ExpCentre exp_centre(float a, float b, float b_lo) {
+    const float pa = a * kLog2e, ea = fmaf(a, kLog2e, -pa);
+    const float pb = b * kLog2e, eb = fmaf(b_lo, kLog2e, fmaf(b, 1.925963033500011e-08f, fmaf(b, kLog2e, -pb)));
+    const DF s = two_sum(pa, pb);
+    const float r = s.lo + (ea + eb);
+    if (fabsf(r) <= kSmallDrift) return {kLog2e, s.hi, fmaf(r, -0.6931471805599453f, 1.f)};
+    const float f = fmaf(expf(-b), -b_lo, expf(-b));
+    return fabsf(a) > kFarCentre ? far_centre(a, f) : ExpCentre{kLog2e, pa, ex2_approx(-ea) * f};
 }
 // 2^{z l - c}
 __device__ __forceinline__ float ce_exp(const ExpCentre &k, float z) { return ex2_approx(fmaf(z, k.l, -k.c)); }
