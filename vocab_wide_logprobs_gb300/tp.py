@@ -44,6 +44,24 @@ def tp_kl_fwd(a_shard, b_shard, direction: int = api.KL_REVERSE, group=None):
     return api.vp_kl_merge(gather_partials(api.vp_kl_partial(a_shard, b_shard, direction), group), direction)
 
 
+def tp_cross_entropy_fwd(x_shard, targets, vocab_start: int, label_smoothing: float = 0.0, z_loss: float = 0.0,
+                         softcap: float = 0.0, group=None, err_word=None):
+    """Losses of global target ids over rows split across ranks: (loss, stats) on every rank. Their gradient is
+    vp_cross_entropy_bwd of each rank's shard, with vocab_total."""
+    parts = api.vp_cross_entropy_partial(x_shard, targets, softcap=softcap, vocab_start=vocab_start)
+    return api.vp_cross_entropy_merge(gather_partials(parts, group), label_smoothing=label_smoothing, z_loss=z_loss,
+                                      err_word=err_word)
+
+
+def tp_embedding_fwd(w_shard, ids, vocab_start: int, scale: float = 1.0, dtype=None, group=None):
+    """Rows for token ids of a table whose rows are split across ranks, on every rank: one rank has a token's row, the
+    others zeros, so the sum is exact; an id of no rank's shard gives zeros. The table's gradient needs no exchange:
+    vp_embedding_bwd of each rank's shard, with sharded."""
+    out = api.vp_embedding_fwd(w_shard, ids, scale=scale, vocab_start=vocab_start, sharded=True, dtype=dtype)
+    dist.all_reduce(out, op=dist.ReduceOp.SUM, group=group)
+    return out
+
+
 # ---------------------------------------------------------------------------
 # The fused linear ops with the head's rows split across ranks ([P2] page "[Feat]
 # [Kernel] Add TP Fused linear logp Triton", "Implementation"): each rank holds
@@ -65,6 +83,14 @@ def tp_linear_kl_fwd(ha, wa_shard, hb, wb_shard, direction: int = api.KL_REVERSE
     """KL of two models whose heads' rows are split the same way across ranks: (kl, stats_a, stats_b)."""
     parts = api.vp_linear_kl_partial(ha, wa_shard, hb, wb_shard, direction)
     return api.vp_kl_merge(gather_partials(parts, group), direction)
+
+
+def tp_linear_cross_entropy_fwd(hidden, w_shard, targets, vocab_start: int, label_smoothing: float = 0.0,
+                                z_loss: float = 0.0, softcap: float = 0.0, group=None, err_word=None):
+    """Losses of global target ids with the head's rows split across ranks: (loss, stats) on every rank."""
+    parts = api.vp_linear_cross_entropy_partial(hidden, w_shard, targets, softcap=softcap, vocab_start=vocab_start)
+    return api.vp_cross_entropy_merge(gather_partials(parts, group), label_smoothing=label_smoothing, z_loss=z_loss,
+                                      err_word=err_word)
 
 
 def reduce_dhidden(dh_term: torch.Tensor, group=None) -> torch.Tensor:
