@@ -802,7 +802,7 @@ VP_API vp_status vp_cross_entropy_merge(const vp_partial *parts, int64_t K, int6
  * Beside VP_GRAD_EXACT and VP_GRAD_FAST the backward takes
  *   VP_GRAD_MIXED  dz as a pair hi + lo where it counts: the gradient GEMMs add the second halves of
  *                  those k-blocks that hold a value whose hi is over 1/16 of its row's scale, |grad_out|
- *                  (1 - p_t + label_smoothing) max(1, |1 + 2 z_loss lse|), as a target's is unless the z-loss
+ *                  (1 - p_t + label_smoothing) max(1, |1 + 2 z_loss lse| / 4), as a target's is unless the z-loss
  *                  outweighs it; dhidden of many rows and a large weight, those of
  *                  the values themselves. What the smaller values can add up to in
  *                  dhidden is a third of what rounding the output adds, relative to the row's scale; a

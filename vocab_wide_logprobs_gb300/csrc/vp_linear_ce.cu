@@ -128,11 +128,11 @@ __device__ __forceinline__ void store_rows(uint4 *stage, const uint4 (&v)[kVecs]
 // Which values of dz the mixed precision carries as a pair. One bf16 value is off by up to 2^-8 of
 // itself, so what the values up to a threshold of a row add to the error of dhidden is 2^-8 sqrt(sum of
 // their squares) |W|, and with a threshold of t times the row's own scale s (for a cross entropy the values
-// add up to about 2 s, s = |g| (1 - p_t), through the cap's slope at the target; a z-loss multiplies every
-// softmax by 1 + 2 zeta lse, and the scale with it where that is more than 1) that is below
+// add up to about 2 s, s = |g| (1 - p_t), through the cap's slope at the target) that is below
 // 2^-8 sqrt(2 t) s |W|: for t = 1/16 about a third of what the output's own rounding adds. The values of a
 // row whose first half is larger, its target's first of all, are pairs. Which 32 x 64 pieces of dz hold one is noted, and the
-// gradient GEMMs take the second halves of no other k-blocks.
+// gradient GEMMs take the second halves of no other k-blocks. A z-loss multiplies every softmax, and the scale,
+// by 1 + 2 zeta lse; beyond 4 the threshold grows with it, so that no row has pairs by the hundred.
 constexpr float kPairShare = 1.f / 16.f;
 constexpr int kFlagRows = 32, kFlagCols = 64;
 
@@ -166,7 +166,7 @@ struct DzCeEpi {
         const CeGradRow gr = ce_grad_row(q, s, valid ? g[row] : 0.f);
         // the record's c is log p of the target
         float limit = kPairShare * fabsf(gr.g) * fmaxf(q.smooth - expm1f(s.c_hi), 9.5367431640625e-07f) *
-                      fmaxf(1.f, fabsf(1.f + gr.a1));
+                      fmaxf(1.f, 0.25f * fabsf(1.f + gr.a1));
         if (kCap) {
             const float zt = (s.m + s.logS_hi + s.c_hi) * q.inv_cap;
             limit *= fmaxf(fmaf(-zt, zt, 1.f), 9.5367431640625e-07f);
@@ -326,8 +326,8 @@ pair_list_kernel(const uint8_t *__restrict__ flags, int row_groups, int pitch, i
     if (tid == 0) count[blockIdx.x] = (int)done;
 }
 
-// dhidden's share of the second halves, without a GEMM: a row's values above its limit are few (those of a cross entropy,
-// with any z-loss, add up to about twice its scale, so some 32 at most, and one or two as a rule), so their second halves times their rows of W are
+// dhidden's share of the second halves, without a GEMM: a row's values above its limit are few (those of a cross entropy
+// add up to about twice its scale, so some 32 at most, 64 with a large z-loss, and one or two as a rule), so their second halves times their rows of W are
 // added to the row's sum as they are. A CTA for a row and 2048 columns: it goes through the row's noted blocks, 32 at a time,
 // in order, so a row's sum does not depend on the rows beside it.
 constexpr int kAddThreads = 256, kAddBlocks = 32;
