@@ -10,7 +10,7 @@
 // Backward: slices of 1024 vectors (2048 with a cap), one read and one write; dx may be x.
 // Bound: DRAM bytes; with a cap on bf16 logits the issue slots, of which the cap takes some 6 a column.
 //   8192 x 75968 bf16, at 6.79 TB/s 183 and 367 us: forward 204, 213 to 225 with the sum that label smoothing asks
-//   for, backward 355; capped 335 and 434. 4096 x 75968 fp32: forward 181, backward 345.
+//   for, backward 355; capped 338 and 450. 4096 x 75968 fp32: forward 181 to 193, backward 345 to 349; capped 249 and 372.
 #include <algorithm>
 
 #include "vp_ce.cuh"
@@ -27,7 +27,7 @@ static int ce_threads(bool bf16, int64_t V) {
     const int64_t most = (V + (bf16 ? 7 : 3)) / (bf16 ? 8 : 4);       // vectors
     return most <= 128 ? 32 : most <= 64 * kCeFwdVecs ? 64 : most <= 128 * kCeFwdVecs ? 128 : kCeThreads;
 }
-constexpr int64_t kCeFewRows = 608;              // four for each SM
+constexpr int64_t kCeFewRows = 608;              // four for each of GB300's 152 SMs; the workspace's size, asked for on any host, follows from it
 constexpr int ce_grad_vecs(bool cap) { return cap ? 8 : 4; }
 
 static int64_t ce_slices(bool bf16, int vecs, int64_t V) {
@@ -265,7 +265,7 @@ ce_grad_kernel(const T *x, int V, Rows rows, const CeRules q, const RowStat *__r
             mode = 2;
             if (err && s == 0 && tid == 0) atomicOr(err, VP_ERRBIT_TARGET_);
         }
-        const CeGradRow row = ce_grad_row(q, st, g_in[r]);
+        const CeGradRow row = ce_grad_row<(kThreads > 32)>(q, st, g_in[r]);
         const float constant = mode == 1 ? 0.f : qnan();
 
         auto one = [&](int j) {

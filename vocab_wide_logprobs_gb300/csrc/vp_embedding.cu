@@ -670,7 +670,8 @@ int sm_count() {
     return sms > 0 ? sms : 1;
 }
 
-// Tokens of a window: as many as leave three CTAs for every SM, since a window costs up to two partial rows (20000 x 1024
+// Tokens of a window: as many as leave three CTAs for each of GB300's 152 SMs and some (the workspace's size, asked for on
+// any host, follows from it), since a window costs up to two partial rows (20000 x 1024
 // bf16 into 151936 rows, 64 tokens and 313 CTAs: 81 us, 32 and 625: 72; 8192 x 4096, 32 and 512: 109, 8 and 2048: 111 to 117).
 int grad_window(int64_t N, int64_t D) {
     const int64_t col_blocks = (D + kGradThreads * kEmbVec - 1) / (kGradThreads * kEmbVec);

@@ -163,7 +163,7 @@ struct DzCeEpi {
         if (tg < 0) mode = 1;
         if (valid && outside && err && col0 == 0 && v0 == 0) atomicOr(err, VP_ERRBIT_TARGET_);
         const int64_t tcol = tg >= 0 ? tl - v0 - col0 : -1;   // target column within this tile
-        const CeGradRow gr = ce_grad_row(q, s, valid ? g[row] : 0.f);
+        const CeGradRow gr = ce_grad_row<true>(q, s, valid ? g[row] : 0.f);
         // the record's c is log p of the target
         float limit = kPairShare * fabsf(gr.g) * fmaxf(q.smooth - expm1f(s.c_hi), 9.5367431640625e-07f) *
                       fmaxf(1.f, 0.25f * fabsf(1.f + gr.a1));
