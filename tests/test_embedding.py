@@ -427,3 +427,11 @@ def test_refusals_of_the_binding():
     assert status(lambda: vp.vp_embedding_bwd(dy, ids, 20, dW=torch.empty(20, 8), dtype=BF16)) == 3
     assert status(lambda: vp.vp_embedding_bwd(dy, ids, 20, err_word=torch.zeros(1))) == 3
     assert status(lambda: vp.vp_embedding_bwd(dy, ids, 20, workspace=torch.zeros(4, 4).t())) == 4
+
+
+@pytest.mark.parametrize("V", [0, -1, -20, 2 ** 31])
+def test_a_table_of_no_rows_is_refused(V):
+    dy, ids = torch.zeros(6, 8), torch.zeros(6, dtype=torch.int64)
+    with pytest.raises(vp.VPError) as e:
+        vp.vp_embedding_bwd(dy, ids, V)
+    assert e.value.status == ERR_SHAPE

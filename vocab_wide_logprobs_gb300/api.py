@@ -1176,6 +1176,8 @@ def vp_embedding_bwd(dy, ids, V: int, scale: float = 1.0, vocab_start: int = 0, 
         raise VPError(3, f"dtype {dtype}")
     if accumulate and dW is None:
         raise VPError(1, "accumulate needs a dW to add to")
+    if not 0 < V < 2 ** 31 - 1:
+        raise VPError(2, f"a table of {V} rows")
     code = _dtype_code(dy)
     _arg(ids, N, torch.int64, dy, "ids")
     _arg(dW, V * D, dtype, dy, "dW")
